@@ -517,6 +517,158 @@ int moe_layer_bwd_nvfp4(const moe_config* cfg, const moe_bf16* dO, const moe_bf1
                         float* dW1, float* dW3, float* dW2, float* aux_loss_out, void* ws, size_t ws_bytes,
                         void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Router losses with gradients. The report lists load balancing among the
+ * router's parts (figures & tables page, Fig. 2); the layer's own aux_coeff
+ * covers the softmax loss over one whole batch. These calls compute from the
+ * logits [T,E] fp32 and the selected experts topk_idx [T,k] (both as
+ * moe_router_topk and the training forwards return them):
+ *   the sequence-wise balance loss
+ *     losses[0] = balance_coeff / S+ * sum_s sum_e f_{s,e} P_{s,e},
+ *     f_{s,e} = E c_{s,e} / (k n_s), P_{s,e} = (1 / n_s) sum_{t in s} p[t,e],
+ *     over the n_s valid tokens of sequence s (S+: sequences that have any;
+ *     c_{s,e}: their slots routed to e; p: the softmax of the logits, or their
+ *     sigmoids divided by the sum over the experts), and
+ *   the z-loss
+ *     losses[1] = z_coeff / n * sum_t (log sum_e exp logits[t,e])^2
+ *     over the n valid tokens of all sequences;
+ * and the gradient of <dlosses, losses> with respect to the logits (f carries
+ * no gradient). With one sequence and softmax losses[0] is the layer's aux
+ * loss. A token is valid when it lies in a sequence (seq_offsets [n_seqs+1]
+ * int32, ascending: sequence s is the rows seq_offsets[s] .. seq_offsets[s+1];
+ * rows outside [seq_offsets[0], seq_offsets[n_seqs]) belong to none; NULL with
+ * n_seqs = 1: all T rows) and token_mask [T] (bytes; NULL: all) is not 0 there.
+ * Nothing of an invalid token is read into a result, whatever its logits
+ * hold; its gradient is 0. A sequence without valid tokens has counts 0 and
+ * adds nothing; with no valid token at all both losses are 0.
+ * Shapes: T >= 1, E <= 256, 1 <= k <= min(E, 16), n_seqs <= 2^20,
+ * T*k < 2^30. Sums are fp32 within about a hundred rows, fp64 beyond, in a
+ * fixed order.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int T, E, k;
+  int n_seqs;
+  int score;           /* moe_score_fn */
+  float balance_coeff;
+  float z_coeff;       /* 0: no z-loss */
+} moe_balance_config;
+
+/* Workspace bytes of moe_balance_loss_fwd and the number of floats in its
+ * `stats` output (0 for an invalid config). */
+size_t moe_balance_workspace_bytes(const moe_balance_config* cfg);
+size_t moe_balance_stats_floats(const moe_balance_config* cfg);
+
+/* losses [2] fp32, counts [n_seqs,E] int32, and stats, what the backward needs
+ * besides the logits. An expert index outside [0,E) of a valid token is not
+ * counted, and offsets that descend or leave [0,T] give unspecified values;
+ * both record MOE_ERR_DEVICE_INDEX. */
+int moe_balance_loss_fwd(const moe_balance_config* cfg, const float* logits, const int32_t* topk_idx,
+                         const int32_t* seq_offsets, const uint8_t* token_mask, float* losses,
+                         int32_t* counts, float* stats, void* ws, size_t ws_bytes, void* stream);
+
+/* dlogits [T,E] fp32 (every row written). dlosses [2] fp32: the gradients of
+ * the two losses (NULL: 1 and 1). */
+int moe_balance_loss_bwd(const moe_balance_config* cfg, const float* logits, const float* stats,
+                         const float* dlosses, const int32_t* seq_offsets, const uint8_t* token_mask,
+                         float* dlogits, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection x [T,K] W
+ * (the shared expert's projections, or any projection around the layer): row
+ * t uses the adapter adapter_idx[t] of its request,
+ *   y[t] = base[t] + scale[a] (x[t] A[a]) B[a],   a = adapter_idx[t],
+ * A [L,K,r], B [L,r,N] bf16, scale [L] fp32, base and y [T,N] bf16 (fp32 if
+ * out_fp32; base is the shared projection's output). Rows with a negative
+ * index use no adapter: y[t] = base[t]. Backward, with du[t] = scale[a] dy[t]
+ * B[a]^T:
+ *   dx[t] = dx_base[t] + du[t] A[a]^T,
+ *   dA[a] = sum_t x[t]^T du[t],  dB[a] = sum_t (scale[a] x[t] A[a])^T dy[t]
+ * (fp32; zero for an adapter without rows). Products of bf16 inputs are exact
+ * and accumulate in fp32; u = scale x A and du enter their second product as
+ * two bf16 parts (16 bits). Every sum has a fixed order.
+ * Shapes: K, N, r multiples of 8, r <= 128, L <= 1024, 1 <= T <= 2^21,
+ * K, N <= 2^20. Adapters of smaller rank are padded with zeros to r.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int T, K, N, L, r;
+  int out_fp32;
+} moe_adapter_config;
+
+/* Bytes of the plan, of the workspace of moe_adapter_fwd (training == 0) or of
+ * both directions (training != 0), and of u_saved; 0 for an invalid config. */
+size_t moe_adapter_plan_bytes(const moe_adapter_config* cfg);
+size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg, int training);
+size_t moe_adapter_saved_bytes(const moe_adapter_config* cfg);
+
+/* The plan of a batch: its rows ordered by adapter (rows of one adapter stay
+ * in token order). It depends on adapter_idx [T] int32, T and L alone: one plan
+ * serves every projection the batch passes through and their backwards. An
+ * index >= L counts as negative and records MOE_ERR_DEVICE_INDEX in the
+ * plan's status word (its first bytes: moe_get_device_status(plan, ...)). The
+ * calls below record MOE_ERR_DEVICE_INDEX in their workspace, and use no row,
+ * when the plan is of another T or L. */
+int moe_adapter_plan(const moe_adapter_config* cfg, const int32_t* adapter_idx, void* plan, size_t plan_bytes,
+                     void* stream);
+
+/* y from x, as above. base NULL: zeros; y may be base itself (rows without an
+ * adapter are then not touched), otherwise the two must not overlap. u_saved
+ * (moe_adapter_saved_bytes, may be NULL) receives what the backward needs. */
+int moe_adapter_fwd(const moe_adapter_config* cfg, const moe_bf16* x, const moe_bf16* A, const moe_bf16* B,
+                    const float* scale, const void* plan, const void* base, void* y, void* u_saved, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/* dx [T,K] (bf16, fp32 if out_fp32; dx_base as base above), dA [L,K,r] and
+ * dB [L,r,N] fp32, given the forward's plan and u_saved. dy [T,N] bf16. */
+int moe_adapter_bwd(const moe_adapter_config* cfg, const moe_bf16* dy, const moe_bf16* x, const moe_bf16* A,
+                    const moe_bf16* B, const float* scale, const void* plan, const void* u_saved,
+                    const void* dx_base, void* dx, float* dA, float* dB, void* ws, size_t ws_bytes,
+                    void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Global norm of many gradients, and clipping:
+ *   norm = sqrt(sum over all tensors of g^2)  (MOE_NORM_L2), or max |g|
+ *          (MOE_NORM_MAX);
+ *   coef = min(1, max_norm / (norm + 1e-6)),  out = round(g * coef).
+ * Squares are summed over 16 or 32 elements in fp32 and from there in fp64, in
+ * a fixed order; where fp32 squares would overflow or lose bits they are taken
+ * in fp64. A NaN anywhere makes the norm NaN, and every clipped gradient; an
+ * infinite norm scales by 0 (infinities become NaN).
+ * ------------------------------------------------------------------------- */
+typedef enum { MOE_FP32 = 0, MOE_BF16 = 1, MOE_FP16 = 2 } moe_dtype;
+typedef enum { MOE_NORM_L2 = 0, MOE_NORM_MAX = 1 } moe_norm_kind;
+
+/* One tensor of a list: n contiguous elements in device memory, aligned to
+ * their own size (views at any element offset are fine). out NULL: scaled in
+ * place; otherwise the scaled values go there and data stays. */
+typedef struct {
+  void* data;
+  void* out;
+  long long n;
+  int dtype;      /* moe_dtype */
+  int reserved;
+} moe_tensor;
+
+/* A tensor list as the calls below take it, built in caller-owned HOST memory
+ * of moe_tensor_list_bytes(n) bytes (8-byte aligned; 0 for n < 0 or n > 49152):
+ * it holds the tensors' addresses and travels in the kernels' parameters. It
+ * touches no GPU. Memory that is written (out, or data in place) must overlap
+ * no other tensor of the list, and an out its own data only as the same
+ * address: MOE_ERR_INVALID_ARG otherwise. The list stays valid as long as the
+ * tensors stay where they are. */
+size_t moe_tensor_list_bytes(int n);
+int moe_tensor_list_build(const moe_tensor* tensors, int n, void* list, size_t list_bytes);
+
+/* Workspace bytes of both calls. */
+size_t moe_grad_norm_workspace_bytes(void);
+
+/* norm [1] fp32. An empty list has norm 0. */
+int moe_grad_norm(const void* list, int kind, float* norm, void* ws, size_t ws_bytes, void* stream);
+
+/* The norm, then the scaling. max_norm >= 0. Where coef is 1, tensors scaled
+ * in place are not touched. */
+int moe_clip_grad_norm(const void* list, int kind, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                       void* stream);
+
 /* Synchronises `stream`, returns in *status_out the first device-side error
  * recorded in `ws` since the last read (MOE_OK if none) and clears it. For
  * tests and debugging; the hot path never calls it. */

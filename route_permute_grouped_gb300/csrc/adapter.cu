@@ -1,0 +1,785 @@
+// Low-rank adapters of many requests beside a shared projection: row t of a
+// batch gets base[t] + s_a (x[t] A_a) B_a of its own adapter a, and the
+// backward of that. Rows are ordered by adapter once for a batch (the plan);
+// every product then works on tiles of up to 64 rows of one adapter.
+#include <math.h>
+
+#include <algorithm>
+
+#include "host_util.h"
+#include "mma.cuh"
+
+namespace moe {
+
+constexpr int kTileRows = 64;
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxAdapters = 1024;
+constexpr int kAdSMs = 152;
+
+// ---------------------------------------------------------------------------
+// the plan
+// ---------------------------------------------------------------------------
+struct PlanLayout {
+  size_t hdr, seg, tiles, order, hist, total;
+  int max_tiles, chunks;
+};
+static PlanLayout plan_layout(const moe_adapter_config& c) {
+  PlanLayout p{};
+  size_t o = 256;  // the status word
+  auto take = [&](size_t b) {
+    const size_t at = o;
+    o += (b + 255) & ~size_t(255);
+    return at;
+  };
+  p.max_tiles = c.T / kTileRows + std::min(c.T, c.L + 1);
+  p.chunks = (c.T + kPlanThreads - 1) / kPlanThreads;
+  p.hdr = take(64);
+  p.seg = take(4 * (static_cast<size_t>(c.L) + 2));
+  p.tiles = take(16 * static_cast<size_t>(p.max_tiles));
+  p.order = take(4 * static_cast<size_t>(c.T));
+  p.hist = take(4 * static_cast<size_t>(p.chunks) * (c.L + 1));
+  p.total = o;
+  return p;
+}
+struct PlanView {
+  const int4* hdr;       // {number of tiles, T, L, kPlanMagic}
+  const int32_t* seg;    // [L + 2]: first position of each adapter, then of the rows without one, then T
+  const int4* tiles;     // {adapter or -1, first position, rows, 0}
+  const int32_t* order;  // [T]: token of each position
+  int T, L;
+  DevStatus* st;
+};
+constexpr int kPlanMagic = 0x706c616e;
+// the number of tiles; 0, and a device error, for a plan of another batch size
+// or number of adapters or a buffer that holds none
+__device__ __forceinline__ int plan_tiles(const PlanView& p) {
+  const int4 h = __ldg(p.hdr);
+  if (h.y == p.T && h.z == p.L && h.w == kPlanMagic) return h.x;
+  set_status(p.st, MOE_ERR_DEVICE_INDEX, 61);
+  return 0;
+}
+static PlanView plan_view(const moe_adapter_config& c, const void* plan, const PlanLayout& p, void* ws) {
+  const uint8_t* b = static_cast<const uint8_t*>(plan);
+  return {reinterpret_cast<const int4*>(b + p.hdr), reinterpret_cast<const int32_t*>(b + p.seg),
+          reinterpret_cast<const int4*>(b + p.tiles), reinterpret_cast<const int32_t*>(b + p.order), c.T, c.L,
+          static_cast<DevStatus*>(ws)};
+}
+
+__device__ __forceinline__ int plan_key(int a, int L, DevStatus* st) {
+  if (a >= L) {
+    set_status(st, MOE_ERR_DEVICE_INDEX, 60);
+    return L;
+  }
+  return a < 0 ? L : a;
+}
+
+// counts of each adapter (key L: rows without one) in a chunk of 1024 rows
+__global__ void __launch_bounds__(kPlanThreads) plan_hist_kernel(const int32_t* __restrict__ idx, int T, int L,
+                                                                 int32_t* __restrict__ hist, DevStatus* st) {
+  __shared__ int s_h[kMaxAdapters + 1];
+  for (int i = threadIdx.x; i <= L; i += kPlanThreads) s_h[i] = 0;
+  __syncthreads();
+  const int t = blockIdx.x * kPlanThreads + threadIdx.x;
+  if (t < T) atomicAdd(&s_h[plan_key(idx[t], L, st)], 1);
+  __syncthreads();
+  for (int i = threadIdx.x; i <= L; i += kPlanThreads) hist[static_cast<size_t>(blockIdx.x) * (L + 1) + i] = s_h[i];
+}
+
+// exclusive scan of two values per key over s_a and s_b ([L + 1], in place) by
+// the whole block: each warp scans 32 keys, one warp the warps' sums
+__device__ __forceinline__ void scan_keys(int* s_a, int* s_b, int n, int* s_w) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int carry_a = 0, carry_b = 0;
+  for (int k0 = 0; k0 < n; k0 += kPlanThreads) {
+    const int i = k0 + threadIdx.x;
+    const int a = i < n ? s_a[i] : 0, b = i < n ? s_b[i] : 0;
+    int xa = a, xb = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int ya = __shfl_up_sync(0xffffffffu, xa, o), yb = __shfl_up_sync(0xffffffffu, xb, o);
+      if (lane >= o) {
+        xa += ya;
+        xb += yb;
+      }
+    }
+    if (lane == 31) {
+      s_w[warp] = xa;
+      s_w[32 + warp] = xb;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int wa = s_w[lane], wb = s_w[32 + lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int ya = __shfl_up_sync(0xffffffffu, wa, o), yb = __shfl_up_sync(0xffffffffu, wb, o);
+        if (lane >= o) {
+          wa += ya;
+          wb += yb;
+        }
+      }
+      s_w[lane] = wa;
+      s_w[32 + lane] = wb;
+    }
+    __syncthreads();
+    const int pa = warp > 0 ? s_w[warp - 1] : 0, pb = warp > 0 ? s_w[32 + warp - 1] : 0;
+    if (i < n) {
+      s_a[i] = carry_a + pa + xa - a;
+      s_b[i] = carry_b + pb + xb - b;
+    }
+    const int ta = s_w[31], tb = s_w[63];
+    __syncthreads();
+    carry_a += ta;
+    carry_b += tb;
+  }
+}
+
+// Positions of a chunk's rows (rows of an adapter stay in token order: a
+// stable counting sort), and from the first chunk the segments and tiles.
+__global__ void __launch_bounds__(kPlanThreads)
+    plan_place_kernel(const int32_t* __restrict__ idx, int T, int L, int chunks, const int32_t* __restrict__ hist,
+                      int4* __restrict__ hdr, int32_t* __restrict__ seg, int4* __restrict__ tiles, int max_tiles,
+                      int32_t* __restrict__ order, DevStatus* st) {
+  __shared__ int s_first[kMaxAdapters + 1];   // first position of each key
+  __shared__ int s_tile[kMaxAdapters + 1];    // first tile of each key
+  __shared__ int s_before[kMaxAdapters + 1];  // rows of each key in earlier chunks
+  __shared__ __align__(4) uint8_t s_warp[32][kMaxAdapters + 1];
+  __shared__ int s_w[64];
+  const int keys = L + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, me = blockIdx.x;
+  for (int i = tid; i < 32 * (kMaxAdapters + 1) / 4; i += kPlanThreads) reinterpret_cast<int*>(&s_warp[0][0])[i] = 0;
+  for (int i = tid; i < keys; i += kPlanThreads) s_first[i] = s_before[i] = 0;
+  __syncthreads();
+  const int t = me * kPlanThreads + tid;
+  const int key = t < T ? plan_key(idx[t], L, st) : -1;
+  const unsigned peers = __match_any_sync(0xffffffffu, key);
+  const int rank = __popc(peers & ((1u << lane) - 1u));
+  if (key >= 0 && rank == 0) s_warp[warp][key] = static_cast<uint8_t>(__popc(peers));
+  if (hist == nullptr) {
+    if (key >= 0 && rank == 0) atomicAdd(&s_first[key], __popc(peers));  // counts until the scan
+  } else {
+    for (int i = tid; i < keys; i += kPlanThreads) {
+      int n = 0, before = 0;
+      for (int c = 0; c < chunks; ++c) {
+        const int h = hist[static_cast<size_t>(c) * keys + i];
+        before += c < me ? h : 0;
+        n += h;
+      }
+      s_first[i] = n;
+      s_before[i] = before;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < keys; i += kPlanThreads) s_tile[i] = (s_first[i] + kTileRows - 1) / kTileRows;
+  __syncthreads();
+  scan_keys(s_first, s_tile, keys, s_w);
+  __syncthreads();
+  if (key >= 0) {
+    int pos = s_first[key] + s_before[key] + rank;
+    for (int w = 0; w < warp; ++w) pos += s_warp[w][key];
+    order[pos] = t;
+  }
+  if (me == 0) {
+    for (int i = tid; i < keys; i += kPlanThreads) {
+      seg[i] = s_first[i];
+      const int n = (i < L ? s_first[i + 1] : T) - s_first[i];
+      const int nt = (n + kTileRows - 1) / kTileRows;
+      for (int j = 0; j < nt; ++j)
+        if (s_tile[i] + j < max_tiles)
+          tiles[s_tile[i] + j] = make_int4(i < L ? i : -1, s_first[i] + j * kTileRows,
+                                           min(kTileRows, n - j * kTileRows), 0);
+      if (i == L) {
+        seg[L + 1] = T;
+        *hdr = make_int4(min(s_tile[L] + nt, max_tiles), T, L, kPlanMagic);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// products
+// ---------------------------------------------------------------------------
+constexpr int kAdThreads = 128;
+constexpr int kBlockK = 64;
+constexpr int kStages = 3;
+
+// Shared-memory rows are padded by 16 bytes: the eight rows of an 8x8 matrix
+// then lie in different banks.
+template <int RP, bool WT>
+struct ShrinkSmem {
+  static constexpr int kXRow = kBlockK + 8;
+  static constexpr int kWRow = WT ? kBlockK + 8 : RP + 8;
+  static constexpr int kX = kTileRows * kXRow * 2;
+  static constexpr int kW = (WT ? RP : kBlockK) * kWRow * 2;
+  static constexpr int kStage = kX + kW;
+  static constexpr int kTotal = kStages * kStage;
+};
+
+// parts[split][position][j] = sum over the split's part of C of X[t][c] W_a[c][j].
+// W_a is [C][r] (WT = false: A of the forward) or [r][C] (WT = true: B of the
+// backward). fp32 accumulation, joined every 64 products in ordinary fp32 adds.
+template <int RP, bool WT>
+__global__ void __launch_bounds__(kAdThreads)
+    adapter_shrink_kernel(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ W, PlanView plan,
+                          int T, int C, int r, int splits, float* __restrict__ parts) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  using S = ShrinkSmem<RP, WT>;
+  if (static_cast<int>(blockIdx.x) >= plan_tiles(plan)) return;
+  const int4 tile = plan.tiles[blockIdx.x];
+  if (tile.x < 0) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nkb = (C + kBlockK - 1) / kBlockK, per = (nkb + splits - 1) / splits;
+  const int kb0 = blockIdx.y * per, kb1 = min(nkb, kb0 + per);
+  const __nv_bfloat16* Wa = W + static_cast<size_t>(tile.x) * C * r;
+  const uint32_t base = smem_u32(smem);
+
+  // this thread's 16-byte pieces of a stage's rows: piece tid % 8 of rows
+  // tid / 8 + 16 i
+  const __nv_bfloat16* xrow[4];
+  bool xok[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = (tid >> 3) + 16 * i;
+    xok[i] = row < tile.z;
+    xrow[i] = X + (xok[i] ? static_cast<size_t>(plan.order[tile.y + row]) * C : 0);
+  }
+  auto load = [&](int kb, int slot) {
+    const uint32_t sx = base + slot * S::kStage, sw = sx + S::kX;
+    const int c0 = kb * kBlockK;
+    const int c = c0 + (tid & 7) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool ok = xok[i] && c < C;
+      cp_async16(sx + (((tid >> 3) + 16 * i) * S::kXRow + (tid & 7) * 8) * 2, ok ? xrow[i] + c : X, ok);
+    }
+    if constexpr (WT) {
+      for (int i = tid; i < RP * 8; i += kAdThreads) {
+        const int j = i >> 3, cc = c0 + (i & 7) * 8;
+        const bool ok = j < r && cc < C;
+        cp_async16(sw + (j * S::kWRow + (i & 7) * 8) * 2, ok ? Wa + static_cast<size_t>(j) * C + cc : W, ok);
+      }
+    } else {
+      for (int i = tid; i < kBlockK * (RP / 8); i += kAdThreads) {
+        const int cc = i / (RP / 8), j = (i % (RP / 8)) * 8;
+        const bool ok = j < r && c0 + cc < C;
+        cp_async16(sw + (cc * S::kWRow + j) * 2, ok ? Wa + static_cast<size_t>(c0 + cc) * r + j : W, ok);
+      }
+    }
+  };
+
+  float acc[RP / 8][4];
+#pragma unroll
+  for (int n = 0; n < RP / 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (kb0 + s < kb1) load(kb0 + s, s);
+    cp_async_commit();
+  }
+  int slot = 0;
+  for (int kb = kb0; kb < kb1; ++kb) {
+    cp_async_wait<kStages - 2>();
+    __syncthreads();
+    {
+      const int nxt = kb + kStages - 1;
+      if (nxt < kb1) load(nxt, (slot + kStages - 1) % kStages);
+      cp_async_commit();
+    }
+    if (warp * 16 < tile.z) {
+      const uint32_t sx = base + slot * S::kStage, sw = sx + S::kX;
+      float part[RP / 8][4];
+#pragma unroll
+      for (int n = 0; n < RP / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[n][i] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kBlockK; k += 16) {
+        uint32_t a[4];
+        ldmatrix_x4(a, sx + ((warp * 16 + (lane & 15)) * S::kXRow + k + 8 * (lane >> 4)) * 2);
+#pragma unroll
+        for (int n = 0; n < RP; n += 16) {
+          uint32_t b[4];
+          if constexpr (WT)
+            ldmatrix_x4(b, sw + ((n + (lane & 7) + 8 * (lane >> 4)) * S::kWRow + k + 8 * ((lane >> 3) & 1)) * 2);
+          else
+            ldmatrix_x4_trans(b, sw + ((k + (lane & 15)) * S::kWRow + n + 8 * (lane >> 4)) * 2);
+          mma_bf16(part[n / 8], a, b[0], b[1]);
+          mma_bf16(part[n / 8 + 1], a, b[2], b[3]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < RP / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] += part[n][i];
+    }
+    slot = (slot + 1) % kStages;
+  }
+  cp_async_wait<0>();
+  float* out = parts + (static_cast<size_t>(blockIdx.y) * T + tile.y) * RP;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = warp * 16 + (lane >> 2) + 8 * h;
+    if (row < tile.z) {
+#pragma unroll
+      for (int n = 0; n < RP / 8; ++n)
+        *reinterpret_cast<float2*>(out + static_cast<size_t>(row) * RP + 8 * n + 2 * (lane & 3)) =
+            make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+    }
+  }
+}
+
+constexpr int kTileCols = 128;
+template <int RP, bool WT, bool F32>
+struct ExpandSmem {
+  static constexpr int kURow = RP + 8;
+  static constexpr int kU = kTileRows * kURow * 2;  // hi; lo follows
+  static constexpr int kWRow = WT ? RP + 8 : kTileCols + 8;
+  static constexpr int kW = (WT ? kTileCols : RP) * kWRow * 2;
+  static constexpr int kYRow = kTileCols * (F32 ? 4 : 2) + 16;  // bytes
+  static constexpr int kTotal = 2 * kU + kW + kTileRows * kYRow;
+};
+
+// out[t][c] = base[t][c] + sum_j u[position][j] W_a[j][c], u = s_a sum over the
+// splits of parts, multiplied as its two bf16 parts (16 bits of u). W_a is
+// [r][C] (WT = false: B of the forward) or [C][r] (WT = true: A of the
+// backward). The blocks of the first columns keep u's two parts for the
+// weight gradients (u_keep: hi [T][RP], then lo).
+template <int RP, bool WT, bool F32>
+__global__ void __launch_bounds__(kAdThreads)
+    adapter_expand_kernel(const float* __restrict__ parts, int splits, const float* __restrict__ scale,
+                          const __nv_bfloat16* __restrict__ W, PlanView plan, int T, int C, int r,
+                          const void* base_in, void* out, __nv_bfloat16* __restrict__ u_keep) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  using S = ExpandSmem<RP, WT, F32>;
+  constexpr int EB = F32 ? 4 : 2, PER = 16 / EB, PIECES = kTileCols / PER;
+  if (static_cast<int>(blockIdx.y) >= plan_tiles(plan)) return;
+  const int4 tile = plan.tiles[blockIdx.y];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c0 = blockIdx.x * kTileCols;
+  if (tile.x < 0) {
+    // rows without an adapter: the base as it is
+    if (base_in == out) return;
+    for (int i = tid; i < tile.z * PIECES; i += kAdThreads) {
+      const int row = i / PIECES, c = c0 + (i % PIECES) * PER;
+      if (c >= C) continue;
+      const size_t at = (static_cast<size_t>(plan.order[tile.y + row]) * C + c) * EB;
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + at) =
+          base_in != nullptr ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base_in) + at)
+                             : make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  const __nv_bfloat16* Wa = W + static_cast<size_t>(tile.x) * C * r;
+  const uint32_t sb = smem_u32(smem), su_hi = sb, su_lo = sb + S::kU, sw = sb + 2 * S::kU;
+  uint8_t* sy = smem + 2 * S::kU + S::kW;
+  // the tile of W and of the base
+  if constexpr (WT) {
+    for (int i = tid; i < kTileCols * (RP / 8); i += kAdThreads) {
+      const int c = i / (RP / 8), j = (i % (RP / 8)) * 8;
+      const bool ok = j < r && c0 + c < C;
+      cp_async16(sw + (c * S::kWRow + j) * 2, ok ? Wa + static_cast<size_t>(c0 + c) * r + j : W, ok);
+    }
+  } else {
+    for (int i = tid; i < RP * (kTileCols / 8); i += kAdThreads) {
+      const int j = i / (kTileCols / 8), c = (i % (kTileCols / 8)) * 8;
+      const bool ok = j < r && c0 + c < C;
+      cp_async16(sw + (j * S::kWRow + c) * 2, ok ? Wa + static_cast<size_t>(j) * C + c0 + c : W, ok);
+    }
+  }
+  for (int i = tid; i < tile.z * PIECES; i += kAdThreads) {
+    const int row = i / PIECES, c = (i % PIECES) * PER;
+    const bool ok = base_in != nullptr && c0 + c < C;
+    cp_async16(smem_u32(sy + row * S::kYRow + c * EB),
+               ok ? static_cast<const uint8_t*>(base_in) +
+                        (static_cast<size_t>(plan.order[tile.y + row]) * C + c0 + c) * EB
+                  : static_cast<const void*>(W),
+               ok);
+  }
+  cp_async_commit();
+  // u of the tile's rows
+  const float sc = scale[tile.x];
+  for (int i = tid; i < kTileRows * (RP / 4); i += kAdThreads) {
+    const int row = i / (RP / 4), j = (i % (RP / 4)) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row < tile.z) {
+      const float* p = parts + static_cast<size_t>(tile.y + row) * RP + j;
+      for (int s = 0; s < splits; ++s) {
+        const float4 w = *reinterpret_cast<const float4*>(p + static_cast<size_t>(s) * T * RP);
+        v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+      }
+    }
+    const float f[4] = {v.x * sc, v.y * sc, v.z * sc, v.w * sc};
+    __nv_bfloat16 hi[4], lo[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) split_bf16(f[q], hi[q], lo[q]);
+    const uint2 h2 = *reinterpret_cast<const uint2*>(hi), l2 = *reinterpret_cast<const uint2*>(lo);
+    *reinterpret_cast<uint2*>(smem + (row * S::kURow + j) * 2) = h2;
+    *reinterpret_cast<uint2*>(smem + S::kU + (row * S::kURow + j) * 2) = l2;
+    if (u_keep != nullptr && blockIdx.x == 0 && row < tile.z) {
+      const size_t at = static_cast<size_t>(tile.y + row) * RP + j;
+      *reinterpret_cast<uint2*>(u_keep + at) = h2;
+      *reinterpret_cast<uint2*>(u_keep + static_cast<size_t>(T) * RP + at) = l2;
+    }
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  if (warp * 16 < tile.z) {
+    float acc[kTileCols / 8][4];
+#pragma unroll
+    for (int n = 0; n < kTileCols / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < RP; k += 16) {
+      uint32_t ah[4], al[4];
+      const uint32_t at = ((warp * 16 + (lane & 15)) * S::kURow + k + 8 * (lane >> 4)) * 2;
+      ldmatrix_x4(ah, su_hi + at);
+      ldmatrix_x4(al, su_lo + at);
+#pragma unroll
+      for (int n = 0; n < kTileCols; n += 16) {
+        uint32_t b[4];
+        if constexpr (WT)
+          ldmatrix_x4(b, sw + ((n + (lane & 7) + 8 * (lane >> 4)) * S::kWRow + k + 8 * ((lane >> 3) & 1)) * 2);
+        else
+          ldmatrix_x4_trans(b, sw + ((k + (lane & 15)) * S::kWRow + n + 8 * (lane >> 4)) * 2);
+        mma_bf16(acc[n / 8], al, b[0], b[1]);
+        mma_bf16(acc[n / 8 + 1], al, b[2], b[3]);
+        mma_bf16(acc[n / 8], ah, b[0], b[1]);
+        mma_bf16(acc[n / 8 + 1], ah, b[2], b[3]);
+      }
+    }
+    // add the base in place (each element by the thread that holds its sum)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = warp * 16 + (lane >> 2) + 8 * h;
+      if (row < tile.z) {
+#pragma unroll
+        for (int n = 0; n < kTileCols / 8; ++n) {
+          uint8_t* q = sy + row * S::kYRow + (8 * n + 2 * (lane & 3)) * EB;
+          if constexpr (F32) {
+            float2 y = *reinterpret_cast<float2*>(q);
+            y.x += acc[n][2 * h];
+            y.y += acc[n][2 * h + 1];
+            *reinterpret_cast<float2*>(q) = y;
+          } else {
+            const uint32_t y = *reinterpret_cast<uint32_t*>(q);
+            *reinterpret_cast<uint32_t*>(q) = pack_bf16x2(bf16_lo(y) + acc[n][2 * h], bf16_hi(y) + acc[n][2 * h + 1]);
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < tile.z * PIECES; i += kAdThreads) {
+    const int row = i / PIECES, c = (i % PIECES) * PER;
+    if (c0 + c < C)
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) +
+                                (static_cast<size_t>(plan.order[tile.y + row]) * C + c0 + c) * EB) =
+          *reinterpret_cast<const uint4*>(sy + row * S::kYRow + c * EB);
+  }
+}
+
+constexpr int kGradCols = 64;
+template <int RP>
+struct WgradSmem {
+  static constexpr int kXRow = kGradCols + 8;
+  static constexpr int kX = kTileRows * kXRow * 2;
+  static constexpr int kVRow = RP + 8;
+  static constexpr int kV = kTileRows * kVRow * 2;
+  static constexpr int kStage = kX + 2 * kV;
+  static constexpr int kTotal = kStages * kStage;
+};
+
+// G_a[c][j] = sum over the rows t of adapter a of X[t][c] V[position][j], V as
+// its two bf16 parts. OUT_T: G_a is stored [r][C] (dB), else [C][r] (dA). The
+// rows of an adapter come in 64s, each joined in ordinary fp32 adds.
+template <int RP, bool OUT_T>
+__global__ void __launch_bounds__(kAdThreads)
+    adapter_wgrad_kernel(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ V, PlanView plan, int T,
+                         int C, int r, float* __restrict__ G) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  using S = WgradSmem<RP>;
+  const int a_id = blockIdx.y, c0 = blockIdx.x * kGradCols;
+  const bool any = plan_tiles(plan) > 0;
+  const int p0 = any ? plan.seg[a_id] : 0, p1 = any ? plan.seg[a_id + 1] : 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = smem_u32(smem);
+  const int blocks = (p1 - p0 + kTileRows - 1) / kTileRows;
+  auto load = [&](int b, int slot) {
+    const uint32_t sx = base + slot * S::kStage, sv = sx + S::kX;
+    const int q0 = p0 + b * kTileRows, n = min(kTileRows, p1 - q0);
+    const int c = c0 + (tid & 7) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = (tid >> 3) + 16 * i;
+      const bool ok = row < n && c < C;
+      cp_async16(sx + (row * S::kXRow + (tid & 7) * 8) * 2,
+                 ok ? X + static_cast<size_t>(plan.order[q0 + row]) * C + c : X, ok);
+    }
+    for (int i = tid; i < kTileRows * (RP / 8); i += kAdThreads) {
+      const int row = i / (RP / 8), j = (i % (RP / 8)) * 8;
+      const bool ok = row < n;
+      const __nv_bfloat16* p = V + (ok ? static_cast<size_t>(q0 + row) * RP + j : 0);
+      const uint32_t d = sv + (row * S::kVRow + j) * 2;
+      cp_async16(d, p, ok);
+      cp_async16(d + S::kV, p + static_cast<size_t>(T) * RP, ok);
+    }
+  };
+  float acc[RP / 8][4];
+#pragma unroll
+  for (int n = 0; n < RP / 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (s < blocks) load(s, s);
+    cp_async_commit();
+  }
+  int slot = 0;
+  for (int b = 0; b < blocks; ++b) {
+    cp_async_wait<kStages - 2>();
+    __syncthreads();
+    if (b + kStages - 1 < blocks) load(b + kStages - 1, (slot + kStages - 1) % kStages);
+    cp_async_commit();
+    const uint32_t sx = base + slot * S::kStage, sv = sx + S::kX;
+    float part[RP / 8][4];
+#pragma unroll
+    for (int n = 0; n < RP / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[n][i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kTileRows; k += 16) {
+      uint32_t a[4];
+      ldmatrix_x4_trans(a, sx + ((k + (lane & 7) + 8 * (lane >> 4)) * S::kXRow + warp * 16 + 8 * ((lane >> 3) & 1)) * 2);
+#pragma unroll
+      for (int n = 0; n < RP; n += 16) {
+        uint32_t bh[4], bl[4];
+        const uint32_t at = sv + ((k + (lane & 15)) * S::kVRow + n + 8 * (lane >> 4)) * 2;
+        ldmatrix_x4_trans(bh, at);
+        ldmatrix_x4_trans(bl, at + S::kV);
+        mma_bf16(part[n / 8], a, bl[0], bl[1]);
+        mma_bf16(part[n / 8 + 1], a, bl[2], bl[3]);
+        mma_bf16(part[n / 8], a, bh[0], bh[1]);
+        mma_bf16(part[n / 8 + 1], a, bh[2], bh[3]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < RP / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] += part[n][i];
+    slot = (slot + 1) % kStages;
+  }
+  cp_async_wait<0>();
+  float* Ga = G + static_cast<size_t>(a_id) * C * r;
+#pragma unroll
+  for (int n = 0; n < RP / 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + warp * 16 + (lane >> 2) + 8 * (i >> 1), j = 8 * n + 2 * (lane & 3) + (i & 1);
+      if (c < C && j < r) Ga[OUT_T ? static_cast<size_t>(j) * C + c : static_cast<size_t>(c) * r + j] = acc[n][i];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+static int check_adapter(const moe_adapter_config* c) {
+  if (c == nullptr) return MOE_ERR_INVALID_ARG;
+  if (c->T < 1 || c->K < 1 || c->N < 1 || c->L < 1 || c->r < 1) return MOE_ERR_INVALID_ARG;
+  if (c->out_fp32 != 0 && c->out_fp32 != 1) return MOE_ERR_INVALID_ARG;
+  if (c->K % 8 != 0 || c->N % 8 != 0 || c->r % 8 != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (c->r > 128 || c->L > kMaxAdapters || c->T > (1 << 21) || c->K > (1 << 20) || c->N > (1 << 20))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+static int padded_rank(int r) { return r <= 16 ? 16 : (r <= 32 ? 32 : (r <= 64 ? 64 : 128)); }
+
+// Splits of the long axis of a shrink: about four CTAs for each SM
+static int shrink_splits(const moe_adapter_config& c, int C) {
+  const int tiles = c.T / kTileRows + std::min(c.T, c.L);
+  const int nkb = (C + kBlockK - 1) / kBlockK;
+  return std::max(1, std::min({4 * kAdSMs / tiles, nkb, 32}));
+}
+
+struct AdapterWs {
+  size_t parts, du, total;
+};
+static AdapterWs adapter_ws(const moe_adapter_config& c, bool training) {
+  AdapterWs w{};
+  size_t o = 256;
+  auto take = [&](size_t b) {
+    const size_t at = o;
+    o += (b + 255) & ~size_t(255);
+    return at;
+  };
+  const size_t rp = padded_rank(c.r), T = c.T;
+  int s = shrink_splits(c, c.K);
+  if (training) s = std::max(s, shrink_splits(c, c.N));
+  w.parts = take(4 * T * rp * s);
+  if (training) w.du = take(4 * T * rp);
+  w.total = o;
+  return w;
+}
+
+template <class K>
+static cudaError_t allow_smem(K kernel, int bytes) {
+  return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)
+                           : cudaSuccess;
+}
+
+template <int RP, bool WT>
+static cudaError_t launch_shrink(const moe_adapter_config& c, int C, const void* X, const void* W, const PlanView& pv,
+                                 int max_tiles, int splits, float* parts, cudaStream_t s) {
+  constexpr int sm = ShrinkSmem<RP, WT>::kTotal;
+  const cudaError_t e = allow_smem(adapter_shrink_kernel<RP, WT>, sm);
+  if (e != cudaSuccess) return e;
+  adapter_shrink_kernel<RP, WT><<<dim3(max_tiles, splits), kAdThreads, sm, s>>>(
+      static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(W), pv, c.T, C, c.r, splits, parts);
+  return cudaGetLastError();
+}
+template <int RP, bool WT, bool F32>
+static cudaError_t launch_expand(const moe_adapter_config& c, int C, const float* parts, int splits,
+                                 const float* scale, const void* W, const PlanView& pv, int max_tiles,
+                                 const void* base, void* out, void* keep, cudaStream_t s) {
+  constexpr int sm = ExpandSmem<RP, WT, F32>::kTotal;
+  const cudaError_t e = allow_smem(adapter_expand_kernel<RP, WT, F32>, sm);
+  if (e != cudaSuccess) return e;
+  adapter_expand_kernel<RP, WT, F32><<<dim3((C + kTileCols - 1) / kTileCols, max_tiles), kAdThreads, sm, s>>>(
+      parts, splits, scale, static_cast<const __nv_bfloat16*>(W), pv, c.T, C, c.r, base, out,
+      static_cast<__nv_bfloat16*>(keep));
+  return cudaGetLastError();
+}
+template <int RP, bool OUT_T>
+static cudaError_t launch_wgrad(const moe_adapter_config& c, int C, const void* X, const void* V, const PlanView& pv,
+                                float* G, cudaStream_t s) {
+  constexpr int sm = WgradSmem<RP>::kTotal;
+  const cudaError_t e = allow_smem(adapter_wgrad_kernel<RP, OUT_T>, sm);
+  if (e != cudaSuccess) return e;
+  adapter_wgrad_kernel<RP, OUT_T><<<dim3((C + kGradCols - 1) / kGradCols, c.L), kAdThreads, sm, s>>>(
+      static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(V), pv, c.T, C, c.r, G);
+  return cudaGetLastError();
+}
+
+static bool any_misaligned(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0) return true;
+  return false;
+}
+
+#define MOE_RANK(r, ...)                              \
+  do {                                                \
+    switch (padded_rank(r)) {                         \
+      case 16: { constexpr int RP = 16; __VA_ARGS__; break; }   \
+      case 32: { constexpr int RP = 32; __VA_ARGS__; break; }   \
+      case 64: { constexpr int RP = 64; __VA_ARGS__; break; }   \
+      default: { constexpr int RP = 128; __VA_ARGS__; break; }  \
+    }                                                 \
+  } while (0)
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_adapter_plan_bytes(const moe_adapter_config* cfg) {
+  return check_adapter(cfg) != MOE_OK ? 0 : plan_layout(*cfg).total;
+}
+size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg, int training) {
+  return check_adapter(cfg) != MOE_OK ? 0 : adapter_ws(*cfg, training != 0).total;
+}
+size_t moe_adapter_saved_bytes(const moe_adapter_config* cfg) {
+  return check_adapter(cfg) != MOE_OK ? 0 : 4 * static_cast<size_t>(cfg->T) * padded_rank(cfg->r);
+}
+
+int moe_adapter_plan(const moe_adapter_config* cfg, const int32_t* adapter_idx, void* plan, size_t plan_bytes,
+                     void* stream) {
+  NvtxRange nvtx("moe_adapter_plan");
+  const int st = check_adapter(cfg);
+  if (st != MOE_OK) return st;
+  const moe_adapter_config& c = *cfg;
+  if (!adapter_idx || !plan || any_misaligned({adapter_idx, plan})) return MOE_ERR_INVALID_ARG;
+  const PlanLayout L = plan_layout(c);
+  if (plan_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* b = static_cast<uint8_t*>(plan);
+  DevStatus* ds = reinterpret_cast<DevStatus*>(b);
+  int32_t* hist = reinterpret_cast<int32_t*>(b + L.hist);
+  if (L.chunks > 1) {
+    plan_hist_kernel<<<L.chunks, kPlanThreads, 0, s>>>(adapter_idx, c.T, c.L, hist, ds);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return status_from_cuda(e);
+  }
+  plan_place_kernel<<<L.chunks, kPlanThreads, 0, s>>>(
+      adapter_idx, c.T, c.L, L.chunks, L.chunks > 1 ? hist : nullptr, reinterpret_cast<int4*>(b + L.hdr),
+      reinterpret_cast<int32_t*>(b + L.seg), reinterpret_cast<int4*>(b + L.tiles), L.max_tiles,
+      reinterpret_cast<int32_t*>(b + L.order), ds);
+  const int rc = status_from_cuda(cudaGetLastError());
+  record_stage(s, 45, L.chunks > 1 ? 2 : 1);
+  return rc;
+}
+
+int moe_adapter_fwd(const moe_adapter_config* cfg, const moe_bf16* x, const moe_bf16* A, const moe_bf16* B,
+                    const float* scale, const void* plan, const void* base, void* y, void* u_saved, void* ws,
+                    size_t ws_bytes, void* stream) {
+  NvtxRange nvtx("moe_adapter_fwd");
+  const int st = check_adapter(cfg);
+  if (st != MOE_OK) return st;
+  const moe_adapter_config& c = *cfg;
+  if (!x || !A || !B || !scale || !plan || !y || !ws || any_misaligned({x, A, B, scale, plan, base, y, u_saved, ws}))
+    return MOE_ERR_INVALID_ARG;
+  const AdapterWs L = adapter_ws(c, false);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const PlanLayout P = plan_layout(c);
+  const PlanView pv = plan_view(c, plan, P, ws);
+  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.parts);
+  const int splits = shrink_splits(c, c.K);
+  cudaError_t e = cudaSuccess;
+  MOE_RANK(c.r, e = launch_shrink<RP, false>(c, c.K, x, A, pv, P.max_tiles, splits, parts, s));
+  if (e != cudaSuccess) return status_from_cuda(e);
+  record_stage(s, 46, 1);
+  if (c.out_fp32)
+    MOE_RANK(c.r, e = launch_expand<RP, false, true>(c, c.N, parts, splits, scale, B, pv, P.max_tiles, base, y, u_saved, s));
+  else
+    MOE_RANK(c.r, e = launch_expand<RP, false, false>(c, c.N, parts, splits, scale, B, pv, P.max_tiles, base, y, u_saved, s));
+  record_stage(s, 47, 1);
+  return status_from_cuda(e);
+}
+
+int moe_adapter_bwd(const moe_adapter_config* cfg, const moe_bf16* dy, const moe_bf16* x, const moe_bf16* A,
+                    const moe_bf16* B, const float* scale, const void* plan, const void* u_saved, const void* dx_base,
+                    void* dx, float* dA, float* dB, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx("moe_adapter_bwd");
+  const int st = check_adapter(cfg);
+  if (st != MOE_OK) return st;
+  const moe_adapter_config& c = *cfg;
+  if (!dy || !x || !A || !B || !scale || !plan || !u_saved || !dx || !dA || !dB || !ws ||
+      any_misaligned({dy, x, A, B, scale, plan, u_saved, dx_base, dx, dA, dB, ws}))
+    return MOE_ERR_INVALID_ARG;
+  const AdapterWs L = adapter_ws(c, true);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const PlanLayout P = plan_layout(c);
+  const PlanView pv = plan_view(c, plan, P, ws);
+  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.parts);
+  void* du = static_cast<uint8_t*>(ws) + L.du;
+  const int splits = shrink_splits(c, c.N);
+  cudaError_t e = cudaSuccess;
+  MOE_RANK(c.r, e = launch_shrink<RP, true>(c, c.N, dy, B, pv, P.max_tiles, splits, parts, s));
+  if (e != cudaSuccess) return status_from_cuda(e);
+  record_stage(s, 46, 1);
+  if (c.out_fp32)
+    MOE_RANK(c.r, e = launch_expand<RP, true, true>(c, c.K, parts, splits, scale, A, pv, P.max_tiles, dx_base, dx, du, s));
+  else
+    MOE_RANK(c.r, e = launch_expand<RP, true, false>(c, c.K, parts, splits, scale, A, pv, P.max_tiles, dx_base, dx, du, s));
+  if (e != cudaSuccess) return status_from_cuda(e);
+  record_stage(s, 47, 1);
+  MOE_RANK(c.r, e = launch_wgrad<RP, false>(c, c.K, x, du, pv, dA, s));
+  if (e != cudaSuccess) return status_from_cuda(e);
+  record_stage(s, 48, 1);
+  MOE_RANK(c.r, e = launch_wgrad<RP, true>(c, c.N, dy, u_saved, pv, dB, s));
+  record_stage(s, 48, 1);
+  return status_from_cuda(e);
+}
+
+}  // extern "C"

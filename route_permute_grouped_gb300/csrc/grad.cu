@@ -1,0 +1,473 @@
+// Global norm of a list of gradients and its clipping: one pass that sums the
+// squares (or takes the maximum) of every tensor, one that scales.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+#include <vector>
+
+#include "host_util.h"
+
+namespace moe {
+
+// A tensor list as the kernels take it: the tensors of one launch by value in
+// the kernel's parameters, so a call copies nothing to the device and captures
+// into a graph as it is. A chunk is kChunkVecs 16-byte vectors of one tensor;
+// `first` holds each tensor's first chunk.
+constexpr int kListTensors = 768;
+constexpr int kGradThreads = 512;
+constexpr int kVecsPerThread = 4;
+constexpr int kChunkVecs = kGradThreads * kVecsPerThread;  // 32 KB
+constexpr int kMaxLaunches = 64;                           // 49152 tensors
+constexpr int kMaxPartials = 2048;                         // CTAs of one launch
+
+struct GradItem {
+  const void* in;
+  void* out;
+  long long n;
+};
+template <int N>
+struct GradBlock {
+  int count;    // tensors
+  int chunks;   // chunks of all of them
+  int first[N];
+  uint8_t dtype[N];
+  GradItem item[N];
+};
+struct GradList {
+  uint32_t magic;
+  int n, launches, pad;
+  GradBlock<kListTensors> block[1];  // `launches` of them
+};
+constexpr uint32_t kListMagic = 0x6d6f6c31u;
+
+static size_t list_bytes(int n) {
+  const int launches = (n + kListTensors - 1) / kListTensors;
+  return offsetof(GradList, block) + sizeof(GradBlock<kListTensors>) * static_cast<size_t>(launches > 0 ? launches : 1);
+}
+static int elem_bytes(int dtype) { return dtype == MOE_FP32 ? 4 : 2; }
+
+// Where the 16-byte vectors of a tensor begin: elements before the first
+// aligned address (at most n), the vectors, and the elements after them.
+struct Span {
+  int head;
+  long long vecs;
+  int tail;
+};
+__host__ __device__ inline Span span_of(const void* p, long long n, int eb) {
+  Span s;
+  const int per = 16 / eb;
+  const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
+  long long head = mis == 0 ? 0 : (16 - mis) / eb;
+  if (head > n) head = n;
+  s.head = static_cast<int>(head);
+  s.vecs = (n - head) / per;
+  s.tail = static_cast<int>(n - head - s.vecs * per);
+  return s;
+}
+
+template <int N>
+__device__ __forceinline__ int find_tensor(const GradBlock<N>& b, int chunk) {
+  int lo = 0, hi = b.count;  // the last tensor whose first chunk is <= chunk
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (b.first[mid] <= chunk) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ float elem_f32(const void* p, long long i, int dtype) {
+  if (dtype == MOE_FP32) return static_cast<const float*>(p)[i];
+  if (dtype == MOE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+__device__ __forceinline__ void store_elem(void* p, long long i, int dtype, float v) {
+  if (dtype == MOE_FP32) static_cast<float*>(p)[i] = v;
+  else if (dtype == MOE_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+// the 4 or 8 values of a 16-byte vector
+template <int DT>
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[DT == MOE_FP32 ? 4 : 8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (DT == MOE_FP32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == MOE_BF16) {
+        f[2 * i] = bf16_lo(w[i]);
+        f[2 * i + 1] = bf16_hi(w[i]);
+      } else {
+        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        f[2 * i] = h.x;
+        f[2 * i + 1] = h.y;
+      }
+    }
+  }
+}
+template <int DT>
+__device__ __forceinline__ uint4 pack(const float (&f)[DT == MOE_FP32 ? 4 : 8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == MOE_FP32) w[i] = __float_as_uint(f[i]);
+    else if constexpr (DT == MOE_BF16) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    else {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Squares of a group of values, added to the thread's double sum. In fp32 a
+// square leaves the range for |g| above 2^64 and loses its bits below 2^-63,
+// so a group whose largest magnitude lies outside [2^-60, 2^60] (and is not 0)
+// is squared in fp64; NaN and infinities take that way too. Elsewhere the
+// group's squares (16 or 32 of them) are added in fp32 and the groups in fp64:
+// 1/16 or 1/32 of the additions, which the small FP64 rate carries.
+constexpr uint32_t kSquareLo = (127u - 60u) << 23, kSquareHi = (127u + 60u) << 23;
+template <int NV>
+__device__ __forceinline__ double squares(const float (&f)[NV], uint32_t& top) {
+  float s = 0.0f;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    s = fmaf(f[i], f[i], s);
+    m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+  }
+  top = max(top, m);
+  if (m <= kSquareHi && (m >= kSquareLo || m == 0)) return s;
+  double d = 0.0;
+  for (int i = 0; i < NV; ++i) d += static_cast<double>(f[i]) * f[i];
+  return d;
+}
+
+template <int DT>
+__device__ __forceinline__ void norm_chunk(const uint4* __restrict__ v, long long vecs, long long at, double& sum,
+                                           uint32_t& top) {
+  constexpr int PER = DT == MOE_FP32 ? 4 : 8;
+  uint4 w[kVecsPerThread];
+#pragma unroll
+  for (int j = 0; j < kVecsPerThread; ++j) {
+    const long long i = at + j * kGradThreads + threadIdx.x;
+    w[j] = i < vecs ? __ldg(v + i) : make_uint4(0, 0, 0, 0);
+  }
+  float f[kVecsPerThread * PER];
+#pragma unroll
+  for (int j = 0; j < kVecsPerThread; ++j) {
+    float g[PER];
+    unpack<DT>(w[j], g);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) f[j * PER + i] = g[i];
+  }
+  sum += squares(f, top);
+}
+
+// One CTA takes chunks blockIdx, blockIdx + gridDim, ...; its sum (fp64) and
+// largest magnitude (fp32 bits: NaN above infinity above the finite values) go
+// to partials[blockIdx], added in a fixed order afterwards.
+struct NormPartial {
+  double sum;
+  unsigned long long top;
+};
+template <int N>
+__global__ void __launch_bounds__(kGradThreads) norm_kernel(const __grid_constant__ GradBlock<N> b,
+                                                            NormPartial* __restrict__ partials) {
+  double sum = 0.0;
+  uint32_t top = 0;
+  for (int c = blockIdx.x; c < b.chunks; c += gridDim.x) {
+    const int t = find_tensor(b, c);
+    const int dt = b.dtype[t];
+    const GradItem it = b.item[t];
+    const int eb = dt == MOE_FP32 ? 4 : 2;
+    const Span sp = span_of(it.in, it.n, eb);
+    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(it.in) + static_cast<size_t>(sp.head) * eb);
+    const long long at = static_cast<long long>(c - b.first[t]) * kChunkVecs;
+    if (dt == MOE_FP32) norm_chunk<MOE_FP32>(v, sp.vecs, at, sum, top);
+    else if (dt == MOE_BF16) norm_chunk<MOE_BF16>(v, sp.vecs, at, sum, top);
+    else norm_chunk<MOE_FP16>(v, sp.vecs, at, sum, top);
+    if (at == 0 && threadIdx.x < static_cast<unsigned>(sp.head + sp.tail)) {
+      const long long i = threadIdx.x < static_cast<unsigned>(sp.head) ? threadIdx.x : it.n - sp.tail + (threadIdx.x - sp.head);
+      const float f[1] = {elem_f32(it.in, i, dt)};
+      sum += squares(f, top);
+    }
+  }
+  __shared__ double s_sum[kGradThreads / 32];
+  __shared__ uint32_t s_top[kGradThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  }
+  if ((threadIdx.x & 31) == 0) {
+    s_sum[threadIdx.x >> 5] = sum;
+    s_top[threadIdx.x >> 5] = top;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kGradThreads / 32; ++w) {
+      sum += s_sum[w];
+      top = max(top, s_top[w]);
+    }
+    partials[blockIdx.x].sum = sum;
+    partials[blockIdx.x].top = top;
+  }
+}
+
+// The norm from the partials, by every thread of a CTA in the same fixed order.
+__device__ __forceinline__ float join_norm(const NormPartial* __restrict__ partials, int n, int kind) {
+  __shared__ double s_sum[kGradThreads];
+  __shared__ uint32_t s_top[kGradThreads];
+  double sum = 0.0;
+  uint32_t top = 0;
+  for (int i = threadIdx.x; i < n; i += kGradThreads) {
+    sum += partials[i].sum;
+    top = max(top, static_cast<uint32_t>(partials[i].top));
+  }
+  s_sum[threadIdx.x] = sum;
+  s_top[threadIdx.x] = top;
+  __syncthreads();
+  for (int st = kGradThreads / 2; st > 0; st >>= 1) {
+    if (threadIdx.x < static_cast<unsigned>(st)) {
+      s_sum[threadIdx.x] += s_sum[threadIdx.x + st];
+      s_top[threadIdx.x] = max(s_top[threadIdx.x], s_top[threadIdx.x + st]);
+    }
+    __syncthreads();
+  }
+  return kind == MOE_NORM_MAX ? __uint_as_float(s_top[0]) : static_cast<float>(sqrt(s_sum[0]));
+}
+
+__global__ void __launch_bounds__(kGradThreads) norm_join_kernel(const NormPartial* __restrict__ partials, int n,
+                                                                 int kind, float* __restrict__ norm) {
+  const float v = join_norm(partials, n, kind);
+  if (threadIdx.x == 0) *norm = v;
+}
+
+template <int DT>
+__device__ __forceinline__ void scale_chunk(const uint4* __restrict__ v, uint4* __restrict__ o, long long vecs,
+                                            long long at, float coef) {
+  constexpr int PER = DT == MOE_FP32 ? 4 : 8;
+  uint4 w[kVecsPerThread];
+#pragma unroll
+  for (int j = 0; j < kVecsPerThread; ++j) {
+    const long long i = at + j * kGradThreads + threadIdx.x;
+    if (i < vecs) w[j] = v[i];
+  }
+#pragma unroll
+  for (int j = 0; j < kVecsPerThread; ++j) {
+    const long long i = at + j * kGradThreads + threadIdx.x;
+    if (i < vecs) {
+      float f[PER];
+      unpack<DT>(w[j], f);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) f[e] *= coef;
+      o[i] = pack<DT>(f);
+    }
+  }
+}
+
+// g = round(g * coef), coef = min(1, max_norm / (norm + 1e-6)) (NaN for a NaN
+// norm). coef = 1 leaves every bit as it is, so tensors scaled in place are
+// then neither read nor written.
+template <int N>
+__global__ void __launch_bounds__(kGradThreads) clip_kernel(const __grid_constant__ GradBlock<N> b,
+                                                            const NormPartial* __restrict__ partials, int n_partials,
+                                                            int kind, float max_norm, float* __restrict__ norm_out) {
+  const float norm = join_norm(partials, n_partials, kind);
+  if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
+  float coef = max_norm / (norm + 1e-6f);
+  if (coef > 1.0f) coef = 1.0f;
+  for (int c = blockIdx.x; c < b.chunks; c += gridDim.x) {
+    const int t = find_tensor(b, c);
+    const int dt = b.dtype[t];
+    const GradItem it = b.item[t];
+    if (coef == 1.0f && it.in == it.out) continue;
+    const int eb = dt == MOE_FP32 ? 4 : 2;
+    const Span sp = span_of(it.in, it.n, eb);
+    const long long at = static_cast<long long>(c - b.first[t]) * kChunkVecs;
+    const size_t skip = static_cast<size_t>(sp.head) * eb;
+    uint8_t* ob = static_cast<uint8_t*>(it.out) + skip;
+    if ((reinterpret_cast<uintptr_t>(ob) & 15u) == 0) {
+      const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(it.in) + skip);
+      uint4* o = reinterpret_cast<uint4*>(ob);
+      if (dt == MOE_FP32) scale_chunk<MOE_FP32>(v, o, sp.vecs, at, coef);
+      else if (dt == MOE_BF16) scale_chunk<MOE_BF16>(v, o, sp.vecs, at, coef);
+      else scale_chunk<MOE_FP16>(v, o, sp.vecs, at, coef);
+    } else {
+      // the output is aligned otherwise than the input: element by element
+      const int per = 16 / eb;
+      const long long end = min(sp.vecs, at + kChunkVecs) * per;
+      for (long long i = at * per + threadIdx.x; i < end; i += kGradThreads)
+        store_elem(it.out, sp.head + i, dt, elem_f32(it.in, sp.head + i, dt) * coef);
+    }
+    if (at == 0 && threadIdx.x < static_cast<unsigned>(sp.head + sp.tail)) {
+      const long long i = threadIdx.x < static_cast<unsigned>(sp.head) ? threadIdx.x : it.n - sp.tail + (threadIdx.x - sp.head);
+      store_elem(it.out, i, dt, elem_f32(it.in, i, dt) * coef);
+    }
+  }
+}
+
+static int grad_grid(int chunks) { return std::max(1, std::min(chunks, std::min(4 * num_sms(), kMaxPartials))); }
+
+// launches `f` with the block in the smallest parameter size that holds it
+template <class F>
+static cudaError_t with_block(const GradBlock<kListTensors>& b, F f) {
+  auto copy = [&](auto& small) {
+    small.count = b.count;
+    small.chunks = b.chunks;
+    memcpy(small.first, b.first, sizeof(int) * b.count);
+    memcpy(small.dtype, b.dtype, b.count);
+    memcpy(small.item, b.item, sizeof(GradItem) * b.count);
+    f(small);
+  };
+  if (b.count <= 16) {
+    GradBlock<16> s;
+    copy(s);
+  } else if (b.count <= 128) {
+    GradBlock<128> s;
+    copy(s);
+  } else {
+    f(b);
+  }
+  return cudaGetLastError();
+}
+
+static const GradList* as_list(const void* list) {
+  const GradList* l = static_cast<const GradList*>(list);
+  return l != nullptr && (reinterpret_cast<uintptr_t>(list) & 7u) == 0 && l->magic == kListMagic ? l : nullptr;
+}
+
+static int run_norm(const GradList& l, NormPartial* partials, int* n_partials, cudaStream_t s) {
+  int at = 0;
+  for (int i = 0; i < l.launches; ++i) {
+    const int grid = grad_grid(l.block[i].chunks);
+    const cudaError_t e = with_block(l.block[i], [&](const auto& b) {
+      norm_kernel<<<grid, kGradThreads, 0, s>>>(b, partials + at);
+    });
+    if (e != cudaSuccess) return status_from_cuda(e);
+    record_stage(s, 40, 1);
+    at += grid;
+  }
+  *n_partials = at;
+  return MOE_OK;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_tensor_list_bytes(int n) { return n < 0 || n > kMaxLaunches * kListTensors ? 0 : list_bytes(n); }
+
+int moe_tensor_list_build(const moe_tensor* ts, int n, void* list, size_t list_size) {
+  if (n < 0 || (ts == nullptr && n > 0) || list == nullptr || (reinterpret_cast<uintptr_t>(list) & 7u) != 0)
+    return MOE_ERR_INVALID_ARG;
+  if (n > kMaxLaunches * kListTensors) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (list_size < list_bytes(n)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  struct Range {
+    uintptr_t lo, hi;
+    int id;
+    bool write;
+  };
+  std::vector<Range> ranges;
+  try {
+    ranges.reserve(2 * static_cast<size_t>(n));
+  } catch (...) {
+    return MOE_ERR_INVALID_ARG;
+  }
+  GradList* l = static_cast<GradList*>(list);
+  l->magic = 0;
+  l->n = n;
+  l->pad = 0;
+  l->launches = std::max(1, (n + kListTensors - 1) / kListTensors);
+  for (int i = 0; i < l->launches; ++i) l->block[i].count = l->block[i].chunks = 0;
+  for (int i = 0; i < n; ++i) {
+    const moe_tensor& t = ts[i];
+    if (t.dtype != MOE_FP32 && t.dtype != MOE_BF16 && t.dtype != MOE_FP16) return MOE_ERR_INVALID_ARG;
+    if (t.n < 0 || (t.n > 0 && t.data == nullptr)) return MOE_ERR_INVALID_ARG;
+    const int eb = elem_bytes(t.dtype);
+    void* out = t.out != nullptr ? t.out : t.data;
+    if (reinterpret_cast<uintptr_t>(t.data) % eb != 0 || reinterpret_cast<uintptr_t>(out) % eb != 0)
+      return MOE_ERR_INVALID_ARG;
+    if (t.n >= (1ll << 42)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (t.n == 0) continue;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(t.data), o = reinterpret_cast<uintptr_t>(out);
+    const size_t bytes = static_cast<size_t>(t.n) * eb;
+    if (out != t.data) ranges.push_back({a, a + bytes, i, false});
+    ranges.push_back({o, o + bytes, i, true});
+    GradBlock<kListTensors>& b = l->block[i / kListTensors];
+    const Span sp = span_of(t.data, t.n, eb);
+    const long long chunks = std::max(1ll, (sp.vecs + kChunkVecs - 1) / kChunkVecs);
+    if (b.chunks + chunks > (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    b.first[b.count] = b.chunks;
+    b.dtype[b.count] = static_cast<uint8_t>(t.dtype);
+    b.item[b.count] = {t.data, out, t.n};
+    b.chunks += static_cast<int>(chunks);
+    ++b.count;
+  }
+  // what is written must not be read or written for another tensor: two CTAs
+  // would race, and a tensor listed twice would be scaled twice
+  std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t read_end = 0, write_end = 0;
+  for (const Range& r : ranges) {
+    if (r.lo < write_end || (r.write && r.lo < read_end)) return MOE_ERR_INVALID_ARG;
+    (r.write ? write_end : read_end) = std::max(r.write ? write_end : read_end, r.hi);
+  }
+  l->magic = kListMagic;
+  return MOE_OK;
+}
+
+size_t moe_grad_norm_workspace_bytes(void) {
+  return 256 + sizeof(NormPartial) * static_cast<size_t>(kMaxLaunches) * kMaxPartials;
+}
+
+int moe_grad_norm(const void* list, int kind, float* norm, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx("moe_grad_norm");
+  const GradList* l = as_list(list);
+  if (l == nullptr || norm == nullptr || ws == nullptr || (kind != MOE_NORM_L2 && kind != MOE_NORM_MAX))
+    return MOE_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(norm) | reinterpret_cast<uintptr_t>(ws)) & 15u) != 0)
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_grad_norm_workspace_bytes()) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  NormPartial* partials = reinterpret_cast<NormPartial*>(static_cast<uint8_t*>(ws) + 256);
+  int n = 0;
+  const int st = run_norm(*l, partials, &n, s);
+  if (st != MOE_OK) return st;
+  norm_join_kernel<<<1, kGradThreads, 0, s>>>(partials, n, kind, norm);
+  const int rc = status_from_cuda(cudaGetLastError());
+  record_stage(s, 41, 1);
+  return rc;
+}
+
+int moe_clip_grad_norm(const void* list, int kind, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                       void* stream) {
+  NvtxRange nvtx("moe_clip_grad_norm");
+  const GradList* l = as_list(list);
+  if (l == nullptr || norm == nullptr || ws == nullptr || (kind != MOE_NORM_L2 && kind != MOE_NORM_MAX) ||
+      !(max_norm >= 0.0f))
+    return MOE_ERR_INVALID_ARG;
+  if (((reinterpret_cast<uintptr_t>(norm) | reinterpret_cast<uintptr_t>(ws)) & 15u) != 0)
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_grad_norm_workspace_bytes()) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  NormPartial* partials = reinterpret_cast<NormPartial*>(static_cast<uint8_t*>(ws) + 256);
+  int n = 0;
+  const int st = run_norm(*l, partials, &n, s);
+  if (st != MOE_OK) return st;
+  for (int i = 0; i < l->launches; ++i) {
+    const cudaError_t e = with_block(l->block[i], [&](const auto& b) {
+      clip_kernel<<<grad_grid(b.chunks), kGradThreads, 0, s>>>(b, partials, n, kind, max_norm,
+                                                               i == 0 ? norm : nullptr);
+    });
+    if (e != cudaSuccess) return status_from_cuda(e);
+    record_stage(s, 42, 1);
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"

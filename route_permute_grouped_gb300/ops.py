@@ -157,6 +157,29 @@ def lib():
         for n in ("moe_nv_quantize_bwd_weights", "moe_nv_quantize_train_weights", "moe_layer_fwd_nvfp4_train",
                   "moe_layer_bwd_nvfp4"):
             getattr(L, n).restype = c_int
+        for n in ("moe_balance_workspace_bytes", "moe_balance_stats_floats"):
+            getattr(L, n).restype = c_size_t
+            getattr(L, n).argtypes = [POINTER(MoeBalanceConfig)]
+        L.moe_balance_loss_fwd.argtypes = [POINTER(MoeBalanceConfig)] + [vp] * 8 + [c_size_t, vp]
+        L.moe_balance_loss_bwd.argtypes = [POINTER(MoeBalanceConfig)] + [vp] * 7
+        for n in ("moe_adapter_plan_bytes", "moe_adapter_saved_bytes"):
+            getattr(L, n).restype = c_size_t
+            getattr(L, n).argtypes = [POINTER(MoeAdapterConfig)]
+        L.moe_adapter_workspace_bytes.restype = c_size_t
+        L.moe_adapter_workspace_bytes.argtypes = [POINTER(MoeAdapterConfig), c_int]
+        L.moe_adapter_plan.argtypes = [POINTER(MoeAdapterConfig), vp, vp, c_size_t, vp]
+        L.moe_adapter_fwd.argtypes = [POINTER(MoeAdapterConfig)] + [vp] * 9 + [c_size_t, vp]
+        L.moe_adapter_bwd.argtypes = [POINTER(MoeAdapterConfig)] + [vp] * 12 + [c_size_t, vp]
+        L.moe_tensor_list_bytes.restype = c_size_t
+        L.moe_tensor_list_bytes.argtypes = [c_int]
+        L.moe_tensor_list_build.argtypes = [POINTER(MoeTensor), c_int, vp, c_size_t]
+        L.moe_grad_norm_workspace_bytes.restype = c_size_t
+        L.moe_grad_norm_workspace_bytes.argtypes = []
+        L.moe_grad_norm.argtypes = [vp, c_int, vp, vp, c_size_t, vp]
+        L.moe_clip_grad_norm.argtypes = [vp, c_int, c_float, vp, vp, c_size_t, vp]
+        for n in ("moe_balance_loss_fwd", "moe_balance_loss_bwd", "moe_adapter_plan", "moe_adapter_fwd",
+                  "moe_adapter_bwd", "moe_tensor_list_build", "moe_grad_norm", "moe_clip_grad_norm"):
+            getattr(L, n).restype = c_int
         _lib = L
     return _lib
 
@@ -167,7 +190,9 @@ STAGE_NAMES = {20: "nv_quantize", 21: "nv_gemm", 22: "mx_quantize_tokens", 24: "
                6: "shared_down", 7: "combine", 10: "combine_bwd", 11: "router_bwd_elem", 12: "dgrad_down_swiglu",
                13: "wgrad_down", 14: "dgrad_gate_up", 15: "wgrad_gate_up", 16: "router_dgrad",
                17: "permute_bwd", 18: "router_wgrad", 19: "aux_loss", 30: "read_ceiling",
-               31: "write_ceiling", 32: "nv_dgrad_down", 33: "nv_swiglu_bwd", 34: "nv_dgrad_gate_up"}
+               31: "write_ceiling", 40: "grad_norm", 41: "grad_norm_join", 42: "grad_clip", 43: "balance_loss",
+               44: "balance_loss_bwd", 45: "adapter_plan", 46: "adapter_shrink", 47: "adapter_expand",
+               48: "adapter_wgrad", 32: "nv_dgrad_down", 33: "nv_swiglu_bwd", 34: "nv_dgrad_gate_up"}
 
 
 def profile_start(capacity: int) -> None:
@@ -740,3 +765,282 @@ def layer_bwd_nvfp4(cfg, dO, x, router_w, nvbw, saved, ws=None, grads=None):
                                    _p(g["dW3"]), _p(g["dW2"]), _p(g["aux_loss"]), _p(ws), ws.numel(), _stream())
     _check(st, "moe_layer_bwd_nvfp4")
     return g
+
+
+# ---------------------------------------------------------------------------
+# Router losses with gradients
+# ---------------------------------------------------------------------------
+def _arg(where, name, t, dtype, shape, optional=False):
+    """A tensor argument of the calls below: on the current CUDA device,
+    contiguous, of the given type (or one of them) and shape; its pointer."""
+    if t is None:
+        if optional:
+            return None
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} is missing")
+    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
+        got = f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
+        want = " or ".join(str(d) for d in dtypes)
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} must be {want} {tuple(shape)}, not {got}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} must be on the current CUDA device, not {t.device}")
+    if not t.is_contiguous():
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} must be contiguous")
+    return c_void_p(t.data_ptr())
+
+
+def _ws_arg(where, ws, nbytes):
+    if ws is None or not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: the workspace must be a uint8 tensor")
+    p = _arg(where, "ws", ws, torch.uint8, ws.shape)
+    if ws.numel() < nbytes:
+        raise MoeError(MOE_ERR_WORKSPACE_TOO_SMALL, where)
+    return p
+
+
+def _scratch(nbytes, device):
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws[:256].zero_()  # device status word
+    return ws
+
+
+class MoeBalanceConfig(ctypes.Structure):
+    _fields_ = [("T", c_int), ("E", c_int), ("k", c_int), ("n_seqs", c_int), ("score", c_int),
+                ("balance_coeff", c_float), ("z_coeff", c_float)]
+
+
+def make_balance_config(T, E, k, n_seqs=1, score="softmax", balance_coeff=1e-2, z_coeff=0.0) -> MoeBalanceConfig:
+    return MoeBalanceConfig(T, E, k, n_seqs, SCORE[score] if isinstance(score, str) else score, balance_coeff, z_coeff)
+
+
+def _balance_sizes(cfg):
+    n = int(lib().moe_balance_workspace_bytes(ctypes.byref(cfg)))
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_balance_workspace_bytes")
+    return n, int(lib().moe_balance_stats_floats(ctypes.byref(cfg)))
+
+
+def balance_workspace(cfg, device="cuda"):
+    return _scratch(_balance_sizes(cfg)[0], device)
+
+
+def balance_loss_fwd(cfg, logits, topk_idx, seq_offsets=None, token_mask=None, ws=None):
+    """The router's balance loss and z-loss (cfg from make_balance_config):
+    (losses [2] fp32, counts [n_seqs, E] int32, stats for the backward).
+    logits [T, E] fp32, topk_idx [T, k] int32, seq_offsets [n_seqs + 1] int32
+    (None with one sequence: all rows), token_mask [T] bool or uint8."""
+    w = "balance_loss_fwd"
+    n_ws, n_stats = _balance_sizes(cfg)
+    args = [_arg(w, "logits", logits, torch.float32, (cfg.T, cfg.E)),
+            _arg(w, "topk_idx", topk_idx, torch.int32, (cfg.T, cfg.k)),
+            _arg(w, "seq_offsets", seq_offsets, torch.int32, (cfg.n_seqs + 1,), optional=True),
+            _arg(w, "token_mask", token_mask, (torch.bool, torch.uint8), (cfg.T,), optional=True)]
+    dev = logits.device
+    losses = torch.empty(2, dtype=torch.float32, device=dev)
+    counts = torch.empty((cfg.n_seqs, cfg.E), dtype=torch.int32, device=dev)
+    stats = torch.empty(n_stats, dtype=torch.float32, device=dev)
+    ws = _scratch(n_ws, dev) if ws is None else ws
+    st = lib().moe_balance_loss_fwd(ctypes.byref(cfg), *args, _p(losses), _p(counts), _p(stats),
+                                    _ws_arg(w, ws, n_ws), ws.numel(), _stream())
+    _check(st, "moe_balance_loss_fwd")
+    return losses, counts, stats
+
+
+def balance_loss_bwd(cfg, logits, stats, dlosses=None, seq_offsets=None, token_mask=None, dlogits=None):
+    """Gradient of <dlosses, losses> for the logits, [T, E] fp32 (dlosses [2]
+    fp32; None: 1 and 1). ``layer_bwd(..., dlogits=...)`` adds it to the layer's
+    own router gradient."""
+    w = "balance_loss_bwd"
+    n_stats = _balance_sizes(cfg)[1]
+    args = [_arg(w, "logits", logits, torch.float32, (cfg.T, cfg.E)),
+            _arg(w, "stats", stats, torch.float32, (n_stats,)),
+            _arg(w, "dlosses", dlosses, torch.float32, (2,), optional=True),
+            _arg(w, "seq_offsets", seq_offsets, torch.int32, (cfg.n_seqs + 1,), optional=True),
+            _arg(w, "token_mask", token_mask, (torch.bool, torch.uint8), (cfg.T,), optional=True)]
+    if dlogits is None:
+        dlogits = torch.empty((cfg.T, cfg.E), dtype=torch.float32, device=logits.device)
+    st = lib().moe_balance_loss_bwd(ctypes.byref(cfg), *args, _arg(w, "dlogits", dlogits, torch.float32,
+                                                                   (cfg.T, cfg.E)), _stream())
+    _check(st, "moe_balance_loss_bwd")
+    return dlogits
+
+
+# ---------------------------------------------------------------------------
+# Low-rank adapters of many requests beside a shared projection
+# ---------------------------------------------------------------------------
+class MoeAdapterConfig(ctypes.Structure):
+    _fields_ = [("T", c_int), ("K", c_int), ("N", c_int), ("L", c_int), ("r", c_int), ("out_fp32", c_int)]
+
+
+def make_adapter_config(T, K, N, L, r, out_fp32=False) -> MoeAdapterConfig:
+    """T rows, a projection of K inputs and N outputs, L adapters of rank r."""
+    return MoeAdapterConfig(T, K, N, L, r, int(out_fp32))
+
+
+def _adapter_bytes(fn, cfg, *more):
+    n = int(fn(ctypes.byref(cfg), *more))
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, fn.__name__)
+    return n
+
+
+def adapter_workspace(cfg, training=False, device="cuda"):
+    return _scratch(_adapter_bytes(lib().moe_adapter_workspace_bytes, cfg, int(training)), device)
+
+
+def alloc_adapter_saved(cfg, device="cuda"):
+    """What the training forward keeps for the backward (an opaque buffer)."""
+    return torch.empty(_adapter_bytes(lib().moe_adapter_saved_bytes, cfg), dtype=torch.uint8, device=device)
+
+
+def adapter_plan(cfg, adapter_idx, plan=None):
+    """The plan of a batch (a uint8 tensor): its rows ordered by adapter.
+    adapter_idx [T] int32, negative for a row without an adapter. One plan
+    serves every projection of the batch, forward and backward, whose config
+    has the same T and L. device_status(plan) tells of an index >= L."""
+    w = "adapter_plan"
+    n = _adapter_bytes(lib().moe_adapter_plan_bytes, cfg)
+    idx = _arg(w, "adapter_idx", adapter_idx, torch.int32, (cfg.T,))
+    plan = _scratch(n, adapter_idx.device) if plan is None else plan
+    _check(lib().moe_adapter_plan(ctypes.byref(cfg), idx, _ws_arg(w, plan, n), plan.numel(), _stream()),
+           "moe_adapter_plan")
+    return plan
+
+
+def _adapter_args(w, cfg, A, B, scale, plan):
+    return (_arg(w, "A", A, torch.bfloat16, (cfg.L, cfg.K, cfg.r)),
+            _arg(w, "B", B, torch.bfloat16, (cfg.L, cfg.r, cfg.N)),
+            _arg(w, "scale", scale, torch.float32, (cfg.L,)),
+            _ws_arg(w, plan, _adapter_bytes(lib().moe_adapter_plan_bytes, cfg)))
+
+
+def adapter_fwd(cfg, x, A, B, scale, plan, base=None, y=None, u=None, ws=None):
+    """y [T, N] = base + scale (x A) B with each row's own adapter (plan from
+    adapter_plan). x [T, K], A [L, K, r], B [L, r, N] bf16, scale [L] fp32;
+    base and y bf16 (fp32 with cfg.out_fp32). base None: zeros; y may be base.
+    u (alloc_adapter_saved): keep what adapter_bwd needs."""
+    w = "adapter_fwd"
+    xp = _arg(w, "x", x, torch.bfloat16, (cfg.T, cfg.K))
+    weights = _adapter_args(w, cfg, A, B, scale, plan)
+    bp = _arg(w, "base", base, _out_dtype(cfg), (cfg.T, cfg.N), optional=True)
+    up = None if u is None else _ws_arg(w, u, _adapter_bytes(lib().moe_adapter_saved_bytes, cfg))
+    ws = adapter_workspace(cfg, False, x.device) if ws is None else ws
+    wp = _ws_arg(w, ws, _adapter_bytes(lib().moe_adapter_workspace_bytes, cfg, 0))
+    if y is None:
+        y = torch.empty((cfg.T, cfg.N), dtype=_out_dtype(cfg), device=x.device)
+    st = lib().moe_adapter_fwd(ctypes.byref(cfg), xp, *weights, bp, _arg(w, "y", y, _out_dtype(cfg), (cfg.T, cfg.N)),
+                               up, wp, ws.numel(), _stream())
+    _check(st, "moe_adapter_fwd")
+    return y
+
+
+def alloc_adapter_grads(cfg, device="cuda"):
+    return {"dx": torch.empty((cfg.T, cfg.K), dtype=_out_dtype(cfg), device=device),
+            "dA": torch.empty((cfg.L, cfg.K, cfg.r), dtype=torch.float32, device=device),
+            "dB": torch.empty((cfg.L, cfg.r, cfg.N), dtype=torch.float32, device=device)}
+
+
+def adapter_bwd(cfg, dy, x, A, B, scale, plan, u, dx_base=None, grads=None, ws=None):
+    """Gradients of adapter_fwd: dict with dx [T, K] = dx_base + the adapters'
+    part (bf16, fp32 with cfg.out_fp32), dA [L, K, r] and dB [L, r, N] fp32.
+    dy [T, N] bf16; the gradient of base is dy itself."""
+    w = "adapter_bwd"
+    dyp = _arg(w, "dy", dy, torch.bfloat16, (cfg.T, cfg.N))
+    xp = _arg(w, "x", x, torch.bfloat16, (cfg.T, cfg.K))
+    weights = _adapter_args(w, cfg, A, B, scale, plan)
+    up = _ws_arg(w, u, _adapter_bytes(lib().moe_adapter_saved_bytes, cfg))
+    bp = _arg(w, "dx_base", dx_base, _out_dtype(cfg), (cfg.T, cfg.K), optional=True)
+    ws = adapter_workspace(cfg, True, x.device) if ws is None else ws
+    wp = _ws_arg(w, ws, _adapter_bytes(lib().moe_adapter_workspace_bytes, cfg, 1))
+    g = alloc_adapter_grads(cfg, x.device) if grads is None else grads
+    st = lib().moe_adapter_bwd(ctypes.byref(cfg), dyp, xp, *weights, up, bp,
+                               _arg(w, "dx", g["dx"], _out_dtype(cfg), (cfg.T, cfg.K)),
+                               _arg(w, "dA", g["dA"], torch.float32, (cfg.L, cfg.K, cfg.r)),
+                               _arg(w, "dB", g["dB"], torch.float32, (cfg.L, cfg.r, cfg.N)),
+                               wp, ws.numel(), _stream())
+    _check(st, "moe_adapter_bwd")
+    return g
+
+
+# ---------------------------------------------------------------------------
+# Global gradient norm and clipping
+# ---------------------------------------------------------------------------
+class MoeTensor(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("out", c_void_p), ("n", c_longlong), ("dtype", c_int), ("reserved", c_int)]
+
+
+GRAD_DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+NORM_KIND = {"l2": 0, "max": 1}
+
+
+class TensorList:
+    """The tensors of tensor_list, kept alive, and the library's list of them."""
+
+    def __init__(self, tensors, out):
+        self.tensors, self.out = tensors, out
+        n = len(tensors)
+        size = int(lib().moe_tensor_list_bytes(n))
+        if size == 0:
+            raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_tensor_list_bytes")
+        self.device = tensors[0].get_device() if n else torch.cuda.current_device()
+        items = (MoeTensor * max(n, 1))()
+        for i, t in enumerate(tensors):
+            o = None if out is None else out[i]
+            for what, v in (("tensor", t), ("out", o)):
+                if v is None and what == "out":
+                    continue
+                if not isinstance(v, torch.Tensor) or v.dtype not in GRAD_DTYPE or not v.is_contiguous():
+                    raise MoeError(MOE_ERR_INVALID_ARG,
+                                   f"tensor_list: {what} {i} must be a contiguous fp32, bf16 or fp16 tensor")
+                if not v.is_cuda or v.get_device() != self.device:
+                    raise MoeError(MOE_ERR_INVALID_ARG, f"tensor_list: {what} {i} must be on one CUDA device with the rest")
+            if o is not None and (o.dtype != t.dtype or o.numel() != t.numel()):
+                raise MoeError(MOE_ERR_INVALID_ARG, f"tensor_list: out {i} must have its tensor's type and size")
+            items[i] = MoeTensor(t.data_ptr(), None if o is None else o.data_ptr(), t.numel(), GRAD_DTYPE[t.dtype], 0)
+        self._list = (ctypes.c_uint64 * ((size + 7) // 8))()
+        _check(lib().moe_tensor_list_build(items, n, self._list, size), "moe_tensor_list_build")
+        self.ptr = ctypes.cast(self._list, c_void_p)
+
+
+def tensor_list(tensors, out=None):
+    """A list of gradients (contiguous fp32, bf16 or fp16 CUDA tensors, views at
+    any offset) for grad_norm and clip_grad_norm, built once for buffers that
+    stay where they are. out: where the clipped values go (None: in place)."""
+    tensors = list(tensors)
+    out = None if out is None else list(out)
+    if out is not None and len(out) != len(tensors):
+        raise MoeError(MOE_ERR_INVALID_ARG, "tensor_list: out must have one tensor for each")
+    return TensorList(tensors, out)
+
+
+def grad_norm_workspace(device="cuda"):
+    return _scratch(int(lib().moe_grad_norm_workspace_bytes()), device)
+
+
+def _norm_call(where, tensors, kind, ws, call):
+    tl = tensors if isinstance(tensors, TensorList) else tensor_list(tensors)
+    if kind not in NORM_KIND:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: kind must be one of {sorted(NORM_KIND)}")
+    if tl.device != torch.cuda.current_device():
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: the tensors must be on the current CUDA device")
+    n = int(lib().moe_grad_norm_workspace_bytes())
+    ws = _scratch(n, torch.device("cuda", tl.device)) if ws is None else ws
+    wp = _ws_arg(where, ws, n)
+    norm = torch.empty(1, dtype=torch.float32, device=ws.device)
+    _check(call(tl.ptr, NORM_KIND[kind], _p(norm), wp, ws.numel()), where)
+    return norm
+
+
+def grad_norm(tensors, kind="l2", ws=None):
+    """The global norm ([1] fp32) of a list of gradients (a tensor_list or the
+    tensors): "l2" or "max"."""
+    return _norm_call("moe_grad_norm", tensors, kind, ws,
+                      lambda p, k, norm, w, nb: lib().moe_grad_norm(p, k, norm, w, nb, _stream()))
+
+
+def clip_grad_norm(tensors, max_norm, kind="l2", ws=None):
+    """Scale the gradients by min(1, max_norm / (norm + 1e-6)), in place or into
+    the tensor_list's out; returns the norm before ([1] fp32)."""
+    return _norm_call("moe_clip_grad_norm", tensors, kind, ws,
+                      lambda p, k, norm, w, nb: lib().moe_clip_grad_norm(p, k, float(max_norm), norm, w, nb,
+                                                                         _stream()))
