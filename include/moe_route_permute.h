@@ -572,6 +572,28 @@ int moe_balance_loss_bwd(const moe_balance_config* cfg, const float* logits, con
                          const float* dlosses, const int32_t* seq_offsets, const uint8_t* token_mask,
                          float* dlogits, void* stream);
 
+/* The layer's backwards with a gradient of the router logits that arises
+ * outside the layer (moe_balance_loss_bwd's dlogits [T,E] fp32; NULL: none),
+ * added to the layer's own before the router's GEMMs: it reaches dx and
+ * dW_router. Everything else as in the calls without it. */
+int moe_layer_bwd_dlogits(const moe_config* cfg, const moe_bf16* dO, const float* dlogits, const moe_bf16* x,
+                          const moe_bf16* router_w, const moe_bf16* W1, const moe_bf16* W3,
+                          const moe_bf16* W2, const moe_bf16* Ws1, const moe_bf16* Ws3,
+                          const moe_bf16* Ws2, const moe_fwd_saved* saved,
+                          void* dx, float* dW_router, float* dW1, float* dW3, float* dW2,
+                          float* dWs1, float* dWs3, float* dWs2,
+                          float* aux_loss_out, void* ws, size_t ws_bytes, void* stream);
+int moe_layer_bwd_mxfp8_dlogits(const moe_config* cfg, const moe_bf16* dO, const float* dlogits,
+                                const moe_bf16* x, const moe_bf16* router_w, const moe_mx_bwd_weights* w,
+                                const moe_fwd_saved* saved, void* dx, float* dW_router, float* dW1,
+                                float* dW3, float* dW2, float* aux_loss_out, int mx_wgrad, void* ws,
+                                size_t ws_bytes, void* stream);
+int moe_layer_bwd_nvfp4_dlogits(const moe_config* cfg, const moe_bf16* dO, const float* dlogits,
+                                const moe_bf16* x, const moe_bf16* router_w, const moe_nv_bwd_weights* w,
+                                const moe_fwd_saved* saved, void* dx, float* dW_router, float* dW1,
+                                float* dW3, float* dW2, float* aux_loss_out, void* ws, size_t ws_bytes,
+                                void* stream);
+
 /* ---------------------------------------------------------------------------
  * Low-rank adapters of many requests beside a shared projection x [T,K] W
  * (the shared expert's projections, or any projection around the layer): row

@@ -914,7 +914,8 @@ static int layer_bwd_core(const moe_config& c, const moe_bf16* dO, const moe_bf1
                           void* ws, const WsLayout& L, const moe_mx_bwd_weights* mx, cudaStream_t s,
                           bool mx_wgrad = false, const moe_bf16* Ws1 = nullptr, const moe_bf16* Ws3 = nullptr,
                           const moe_bf16* Ws2 = nullptr, float* dWs1 = nullptr, float* dWs3 = nullptr,
-                          float* dWs2 = nullptr, const moe_nv_bwd_weights* nv = nullptr) {
+                          float* dWs2 = nullptr, const moe_nv_bwd_weights* nv = nullptr,
+                          const float* dlogits = nullptr) {
   // memory-saving backward: a recomputed from h13, gate gradient from the dgrad
   const bool recompute = mx == nullptr && saved->a == nullptr;
   DevStatus* st = at<DevStatus>(ws, 0);
@@ -964,7 +965,7 @@ static int layer_bwd_core(const moe_config& c, const moe_bf16* dO, const moe_bf1
   }
   // 2. router backward (element-wise): dL as bf16 hi/lo
   MOE_CUDA(launch_router_bwd(c, saved->logits, saved->topk_idx, saved->topk_gate, dgate, recompute ? dg_part : nullptr,
-                             n_part, saved->row_id_map, saved->counts, Ep, dL_hl, s, st));
+                             n_part, saved->row_id_map, saved->counts, Ep, dL_hl, s, st, dlogits));
   stage_done(s, STAGE_ROUTER_BWD, 1);
   // 3. da = dy_perm W2_e^T with the SwiGLU backward epilogue -> dh13
   if (nv != nullptr) {
@@ -1146,13 +1147,22 @@ int moe_layer_bwd(const moe_config* cfg, const moe_bf16* dO, const moe_bf16* x, 
                   const moe_bf16* Ws3, const moe_bf16* Ws2, const moe_fwd_saved* saved, void* dx, float* dW_router,
                   float* dW1, float* dW3, float* dW2, float* dWs1, float* dWs3, float* dWs2, float* aux_loss_out,
                   void* ws, size_t ws_bytes, void* stream) {
+  return moe_layer_bwd_dlogits(cfg, dO, nullptr, x, router_w, W1, W3, W2, Ws1, Ws3, Ws2, saved, dx, dW_router, dW1,
+                               dW3, dW2, dWs1, dWs3, dWs2, aux_loss_out, ws, ws_bytes, stream);
+}
+
+int moe_layer_bwd_dlogits(const moe_config* cfg, const moe_bf16* dO, const float* dlogits, const moe_bf16* x,
+                          const moe_bf16* router_w, const moe_bf16* W1, const moe_bf16* W3, const moe_bf16* W2,
+                          const moe_bf16* Ws1, const moe_bf16* Ws3, const moe_bf16* Ws2, const moe_fwd_saved* saved,
+                          void* dx, float* dW_router, float* dW1, float* dW3, float* dW2, float* dWs1, float* dWs3,
+                          float* dWs2, float* aux_loss_out, void* ws, size_t ws_bytes, void* stream) {
   NvtxRange nvtx("moe_layer_bwd");
   MOE_TRY(check_cfg(cfg));
   const moe_config& c = *cfg;
   if (!dO || !x || !router_w || !W1 || !W3 || !W2 || !saved || !dx || !dW_router || !dW1 || !dW3 || !dW2 || !ws)
     return MOE_ERR_INVALID_ARG;
-  if (!all_aligned16({dO, x, router_w, W1, W3, W2, Ws1, Ws3, Ws2, dx, dW_router, dW1, dW3, dW2, dWs1, dWs3, dWs2,
-                      aux_loss_out, ws}) ||
+  if (!all_aligned16({dO, dlogits, x, router_w, W1, W3, W2, Ws1, Ws3, Ws2, dx, dW_router, dW1, dW3, dW2, dWs1, dWs3,
+                      dWs2, aux_loss_out, ws}) ||
       !saved_aligned16(saved))
     return MOE_ERR_INVALID_ARG;
   if (!saved->topk_idx || !saved->topk_gate || !saved->logits || !saved->row_id_map || !saved->counts ||
@@ -1166,7 +1176,8 @@ int moe_layer_bwd(const moe_config* cfg, const moe_bf16* dO, const moe_bf16* x, 
   const WsLayout L = ws_layout(c, true);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   return layer_bwd_core(c, dO, x, router_w, W1, W3, W2, saved, dx, dW_router, dW1, dW3, dW2, aux_loss_out, ws, L,
-                        nullptr, static_cast<cudaStream_t>(stream), false, Ws1, Ws3, Ws2, dWs1, dWs3, dWs2);
+                        nullptr, static_cast<cudaStream_t>(stream), false, Ws1, Ws3, Ws2, dWs1, dWs3, dWs2, nullptr,
+                        dlogits);
 }
 
 // ---------------------------------------------------------------------------
@@ -1343,6 +1354,14 @@ int moe_layer_bwd_mxfp8(const moe_config* cfg, const moe_bf16* dO, const moe_bf1
                         const moe_mx_bwd_weights* w, const moe_fwd_saved* saved, void* dx, float* dW_router,
                         float* dW1, float* dW3, float* dW2, float* aux_loss_out, int mx_wgrad, void* ws,
                         size_t ws_bytes, void* stream) {
+  return moe_layer_bwd_mxfp8_dlogits(cfg, dO, nullptr, x, router_w, w, saved, dx, dW_router, dW1, dW3, dW2,
+                                     aux_loss_out, mx_wgrad, ws, ws_bytes, stream);
+}
+
+int moe_layer_bwd_mxfp8_dlogits(const moe_config* cfg, const moe_bf16* dO, const float* dlogits, const moe_bf16* x,
+                                const moe_bf16* router_w, const moe_mx_bwd_weights* w, const moe_fwd_saved* saved,
+                                void* dx, float* dW_router, float* dW1, float* dW3, float* dW2, float* aux_loss_out,
+                                int mx_wgrad, void* ws, size_t ws_bytes, void* stream) {
   NvtxRange nvtx("moe_layer_bwd_mxfp8");
   MOE_TRY(check_cfg(cfg));
   const moe_config& c = *cfg;
@@ -1351,13 +1370,14 @@ int moe_layer_bwd_mxfp8(const moe_config* cfg, const moe_bf16* dO, const moe_bf1
   if (!dO || !x || !router_w || !w || !w->w2h || !w->sf2h || !w->w13f || !w->sf13f || !mx_saved_ok(c, saved) ||
       !dx || !dW_router || !dW1 || !dW3 || !dW2 || !ws)
     return MOE_ERR_INVALID_ARG;
-  if (!all_aligned16({dO, x, router_w, w->w2h, w->sf2h, w->w13f, w->sf13f, dx, dW_router, dW1, dW3, dW2,
+  if (!all_aligned16({dO, dlogits, x, router_w, w->w2h, w->sf2h, w->w13f, w->sf13f, dx, dW_router, dW1, dW3, dW2,
                       aux_loss_out, ws}))
     return MOE_ERR_INVALID_ARG;
   const WsLayout L = ws_layout(c, true, true);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   return layer_bwd_core(c, dO, x, router_w, nullptr, nullptr, nullptr, saved, dx, dW_router, dW1, dW3, dW2,
-                        aux_loss_out, ws, L, w, static_cast<cudaStream_t>(stream), mx_wgrad != 0);
+                        aux_loss_out, ws, L, w, static_cast<cudaStream_t>(stream), mx_wgrad != 0, nullptr, nullptr,
+                        nullptr, nullptr, nullptr, nullptr, nullptr, dlogits);
 }
 
 // ---------------------------------------------------------------------------
@@ -1732,6 +1752,14 @@ int moe_layer_bwd_nvfp4(const moe_config* cfg, const moe_bf16* dO, const moe_bf1
                         const moe_nv_bwd_weights* w, const moe_fwd_saved* saved, void* dx, float* dW_router,
                         float* dW1, float* dW3, float* dW2, float* aux_loss_out, void* ws, size_t ws_bytes,
                         void* stream) {
+  return moe_layer_bwd_nvfp4_dlogits(cfg, dO, nullptr, x, router_w, w, saved, dx, dW_router, dW1, dW3, dW2,
+                                     aux_loss_out, ws, ws_bytes, stream);
+}
+
+int moe_layer_bwd_nvfp4_dlogits(const moe_config* cfg, const moe_bf16* dO, const float* dlogits, const moe_bf16* x,
+                                const moe_bf16* router_w, const moe_nv_bwd_weights* w, const moe_fwd_saved* saved,
+                                void* dx, float* dW_router, float* dW1, float* dW3, float* dW2, float* aux_loss_out,
+                                void* ws, size_t ws_bytes, void* stream) {
   NvtxRange nvtx("moe_layer_bwd_nvfp4");
   MOE_TRY(check_cfg(cfg));
   const moe_config& c = *cfg;
@@ -1739,14 +1767,14 @@ int moe_layer_bwd_nvfp4(const moe_config* cfg, const moe_bf16* dO, const moe_bf1
   if (!dO || !x || !router_w || !w || !w->w2h || !w->sf2h || !w->g2h || !w->w13f || !w->sf13f || !w->g13f ||
       !nv_saved_ok(c, saved) || !dx || !dW_router || !dW1 || !dW3 || !dW2 || !ws)
     return MOE_ERR_INVALID_ARG;
-  if (!all_aligned16({dO, x, router_w, w->w2h, w->sf2h, w->g2h, w->w13f, w->sf13f, w->g13f, dx, dW_router, dW1,
+  if (!all_aligned16({dO, dlogits, x, router_w, w->w2h, w->sf2h, w->g2h, w->w13f, w->sf13f, w->g13f, dx, dW_router, dW1,
                       dW3, dW2, aux_loss_out, ws}))
     return MOE_ERR_INVALID_ARG;
   const WsLayout L = ws_layout(c, true, false, true);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   return layer_bwd_core(c, dO, x, router_w, nullptr, nullptr, nullptr, saved, dx, dW_router, dW1, dW3, dW2,
                         aux_loss_out, ws, L, nullptr, static_cast<cudaStream_t>(stream), false, nullptr, nullptr,
-                        nullptr, nullptr, nullptr, nullptr, w);
+                        nullptr, nullptr, nullptr, nullptr, w, dlogits);
 }
 
 }  // extern "C"

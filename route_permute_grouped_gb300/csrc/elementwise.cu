@@ -263,7 +263,8 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
                       const float* __restrict__ gate, const float* __restrict__ dgate,
                       const float* __restrict__ dg_part, int n_part, const int32_t* __restrict__ row_id_map,
                       const int32_t* __restrict__ counts, int T, int E, int k, int score, float gate_scale,
-                      float aux_coeff, int Ep, __nv_bfloat16* __restrict__ dL_hl, DevStatus* st) {
+                      float aux_coeff, int Ep, __nv_bfloat16* __restrict__ dL_hl, DevStatus* st,
+                      const float* __restrict__ dlogits) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * kWarpsPerBlock + warp;
   if (t >= T) return;
@@ -338,6 +339,14 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32)
     for (int j = 0; j < NJ; ++j) {
       const float p = v[j] / sum;
       d[j] = p * (dp_scale * cnt[j] - pdp);
+    }
+  }
+  // the caller's own gradient of the logits (the losses outside the layer)
+  if (dlogits != nullptr) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int e = lane + 32 * j;
+      if (e < E) d[j] += dlogits[static_cast<size_t>(t) * E + e];
     }
   }
   // scatter the selected slots' terms to their experts' lanes
@@ -533,12 +542,12 @@ cudaError_t launch_combine_bwd(const moe_config& c, const __nv_bfloat16* dO, con
 cudaError_t launch_router_bwd(const moe_config& c, const float* logits, const int32_t* topk_idx, const float* gate,
                               const float* dgate, const float* dg_part, int n_part, const int32_t* row_id_map,
                               const int32_t* counts, int Ep, __nv_bfloat16* dL_hl, cudaStream_t st,
-                              DevStatus* ds) {
+                              DevStatus* ds, const float* dlogits) {
   NvtxRange nvtx("moe.router_backward");
   const dim3 g(blocks_for(c.T)), b(kWarpsPerBlock * 32);
 #define MOE_ROUTER_BWD(NJ)                                                                                  \
   router_bwd_kernel<NJ><<<g, b, 0, st>>>(logits, topk_idx, gate, dgate, dg_part, n_part, row_id_map, counts, \
-                                         c.T, c.E, c.k, c.score, c.gate_scale, c.aux_coeff, Ep, dL_hl, ds)
+                                         c.T, c.E, c.k, c.score, c.gate_scale, c.aux_coeff, Ep, dL_hl, ds, dlogits)
   // Ep (a multiple of 64, <= 256) columns over 32 lanes
   if (Ep <= 64) MOE_ROUTER_BWD(2);
   else if (Ep <= 128) MOE_ROUTER_BWD(4);

@@ -161,6 +161,12 @@ def lib():
             getattr(L, n).restype = c_size_t
             getattr(L, n).argtypes = [POINTER(MoeBalanceConfig)]
         L.moe_balance_loss_fwd.argtypes = [POINTER(MoeBalanceConfig)] + [vp] * 8 + [c_size_t, vp]
+        L.moe_layer_bwd_dlogits.argtypes = [POINTER(MoeConfig)] + [vp] * 10 + [POINTER(MoeFwdSaved)] + [vp] * 10 + [
+            c_size_t, vp]
+        L.moe_layer_bwd_mxfp8_dlogits.argtypes = [POINTER(MoeConfig), vp, vp, vp, vp, POINTER(MoeMxBwdWeights),
+                                                  POINTER(MoeFwdSaved)] + [vp] * 6 + [c_int, vp, c_size_t, vp]
+        L.moe_layer_bwd_nvfp4_dlogits.argtypes = [POINTER(MoeConfig), vp, vp, vp, vp, POINTER(MoeNvBwdWeights),
+                                                  POINTER(MoeFwdSaved)] + [vp] * 7 + [c_size_t, vp]
         L.moe_balance_loss_bwd.argtypes = [POINTER(MoeBalanceConfig)] + [vp] * 7
         for n in ("moe_adapter_plan_bytes", "moe_adapter_saved_bytes"):
             getattr(L, n).restype = c_size_t
@@ -177,7 +183,8 @@ def lib():
         L.moe_grad_norm_workspace_bytes.argtypes = []
         L.moe_grad_norm.argtypes = [vp, c_int, vp, vp, c_size_t, vp]
         L.moe_clip_grad_norm.argtypes = [vp, c_int, c_float, vp, vp, c_size_t, vp]
-        for n in ("moe_balance_loss_fwd", "moe_balance_loss_bwd", "moe_adapter_plan", "moe_adapter_fwd",
+        for n in ("moe_layer_bwd_dlogits", "moe_layer_bwd_mxfp8_dlogits", "moe_layer_bwd_nvfp4_dlogits",
+                  "moe_balance_loss_fwd", "moe_balance_loss_bwd", "moe_adapter_plan", "moe_adapter_fwd",
                   "moe_adapter_bwd", "moe_tensor_list_build", "moe_grad_norm", "moe_clip_grad_norm"):
             getattr(L, n).restype = c_int
         _lib = L
@@ -426,18 +433,25 @@ def alloc_grads(cfg, device="cuda"):
     return g
 
 
-def layer_bwd(cfg, dO, x, router_w, W1, W3, W2, saved, ws=None, grads=None, Ws=None):
+def _dlogits(where, cfg, dlogits):
+    return _arg(where, "dlogits", dlogits, torch.float32, (cfg.T, cfg.E), optional=True)
+
+
+def layer_bwd(cfg, dO, x, router_w, W1, W3, W2, saved, ws=None, grads=None, Ws=None, dlogits=None):
     """Whole layer backward (``Ws``: the shared expert's weights when
-    cfg.F_shared > 0; its gradients land in grads dWs1, dWs3, dWs2)."""
+    cfg.F_shared > 0; its gradients land in grads dWs1, dWs3, dWs2).
+    ``dlogits`` [T, E] fp32 (balance_loss_bwd): a gradient of the router logits
+    from outside the layer, carried into dx and dW_r with the layer's own."""
     dev = x.device
     g = alloc_grads(cfg, dev) if grads is None else grads
     ws = workspace(cfg, True, dev) if ws is None else ws
     sv = _saved_struct(saved)
     Ws1, Ws3, Ws2 = Ws if Ws is not None else (None, None, None)
-    st = lib().moe_layer_bwd(ctypes.byref(cfg), _p(dO), _p(x), _p(router_w), _p(W1), _p(W3), _p(W2), _p(Ws1),
-                             _p(Ws3), _p(Ws2), ctypes.byref(sv), _p(g["dx"]), _p(g["dW_r"]), _p(g["dW1"]),
-                             _p(g["dW3"]), _p(g["dW2"]), _p(g.get("dWs1")), _p(g.get("dWs3")), _p(g.get("dWs2")),
-                             _p(g["aux_loss"]), _p(ws), ws.numel(), _stream())
+    st = lib().moe_layer_bwd_dlogits(ctypes.byref(cfg), _p(dO), _dlogits("layer_bwd", cfg, dlogits), _p(x),
+                                     _p(router_w), _p(W1), _p(W3), _p(W2), _p(Ws1), _p(Ws3), _p(Ws2),
+                                     ctypes.byref(sv), _p(g["dx"]), _p(g["dW_r"]), _p(g["dW1"]), _p(g["dW3"]),
+                                     _p(g["dW2"]), _p(g.get("dWs1")), _p(g.get("dWs3")), _p(g.get("dWs2")),
+                                     _p(g["aux_loss"]), _p(ws), ws.numel(), _stream())
     _check(st, "moe_layer_bwd")
     return g
 
@@ -568,18 +582,18 @@ def layer_fwd_mxfp8_train(cfg, x, router_w, mxw, saved, expert_bias=None, logit_
     return y
 
 
-def layer_bwd_mxfp8(cfg, dO, x, router_w, mxbw, saved, ws=None, grads=None, mx_wgrad=False):
+def layer_bwd_mxfp8(cfg, dO, x, router_w, mxbw, saved, ws=None, grads=None, mx_wgrad=False, dlogits=None):
     """Backward of the MXFP8 training step (``mxbw`` from
-    mx_quantize_bwd_weights); gradients as layer_bwd. ``mx_wgrad``: the weight
+    mx_quantize_bwd_weights); gradients and ``dlogits`` as layer_bwd. ``mx_wgrad``: the weight
     gradients in MXFP8 too (operands quantised along each expert's tokens)."""
     dev = x.device
     g = alloc_grads(cfg, dev) if grads is None else grads
     ws = mx_train_workspace(cfg, dev) if ws is None else ws
     w = MoeMxBwdWeights(*[mxbw[n].data_ptr() for n in MX_BWD_WEIGHT_FIELDS])
-    st = lib().moe_layer_bwd_mxfp8(ctypes.byref(cfg), _p(dO), _p(x), _p(router_w), ctypes.byref(w),
-                                   ctypes.byref(_saved_struct(saved)), _p(g["dx"]), _p(g["dW_r"]), _p(g["dW1"]),
-                                   _p(g["dW3"]), _p(g["dW2"]), _p(g["aux_loss"]), int(bool(mx_wgrad)), _p(ws),
-                                   ws.numel(), _stream())
+    st = lib().moe_layer_bwd_mxfp8_dlogits(ctypes.byref(cfg), _p(dO), _dlogits("layer_bwd_mxfp8", cfg, dlogits),
+                                           _p(x), _p(router_w), ctypes.byref(w), ctypes.byref(_saved_struct(saved)),
+                                           _p(g["dx"]), _p(g["dW_r"]), _p(g["dW1"]), _p(g["dW3"]), _p(g["dW2"]),
+                                           _p(g["aux_loss"]), int(bool(mx_wgrad)), _p(ws), ws.numel(), _stream())
     _check(st, "moe_layer_bwd_mxfp8")
     return g
 
@@ -753,16 +767,17 @@ def layer_fwd_nvfp4_train(cfg, x, router_w, nvw, saved, expert_bias=None, logit_
     return y
 
 
-def layer_bwd_nvfp4(cfg, dO, x, router_w, nvbw, saved, ws=None, grads=None):
+def layer_bwd_nvfp4(cfg, dO, x, router_w, nvbw, saved, ws=None, grads=None, dlogits=None):
     """Backward of the NVFP4 training step (``nvbw`` from
-    nv_quantize_bwd_weights); gradients as layer_bwd."""
+    nv_quantize_bwd_weights); gradients and ``dlogits`` as layer_bwd."""
     dev = x.device
     g = alloc_grads(cfg, dev) if grads is None else grads
     ws = nv_train_workspace(cfg, dev) if ws is None else ws
     w = MoeNvBwdWeights(*[nvbw[n].data_ptr() for n, _ in MoeNvBwdWeights._fields_])
-    st = lib().moe_layer_bwd_nvfp4(ctypes.byref(cfg), _p(dO), _p(x), _p(router_w), ctypes.byref(w),
-                                   ctypes.byref(_saved_struct(saved)), _p(g["dx"]), _p(g["dW_r"]), _p(g["dW1"]),
-                                   _p(g["dW3"]), _p(g["dW2"]), _p(g["aux_loss"]), _p(ws), ws.numel(), _stream())
+    st = lib().moe_layer_bwd_nvfp4_dlogits(ctypes.byref(cfg), _p(dO), _dlogits("layer_bwd_nvfp4", cfg, dlogits),
+                                           _p(x), _p(router_w), ctypes.byref(w), ctypes.byref(_saved_struct(saved)),
+                                           _p(g["dx"]), _p(g["dW_r"]), _p(g["dW1"]), _p(g["dW3"]), _p(g["dW2"]),
+                                           _p(g["aux_loss"]), _p(ws), ws.numel(), _stream())
     _check(st, "moe_layer_bwd_nvfp4")
     return g
 
