@@ -541,9 +541,9 @@ int moe_layer_bwd_nvfp4(const moe_config* cfg, const moe_bf16* dO, const moe_bf1
  * Nothing of an invalid token is read into a result, whatever its logits
  * hold; its gradient is 0. A sequence without valid tokens has counts 0 and
  * adds nothing; with no valid token at all both losses are 0.
- * Shapes: T >= 1, E <= 256, 1 <= k <= min(E, 16), n_seqs <= 2^20,
- * T*k < 2^30. Sums are fp32 within about a hundred rows, fp64 beyond, in a
- * fixed order.
+ * Shapes: T >= 1, E <= 256, 1 <= k <= min(E, 16), n_seqs <= 65536,
+ * T*k < 2^30. Sums are fp32 within about a hundred rows and two floats
+ * (48 bits) beyond, in a fixed order.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int T, E, k;
@@ -651,8 +651,8 @@ int moe_adapter_bwd(const moe_adapter_config* cfg, const moe_bf16* dy, const moe
  *   norm = sqrt(sum over all tensors of g^2)  (MOE_NORM_L2), or max |g|
  *          (MOE_NORM_MAX);
  *   coef = min(1, max_norm / (norm + 1e-6)),  out = round(g * coef).
- * Squares are summed over 16 or 32 elements in fp32 and from there in fp64, in
- * a fixed order; where fp32 squares would overflow or lose bits they are taken
+ * Squares are summed over 16 or 32 elements in fp32 and from there in two
+ * floats or fp64, in a fixed order; where fp32 squares would overflow or lose bits they are taken
  * in fp64. A NaN anywhere makes the norm NaN, and every clipped gradient; an
  * infinite norm scales by 0 (infinities become NaN).
  * ------------------------------------------------------------------------- */
@@ -680,7 +680,8 @@ typedef struct {
 size_t moe_tensor_list_bytes(int n);
 int moe_tensor_list_build(const moe_tensor* tensors, int n, void* list, size_t list_bytes);
 
-/* Workspace bytes of both calls. */
+/* Workspace bytes of both calls. The first 256 bytes must be 0 before the
+ * workspace's first use (the calls leave them 0). */
 size_t moe_grad_norm_workspace_bytes(void);
 
 /* norm [1] fp32. An empty list has norm 0. */

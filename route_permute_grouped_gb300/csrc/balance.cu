@@ -10,18 +10,18 @@
 namespace moe {
 
 // Rows are handled by groups of G lanes, each lane holding NV sets of four
-// consecutive experts (set j: experts 4 (lane + G j) ..): 4 G NV >= E.
+// consecutive experts (set j: experts 4 (lane + G j) ..): 4 G NV >= E. A group
+// takes kBalUnroll rows at a time, so that their loads and the latencies of
+// their reductions overlap.
 constexpr int kBalThreads = 256;
 constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kBalUnroll = 2;
 
-// Chunks of the token axis: sequence s takes the chunk numbers from
-// base(s) = off[s] / CH + s on, ceil(len / CH) of them, which is less than
-// base(s + 1) - base(s) + 1, so each chunk number belongs to one sequence at
-// most and nothing has to be scanned.
-struct BalChunk {
-  int s, lo, hi;  // rows [lo, hi) of sequence s; lo == hi: no rows
-};
-
+// The forward's blocks take equal runs of CH rows, whatever sequences lie in
+// them (their partial sums would otherwise come from as many short blocks as
+// there are ends of sequences). Block b's part of sequence s goes to slot b + s:
+// along the rows the pairs (b, s) step up one at a time in b or s, so each has a
+// slot of its own and those of a sequence are neighbours.
 __device__ __forceinline__ int seq_begin(const int32_t* off, int s, int S, int T) {
   if (off == nullptr) return s == 0 ? 0 : T;
   const int v = off[s];
@@ -32,50 +32,71 @@ __device__ __forceinline__ int seq_begin(const int32_t* off, int s, int S, int T
 template <class F>
 __device__ __forceinline__ int count_le(int S, F key, int c) {
   int n = 0;
-  for (int s0 = 0; s0 < S; s0 += kBalThreads) {
+  for (int s0 = 0; s0 < S; s0 += static_cast<int>(blockDim.x)) {
     const int s = s0 + static_cast<int>(threadIdx.x);
     n += __syncthreads_count(s < S && key(s) <= c);
   }
   return n;
 }
 
-__device__ __forceinline__ BalChunk chunk_of(const int32_t* off, int S, int T, int CH, int c) {
-  const int s = count_le(S, [&](int i) { return seq_begin(off, i, S, T) / CH + i; }, c) - 1;
-  BalChunk r{-1, 0, 0};
-  if (s < 0) return r;
-  const int b = seq_begin(off, s, S, T), e = seq_begin(off, s + 1, S, T);
-  const long long lo = b + static_cast<long long>(c - (b / CH + s)) * CH;
-  r.s = s;
-  if (lo >= b && lo < e) {  // offsets that descend give chunks without rows
-    r.lo = static_cast<int>(lo);
-    r.hi = static_cast<int>(min(static_cast<long long>(e), lo + CH));
-  }
+// Two floats in one 64-bit register and the packed arithmetic on them (one
+// instruction for two elements).
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ f2 both(float a) { return pack2(a, a); }
+__device__ __forceinline__ float2 unpack2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float side_sum(f2 v) {
+  const float2 x = unpack2(v);
+  return x.x + x.y;
+}
 
+// `top`: the largest |logit| this lane has loaded so far
 template <int G, int NV, bool VEC>
-__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int gl, float (&v)[4 * NV]) {
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int gl, f2 (&v)[2 * NV], float& top) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int e = 4 * (gl + G * j);
+    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     if constexpr (VEC) {
       if (e < E) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(row + e));
-        v[4 * j] = x.x; v[4 * j + 1] = x.y; v[4 * j + 2] = x.z; v[4 * j + 3] = x.w;
-      } else {
-        v[4 * j] = v[4 * j + 1] = v[4 * j + 2] = v[4 * j + 3] = -INFINITY;
+        const float4 q = __ldg(reinterpret_cast<const float4*>(row + e));
+        x[0] = q.x; x[1] = q.y; x[2] = q.z; x[3] = q.w;
+        top = fmaxf(fmaxf(top, fmaxf(fabsf(x[0]), fabsf(x[1]))), fmaxf(fabsf(x[2]), fabsf(x[3])));
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * j + i] = e + i < E ? __ldg(row + e + i) : -INFINITY;
+      for (int i = 0; i < 4; ++i)
+        if (e + i < E) {
+          x[i] = __ldg(row + e + i);
+          top = fmaxf(top, fabsf(x[i]));
+        }
     }
+    v[2 * j] = pack2(x[0], x[1]);
+    v[2 * j + 1] = pack2(x[2], x[3]);
   }
-}
-template <int G>
-__device__ __forceinline__ float group_sum(float x) {
-#pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
 }
 template <int G>
 __device__ __forceinline__ float group_max(float x) {
@@ -83,31 +104,138 @@ __device__ __forceinline__ float group_max(float x) {
   for (int o = G / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
 }
-
-// softmax of a row: v -> exp(v - max), returns 1 / sum and the row's
-// log-sum-exp
-template <int G, int NV>
-__device__ __forceinline__ float row_softmax(float (&v)[4 * NV], float& lse) {
-  float m = v[0];
+// The sums of a and of b over the lanes of a group: the halves of the group
+// exchange one of the two first, so each reduces one value (G = 32: 6 shuffles
+// for two sums instead of 10).
+template <int G>
+__device__ __forceinline__ void group_sum2(float& a, float& b, int gl) {
+  const bool up = (gl & (G / 2)) != 0;
+  float keep = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, G / 2);
 #pragma unroll
-  for (int i = 1; i < 4 * NV; ++i) m = fmaxf(m, v[i]);
-  m = group_max<G>(m);
-  float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4 * NV; ++i) {
-    v[i] = expf(v[i] - m);
-    sum += v[i];
-  }
-  sum = group_sum<G>(sum);
-  lse = m + logf(sum);
-  return 1.0f / sum;
+  for (int o = G / 4; o > 0; o >>= 1) keep += __shfl_xor_sync(0xffffffffu, keep, o);
+  const float other = __shfl_xor_sync(0xffffffffu, keep, G / 2);
+  a = up ? other : keep;
+  b = up ? keep : other;
 }
 
-// sigmoid and 1 - sigmoid without cancellation: t = exp(-|l|)
-__device__ __forceinline__ float2 sigmoid2(float l) {
-  const float t = expf(-fabsf(l));
-  const float a = 1.0f / (1.0f + t), b = t * a;
-  return l >= 0.0f ? make_float2(a, b) : make_float2(b, a);
+// The score functions of the kBalUnroll = 2 rows of a group. On return v holds
+// exp(l - m), `inv` the inverse of their sum and `lse` the log-sum-exp; for
+// sigmoid scores s holds the sigmoids and `sinv` the inverse of their sum. The
+// backward (BWD) has in s the slopes sigmoid (1 - sigmoid) instead, and in `dot`
+// the sum of the unnormalised scores times w.
+//
+// What bounds a row beside its bytes is its instructions (the first kernels: 36
+// an element, 113 us for 131021 x 256 sigmoid scores; these: 38 us) and the
+// special functions among them (16 a clock and SM). So m is 0 (NEAR) as long as no
+// logit of the warp's rows is beyond 40 in magnitude: no maximum is reduced, one
+// exponential x = exp(l) serves both scores, sigmoid(l) = x / (1 + x) and
+// 1 - sigmoid(l) = 1 / (1 + x) without cancellation, and the sum stays below
+// 256 e^40. Rows with larger logits take m = max l and exp(-|l|). exp is
+// exp2(x log2 e): the argument is off by half a step of itself, as l - m is.
+constexpr float kNear = 40.0f;
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+template <int G, int NV, bool SIG, bool BWD, bool NEAR, class Weights>
+__device__ __forceinline__ void row_scores(int gl, f2 (&v)[kBalUnroll][2 * NV], f2 (&s)[kBalUnroll][2 * NV],
+                                           const f2 (&w)[2 * NV], Weights weights_of, float (&inv)[kBalUnroll],
+                                           float (&lse)[kBalUnroll], float (&sinv)[kBalUnroll],
+                                           float (&dot)[kBalUnroll]) {
+  static_assert(kBalUnroll == 2, "the sums are reduced in pairs");
+  float sum[2], ssum[2], m[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    if constexpr (!NEAR) {
+      m[u] = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 2 * NV; ++i) {
+        const float2 l = unpack2(v[u][i]);
+        m[u] = fmaxf(m[u], fmaxf(l.x, l.y));
+      }
+      m[u] = group_max<G>(m[u]);
+    }
+    weights_of(u);  // into w
+    f2 sum2 = both(0.0f), ssum2 = both(0.0f), dot2 = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < 2 * NV; ++i) {
+      const f2 l2 = v[u][i];
+      const float2 x = unpack2(mul2(NEAR ? l2 : add2(l2, both(-m[u])), both(kLog2e)));
+      v[u][i] = pack2(ex2_approx(x.x), ex2_approx(x.y));
+      sum2 = add2(sum2, v[u][i]);
+      if constexpr (SIG) {
+        f2 a, b;
+        if constexpr (NEAR) {
+          const float2 o = unpack2(add2(v[u][i], both(1.0f)));
+          b = pack2(rcp_approx(o.x), rcp_approx(o.y));
+          a = mul2(v[u][i], b);
+        } else {
+          const float2 l = unpack2(l2);
+          const float tx = __expf(-fabsf(l.x)), ty = __expf(-fabsf(l.y));
+          const float rx = rcp_approx(1.0f + tx), ry = rcp_approx(1.0f + ty);
+          a = pack2(l.x >= 0.0f ? rx : tx * rx, l.y >= 0.0f ? ry : ty * ry);
+          b = pack2(l.x >= 0.0f ? tx * rx : rx, l.y >= 0.0f ? ty * ry : ry);
+        }
+        s[u][i] = BWD ? mul2(a, b) : a;
+        ssum2 = add2(ssum2, a);
+        if constexpr (BWD) dot2 = fma2(a, w[i], dot2);
+      } else if constexpr (BWD) {
+        dot2 = fma2(v[u][i], w[i], dot2);
+      }
+    }
+    sum[u] = side_sum(sum2);
+    ssum[u] = SIG ? side_sum(ssum2) : 0.0f;
+    dot[u] = BWD ? side_sum(dot2) : 0.0f;
+  }
+  group_sum2<G>(sum[0], sum[1], gl);
+  if constexpr (SIG) group_sum2<G>(ssum[0], ssum[1], gl);
+  if constexpr (BWD) group_sum2<G>(dot[0], dot[1], gl);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    lse[u] = m[u] + __logf(sum[u]);
+    inv[u] = __fdividef(1.0f, sum[u]);
+    if constexpr (SIG) sinv[u] = __fdividef(1.0f, ssum[u]);
+  }
+}
+
+// A sum in two floats: s + e is the exact sum so far but for the roundings of e.
+// For sums of many partial sums in a fixed order (fp64 additions run at about two
+// a clock and SM: a block-wide fp64 tree took 36 us where this takes one).
+struct Sum2 {
+  float s = 0.0f, e = 0.0f;
+  __device__ __forceinline__ void add(float x) {
+    const float t = s + x, b = t - s;
+    e += (s - (t - b)) + (x - b);
+    s = t;
+  }
+  __device__ __forceinline__ void add(const Sum2& o) {
+    add(o.s);
+    e += o.e;
+  }
+  // e of an infinite sum is not a number
+  __device__ __forceinline__ float value() const { return isfinite(s) ? s + e : s; }
+};
+__device__ __forceinline__ Sum2 warp_sum(Sum2 x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Sum2 y;
+    y.s = __shfl_xor_sync(0xffffffffu, x.s, o);
+    y.e = __shfl_xor_sync(0xffffffffu, x.e, o);
+    x.add(y);
+  }
+  return x;
+}
+__device__ __forceinline__ int warp_sum(int x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
 }
 
 struct BalParams {
@@ -115,16 +243,16 @@ struct BalParams {
   const int32_t* topk;
   const int32_t* off;
   const uint8_t* mask;
-  int T, E, k, S, CH, chunks;
-  int sigmoid, need_lse;
+  int T, E, k, S, CH, slots;
+  int sigmoid, need_lse;  // need_lse: z_coeff is not 0
   float balance_coeff, z_coeff;
   // workspace
-  float* part_p;      // [chunks][E] sums of p
-  int32_t* part_c;    // [chunks][E] counts
-  float* part_z;      // [chunks] sums of lse^2
-  int32_t* part_n;    // [chunks] valid rows
-  double* seq_b;      // [S] balance loss of each sequence (before the mean over sequences)
-  double* seq_z;      // [S] sum of lse^2
+  float* part_p;      // [slots][E] sums of p
+  int32_t* part_c;    // [slots][E] counts
+  float* part_z;      // [slots] sums of lse^2
+  int32_t* part_n;    // [slots] valid rows
+  float2* seq_b;      // [S][32-expert groups] balance loss of each sequence (before the mean over sequences)
+  float2* seq_z;      // [S] sum of lse^2
   int32_t* seq_n;     // [S]
   int* ticket;
   // outputs
@@ -134,64 +262,22 @@ struct BalParams {
   DevStatus* st;
 };
 
-// Forward, first pass: every chunk's sums of p, counts, sum of lse^2 and
-// number of valid rows. The sums over rows stay in registers, one set per lane
+// Forward, first pass: each block's sums of p, counts, sum of lse^2 and number
+// of valid rows for every sequence in its rows. The sums over rows stay in registers, one set per lane
 // group, and are joined over the groups and warps in a fixed order.
-template <int G, int NV, bool VEC>
-__global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalParams p) {
+struct BalChunk {
+  int lo, hi;
+};
+template <int G, int NV, bool VEC, bool SIG>
+__device__ __forceinline__ void part_of_sequence(const BalParams& p, const BalChunk ch, int slot) {
   __shared__ int s_cnt[256];
   __shared__ float s_sum[kBalWarps][256];
   __shared__ float s_z[kBalWarps];
   __shared__ int s_n[kBalWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (blockIdx.x == 0 && tid == 0) *p.ticket = 0;
-  const BalChunk ch = chunk_of(p.off, p.S, p.T, p.CH, blockIdx.x);
-  if (ch.s < 0 || ch.lo >= ch.hi) return;
+  __syncthreads();  // the last sequence's sums have been read
   s_cnt[tid] = 0;
   __syncthreads();
-  const int gl = lane & (G - 1), grp = lane / G;
-  constexpr int RPW = 32 / G;
-  float acc[4 * NV];
-#pragma unroll
-  for (int i = 0; i < 4 * NV; ++i) acc[i] = 0.0f;
-  float z = 0.0f;
-  int n = 0;
-  for (int t0 = ch.lo + warp * RPW; t0 < ch.hi; t0 += kBalWarps * RPW) {
-    const int t = t0 + grp;
-    const bool ok = t < ch.hi && (p.mask == nullptr || p.mask[t] != 0);
-    float v[4 * NV];
-    if (ok) {
-      load_row<G, NV, VEC>(p.logits + static_cast<size_t>(t) * p.E, p.E, gl, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4 * NV; ++i) v[i] = 0.0f;
-    }
-    if (p.sigmoid) {
-      float s[4 * NV], sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4 * NV; ++i) {
-        s[i] = sigmoid2(v[i]).x;
-        sum += s[i];
-      }
-      const float inv = 1.0f / group_sum<G>(sum);
-      if (ok) {
-#pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) acc[i] += s[i] * inv;
-      }
-    }
-    float lse = 0.0f;
-    if (!p.sigmoid || p.need_lse) {
-      const float inv = row_softmax<G, NV>(v, lse);
-      if (!p.sigmoid && ok) {
-#pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) acc[i] += v[i] * inv;
-      }
-    }
-    if (ok && gl == 0) {
-      z += lse * lse;
-      ++n;
-    }
-  }
   // the selected experts of the valid rows
   const int slots = (ch.hi - ch.lo) * p.k;
   const int32_t* idx = p.topk + static_cast<size_t>(ch.lo) * p.k;
@@ -200,6 +286,54 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalPara
     const int e = __ldg(idx + i);
     if (e < 0 || e >= p.E) set_status(p.st, MOE_ERR_DEVICE_INDEX, 50);
     else atomicAdd(&s_cnt[e], 1);
+  }
+  const int gl = lane & (G - 1), grp = lane / G;
+  constexpr int RPW = 32 / G, U = kBalUnroll;
+  f2 acc2[2 * NV];
+#pragma unroll
+  for (int i = 0; i < 2 * NV; ++i) acc2[i] = both(0.0f);
+  float z = 0.0f;
+  int n = 0;
+  for (int t0 = ch.lo + warp * RPW; t0 < ch.hi; t0 += U * kBalWarps * RPW) {
+    f2 v[U][2 * NV];
+    float top = 0.0f;
+    bool ok[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * kBalWarps * RPW + grp;
+      ok[u] = t < ch.hi && (p.mask == nullptr || p.mask[t] != 0);
+      if (ok[u]) {
+        load_row<G, NV, VEC>(p.logits + static_cast<size_t>(t) * p.E, p.E, gl, v[u], top);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2 * NV; ++i) v[u][i] = both(0.0f);
+      }
+    }
+    const bool near = __all_sync(0xffffffffu, top <= kNear);
+    f2 s[U][2 * NV];
+    float inv[U], lse[U], sinv[U], dot[U];
+    const auto none = [](int) {};
+    if (near) row_scores<G, NV, SIG, false, true>(gl, v, s, acc2, none, inv, lse, sinv, dot);
+    else row_scores<G, NV, SIG, false, false>(gl, v, s, acc2, none, inv, lse, sinv, dot);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (ok[u]) {
+        const f2 scale = both(SIG ? sinv[u] : inv[u]);
+#pragma unroll
+        for (int i = 0; i < 2 * NV; ++i) acc2[i] = fma2(SIG ? s[u][i] : v[u][i], scale, acc2[i]);
+        if (gl == 0) {
+          z += lse[u] * lse[u];
+          ++n;
+        }
+      }
+    }
+  }
+  float acc[4 * NV];
+#pragma unroll
+  for (int i = 0; i < 2 * NV; ++i) {
+    const float2 x = unpack2(acc2[i]);
+    acc[2 * i] = x.x;
+    acc[2 * i + 1] = x.y;
   }
   // groups of a warp, then warps
 #pragma unroll
@@ -216,10 +350,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalPara
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = 4 * (gl + G * j) + i;
-        if (e < 256) s_sum[warp][e] = acc[4 * j + i];
-      }
+      for (int i = 0; i < 4; ++i) s_sum[warp][4 * (gl + G * j) + i] = acc[4 * j + i];
   }
   if (lane == 0) {
     s_z[warp] = z;
@@ -230,140 +361,178 @@ __global__ void __launch_bounds__(kBalThreads) balance_part_kernel(const BalPara
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < kBalWarps; ++w) s += s_sum[w][tid];
-    p.part_p[static_cast<size_t>(blockIdx.x) * p.E + tid] = s;
-    p.part_c[static_cast<size_t>(blockIdx.x) * p.E + tid] = s_cnt[tid];
+    p.part_p[static_cast<size_t>(slot) * p.E + tid] = s;
+    p.part_c[static_cast<size_t>(slot) * p.E + tid] = s_cnt[tid];
   }
   if (tid == 0) {
     for (int w = 1; w < kBalWarps; ++w) {
       z += s_z[w];
       n += s_n[w];
     }
-    p.part_z[blockIdx.x] = z;
-    p.part_n[blockIdx.x] = n;
+    p.part_z[slot] = z;
+    p.part_n[slot] = n;
   }
 }
 
-// Forward, second pass: one block per sequence adds its chunks (fp64, fixed
-// order), writes its counts and the weight row of the backward; the block that
-// finishes last adds the sequences.
-constexpr int kBalJoin = 1024;
-__global__ void __launch_bounds__(kBalJoin) balance_join_kernel(const BalParams p) {
-  __shared__ double s_p[kBalJoin];
-  __shared__ int s_c[kBalJoin];
-  __shared__ double s_z[32];
-  __shared__ int s_n[32];
+template <int G, int NV, bool VEC, bool SIG>
+__global__ void __launch_bounds__(kBalThreads, 4) balance_part_kernel(const BalParams p) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
+  const int lo = blockIdx.x * p.CH, hi = min(p.T, lo + p.CH);
+  // the first sequence that ends behind the first row
+  int s = p.off == nullptr ? 0 : count_le(p.S, [&](int i) { return seq_begin(p.off, i + 1, p.S, p.T); }, lo);
+  for (; s < p.S; ++s) {
+    const int begin = seq_begin(p.off, s, p.S, p.T);
+    if (begin >= hi) break;
+    BalChunk ch;
+    ch.lo = max(lo, begin);
+    ch.hi = min(hi, seq_begin(p.off, s + 1, p.S, p.T));
+    if (ch.lo < ch.hi) part_of_sequence<G, NV, VEC, SIG>(p, ch, blockIdx.x + s);
+  }
+  chain_release();
+}
+
+// Forward, second pass: a block for each sequence and 32 experts adds their
+// slots (a lane an expert, the warps sharing the slots; fixed order), writes
+// the counts and the weight row of the backward; the block that finishes last
+// adds the sequences.
+template <int kBalJoinWarps>
+__global__ void __launch_bounds__(32 * kBalJoinWarps) balance_join_kernel(const BalParams p) {
+  constexpr int kBalJoin = 32 * kBalJoinWarps, kBatch = 10;
+  __shared__ Sum2 s_p[kBalJoinWarps][32];
+  __shared__ int s_c[kBalJoinWarps][32];
+  __shared__ Sum2 s_z[kBalJoinWarps], s_b[kBalJoinWarps];
+  __shared__ int s_n[kBalJoinWarps], s_f[kBalJoinWarps];
   __shared__ int s_last;
-  const int s = blockIdx.x, tid = threadIdx.x, E = p.E;
+  const int s = blockIdx.x, cg = blockIdx.y, groups = gridDim.y, E = p.E;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = seq_begin(p.off, s, p.S, p.T), e = seq_begin(p.off, s + 1, p.S, p.T);
+  chain_wait();
   if (tid == 0 && p.off != nullptr) {
     const int rb = p.off[s], re = p.off[s + 1];
     if (rb < 0 || re < rb || re > p.T) set_status(p.st, MOE_ERR_DEVICE_INDEX, 51);
   }
-  const int first = b / p.CH + s;
-  const int nch = e > b ? min((e - b + p.CH - 1) / p.CH, p.chunks - first) : 0;
-  // thread (g, x): expert x, chunks g, g + groups, ...
-  const int Eb = (E + 31) & ~31, groups = kBalJoin / Eb, x = tid % Eb, g = tid / Eb;
-  double P = 0.0;
-  int c = 0;
-  if (x < E && g < groups) {
-    for (int i = g; i < nch; i += groups) {
-      P += p.part_p[static_cast<size_t>(first + i) * E + x];
-      c += p.part_c[static_cast<size_t>(first + i) * E + x];
+  const int first = b / p.CH + s, x = 32 * cg + lane;
+  const int nch = e > b ? min((e - 1) / p.CH - b / p.CH + 1, p.slots - first) : 0;
+  Sum2 P, z;
+  int c = 0, n = 0;
+  if (x < E) {
+    // kBatch loads in flight: the sums wait for memory once a batch
+    for (int i0 = warp; i0 < nch; i0 += kBatch * kBalJoinWarps) {
+      float pv[kBatch];
+      int cv[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j * kBalJoinWarps;
+        const size_t at = static_cast<size_t>(first + i) * E + x;
+        pv[j] = i < nch ? p.part_p[at] : 0.0f;
+        cv[j] = i < nch ? p.part_c[at] : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        P.add(pv[j]);
+        c += cv[j];
+      }
     }
   }
-  double z = 0.0;
-  int n = 0;
   for (int i = tid; i < nch; i += kBalJoin) {
-    z += p.part_z[first + i];
+    z.add(p.part_z[first + i]);
     n += p.part_n[first + i];
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    z += __shfl_xor_sync(0xffffffffu, z, o);
-    n += __shfl_xor_sync(0xffffffffu, n, o);
+  n = warp_sum(n);
+  z = warp_sum(z);
+  s_p[warp][lane] = P;
+  s_c[warp][lane] = c;
+  if (lane == 0) {
+    s_z[warp] = z;
+    s_n[warp] = n;
   }
-  if ((tid & 31) == 0) {
-    s_z[tid >> 5] = z;
-    s_n[tid >> 5] = n;
-  }
-  s_p[tid] = P;
-  s_c[tid] = c;
   __syncthreads();
-  z = 0.0;
-  n = 0;
-  for (int w = 0; w < 32; ++w) {
-    z += s_z[w];
-    n += s_n[w];
-  }
-  double term = 0.0;
-  if (tid < E) {
-    P = 0.0;
+  if (warp == 0) {
+    n = 0;
+    P = Sum2();
     c = 0;
-    for (int i = 0; i < groups; ++i) {
-      P += s_p[i * Eb + tid];
-      c += s_c[i * Eb + tid];
+    z = Sum2();
+#pragma unroll
+    for (int w = 0; w < kBalJoinWarps; ++w) {
+      n += s_n[w];
+      z.add(s_z[w]);
+      P.add(s_p[w][lane]);
+      c += s_c[w][lane];
     }
-    p.counts[static_cast<size_t>(s) * E + tid] = c;
-    double w = 0.0;
-    if (n > 0) {
-      w = static_cast<double>(p.balance_coeff) * E * c / (static_cast<double>(p.k) * n * n);
-      term = w * P;
+    float w = 0.0f;
+    if (x < E) {
+      // in the order that keeps the factors near 1: f, then the two means
+      if (n > 0) w = p.balance_coeff * (static_cast<float>(E) / p.k * (static_cast<float>(c) / n)) / n;
+      p.counts[static_cast<size_t>(s) * E + x] = c;
+      p.stats[static_cast<size_t>(s) * E + x] = w;
     }
-    p.stats[static_cast<size_t>(s) * E + tid] = static_cast<float>(w);
-  }
-  __syncthreads();
-  s_p[tid] = term;
-  __syncthreads();
-  for (int st = kBalJoin / 2; st > 0; st >>= 1) {
-    if (tid < st) s_p[tid] += s_p[tid + st];
-    __syncthreads();
-  }
-  if (tid == 0) {
-    p.seq_b[s] = s_p[0];
-    p.seq_z[s] = z;
-    p.seq_n[s] = n;
-    __threadfence();
-    s_last = atomicAdd(p.ticket, 1) == p.S - 1;
-    __threadfence();
+    Sum2 term;
+    term.add(w * P.value());
+    term = warp_sum(term);
+    if (lane == 0) {
+      p.seq_b[static_cast<size_t>(s) * groups + cg] = make_float2(term.s, term.e);
+      if (cg == 0) {
+        p.seq_z[s] = make_float2(z.s, z.e);
+        p.seq_n[s] = n;
+      }
+      __threadfence();
+      s_last = atomicAdd(p.ticket, 1) == p.S * groups - 1;
+      __threadfence();
+    }
   }
   __syncthreads();
   if (!s_last) return;
-  double lb = 0.0, lz = 0.0, cnt = 0.0, filled = 0.0;
+  Sum2 lb, lz;
+  int cnt = 0, filled = 0;
+  for (int i = tid; i < p.S * groups; i += kBalJoin) {
+    const float2 v = __ldcg(p.seq_b + i);
+    lb.add(v.x);
+    lb.e += v.y;
+  }
   for (int i = tid; i < p.S; i += kBalJoin) {
-    lb += __ldcg(p.seq_b + i);
-    lz += __ldcg(p.seq_z + i);
+    const float2 v = __ldcg(p.seq_z + i);
+    lz.add(v.x);
+    lz.e += v.y;
     const int m = __ldcg(p.seq_n + i);
     cnt += m;
-    filled += m > 0 ? 1.0 : 0.0;
+    filled += m > 0;
   }
-  double* vals[4] = {&lb, &lz, &cnt, &filled};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    __syncthreads();
-    s_p[tid] = *vals[j];
-    __syncthreads();
-    for (int st = kBalJoin / 2; st > 0; st >>= 1) {
-      if (tid < st) s_p[tid] += s_p[tid + st];
-      __syncthreads();
-    }
-    *vals[j] = s_p[0];
+  lb = warp_sum(lb);
+  lz = warp_sum(lz);
+  cnt = warp_sum(cnt);
+  filled = warp_sum(filled);
+  if (lane == 0) {
+    s_b[warp] = lb;
+    s_z[warp] = lz;
+    s_n[warp] = cnt;
+    s_f[warp] = filled;
   }
+  __syncthreads();
   if (tid == 0) {
-    const double share = filled > 0 ? 1.0 / filled : 0.0, per = cnt > 0 ? p.z_coeff / cnt : 0.0;
-    p.losses[0] = static_cast<float>(lb * share);
-    p.losses[1] = per != 0.0 ? static_cast<float>(lz * per) : 0.0f;
+    for (int w = 1; w < kBalJoinWarps; ++w) {
+      lb.add(s_b[w]);
+      lz.add(s_z[w]);
+      cnt += s_n[w];
+      filled += s_f[w];
+    }
+    const float share = filled > 0 ? 1.0f / filled : 0.0f, per = cnt > 0 ? p.z_coeff / cnt : 0.0f;
+    p.losses[0] = filled > 0 ? lb.value() * share : 0.0f;
+    p.losses[1] = per != 0.0f ? lz.value() * per : 0.0f;
     float* tail = p.stats + static_cast<size_t>(p.S) * E;
-    tail[0] = static_cast<float>(share);
-    tail[1] = static_cast<float>(2.0 * per);
+    tail[0] = share;
+    tail[1] = 2.0f * per;
   }
 }
 
 // Backward: one pass over the logits. w is the sequence's weight row
 // alpha E c / (k n^2); the mean over the sequences and the losses' own
 // gradients scale it.
-template <int G, int NV, bool VEC>
-__global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(const BalParams p, const float* __restrict__ dlosses,
-                                                                  int rows_per_block, float* __restrict__ dlogits) {
+constexpr int kBalBwdThreads = 256;
+constexpr int kBalBwdWarps = kBalBwdThreads / 32;
+template <int G, int NV, bool VEC, bool SIG>
+__global__ void __launch_bounds__(kBalBwdThreads, 4)
+    balance_bwd_kernel(const BalParams p, const float* __restrict__ dlosses, int rows_per_block,
+                       float* __restrict__ dlogits) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int lo = static_cast<int>(min(static_cast<long long>(blockIdx.x) * rows_per_block, static_cast<long long>(p.T)));
   const int hi = static_cast<int>(min(static_cast<long long>(lo) + rows_per_block, static_cast<long long>(p.T)));
@@ -373,81 +542,78 @@ __global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(const BalParam
   const float gb = (dlosses != nullptr ? dlosses[0] : 1.0f) * tail[0];
   const float gz = (dlosses != nullptr ? dlosses[1] : 1.0f) * tail[1];
   const int gl = lane & (G - 1), grp = lane / G;
-  constexpr int RPW = 32 / G;
-  int s = s0, have = -1;
-  float w[4 * NV];
-  for (int t0 = lo + warp * RPW; t0 < hi; t0 += kBalWarps * RPW) {
-    const int t = t0 + grp;
-    bool ok = t < hi;
-    if (ok) {
-      while (s + 1 < p.S && seq_begin(p.off, s + 1, p.S, p.T) <= t) ++s;
-      ok = s >= 0 && t >= seq_begin(p.off, s, p.S, p.T) && t < seq_begin(p.off, s + 1, p.S, p.T) &&
-           (p.mask == nullptr || p.mask[t] != 0);
-    }
-    float v[4 * NV], sg[4 * NV], d[4 * NV];
-    if (ok) {
-      load_row<G, NV, VEC>(p.logits + static_cast<size_t>(t) * p.E, p.E, gl, v);
-      if (have != s) {
-        have = s;
+  constexpr int RPW = 32 / G, U = kBalUnroll;
+  int s = s0, have = -1;  // the sequence of the row at hand, and the one whose weights w holds
+  int begin = s >= 0 ? seq_begin(p.off, s, p.S, p.T) : 0, end = s >= 0 ? seq_begin(p.off, s + 1, p.S, p.T) : 0;
+  f2 w[2 * NV];
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+  for (int i = 0; i < 2 * NV; ++i) w[i] = both(0.0f);
+  for (int t0 = lo + warp * RPW; t0 < hi; t0 += U * kBalBwdWarps * RPW) {
+    f2 v[U][2 * NV];
+    float top = 0.0f;
+    int seq[U];  // -1: no valid row
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e = 4 * (gl + G * j) + i;
-            w[4 * j + i] = e < p.E ? gb * p.stats[static_cast<size_t>(s) * p.E + e] : 0.0f;
-          }
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * kBalBwdWarps * RPW + grp;
+      seq[u] = -1;
+      if (t < hi) {
+        if (t >= end && s + 1 < p.S) {  // rows come in ascending order
+          while (s + 1 < p.S && seq_begin(p.off, s + 1, p.S, p.T) <= t) ++s;
+          begin = seq_begin(p.off, s, p.S, p.T);
+          end = seq_begin(p.off, s + 1, p.S, p.T);
+        }
+        if (s >= 0 && t >= begin && t < end && (p.mask == nullptr || p.mask[t] != 0)) seq[u] = s;
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4 * NV; ++i) v[i] = 0.0f;
-      have = -1;
-#pragma unroll
-      for (int i = 0; i < 4 * NV; ++i) w[i] = 0.0f;
-    }
-    if (p.sigmoid) {
-      float sum = 0.0f, dot = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4 * NV; ++i) {
-        const float2 q = sigmoid2(v[i]);
-        sg[i] = q.x;
-        d[i] = q.x * q.y;
-        sum += q.x;
-        dot += q.x * w[i];
-      }
-      const float inv = 1.0f / group_sum<G>(sum);
-      const float mean = group_sum<G>(dot) * inv;
-#pragma unroll
-      for (int i = 0; i < 4 * NV; ++i) d[i] = d[i] * inv * (w[i] - mean);
-    }
-    if (!p.sigmoid || p.need_lse) {
-      float lse;
-      const float inv = row_softmax<G, NV>(v, lse);
-      const float zz = gz * lse;
-      if (!p.sigmoid) {
-        float dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) dot += v[i] * w[i];
-        const float mean = group_sum<G>(dot) * inv;
-#pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) d[i] = v[i] * inv * (p.need_lse ? w[i] - mean + zz : w[i] - mean);
+      if (seq[u] >= 0) {
+        load_row<G, NV, VEC>(p.logits + static_cast<size_t>(t) * p.E, p.E, gl, v[u], top);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) d[i] += v[i] * inv * zz;
+        for (int i = 0; i < 2 * NV; ++i) v[u][i] = both(0.0f);
       }
     }
-    if (t < hi) {
+    const bool near = __all_sync(0xffffffffu, top <= kNear);
+    const auto weights_of = [&](int u) {
+      if (seq[u] < 0 || seq[u] == have) return;
+      have = seq[u];
+#pragma unroll
+      for (int i = 0; i < 2 * NV; ++i) {
+        const int e = 4 * (gl + G * (i >> 1)) + 2 * (i & 1);
+        const float* row = p.stats + static_cast<size_t>(have) * p.E;
+        w[i] = pack2(e < p.E ? gb * row[e] : 0.0f, e + 1 < p.E ? gb * row[e + 1] : 0.0f);
+      }
+    };
+    f2 q[U][2 * NV];
+    float inv[U], lse[U], sinv[U], dot[U];
+    if (near) row_scores<G, NV, SIG, true, true>(gl, v, q, w, weights_of, inv, lse, sinv, dot);
+    else row_scores<G, NV, SIG, true, false>(gl, v, q, w, weights_of, inv, lse, sinv, dot);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * kBalBwdWarps * RPW + grp;
+      if (t >= hi) continue;
+      weights_of(u);
+      const bool live = seq[u] >= 0;
+      const f2 mean = both(-dot[u] * (SIG ? sinv[u] : inv[u]));
+      const f2 zz = both(p.need_lse ? gz * lse[u] * inv[u] : 0.0f);
+      const f2 scale = both(SIG ? sinv[u] : inv[u]);
       float* out = dlogits + static_cast<size_t>(t) * p.E;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
+        float d[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = 2 * j + h;
+          const f2 away = mul2(add2(w[i], mean), scale);
+          const float2 x = unpack2(SIG ? fma2(q[u][i], away, mul2(v[u][i], zz)) : mul2(v[u][i], add2(away, zz)));
+          d[2 * h] = live ? x.x : 0.0f;
+          d[2 * h + 1] = live ? x.y : 0.0f;
+        }
         const int e = 4 * (gl + G * j);
         if constexpr (VEC) {
-          if (e < p.E)
-            *reinterpret_cast<float4*>(out + e) = ok ? make_float4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3])
-                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+          if (e < p.E) __stcs(reinterpret_cast<float4*>(out + e), make_float4(d[0], d[1], d[2], d[3]));
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (e + i < p.E) out[e + i] = ok ? d[4 * j + i] : 0.0f;
+            if (e + i < p.E) out[e + i] = d[i];
         }
       }
     }
@@ -457,11 +623,17 @@ __global__ void __launch_bounds__(kBalThreads) balance_bwd_kernel(const BalParam
 // Lanes of a row by E: the smallest group whose lanes hold four experts each,
 // two sets of four from 129 experts on.
 template <class F>
-static cudaError_t balance_dispatch(int E, bool vec, F f) {
-#define MOE_BAL(G, NV)                                                            \
-  do {                                                                            \
-    if (vec) f(std::integral_constant<int, G>{}, std::integral_constant<int, NV>{}, std::true_type{}); \
-    else f(std::integral_constant<int, G>{}, std::integral_constant<int, NV>{}, std::false_type{});    \
+static cudaError_t balance_dispatch(int E, bool sigmoid, F f) {
+  const bool vec = E % 4 == 0;
+#define MOE_BAL_SIG(G, NV, VEC)                                                                                  \
+  do {                                                                                                           \
+    if (sigmoid) f(std::integral_constant<int, G>{}, std::integral_constant<int, NV>{}, VEC{}, std::true_type{}); \
+    else f(std::integral_constant<int, G>{}, std::integral_constant<int, NV>{}, VEC{}, std::false_type{});       \
+  } while (0)
+#define MOE_BAL(G, NV)                               \
+  do {                                               \
+    if (vec) MOE_BAL_SIG(G, NV, std::true_type);     \
+    else MOE_BAL_SIG(G, NV, std::false_type);        \
   } while (0)
   if (E <= 8) MOE_BAL(2, 1);
   else if (E <= 16) MOE_BAL(4, 1);
@@ -470,6 +642,7 @@ static cudaError_t balance_dispatch(int E, bool vec, F f) {
   else if (E <= 128) MOE_BAL(32, 1);
   else MOE_BAL(32, 2);
 #undef MOE_BAL
+#undef MOE_BAL_SIG
   return cudaGetLastError();
 }
 
@@ -478,20 +651,21 @@ static int check_balance(const moe_balance_config* c) {
   if (c->T < 1 || c->E < 1 || c->k < 1 || c->n_seqs < 1 || c->k > c->E) return MOE_ERR_INVALID_ARG;
   if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
   if (!isfinite(c->balance_coeff) || !isfinite(c->z_coeff)) return MOE_ERR_INVALID_ARG;
-  if (c->E > 256 || c->k > 16 || c->n_seqs > (1 << 20)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (c->E > 256 || c->k > 16 || c->n_seqs > (1 << 16)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (static_cast<long long>(c->T) * c->k >= (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
 }
 
-// Rows of a chunk: about two chunks for each SM, whole passes of the block
-static int balance_chunk_rows(int T) {
-  const int want = (T + 303) / 304;
-  return std::max(64, (want + 31) / 32 * 32);
+// Rows of a block: one wave of four blocks for each SM (blocks of half a wave more
+// than that took 70 us where one wave takes 39), whole passes of a block
+static int balance_block_rows(int T) {
+  const int want = (T + 4 * 152 - 1) / (4 * 152);
+  return std::max(32, want);
 }
 
 struct BalWs {
   size_t part_p, part_c, part_z, part_n, seq_b, seq_z, seq_n, total;
-  int CH, chunks;
+  int CH, blocks, slots;
 };
 static BalWs balance_ws(const moe_balance_config& c) {
   BalWs w{};
@@ -501,14 +675,15 @@ static BalWs balance_ws(const moe_balance_config& c) {
     o += (b + 255) & ~size_t(255);
     return at;
   };
-  w.CH = balance_chunk_rows(c.T);
-  w.chunks = c.T / w.CH + c.n_seqs + 1;
-  const size_t n = w.chunks, S = c.n_seqs;
+  w.CH = balance_block_rows(c.T);
+  w.blocks = (c.T + w.CH - 1) / w.CH;
+  w.slots = w.blocks + c.n_seqs;
+  const size_t n = w.slots, S = c.n_seqs;
   w.part_p = take(4 * n * c.E);
   w.part_c = take(4 * n * c.E);
   w.part_z = take(4 * n);
   w.part_n = take(4 * n);
-  w.seq_b = take(8 * S);
+  w.seq_b = take(8 * S * ((c.E + 31) / 32));
   w.seq_z = take(8 * S);
   w.seq_n = take(4 * S);
   w.total = o;
@@ -568,13 +743,13 @@ int moe_balance_loss_fwd(const moe_balance_config* cfg, const float* logits, con
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.topk = topk_idx;
   p.CH = L.CH;
-  p.chunks = L.chunks;
+  p.slots = L.slots;
   p.part_p = reinterpret_cast<float*>(w + L.part_p);
   p.part_c = reinterpret_cast<int32_t*>(w + L.part_c);
   p.part_z = reinterpret_cast<float*>(w + L.part_z);
   p.part_n = reinterpret_cast<int32_t*>(w + L.part_n);
-  p.seq_b = reinterpret_cast<double*>(w + L.seq_b);
-  p.seq_z = reinterpret_cast<double*>(w + L.seq_z);
+  p.seq_b = reinterpret_cast<float2*>(w + L.seq_b);
+  p.seq_z = reinterpret_cast<float2*>(w + L.seq_z);
   p.seq_n = reinterpret_cast<int32_t*>(w + L.seq_n);
   p.st = reinterpret_cast<DevStatus*>(w);
   p.ticket = &p.st->chunk_counter;
@@ -582,13 +757,15 @@ int moe_balance_loss_fwd(const moe_balance_config* cfg, const float* logits, con
   p.losses = losses;
   p.stats = stats;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = balance_dispatch(c.E, c.E % 4 == 0, [&](auto g, auto nv, auto vec) {
-    balance_part_kernel<decltype(g)::value, decltype(nv)::value, decltype(vec)::value>
-        <<<L.chunks, kBalThreads, 0, s>>>(p);
+  cudaError_t e = balance_dispatch(c.E, p.sigmoid, [&](auto g, auto nv, auto vec, auto sig) {
+    balance_part_kernel<decltype(g)::value, decltype(nv)::value, decltype(vec)::value, decltype(sig)::value>
+        <<<L.blocks, kBalThreads, 0, s>>>(p);
   });
   if (e != cudaSuccess) return status_from_cuda(e);
-  balance_join_kernel<<<c.n_seqs, kBalJoin, 0, s>>>(p);
-  e = cudaGetLastError();
+  // few, long sequences: a large block for each; many short ones: small blocks
+  const dim3 grid(c.n_seqs, (c.E + 31) / 32);
+  e = L.slots / c.n_seqs > 40 ? launch_chained(balance_join_kernel<32>, grid, 1024, 0, s, p)
+                              : launch_chained(balance_join_kernel<4>, grid, 128, 0, s, p);
   record_stage(s, 43, 2);
   return status_from_cuda(e);
 }
@@ -608,12 +785,11 @@ int moe_balance_loss_bwd(const moe_balance_config* cfg, const float* logits, con
   BalParams p = balance_params(c, logits, seq_offsets, token_mask);
   p.stats = const_cast<float*>(stats);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int grid_max = 8 * num_sms();
-  const int rows = std::max(32, (c.T + grid_max - 1) / grid_max);
+  const int rows = balance_block_rows(c.T);
   const int grid = (c.T + rows - 1) / rows;
-  const cudaError_t e = balance_dispatch(c.E, c.E % 4 == 0, [&](auto g, auto nv, auto vec) {
-    balance_bwd_kernel<decltype(g)::value, decltype(nv)::value, decltype(vec)::value>
-        <<<grid, kBalThreads, 0, s>>>(p, dlosses, rows, dlogits);
+  const cudaError_t e = balance_dispatch(c.E, p.sigmoid, [&](auto g, auto nv, auto vec, auto sig) {
+    balance_bwd_kernel<decltype(g)::value, decltype(nv)::value, decltype(vec)::value, decltype(sig)::value>
+        <<<grid, kBalBwdThreads, 0, s>>>(p, dlosses, rows, dlogits);
   });
   record_stage(s, 44, 1);
   return status_from_cuda(e);

@@ -54,6 +54,14 @@ __device__ __forceinline__ uint64_t globaltimer() {
   return t;
 }
 
+// Launches that follow another of the same call (launch_chained): the next
+// kernel may start when every block of this one has called chain_release or
+// ended, and waits in chain_wait until this one has finished and its writes are
+// visible. What runs before chain_wait must not touch memory that an earlier
+// kernel writes or reads-and-expects-unchanged.
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void chain_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // bf16 helpers
 // ---------------------------------------------------------------------------

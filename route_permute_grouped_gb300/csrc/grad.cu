@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <type_traits>
 #include <vector>
 
 #include "host_util.h"
@@ -30,6 +31,7 @@ template <int N>
 struct GradBlock {
   int count;    // tensors
   int chunks;   // chunks of all of them
+  int apart;    // some tensor has an output of its own
   int first[N];
   uint8_t dtype[N];
   GradItem item[N];
@@ -122,32 +124,46 @@ __device__ __forceinline__ uint4 pack(const float (&f)[DT == MOE_FP32 ? 4 : 8]) 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Squares of a group of values, added to the thread's double sum. In fp32 a
-// square leaves the range for |g| above 2^64 and loses its bits below 2^-63,
-// so a group whose largest magnitude lies outside [2^-60, 2^60] (and is not 0)
-// is squared in fp64; NaN and infinities take that way too. Elsewhere the
-// group's squares (16 or 32 of them) are added in fp32 and the groups in fp64:
-// 1/16 or 1/32 of the additions, which the small FP64 rate carries.
-constexpr uint32_t kSquareLo = (127u - 60u) << 23, kSquareHi = (127u + 60u) << 23;
-template <int NV>
-__device__ __forceinline__ double squares(const float (&f)[NV], uint32_t& top) {
-  float s = 0.0f;
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    s = fmaf(f[i], f[i], s);
-    m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+// The squares of a thread's values: a sum in two floats (s + e: the exact sum but
+// for the roundings of e), and beside it one in fp64 for values whose squares
+// leave fp32. A square leaves its range for |g| above 2^64 and loses its bits
+// below 2^-63, so a group (the 16 or 32 values of a pass) whose largest magnitude
+// lies outside [2^-60, 2^40] and is not 0 is squared in fp64; NaN and infinities
+// take that way too. Elsewhere the group's squares are added in fp32 and the
+// groups in two floats: 2^85 a group leaves room for 2^42 of them. fp64 runs at
+// about two additions a clock and SM, which even the blocks' own reductions felt
+// (norm of 123 MB: 32 us with fp64 throughout).
+constexpr uint32_t kSquareLo = (127u - 60u) << 23, kSquareHi = (127u + 40u) << 23;
+struct Squares {
+  float s = 0.0f, e = 0.0f;
+  uint32_t top = 0;  // largest magnitude, as fp32 bits: NaN above infinity above the finite values
+  double far = 0.0;
+  __device__ __forceinline__ void add(float x) {
+    const float t = s + x, b = t - s;
+    e += (s - (t - b)) + (x - b);
+    s = t;
   }
-  top = max(top, m);
-  if (m <= kSquareHi && (m >= kSquareLo || m == 0)) return s;
-  double d = 0.0;
-  for (int i = 0; i < NV; ++i) d += static_cast<double>(f[i]) * f[i];
-  return d;
-}
+  template <int NV>
+  __device__ __forceinline__ void group(const float (&f)[NV]) {
+    float q = 0.0f;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      q = fmaf(f[i], f[i], q);
+      m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+    }
+    top = max(top, m);
+    if (m <= kSquareHi && (m >= kSquareLo || m == 0)) {
+      add(q);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) far += static_cast<double>(f[i]) * f[i];
+    }
+  }
+};
 
 template <int DT>
-__device__ __forceinline__ void norm_chunk(const uint4* __restrict__ v, long long vecs, long long at, double& sum,
-                                           uint32_t& top) {
+__device__ __forceinline__ void norm_chunk(const uint4* __restrict__ v, long long vecs, long long at, Squares& sq) {
   constexpr int PER = DT == MOE_FP32 ? 4 : 8;
   uint4 w[kVecsPerThread];
 #pragma unroll
@@ -163,87 +179,120 @@ __device__ __forceinline__ void norm_chunk(const uint4* __restrict__ v, long lon
 #pragma unroll
     for (int i = 0; i < PER; ++i) f[j * PER + i] = g[i];
   }
-  sum += squares(f, top);
+  sq.group(f);
 }
 
-// One CTA takes chunks blockIdx, blockIdx + gridDim, ...; its sum (fp64) and
-// largest magnitude (fp32 bits: NaN above infinity above the finite values) go
-// to partials[blockIdx], added in a fixed order afterwards.
+// A CTA takes the chunks first, first + blocks, ... (neighbouring CTAs on
+// neighbouring chunks: runs of chunks for each CTA took 10% longer to scale
+// 2.4 GB). The tensor of the first one is searched, later ones lie further on.
+template <int N>
+struct ChunkWalk {
+  int c, t;
+  __device__ __forceinline__ ChunkWalk(const GradBlock<N>& b, int first) : c(first) {
+    t = c < b.chunks ? find_tensor(b, c) : 0;
+  }
+  __device__ __forceinline__ void next(const GradBlock<N>& b, int blocks) {
+    c += blocks;
+    if (c >= b.chunks) return;
+    if (t + 1 < b.count && b.first[t + 1] <= c) {
+      ++t;
+      if (t + 1 < b.count && b.first[t + 1] <= c) t = find_tensor(b, c);
+    }
+  }
+};
+
+// Each CTA's sum (fp64) and largest magnitude go to its partial; the CTA that
+// arrives last, over all launches of a list, adds them in a fixed order, writes
+// the norm and puts the ticket back to 0.
 struct NormPartial {
   double sum;
   unsigned long long top;
 };
+constexpr int kGradWarps = kGradThreads / 32;
 template <int N>
-__global__ void __launch_bounds__(kGradThreads) norm_kernel(const __grid_constant__ GradBlock<N> b,
-                                                            NormPartial* __restrict__ partials) {
-  double sum = 0.0;
-  uint32_t top = 0;
-  for (int c = blockIdx.x; c < b.chunks; c += gridDim.x) {
-    const int t = find_tensor(b, c);
+__global__ void __launch_bounds__(kGradThreads)
+    norm_kernel(const __grid_constant__ GradBlock<N> b, NormPartial* __restrict__ partials, int at_partial, int all,
+                int kind, int* __restrict__ ticket, float* __restrict__ norm) {
+  Squares sq;
+  for (ChunkWalk<N> run(b, blockIdx.x); run.c < b.chunks; run.next(b, gridDim.x)) {
+    const int c = run.c, t = run.t;
     const int dt = b.dtype[t];
     const GradItem it = b.item[t];
     const int eb = dt == MOE_FP32 ? 4 : 2;
     const Span sp = span_of(it.in, it.n, eb);
     const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(it.in) + static_cast<size_t>(sp.head) * eb);
     const long long at = static_cast<long long>(c - b.first[t]) * kChunkVecs;
-    if (dt == MOE_FP32) norm_chunk<MOE_FP32>(v, sp.vecs, at, sum, top);
-    else if (dt == MOE_BF16) norm_chunk<MOE_BF16>(v, sp.vecs, at, sum, top);
-    else norm_chunk<MOE_FP16>(v, sp.vecs, at, sum, top);
+    if (dt == MOE_FP32) norm_chunk<MOE_FP32>(v, sp.vecs, at, sq);
+    else if (dt == MOE_BF16) norm_chunk<MOE_BF16>(v, sp.vecs, at, sq);
+    else norm_chunk<MOE_FP16>(v, sp.vecs, at, sq);
     if (at == 0 && threadIdx.x < static_cast<unsigned>(sp.head + sp.tail)) {
       const long long i = threadIdx.x < static_cast<unsigned>(sp.head) ? threadIdx.x : it.n - sp.tail + (threadIdx.x - sp.head);
       const float f[1] = {elem_f32(it.in, i, dt)};
-      sum += squares(f, top);
+      sq.group(f);
     }
   }
-  __shared__ double s_sum[kGradThreads / 32];
-  __shared__ uint32_t s_top[kGradThreads / 32];
+  __shared__ float2 s_sum[kGradWarps];
+  __shared__ uint32_t s_top[kGradWarps];
+  __shared__ double s_far[kGradThreads];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  chain_release();
+  const bool any_far = __syncthreads_or(sq.far != 0.0) != 0;  // true for NaN
+  if (any_far) s_far[tid] = sq.far;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float os = __shfl_xor_sync(0xffffffffu, sq.s, o), oe = __shfl_xor_sync(0xffffffffu, sq.e, o);
+    sq.add(os);
+    sq.e += oe;
+    sq.top = max(sq.top, __shfl_xor_sync(0xffffffffu, sq.top, o));
   }
-  if ((threadIdx.x & 31) == 0) {
-    s_sum[threadIdx.x >> 5] = sum;
-    s_top[threadIdx.x >> 5] = top;
+  if (lane == 0) {
+    s_sum[warp] = make_float2(sq.s, sq.e);
+    s_top[warp] = sq.top;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kGradThreads / 32; ++w) {
-      sum += s_sum[w];
-      top = max(top, s_top[w]);
+  if (tid == 0) {
+    for (int w = 1; w < kGradWarps; ++w) {
+      sq.add(s_sum[w].x);
+      sq.e += s_sum[w].y;
+      sq.top = max(sq.top, s_top[w]);
     }
-    partials[blockIdx.x].sum = sum;
-    partials[blockIdx.x].top = top;
+    double sum = static_cast<double>(sq.s) + sq.e;
+    if (any_far)
+      for (int i = 0; i < kGradThreads; ++i) sum += s_far[i];
+    partials[at_partial + blockIdx.x].sum = sum;
+    partials[at_partial + blockIdx.x].top = sq.top;
+    __threadfence();
+    s_last = atomicAdd(ticket, 1) == all - 1;
+    __threadfence();
   }
-}
-
-// The norm from the partials, by every thread of a CTA in the same fixed order.
-__device__ __forceinline__ float join_norm(const NormPartial* __restrict__ partials, int n, int kind) {
-  __shared__ double s_sum[kGradThreads];
-  __shared__ uint32_t s_top[kGradThreads];
+  __syncthreads();
+  if (!s_last) return;
+  // a warp's worth of fp64 additions: the block's threads add what lies
+  // kGradThreads apart (rarely more than two), lane l those of threads l, l + 32, ...
   double sum = 0.0;
   uint32_t top = 0;
-  for (int i = threadIdx.x; i < n; i += kGradThreads) {
-    sum += partials[i].sum;
-    top = max(top, static_cast<uint32_t>(partials[i].top));
+  for (int i = tid; i < all; i += kGradThreads) {
+    sum += __ldcg(&partials[i].sum);
+    top = max(top, static_cast<uint32_t>(__ldcg(&partials[i].top)));
   }
-  s_sum[threadIdx.x] = sum;
-  s_top[threadIdx.x] = top;
+  s_far[tid] = sum;
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) s_top[warp] = top;
   __syncthreads();
-  for (int st = kGradThreads / 2; st > 0; st >>= 1) {
-    if (threadIdx.x < static_cast<unsigned>(st)) {
-      s_sum[threadIdx.x] += s_sum[threadIdx.x + st];
-      s_top[threadIdx.x] = max(s_top[threadIdx.x], s_top[threadIdx.x + st]);
-    }
-    __syncthreads();
+  if (warp != 0) return;
+  sum = 0.0;
+#pragma unroll
+  for (int w = 0; w < kGradWarps; ++w) {
+    sum += s_far[32 * w + lane];
+    top = max(top, s_top[w]);
   }
-  return kind == MOE_NORM_MAX ? __uint_as_float(s_top[0]) : static_cast<float>(sqrt(s_sum[0]));
-}
-
-__global__ void __launch_bounds__(kGradThreads) norm_join_kernel(const NormPartial* __restrict__ partials, int n,
-                                                                 int kind, float* __restrict__ norm) {
-  const float v = join_norm(partials, n, kind);
-  if (threadIdx.x == 0) *norm = v;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) {
+    *norm = kind == MOE_NORM_MAX ? __uint_as_float(top) : static_cast<float>(sqrt(sum));
+    *ticket = 0;
+  }
 }
 
 template <int DT>
@@ -271,17 +320,19 @@ __device__ __forceinline__ void scale_chunk(const uint4* __restrict__ v, uint4* 
 
 // g = round(g * coef), coef = min(1, max_norm / (norm + 1e-6)) (NaN for a NaN
 // norm). coef = 1 leaves every bit as it is, so tensors scaled in place are
-// then neither read nor written.
+// then neither read nor written. The chunks go from the last one down: what the
+// norm's pass read last is what L2 still holds.
 template <int N>
 __global__ void __launch_bounds__(kGradThreads) clip_kernel(const __grid_constant__ GradBlock<N> b,
-                                                            const NormPartial* __restrict__ partials, int n_partials,
-                                                            int kind, float max_norm, float* __restrict__ norm_out) {
-  const float norm = join_norm(partials, n_partials, kind);
-  if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
-  float coef = max_norm / (norm + 1e-6f);
+                                                            const float* __restrict__ norm, float max_norm) {
+  if (static_cast<int>(blockIdx.x) >= b.chunks) return;
+  chain_wait();
+  float coef = max_norm / (__ldcg(norm) + 1e-6f);
   if (coef > 1.0f) coef = 1.0f;
-  for (int c = blockIdx.x; c < b.chunks; c += gridDim.x) {
-    const int t = find_tensor(b, c);
+  if (coef == 1.0f && !b.apart) return;
+  const int last = (b.chunks - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x);
+  for (int i = last; i >= 0; --i) {
+    const int c = blockIdx.x + i * gridDim.x, t = find_tensor(b, c);
     const int dt = b.dtype[t];
     const GradItem it = b.item[t];
     if (coef == 1.0f && it.in == it.out) continue;
@@ -310,6 +361,10 @@ __global__ void __launch_bounds__(kGradThreads) clip_kernel(const __grid_constan
   }
 }
 
+template <int N>
+static auto clip_kernel_of(const GradBlock<N>*) {
+  return clip_kernel<N>;
+}
 static int grad_grid(int chunks) { return std::max(1, std::min(chunks, std::min(4 * num_sms(), kMaxPartials))); }
 
 // launches `f` with the block in the smallest parameter size that holds it
@@ -318,6 +373,7 @@ static cudaError_t with_block(const GradBlock<kListTensors>& b, F f) {
   auto copy = [&](auto& small) {
     small.count = b.count;
     small.chunks = b.chunks;
+    small.apart = b.apart;
     memcpy(small.first, b.first, sizeof(int) * b.count);
     memcpy(small.dtype, b.dtype, b.count);
     memcpy(small.item, b.item, sizeof(GradItem) * b.count);
@@ -340,18 +396,21 @@ static const GradList* as_list(const void* list) {
   return l != nullptr && (reinterpret_cast<uintptr_t>(list) & 7u) == 0 && l->magic == kListMagic ? l : nullptr;
 }
 
-static int run_norm(const GradList& l, NormPartial* partials, int* n_partials, cudaStream_t s) {
+static int run_norm(const GradList& l, int kind, float* norm, void* ws, cudaStream_t s) {
+  int* ticket = &static_cast<DevStatus*>(ws)->chunk_counter;
+  NormPartial* partials = reinterpret_cast<NormPartial*>(static_cast<uint8_t*>(ws) + sizeof(DevStatus));
+  int all = 0;
+  for (int i = 0; i < l.launches; ++i) all += grad_grid(l.block[i].chunks);
   int at = 0;
   for (int i = 0; i < l.launches; ++i) {
     const int grid = grad_grid(l.block[i].chunks);
     const cudaError_t e = with_block(l.block[i], [&](const auto& b) {
-      norm_kernel<<<grid, kGradThreads, 0, s>>>(b, partials + at);
+      norm_kernel<<<grid, kGradThreads, 0, s>>>(b, partials, at, all, kind, ticket, norm);
     });
     if (e != cudaSuccess) return status_from_cuda(e);
     record_stage(s, 40, 1);
     at += grid;
   }
-  *n_partials = at;
   return MOE_OK;
 }
 
@@ -384,7 +443,7 @@ int moe_tensor_list_build(const moe_tensor* ts, int n, void* list, size_t list_s
   l->n = n;
   l->pad = 0;
   l->launches = std::max(1, (n + kListTensors - 1) / kListTensors);
-  for (int i = 0; i < l->launches; ++i) l->block[i].count = l->block[i].chunks = 0;
+  for (int i = 0; i < l->launches; ++i) l->block[i].count = l->block[i].chunks = l->block[i].apart = 0;
   for (int i = 0; i < n; ++i) {
     const moe_tensor& t = ts[i];
     if (t.dtype != MOE_FP32 && t.dtype != MOE_BF16 && t.dtype != MOE_FP16) return MOE_ERR_INVALID_ARG;
@@ -403,6 +462,7 @@ int moe_tensor_list_build(const moe_tensor* ts, int n, void* list, size_t list_s
     const Span sp = span_of(t.data, t.n, eb);
     const long long chunks = std::max(1ll, (sp.vecs + kChunkVecs - 1) / kChunkVecs);
     if (b.chunks + chunks > (1ll << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (out != t.data) b.apart = 1;
     b.first[b.count] = b.chunks;
     b.dtype[b.count] = static_cast<uint8_t>(t.dtype);
     b.item[b.count] = {t.data, out, t.n};
@@ -422,7 +482,7 @@ int moe_tensor_list_build(const moe_tensor* ts, int n, void* list, size_t list_s
 }
 
 size_t moe_grad_norm_workspace_bytes(void) {
-  return 256 + sizeof(NormPartial) * static_cast<size_t>(kMaxLaunches) * kMaxPartials;
+  return sizeof(DevStatus) + sizeof(NormPartial) * static_cast<size_t>(kMaxLaunches) * kMaxPartials;
 }
 
 int moe_grad_norm(const void* list, int kind, float* norm, void* ws, size_t ws_bytes, void* stream) {
@@ -434,14 +494,7 @@ int moe_grad_norm(const void* list, int kind, float* norm, void* ws, size_t ws_b
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_grad_norm_workspace_bytes()) return MOE_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  NormPartial* partials = reinterpret_cast<NormPartial*>(static_cast<uint8_t*>(ws) + 256);
-  int n = 0;
-  const int st = run_norm(*l, partials, &n, s);
-  if (st != MOE_OK) return st;
-  norm_join_kernel<<<1, kGradThreads, 0, s>>>(partials, n, kind, norm);
-  const int rc = status_from_cuda(cudaGetLastError());
-  record_stage(s, 41, 1);
-  return rc;
+  return run_norm(*l, kind, norm, ws, s);
 }
 
 int moe_clip_grad_norm(const void* list, int kind, float max_norm, float* norm, void* ws, size_t ws_bytes,
@@ -455,17 +508,18 @@ int moe_clip_grad_norm(const void* list, int kind, float max_norm, float* norm, 
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_grad_norm_workspace_bytes()) return MOE_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  NormPartial* partials = reinterpret_cast<NormPartial*>(static_cast<uint8_t*>(ws) + 256);
-  int n = 0;
-  const int st = run_norm(*l, partials, &n, s);
+  const int st = run_norm(*l, kind, norm, ws, s);
   if (st != MOE_OK) return st;
   for (int i = 0; i < l->launches; ++i) {
+    cudaError_t e2 = cudaSuccess;
     const cudaError_t e = with_block(l->block[i], [&](const auto& b) {
-      clip_kernel<<<grad_grid(b.chunks), kGradThreads, 0, s>>>(b, partials, n, kind, max_norm,
-                                                               i == 0 ? norm : nullptr);
+      using Block = std::remove_cv_t<std::remove_reference_t<decltype(b)>>;
+      e2 = launch_chained(clip_kernel_of(static_cast<const Block*>(nullptr)), grad_grid(b.chunks), kGradThreads, 0, s,
+                          b, static_cast<const float*>(norm), max_norm);
     });
+    if (e2 != cudaSuccess) return status_from_cuda(e2);
     if (e != cudaSuccess) return status_from_cuda(e);
-    record_stage(s, 42, 1);
+    record_stage(s, 41, 1);
   }
   return MOE_OK;
 }

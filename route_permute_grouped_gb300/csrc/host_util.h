@@ -30,6 +30,26 @@ bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t ou
                    uint32_t box_inner, uint32_t box_outer);
 
 int num_sms();
+
+// A launch that may begin before the kernel ahead of it in the stream has ended
+// (programmatic dependent launch); the kernel calls chain_wait() before it
+// reads or writes anything that the one ahead touches. Used behind the library's own
+// kernels of the same call only: it hides most of a launch's latency, about 2 us.
+template <class... P, class... A>
+cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const void* ptrs[] = {static_cast<const void*>(&args)...};
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kernel), const_cast<void**>(ptrs));
+}
 // Bookkeeping every entry point does after enqueueing a stage: launch counter,
 // profiling event (tag as in moe_profile_start), debug synchronisation.
 void record_stage(cudaStream_t s, int tag, int launches);

@@ -197,7 +197,7 @@ STAGE_NAMES = {20: "nv_quantize", 21: "nv_gemm", 22: "mx_quantize_tokens", 24: "
                6: "shared_down", 7: "combine", 10: "combine_bwd", 11: "router_bwd_elem", 12: "dgrad_down_swiglu",
                13: "wgrad_down", 14: "dgrad_gate_up", 15: "wgrad_gate_up", 16: "router_dgrad",
                17: "permute_bwd", 18: "router_wgrad", 19: "aux_loss", 30: "read_ceiling",
-               31: "write_ceiling", 40: "grad_norm", 41: "grad_norm_join", 42: "grad_clip", 43: "balance_loss",
+               31: "write_ceiling", 40: "grad_norm", 41: "grad_clip", 43: "balance_loss",
                44: "balance_loss_bwd", 45: "adapter_plan", 46: "adapter_shrink", 47: "adapter_expand",
                48: "adapter_wgrad", 32: "nv_dgrad_down", 33: "nv_swiglu_bwd", 34: "nv_dgrad_gate_up"}
 
@@ -265,7 +265,9 @@ def _p(t):
 
 
 def _stream():
-    return c_void_p(torch.cuda.current_stream().cuda_stream)
+    """The current stream of the current device, as the library takes it (the
+    raw handle: building a torch.cuda.Stream for it costs microseconds)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _check(st, where):
@@ -787,30 +789,54 @@ def layer_bwd_nvfp4(cfg, dO, x, router_w, nvbw, saved, ws=None, grads=None, dlog
 # ---------------------------------------------------------------------------
 def _arg(where, name, t, dtype, shape, optional=False):
     """A tensor argument of the calls below: on the current CUDA device,
-    contiguous, of the given type (or one of them) and shape; its pointer."""
+    contiguous, of the given type (or one of them) and shape; its address."""
+    if isinstance(t, torch.Tensor):
+        if ((t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)) and t.shape == shape and t.is_cuda
+                and t.get_device() == torch._C._cuda_getDevice() and t.is_contiguous()):
+            return t.data_ptr()
+    elif t is None and optional:
+        return None
+    raise _arg_error(where, name, t, dtype if type(dtype) is tuple else (dtype,), shape)
+
+
+def _arg_error(where, name, t, dtypes, shape):
     if t is None:
-        if optional:
-            return None
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} is missing")
-    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
+        why = "is missing"
+    elif not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape:
         got = f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
-        want = " or ".join(str(d) for d in dtypes)
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} must be {want} {tuple(shape)}, not {got}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} must be on the current CUDA device, not {t.device}")
-    if not t.is_contiguous():
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} must be contiguous")
-    return c_void_p(t.data_ptr())
+        why = f"must be {' or '.join(str(d) for d in dtypes)} {tuple(shape)}, not {got}"
+    elif not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        why = f"must be on the current CUDA device, not {t.device}"
+    else:
+        why = "must be contiguous"
+    return MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} {why}")
 
 
 def _ws_arg(where, ws, nbytes):
-    if ws is None or not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8:
+    if not isinstance(ws, torch.Tensor):
         raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: the workspace must be a uint8 tensor")
-    p = _arg(where, "ws", ws, torch.uint8, ws.shape)
+    p = _arg(where, "the workspace", ws, torch.uint8, ws.shape)
     if ws.numel() < nbytes:
         raise MoeError(MOE_ERR_WORKSPACE_TOO_SMALL, where)
     return p
+
+
+_size_cache = {}
+
+
+def _size(name, cfg, *more):
+    """A size the library gives for a config, asked once for each config's
+    values; raises for a config it refuses."""
+    key = (name, bytes(cfg), more)
+    n = _size_cache.get(key)
+    if n is None:
+        n = int(getattr(lib(), name)(ctypes.byref(cfg), *more))
+        if n == 0:
+            raise MoeError(MOE_ERR_INVALID_ARG, name)
+        if len(_size_cache) >= 4096:
+            _size_cache.clear()
+        _size_cache[key] = n
+    return n
 
 
 def _scratch(nbytes, device):
@@ -829,10 +855,7 @@ def make_balance_config(T, E, k, n_seqs=1, score="softmax", balance_coeff=1e-2, 
 
 
 def _balance_sizes(cfg):
-    n = int(lib().moe_balance_workspace_bytes(ctypes.byref(cfg)))
-    if n == 0:
-        raise MoeError(MOE_ERR_INVALID_ARG, "moe_balance_workspace_bytes")
-    return n, int(lib().moe_balance_stats_floats(ctypes.byref(cfg)))
+    return _size("moe_balance_workspace_bytes", cfg), _size("moe_balance_stats_floats", cfg)
 
 
 def balance_workspace(cfg, device="cuda"):
@@ -892,20 +915,13 @@ def make_adapter_config(T, K, N, L, r, out_fp32=False) -> MoeAdapterConfig:
     return MoeAdapterConfig(T, K, N, L, r, int(out_fp32))
 
 
-def _adapter_bytes(fn, cfg, *more):
-    n = int(fn(ctypes.byref(cfg), *more))
-    if n == 0:
-        raise MoeError(MOE_ERR_INVALID_ARG, fn.__name__)
-    return n
-
-
 def adapter_workspace(cfg, training=False, device="cuda"):
-    return _scratch(_adapter_bytes(lib().moe_adapter_workspace_bytes, cfg, int(training)), device)
+    return _scratch(_size("moe_adapter_workspace_bytes", cfg, int(training)), device)
 
 
 def alloc_adapter_saved(cfg, device="cuda"):
     """What the training forward keeps for the backward (an opaque buffer)."""
-    return torch.empty(_adapter_bytes(lib().moe_adapter_saved_bytes, cfg), dtype=torch.uint8, device=device)
+    return torch.empty(_size("moe_adapter_saved_bytes", cfg), dtype=torch.uint8, device=device)
 
 
 def adapter_plan(cfg, adapter_idx, plan=None):
@@ -914,7 +930,7 @@ def adapter_plan(cfg, adapter_idx, plan=None):
     serves every projection of the batch, forward and backward, whose config
     has the same T and L. device_status(plan) tells of an index >= L."""
     w = "adapter_plan"
-    n = _adapter_bytes(lib().moe_adapter_plan_bytes, cfg)
+    n = _size("moe_adapter_plan_bytes", cfg)
     idx = _arg(w, "adapter_idx", adapter_idx, torch.int32, (cfg.T,))
     plan = _scratch(n, adapter_idx.device) if plan is None else plan
     _check(lib().moe_adapter_plan(ctypes.byref(cfg), idx, _ws_arg(w, plan, n), plan.numel(), _stream()),
@@ -926,7 +942,7 @@ def _adapter_args(w, cfg, A, B, scale, plan):
     return (_arg(w, "A", A, torch.bfloat16, (cfg.L, cfg.K, cfg.r)),
             _arg(w, "B", B, torch.bfloat16, (cfg.L, cfg.r, cfg.N)),
             _arg(w, "scale", scale, torch.float32, (cfg.L,)),
-            _ws_arg(w, plan, _adapter_bytes(lib().moe_adapter_plan_bytes, cfg)))
+            _ws_arg(w, plan, _size("moe_adapter_plan_bytes", cfg)))
 
 
 def adapter_fwd(cfg, x, A, B, scale, plan, base=None, y=None, u=None, ws=None):
@@ -938,9 +954,9 @@ def adapter_fwd(cfg, x, A, B, scale, plan, base=None, y=None, u=None, ws=None):
     xp = _arg(w, "x", x, torch.bfloat16, (cfg.T, cfg.K))
     weights = _adapter_args(w, cfg, A, B, scale, plan)
     bp = _arg(w, "base", base, _out_dtype(cfg), (cfg.T, cfg.N), optional=True)
-    up = None if u is None else _ws_arg(w, u, _adapter_bytes(lib().moe_adapter_saved_bytes, cfg))
+    up = None if u is None else _ws_arg(w, u, _size("moe_adapter_saved_bytes", cfg))
     ws = adapter_workspace(cfg, False, x.device) if ws is None else ws
-    wp = _ws_arg(w, ws, _adapter_bytes(lib().moe_adapter_workspace_bytes, cfg, 0))
+    wp = _ws_arg(w, ws, _size("moe_adapter_workspace_bytes", cfg, 0))
     if y is None:
         y = torch.empty((cfg.T, cfg.N), dtype=_out_dtype(cfg), device=x.device)
     st = lib().moe_adapter_fwd(ctypes.byref(cfg), xp, *weights, bp, _arg(w, "y", y, _out_dtype(cfg), (cfg.T, cfg.N)),
@@ -963,10 +979,10 @@ def adapter_bwd(cfg, dy, x, A, B, scale, plan, u, dx_base=None, grads=None, ws=N
     dyp = _arg(w, "dy", dy, torch.bfloat16, (cfg.T, cfg.N))
     xp = _arg(w, "x", x, torch.bfloat16, (cfg.T, cfg.K))
     weights = _adapter_args(w, cfg, A, B, scale, plan)
-    up = _ws_arg(w, u, _adapter_bytes(lib().moe_adapter_saved_bytes, cfg))
+    up = _ws_arg(w, u, _size("moe_adapter_saved_bytes", cfg))
     bp = _arg(w, "dx_base", dx_base, _out_dtype(cfg), (cfg.T, cfg.K), optional=True)
     ws = adapter_workspace(cfg, True, x.device) if ws is None else ws
-    wp = _ws_arg(w, ws, _adapter_bytes(lib().moe_adapter_workspace_bytes, cfg, 1))
+    wp = _ws_arg(w, ws, _size("moe_adapter_workspace_bytes", cfg, 1))
     g = alloc_adapter_grads(cfg, x.device) if grads is None else grads
     st = lib().moe_adapter_bwd(ctypes.byref(cfg), dyp, xp, *weights, up, bp,
                                _arg(w, "dx", g["dx"], _out_dtype(cfg), (cfg.T, cfg.K)),

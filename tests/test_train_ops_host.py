@@ -32,7 +32,7 @@ def _moved(call, n, optional=()):
 @pytest.mark.parametrize("over,code", [(dict(T=0), BAD), (dict(E=0), BAD), (dict(k=0), BAD), (dict(k=9), BAD), (dict(n_seqs=0), BAD),
                                        (dict(score=2), BAD), (dict(balance_coeff=float("nan")), BAD),
                                        (dict(z_coeff=float("inf")), BAD), (dict(E=257), SHAPE), (dict(E=64, k=17), SHAPE),
-                                       (dict(T=2 ** 30), SHAPE), (dict(n_seqs=2 ** 20 + 1), SHAPE)])
+                                       (dict(T=2 ** 30), SHAPE), (dict(n_seqs=65537), SHAPE)])
 def test_balance_configs(lib, over, code):
     d = dict(T=64, E=8, k=2) | over
     cfg = ops.make_balance_config(**d)
