@@ -606,8 +606,9 @@ int moe_layer_bwd_nvfp4_dlogits(const moe_config* cfg, const moe_bf16* dO, const
  *   dx[t] = dx_base[t] + du[t] A[a]^T,
  *   dA[a] = sum_t x[t]^T du[t],  dB[a] = sum_t (scale[a] x[t] A[a])^T dy[t]
  * (fp32; zero for an adapter without rows). Products of bf16 inputs are exact
- * and accumulate in fp32; u = scale x A and du enter their second product as
- * two bf16 parts (16 bits). Every sum has a fixed order.
+ * and accumulate in fp32; u = scale x A and du (fp32) enter their second
+ * product in bf16 parts, two for bf16 results and three (24 bits) for fp32
+ * ones. Every sum has a fixed order.
  * Shapes: K, N, r multiples of 8, r <= 128, L <= 1024, 1 <= T <= 2^21,
  * K, N <= 2^20. Adapters of smaller rank are padded with zeros to r.
  * ------------------------------------------------------------------------- */

@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "host_util.h"
 #include "mma.cuh"
@@ -313,6 +314,7 @@ __global__ void __launch_bounds__(kAdThreads)
     }
     slot = (slot + 1) % kStages;
   }
+  chain_release();
   cp_async_wait<0>();
   float* out = parts + (static_cast<size_t>(blockIdx.y) * T + tile.y) * RP;
 #pragma unroll
@@ -327,74 +329,99 @@ __global__ void __launch_bounds__(kAdThreads)
   }
 }
 
+// Columns of a block's step: four warps as 2 x 2, each 32 rows x 64 columns.
 constexpr int kTileCols = 128;
 template <int RP, bool WT, bool F32>
 struct ExpandSmem {
+  // parts of u that the product takes: two (16 bits) leave an error of 2^-17 of
+  // u, far below the rounding of a bf16 result; fp32 results take all three
+  static constexpr int kParts = F32 ? 3 : 2;
+  static constexpr bool kRegs = kParts * RP <= 128;  // u's fragments stay in registers
   static constexpr int kURow = RP + 8;
-  static constexpr int kU = kTileRows * kURow * 2;  // hi; lo follows
+  static constexpr int kU = kTileRows * kURow * 2;  // one part
   static constexpr int kWRow = WT ? RP + 8 : kTileCols + 8;
   static constexpr int kW = (WT ? kTileCols : RP) * kWRow * 2;
-  static constexpr int kYRow = kTileCols * (F32 ? 4 : 2) + 16;  // bytes
-  static constexpr int kTotal = 2 * kU + kW + kTileRows * kYRow;
+  static constexpr int kYRow = 64 * (F32 ? 4 : 2) + 16;  // bytes of a row of a warp's 32 x 64 block
+  static constexpr int kY = 32 * kYRow;
+  static constexpr int kTotal = kParts * kU + 2 * kW + 2 * 4 * kY + 4 * kTileRows;
 };
 
 // out[t][c] = base[t][c] + sum_j u[position][j] W_a[j][c], u = s_a sum over the
-// splits of parts, multiplied as its two bf16 parts (16 bits of u). W_a is
-// [r][C] (WT = false: B of the forward) or [C][r] (WT = true: A of the
-// backward). The blocks of the first columns keep u's two parts for the
-// weight gradients (u_keep: hi [T][RP], then lo).
+// splits of parts. W_a is [r][C] (WT = false: B of the forward) or [C][r]
+// (WT = true: A of the backward). A block takes 64 rows of one adapter and runs
+// over its share of the columns, u's bf16 parts in registers (shared memory at
+// the largest ranks), the next step's tiles of W and of the base on their way
+// while this step's are multiplied; each warp brings, completes and stores its
+// own 32 x 64 piece of the output in whole 128-byte lines. The blocks of the
+// first columns keep u's three parts for the weight gradients (u_keep:
+// [3][T][RP]).
+// Bound by memory: base and out once, W_a from L2 once for every 64 rows.
 template <int RP, bool WT, bool F32>
-__global__ void __launch_bounds__(kAdThreads)
+__global__ void __launch_bounds__(kAdThreads, RP <= 64 && !F32 ? 3 : 2)
     adapter_expand_kernel(const float* __restrict__ parts, int splits, const float* __restrict__ scale,
-                          const __nv_bfloat16* __restrict__ W, PlanView plan, int T, int C, int r,
+                          const __nv_bfloat16* __restrict__ W, PlanView plan, int T, int C, int r, int steps,
                           const void* base_in, void* out, __nv_bfloat16* __restrict__ u_keep) {
   extern __shared__ __align__(16) uint8_t smem[];
   using S = ExpandSmem<RP, WT, F32>;
-  constexpr int EB = F32 ? 4 : 2, PER = 16 / EB, PIECES = kTileCols / PER;
-  if (static_cast<int>(blockIdx.y) >= plan_tiles(plan)) return;
-  const int4 tile = plan.tiles[blockIdx.y];
+  constexpr int EB = F32 ? 4 : 2, PER = 16 / EB, PIECES = 64 / PER, PARTS = S::kParts;
+  chain_wait();
+  if (static_cast<int>(blockIdx.x) >= plan_tiles(plan)) return;
+  const int4 tile = plan.tiles[blockIdx.x];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int c0 = blockIdx.x * kTileCols;
+  const int first = blockIdx.y * steps * kTileCols, last = min(C, first + steps * kTileCols);
+  if (first >= last) return;
+  int* s_tok = reinterpret_cast<int*>(smem + PARTS * S::kU + 2 * S::kW + 8 * S::kY);
+  if (tid < tile.z) s_tok[tid] = plan.order[tile.y + tid];
+  __syncthreads();
   if (tile.x < 0) {
     // rows without an adapter: the base as it is
     if (base_in == out) return;
-    for (int i = tid; i < tile.z * PIECES; i += kAdThreads) {
-      const int row = i / PIECES, c = c0 + (i % PIECES) * PER;
-      if (c >= C) continue;
-      const size_t at = (static_cast<size_t>(plan.order[tile.y + row]) * C + c) * EB;
-      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + at) =
-          base_in != nullptr ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base_in) + at)
-                             : make_uint4(0, 0, 0, 0);
+    const int vecs = (last - first) / PER;
+    for (int row = warp; row < tile.z; row += kAdThreads / 32) {
+      const size_t at = (static_cast<size_t>(s_tok[row]) * C + first) * EB;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base_in) + at);
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + at);
+      for (int i = lane; i < vecs; i += 32) dst[i] = base_in != nullptr ? src[i] : make_uint4(0, 0, 0, 0);
     }
     return;
   }
   const __nv_bfloat16* Wa = W + static_cast<size_t>(tile.x) * C * r;
-  const uint32_t sb = smem_u32(smem), su_hi = sb, su_lo = sb + S::kU, sw = sb + 2 * S::kU;
-  uint8_t* sy = smem + 2 * S::kU + S::kW;
-  // the tile of W and of the base
-  if constexpr (WT) {
-    for (int i = tid; i < kTileCols * (RP / 8); i += kAdThreads) {
-      const int c = i / (RP / 8), j = (i % (RP / 8)) * 8;
-      const bool ok = j < r && c0 + c < C;
-      cp_async16(sw + (c * S::kWRow + j) * 2, ok ? Wa + static_cast<size_t>(c0 + c) * r + j : W, ok);
+  const uint32_t sb = smem_u32(smem);
+  const int wm = (warp & 1) * 32, wn = (warp >> 1) * 64;
+  const bool mine = wm < tile.z;  // this warp has rows
+  uint8_t* sy0 = smem + PARTS * S::kU + 2 * S::kW + warp * S::kY;
+  auto load = [&](int c0, int slot) {
+    const uint32_t sw = sb + PARTS * S::kU + slot * S::kW;
+    if constexpr (WT) {
+#pragma unroll
+      for (int k = 0; k < kTileCols * (RP / 8) / kAdThreads; ++k) {
+        const int i = tid + k * kAdThreads, c = i / (RP / 8), j = (i % (RP / 8)) * 8;
+        const bool ok = j < r && c0 + c < last;
+        cp_async16(sw + (c * S::kWRow + j) * 2, ok ? Wa + static_cast<size_t>(c0 + c) * r + j : W, ok);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < RP * (kTileCols / 8) / kAdThreads; ++k) {
+        const int i = tid + k * kAdThreads, j = i / (kTileCols / 8), c = (i % (kTileCols / 8)) * 8;
+        const bool ok = j < r && c0 + c < last;
+        cp_async16(sw + (j * S::kWRow + c) * 2, ok ? Wa + static_cast<size_t>(j) * C + c0 + c : W, ok);
+      }
     }
-  } else {
-    for (int i = tid; i < RP * (kTileCols / 8); i += kAdThreads) {
-      const int j = i / (kTileCols / 8), c = (i % (kTileCols / 8)) * 8;
-      const bool ok = j < r && c0 + c < C;
-      cp_async16(sw + (j * S::kWRow + c) * 2, ok ? Wa + static_cast<size_t>(j) * C + c0 + c : W, ok);
+    if (mine && base_in != nullptr) {
+      const uint32_t sy = smem_u32(sy0 + slot * 4 * S::kY);
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k) {
+        const int i = lane + 32 * k, row = i / PIECES, c = (i % PIECES) * PER;
+        const bool ok = wm + row < tile.z && c0 + wn + c < last;
+        if (ok)
+          cp_async16(sy + row * S::kYRow + c * EB,
+                     static_cast<const uint8_t*>(base_in) + (static_cast<size_t>(s_tok[wm + row]) * C + c0 + wn + c) * EB,
+                     true);
+      }
     }
-  }
-  for (int i = tid; i < tile.z * PIECES; i += kAdThreads) {
-    const int row = i / PIECES, c = (i % PIECES) * PER;
-    const bool ok = base_in != nullptr && c0 + c < C;
-    cp_async16(smem_u32(sy + row * S::kYRow + c * EB),
-               ok ? static_cast<const uint8_t*>(base_in) +
-                        (static_cast<size_t>(plan.order[tile.y + row]) * C + c0 + c) * EB
-                  : static_cast<const void*>(W),
-               ok);
-  }
-  cp_async_commit();
+    cp_async_commit();
+  };
+  load(first, 0);
   // u of the tile's rows
   const float sc = scale[tile.x];
   for (int i = tid; i < kTileRows * (RP / 4); i += kAdThreads) {
@@ -408,73 +435,101 @@ __global__ void __launch_bounds__(kAdThreads)
       }
     }
     const float f[4] = {v.x * sc, v.y * sc, v.z * sc, v.w * sc};
-    __nv_bfloat16 hi[4], lo[4];
+    __nv_bfloat16 part[3][4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) split_bf16(f[q], hi[q], lo[q]);
-    const uint2 h2 = *reinterpret_cast<const uint2*>(hi), l2 = *reinterpret_cast<const uint2*>(lo);
-    *reinterpret_cast<uint2*>(smem + (row * S::kURow + j) * 2) = h2;
-    *reinterpret_cast<uint2*>(smem + S::kU + (row * S::kURow + j) * 2) = l2;
-    if (u_keep != nullptr && blockIdx.x == 0 && row < tile.z) {
-      const size_t at = static_cast<size_t>(tile.y + row) * RP + j;
-      *reinterpret_cast<uint2*>(u_keep + at) = h2;
-      *reinterpret_cast<uint2*>(u_keep + static_cast<size_t>(T) * RP + at) = l2;
+    for (int q = 0; q < 4; ++q) split_bf16(f[q], part[0][q], part[1][q], part[2][q]);
+#pragma unroll
+    for (int h = 0; h < 3; ++h) {
+      const uint2 v2 = *reinterpret_cast<const uint2*>(part[h]);
+      if (h < PARTS) *reinterpret_cast<uint2*>(smem + h * S::kU + (row * S::kURow + j) * 2) = v2;
+      if (u_keep != nullptr && blockIdx.y == 0 && row < tile.z)
+        *reinterpret_cast<uint2*>(u_keep + (static_cast<size_t>(h) * T + tile.y + row) * RP + j) = v2;
     }
   }
-  cp_async_wait<0>();
   __syncthreads();
-  if (warp * 16 < tile.z) {
-    float acc[kTileCols / 8][4];
+  auto u_frag = [&](uint32_t (&a)[4], int h, int m, int k) {
+    ldmatrix_x4(a, sb + h * S::kU + ((wm + 16 * m + (lane & 15)) * S::kURow + k + 8 * (lane >> 4)) * 2);
+  };
+  uint32_t ua[S::kRegs ? PARTS : 1][2][S::kRegs ? RP / 16 : 1][4];
+  if constexpr (S::kRegs) {
 #pragma unroll
-    for (int n = 0; n < kTileCols / 8; ++n)
+    for (int h = 0; h < PARTS; ++h)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int k = 0; k < RP; k += 16) {
-      uint32_t ah[4], al[4];
-      const uint32_t at = ((warp * 16 + (lane & 15)) * S::kURow + k + 8 * (lane >> 4)) * 2;
-      ldmatrix_x4(ah, su_hi + at);
-      ldmatrix_x4(al, su_lo + at);
+        for (int k = 0; k < RP / 16; ++k) u_frag(ua[h][m][k], h, m, 16 * k);
+  }
+  int slot = 0;
+  for (int c0 = first; c0 < last; c0 += kTileCols, slot ^= 1) {
+    cp_async_wait<0>();
+    __syncthreads();  // this step's tiles are here, the last step's have been read
+    if (c0 + kTileCols < last) load(c0 + kTileCols, slot ^ 1);
+    if (!mine) continue;
+    const uint32_t sw = sb + PARTS * S::kU + slot * S::kW;
+    float acc[2][8][4];
 #pragma unroll
-      for (int n = 0; n < kTileCols; n += 16) {
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < RP / 16; ++k) {
+      uint32_t a[S::kRegs ? 1 : PARTS][2][4];
+      if constexpr (!S::kRegs) {
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) u_frag(a[h][m], h, m, 16 * k);
+      }
+#pragma unroll
+      for (int n = 0; n < 8; n += 2) {
         uint32_t b[4];
         if constexpr (WT)
-          ldmatrix_x4(b, sw + ((n + (lane & 7) + 8 * (lane >> 4)) * S::kWRow + k + 8 * ((lane >> 3) & 1)) * 2);
+          ldmatrix_x4(b, sw + ((wn + 8 * n + (lane & 7) + 8 * (lane >> 4)) * S::kWRow + 16 * k + 8 * ((lane >> 3) & 1)) * 2);
         else
-          ldmatrix_x4_trans(b, sw + ((k + (lane & 15)) * S::kWRow + n + 8 * (lane >> 4)) * 2);
-        mma_bf16(acc[n / 8], al, b[0], b[1]);
-        mma_bf16(acc[n / 8 + 1], al, b[2], b[3]);
-        mma_bf16(acc[n / 8], ah, b[0], b[1]);
-        mma_bf16(acc[n / 8 + 1], ah, b[2], b[3]);
+          ldmatrix_x4_trans(b, sw + ((16 * k + (lane & 15)) * S::kWRow + wn + 8 * n + 8 * (lane >> 4)) * 2);
+#pragma unroll
+        for (int h = PARTS - 1; h >= 0; --h)  // the small parts first
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint32_t(&f)[4] = S::kRegs ? ua[S::kRegs ? h : 0][m][S::kRegs ? k : 0] : a[S::kRegs ? 0 : h][m];
+            mma_bf16(acc[m][n], f, b[0], b[1]);
+            mma_bf16(acc[m][n + 1], f, b[2], b[3]);
+          }
       }
     }
-    // add the base in place (each element by the thread that holds its sum)
+    // add the base in shared memory (each element by the thread that holds its sum)
+    uint8_t* sy = sy0 + slot * 4 * S::kY;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = warp * 16 + (lane >> 2) + 8 * h;
-      if (row < tile.z) {
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int n = 0; n < kTileCols / 8; ++n) {
-          uint8_t* q = sy + row * S::kYRow + (8 * n + 2 * (lane & 3)) * EB;
-          if constexpr (F32) {
-            float2 y = *reinterpret_cast<float2*>(q);
-            y.x += acc[n][2 * h];
-            y.y += acc[n][2 * h + 1];
-            *reinterpret_cast<float2*>(q) = y;
-          } else {
-            const uint32_t y = *reinterpret_cast<uint32_t*>(q);
-            *reinterpret_cast<uint32_t*>(q) = pack_bf16x2(bf16_lo(y) + acc[n][2 * h], bf16_hi(y) + acc[n][2 * h + 1]);
+      for (int h = 0; h < 2; ++h) {
+        const int row = 16 * m + (lane >> 2) + 8 * h;
+        if (wm + row < tile.z) {
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            uint8_t* q = sy + row * S::kYRow + (8 * n + 2 * (lane & 3)) * EB;
+            const float x = acc[m][n][2 * h], y = acc[m][n][2 * h + 1];
+            if constexpr (F32) {
+              float2 v = base_in != nullptr ? *reinterpret_cast<float2*>(q) : make_float2(0.f, 0.f);
+              *reinterpret_cast<float2*>(q) = make_float2(v.x + x, v.y + y);
+            } else {
+              const uint32_t v = base_in != nullptr ? *reinterpret_cast<uint32_t*>(q) : 0u;
+              *reinterpret_cast<uint32_t*>(q) = pack_bf16x2(bf16_lo(v) + x, bf16_hi(v) + y);
+            }
           }
         }
       }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k) {
+      const int i = lane + 32 * k, row = i / PIECES, c = (i % PIECES) * PER;
+      if (wm + row < tile.z && c0 + wn + c < last)
+        __stcs(reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) +
+                                        (static_cast<size_t>(s_tok[wm + row]) * C + c0 + wn + c) * EB),
+               *reinterpret_cast<const uint4*>(sy + row * S::kYRow + c * EB));
     }
-  }
-  __syncthreads();
-  for (int i = tid; i < tile.z * PIECES; i += kAdThreads) {
-    const int row = i / PIECES, c = (i % PIECES) * PER;
-    if (c0 + c < C)
-      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) +
-                                (static_cast<size_t>(plan.order[tile.y + row]) * C + c0 + c) * EB) =
-          *reinterpret_cast<const uint4*>(sy + row * S::kYRow + c * EB);
   }
 }
 
@@ -485,12 +540,12 @@ struct WgradSmem {
   static constexpr int kX = kTileRows * kXRow * 2;
   static constexpr int kVRow = RP + 8;
   static constexpr int kV = kTileRows * kVRow * 2;
-  static constexpr int kStage = kX + 2 * kV;
+  static constexpr int kStage = kX + 3 * kV;
   static constexpr int kTotal = kStages * kStage;
 };
 
 // G_a[c][j] = sum over the rows t of adapter a of X[t][c] V[position][j], V as
-// its two bf16 parts. OUT_T: G_a is stored [r][C] (dB), else [C][r] (dA). The
+// its three bf16 parts. OUT_T: G_a is stored [r][C] (dB), else [C][r] (dA). The
 // rows of an adapter come in 64s, each joined in ordinary fp32 adds.
 template <int RP, bool OUT_T>
 __global__ void __launch_bounds__(kAdThreads)
@@ -520,8 +575,8 @@ __global__ void __launch_bounds__(kAdThreads)
       const bool ok = row < n;
       const __nv_bfloat16* p = V + (ok ? static_cast<size_t>(q0 + row) * RP + j : 0);
       const uint32_t d = sv + (row * S::kVRow + j) * 2;
-      cp_async16(d, p, ok);
-      cp_async16(d + S::kV, p + static_cast<size_t>(T) * RP, ok);
+#pragma unroll
+      for (int h = 0; h < 3; ++h) cp_async16(d + h * S::kV, p + static_cast<size_t>(h) * T * RP, ok);
     }
   };
   float acc[RP / 8][4];
@@ -552,14 +607,14 @@ __global__ void __launch_bounds__(kAdThreads)
       ldmatrix_x4_trans(a, sx + ((k + (lane & 7) + 8 * (lane >> 4)) * S::kXRow + warp * 16 + 8 * ((lane >> 3) & 1)) * 2);
 #pragma unroll
       for (int n = 0; n < RP; n += 16) {
-        uint32_t bh[4], bl[4];
         const uint32_t at = sv + ((k + (lane & 15)) * S::kVRow + n + 8 * (lane >> 4)) * 2;
-        ldmatrix_x4_trans(bh, at);
-        ldmatrix_x4_trans(bl, at + S::kV);
-        mma_bf16(part[n / 8], a, bl[0], bl[1]);
-        mma_bf16(part[n / 8 + 1], a, bl[2], bl[3]);
-        mma_bf16(part[n / 8], a, bh[0], bh[1]);
-        mma_bf16(part[n / 8 + 1], a, bh[2], bh[3]);
+#pragma unroll
+        for (int h = 2; h >= 0; --h) {
+          uint32_t bq[4];
+          ldmatrix_x4_trans(bq, at + h * S::kV);
+          mma_bf16(part[n / 8], a, bq[0], bq[1]);
+          mma_bf16(part[n / 8 + 1], a, bq[2], bq[3]);
+        }
       }
     }
 #pragma unroll
@@ -615,22 +670,30 @@ static AdapterWs adapter_ws(const moe_adapter_config& c, bool training) {
   int s = shrink_splits(c, c.K);
   if (training) s = std::max(s, shrink_splits(c, c.N));
   w.parts = take(4 * T * rp * s);
-  if (training) w.du = take(4 * T * rp);
+  if (training) w.du = take(6 * T * rp);
   w.total = o;
   return w;
 }
 
-template <class K>
-static cudaError_t allow_smem(K kernel, int bytes) {
-  return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)
-                           : cudaSuccess;
+// the shared memory of a kernel, allowed once for each device
+template <auto Kernel>
+static cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || bytes <= 48 * 1024) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  const cudaError_t a = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (a == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+  return a;
 }
 
 template <int RP, bool WT>
 static cudaError_t launch_shrink(const moe_adapter_config& c, int C, const void* X, const void* W, const PlanView& pv,
                                  int max_tiles, int splits, float* parts, cudaStream_t s) {
   constexpr int sm = ShrinkSmem<RP, WT>::kTotal;
-  const cudaError_t e = allow_smem(adapter_shrink_kernel<RP, WT>, sm);
+  const cudaError_t e = allow_smem<adapter_shrink_kernel<RP, WT>>(sm);
   if (e != cudaSuccess) return e;
   adapter_shrink_kernel<RP, WT><<<dim3(max_tiles, splits), kAdThreads, sm, s>>>(
       static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(W), pv, c.T, C, c.r, splits, parts);
@@ -641,18 +704,22 @@ static cudaError_t launch_expand(const moe_adapter_config& c, int C, const float
                                  const float* scale, const void* W, const PlanView& pv, int max_tiles,
                                  const void* base, void* out, void* keep, cudaStream_t s) {
   constexpr int sm = ExpandSmem<RP, WT, F32>::kTotal;
-  const cudaError_t e = allow_smem(adapter_expand_kernel<RP, WT, F32>, sm);
+  const cudaError_t e = allow_smem<adapter_expand_kernel<RP, WT, F32>>(sm);
   if (e != cudaSuccess) return e;
-  adapter_expand_kernel<RP, WT, F32><<<dim3((C + kTileCols - 1) / kTileCols, max_tiles), kAdThreads, sm, s>>>(
-      parts, splits, scale, static_cast<const __nv_bfloat16*>(W), pv, c.T, C, c.r, base, out,
-      static_cast<__nv_bfloat16*>(keep));
-  return cudaGetLastError();
+  // about six blocks for each SM (two or three run at a time, in even waves)
+  const int cols = (C + kTileCols - 1) / kTileCols;
+  const int tiles = c.T / kTileRows + std::min(c.T, c.L);
+  const int ranges = std::max(1, std::min(cols, (6 * kAdSMs + tiles - 1) / tiles));
+  const int steps = (cols + ranges - 1) / ranges;
+  return launch_chained(adapter_expand_kernel<RP, WT, F32>, dim3(max_tiles, (cols + steps - 1) / steps), kAdThreads,
+                        sm, s, parts, splits, scale, static_cast<const __nv_bfloat16*>(W), pv, c.T, C, c.r, steps,
+                        base, out, static_cast<__nv_bfloat16*>(keep));
 }
 template <int RP, bool OUT_T>
 static cudaError_t launch_wgrad(const moe_adapter_config& c, int C, const void* X, const void* V, const PlanView& pv,
                                 float* G, cudaStream_t s) {
   constexpr int sm = WgradSmem<RP>::kTotal;
-  const cudaError_t e = allow_smem(adapter_wgrad_kernel<RP, OUT_T>, sm);
+  const cudaError_t e = allow_smem<adapter_wgrad_kernel<RP, OUT_T>>(sm);
   if (e != cudaSuccess) return e;
   adapter_wgrad_kernel<RP, OUT_T><<<dim3((C + kGradCols - 1) / kGradCols, c.L), kAdThreads, sm, s>>>(
       static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(V), pv, c.T, C, c.r, G);
@@ -688,7 +755,7 @@ size_t moe_adapter_workspace_bytes(const moe_adapter_config* cfg, int training) 
   return check_adapter(cfg) != MOE_OK ? 0 : adapter_ws(*cfg, training != 0).total;
 }
 size_t moe_adapter_saved_bytes(const moe_adapter_config* cfg) {
-  return check_adapter(cfg) != MOE_OK ? 0 : 4 * static_cast<size_t>(cfg->T) * padded_rank(cfg->r);
+  return check_adapter(cfg) != MOE_OK ? 0 : 6 * static_cast<size_t>(cfg->T) * padded_rank(cfg->r);
 }
 
 int moe_adapter_plan(const moe_adapter_config* cfg, const int32_t* adapter_idx, void* plan, size_t plan_bytes,

@@ -43,12 +43,14 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// v = hi + lo with hi and lo in bf16: 16 bits of v (a difference of at most
-// 2^-18 v). lo is 0 where hi is not finite, so that an infinity stays one.
-__device__ __forceinline__ void split_bf16(float v, __nv_bfloat16& hi, __nv_bfloat16& lo) {
-  hi = __float2bfloat16_rn(v);
-  const float h = __bfloat162float(hi);
-  lo = __float2bfloat16_rn(isfinite(h) ? v - h : 0.0f);
+// v = a + b + c in three bf16 parts: a alone is off by 2^-8 v at most, a + b by
+// 2^-17 v, all three by 2^-25 v. b and c are 0 where a is not finite, so that an
+// infinity stays one.
+__device__ __forceinline__ void split_bf16(float v, __nv_bfloat16& a, __nv_bfloat16& b, __nv_bfloat16& c) {
+  a = __float2bfloat16_rn(v);
+  const float fa = __bfloat162float(a), rest = isfinite(fa) ? v - fa : 0.0f;
+  b = __float2bfloat16_rn(rest);
+  c = __float2bfloat16_rn(rest - __bfloat162float(b));
 }
 
 }  // namespace moe
