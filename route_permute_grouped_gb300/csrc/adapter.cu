@@ -7,8 +7,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "host_util.h"
-#include "mma.cuh"
+#include "adapter_tc.cuh"
 
 namespace moe {
 
@@ -21,8 +20,8 @@ constexpr int kAdSMs = 152;
 // the plan
 // ---------------------------------------------------------------------------
 struct PlanLayout {
-  size_t hdr, seg, tiles, order, hist, total;
-  int max_tiles, chunks;
+  size_t hdr, seg, tiles, big, order, hist, total;
+  int max_tiles, max_big, chunks;
 };
 static PlanLayout plan_layout(const moe_adapter_config& c) {
   PlanLayout p{};
@@ -33,57 +32,46 @@ static PlanLayout plan_layout(const moe_adapter_config& c) {
     return at;
   };
   p.max_tiles = c.T / kTileRows + std::min(c.T, c.L + 1);
+  p.max_big = c.T / 128 + std::min(c.T, c.L + 1);
   p.chunks = (c.T + kPlanThreads - 1) / kPlanThreads;
   p.hdr = take(64);
   p.seg = take(4 * (static_cast<size_t>(c.L) + 2));
   p.tiles = take(16 * static_cast<size_t>(p.max_tiles));
+  p.big = take(16 * static_cast<size_t>(p.max_big));
   p.order = take(4 * static_cast<size_t>(c.T));
-  p.hist = take(4 * static_cast<size_t>(p.chunks) * (c.L + 1));
+  p.hist = take(4 * static_cast<size_t>(p.chunks) * (c.L + 2));
   p.total = o;
   return p;
-}
-struct PlanView {
-  const int4* hdr;       // {number of tiles, T, L, kPlanMagic}
-  const int32_t* seg;    // [L + 2]: first position of each adapter, then of the rows without one, then T
-  const int4* tiles;     // {adapter or -1, first position, rows, 0}
-  const int32_t* order;  // [T]: token of each position
-  int T, L;
-  DevStatus* st;
-};
-constexpr int kPlanMagic = 0x706c616e;
-// the number of tiles; 0, and a device error, for a plan of another batch size
-// or number of adapters or a buffer that holds none
-__device__ __forceinline__ int plan_tiles(const PlanView& p) {
-  const int4 h = __ldg(p.hdr);
-  if (h.y == p.T && h.z == p.L && h.w == kPlanMagic) return h.x;
-  set_status(p.st, MOE_ERR_DEVICE_INDEX, 61);
-  return 0;
 }
 static PlanView plan_view(const moe_adapter_config& c, const void* plan, const PlanLayout& p, void* ws) {
   const uint8_t* b = static_cast<const uint8_t*>(plan);
   return {reinterpret_cast<const int4*>(b + p.hdr), reinterpret_cast<const int32_t*>(b + p.seg),
-          reinterpret_cast<const int4*>(b + p.tiles), reinterpret_cast<const int32_t*>(b + p.order), c.T, c.L,
+          reinterpret_cast<const int4*>(b + p.tiles), reinterpret_cast<const int4*>(b + p.big),
+          reinterpret_cast<const int32_t*>(b + p.order), c.T, c.L,
           static_cast<DevStatus*>(ws)};
 }
 
-__device__ __forceinline__ int plan_key(int a, int L, DevStatus* st) {
-  if (a >= L) {
-    set_status(st, MOE_ERR_DEVICE_INDEX, 60);
-    return L;
-  }
-  return a < 0 ? L : a;
+// The key of a row: its adapter, or L for none. An index >= L counts as none and
+// is reported through `bad`.
+__device__ __forceinline__ int plan_key(int a, int L, bool& bad) {
+  bad = a >= L;
+  return a < 0 || bad ? L : a;
 }
 
-// counts of each adapter (key L: rows without one) in a chunk of 1024 rows
+// counts of each key in a chunk of 1024 rows, and whether it has a bad index
 __global__ void __launch_bounds__(kPlanThreads) plan_hist_kernel(const int32_t* __restrict__ idx, int T, int L,
-                                                                 int32_t* __restrict__ hist, DevStatus* st) {
+                                                                 int32_t* __restrict__ hist) {
   __shared__ int s_h[kMaxAdapters + 1];
   for (int i = threadIdx.x; i <= L; i += kPlanThreads) s_h[i] = 0;
   __syncthreads();
   const int t = blockIdx.x * kPlanThreads + threadIdx.x;
-  if (t < T) atomicAdd(&s_h[plan_key(idx[t], L, st)], 1);
-  __syncthreads();
-  for (int i = threadIdx.x; i <= L; i += kPlanThreads) hist[static_cast<size_t>(blockIdx.x) * (L + 1) + i] = s_h[i];
+  bool bad = false;
+  if (t < T) atomicAdd(&s_h[plan_key(idx[t], L, bad)], 1);
+  bad = __syncthreads_or(bad);
+  int32_t* row = hist + static_cast<size_t>(blockIdx.x) * (L + 2);
+  for (int i = threadIdx.x; i <= L; i += kPlanThreads) row[i] = s_h[i];
+  if (threadIdx.x == 0) row[L + 1] = bad;
+  chain_release();
 }
 
 // exclusive scan of two values per key over s_a and s_b ([L + 1], in place) by
@@ -135,13 +123,14 @@ __device__ __forceinline__ void scan_keys(int* s_a, int* s_b, int n, int* s_w) {
 }
 
 // Positions of a chunk's rows (rows of an adapter stay in token order: a
-// stable counting sort), and from the first chunk the segments and tiles.
+// stable counting sort), and from the first chunk the segments, the tiles of both
+// sizes and the status.
 __global__ void __launch_bounds__(kPlanThreads)
     plan_place_kernel(const int32_t* __restrict__ idx, int T, int L, int chunks, const int32_t* __restrict__ hist,
                       int4* __restrict__ hdr, int32_t* __restrict__ seg, int4* __restrict__ tiles, int max_tiles,
-                      int32_t* __restrict__ order, DevStatus* st) {
+                      int4* __restrict__ big, int max_big, int32_t* __restrict__ order, DevStatus* st) {
   __shared__ int s_first[kMaxAdapters + 1];   // first position of each key
-  __shared__ int s_tile[kMaxAdapters + 1];    // first tile of each key
+  __shared__ int s_tile[kMaxAdapters + 1];    // first tile of each key: 64 rows in the low half, 128 in the high
   __shared__ int s_before[kMaxAdapters + 1];  // rows of each key in earlier chunks
   __shared__ __align__(4) uint8_t s_warp[32][kMaxAdapters + 1];
   __shared__ int s_w[64];
@@ -150,7 +139,9 @@ __global__ void __launch_bounds__(kPlanThreads)
   for (int i = tid; i < keys; i += kPlanThreads) s_first[i] = s_before[i] = 0;
   __syncthreads();
   const int t = me * kPlanThreads + tid;
-  const int key = t < T ? plan_key(idx[t], L, st) : -1;
+  bool bad = false;
+  const int key = t < T ? plan_key(idx[t], L, bad) : -1;
+  chain_wait();
   const unsigned peers = __match_any_sync(0xffffffffu, key);
   const int rank = __popc(peers & ((1u << lane) - 1u));
   if (key >= 0 && rank == 0) s_warp[warp][key] = static_cast<uint8_t>(__popc(peers));
@@ -160,7 +151,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     for (int i = tid; i < keys; i += kPlanThreads) {
       int n = 0, before = 0;
       for (int c = 0; c < chunks; ++c) {
-        const int h = hist[static_cast<size_t>(c) * keys + i];
+        const int h = hist[static_cast<size_t>(c) * (keys + 1) + i];
         before += c < me ? h : 0;
         n += h;
       }
@@ -169,7 +160,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
   }
   __syncthreads();
-  for (int i = tid; i < keys; i += kPlanThreads) s_tile[i] = (s_first[i] + kTileRows - 1) / kTileRows;
+  for (int i = tid; i < keys; i += kPlanThreads)
+    s_tile[i] = (s_first[i] + kTileRows - 1) / kTileRows | ((s_first[i] + 127) / 128) << 16;
   __syncthreads();
   scan_keys(s_first, s_tile, keys, s_w);
   __syncthreads();
@@ -181,17 +173,24 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (me == 0) {
     for (int i = tid; i < keys; i += kPlanThreads) {
       seg[i] = s_first[i];
-      const int n = (i < L ? s_first[i + 1] : T) - s_first[i];
-      const int nt = (n + kTileRows - 1) / kTileRows;
+      const int n = (i < L ? s_first[i + 1] : T) - s_first[i], a = i < L ? i : -1;
+      const int nt = (n + kTileRows - 1) / kTileRows, t0 = s_tile[i] & 0xffff;
+      const int nb = (n + 127) / 128, b0 = static_cast<int>(static_cast<uint32_t>(s_tile[i]) >> 16);
       for (int j = 0; j < nt; ++j)
-        if (s_tile[i] + j < max_tiles)
-          tiles[s_tile[i] + j] = make_int4(i < L ? i : -1, s_first[i] + j * kTileRows,
-                                           min(kTileRows, n - j * kTileRows), 0);
+        if (t0 + j < max_tiles)
+          tiles[t0 + j] = make_int4(a, s_first[i] + j * kTileRows, min(kTileRows, n - j * kTileRows), 0);
+      for (int j = 0; j < nb; ++j)
+        if (b0 + j < max_big) big[b0 + j] = make_int4(a, s_first[i] + j * 128, min(128, n - j * 128), 0);
       if (i == L) {
         seg[L + 1] = T;
-        *hdr = make_int4(min(s_tile[L] + nt, max_tiles), T, L, kPlanMagic);
+        hdr[0] = make_int4(min(t0 + nt, max_tiles), T, L, kPlanMagic);
+        hdr[1] = make_int4(min(b0 + nb, max_big), 0, 0, 0);
       }
     }
+    if (hist != nullptr)
+      for (int c = tid; c < chunks; c += kPlanThreads) bad |= hist[static_cast<size_t>(c) * (keys + 1) + L + 1] != 0;
+    bad = __syncthreads_or(bad);
+    if (tid == 0) st->status = bad ? MOE_ERR_DEVICE_INDEX : MOE_OK;
   }
 }
 
@@ -223,6 +222,7 @@ __global__ void __launch_bounds__(kAdThreads)
                           int T, int C, int r, int splits, float* __restrict__ parts) {
   extern __shared__ __align__(16) uint8_t smem[];
   using S = ShrinkSmem<RP, WT>;
+  chain_wait();
   if (static_cast<int>(blockIdx.x) >= plan_tiles(plan)) return;
   const int4 tile = plan.tiles[blockIdx.x];
   if (tile.x < 0) return;
@@ -533,107 +533,6 @@ __global__ void __launch_bounds__(kAdThreads, RP <= 64 && !F32 ? 3 : 2)
   }
 }
 
-constexpr int kGradCols = 64;
-template <int RP>
-struct WgradSmem {
-  static constexpr int kXRow = kGradCols + 8;
-  static constexpr int kX = kTileRows * kXRow * 2;
-  static constexpr int kVRow = RP + 8;
-  static constexpr int kV = kTileRows * kVRow * 2;
-  static constexpr int kStage = kX + 3 * kV;
-  static constexpr int kTotal = kStages * kStage;
-};
-
-// G_a[c][j] = sum over the rows t of adapter a of X[t][c] V[position][j], V as
-// its three bf16 parts. OUT_T: G_a is stored [r][C] (dB), else [C][r] (dA). The
-// rows of an adapter come in 64s, each joined in ordinary fp32 adds.
-template <int RP, bool OUT_T>
-__global__ void __launch_bounds__(kAdThreads)
-    adapter_wgrad_kernel(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ V, PlanView plan, int T,
-                         int C, int r, float* __restrict__ G) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  using S = WgradSmem<RP>;
-  const int a_id = blockIdx.y, c0 = blockIdx.x * kGradCols;
-  const bool any = plan_tiles(plan) > 0;
-  const int p0 = any ? plan.seg[a_id] : 0, p1 = any ? plan.seg[a_id + 1] : 0;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t base = smem_u32(smem);
-  const int blocks = (p1 - p0 + kTileRows - 1) / kTileRows;
-  auto load = [&](int b, int slot) {
-    const uint32_t sx = base + slot * S::kStage, sv = sx + S::kX;
-    const int q0 = p0 + b * kTileRows, n = min(kTileRows, p1 - q0);
-    const int c = c0 + (tid & 7) * 8;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = (tid >> 3) + 16 * i;
-      const bool ok = row < n && c < C;
-      cp_async16(sx + (row * S::kXRow + (tid & 7) * 8) * 2,
-                 ok ? X + static_cast<size_t>(plan.order[q0 + row]) * C + c : X, ok);
-    }
-    for (int i = tid; i < kTileRows * (RP / 8); i += kAdThreads) {
-      const int row = i / (RP / 8), j = (i % (RP / 8)) * 8;
-      const bool ok = row < n;
-      const __nv_bfloat16* p = V + (ok ? static_cast<size_t>(q0 + row) * RP + j : 0);
-      const uint32_t d = sv + (row * S::kVRow + j) * 2;
-#pragma unroll
-      for (int h = 0; h < 3; ++h) cp_async16(d + h * S::kV, p + static_cast<size_t>(h) * T * RP, ok);
-    }
-  };
-  float acc[RP / 8][4];
-#pragma unroll
-  for (int n = 0; n < RP / 8; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
-    if (s < blocks) load(s, s);
-    cp_async_commit();
-  }
-  int slot = 0;
-  for (int b = 0; b < blocks; ++b) {
-    cp_async_wait<kStages - 2>();
-    __syncthreads();
-    if (b + kStages - 1 < blocks) load(b + kStages - 1, (slot + kStages - 1) % kStages);
-    cp_async_commit();
-    const uint32_t sx = base + slot * S::kStage, sv = sx + S::kX;
-    float part[RP / 8][4];
-#pragma unroll
-    for (int n = 0; n < RP / 8; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) part[n][i] = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kTileRows; k += 16) {
-      uint32_t a[4];
-      ldmatrix_x4_trans(a, sx + ((k + (lane & 7) + 8 * (lane >> 4)) * S::kXRow + warp * 16 + 8 * ((lane >> 3) & 1)) * 2);
-#pragma unroll
-      for (int n = 0; n < RP; n += 16) {
-        const uint32_t at = sv + ((k + (lane & 15)) * S::kVRow + n + 8 * (lane >> 4)) * 2;
-#pragma unroll
-        for (int h = 2; h >= 0; --h) {
-          uint32_t bq[4];
-          ldmatrix_x4_trans(bq, at + h * S::kV);
-          mma_bf16(part[n / 8], a, bq[0], bq[1]);
-          mma_bf16(part[n / 8 + 1], a, bq[2], bq[3]);
-        }
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < RP / 8; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] += part[n][i];
-    slot = (slot + 1) % kStages;
-  }
-  cp_async_wait<0>();
-  float* Ga = G + static_cast<size_t>(a_id) * C * r;
-#pragma unroll
-  for (int n = 0; n < RP / 8; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = c0 + warp * 16 + (lane >> 2) + 8 * (i >> 1), j = 8 * n + 2 * (lane & 3) + (i & 1);
-      if (c < C && j < r) Ga[OUT_T ? static_cast<size_t>(j) * C + c : static_cast<size_t>(c) * r + j] = acc[n][i];
-    }
-}
-
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
@@ -655,8 +554,30 @@ static int shrink_splits(const moe_adapter_config& c, int C) {
   return std::max(1, std::min({4 * kAdSMs / tiles, nkb, 32}));
 }
 
+// Batches from 512 rows on take the tensor memory kernels; smaller ones, whose
+// adapters have a few rows each, tiles of 64 on mma.sync.
+constexpr int kTcRows = 512;
+static int big_tiles(const moe_adapter_config& c) { return c.T / 128 + std::min(c.T, c.L); }
+// two CTAs for each SM
+static int shrink_splits_tc(const moe_adapter_config& c, int C) {
+  const int nkb = (C + 63) / 64;
+  return std::max(1, std::min({2 * kAdSMs / big_tiles(c), nkb, 32}));
+}
+// Runs of rows of the weight gradients: together with the column tiles about one
+// block for each SM
+static RowRuns wgrad_runs(const moe_adapter_config& c, int C, int* col_tiles, size_t* partial_floats) {
+  const int rp = padded_rank(c.r), cols = rp <= 64 ? 256 : 128;
+  *col_tiles = (C + cols - 1) / cols;
+  const int want = std::max(1, kAdSMs / *col_tiles);
+  RowRuns run;
+  run.rows = ((c.T + want - 1) / want + 63) / 64 * 64;
+  run.runs = (c.T + run.rows - 1) / run.rows;
+  *partial_floats = 2 * static_cast<size_t>(run.runs) * *col_tiles * cols * rp;
+  return run;
+}
+
 struct AdapterWs {
-  size_t parts, du, total;
+  size_t parts, du, partial, total;
 };
 static AdapterWs adapter_ws(const moe_adapter_config& c, bool training) {
   AdapterWs w{};
@@ -667,10 +588,18 @@ static AdapterWs adapter_ws(const moe_adapter_config& c, bool training) {
     return at;
   };
   const size_t rp = padded_rank(c.r), T = c.T;
-  int s = shrink_splits(c, c.K);
-  if (training) s = std::max(s, shrink_splits(c, c.N));
+  auto splits = [&](int C) { return c.T >= kTcRows ? shrink_splits_tc(c, C) : shrink_splits(c, C); };
+  int s = splits(c.K);
+  if (training) s = std::max(s, splits(c.N));
   w.parts = take(4 * T * rp * s);
-  if (training) w.du = take(6 * T * rp);
+  if (training) {
+    w.du = take(6 * T * rp);
+    int tiles;
+    size_t a, b;
+    wgrad_runs(c, c.K, &tiles, &a);
+    wgrad_runs(c, c.N, &tiles, &b);
+    w.partial = take(4 * std::max(a, b));
+  }
   w.total = o;
   return w;
 }
@@ -689,20 +618,46 @@ static cudaError_t allow_smem(int bytes) {
   return a;
 }
 
+// parts of X W: the number of splits it left in *splits
 template <int RP, bool WT>
 static cudaError_t launch_shrink(const moe_adapter_config& c, int C, const void* X, const void* W, const PlanView& pv,
-                                 int max_tiles, int splits, float* parts, cudaStream_t s) {
+                                 const PlanLayout& P, float* parts, int* splits, cudaStream_t s) {
+  const auto* x = static_cast<const __nv_bfloat16*>(X);
+  const auto* w = static_cast<const __nv_bfloat16*>(W);
+  if (c.T >= kTcRows) {
+    constexpr int sm = TcShrink<RP, WT>::kTotal;
+    const cudaError_t e = allow_smem<adapter_shrink_tc<RP, WT>>(sm);
+    if (e != cudaSuccess) return e;
+    *splits = shrink_splits_tc(c, C);
+    return launch_chained(adapter_shrink_tc<RP, WT>, dim3(P.max_big, *splits), kTcThreads, sm, s, x, w, pv, c.T, C, c.r,
+                          *splits, parts, static_cast<uint64_t>(wait_limit_ns()));
+  }
   constexpr int sm = ShrinkSmem<RP, WT>::kTotal;
   const cudaError_t e = allow_smem<adapter_shrink_kernel<RP, WT>>(sm);
   if (e != cudaSuccess) return e;
-  adapter_shrink_kernel<RP, WT><<<dim3(max_tiles, splits), kAdThreads, sm, s>>>(
-      static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(W), pv, c.T, C, c.r, splits, parts);
-  return cudaGetLastError();
+  *splits = shrink_splits(c, C);
+  return launch_chained(adapter_shrink_kernel<RP, WT>, dim3(P.max_tiles, *splits), kAdThreads, sm, s, x, w, pv, c.T, C,
+                        c.r, *splits, parts);
 }
+
 template <int RP, bool WT, bool F32>
 static cudaError_t launch_expand(const moe_adapter_config& c, int C, const float* parts, int splits,
-                                 const float* scale, const void* W, const PlanView& pv, int max_tiles,
+                                 const float* scale, const void* W, const PlanView& pv, const PlanLayout& P,
                                  const void* base, void* out, void* keep, cudaStream_t s) {
+  const auto* w = static_cast<const __nv_bfloat16*>(W);
+  auto* k = static_cast<__nv_bfloat16*>(keep);
+  if (c.T >= kTcRows) {
+    using S = TcExpand<RP, WT, F32>;
+    const cudaError_t e = allow_smem<adapter_expand_tc<RP, WT, F32>>(S::kTotal);
+    if (e != cudaSuccess) return e;
+    // about one block for each SM, more only where there are more tiles
+    const int cols = (C + S::NC - 1) / S::NC;
+    const int ranges = std::max(1, std::min(cols, (kAdSMs + big_tiles(c) / 2) / big_tiles(c)));
+    const int steps = (cols + ranges - 1) / ranges;
+    return launch_chained(adapter_expand_tc<RP, WT, F32>, dim3(P.max_big, (cols + steps - 1) / steps), kTcThreads,
+                          S::kTotal, s, parts, splits, scale, w, pv, c.T, C, c.r, steps, base, out, k,
+                          static_cast<uint64_t>(wait_limit_ns()));
+  }
   constexpr int sm = ExpandSmem<RP, WT, F32>::kTotal;
   const cudaError_t e = allow_smem<adapter_expand_kernel<RP, WT, F32>>(sm);
   if (e != cudaSuccess) return e;
@@ -711,19 +666,26 @@ static cudaError_t launch_expand(const moe_adapter_config& c, int C, const float
   const int tiles = c.T / kTileRows + std::min(c.T, c.L);
   const int ranges = std::max(1, std::min(cols, (6 * kAdSMs + tiles - 1) / tiles));
   const int steps = (cols + ranges - 1) / ranges;
-  return launch_chained(adapter_expand_kernel<RP, WT, F32>, dim3(max_tiles, (cols + steps - 1) / steps), kAdThreads,
-                        sm, s, parts, splits, scale, static_cast<const __nv_bfloat16*>(W), pv, c.T, C, c.r, steps,
-                        base, out, static_cast<__nv_bfloat16*>(keep));
+  return launch_chained(adapter_expand_kernel<RP, WT, F32>, dim3(P.max_tiles, (cols + steps - 1) / steps), kAdThreads,
+                        sm, s, parts, splits, scale, w, pv, c.T, C, c.r, steps, base, out, k);
 }
+
 template <int RP, bool OUT_T>
 static cudaError_t launch_wgrad(const moe_adapter_config& c, int C, const void* X, const void* V, const PlanView& pv,
-                                float* G, cudaStream_t s) {
-  constexpr int sm = WgradSmem<RP>::kTotal;
-  const cudaError_t e = allow_smem<adapter_wgrad_kernel<RP, OUT_T>>(sm);
+                                float* G, float* partial, cudaStream_t s) {
+  constexpr int sm = TcWgrad<RP>::kTotal;
+  cudaError_t e = allow_smem<adapter_wgrad_tc<RP, OUT_T>>(sm);
   if (e != cudaSuccess) return e;
-  adapter_wgrad_kernel<RP, OUT_T><<<dim3((C + kGradCols - 1) / kGradCols, c.L), kAdThreads, sm, s>>>(
-      static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(V), pv, c.T, C, c.r, G);
-  return cudaGetLastError();
+  int col_tiles;
+  size_t floats;
+  const RowRuns run = wgrad_runs(c, C, &col_tiles, &floats);
+  e = launch_chained(adapter_wgrad_tc<RP, OUT_T>, dim3(col_tiles, run.runs), kTcThreads, sm, s,
+                     static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(V), pv, c.T, C, c.r, run,
+                     G, partial, static_cast<uint64_t>(wait_limit_ns()));
+  if (e != cudaSuccess) return e;
+  const int blocks = std::max(1, std::min(64, C * c.r / 2048));
+  return launch_chained(adapter_wgrad_join<RP, OUT_T>, dim3(blocks, c.L), 256, 0, s, pv, C, c.r, run, col_tiles, G,
+                        static_cast<const float*>(partial));
 }
 
 static bool any_misaligned(std::initializer_list<const void*> ps) {
@@ -772,15 +734,26 @@ int moe_adapter_plan(const moe_adapter_config* cfg, const int32_t* adapter_idx, 
   DevStatus* ds = reinterpret_cast<DevStatus*>(b);
   int32_t* hist = reinterpret_cast<int32_t*>(b + L.hist);
   if (L.chunks > 1) {
-    plan_hist_kernel<<<L.chunks, kPlanThreads, 0, s>>>(adapter_idx, c.T, c.L, hist, ds);
+    plan_hist_kernel<<<L.chunks, kPlanThreads, 0, s>>>(adapter_idx, c.T, c.L, hist);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return status_from_cuda(e);
   }
-  plan_place_kernel<<<L.chunks, kPlanThreads, 0, s>>>(
-      adapter_idx, c.T, c.L, L.chunks, L.chunks > 1 ? hist : nullptr, reinterpret_cast<int4*>(b + L.hdr),
-      reinterpret_cast<int32_t*>(b + L.seg), reinterpret_cast<int4*>(b + L.tiles), L.max_tiles,
-      reinterpret_cast<int32_t*>(b + L.order), ds);
-  const int rc = status_from_cuda(cudaGetLastError());
+  int4* hdr = reinterpret_cast<int4*>(b + L.hdr);
+  int32_t* seg = reinterpret_cast<int32_t*>(b + L.seg);
+  int4* tiles = reinterpret_cast<int4*>(b + L.tiles);
+  int4* big = reinterpret_cast<int4*>(b + L.big);
+  int32_t* order = reinterpret_cast<int32_t*>(b + L.order);
+  const int32_t* counted = L.chunks > 1 ? hist : nullptr;
+  cudaError_t e = cudaSuccess;
+  if (L.chunks > 1) {
+    e = launch_chained(plan_place_kernel, L.chunks, kPlanThreads, 0, s, adapter_idx, c.T, c.L, L.chunks, counted, hdr,
+                       seg, tiles, L.max_tiles, big, L.max_big, order, ds);
+  } else {
+    plan_place_kernel<<<1, kPlanThreads, 0, s>>>(adapter_idx, c.T, c.L, 1, counted, hdr, seg, tiles, L.max_tiles, big,
+                                                 L.max_big, order, ds);
+    e = cudaGetLastError();
+  }
+  const int rc = status_from_cuda(e);
   record_stage(s, 45, L.chunks > 1 ? 2 : 1);
   return rc;
 }
@@ -800,15 +773,15 @@ int moe_adapter_fwd(const moe_adapter_config* cfg, const moe_bf16* x, const moe_
   const PlanLayout P = plan_layout(c);
   const PlanView pv = plan_view(c, plan, P, ws);
   float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.parts);
-  const int splits = shrink_splits(c, c.K);
+  int splits = 1;
   cudaError_t e = cudaSuccess;
-  MOE_RANK(c.r, e = launch_shrink<RP, false>(c, c.K, x, A, pv, P.max_tiles, splits, parts, s));
+  MOE_RANK(c.r, e = launch_shrink<RP, false>(c, c.K, x, A, pv, P, parts, &splits, s));
   if (e != cudaSuccess) return status_from_cuda(e);
   record_stage(s, 46, 1);
   if (c.out_fp32)
-    MOE_RANK(c.r, e = launch_expand<RP, false, true>(c, c.N, parts, splits, scale, B, pv, P.max_tiles, base, y, u_saved, s));
+    MOE_RANK(c.r, e = launch_expand<RP, false, true>(c, c.N, parts, splits, scale, B, pv, P, base, y, u_saved, s));
   else
-    MOE_RANK(c.r, e = launch_expand<RP, false, false>(c, c.N, parts, splits, scale, B, pv, P.max_tiles, base, y, u_saved, s));
+    MOE_RANK(c.r, e = launch_expand<RP, false, false>(c, c.N, parts, splits, scale, B, pv, P, base, y, u_saved, s));
   record_stage(s, 47, 1);
   return status_from_cuda(e);
 }
@@ -830,22 +803,23 @@ int moe_adapter_bwd(const moe_adapter_config* cfg, const moe_bf16* dy, const moe
   const PlanView pv = plan_view(c, plan, P, ws);
   float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.parts);
   void* du = static_cast<uint8_t*>(ws) + L.du;
-  const int splits = shrink_splits(c, c.N);
+  float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.partial);
+  int splits = 1;
   cudaError_t e = cudaSuccess;
-  MOE_RANK(c.r, e = launch_shrink<RP, true>(c, c.N, dy, B, pv, P.max_tiles, splits, parts, s));
+  MOE_RANK(c.r, e = launch_shrink<RP, true>(c, c.N, dy, B, pv, P, parts, &splits, s));
   if (e != cudaSuccess) return status_from_cuda(e);
   record_stage(s, 46, 1);
   if (c.out_fp32)
-    MOE_RANK(c.r, e = launch_expand<RP, true, true>(c, c.K, parts, splits, scale, A, pv, P.max_tiles, dx_base, dx, du, s));
+    MOE_RANK(c.r, e = launch_expand<RP, true, true>(c, c.K, parts, splits, scale, A, pv, P, dx_base, dx, du, s));
   else
-    MOE_RANK(c.r, e = launch_expand<RP, true, false>(c, c.K, parts, splits, scale, A, pv, P.max_tiles, dx_base, dx, du, s));
+    MOE_RANK(c.r, e = launch_expand<RP, true, false>(c, c.K, parts, splits, scale, A, pv, P, dx_base, dx, du, s));
   if (e != cudaSuccess) return status_from_cuda(e);
   record_stage(s, 47, 1);
-  MOE_RANK(c.r, e = launch_wgrad<RP, false>(c, c.K, x, du, pv, dA, s));
+  MOE_RANK(c.r, e = launch_wgrad<RP, false>(c, c.K, x, du, pv, dA, partial, s));
   if (e != cudaSuccess) return status_from_cuda(e);
-  record_stage(s, 48, 1);
-  MOE_RANK(c.r, e = launch_wgrad<RP, true>(c, c.N, dy, u_saved, pv, dB, s));
-  record_stage(s, 48, 1);
+  record_stage(s, 48, 2);
+  MOE_RANK(c.r, e = launch_wgrad<RP, true>(c, c.N, dy, u_saved, pv, dB, partial, s));
+  record_stage(s, 48, 2);
   return status_from_cuda(e);
 }
 

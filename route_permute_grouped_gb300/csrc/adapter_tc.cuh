@@ -1,0 +1,722 @@
+// The adapters' products on the tensor memory path (tcgen05, one CTA, M = 128):
+//   shrink  parts[position][j]  = X[t] W_a          128 rows of one adapter
+//   expand  out[t]              = base[t] + u W_a   128 rows of one adapter
+//   wgrad   G_a                 = X_a^T V_a         columns of X, rows in equal runs
+// The rows of X, base and out are gathered through the plan's order, so the
+// tiles come by 16-byte cp.async copies written in the 128-byte swizzle that the
+// MMA's descriptors expect, not by TMA boxes.
+//
+// All three run nine warps: 0-3 epilogue (TMEM lane quarter = warp), 4 TMEM
+// owner and MMA issuer, 5-8 producers. A stage of operands is full when the
+// 128 producer threads have seen their copies land (and fenced them for the
+// tensor cores), empty again when the MMAs that read it have completed.
+//
+// fp32 accumulation in tensor memory cuts each addition at the accumulator's last
+// bit: measured against fp64 the sum of K products is too small by 1e-9 K of
+// itself (K = 512: 5.1e-7, 4096: 4.1e-6). So a sum runs over at most kFlush = 8
+// blocks of 64 in tensor memory; the epilogue adds those in registers in ordinary
+// fp32 while the MMAs go on with the other accumulator.
+#pragma once
+#include "host_util.h"
+#include "mma.cuh"
+
+namespace moe {
+
+constexpr int kTcThreads = 288;
+constexpr int kTcProducers = 128;
+constexpr int kFlush = 8;
+
+struct PlanView {
+  const int4* hdr;       // {number of 64-row tiles, T, L, kPlanMagic}, {number of 128-row tiles, 0, 0, 0}
+  const int32_t* seg;    // [L + 2]: first position of each adapter, then of the rows without one, then T
+  const int4* tiles;     // 64-row tiles {adapter or -1, first position, rows, 0}
+  const int4* big;       // the same in 128 rows
+  const int32_t* order;  // [T]: token of each position
+  int T, L;
+  DevStatus* st;
+};
+constexpr int kPlanMagic = 0x706c616f;
+// the number of tiles (of 64 rows, or 128 with `big`); 0, and a device error, for
+// a plan of another batch size or number of adapters or a buffer that holds none
+__device__ __forceinline__ int plan_tiles(const PlanView& p, bool big = false) {
+  const int4 h = __ldg(p.hdr);
+  if (h.y == p.T && h.z == p.L && h.w == kPlanMagic) return big ? __ldg(p.hdr + 1).x : h.x;
+  set_status(p.st, MOE_ERR_DEVICE_INDEX, 61);
+  return 0;
+}
+
+// byte offset of 16-byte piece c of row r in a tile of 128-byte rows, swizzled
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+// Barriers and roles' common state at the end of dynamic shared memory
+template <int NST>
+struct TcBars {
+  uint64_t full[NST], empty[NST], tfull[2], tempty[2], ready, drain;
+  uint32_t tmem;
+  int abort;
+};
+template <int NST>
+__device__ __forceinline__ void tc_init(TcBars<NST>* b, int empty_count, uint32_t tmem_cols) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(b->full + s, kTcProducers);
+      mbar_init(b->empty + s, empty_count);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b->tfull + i, 1);
+      mbar_init(b->tempty + i, 128);
+    }
+    mbar_init(&b->ready, 128);
+    mbar_init(&b->drain, 1);
+    b->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp_id() == 4) {
+    tmem_alloc(&b->tmem, tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+}
+// Every thread ends here. After a wait that ran out the MMAs in flight are given
+// their (bounded) time before the tensor memory is freed.
+template <int NST>
+__device__ __forceinline__ void tc_end(TcBars<NST>* b, uint32_t tmem_cols, uint64_t lim) {
+  tc_fence_before();
+  __syncthreads();
+  if (warp_id() == 4) {
+    tc_fence_after();
+    if (*static_cast<volatile int*>(&b->abort)) {
+      int zero = 0;
+      if (elect_lane0()) umma_commit(&b->drain);
+      __syncwarp();
+      mbar_wait_bounded(&b->drain, 0, &zero, lim, nullptr, 0);
+    }
+    tmem_dealloc(b->tmem, tmem_cols);
+  }
+}
+
+// A producer thread's side of the ring: copies of stage i are announced when
+// those of kLag later stages have been issued
+template <int NST>
+struct TcRing {
+  static constexpr int kLag = NST > 2 ? 2 : 1;
+  TcBars<NST>* b;
+  int i = 0;  // stages begun
+  __device__ __forceinline__ explicit TcRing(TcBars<NST>* bars) : b(bars) {}
+  __device__ __forceinline__ int slot() const { return i % NST; }
+  __device__ __forceinline__ bool begin(uint64_t lim, DevStatus* st) {
+    return mbar_wait_bounded(b->empty + slot(), ((i / NST) & 1) ^ 1, &b->abort, lim, st, 62);
+  }
+  __device__ __forceinline__ void commit() {
+    cp_async_commit();
+    if (i >= kLag) {
+      cp_async_wait<kLag>();
+      fence_proxy_async_smem();
+      mbar_arrive(b->full + (i - kLag) % NST);
+    }
+    ++i;
+  }
+  __device__ __forceinline__ void end() {
+    cp_async_wait<0>();
+    fence_proxy_async_smem();
+    for (int j = i > kLag ? i - kLag : 0; j < i; ++j) mbar_arrive(b->full + j % NST);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// shrink
+// ---------------------------------------------------------------------------
+template <int RP, bool WT>
+struct TcShrink {
+  static constexpr int kX = 128 * 128;
+  static constexpr int kW = WT ? RP * 128 : (RP + 63) / 64 * 8192;
+  static constexpr int kStage = kX + kW;
+  static constexpr int NST = 4;
+  static constexpr int kAcc = RP < 32 ? 32 : RP;  // TMEM columns of an accumulator
+  static constexpr uint32_t kTmem = 2 * kAcc;
+  static constexpr int kTotal = NST * kStage + sizeof(TcBars<NST>) + 1024;
+};
+
+// parts[split][position][j] = sum over the split's part of C of X[t][c] W_a[c][j];
+// W_a is [C][r] (WT = false) or [r][C] (WT = true). Bound by the rows of X, read
+// once; W_a comes from L2 for every 128 rows.
+template <int RP, bool WT>
+__global__ void __launch_bounds__(kTcThreads, RP <= 64 ? 2 : 1)
+    adapter_shrink_tc(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ W, PlanView plan, int T,
+                      int C, int r, int splits, float* __restrict__ parts, uint64_t lim) {
+  using S = TcShrink<RP, WT>;
+  constexpr int NST = S::NST;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  auto* bars = reinterpret_cast<TcBars<NST>*>(smem + NST * S::kStage);
+  chain_wait();
+  if (static_cast<int>(blockIdx.x) >= plan_tiles(plan, true)) return;
+  const int4 tile = plan.big[blockIdx.x];
+  if (tile.x < 0) return;
+  const int warp = warp_id(), lane = lane_id();
+  const int nkb = (C + 63) / 64, per = (nkb + splits - 1) / splits;
+  const int kb0 = blockIdx.y * per, kb1 = min(nkb, kb0 + per);
+  const uint32_t base = smem_u32(smem);
+  tc_init(bars, 1, S::kTmem);
+  const uint32_t tmem = bars->tmem;
+
+  if (warp >= 5) {
+    const int p = threadIdx.x - 160;
+    const __nv_bfloat16* Wa = W + static_cast<size_t>(tile.x) * C * r;
+    const int c8 = p & 7;
+    const __nv_bfloat16* row[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int q = (p >> 3) + 16 * i;
+      row[i] = q < tile.z ? X + static_cast<size_t>(plan.order[tile.y + q]) * C + c8 * 8 : nullptr;
+    }
+    TcRing<NST> ring(bars);
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!ring.begin(lim, plan.st)) break;
+      const uint32_t sx = base + ring.slot() * S::kStage, sw = sx + S::kX;
+      const int c0 = kb * 64;
+      const bool in = c0 + c8 * 8 < C;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool ok = in && row[i] != nullptr;
+        cp_async16(sx + swz((p >> 3) + 16 * i, c8), ok ? row[i] + c0 : X, ok);
+      }
+      if constexpr (WT) {
+#pragma unroll
+        for (int i = p; i < RP * 8; i += kTcProducers) {
+          const int j = i >> 3;
+          const bool ok = in && j < r;
+          cp_async16(sw + swz(j, c8), ok ? Wa + static_cast<size_t>(j) * C + c0 + c8 * 8 : W, ok);
+        }
+      } else {
+#pragma unroll
+        for (int i = p; i < 64 * (RP / 8); i += kTcProducers) {
+          const int k = i / (RP / 8), j8 = i % (RP / 8);
+          const bool ok = c0 + k < C && j8 * 8 < r;
+          cp_async16(sw + (j8 >> 3) * 8192 + swz(k, j8 & 7), ok ? Wa + static_cast<size_t>(c0 + k) * r + j8 * 8 : W, ok);
+        }
+      }
+      ring.commit();
+    }
+    ring.end();
+  } else if (warp == 4) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, RP, false, !WT);
+    const uint32_t hi = sdesc_hi_sw128(1024);
+    const uint32_t a0 = sdesc_lo(base, 16), b0 = sdesc_lo(base + S::kX, WT ? 16 : 8192);
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int i = kb - kb0, s = i % NST, chunk = i / kFlush, buf = chunk & 1;
+      if (i % kFlush == 0 && !mbar_wait_bounded(bars->tempty + buf, ((chunk >> 1) & 1) ^ 1, &bars->abort, lim, plan.st, 63))
+        break;
+      if (!mbar_wait_bounded(bars->full + s, (i / NST) & 1, &bars->abort, lim, plan.st, 64)) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t so = static_cast<uint32_t>(s * S::kStage) >> 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          umma_bf16_w(tmem + buf * S::kAcc, a0 + so + 2 * k, b0 + so + k * (WT ? 2 : 128), hi, idesc,
+                      i % kFlush != 0 || k != 0);
+        umma_commit(bars->empty + s);
+        if (i % kFlush == kFlush - 1 || kb + 1 == kb1) umma_commit(bars->tfull + buf);
+      }
+      __syncwarp();
+    }
+  } else {
+    float acc[RP];
+#pragma unroll
+    for (int j = 0; j < RP; ++j) acc[j] = 0.0f;
+    const int chunks = (kb1 - kb0 + kFlush - 1) / kFlush;
+    bool ok = true;
+    for (int c = 0; c < chunks; ++c) {
+      const int buf = c & 1;
+      if (!mbar_wait_bounded(bars->tfull + buf, (c >> 1) & 1, &bars->abort, lim, plan.st, 65)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int j = 0; j < RP; j += 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem + buf * S::kAcc + j + (static_cast<uint32_t>(warp) << 21), v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 32 && j + q < RP; ++q) acc[j + q] += __uint_as_float(v[q]);
+      }
+      tc_fence_before();
+      mbar_arrive(bars->tempty + buf);
+    }
+    const int q = warp * 32 + lane;
+    if (ok && q < tile.z) {
+      float4* out = reinterpret_cast<float4*>(parts + (static_cast<size_t>(blockIdx.y) * T + tile.y + q) * RP);
+#pragma unroll
+      for (int j = 0; j < RP; j += 4) out[j / 4] = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+    }
+  }
+  chain_release();
+  tc_end(bars, S::kTmem, lim);
+}
+
+// ---------------------------------------------------------------------------
+// expand
+// ---------------------------------------------------------------------------
+template <int RP, bool WT, bool F32>
+struct TcExpand {
+  static constexpr int kParts = F32 ? 3 : 2;  // of u: 2^-17 of it, or 2^-25 for an fp32 result
+  static constexpr int NC = F32 ? 64 : 128;   // columns of a step
+  static constexpr int kUChunks = (kParts * RP + 63) / 64;
+  static constexpr int kU = kUChunks * 128 * 128;
+  static constexpr int kWChunk = WT ? NC * 128 : RP * 128;  // 64 wide
+  static constexpr int kW = (WT ? (RP + 63) / 64 : NC / 64) * kWChunk;
+  static constexpr int kYRow = NC * (F32 ? 4 : 2) + 16;
+  static constexpr int kY = 128 * kYRow;
+  static constexpr int kStage = (kW + kY + 1023) / 1024 * 1024;
+  static constexpr int NST = RP <= 64 ? 3 : 2;
+  static constexpr uint32_t kTmem = 2 * NC;
+  static constexpr int kTotal = kU + NST * kStage + sizeof(TcBars<NST>) + 128 * 4 + 1024;
+};
+
+// out[t][c] = base[t][c] + sum_j u[position][j] W_a[j][c], u = s_a sum over the
+// splits of parts. u's bf16 parts lie side by side along the contraction, each
+// against the same tile of W_a, [r][C] (WT = false) or [C][r] (WT = true). Bound by
+// base and out. The blocks of the first columns keep u's three parts for the
+// weight gradients (u_keep: [3][T][RP]).
+template <int RP, bool WT, bool F32>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    adapter_expand_tc(const float* __restrict__ parts, int splits, const float* __restrict__ scale,
+                      const __nv_bfloat16* __restrict__ W, PlanView plan, int T, int C, int r, int steps,
+                      const void* base_in, void* out, __nv_bfloat16* __restrict__ u_keep, uint64_t lim) {
+  using S = TcExpand<RP, WT, F32>;
+  constexpr int NST = S::NST, NC = S::NC, EB = F32 ? 4 : 2, PER = 16 / EB, PIECES = NC / PER;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  auto* bars = reinterpret_cast<TcBars<NST>*>(smem + S::kU + NST * S::kStage);
+  int* s_tok = reinterpret_cast<int*>(bars + 1);
+  chain_wait();
+  if (static_cast<int>(blockIdx.x) >= plan_tiles(plan, true)) return;
+  const int4 tile = plan.big[blockIdx.x];
+  const int first = blockIdx.y * steps * NC, last = min(C, first + steps * NC);
+  if (first >= last) return;
+  const int warp = warp_id(), lane = lane_id();
+  if (tile.x < 0 && base_in == out) return;
+  if (threadIdx.x < static_cast<unsigned>(tile.z)) s_tok[threadIdx.x] = plan.order[tile.y + threadIdx.x];
+  if (tile.x < 0) {
+    // rows without an adapter: the base as it is
+    __syncthreads();
+    const int vecs = (last - first) / PER;
+    for (int row = warp; row < tile.z; row += kTcThreads / 32) {
+      const size_t at = (static_cast<size_t>(s_tok[row]) * C + first) * EB;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base_in) + at);
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + at);
+      for (int i = lane; i < vecs; i += 32) dst[i] = base_in != nullptr ? src[i] : make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  const uint32_t sb = smem_u32(smem);
+  tc_init(bars, 1 + 128, S::kTmem);
+  const uint32_t tmem = bars->tmem;
+  const int n = (last - first + NC - 1) / NC;
+
+  if (warp >= 5) {
+    const int p = threadIdx.x - 160;
+    const __nv_bfloat16* Wa = W + static_cast<size_t>(tile.x) * C * r;
+    TcRing<NST> ring(bars);
+    for (int i = 0; i < n; ++i) {
+      if (!ring.begin(lim, plan.st)) break;
+      const uint32_t sw = sb + S::kU + ring.slot() * S::kStage, sy = sw + S::kW;
+      const int c0 = first + i * NC;
+      if constexpr (WT) {
+#pragma unroll 4
+        for (int k = p; k < NC * (RP / 8); k += kTcProducers) {
+          const int c = k / (RP / 8), j8 = k % (RP / 8);
+          const bool ok = j8 * 8 < r && c0 + c < last;
+          cp_async16(sw + (j8 >> 3) * S::kWChunk + swz(c, j8 & 7),
+                     ok ? Wa + static_cast<size_t>(c0 + c) * r + j8 * 8 : W, ok);
+        }
+      } else {
+#pragma unroll 4
+        for (int k = p; k < RP * (NC / 8); k += kTcProducers) {
+          const int j = k / (NC / 8), c8 = k % (NC / 8);
+          const bool ok = j < r && c0 + c8 * 8 < last;
+          cp_async16(sw + (c8 >> 3) * S::kWChunk + swz(j, c8 & 7),
+                     ok ? Wa + static_cast<size_t>(j) * C + c0 + c8 * 8 : W, ok);
+        }
+      }
+      if (base_in != nullptr) {
+        const int cp = p % PIECES;
+        const bool in = c0 + cp * PER < last;
+#pragma unroll
+        for (int k = 0; k < 128 * PIECES / kTcProducers; ++k) {
+          const int row = p / PIECES + k * (kTcProducers / PIECES);
+          if (in && row < tile.z)
+            cp_async16(sy + row * S::kYRow + cp * 16,
+                       static_cast<const uint8_t*>(base_in) + (static_cast<size_t>(s_tok[row]) * C + c0 + cp * PER) * EB,
+                       true);
+        }
+      }
+      ring.commit();
+    }
+    ring.end();
+  } else if (warp == 4) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, NC, false, !WT);
+    const uint32_t hi = sdesc_hi_sw128(1024);
+    const uint32_t a0 = sdesc_lo(sb, 16), b0 = sdesc_lo(sb + S::kU, WT ? 16 : S::kWChunk);
+    bool ok = mbar_wait_bounded(&bars->ready, 0, &bars->abort, lim, plan.st, 66);
+    for (int i = 0; i < n && ok; ++i) {
+      const int s = i % NST, buf = i & 1;
+      if (!mbar_wait_bounded(bars->tempty + buf, ((i >> 1) & 1) ^ 1, &bars->abort, lim, plan.st, 67) ||
+          !mbar_wait_bounded(bars->full + s, (i / NST) & 1, &bars->abort, lim, plan.st, 68))
+        break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t b = b0 + (static_cast<uint32_t>(s * S::kStage) >> 4);
+        // the small parts first
+#pragma unroll
+        for (int h = S::kParts - 1; h >= 0; --h)
+#pragma unroll
+          for (int k = 0; k < RP / 16; ++k) {
+            const int ak = h * RP + 16 * k;  // column of u's row of parts
+            const uint32_t a = a0 + (ak / 64) * (16384 >> 4) + ((ak % 64) * 2 >> 4);
+            const uint32_t bk = WT ? (16 * k / 64) * (S::kWChunk >> 4) + ((16 * k % 64) * 2 >> 4) : k * 128;
+            umma_bf16_w(tmem + buf * NC, a, b + bk, hi, idesc, h != S::kParts - 1 || k != 0);
+          }
+        umma_commit(bars->empty + s);
+        umma_commit(bars->tfull + buf);
+      }
+      __syncwarp();
+    }
+  } else {
+    // u of this thread's row
+    const int q = warp * 32 + lane;
+    const bool live = q < tile.z;
+    const float sc = scale[tile.x];
+    const float* up = parts + static_cast<size_t>(tile.y + (live ? q : 0)) * RP;
+#pragma unroll 1
+    for (int j = 0; j < RP; j += 8) {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+      if (live) {
+        for (int s = 0; s < splits; ++s) {
+          const float4* w = reinterpret_cast<const float4*>(up + static_cast<size_t>(s) * T * RP + j);
+          const float4 x = w[0], y = w[1];
+          f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+          f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+        }
+      }
+      __nv_bfloat16 part[3][8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) split_bf16(f[e] * sc, part[0][e], part[1][e], part[2][e]);
+#pragma unroll
+      for (int h = 0; h < 3; ++h) {
+        const uint4 v = *reinterpret_cast<const uint4*>(part[h]);
+        const int ak = h * RP + j;
+        if (h < S::kParts) *reinterpret_cast<uint4*>(smem + (ak / 64) * 16384 + swz(q, (ak % 64) / 8)) = v;
+        if (u_keep != nullptr && blockIdx.y == 0 && live)
+          *reinterpret_cast<uint4*>(u_keep + (static_cast<size_t>(h) * T + tile.y + q) * RP + j) = v;
+      }
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(&bars->ready);
+    for (int i = 0; i < n; ++i) {
+      const int s = i % NST, buf = i & 1, c0 = first + i * NC;
+      if (!mbar_wait_bounded(bars->full + s, (i / NST) & 1, &bars->abort, lim, plan.st, 69) ||
+          !mbar_wait_bounded(bars->tfull + buf, (i >> 1) & 1, &bars->abort, lim, plan.st, 70))
+        break;
+      tc_fence_after();
+      uint8_t* sy = smem + S::kU + s * S::kStage + S::kW + warp * 32 * S::kYRow;
+      uint8_t* mine = sy + lane * S::kYRow;
+#pragma unroll
+      for (int j = 0; j < NC; j += 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem + buf * NC + j + (static_cast<uint32_t>(warp) << 21), v);
+        tmem_ld_wait();
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += PER) {
+            uint4* y = reinterpret_cast<uint4*>(mine + (j + e) * EB);
+            uint4 w = base_in != nullptr ? *y : make_uint4(0, 0, 0, 0);
+            if constexpr (F32) {
+              w.x = __float_as_uint(__uint_as_float(w.x) + __uint_as_float(v[e]));
+              w.y = __float_as_uint(__uint_as_float(w.y) + __uint_as_float(v[e + 1]));
+              w.z = __float_as_uint(__uint_as_float(w.z) + __uint_as_float(v[e + 2]));
+              w.w = __float_as_uint(__uint_as_float(w.w) + __uint_as_float(v[e + 3]));
+            } else {
+              w.x = pack_bf16x2(bf16_lo(w.x) + __uint_as_float(v[e]), bf16_hi(w.x) + __uint_as_float(v[e + 1]));
+              w.y = pack_bf16x2(bf16_lo(w.y) + __uint_as_float(v[e + 2]), bf16_hi(w.y) + __uint_as_float(v[e + 3]));
+              w.z = pack_bf16x2(bf16_lo(w.z) + __uint_as_float(v[e + 4]), bf16_hi(w.z) + __uint_as_float(v[e + 5]));
+              w.w = pack_bf16x2(bf16_lo(w.w) + __uint_as_float(v[e + 6]), bf16_hi(w.w) + __uint_as_float(v[e + 7]));
+            }
+            *y = w;
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bars->tempty + buf);
+      __syncwarp();
+      // whole lines of the warp's 32 rows
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k) {
+        const int e = lane + 32 * k, row = e / PIECES, c = (e % PIECES) * PER;
+        if (warp * 32 + row < tile.z && c0 + c < last)
+          __stcs(reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) +
+                                          (static_cast<size_t>(s_tok[warp * 32 + row]) * C + c0 + c) * EB),
+                 *reinterpret_cast<const uint4*>(sy + row * S::kYRow + c * EB));
+      }
+      mbar_arrive(bars->empty + s);
+    }
+  }
+  chain_release();
+  tc_end(bars, S::kTmem, lim);
+}
+
+// ---------------------------------------------------------------------------
+// weight gradients
+// ---------------------------------------------------------------------------
+template <int RP>
+struct TcWgrad {
+  static constexpr int CT = RP <= 64 ? 2 : 1;           // 128-column tiles of X in a block
+  static constexpr int kCols = CT * 128;
+  static constexpr int kX = CT * 16384;
+  static constexpr int kN = 3 * RP;                     // the parts of V side by side
+  static constexpr int kV = (kN + 63) / 64 * 8192;
+  static constexpr int kStage = kX + kV;
+  static constexpr int NST = RP <= 32 ? 4 : 3;
+  static constexpr int kSet = (kN + 63) / 64 * 64;      // TMEM columns of a tile's accumulators
+  static constexpr int kAcc = CT * kSet;                // of both tiles'
+  static constexpr int kBufs = 2 * kAcc <= 512 ? 2 : 1;
+  static constexpr uint32_t kTmem = kBufs * kAcc <= 128 ? 128 : (kBufs * kAcc <= 256 ? 256 : 512);
+  static constexpr int kTotal = NST * kStage + sizeof(TcBars<NST>) + 1024;
+};
+
+// the rows of run y: positions [y rows, (y + 1) rows) of those with an adapter
+struct RowRuns {
+  int rows, runs;
+};
+
+// G_a[c][j] = sum over the rows t of adapter a of X[t][c] V[position][j]. A block
+// takes kCols columns and one of equal runs of rows, whatever adapters lie in it;
+// what it has of an adapter that lies in its run alone is the result, of others a
+// partial (at most two a run: at its start and at its end) that
+// adapter_wgrad_join adds up. V's three bf16 parts lie side by side as the MMA's N,
+// so X is read from shared memory once for the three; their sums are added in the
+// epilogue, the small ones first. OUT_T: G_a is stored [r][C] (dB), else [C][r].
+template <int RP, bool OUT_T>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    adapter_wgrad_tc(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ V, PlanView plan, int T,
+                     int C, int r, RowRuns run, float* __restrict__ G, float* __restrict__ partial, uint64_t lim) {
+  using S = TcWgrad<RP>;
+  constexpr int NST = S::NST, CT = S::CT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  auto* bars = reinterpret_cast<TcBars<NST>*>(smem + NST * S::kStage);
+  chain_wait();
+  if (plan_tiles(plan) == 0) return;
+  const int live = plan.seg[plan.L];
+  const int P0 = blockIdx.y * run.rows, P1 = min(live, P0 + run.rows);
+  if (P0 >= P1) return;
+  const int warp = warp_id(), lane = lane_id(), c0 = blockIdx.x * S::kCols;
+  // the first adapter with rows behind P0
+  int a0 = 0;
+  for (int i0 = 0; i0 < plan.L; i0 += kTcThreads) {
+    const int i = i0 + static_cast<int>(threadIdx.x);
+    a0 += __syncthreads_count(i < plan.L && plan.seg[i + 1] <= P0);
+  }
+  const uint32_t base = smem_u32(smem);
+  tc_init(bars, 1, S::kTmem);
+  const uint32_t tmem = bars->tmem;
+
+  if (warp >= 5) {
+    const int p = threadIdx.x - 160, w = warp - 5;
+    TcRing<NST> ring(bars);
+    bool ok = true;
+    for (int a = a0; a < plan.L && ok; ++a) {
+      const int lo = max(plan.seg[a], P0), hi = min(plan.seg[a + 1], P1);
+      if (plan.seg[a] >= P1) break;
+      for (int q0 = lo; q0 < hi; q0 += 64) {
+        const int n = min(64, hi - q0);
+        // tokens of the block's rows: lane l holds those of rows l and l + 32
+        const int t0 = lane < n ? plan.order[q0 + lane] : 0, t1 = lane + 32 < n ? plan.order[q0 + lane + 32] : 0;
+        if (!ring.begin(lim, plan.st)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sx = base + ring.slot() * S::kStage, sv = sx + S::kX;
+        // X: a warp copies 32 pieces of 16 bytes: 256 columns of a row, or 128 of two
+        constexpr int RPI = 32 / (16 * CT);  // rows at a time
+#pragma unroll
+        for (int i = 0; i < 16 / RPI; ++i) {
+          const int row = (w * (16 / RPI) + i) * RPI + (RPI == 2 ? lane >> 4 : 0);
+          const int c8 = RPI == 2 ? lane & 15 : lane, c = c0 + c8 * 8;
+          const int tok = __shfl_sync(0xffffffffu, row < 32 ? t0 : t1, row & 31);
+          const bool in = row < n && c < C;
+          cp_async16(sx + (c8 >> 3) * 8192 + swz(row, c8 & 7), in ? X + static_cast<size_t>(tok) * C + c : X, in);
+        }
+#pragma unroll
+        for (int k = 0; k < 64 * (RP / 8) / kTcProducers; ++k) {
+          const int i = p + k * kTcProducers, row = i / (RP / 8), j8 = i % (RP / 8);
+          const bool in = row < n;
+          const __nv_bfloat16* src = V + (in ? static_cast<size_t>(q0 + row) * RP + j8 * 8 : 0);
+#pragma unroll
+          for (int h = 0; h < 3; ++h) {
+            const int col8 = h * (RP / 8) + j8;
+            cp_async16(sv + (col8 >> 3) * 8192 + swz(row, col8 & 7), src + static_cast<size_t>(h) * T * RP, in);
+          }
+        }
+        ring.commit();
+      }
+    }
+    ring.end();
+  } else if (warp == 4) {
+    constexpr int NI = S::kN <= 256 ? 1 : 3;  // instructions over N
+    constexpr uint32_t idesc = idesc_bf16_f32(128, S::kN / NI, true, true);
+    const uint32_t dhi = sdesc_hi_sw128(1024);
+    const uint32_t d0 = sdesc_lo(base, 8192), v0 = sdesc_lo(base + S::kX, 8192);
+    int i = 0, chunk = 0;
+    bool ok = true;
+    for (int a = a0; a < plan.L && ok; ++a) {
+      const int lo = max(plan.seg[a], P0), hi = min(plan.seg[a + 1], P1);
+      if (plan.seg[a] >= P1) break;
+      const int blocks = (hi - lo + 63) / 64;
+      for (int b = 0; b < blocks; ++b, ++i) {
+        const int s = i % NST, buf = S::kBufs == 2 ? chunk & 1 : 0;
+        const uint32_t use = S::kBufs == 2 ? chunk >> 1 : chunk;
+        if (b % kFlush == 0 && !mbar_wait_bounded(bars->tempty + buf, (use & 1) ^ 1, &bars->abort, lim, plan.st, 71)) {
+          ok = false;
+          break;
+        }
+        if (!mbar_wait_bounded(bars->full + s, (i / NST) & 1, &bars->abort, lim, plan.st, 72)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const bool done = b % kFlush == kFlush - 1 || b + 1 == blocks;
+        if (lane == 0) {
+          const uint32_t so = static_cast<uint32_t>(s * S::kStage) >> 4;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+              for (int h = 0; h < NI; ++h)
+                umma_bf16_w(tmem + buf * S::kAcc + ct * S::kSet + h * (S::kN / NI), d0 + so + ct * (16384 >> 4) + k * 128,
+                            v0 + so + h * (S::kN / NI / 64) * (8192 >> 4) + k * 128, dhi, idesc,
+                            b % kFlush != 0 || k != 0);
+          umma_commit(bars->empty + s);
+          if (done) umma_commit(bars->tfull + buf);
+        }
+        __syncwarp();
+        if (done) ++chunk;
+      }
+    }
+  } else {
+    const uint32_t quarter = static_cast<uint32_t>(warp) << 21;
+    int chunk = 0;
+    bool ok = true;
+    for (int a = a0; a < plan.L && ok; ++a) {
+      const int sa = plan.seg[a], se = plan.seg[a + 1];
+      if (sa >= P1) break;
+      const int lo = max(sa, P0), hi = min(se, P1);
+      if (lo >= hi) continue;
+      const int chunks = ((hi - lo + 63) / 64 + kFlush - 1) / kFlush;
+      float acc[CT][RP];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int j = 0; j < RP; ++j) acc[ct][j] = 0.0f;
+      for (int k = 0; k < chunks; ++k, ++chunk) {
+        const int buf = S::kBufs == 2 ? chunk & 1 : 0;
+        const uint32_t use = S::kBufs == 2 ? chunk >> 1 : chunk;
+        if (!mbar_wait_bounded(bars->tfull + buf, use & 1, &bars->abort, lim, plan.st, 73)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const uint32_t at = tmem + buf * S::kAcc + ct * S::kSet + quarter;
+          if constexpr (RP == 16) {
+            uint32_t x[32], y[32];  // parts 0 and 1, part 2 (and 16 columns of no use)
+            tmem_ld32(at, x);
+            tmem_ld32(at + 32, y);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              acc[ct][j] += __uint_as_float(x[j]) + (__uint_as_float(x[16 + j]) + __uint_as_float(y[j]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < RP; j += 32) {
+#pragma unroll
+              for (int h = 2; h >= 0; --h) {
+                uint32_t x[32];
+                tmem_ld32(at + h * RP + j, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 32; ++q) acc[ct][j + q] += __uint_as_float(x[q]);
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(bars->tempty + buf);
+      }
+      if (!ok) break;
+      const bool whole = lo == sa && hi == se;
+      float* slot = partial + (static_cast<size_t>(2 * blockIdx.y + (lo > sa ? 0 : 1)) * gridDim.x + blockIdx.x) *
+                                  (S::kCols * RP);
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const int row = ct * 128 + warp * 32 + lane, c = c0 + row;
+        if (!whole) {
+          // [j][column]: a warp writes whole lines
+#pragma unroll
+          for (int j = 0; j < RP; ++j) slot[static_cast<size_t>(j) * S::kCols + row] = acc[ct][j];
+        } else if (c < C) {
+          float* g = G + static_cast<size_t>(a) * C * r;
+          if constexpr (OUT_T) {
+#pragma unroll
+            for (int j = 0; j < RP; ++j)
+              if (j < r) g[static_cast<size_t>(j) * C + c] = acc[ct][j];
+          } else {
+#pragma unroll
+            for (int j = 0; j < RP; j += 4)
+              if (j < r)
+                *reinterpret_cast<float4*>(g + static_cast<size_t>(c) * r + j) =
+                    make_float4(acc[ct][j], acc[ct][j + 1], acc[ct][j + 2], acc[ct][j + 3]);
+          }
+        }
+      }
+    }
+  }
+  chain_release();
+  tc_end(bars, S::kTmem, lim);
+}
+
+// Adapters whose rows lie in several runs: the sum of their partials, run by run.
+// Adapters without rows: zeros.
+template <int RP, bool OUT_T>
+__global__ void __launch_bounds__(256) adapter_wgrad_join(PlanView plan, int C, int r, RowRuns run, int col_tiles,
+                                                          float* __restrict__ G, const float* __restrict__ partial) {
+  constexpr int kCols = TcWgrad<RP>::kCols;
+  chain_wait();
+  const bool any = plan_tiles(plan) > 0;
+  const int a = blockIdx.y, lo = any ? plan.seg[a] : 0, hi = any ? plan.seg[a + 1] : 0;
+  const int y0 = lo / run.rows, y1 = hi > lo ? (hi - 1) / run.rows : y0;
+  if (hi > lo && y0 == y1) return;
+  float* g = G + static_cast<size_t>(a) * C * r;
+  const int n = C * r;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
+    // the order of the partials' memory: columns run fastest
+    const int j = i / C, c = i % C;
+    float s = 0.0f;
+    if (hi > lo)
+      for (int y = y0; y <= y1; ++y)
+        s += partial[((static_cast<size_t>(2 * y + (y == y0 ? 1 : 0)) * col_tiles + c / kCols) * RP + j) * kCols +
+                     c % kCols];
+    g[OUT_T ? static_cast<size_t>(j) * C + c : static_cast<size_t>(c) * r + j] = s;
+  }
+}
+
+}  // namespace moe

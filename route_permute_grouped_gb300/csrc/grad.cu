@@ -325,8 +325,8 @@ __device__ __forceinline__ void scale_chunk(const uint4* __restrict__ v, uint4* 
 template <int N>
 __global__ void __launch_bounds__(kGradThreads) clip_kernel(const __grid_constant__ GradBlock<N> b,
                                                             const float* __restrict__ norm, float max_norm) {
-  if (static_cast<int>(blockIdx.x) >= b.chunks) return;
   chain_wait();
+  if (static_cast<int>(blockIdx.x) >= b.chunks) return;
   float coef = max_norm / (__ldcg(norm) + 1e-6f);
   if (coef > 1.0f) coef = 1.0f;
   if (coef == 1.0f && !b.apart) return;

@@ -932,7 +932,7 @@ def adapter_plan(cfg, adapter_idx, plan=None):
     w = "adapter_plan"
     n = _size("moe_adapter_plan_bytes", cfg)
     idx = _arg(w, "adapter_idx", adapter_idx, torch.int32, (cfg.T,))
-    plan = _scratch(n, adapter_idx.device) if plan is None else plan
+    plan = torch.empty(n, dtype=torch.uint8, device=adapter_idx.device) if plan is None else plan
     _check(lib().moe_adapter_plan(ctypes.byref(cfg), idx, _ws_arg(w, plan, n), plan.numel(), _stream()),
            "moe_adapter_plan")
     return plan

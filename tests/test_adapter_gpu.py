@@ -104,6 +104,26 @@ def test_ranks(r):
 
 
 @pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("r", [8, 16, 24, 32, 40, 64, 96, 128])
+def test_ranks_of_larger_batches(r, f32):
+    _compare(_inputs(600, 200, 328, 3, r, r, f32), _idx(600, 3, r), f32)
+
+
+@pytest.mark.parametrize("T,K,N,L,r", [(513, 1160, 648, 2, 16), (1500, 136, 2056, 1, 64), (3000, 72, 88, 700, 8),
+                                       (5000, 264, 40, 2, 32), (640, 2056, 1032, 5, 128)])
+def test_long_axes_and_many_segments(T, K, N, L, r):
+    # sums longer than an accumulator's turn, several runs of rows for an adapter, adapters of a few rows
+    _compare(_inputs(T, K, N, L, r, T), _idx(T, L, T, none=0.02))
+
+
+@pytest.mark.parametrize("T", [511, 512, 513, 1024, 1025])
+def test_both_forms_agree_at_their_border(T):
+    idx = np.sort(_idx(T, 3, T, none=0.0))
+    _compare(_inputs(T, 128, 128, 3, 16, T), idx)
+    _compare(_inputs(T, 128, 128, 3, 16, T), np.full(T, 2))
+
+
+@pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("T,K,N,L", [(1, 8, 8, 1), (1, 1024, 136, 5), (2, 64, 64, 1), (15, 72, 88, 40), (64, 128, 256, 1),
                                      (65, 264, 120, 2), (130, 520, 504, 200), (700, 200, 328, 4), (1024, 64, 64, 1024),
                                      (1025, 72, 64, 33), (2500, 256, 192, 3)])
