@@ -650,9 +650,9 @@ static cudaError_t launch_expand(const moe_adapter_config& c, int C, const float
     using S = TcExpand<RP, WT, F32>;
     const cudaError_t e = allow_smem<adapter_expand_tc<RP, WT, F32>>(S::kTotal);
     if (e != cudaSuccess) return e;
-    // about one block for each SM, more only where there are more tiles
+    // about one wave of blocks, more only where there are more tiles
     const int cols = (C + S::NC - 1) / S::NC;
-    const int ranges = std::max(1, std::min(cols, (kAdSMs + big_tiles(c) / 2) / big_tiles(c)));
+    const int ranges = std::max(1, std::min(cols, (S::kBlocks * kAdSMs + big_tiles(c) / 2) / big_tiles(c)));
     const int steps = (cols + ranges - 1) / ranges;
     return launch_chained(adapter_expand_tc<RP, WT, F32>, dim3(P.max_big, (cols + steps - 1) / steps), kTcThreads,
                           S::kTotal, s, parts, splits, scale, w, pv, c.T, C, c.r, steps, base, out, k,
@@ -683,9 +683,8 @@ static cudaError_t launch_wgrad(const moe_adapter_config& c, int C, const void* 
                      static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(V), pv, c.T, C, c.r, run,
                      G, partial, static_cast<uint64_t>(wait_limit_ns()));
   if (e != cudaSuccess) return e;
-  const int blocks = std::max(1, std::min(64, C * c.r / 2048));
-  return launch_chained(adapter_wgrad_join<RP, OUT_T>, dim3(blocks, c.L), 256, 0, s, pv, C, c.r, run, col_tiles, G,
-                        static_cast<const float*>(partial));
+  return launch_chained(adapter_wgrad_join<RP, OUT_T>, dim3((C * c.r + 1023) / 1024, run.runs + kZeroRows), 256, 0, s, pv,
+                        C, c.r, run, col_tiles, G, static_cast<const float*>(partial));
 }
 
 static bool any_misaligned(std::initializer_list<const void*> ps) {

@@ -265,16 +265,17 @@ __global__ void __launch_bounds__(kTcThreads, RP <= 64 ? 2 : 1)
 template <int RP, bool WT, bool F32>
 struct TcExpand {
   static constexpr int kParts = F32 ? 3 : 2;  // of u: 2^-17 of it, or 2^-25 for an fp32 result
-  static constexpr int NC = F32 ? 64 : 128;   // columns of a step
+  static constexpr int NC = F32 ? 32 : 64;    // columns of a step: 128-byte lines of base and out
   static constexpr int kUChunks = (kParts * RP + 63) / 64;
   static constexpr int kU = kUChunks * 128 * 128;
   static constexpr int kWChunk = WT ? NC * 128 : RP * 128;  // 64 wide
-  static constexpr int kW = (WT ? (RP + 63) / 64 : NC / 64) * kWChunk;
+  static constexpr int kW = (WT ? (RP + 63) / 64 : 1) * kWChunk;
   static constexpr int kYRow = NC * (F32 ? 4 : 2) + 16;
   static constexpr int kY = 128 * kYRow;
   static constexpr int kStage = (kW + kY + 1023) / 1024 * 1024;
   static constexpr int NST = RP <= 64 ? 3 : 2;
   static constexpr uint32_t kTmem = 2 * NC;
+  static constexpr int kBlocks = F32 || RP > 64 ? 1 : 2;  // resident on an SM
   static constexpr int kTotal = kU + NST * kStage + sizeof(TcBars<NST>) + 128 * 4 + 1024;
 };
 
@@ -284,7 +285,7 @@ struct TcExpand {
 // base and out. The blocks of the first columns keep u's three parts for the
 // weight gradients (u_keep: [3][T][RP]).
 template <int RP, bool WT, bool F32>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(kTcThreads, TcExpand<RP, WT, F32>::kBlocks)
     adapter_expand_tc(const float* __restrict__ parts, int splits, const float* __restrict__ scale,
                       const __nv_bfloat16* __restrict__ W, PlanView plan, int T, int C, int r, int steps,
                       const void* base_in, void* out, __nv_bfloat16* __restrict__ u_keep, uint64_t lim) {
@@ -426,6 +427,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           !mbar_wait_bounded(bars->tfull + buf, (i >> 1) & 1, &bars->abort, lim, plan.st, 70))
         break;
       tc_fence_after();
+      if (warp * 32 >= tile.z) {  // no rows for this warp
+        mbar_arrive(bars->tempty + buf);
+        mbar_arrive(bars->empty + s);
+        continue;
+      }
       uint8_t* sy = smem + S::kU + s * S::kStage + S::kW + warp * 32 * S::kYRow;
       uint8_t* mine = sy + lane * S::kYRow;
 #pragma unroll
@@ -532,13 +538,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int p = threadIdx.x - 160, w = warp - 5;
     TcRing<NST> ring(bars);
     bool ok = true;
+    // tokens of a block's rows, lane l those of rows l and l + 32, asked for one
+    // block ahead: positions run on from one block, or adapter, to the next
+    int next0 = plan.order[min(P0 + lane, T - 1)], next1 = plan.order[min(P0 + lane + 32, T - 1)];
     for (int a = a0; a < plan.L && ok; ++a) {
       const int lo = max(plan.seg[a], P0), hi = min(plan.seg[a + 1], P1);
       if (plan.seg[a] >= P1) break;
       for (int q0 = lo; q0 < hi; q0 += 64) {
         const int n = min(64, hi - q0);
-        // tokens of the block's rows: lane l holds those of rows l and l + 32
-        const int t0 = lane < n ? plan.order[q0 + lane] : 0, t1 = lane + 32 < n ? plan.order[q0 + lane + 32] : 0;
+        const int t0 = next0, t1 = next1;
+        next0 = plan.order[min(q0 + n + lane, T - 1)];
+        next1 = plan.order[min(q0 + n + lane + 32, T - 1)];
         if (!ring.begin(lim, plan.st)) {
           ok = false;
           break;
@@ -694,28 +704,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_end(bars, S::kTmem, lim);
 }
 
-// Adapters whose rows lie in several runs: the sum of their partials, run by run.
-// Adapters without rows: zeros.
+// What the runs leave: blockIdx.y = y < runs: the adapter that begins in run y and
+// goes on behind it, the sum of its partials run by run; from there on the adapters
+// without rows (every kZeroRows-th for one y), zeros. A block takes 1024 values.
+constexpr int kZeroRows = 16;
 template <int RP, bool OUT_T>
 __global__ void __launch_bounds__(256) adapter_wgrad_join(PlanView plan, int C, int r, RowRuns run, int col_tiles,
                                                           float* __restrict__ G, const float* __restrict__ partial) {
   constexpr int kCols = TcWgrad<RP>::kCols;
   chain_wait();
   const bool any = plan_tiles(plan) > 0;
-  const int a = blockIdx.y, lo = any ? plan.seg[a] : 0, hi = any ? plan.seg[a + 1] : 0;
-  const int y0 = lo / run.rows, y1 = hi > lo ? (hi - 1) / run.rows : y0;
-  if (hi > lo && y0 == y1) return;
-  float* g = G + static_cast<size_t>(a) * C * r;
-  const int n = C * r;
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
-    // the order of the partials' memory: columns run fastest
-    const int j = i / C, c = i % C;
-    float s = 0.0f;
-    if (hi > lo)
-      for (int y = y0; y <= y1; ++y)
-        s += partial[((static_cast<size_t>(2 * y + (y == y0 ? 1 : 0)) * col_tiles + c / kCols) * RP + j) * kCols +
-                     c % kCols];
-    g[OUT_T ? static_cast<size_t>(j) * C + c : static_cast<size_t>(c) * r + j] = s;
+  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;  // of the C r values, columns running fastest
+  const int n = C * r, y = blockIdx.y;
+  if (y >= run.runs) {
+    for (int a = y - run.runs; a < plan.L; a += kZeroRows)
+      if (i < n && (!any || plan.seg[a] == plan.seg[a + 1]))
+        *reinterpret_cast<float4*>(G + static_cast<size_t>(a) * n + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    return;
+  }
+  if (!any) return;
+  // the adapter of the run's last position, if it has rows in the next run too
+  const int end = (y + 1) * run.rows;
+  if (end >= plan.seg[plan.L]) return;
+  int a = 0;
+  for (int k0 = 0; k0 < plan.L; k0 += 256) {
+    const int k = k0 + static_cast<int>(threadIdx.x);
+    a += __syncthreads_count(k < plan.L && plan.seg[k + 1] <= end - 1);
+  }
+  const int lo = plan.seg[a], hi = plan.seg[a + 1];
+  if (hi <= end || lo < y * run.rows || i >= n) return;
+  const int y1 = (hi - 1) / run.rows, j = i / C, c = i % C;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = y; k <= y1; ++k) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(
+        partial + ((static_cast<size_t>(2 * k + (k == y ? 1 : 0)) * col_tiles + c / kCols) * RP + j) * kCols + c % kCols));
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  float* g = G + static_cast<size_t>(a) * n;
+  if constexpr (OUT_T) {
+    *reinterpret_cast<float4*>(g + i) = s;
+  } else {
+    const float f[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) g[static_cast<size_t>(c + e) * r + j] = f[e];
   }
 }
 
