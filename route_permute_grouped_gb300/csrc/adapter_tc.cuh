@@ -8,8 +8,8 @@
 //
 // All three run nine warps: 0-3 epilogue (TMEM lane quarter = warp), 4 TMEM
 // owner and MMA issuer, 5-8 producers. A stage of operands is full when the
-// 128 producer threads have seen their copies land (and fenced them for the
-// tensor cores), empty again when the MMAs that read it have completed.
+// copies of the 128 producer threads have landed, empty again when the MMAs that
+// read it have completed.
 //
 // fp32 accumulation in tensor memory cuts each addition at the accumulator's last
 // bit: measured against fp64 the sum of K products is too small by 1e-9 K of
@@ -99,33 +99,34 @@ __device__ __forceinline__ void tc_end(TcBars<NST>* b, uint32_t tmem_cols, uint6
   }
 }
 
-// A producer thread's side of the ring: copies of stage i are announced when
-// those of kLag later stages have been issued
+// A producer thread's side of the ring: it waits for a slot, issues its copies and
+// goes on; the copies' landing arrives on the stage's barrier by itself.
 template <int NST>
 struct TcRing {
-  static constexpr int kLag = NST > 2 ? 2 : 1;
   TcBars<NST>* b;
-  int i = 0;  // stages begun
+  int i = 0;  // stages issued
   __device__ __forceinline__ explicit TcRing(TcBars<NST>* bars) : b(bars) {}
   __device__ __forceinline__ int slot() const { return i % NST; }
   __device__ __forceinline__ bool begin(uint64_t lim, DevStatus* st) {
     return mbar_wait_bounded(b->empty + slot(), ((i / NST) & 1) ^ 1, &b->abort, lim, st, 62);
   }
   __device__ __forceinline__ void commit() {
-    cp_async_commit();
-    if (i >= kLag) {
-      cp_async_wait<kLag>();
-      fence_proxy_async_smem();
-      mbar_arrive(b->full + (i - kLag) % NST);
-    }
+    cp_async_arrive(b->full + slot());
     ++i;
   }
-  __device__ __forceinline__ void end() {
-    cp_async_wait<0>();
-    fence_proxy_async_smem();
-    for (int j = i > kLag ? i - kLag : 0; j < i; ++j) mbar_arrive(b->full + j % NST);
-  }
+  // no thread leaves with copies in flight
+  __device__ __forceinline__ void end() { cp_async_wait_all(); }
 };
+// The MMA issuer's wait for a stage. The copies are generic-proxy writes; the
+// fence, between the barrier and the MMAs of this thread, orders them before the
+// tensor cores' reads.
+template <int NST>
+__device__ __forceinline__ bool tc_stage_ready(TcBars<NST>* b, int i, uint64_t lim, DevStatus* st, int where) {
+  if (!mbar_wait_bounded(b->full + i % NST, (i / NST) & 1, &b->abort, lim, st, where)) return false;
+  fence_proxy_async_smem();
+  tc_fence_after();
+  return true;
+}
 
 // ---------------------------------------------------------------------------
 // shrink
@@ -211,8 +212,7 @@ __global__ void __launch_bounds__(kTcThreads, RP <= 64 ? 2 : 1)
       const int i = kb - kb0, s = i % NST, chunk = i / kFlush, buf = chunk & 1;
       if (i % kFlush == 0 && !mbar_wait_bounded(bars->tempty + buf, ((chunk >> 1) & 1) ^ 1, &bars->abort, lim, plan.st, 63))
         break;
-      if (!mbar_wait_bounded(bars->full + s, (i / NST) & 1, &bars->abort, lim, plan.st, 64)) break;
-      tc_fence_after();
+      if (!tc_stage_ready(bars, i, lim, plan.st, 64)) break;
       if (lane == 0) {
         const uint32_t so = static_cast<uint32_t>(s * S::kStage) >> 4;
 #pragma unroll
@@ -323,6 +323,17 @@ __global__ void __launch_bounds__(kTcThreads, TcExpand<RP, WT, F32>::kBlocks)
   if (warp >= 5) {
     const int p = threadIdx.x - 160;
     const __nv_bfloat16* Wa = W + static_cast<size_t>(tile.x) * C * r;
+    // this thread's pieces of the base's rows: piece cp of rows p / PIECES + k kRowStep
+    constexpr int kRowStep = kTcProducers / PIECES, kRows = 128 / kRowStep;
+    const int cp = p % PIECES;
+    const uint8_t* from[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int row = p / PIECES + k * kRowStep;
+      from[k] = base_in != nullptr && row < tile.z
+                    ? static_cast<const uint8_t*>(base_in) + (static_cast<size_t>(s_tok[row]) * C + cp * PER) * EB
+                    : nullptr;
+    }
     TcRing<NST> ring(bars);
     for (int i = 0; i < n; ++i) {
       if (!ring.begin(lim, plan.st)) break;
@@ -345,18 +356,11 @@ __global__ void __launch_bounds__(kTcThreads, TcExpand<RP, WT, F32>::kBlocks)
                      ok ? Wa + static_cast<size_t>(j) * C + c0 + c8 * 8 : W, ok);
         }
       }
-      if (base_in != nullptr) {
-        const int cp = p % PIECES;
-        const bool in = c0 + cp * PER < last;
+      const bool in = c0 + cp * PER < last;
 #pragma unroll
-        for (int k = 0; k < 128 * PIECES / kTcProducers; ++k) {
-          const int row = p / PIECES + k * (kTcProducers / PIECES);
-          if (in && row < tile.z)
-            cp_async16(sy + row * S::kYRow + cp * 16,
-                       static_cast<const uint8_t*>(base_in) + (static_cast<size_t>(s_tok[row]) * C + c0 + cp * PER) * EB,
-                       true);
-        }
-      }
+      for (int k = 0; k < kRows; ++k)
+        if (in && from[k] != nullptr)
+          cp_async16(sy + (p / PIECES + k * kRowStep) * S::kYRow + cp * 16, from[k] + static_cast<size_t>(c0) * EB, true);
       ring.commit();
     }
     ring.end();
@@ -368,9 +372,8 @@ __global__ void __launch_bounds__(kTcThreads, TcExpand<RP, WT, F32>::kBlocks)
     for (int i = 0; i < n && ok; ++i) {
       const int s = i % NST, buf = i & 1;
       if (!mbar_wait_bounded(bars->tempty + buf, ((i >> 1) & 1) ^ 1, &bars->abort, lim, plan.st, 67) ||
-          !mbar_wait_bounded(bars->full + s, (i / NST) & 1, &bars->abort, lim, plan.st, 68))
+          !tc_stage_ready(bars, i, lim, plan.st, 68))
         break;
-      tc_fence_after();
       if (lane == 0) {
         const uint32_t b = b0 + (static_cast<uint32_t>(s * S::kStage) >> 4);
         // the small parts first
@@ -597,11 +600,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           ok = false;
           break;
         }
-        if (!mbar_wait_bounded(bars->full + s, (i / NST) & 1, &bars->abort, lim, plan.st, 72)) {
+        if (!tc_stage_ready(bars, i, lim, plan.st, 72)) {
           ok = false;
           break;
         }
-        tc_fence_after();
         const bool done = b % kFlush == kFlush - 1 || b + 1 == blocks;
         if (lane == 0) {
           const uint32_t so = static_cast<uint32_t>(s * S::kStage) >> 4;

@@ -17,6 +17,13 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// one of the barrier's expected arrivals, made when this thread's copies so far
+// have landed
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // four 8x8 matrices of 16-bit values; lane l gives the address of row l % 8 of
 // matrix l / 8; register j holds, of matrix j, row lane / 4, columns
 // 2 (lane % 4) and + 1 (transposed form: the same of its transpose)
