@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(kAdThreads)
   extern __shared__ __align__(16) uint8_t smem[];
   using S = ShrinkSmem<RP, WT>;
   chain_wait();
+  const int4 tile = __ldg(plan.tiles + blockIdx.x);  // (in bounds for every block, of use to the first ones)
   if (static_cast<int>(blockIdx.x) >= plan_tiles(plan)) return;
-  const int4 tile = plan.tiles[blockIdx.x];
   if (tile.x < 0) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nkb = (C + kBlockK - 1) / kBlockK, per = (nkb + splits - 1) / splits;
@@ -365,8 +365,8 @@ __global__ void __launch_bounds__(kAdThreads, RP <= 64 && !F32 ? 3 : 2)
   using S = ExpandSmem<RP, WT, F32>;
   constexpr int EB = F32 ? 4 : 2, PER = 16 / EB, PIECES = 64 / PER, PARTS = S::kParts;
   chain_wait();
+  const int4 tile = __ldg(plan.tiles + blockIdx.x);  // (in bounds for every block, of use to the first ones)
   if (static_cast<int>(blockIdx.x) >= plan_tiles(plan)) return;
-  const int4 tile = plan.tiles[blockIdx.x];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int first = blockIdx.y * steps * kTileCols, last = min(C, first + steps * kTileCols);
   if (first >= last) return;
@@ -808,6 +808,10 @@ int moe_adapter_bwd(const moe_adapter_config* cfg, const moe_bf16* dy, const moe
   MOE_RANK(c.r, e = launch_shrink<RP, true>(c, c.N, dy, B, pv, P, parts, &splits, s));
   if (e != cudaSuccess) return status_from_cuda(e);
   record_stage(s, 46, 1);
+  // dB reads dy again while much of it is still in L2
+  MOE_RANK(c.r, e = launch_wgrad<RP, true>(c, c.N, dy, u_saved, pv, dB, partial, s));
+  if (e != cudaSuccess) return status_from_cuda(e);
+  record_stage(s, 48, 2);
   if (c.out_fp32)
     MOE_RANK(c.r, e = launch_expand<RP, true, true>(c, c.K, parts, splits, scale, A, pv, P, dx_base, dx, du, s));
   else
@@ -815,9 +819,6 @@ int moe_adapter_bwd(const moe_adapter_config* cfg, const moe_bf16* dy, const moe
   if (e != cudaSuccess) return status_from_cuda(e);
   record_stage(s, 47, 1);
   MOE_RANK(c.r, e = launch_wgrad<RP, false>(c, c.K, x, du, pv, dA, partial, s));
-  if (e != cudaSuccess) return status_from_cuda(e);
-  record_stage(s, 48, 2);
-  MOE_RANK(c.r, e = launch_wgrad<RP, true>(c, c.N, dy, u_saved, pv, dB, partial, s));
   record_stage(s, 48, 2);
   return status_from_cuda(e);
 }

@@ -39,8 +39,8 @@ constexpr int kPlanMagic = 0x706c616f;
 // the number of tiles (of 64 rows, or 128 with `big`); 0, and a device error, for
 // a plan of another batch size or number of adapters or a buffer that holds none
 __device__ __forceinline__ int plan_tiles(const PlanView& p, bool big = false) {
-  const int4 h = __ldg(p.hdr);
-  if (h.y == p.T && h.z == p.L && h.w == kPlanMagic) return big ? __ldg(p.hdr + 1).x : h.x;
+  const int4 h = __ldg(p.hdr), h2 = __ldg(p.hdr + 1);
+  if (h.y == p.T && h.z == p.L && h.w == kPlanMagic) return big ? h2.x : h.x;
   set_status(p.st, MOE_ERR_DEVICE_INDEX, 61);
   return 0;
 }
@@ -155,8 +155,8 @@ __global__ void __launch_bounds__(kTcThreads, RP <= 64 ? 2 : 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto* bars = reinterpret_cast<TcBars<NST>*>(smem + NST * S::kStage);
   chain_wait();
+  const int4 tile = __ldg(plan.big + blockIdx.x);  // (in bounds for every block, of use to the first ones)
   if (static_cast<int>(blockIdx.x) >= plan_tiles(plan, true)) return;
-  const int4 tile = plan.big[blockIdx.x];
   if (tile.x < 0) return;
   const int warp = warp_id(), lane = lane_id();
   const int nkb = (C + 63) / 64, per = (nkb + splits - 1) / splits;
@@ -296,8 +296,8 @@ __global__ void __launch_bounds__(kTcThreads, TcExpand<RP, WT, F32>::kBlocks)
   auto* bars = reinterpret_cast<TcBars<NST>*>(smem + S::kU + NST * S::kStage);
   int* s_tok = reinterpret_cast<int*>(bars + 1);
   chain_wait();
+  const int4 tile = __ldg(plan.big + blockIdx.x);  // (in bounds for every block, of use to the first ones)
   if (static_cast<int>(blockIdx.x) >= plan_tiles(plan, true)) return;
-  const int4 tile = plan.big[blockIdx.x];
   const int first = blockIdx.y * steps * NC, last = min(C, first + steps * NC);
   if (first >= last) return;
   const int warp = warp_id(), lane = lane_id();
@@ -392,34 +392,45 @@ __global__ void __launch_bounds__(kTcThreads, TcExpand<RP, WT, F32>::kBlocks)
       __syncwarp();
     }
   } else {
-    // u of this thread's row
+    // u of the tile: eight lanes a row of 64 (whole lines), all loads of two
+    // pieces in flight (a row a thread took 11 us of a block's 60)
     const int q = warp * 32 + lane;
     const bool live = q < tile.z;
     const float sc = scale[tile.x];
-    const float* up = parts + static_cast<size_t>(tile.y + (live ? q : 0)) * RP;
+    constexpr int U8 = RP / 8, kAtOnce = 2;
 #pragma unroll 1
-    for (int j = 0; j < RP; j += 8) {
-      float f[8];
+    for (int k0 = 0; k0 < U8; k0 += kAtOnce) {
+      float f[kAtOnce][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = 0.0f;
-      if (live) {
-        for (int s = 0; s < splits; ++s) {
-          const float4* w = reinterpret_cast<const float4*>(up + static_cast<size_t>(s) * T * RP + j);
-          const float4 x = w[0], y = w[1];
-          f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
-          f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int i = q + (k0 + k) * 128, row = i / U8, j = i % U8 * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[k][e] = 0.0f;
+        if (row < tile.z) {
+          const float* up = parts + static_cast<size_t>(tile.y + row) * RP + j;
+#pragma unroll 4
+          for (int s = 0; s < splits; ++s) {
+            const float4* w = reinterpret_cast<const float4*>(up + static_cast<size_t>(s) * T * RP);
+            const float4 x = __ldcg(w), y = __ldcg(w + 1);
+            f[k][0] += x.x; f[k][1] += x.y; f[k][2] += x.z; f[k][3] += x.w;
+            f[k][4] += y.x; f[k][5] += y.y; f[k][6] += y.z; f[k][7] += y.w;
+          }
         }
       }
-      __nv_bfloat16 part[3][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) split_bf16(f[e] * sc, part[0][e], part[1][e], part[2][e]);
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int i = q + (k0 + k) * 128, row = i / U8, j = i % U8 * 8;
+        __nv_bfloat16 part[3][8];
 #pragma unroll
-      for (int h = 0; h < 3; ++h) {
-        const uint4 v = *reinterpret_cast<const uint4*>(part[h]);
-        const int ak = h * RP + j;
-        if (h < S::kParts) *reinterpret_cast<uint4*>(smem + (ak / 64) * 16384 + swz(q, (ak % 64) / 8)) = v;
-        if (u_keep != nullptr && blockIdx.y == 0 && live)
-          *reinterpret_cast<uint4*>(u_keep + (static_cast<size_t>(h) * T + tile.y + q) * RP + j) = v;
+        for (int e = 0; e < 8; ++e) split_bf16(f[k][e] * sc, part[0][e], part[1][e], part[2][e]);
+#pragma unroll
+        for (int h = 0; h < 3; ++h) {
+          const uint4 v = *reinterpret_cast<const uint4*>(part[h]);
+          const int ak = h * RP + j;
+          if (h < S::kParts) *reinterpret_cast<uint4*>(smem + (ak / 64) * 16384 + swz(row, (ak % 64) / 8)) = v;
+          if (u_keep != nullptr && blockIdx.y == 0 && row < tile.z)
+            *reinterpret_cast<uint4*>(u_keep + (static_cast<size_t>(h) * T + tile.y + row) * RP + j) = v;
+        }
       }
     }
     fence_proxy_async_smem();
@@ -682,9 +693,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int ct = 0; ct < CT; ++ct) {
         const int row = ct * 128 + warp * 32 + lane, c = c0 + row;
         if (!whole) {
-          // [j][column]: a warp writes whole lines
+          // as G lies: [j][column] or [column][j]
 #pragma unroll
-          for (int j = 0; j < RP; ++j) slot[static_cast<size_t>(j) * S::kCols + row] = acc[ct][j];
+          for (int j = 0; j < RP; j += 4) {
+            if constexpr (OUT_T) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) slot[static_cast<size_t>(j + e) * S::kCols + row] = acc[ct][j + e];
+            } else {
+              *reinterpret_cast<float4*>(slot + static_cast<size_t>(row) * RP + j) =
+                  make_float4(acc[ct][j], acc[ct][j + 1], acc[ct][j + 2], acc[ct][j + 3]);
+            }
+          }
         } else if (c < C) {
           float* g = G + static_cast<size_t>(a) * C * r;
           if constexpr (OUT_T) {
@@ -716,7 +735,7 @@ __global__ void __launch_bounds__(256) adapter_wgrad_join(PlanView plan, int C, 
   constexpr int kCols = TcWgrad<RP>::kCols;
   chain_wait();
   const bool any = plan_tiles(plan) > 0;
-  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;  // of the C r values, columns running fastest
+  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;  // of the C r values, as G lies
   const int n = C * r, y = blockIdx.y;
   if (y >= run.runs) {
     for (int a = y - run.runs; a < plan.L; a += kZeroRows)
@@ -735,21 +754,16 @@ __global__ void __launch_bounds__(256) adapter_wgrad_join(PlanView plan, int C, 
   }
   const int lo = plan.seg[a], hi = plan.seg[a + 1];
   if (hi <= end || lo < y * run.rows || i >= n) return;
-  const int y1 = (hi - 1) / run.rows, j = i / C, c = i % C;
+  // four neighbours of G: columns c .. c + 3 of row j (OUT_T), or rows j .. j + 3 of column c
+  const int y1 = (hi - 1) / run.rows, j = OUT_T ? i / C : i % r, c = OUT_T ? i % C : i / r;
+  const size_t at = OUT_T ? static_cast<size_t>(j) * kCols + c % kCols : static_cast<size_t>(c % kCols) * RP + j;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k = y; k <= y1; ++k) {
     const float4 v = __ldcg(reinterpret_cast<const float4*>(
-        partial + ((static_cast<size_t>(2 * k + (k == y ? 1 : 0)) * col_tiles + c / kCols) * RP + j) * kCols + c % kCols));
+        partial + (static_cast<size_t>(2 * k + (k == y ? 1 : 0)) * col_tiles + c / kCols) * (RP * kCols) + at));
     s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
   }
-  float* g = G + static_cast<size_t>(a) * n;
-  if constexpr (OUT_T) {
-    *reinterpret_cast<float4*>(g + i) = s;
-  } else {
-    const float f[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) g[static_cast<size_t>(c + e) * r + j] = f[e];
-  }
+  *reinterpret_cast<float4*>(G + static_cast<size_t>(a) * n + i) = s;
 }
 
 }  // namespace moe
