@@ -629,7 +629,8 @@ static cudaError_t launch_shrink(const moe_adapter_config& c, int C, const void*
     const cudaError_t e = allow_smem<adapter_shrink_tc<RP, WT>>(sm);
     if (e != cudaSuccess) return e;
     *splits = shrink_splits_tc(c, C);
-    return launch_chained(adapter_shrink_tc<RP, WT>, dim3(P.max_big, *splits), kTcThreads, sm, s, x, w, pv, c.T, C, c.r,
+    return launch_chained(adapter_shrink_tc<RP, WT>, dim3(P.max_big, *splits),
+                          TcShrink<RP, WT>::R::kThreads, sm, s, x, w, pv, c.T, C, c.r,
                           *splits, parts, static_cast<uint64_t>(wait_limit_ns()));
   }
   constexpr int sm = ShrinkSmem<RP, WT>::kTotal;
@@ -654,7 +655,7 @@ static cudaError_t launch_expand(const moe_adapter_config& c, int C, const float
     const int cols = (C + S::NC - 1) / S::NC;
     const int ranges = std::max(1, std::min(cols, (S::kBlocks * kAdSMs + big_tiles(c) / 2) / big_tiles(c)));
     const int steps = (cols + ranges - 1) / ranges;
-    return launch_chained(adapter_expand_tc<RP, WT, F32>, dim3(P.max_big, (cols + steps - 1) / steps), kTcThreads,
+    return launch_chained(adapter_expand_tc<RP, WT, F32>, dim3(P.max_big, (cols + steps - 1) / steps), S::R::kThreads,
                           S::kTotal, s, parts, splits, scale, w, pv, c.T, C, c.r, steps, base, out, k,
                           static_cast<uint64_t>(wait_limit_ns()));
   }
@@ -679,7 +680,7 @@ static cudaError_t launch_wgrad(const moe_adapter_config& c, int C, const void* 
   int col_tiles;
   size_t floats;
   const RowRuns run = wgrad_runs(c, C, &col_tiles, &floats);
-  e = launch_chained(adapter_wgrad_tc<RP, OUT_T>, dim3(col_tiles, run.runs), kTcThreads, sm, s,
+  e = launch_chained(adapter_wgrad_tc<RP, OUT_T>, dim3(col_tiles, run.runs), TcWgrad<RP>::R::kThreads, sm, s,
                      static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(V), pv, c.T, C, c.r, run,
                      G, partial, static_cast<uint64_t>(wait_limit_ns()));
   if (e != cudaSuccess) return e;

@@ -6,10 +6,10 @@
 // tiles come by 16-byte cp.async copies written in the 128-byte swizzle that the
 // MMA's descriptors expect, not by TMA boxes.
 //
-// All three run nine warps: 0-3 epilogue (TMEM lane quarter = warp), 4 TMEM
-// owner and MMA issuer, 5-8 producers. A stage of operands is full when the
-// copies of the 128 producer threads have landed, empty again when the MMAs that
-// read it have completed.
+// Warps: first the epilogue's (TMEM lane quarter = warp % 4), then the TMEM owner
+// and MMA issuer, then the producers. A stage of operands is full when the copies
+// of all producer threads have landed, empty again when the MMAs that read it
+// have completed.
 //
 // fp32 accumulation in tensor memory cuts each addition at the accumulator's last
 // bit: measured against fp64 the sum of K products is too small by 1e-9 K of
@@ -22,9 +22,16 @@
 
 namespace moe {
 
-constexpr int kTcThreads = 288;
-constexpr int kTcProducers = 128;
 constexpr int kFlush = 8;
+// threads of a kernel's roles
+template <int EPI_WARPS, int PRODUCER_WARPS>
+struct TcRoles {
+  static constexpr int kOwner = EPI_WARPS;  // the MMA issuer's warp
+  static constexpr int kEpi = EPI_WARPS * 32;
+  static constexpr int kProducers = PRODUCER_WARPS * 32;
+  static constexpr int kFirstProducer = kEpi + 32;
+  static constexpr int kThreads = kFirstProducer + kProducers;
+};
 
 struct PlanView {
   const int4* hdr;       // {number of 64-row tiles, T, L, kPlanMagic}, {number of 128-row tiles, 0, 0, 0}
@@ -57,23 +64,23 @@ struct TcBars {
   uint32_t tmem;
   int abort;
 };
-template <int NST>
+template <class R, int NST>
 __device__ __forceinline__ void tc_init(TcBars<NST>* b, int empty_count, uint32_t tmem_cols) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {
-      mbar_init(b->full + s, kTcProducers);
+      mbar_init(b->full + s, R::kProducers);
       mbar_init(b->empty + s, empty_count);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(b->tfull + i, 1);
       mbar_init(b->tempty + i, 128);
     }
-    mbar_init(&b->ready, 128);
+    mbar_init(&b->ready, R::kThreads);
     mbar_init(&b->drain, 1);
     b->abort = 0;
     fence_barrier_init();
   }
-  if (warp_id() == 4) {
+  if (warp_id() == R::kOwner) {
     tmem_alloc(&b->tmem, tmem_cols);
     tmem_relinquish();
   }
@@ -83,11 +90,11 @@ __device__ __forceinline__ void tc_init(TcBars<NST>* b, int empty_count, uint32_
 }
 // Every thread ends here. After a wait that ran out the MMAs in flight are given
 // their (bounded) time before the tensor memory is freed.
-template <int NST>
+template <class R, int NST>
 __device__ __forceinline__ void tc_end(TcBars<NST>* b, uint32_t tmem_cols, uint64_t lim) {
   tc_fence_before();
   __syncthreads();
-  if (warp_id() == 4) {
+  if (warp_id() == R::kOwner) {
     tc_fence_after();
     if (*static_cast<volatile int*>(&b->abort)) {
       int zero = 0;
@@ -133,6 +140,7 @@ __device__ __forceinline__ bool tc_stage_ready(TcBars<NST>* b, int i, uint64_t l
 // ---------------------------------------------------------------------------
 template <int RP, bool WT>
 struct TcShrink {
+  using R = TcRoles<4, 4>;
   static constexpr int kX = 128 * 128;
   static constexpr int kW = WT ? RP * 128 : (RP + 63) / 64 * 8192;
   static constexpr int kStage = kX + kW;
@@ -146,10 +154,11 @@ struct TcShrink {
 // W_a is [C][r] (WT = false) or [r][C] (WT = true). Bound by the rows of X, read
 // once; W_a comes from L2 for every 128 rows.
 template <int RP, bool WT>
-__global__ void __launch_bounds__(kTcThreads, RP <= 64 ? 2 : 1)
+__global__ void __launch_bounds__(TcRoles<4, 4>::kThreads, RP <= 64 ? 2 : 1)
     adapter_shrink_tc(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ W, PlanView plan, int T,
                       int C, int r, int splits, float* __restrict__ parts, uint64_t lim) {
   using S = TcShrink<RP, WT>;
+  using R = typename S::R;
   constexpr int NST = S::NST;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -162,11 +171,11 @@ __global__ void __launch_bounds__(kTcThreads, RP <= 64 ? 2 : 1)
   const int nkb = (C + 63) / 64, per = (nkb + splits - 1) / splits;
   const int kb0 = blockIdx.y * per, kb1 = min(nkb, kb0 + per);
   const uint32_t base = smem_u32(smem);
-  tc_init(bars, 1, S::kTmem);
+  tc_init<R>(bars, 1, S::kTmem);
   const uint32_t tmem = bars->tmem;
 
-  if (warp >= 5) {
-    const int p = threadIdx.x - 160;
+  if (warp > R::kOwner) {
+    const int p = threadIdx.x - R::kFirstProducer;
     const __nv_bfloat16* Wa = W + static_cast<size_t>(tile.x) * C * r;
     const int c8 = p & 7;
     const __nv_bfloat16* row[8];
@@ -188,14 +197,14 @@ __global__ void __launch_bounds__(kTcThreads, RP <= 64 ? 2 : 1)
       }
       if constexpr (WT) {
 #pragma unroll
-        for (int i = p; i < RP * 8; i += kTcProducers) {
+        for (int i = p; i < RP * 8; i += R::kProducers) {
           const int j = i >> 3;
           const bool ok = in && j < r;
           cp_async16(sw + swz(j, c8), ok ? Wa + static_cast<size_t>(j) * C + c0 + c8 * 8 : W, ok);
         }
       } else {
 #pragma unroll
-        for (int i = p; i < 64 * (RP / 8); i += kTcProducers) {
+        for (int i = p; i < 64 * (RP / 8); i += R::kProducers) {
           const int k = i / (RP / 8), j8 = i % (RP / 8);
           const bool ok = c0 + k < C && j8 * 8 < r;
           cp_async16(sw + (j8 >> 3) * 8192 + swz(k, j8 & 7), ok ? Wa + static_cast<size_t>(c0 + k) * r + j8 * 8 : W, ok);
@@ -204,7 +213,7 @@ __global__ void __launch_bounds__(kTcThreads, RP <= 64 ? 2 : 1)
       ring.commit();
     }
     ring.end();
-  } else if (warp == 4) {
+  } else if (warp == R::kOwner) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, RP, false, !WT);
     const uint32_t hi = sdesc_hi_sw128(1024);
     const uint32_t a0 = sdesc_lo(base, 16), b0 = sdesc_lo(base + S::kX, WT ? 16 : 8192);
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(kTcThreads, RP <= 64 ? 2 : 1)
     }
   }
   chain_release();
-  tc_end(bars, S::kTmem, lim);
+  tc_end<R>(bars, S::kTmem, lim);
 }
 
 // ---------------------------------------------------------------------------
@@ -264,6 +273,9 @@ __global__ void __launch_bounds__(kTcThreads, RP <= 64 ? 2 : 1)
 // ---------------------------------------------------------------------------
 template <int RP, bool WT, bool F32>
 struct TcExpand {
+  // two sets of epilogue warps take the steps in turn (one set: 57 us for 16384 x
+  // 4096, a step's epilogue being longer than its bytes)
+  using R = TcRoles<8, 3>;
   static constexpr int kParts = F32 ? 3 : 2;  // of u: 2^-17 of it, or 2^-25 for an fp32 result
   static constexpr int NC = F32 ? 32 : 64;    // columns of a step: 128-byte lines of base and out
   static constexpr int kUChunks = (kParts * RP + 63) / 64;
@@ -285,11 +297,12 @@ struct TcExpand {
 // base and out. The blocks of the first columns keep u's three parts for the
 // weight gradients (u_keep: [3][T][RP]).
 template <int RP, bool WT, bool F32>
-__global__ void __launch_bounds__(kTcThreads, TcExpand<RP, WT, F32>::kBlocks)
+__global__ void __launch_bounds__(TcRoles<8, 3>::kThreads, TcExpand<RP, WT, F32>::kBlocks)
     adapter_expand_tc(const float* __restrict__ parts, int splits, const float* __restrict__ scale,
                       const __nv_bfloat16* __restrict__ W, PlanView plan, int T, int C, int r, int steps,
                       const void* base_in, void* out, __nv_bfloat16* __restrict__ u_keep, uint64_t lim) {
   using S = TcExpand<RP, WT, F32>;
+  using R = typename S::R;
   constexpr int NST = S::NST, NC = S::NC, EB = F32 ? 4 : 2, PER = 16 / EB, PIECES = NC / PER;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -307,7 +320,7 @@ __global__ void __launch_bounds__(kTcThreads, TcExpand<RP, WT, F32>::kBlocks)
     // rows without an adapter: the base as it is
     __syncthreads();
     const int vecs = (last - first) / PER;
-    for (int row = warp; row < tile.z; row += kTcThreads / 32) {
+    for (int row = warp; row < tile.z; row += R::kThreads / 32) {
       const size_t at = (static_cast<size_t>(s_tok[row]) * C + first) * EB;
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base_in) + at);
       uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + at);
@@ -316,15 +329,62 @@ __global__ void __launch_bounds__(kTcThreads, TcExpand<RP, WT, F32>::kBlocks)
     return;
   }
   const uint32_t sb = smem_u32(smem);
-  tc_init(bars, 1 + 128, S::kTmem);
+  tc_init<R>(bars, 1 + 128, S::kTmem);
   const uint32_t tmem = bars->tmem;
   const int n = (last - first + NC - 1) / NC;
+  // u of the tile, by every warp (the producers' first stages are on their way by
+  // then): neighbouring lanes along a row, whole lines, the loads of two pieces in
+  // flight. (A row a thread, four warps: 11 us of a block's 60.)
+  const auto build_u = [&]() {
+    const float sc = scale[tile.x];
+    constexpr int U8 = RP / 8, kItems = 128 * U8;
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < kItems; i0 += 2 * R::kThreads) {
+      float f[2][8];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = i0 + k * R::kThreads, row = i / U8, j = i % U8 * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[k][e] = 0.0f;
+        if (row < tile.z) {
+          const float* up = parts + static_cast<size_t>(tile.y + row) * RP + j;
+#pragma unroll 4
+          for (int s = 0; s < splits; ++s) {
+            const float4* w = reinterpret_cast<const float4*>(up + static_cast<size_t>(s) * T * RP);
+            const float4 x = __ldcg(w), y = __ldcg(w + 1);
+            f[k][0] += x.x; f[k][1] += x.y; f[k][2] += x.z; f[k][3] += x.w;
+            f[k][4] += y.x; f[k][5] += y.y; f[k][6] += y.z; f[k][7] += y.w;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = i0 + k * R::kThreads, row = i / U8, j = i % U8 * 8;
+        if (i >= kItems) break;
+        __nv_bfloat16 part[3][8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) split_bf16(f[k][e] * sc, part[0][e], part[1][e], part[2][e]);
+#pragma unroll
+        for (int h = 0; h < 3; ++h) {
+          const uint4 v = *reinterpret_cast<const uint4*>(part[h]);
+          const int ak = h * RP + j;
+          if (h < S::kParts) *reinterpret_cast<uint4*>(smem + (ak / 64) * 16384 + swz(row, (ak % 64) / 8)) = v;
+          if (u_keep != nullptr && blockIdx.y == 0 && row < tile.z)
+            *reinterpret_cast<uint4*>(u_keep + (static_cast<size_t>(h) * T + tile.y + row) * RP + j) = v;
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(&bars->ready);
+  };
 
-  if (warp >= 5) {
-    const int p = threadIdx.x - 160;
+  if (warp > R::kOwner) {
+    const int p = threadIdx.x - R::kFirstProducer;
     const __nv_bfloat16* Wa = W + static_cast<size_t>(tile.x) * C * r;
     // this thread's pieces of the base's rows: piece cp of rows p / PIECES + k kRowStep
-    constexpr int kRowStep = kTcProducers / PIECES, kRows = 128 / kRowStep;
+    constexpr int kWPieces = WT ? RP / 8 : NC / 8, kWRows = WT ? NC : RP, kWStep = R::kProducers / kWPieces;
+    const int wq = p % kWPieces;
+    constexpr int kRowStep = R::kProducers / PIECES, kRows = (128 + kRowStep - 1) / kRowStep;
     const int cp = p % PIECES;
     const uint8_t* from[kRows];
 #pragma unroll
@@ -339,21 +399,15 @@ __global__ void __launch_bounds__(kTcThreads, TcExpand<RP, WT, F32>::kBlocks)
       if (!ring.begin(lim, plan.st)) break;
       const uint32_t sw = sb + S::kU + ring.slot() * S::kStage, sy = sw + S::kW;
       const int c0 = first + i * NC;
-      if constexpr (WT) {
-#pragma unroll 4
-        for (int k = p; k < NC * (RP / 8); k += kTcProducers) {
-          const int c = k / (RP / 8), j8 = k % (RP / 8);
-          const bool ok = j8 * 8 < r && c0 + c < last;
-          cp_async16(sw + (j8 >> 3) * S::kWChunk + swz(c, j8 & 7),
-                     ok ? Wa + static_cast<size_t>(c0 + c) * r + j8 * 8 : W, ok);
-        }
-      } else {
-#pragma unroll 4
-        for (int k = p; k < RP * (NC / 8); k += kTcProducers) {
-          const int j = k / (NC / 8), c8 = k % (NC / 8);
-          const bool ok = j < r && c0 + c8 * 8 < last;
-          cp_async16(sw + (c8 >> 3) * S::kWChunk + swz(j, c8 & 7),
-                     ok ? Wa + static_cast<size_t>(j) * C + c0 + c8 * 8 : W, ok);
+      // W: piece wq of rows p / kWPieces + k kWStep (rows: columns of out, or ranks)
+#pragma unroll
+      for (int k = 0; k < (kWRows + kWStep - 1) / kWStep; ++k) {
+        const int row = p / kWPieces + k * kWStep;
+        if (row < kWRows) {
+          const bool ok = WT ? wq * 8 < r && c0 + row < last : row < r && c0 + wq * 8 < last;
+          const __nv_bfloat16* src = WT ? Wa + static_cast<size_t>(c0 + row) * r + wq * 8
+                                        : Wa + static_cast<size_t>(row) * C + c0 + wq * 8;
+          cp_async16(sw + (wq >> 3) * S::kWChunk + swz(row, wq & 7), ok ? src : W, ok);
         }
       }
       const bool in = c0 + cp * PER < last;
@@ -362,13 +416,16 @@ __global__ void __launch_bounds__(kTcThreads, TcExpand<RP, WT, F32>::kBlocks)
         if (in && from[k] != nullptr)
           cp_async16(sy + (p / PIECES + k * kRowStep) * S::kYRow + cp * 16, from[k] + static_cast<size_t>(c0) * EB, true);
       ring.commit();
+      if (i == min(n, NST) - 1) build_u();
     }
     ring.end();
-  } else if (warp == 4) {
+  } else if (warp == R::kOwner) {
     constexpr uint32_t idesc = idesc_bf16_f32(128, NC, false, !WT);
     const uint32_t hi = sdesc_hi_sw128(1024);
     const uint32_t a0 = sdesc_lo(sb, 16), b0 = sdesc_lo(sb + S::kU, WT ? 16 : S::kWChunk);
+    build_u();
     bool ok = mbar_wait_bounded(&bars->ready, 0, &bars->abort, lim, plan.st, 66);
+    fence_proxy_async_smem();
     for (int i = 0; i < n && ok; ++i) {
       const int s = i % NST, buf = i & 1;
       if (!mbar_wait_bounded(bars->tempty + buf, ((i >> 1) & 1) ^ 1, &bars->abort, lim, plan.st, 67) ||
@@ -392,104 +449,75 @@ __global__ void __launch_bounds__(kTcThreads, TcExpand<RP, WT, F32>::kBlocks)
       __syncwarp();
     }
   } else {
-    // u of the tile: eight lanes a row of 64 (whole lines), all loads of two
-    // pieces in flight (a row a thread took 11 us of a block's 60)
-    const int q = warp * 32 + lane;
-    const bool live = q < tile.z;
-    const float sc = scale[tile.x];
-    constexpr int U8 = RP / 8, kAtOnce = 2;
-#pragma unroll 1
-    for (int k0 = 0; k0 < U8; k0 += kAtOnce) {
-      float f[kAtOnce][8];
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const int i = q + (k0 + k) * 128, row = i / U8, j = i % U8 * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[k][e] = 0.0f;
-        if (row < tile.z) {
-          const float* up = parts + static_cast<size_t>(tile.y + row) * RP + j;
-#pragma unroll 4
-          for (int s = 0; s < splits; ++s) {
-            const float4* w = reinterpret_cast<const float4*>(up + static_cast<size_t>(s) * T * RP);
-            const float4 x = __ldcg(w), y = __ldcg(w + 1);
-            f[k][0] += x.x; f[k][1] += x.y; f[k][2] += x.z; f[k][3] += x.w;
-            f[k][4] += y.x; f[k][5] += y.y; f[k][6] += y.z; f[k][7] += y.w;
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const int i = q + (k0 + k) * 128, row = i / U8, j = i % U8 * 8;
-        __nv_bfloat16 part[3][8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) split_bf16(f[k][e] * sc, part[0][e], part[1][e], part[2][e]);
-#pragma unroll
-        for (int h = 0; h < 3; ++h) {
-          const uint4 v = *reinterpret_cast<const uint4*>(part[h]);
-          const int ak = h * RP + j;
-          if (h < S::kParts) *reinterpret_cast<uint4*>(smem + (ak / 64) * 16384 + swz(row, (ak % 64) / 8)) = v;
-          if (u_keep != nullptr && blockIdx.y == 0 && row < tile.z)
-            *reinterpret_cast<uint4*>(u_keep + (static_cast<size_t>(h) * T + tile.y + row) * RP + j) = v;
-        }
-      }
-    }
-    fence_proxy_async_smem();
-    mbar_arrive(&bars->ready);
-    for (int i = 0; i < n; ++i) {
+    build_u();
+    const int quarter = warp & 3;
+    const bool live = quarter * 32 + lane < tile.z;
+    for (int i = warp >> 2; i < n; i += 2) {
       const int s = i % NST, buf = i & 1, c0 = first + i * NC;
       if (!mbar_wait_bounded(bars->full + s, (i / NST) & 1, &bars->abort, lim, plan.st, 69) ||
           !mbar_wait_bounded(bars->tfull + buf, (i >> 1) & 1, &bars->abort, lim, plan.st, 70))
         break;
       tc_fence_after();
-      if (warp * 32 >= tile.z) {  // no rows for this warp
+      if (quarter * 32 >= tile.z) {  // no rows for this warp
         mbar_arrive(bars->tempty + buf);
         mbar_arrive(bars->empty + s);
         continue;
       }
-      uint8_t* sy = smem + S::kU + s * S::kStage + S::kW + warp * 32 * S::kYRow;
+      uint8_t* sy = smem + S::kU + s * S::kStage + S::kW + quarter * 32 * S::kYRow;
       uint8_t* mine = sy + lane * S::kYRow;
 #pragma unroll
       for (int j = 0; j < NC; j += 32) {
         uint32_t v[32];
-        tmem_ld32(tmem + buf * NC + j + (static_cast<uint32_t>(warp) << 21), v);
+        tmem_ld32(tmem + buf * NC + j + (static_cast<uint32_t>(quarter) << 21), v);
+        // the row's pieces of the base, all asked for before the first is used
+        uint4 w[32 / PER];
+        uint4* y = reinterpret_cast<uint4*>(mine + j * EB);
+#pragma unroll
+        for (int e = 0; e < 32 / PER; ++e) w[e] = base_in != nullptr && live ? y[e] : make_uint4(0, 0, 0, 0);
         tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32 / PER; ++e) {
+          const uint32_t* a = v + e * PER;
+          if constexpr (F32) {
+            w[e].x = __float_as_uint(__uint_as_float(w[e].x) + __uint_as_float(a[0]));
+            w[e].y = __float_as_uint(__uint_as_float(w[e].y) + __uint_as_float(a[1]));
+            w[e].z = __float_as_uint(__uint_as_float(w[e].z) + __uint_as_float(a[2]));
+            w[e].w = __float_as_uint(__uint_as_float(w[e].w) + __uint_as_float(a[3]));
+          } else {
+            w[e].x = pack_bf16x2(bf16_lo(w[e].x) + __uint_as_float(a[0]), bf16_hi(w[e].x) + __uint_as_float(a[1]));
+            w[e].y = pack_bf16x2(bf16_lo(w[e].y) + __uint_as_float(a[2]), bf16_hi(w[e].y) + __uint_as_float(a[3]));
+            w[e].z = pack_bf16x2(bf16_lo(w[e].z) + __uint_as_float(a[4]), bf16_hi(w[e].z) + __uint_as_float(a[5]));
+            w[e].w = pack_bf16x2(bf16_lo(w[e].w) + __uint_as_float(a[6]), bf16_hi(w[e].w) + __uint_as_float(a[7]));
+          }
+        }
         if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; e += PER) {
-            uint4* y = reinterpret_cast<uint4*>(mine + (j + e) * EB);
-            uint4 w = base_in != nullptr ? *y : make_uint4(0, 0, 0, 0);
-            if constexpr (F32) {
-              w.x = __float_as_uint(__uint_as_float(w.x) + __uint_as_float(v[e]));
-              w.y = __float_as_uint(__uint_as_float(w.y) + __uint_as_float(v[e + 1]));
-              w.z = __float_as_uint(__uint_as_float(w.z) + __uint_as_float(v[e + 2]));
-              w.w = __float_as_uint(__uint_as_float(w.w) + __uint_as_float(v[e + 3]));
-            } else {
-              w.x = pack_bf16x2(bf16_lo(w.x) + __uint_as_float(v[e]), bf16_hi(w.x) + __uint_as_float(v[e + 1]));
-              w.y = pack_bf16x2(bf16_lo(w.y) + __uint_as_float(v[e + 2]), bf16_hi(w.y) + __uint_as_float(v[e + 3]));
-              w.z = pack_bf16x2(bf16_lo(w.z) + __uint_as_float(v[e + 4]), bf16_hi(w.z) + __uint_as_float(v[e + 5]));
-              w.w = pack_bf16x2(bf16_lo(w.w) + __uint_as_float(v[e + 6]), bf16_hi(w.w) + __uint_as_float(v[e + 7]));
-            }
-            *y = w;
-          }
+          for (int e = 0; e < 32 / PER; ++e) y[e] = w[e];
         }
       }
       tc_fence_before();
       mbar_arrive(bars->tempty + buf);
       __syncwarp();
       // whole lines of the warp's 32 rows
+      uint4 o[PIECES];
 #pragma unroll
       for (int k = 0; k < PIECES; ++k) {
         const int e = lane + 32 * k, row = e / PIECES, c = (e % PIECES) * PER;
-        if (warp * 32 + row < tile.z && c0 + c < last)
-          __stcs(reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) +
-                                          (static_cast<size_t>(s_tok[warp * 32 + row]) * C + c0 + c) * EB),
-                 *reinterpret_cast<const uint4*>(sy + row * S::kYRow + c * EB));
+        o[k] = *reinterpret_cast<const uint4*>(sy + row * S::kYRow + c * EB);
       }
       mbar_arrive(bars->empty + s);
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k) {
+        const int e = lane + 32 * k, row = e / PIECES, c = (e % PIECES) * PER;
+        if (quarter * 32 + row < tile.z && c0 + c < last)
+          __stcs(reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) +
+                                          (static_cast<size_t>(s_tok[quarter * 32 + row]) * C + c0 + c) * EB),
+                 o[k]);
+      }
     }
   }
   chain_release();
-  tc_end(bars, S::kTmem, lim);
+  tc_end<R>(bars, S::kTmem, lim);
 }
 
 // ---------------------------------------------------------------------------
@@ -497,6 +525,7 @@ __global__ void __launch_bounds__(kTcThreads, TcExpand<RP, WT, F32>::kBlocks)
 // ---------------------------------------------------------------------------
 template <int RP>
 struct TcWgrad {
+  using R = TcRoles<4, 7>;  // twelve warps have the registers of nine
   static constexpr int CT = RP <= 64 ? 2 : 1;           // 128-column tiles of X in a block
   static constexpr int kCols = CT * 128;
   static constexpr int kX = CT * 16384;
@@ -524,10 +553,11 @@ struct RowRuns {
 // so X is read from shared memory once for the three; their sums are added in the
 // epilogue, the small ones first. OUT_T: G_a is stored [r][C] (dB), else [C][r].
 template <int RP, bool OUT_T>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(TcRoles<4, 7>::kThreads, 1)
     adapter_wgrad_tc(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ V, PlanView plan, int T,
                      int C, int r, RowRuns run, float* __restrict__ G, float* __restrict__ partial, uint64_t lim) {
   using S = TcWgrad<RP>;
+  using R = typename S::R;
   constexpr int NST = S::NST, CT = S::CT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -540,16 +570,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int warp = warp_id(), lane = lane_id(), c0 = blockIdx.x * S::kCols;
   // the first adapter with rows behind P0
   int a0 = 0;
-  for (int i0 = 0; i0 < plan.L; i0 += kTcThreads) {
+  for (int i0 = 0; i0 < plan.L; i0 += R::kThreads) {
     const int i = i0 + static_cast<int>(threadIdx.x);
     a0 += __syncthreads_count(i < plan.L && plan.seg[i + 1] <= P0);
   }
   const uint32_t base = smem_u32(smem);
-  tc_init(bars, 1, S::kTmem);
+  tc_init<R>(bars, 1, S::kTmem);
   const uint32_t tmem = bars->tmem;
 
-  if (warp >= 5) {
-    const int p = threadIdx.x - 160, w = warp - 5;
+  if (warp > R::kOwner) {
+    const int p = threadIdx.x - R::kFirstProducer, w = warp - R::kOwner - 1;
     TcRing<NST> ring(bars);
     bool ok = true;
     // tokens of a block's rows, lane l those of rows l and l + 32, asked for one
@@ -569,31 +599,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         const uint32_t sx = base + ring.slot() * S::kStage, sv = sx + S::kX;
         // X: a warp copies 32 pieces of 16 bytes: 256 columns of a row, or 128 of two
-        constexpr int RPI = 32 / (16 * CT);  // rows at a time
+        constexpr int RPI = 32 / (16 * CT), kPW = R::kProducers / 32;
+        const int c8 = RPI == 2 ? lane & 15 : lane, c = c0 + c8 * 8;
 #pragma unroll
-        for (int i = 0; i < 16 / RPI; ++i) {
-          const int row = (w * (16 / RPI) + i) * RPI + (RPI == 2 ? lane >> 4 : 0);
-          const int c8 = RPI == 2 ? lane & 15 : lane, c = c0 + c8 * 8;
+        for (int i = 0; i < (64 / RPI + kPW - 1) / kPW; ++i) {
+          const int row = (w + i * kPW) * RPI + (RPI == 2 ? lane >> 4 : 0);
           const int tok = __shfl_sync(0xffffffffu, row < 32 ? t0 : t1, row & 31);
-          const bool in = row < n && c < C;
-          cp_async16(sx + (c8 >> 3) * 8192 + swz(row, c8 & 7), in ? X + static_cast<size_t>(tok) * C + c : X, in);
+          if (w + i * kPW < 64 / RPI) {
+            const bool in = row < n && c < C;
+            cp_async16(sx + (c8 >> 3) * 8192 + swz(row, c8 & 7), in ? X + static_cast<size_t>(tok) * C + c : X, in);
+          }
         }
+        constexpr int kPieces = 64 * (RP / 8);
 #pragma unroll
-        for (int k = 0; k < 64 * (RP / 8) / kTcProducers; ++k) {
-          const int i = p + k * kTcProducers, row = i / (RP / 8), j8 = i % (RP / 8);
-          const bool in = row < n;
-          const __nv_bfloat16* src = V + (in ? static_cast<size_t>(q0 + row) * RP + j8 * 8 : 0);
+        for (int k = 0; k < (kPieces + R::kProducers - 1) / R::kProducers; ++k) {
+          const int i = p + k * R::kProducers, row = i / (RP / 8), j8 = i % (RP / 8);
+          if (i < kPieces) {
+            const bool in = row < n;
+            const __nv_bfloat16* src = V + (in ? static_cast<size_t>(q0 + row) * RP + j8 * 8 : 0);
 #pragma unroll
-          for (int h = 0; h < 3; ++h) {
-            const int col8 = h * (RP / 8) + j8;
-            cp_async16(sv + (col8 >> 3) * 8192 + swz(row, col8 & 7), src + static_cast<size_t>(h) * T * RP, in);
+            for (int h = 0; h < 3; ++h) {
+              const int col8 = h * (RP / 8) + j8;
+              cp_async16(sv + (col8 >> 3) * 8192 + swz(row, col8 & 7), src + static_cast<size_t>(h) * T * RP, in);
+            }
           }
         }
         ring.commit();
       }
     }
     ring.end();
-  } else if (warp == 4) {
+  } else if (warp == R::kOwner) {
     constexpr int NI = S::kN <= 256 ? 1 : 3;  // instructions over N
     constexpr uint32_t idesc = idesc_bf16_f32(128, S::kN / NI, true, true);
     const uint32_t dhi = sdesc_hi_sw128(1024);
@@ -722,7 +757,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   }
   chain_release();
-  tc_end(bars, S::kTmem, lim);
+  tc_end<R>(bars, S::kTmem, lim);
 }
 
 // What the runs leave: blockIdx.y = y < runs: the adapter that begins in run y and
