@@ -2,6 +2,7 @@
 // batch gets base[t] + s_a (x[t] A_a) B_a of its own adapter a, and the
 // backward of that. Rows are ordered by adapter once for a batch (the plan);
 // every product then works on tiles of up to 64 rows of one adapter.
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -13,6 +14,7 @@ namespace moe {
 
 constexpr int kTileRows = 64;
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanChunks = 8;
 constexpr int kMaxAdapters = 1024;
 constexpr int kAdSMs = 152;
 
@@ -146,10 +148,30 @@ __global__ void __launch_bounds__(kPlanThreads)
   const int rank = __popc(peers & ((1u << lane) - 1u));
   if (key >= 0 && rank == 0) s_warp[warp][key] = static_cast<uint8_t>(__popc(peers));
   if (hist == nullptr) {
-    if (key >= 0 && rank == 0) atomicAdd(&s_first[key], __popc(peers));  // counts until the scan
+    // few chunks: every block counts them all (s_first holds counts until the scan)
+    for (int c0 = 0; c0 < chunks; c0 += 4) {
+      int a[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int tc = (c0 + u) * kPlanThreads + tid;
+        a[u] = tc < T ? idx[tc] : INT_MIN;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        bool b = false;
+        const int k = (c0 + u) * kPlanThreads + tid < T ? plan_key(a[u], L, b) : -1;
+        bad |= b;
+        const unsigned same = __match_any_sync(0xffffffffu, k);
+        if (k >= 0 && lane == __ffs(same) - 1) {
+          atomicAdd(&s_first[k], __popc(same));
+          if (c0 + u < me) atomicAdd(&s_before[k], __popc(same));
+        }
+      }
+    }
   } else {
     for (int i = tid; i < keys; i += kPlanThreads) {
       int n = 0, before = 0;
+#pragma unroll 8
       for (int c = 0; c < chunks; ++c) {
         const int h = hist[static_cast<size_t>(c) * (keys + 1) + i];
         before += c < me ? h : 0;
@@ -167,6 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   __syncthreads();
   if (key >= 0) {
     int pos = s_first[key] + s_before[key] + rank;
+#pragma unroll 8
     for (int w = 0; w < warp; ++w) pos += s_warp[w][key];
     order[pos] = t;
   }
@@ -547,21 +570,26 @@ static int check_adapter(const moe_adapter_config* c) {
 }
 static int padded_rank(int r) { return r <= 16 ? 16 : (r <= 32 ? 32 : (r <= 64 ? 64 : 128)); }
 
-// Splits of the long axis of a shrink: about four CTAs for each SM
+// Splits of the long axis of a shrink: three blocks for each SM, and no more than
+// the expanding product, whose every block adds them up, reads without loss (rank
+// 64, one adapter, 1024 rows: 32 splits 36.9 us, 12 20.0)
 static int shrink_splits(const moe_adapter_config& c, int C) {
   const int tiles = c.T / kTileRows + std::min(c.T, c.L);
   const int nkb = (C + kBlockK - 1) / kBlockK;
-  return std::max(1, std::min({4 * kAdSMs / tiles, nkb, 32}));
+  return std::max(1, std::min({3 * kAdSMs / tiles, nkb, 12}));
 }
 
-// Batches from 512 rows on take the tensor memory kernels; smaller ones, whose
-// adapters have a few rows each, tiles of 64 on mma.sync.
-constexpr int kTcRows = 512;
+// Batches from 2048 rows on take the tensor memory kernels, smaller ones tiles of
+// 64 rows on mma.sync. Forward, K = N = 4096, the two forms in us: 64 rows of 48
+// adapters, rank 16: tcgen05 17, mma.sync 9; 1024 rows of 8, rank 16: 17, 12; 2048
+// rows of 64, rank 64: 37, 43; 4096 rows of one, rank 64: 32, 46.
+constexpr int kTcRows = 2048;
 static int big_tiles(const moe_adapter_config& c) { return c.T / 128 + std::min(c.T, c.L); }
-// two CTAs for each SM
+// two blocks for each SM, at most four splits (as above: each is read again by
+// every block of the expanding product)
 static int shrink_splits_tc(const moe_adapter_config& c, int C) {
   const int nkb = (C + 63) / 64;
-  return std::max(1, std::min({2 * kAdSMs / big_tiles(c), nkb, 32}));
+  return std::max(1, std::min({2 * kAdSMs / big_tiles(c), nkb, 4}));
 }
 // Runs of rows of the weight gradients: together with the column tiles about one
 // block for each SM
@@ -653,7 +681,7 @@ static cudaError_t launch_expand(const moe_adapter_config& c, int C, const float
     if (e != cudaSuccess) return e;
     // about one wave of blocks, more only where there are more tiles
     const int cols = (C + S::NC - 1) / S::NC;
-    const int ranges = std::max(1, std::min(cols, (S::kBlocks * kAdSMs + big_tiles(c) / 2) / big_tiles(c)));
+    const int ranges = std::max(1, std::min({cols, 16, (S::kBlocks * kAdSMs + big_tiles(c) / 2) / big_tiles(c)}));
     const int steps = (cols + ranges - 1) / ranges;
     return launch_chained(adapter_expand_tc<RP, WT, F32>, dim3(P.max_big, (cols + steps - 1) / steps), S::R::kThreads,
                           S::kTotal, s, parts, splits, scale, w, pv, c.T, C, c.r, steps, base, out, k,
@@ -662,10 +690,10 @@ static cudaError_t launch_expand(const moe_adapter_config& c, int C, const float
   constexpr int sm = ExpandSmem<RP, WT, F32>::kTotal;
   const cudaError_t e = allow_smem<adapter_expand_kernel<RP, WT, F32>>(sm);
   if (e != cudaSuccess) return e;
-  // about six blocks for each SM (two or three run at a time, in even waves)
+  // about three blocks for each SM, as many as run at a time
   const int cols = (C + kTileCols - 1) / kTileCols;
   const int tiles = c.T / kTileRows + std::min(c.T, c.L);
-  const int ranges = std::max(1, std::min(cols, (6 * kAdSMs + tiles - 1) / tiles));
+  const int ranges = std::max(1, std::min(cols, (3 * kAdSMs + tiles - 1) / tiles));
   const int steps = (cols + ranges - 1) / ranges;
   return launch_chained(adapter_expand_kernel<RP, WT, F32>, dim3(P.max_tiles, (cols + steps - 1) / steps), kAdThreads,
                         sm, s, parts, splits, scale, w, pv, c.T, C, c.r, steps, base, out, k);
@@ -733,7 +761,9 @@ int moe_adapter_plan(const moe_adapter_config* cfg, const int32_t* adapter_idx, 
   uint8_t* b = static_cast<uint8_t*>(plan);
   DevStatus* ds = reinterpret_cast<DevStatus*>(b);
   int32_t* hist = reinterpret_cast<int32_t*>(b + L.hist);
-  if (L.chunks > 1) {
+  // up to kPlanChunks chunks the placing blocks count for themselves
+  const bool counted_first = L.chunks > kPlanChunks;
+  if (counted_first) {
     plan_hist_kernel<<<L.chunks, kPlanThreads, 0, s>>>(adapter_idx, c.T, c.L, hist);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return status_from_cuda(e);
@@ -743,18 +773,18 @@ int moe_adapter_plan(const moe_adapter_config* cfg, const int32_t* adapter_idx, 
   int4* tiles = reinterpret_cast<int4*>(b + L.tiles);
   int4* big = reinterpret_cast<int4*>(b + L.big);
   int32_t* order = reinterpret_cast<int32_t*>(b + L.order);
-  const int32_t* counted = L.chunks > 1 ? hist : nullptr;
+  const int32_t* counted = counted_first ? hist : nullptr;
   cudaError_t e = cudaSuccess;
-  if (L.chunks > 1) {
+  if (counted_first) {
     e = launch_chained(plan_place_kernel, L.chunks, kPlanThreads, 0, s, adapter_idx, c.T, c.L, L.chunks, counted, hdr,
                        seg, tiles, L.max_tiles, big, L.max_big, order, ds);
   } else {
-    plan_place_kernel<<<1, kPlanThreads, 0, s>>>(adapter_idx, c.T, c.L, 1, counted, hdr, seg, tiles, L.max_tiles, big,
-                                                 L.max_big, order, ds);
+    plan_place_kernel<<<L.chunks, kPlanThreads, 0, s>>>(adapter_idx, c.T, c.L, L.chunks, counted, hdr, seg, tiles,
+                                                        L.max_tiles, big, L.max_big, order, ds);
     e = cudaGetLastError();
   }
   const int rc = status_from_cuda(e);
-  record_stage(s, 45, L.chunks > 1 ? 2 : 1);
+  record_stage(s, 45, counted_first ? 2 : 1);
   return rc;
 }
 

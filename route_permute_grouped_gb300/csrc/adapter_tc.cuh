@@ -285,9 +285,9 @@ struct TcExpand {
   static constexpr int kYRow = NC * (F32 ? 4 : 2) + 16;
   static constexpr int kY = 128 * kYRow;
   static constexpr int kStage = (kW + kY + 1023) / 1024 * 1024;
-  static constexpr int NST = RP <= 64 ? 3 : 2;
+  static constexpr int NST = RP > 64 || (F32 && RP == 64) ? 2 : 3;
   static constexpr uint32_t kTmem = 2 * NC;
-  static constexpr int kBlocks = F32 || RP > 64 ? 1 : 2;  // resident on an SM
+  static constexpr int kBlocks = RP > 64 ? 1 : 2;  // resident on an SM
   static constexpr int kTotal = kU + NST * kStage + sizeof(TcBars<NST>) + 128 * 4 + 1024;
 };
 
@@ -469,30 +469,33 @@ __global__ void __launch_bounds__(TcRoles<8, 3>::kThreads, TcExpand<RP, WT, F32>
       for (int j = 0; j < NC; j += 32) {
         uint32_t v[32];
         tmem_ld32(tmem + buf * NC + j + (static_cast<uint32_t>(quarter) << 21), v);
-        // the row's pieces of the base, all asked for before the first is used
-        uint4 w[32 / PER];
         uint4* y = reinterpret_cast<uint4*>(mine + j * EB);
 #pragma unroll
-        for (int e = 0; e < 32 / PER; ++e) w[e] = base_in != nullptr && live ? y[e] : make_uint4(0, 0, 0, 0);
-        tmem_ld_wait();
+        for (int e0 = 0; e0 < 32 / PER; e0 += 4) {
+          // the row's pieces of the base, asked for before the first is used
+          uint4 w[4];
 #pragma unroll
-        for (int e = 0; e < 32 / PER; ++e) {
-          const uint32_t* a = v + e * PER;
-          if constexpr (F32) {
-            w[e].x = __float_as_uint(__uint_as_float(w[e].x) + __uint_as_float(a[0]));
-            w[e].y = __float_as_uint(__uint_as_float(w[e].y) + __uint_as_float(a[1]));
-            w[e].z = __float_as_uint(__uint_as_float(w[e].z) + __uint_as_float(a[2]));
-            w[e].w = __float_as_uint(__uint_as_float(w[e].w) + __uint_as_float(a[3]));
-          } else {
-            w[e].x = pack_bf16x2(bf16_lo(w[e].x) + __uint_as_float(a[0]), bf16_hi(w[e].x) + __uint_as_float(a[1]));
-            w[e].y = pack_bf16x2(bf16_lo(w[e].y) + __uint_as_float(a[2]), bf16_hi(w[e].y) + __uint_as_float(a[3]));
-            w[e].z = pack_bf16x2(bf16_lo(w[e].z) + __uint_as_float(a[4]), bf16_hi(w[e].z) + __uint_as_float(a[5]));
-            w[e].w = pack_bf16x2(bf16_lo(w[e].w) + __uint_as_float(a[6]), bf16_hi(w[e].w) + __uint_as_float(a[7]));
+          for (int e = 0; e < 4; ++e) w[e] = base_in != nullptr && live ? y[e0 + e] : make_uint4(0, 0, 0, 0);
+          if (e0 == 0) tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t* a = v + (e0 + e) * PER;
+            if constexpr (F32) {
+              w[e].x = __float_as_uint(__uint_as_float(w[e].x) + __uint_as_float(a[0]));
+              w[e].y = __float_as_uint(__uint_as_float(w[e].y) + __uint_as_float(a[1]));
+              w[e].z = __float_as_uint(__uint_as_float(w[e].z) + __uint_as_float(a[2]));
+              w[e].w = __float_as_uint(__uint_as_float(w[e].w) + __uint_as_float(a[3]));
+            } else {
+              w[e].x = pack_bf16x2(bf16_lo(w[e].x) + __uint_as_float(a[0]), bf16_hi(w[e].x) + __uint_as_float(a[1]));
+              w[e].y = pack_bf16x2(bf16_lo(w[e].y) + __uint_as_float(a[2]), bf16_hi(w[e].y) + __uint_as_float(a[3]));
+              w[e].z = pack_bf16x2(bf16_lo(w[e].z) + __uint_as_float(a[4]), bf16_hi(w[e].z) + __uint_as_float(a[5]));
+              w[e].w = pack_bf16x2(bf16_lo(w[e].w) + __uint_as_float(a[6]), bf16_hi(w[e].w) + __uint_as_float(a[7]));
+            }
           }
-        }
-        if (live) {
+          if (live) {
 #pragma unroll
-          for (int e = 0; e < 32 / PER; ++e) y[e] = w[e];
+            for (int e = 0; e < 4; ++e) y[e0 + e] = w[e];
+          }
         }
       }
       tc_fence_before();

@@ -106,17 +106,17 @@ def test_ranks(r):
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("r", [8, 16, 24, 32, 40, 64, 96, 128])
 def test_ranks_of_larger_batches(r, f32):
-    _compare(_inputs(600, 200, 328, 3, r, r, f32), _idx(600, 3, r), f32)
+    _compare(_inputs(2100, 200, 328, 3, r, r, f32), _idx(2100, 3, r), f32)
 
 
-@pytest.mark.parametrize("T,K,N,L,r", [(513, 1160, 648, 2, 16), (1500, 136, 2056, 1, 64), (3000, 72, 88, 700, 8),
-                                       (5000, 264, 40, 2, 32), (640, 2056, 1032, 5, 128)])
+@pytest.mark.parametrize("T,K,N,L,r", [(513, 1160, 648, 2, 16), (2500, 136, 2056, 1, 64), (3000, 72, 88, 700, 8),
+                                       (5000, 264, 40, 2, 32), (2050, 2056, 1032, 5, 128), (2300, 1160, 136, 1024, 24)])
 def test_long_axes_and_many_segments(T, K, N, L, r):
     # sums longer than an accumulator's turn, several runs of rows for an adapter, adapters of a few rows
     _compare(_inputs(T, K, N, L, r, T), _idx(T, L, T, none=0.02))
 
 
-@pytest.mark.parametrize("T", [511, 512, 513, 1024, 1025])
+@pytest.mark.parametrize("T", [1023, 1024, 1025, 2047, 2048, 2049])
 def test_both_forms_agree_at_their_border(T):
     idx = np.sort(_idx(T, 3, T, none=0.0))
     _compare(_inputs(T, 128, 128, 3, 16, T), idx)
@@ -211,7 +211,7 @@ def test_an_index_out_of_range_counts_as_none_and_is_reported():
     assert torch.equal(*ys)
 
 
-@pytest.mark.parametrize("T", [100, 3000])
+@pytest.mark.parametrize("T", [100, 3000, 20000])
 def test_graph_replay_with_another_batch(T):
     # plan, forward and backward captured once serve any batch of the size
     d = _inputs(T, 128, 192, 5, 32, 6)
@@ -275,3 +275,29 @@ def test_a_plan_of_another_batch_is_reported():
         ws, y = ops.adapter_workspace(cfg), c["base"].clone()
         ops.adapter_fwd(cfg, c["x"], c["A"], c["B"], c["scale"], plan, base=c["base"], y=y, ws=ws)
         assert ops.device_status(ws) == ops.MOE_ERR_DEVICE_INDEX and torch.equal(y, c["base"])
+
+
+@pytest.mark.parametrize("T,L", [(1, 1), (1024, 3), (8192, 1024), (8193, 7), (70000, 40)])
+def test_plan_orders_rows_by_adapter(T, L):
+    # the plan's order seen through rank-8 products with one-hot rows: each row gets its own adapter's
+    # constant, and the gradient of an adapter counts its rows
+    rng = np.random.default_rng(T)
+    idx = rng.integers(-1, L, T)
+    cfg = ops.make_adapter_config(T, 8, 8, L, 8, out_fp32=True)
+    x = torch.zeros((T, 8), dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1
+    A = torch.zeros((L, 8, 8), dtype=torch.bfloat16, device="cuda")
+    A[:, 0, 0] = 1
+    B = torch.zeros((L, 8, 8), dtype=torch.bfloat16, device="cuda")
+    B[:, 0, 0] = (torch.arange(L, device="cuda") % 32 + 1).to(torch.bfloat16)
+    B[:, 0, 1] = (torch.arange(L, device="cuda") // 32 + 1).to(torch.bfloat16)
+    plan = ops.adapter_plan(cfg, torch.from_numpy(idx.astype(np.int32)).cuda())
+    u = ops.alloc_adapter_saved(cfg)
+    y = ops.adapter_fwd(cfg, x, A, B, torch.ones(L, device="cuda"), plan, u=u).cpu().numpy()
+    want = np.where(idx[:, None] >= 0, np.stack([idx % 32 + 1, idx // 32 + 1], 1), 0)
+    assert np.array_equal(y[:, :2], want) and not y[:, 2:].any()
+    dy = torch.zeros((T, 8), dtype=torch.bfloat16, device="cuda")
+    dy[:, 3] = 1
+    g = ops.adapter_bwd(cfg, dy, x, A, B, torch.ones(L, device="cuda"), plan, u)
+    count = np.bincount(idx[idx >= 0], minlength=L)
+    assert np.array_equal(g["dB"][:, 0, 3].cpu().numpy(), count) and int(g["dB"].sum()) == count.sum()
