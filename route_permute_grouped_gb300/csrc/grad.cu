@@ -295,22 +295,39 @@ __global__ void __launch_bounds__(kGradThreads)
   }
 }
 
-template <int DT>
-__device__ __forceinline__ void scale_chunk(const uint4* __restrict__ v, uint4* __restrict__ o, long long vecs,
-                                            long long at, float coef) {
-  constexpr int PER = DT == MOE_FP32 ? 4 : 8;
+// A chunk of a tensor in the thread's registers
+struct Chunk {
+  GradItem it;
+  Span sp;
+  int dt, eb;
+  long long at;  // first vector
   uint4 w[kVecsPerThread];
+};
+template <int N>
+__device__ __forceinline__ void fetch(const GradBlock<N>& b, int c, Chunk& k) {
+  const int t = find_tensor(b, c);
+  k.it = b.item[t];
+  k.dt = b.dtype[t];
+  k.eb = k.dt == MOE_FP32 ? 4 : 2;
+  k.sp = span_of(k.it.in, k.it.n, k.eb);
+  k.at = static_cast<long long>(c - b.first[t]) * kChunkVecs;
+  const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(k.it.in) +
+                                                  static_cast<size_t>(k.sp.head) * k.eb);
 #pragma unroll
   for (int j = 0; j < kVecsPerThread; ++j) {
-    const long long i = at + j * kGradThreads + threadIdx.x;
-    if (i < vecs) w[j] = v[i];
+    const long long i = k.at + j * kGradThreads + threadIdx.x;
+    if (i < k.sp.vecs) k.w[j] = v[i];
   }
+}
+template <int DT>
+__device__ __forceinline__ void scale_chunk(const Chunk& k, uint4* __restrict__ o, float coef) {
+  constexpr int PER = DT == MOE_FP32 ? 4 : 8;
 #pragma unroll
   for (int j = 0; j < kVecsPerThread; ++j) {
-    const long long i = at + j * kGradThreads + threadIdx.x;
-    if (i < vecs) {
+    const long long i = k.at + j * kGradThreads + threadIdx.x;
+    if (i < k.sp.vecs) {
       float f[PER];
-      unpack<DT>(w[j], f);
+      unpack<DT>(k.w[j], f);
 #pragma unroll
       for (int e = 0; e < PER; ++e) f[e] *= coef;
       o[i] = pack<DT>(f);
@@ -320,44 +337,45 @@ __device__ __forceinline__ void scale_chunk(const uint4* __restrict__ v, uint4* 
 
 // g = round(g * coef), coef = min(1, max_norm / (norm + 1e-6)) (NaN for a NaN
 // norm). coef = 1 leaves every bit as it is, so tensors scaled in place are
-// then neither read nor written. The chunks go from the last one down: what the
-// norm's pass read last is what L2 still holds.
+// then neither read further nor written. The chunks go from the last one down:
+// what the norm's pass read last is what L2 still holds. A block's first chunk is
+// on its way while the norm's last block still adds up: the norm's kernel only
+// reads it.
 template <int N>
 __global__ void __launch_bounds__(kGradThreads) clip_kernel(const __grid_constant__ GradBlock<N> b,
                                                             const float* __restrict__ norm, float max_norm) {
+  const int grid = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
+  const bool any = first < b.chunks;
+  int i = any ? (b.chunks - 1 - first) / grid : 0;
+  Chunk k;
+  if (any) fetch(b, first + i * grid, k);
   chain_wait();
-  if (static_cast<int>(blockIdx.x) >= b.chunks) return;
   float coef = max_norm / (__ldcg(norm) + 1e-6f);
   if (coef > 1.0f) coef = 1.0f;
-  if (coef == 1.0f && !b.apart) return;
-  const int last = (b.chunks - 1 - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x);
-  for (int i = last; i >= 0; --i) {
-    const int c = blockIdx.x + i * gridDim.x, t = find_tensor(b, c);
-    const int dt = b.dtype[t];
-    const GradItem it = b.item[t];
-    if (coef == 1.0f && it.in == it.out) continue;
-    const int eb = dt == MOE_FP32 ? 4 : 2;
-    const Span sp = span_of(it.in, it.n, eb);
-    const long long at = static_cast<long long>(c - b.first[t]) * kChunkVecs;
-    const size_t skip = static_cast<size_t>(sp.head) * eb;
-    uint8_t* ob = static_cast<uint8_t*>(it.out) + skip;
-    if ((reinterpret_cast<uintptr_t>(ob) & 15u) == 0) {
-      const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(it.in) + skip);
-      uint4* o = reinterpret_cast<uint4*>(ob);
-      if (dt == MOE_FP32) scale_chunk<MOE_FP32>(v, o, sp.vecs, at, coef);
-      else if (dt == MOE_BF16) scale_chunk<MOE_BF16>(v, o, sp.vecs, at, coef);
-      else scale_chunk<MOE_FP16>(v, o, sp.vecs, at, coef);
-    } else {
-      // the output is aligned otherwise than the input: element by element
-      const int per = 16 / eb;
-      const long long end = min(sp.vecs, at + kChunkVecs) * per;
-      for (long long i = at * per + threadIdx.x; i < end; i += kGradThreads)
-        store_elem(it.out, sp.head + i, dt, elem_f32(it.in, sp.head + i, dt) * coef);
+  if (!any || (coef == 1.0f && !b.apart)) return;
+  while (true) {
+    if (coef != 1.0f || k.it.in != k.it.out) {
+      uint8_t* ob = static_cast<uint8_t*>(k.it.out) + static_cast<size_t>(k.sp.head) * k.eb;
+      if ((reinterpret_cast<uintptr_t>(ob) & 15u) == 0) {
+        uint4* o = reinterpret_cast<uint4*>(ob);
+        if (k.dt == MOE_FP32) scale_chunk<MOE_FP32>(k, o, coef);
+        else if (k.dt == MOE_BF16) scale_chunk<MOE_BF16>(k, o, coef);
+        else scale_chunk<MOE_FP16>(k, o, coef);
+      } else {
+        // the output is aligned otherwise than the input: element by element
+        const int per = 16 / k.eb;
+        const long long end = min(k.sp.vecs, k.at + kChunkVecs) * per;
+        for (long long e = k.at * per + threadIdx.x; e < end; e += kGradThreads)
+          store_elem(k.it.out, k.sp.head + e, k.dt, elem_f32(k.it.in, k.sp.head + e, k.dt) * coef);
+      }
+      const unsigned head = static_cast<unsigned>(k.sp.head);
+      if (k.at == 0 && threadIdx.x < head + k.sp.tail) {
+        const long long e = threadIdx.x < head ? threadIdx.x : k.it.n - k.sp.tail + (threadIdx.x - head);
+        store_elem(k.it.out, e, k.dt, elem_f32(k.it.in, e, k.dt) * coef);
+      }
     }
-    if (at == 0 && threadIdx.x < static_cast<unsigned>(sp.head + sp.tail)) {
-      const long long i = threadIdx.x < static_cast<unsigned>(sp.head) ? threadIdx.x : it.n - sp.tail + (threadIdx.x - sp.head);
-      store_elem(it.out, i, dt, elem_f32(it.in, i, dt) * coef);
-    }
+    if (--i < 0) return;
+    fetch(b, first + i * grid, k);
   }
 }
 

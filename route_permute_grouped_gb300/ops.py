@@ -791,9 +791,10 @@ def _arg(where, name, t, dtype, shape, optional=False):
     """A tensor argument of the calls below: on the current CUDA device,
     contiguous, of the given type (or one of them) and shape; its address."""
     if isinstance(t, torch.Tensor):
-        if ((t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)) and t.shape == shape and t.is_cuda
-                and t.get_device() == torch._C._cuda_getDevice() and t.is_contiguous()):
-            return t.data_ptr()
+        if ((t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)) and t.shape == shape and t.is_contiguous()):
+            d = t.get_device()  # -1: not on a GPU
+            if d >= 0 and d == torch._C._cuda_getDevice():
+                return t.data_ptr()
     elif t is None and optional:
         return None
     raise _arg_error(where, name, t, dtype if type(dtype) is tuple else (dtype,), shape)
