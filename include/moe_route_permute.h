@@ -634,13 +634,15 @@ int moe_adapter_plan(const moe_adapter_config* cfg, const int32_t* adapter_idx, 
                      void* stream);
 
 /* y from x, as above. base NULL: zeros; y may be base itself (rows without an
- * adapter are then not touched), otherwise the two must not overlap. u_saved
+ * adapter are then not touched); a y that overlaps base otherwise is
+ * MOE_ERR_INVALID_ARG. u_saved
  * (moe_adapter_saved_bytes, may be NULL) receives what the backward needs. */
 int moe_adapter_fwd(const moe_adapter_config* cfg, const moe_bf16* x, const moe_bf16* A, const moe_bf16* B,
                     const float* scale, const void* plan, const void* base, void* y, void* u_saved, void* ws,
                     size_t ws_bytes, void* stream);
 
-/* dx [T,K] (bf16, fp32 if out_fp32; dx_base as base above), dA [L,K,r] and
+/* dx [T,K] (bf16, fp32 if out_fp32; dx_base as base above; x and dy must not
+ * overlap dx: MOE_ERR_INVALID_ARG), dA [L,K,r] and
  * dB [L,r,N] fp32, given the forward's plan and u_saved. dy [T,N] bf16. */
 int moe_adapter_bwd(const moe_adapter_config* cfg, const moe_bf16* dy, const moe_bf16* x, const moe_bf16* A,
                     const moe_bf16* B, const float* scale, const void* plan, const void* u_saved,
@@ -729,7 +731,9 @@ void moe_debug_set_fault(int fault);
  * data gradient + SwiGLU backward, down weight gradient, gate/up data
  * gradient, gate/up weight gradient; 30 moe_read_ceiling, 31
  * moe_write_ceiling; 32 NVFP4 down data gradient (da), 33 NVFP4 SwiGLU
- * backward, 34 NVFP4 gate/up data gradient).
+ * backward, 34 NVFP4 gate/up data gradient; 40 gradient norm, 41 clipping, 43
+ * balance loss, 44 its backward, 45 adapter plan, 46-48 an adapter product: to
+ * rank r, from rank r, weight gradient).
  * moe_profile_stop() stops recording. moe_profile_read() waits for the events
  * and returns their number; ms[i] is the time from event i-1 to event i
  * (0 for call starts). moe_debug_launch_count() returns the number of kernels

@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       int n = 0, before = 0;
 #pragma unroll 8
       for (int c = 0; c < chunks; ++c) {
-        const int h = hist[static_cast<size_t>(c) * (keys + 1) + i];
+        const int h = __ldcg(hist + static_cast<size_t>(c) * (keys + 1) + i);
         before += c < me ? h : 0;
         n += h;
       }
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       }
     }
     if (hist != nullptr)
-      for (int c = tid; c < chunks; c += kPlanThreads) bad |= hist[static_cast<size_t>(c) * (keys + 1) + L + 1] != 0;
+      for (int c = tid; c < chunks; c += kPlanThreads) bad |= __ldcg(hist + static_cast<size_t>(c) * (keys + 1) + L + 1) != 0;
     bad = __syncthreads_or(bad);
     if (tid == 0) st->status = bad ? MOE_ERR_DEVICE_INDEX : MOE_OK;
   }
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kAdThreads)
   extern __shared__ __align__(16) uint8_t smem[];
   using S = ShrinkSmem<RP, WT>;
   chain_wait();
-  const int4 tile = __ldg(plan.tiles + blockIdx.x);  // (in bounds for every block, of use to the first ones)
+  const int4 tile = __ldcg(plan.tiles + blockIdx.x);  // (in bounds for every block, of use to the first ones)
   if (static_cast<int>(blockIdx.x) >= plan_tiles(plan)) return;
   if (tile.x < 0) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kAdThreads, RP <= 64 && !F32 ? 3 : 2)
   using S = ExpandSmem<RP, WT, F32>;
   constexpr int EB = F32 ? 4 : 2, PER = 16 / EB, PIECES = 64 / PER, PARTS = S::kParts;
   chain_wait();
-  const int4 tile = __ldg(plan.tiles + blockIdx.x);  // (in bounds for every block, of use to the first ones)
+  const int4 tile = __ldcg(plan.tiles + blockIdx.x);  // (in bounds for every block, of use to the first ones)
   if (static_cast<int>(blockIdx.x) >= plan_tiles(plan)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int first = blockIdx.y * steps * kTileCols, last = min(C, first + steps * kTileCols);
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kAdThreads, RP <= 64 && !F32 ? 3 : 2)
     if (row < tile.z) {
       const float* p = parts + static_cast<size_t>(tile.y + row) * RP + j;
       for (int s = 0; s < splits; ++s) {
-        const float4 w = *reinterpret_cast<const float4*>(p + static_cast<size_t>(s) * T * RP);
+        const float4 w = __ldcg(reinterpret_cast<const float4*>(p + static_cast<size_t>(s) * T * RP));
         v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
       }
     }
@@ -716,6 +716,11 @@ static cudaError_t launch_wgrad(const moe_adapter_config& c, int C, const void* 
                         C, c.r, run, col_tiles, G, static_cast<const float*>(partial));
 }
 
+// two arrays of `a_bytes` and `b_bytes` that share memory
+static bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + b_bytes && y < x + a_bytes;
+}
 static bool any_misaligned(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0) return true;
@@ -797,6 +802,8 @@ int moe_adapter_fwd(const moe_adapter_config* cfg, const moe_bf16* x, const moe_
   const moe_adapter_config& c = *cfg;
   if (!x || !A || !B || !scale || !plan || !y || !ws || any_misaligned({x, A, B, scale, plan, base, y, u_saved, ws}))
     return MOE_ERR_INVALID_ARG;
+  const size_t yb = static_cast<size_t>(c.T) * c.N * (c.out_fp32 ? 4 : 2);
+  if (base != y && overlap(base, yb, y, yb)) return MOE_ERR_INVALID_ARG;
   const AdapterWs L = adapter_ws(c, false);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -825,6 +832,11 @@ int moe_adapter_bwd(const moe_adapter_config* cfg, const moe_bf16* dy, const moe
   const moe_adapter_config& c = *cfg;
   if (!dy || !x || !A || !B || !scale || !plan || !u_saved || !dx || !dA || !dB || !ws ||
       any_misaligned({dy, x, A, B, scale, plan, u_saved, dx_base, dx, dA, dB, ws}))
+    return MOE_ERR_INVALID_ARG;
+  // dx is written before x is read for dA
+  const size_t xb = static_cast<size_t>(c.T) * c.K * (c.out_fp32 ? 4 : 2);
+  if ((dx_base != dx && overlap(dx_base, xb, dx, xb)) || overlap(x, 2 * static_cast<size_t>(c.T) * c.K, dx, xb) ||
+      overlap(dy, 2 * static_cast<size_t>(c.T) * c.N, dx, xb))
     return MOE_ERR_INVALID_ARG;
   const AdapterWs L = adapter_ws(c, true);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;

@@ -46,7 +46,7 @@ constexpr int kPlanMagic = 0x706c616f;
 // the number of tiles (of 64 rows, or 128 with `big`); 0, and a device error, for
 // a plan of another batch size or number of adapters or a buffer that holds none
 __device__ __forceinline__ int plan_tiles(const PlanView& p, bool big = false) {
-  const int4 h = __ldg(p.hdr), h2 = __ldg(p.hdr + 1);
+  const int4 h = __ldcg(p.hdr), h2 = __ldcg(p.hdr + 1);
   if (h.y == p.T && h.z == p.L && h.w == kPlanMagic) return big ? h2.x : h.x;
   set_status(p.st, MOE_ERR_DEVICE_INDEX, 61);
   return 0;
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(TcRoles<4, 4>::kThreads, RP <= 64 ? 2 : 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto* bars = reinterpret_cast<TcBars<NST>*>(smem + NST * S::kStage);
   chain_wait();
-  const int4 tile = __ldg(plan.big + blockIdx.x);  // (in bounds for every block, of use to the first ones)
+  const int4 tile = __ldcg(plan.big + blockIdx.x);  // (in bounds for every block, of use to the first ones)
   if (static_cast<int>(blockIdx.x) >= plan_tiles(plan, true)) return;
   if (tile.x < 0) return;
   const int warp = warp_id(), lane = lane_id();
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(TcRoles<8, 3>::kThreads, TcExpand<RP, WT, F32>
   auto* bars = reinterpret_cast<TcBars<NST>*>(smem + S::kU + NST * S::kStage);
   int* s_tok = reinterpret_cast<int*>(bars + 1);
   chain_wait();
-  const int4 tile = __ldg(plan.big + blockIdx.x);  // (in bounds for every block, of use to the first ones)
+  const int4 tile = __ldcg(plan.big + blockIdx.x);  // (in bounds for every block, of use to the first ones)
   if (static_cast<int>(blockIdx.x) >= plan_tiles(plan, true)) return;
   const int first = blockIdx.y * steps * NC, last = min(C, first + steps * NC);
   if (first >= last) return;

@@ -77,8 +77,28 @@ def test_adapter_pointers(lib):
     cfg = ops.make_adapter_config(64, 64, 64, 4, 16)
     _moved(lambda p: lib.moe_adapter_plan(ctypes.byref(cfg), *p, 16, None), 2)
     _moved(lambda p: lib.moe_adapter_fwd(ctypes.byref(cfg), *p, 16, None), 9, optional=(5, 7))
-    _moved(lambda p: lib.moe_adapter_bwd(ctypes.byref(cfg), *p, 16, None), 12, optional=(7,))
+    apart = lambda p: [P(None if q.value is None else q.value + (i << 24)) for i, q in enumerate(p)]
+    _moved(lambda p: lib.moe_adapter_bwd(ctypes.byref(cfg), *apart(p), 16, None), 12, optional=(7,))
     assert lib.moe_adapter_plan(None, P(4096), P(4096), 1 << 40, None) == BAD
+
+
+def test_adapter_refuses_overlapping_outputs(lib):
+    # y over a shifted base, dx over x, dy or a shifted dx_base; the small workspace stops what is allowed
+    cfg = ops.make_adapter_config(64, 64, 64, 4, 16)
+    nbytes = 64 * 64 * 2
+    def fwd(base, y):
+        p = [P(1 << 20)] * 9
+        p[5], p[6] = P(base), P(y)
+        return lib.moe_adapter_fwd(ctypes.byref(cfg), *p, 16, None)
+    assert fwd(1 << 16, 1 << 16) == SMALL and fwd(1 << 16, (1 << 16) + nbytes) == SMALL and fwd(None, 1 << 16) == SMALL
+    assert fwd(1 << 16, (1 << 16) + 16) == BAD and fwd((1 << 16) + nbytes - 16, 1 << 16) == BAD
+    def bwd(dy, x, dx_base, dx):
+        p = [P((i + 1) << 24) for i in range(12)]
+        p[0], p[1], p[7], p[8] = P(dy), P(x), P(dx_base), P(dx)
+        return lib.moe_adapter_bwd(ctypes.byref(cfg), *p, 16, None)
+    a, b, c, d = (i << 16 for i in (1, 2, 3, 4))
+    assert bwd(a, b, c, d) == SMALL and bwd(a, b, c, c) == SMALL and bwd(a, b, None, d) == SMALL
+    assert bwd(a, b, c, a) == BAD and bwd(a, b, c, b) == BAD and bwd(a, b, c, c + 32) == BAD and bwd(a, b, c, b + nbytes - 16) == BAD
 
 
 def _build(lib, items, n=None):
