@@ -605,7 +605,7 @@ static RowRuns wgrad_runs(const moe_adapter_config& c, int C, int* col_tiles, si
 }
 
 struct AdapterWs {
-  size_t parts, du, partial, total;
+  size_t parts, du, partial_a, partial_b, total;
 };
 static AdapterWs adapter_ws(const moe_adapter_config& c, bool training) {
   AdapterWs w{};
@@ -626,7 +626,8 @@ static AdapterWs adapter_ws(const moe_adapter_config& c, bool training) {
     size_t a, b;
     wgrad_runs(c, c.K, &tiles, &a);
     wgrad_runs(c, c.N, &tiles, &b);
-    w.partial = take(4 * std::max(a, b));
+    w.partial_a = take(4 * a);
+    w.partial_b = take(4 * b);
   }
   w.total = o;
   return w;
@@ -700,20 +701,22 @@ static cudaError_t launch_expand(const moe_adapter_config& c, int C, const float
 }
 
 template <int RP, bool OUT_T>
-static cudaError_t launch_wgrad(const moe_adapter_config& c, int C, const void* X, const void* V, const PlanView& pv,
-                                float* G, float* partial, cudaStream_t s) {
+static cudaError_t launch_wgrad(const moe_adapter_config& c, const WgradSide& side, const void* X, const void* V,
+                                const PlanView& pv, cudaStream_t s) {
   constexpr int sm = TcWgrad<RP>::kTotal;
-  cudaError_t e = allow_smem<adapter_wgrad_tc<RP, OUT_T>>(sm);
+  const cudaError_t e = allow_smem<adapter_wgrad_tc<RP, OUT_T>>(sm);
   if (e != cudaSuccess) return e;
-  int col_tiles;
-  size_t floats;
-  const RowRuns run = wgrad_runs(c, C, &col_tiles, &floats);
-  e = launch_chained(adapter_wgrad_tc<RP, OUT_T>, dim3(col_tiles, run.runs), TcWgrad<RP>::R::kThreads, sm, s,
-                     static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(V), pv, c.T, C, c.r, run,
-                     G, partial, static_cast<uint64_t>(wait_limit_ns()));
-  if (e != cudaSuccess) return e;
-  return launch_chained(adapter_wgrad_join<RP, OUT_T>, dim3((C * c.r + 1023) / 1024, run.runs + kZeroRows), 256, 0, s, pv,
-                        C, c.r, run, col_tiles, G, static_cast<const float*>(partial));
+  return launch_chained(adapter_wgrad_tc<RP, OUT_T>, dim3(side.col_tiles, side.run.runs), TcWgrad<RP>::R::kThreads, sm, s,
+                        static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(V), pv, c.T, c.r, side,
+                        static_cast<uint64_t>(wait_limit_ns()));
+}
+template <int RP>
+static cudaError_t launch_wgrad_join(const moe_adapter_config& c, const WgradSide& dA, const WgradSide& dB,
+                                     const PlanView& pv, cudaStream_t s) {
+  const int values = std::max(dA.C, dB.C) * c.r, runs = std::max(dA.run.runs, dB.run.runs);
+  const int zero_rows = std::min(c.L, 16);
+  return launch_chained(adapter_wgrad_join<RP>, dim3((values + kJoinValues - 1) / kJoinValues, runs + zero_rows, 2), 256,
+                        0, s, pv, c.r, zero_rows, dA, dB);
 }
 
 // two arrays of `a_bytes` and `b_bytes` that share memory
@@ -845,24 +848,31 @@ int moe_adapter_bwd(const moe_adapter_config* cfg, const moe_bf16* dy, const moe
   const PlanView pv = plan_view(c, plan, P, ws);
   float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.parts);
   void* du = static_cast<uint8_t*>(ws) + L.du;
-  float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.partial);
+  size_t floats;
+  WgradSide side_a{dA, reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.partial_a), c.K, 0, {}};
+  WgradSide side_b{dB, reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.partial_b), c.N, 0, {}};
+  side_a.run = wgrad_runs(c, c.K, &side_a.col_tiles, &floats);
+  side_b.run = wgrad_runs(c, c.N, &side_b.col_tiles, &floats);
   int splits = 1;
   cudaError_t e = cudaSuccess;
   MOE_RANK(c.r, e = launch_shrink<RP, true>(c, c.N, dy, B, pv, P, parts, &splits, s));
   if (e != cudaSuccess) return status_from_cuda(e);
   record_stage(s, 46, 1);
   // dB reads dy again while much of it is still in L2
-  MOE_RANK(c.r, e = launch_wgrad<RP, true>(c, c.N, dy, u_saved, pv, dB, partial, s));
+  MOE_RANK(c.r, e = launch_wgrad<RP, true>(c, side_b, dy, u_saved, pv, s));
   if (e != cudaSuccess) return status_from_cuda(e);
-  record_stage(s, 48, 2);
+  record_stage(s, 48, 1);
   if (c.out_fp32)
     MOE_RANK(c.r, e = launch_expand<RP, true, true>(c, c.K, parts, splits, scale, A, pv, P, dx_base, dx, du, s));
   else
     MOE_RANK(c.r, e = launch_expand<RP, true, false>(c, c.K, parts, splits, scale, A, pv, P, dx_base, dx, du, s));
   if (e != cudaSuccess) return status_from_cuda(e);
   record_stage(s, 47, 1);
-  MOE_RANK(c.r, e = launch_wgrad<RP, false>(c, c.K, x, du, pv, dA, partial, s));
-  record_stage(s, 48, 2);
+  MOE_RANK(c.r, e = launch_wgrad<RP, false>(c, side_a, x, du, pv, s));
+  if (e != cudaSuccess) return status_from_cuda(e);
+  record_stage(s, 48, 1);
+  MOE_RANK(c.r, e = launch_wgrad_join<RP>(c, side_a, side_b, pv, s));
+  record_stage(s, 48, 1);
   return status_from_cuda(e);
 }
 

@@ -547,6 +547,12 @@ struct TcWgrad {
 struct RowRuns {
   int rows, runs;
 };
+struct WgradSide {
+  float* G;
+  float* partial;
+  int C, col_tiles;
+  RowRuns run;
+};
 
 // G_a[c][j] = sum over the rows t of adapter a of X[t][c] V[position][j]. A block
 // takes kCols columns and one of equal runs of rows, whatever adapters lie in it;
@@ -558,10 +564,14 @@ struct RowRuns {
 template <int RP, bool OUT_T>
 __global__ void __launch_bounds__(TcRoles<4, 7>::kThreads, 1)
     adapter_wgrad_tc(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ V, PlanView plan, int T,
-                     int C, int r, RowRuns run, float* __restrict__ G, float* __restrict__ partial, uint64_t lim) {
+                     int r, WgradSide side, uint64_t lim) {
   using S = TcWgrad<RP>;
   using R = typename S::R;
   constexpr int NST = S::NST, CT = S::CT;
+  const int C = side.C;
+  const RowRuns run = side.run;
+  float* G = side.G;
+  float* partial = side.partial;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto* bars = reinterpret_cast<TcBars<NST>*>(smem + NST * S::kStage);
@@ -763,22 +773,30 @@ __global__ void __launch_bounds__(TcRoles<4, 7>::kThreads, 1)
   tc_end<R>(bars, S::kTmem, lim);
 }
 
-// What the runs leave: blockIdx.y = y < runs: the adapter that begins in run y and
-// goes on behind it, the sum of its partials run by run; from there on the adapters
-// without rows (every kZeroRows-th for one y), zeros. A block takes 1024 values.
-constexpr int kZeroRows = 16;
+// What the runs leave of dA (blockIdx.z = 0) and dB (1): for y = blockIdx.y < runs
+// the adapter that begins in run y and goes on behind it, the sum of its partials
+// run by run; from y = runs on the adapters without rows (every zero_rows-th for
+// one y), zeros. A block takes kJoinValues values: blocks of 1024 were twelve
+// thousand, most of them with nothing to do, and took 25 us. (Summed by the last
+// block of adapter_wgrad_tc to finish an adapter instead: 302 us for a step of 274.)
+constexpr int kJoinValues = 4096;
 template <int RP, bool OUT_T>
-__global__ void __launch_bounds__(256) adapter_wgrad_join(PlanView plan, int C, int r, RowRuns run, int col_tiles,
-                                                          float* __restrict__ G, const float* __restrict__ partial) {
+__device__ __forceinline__ void wgrad_join(const PlanView& plan, int r, int zero_rows, const WgradSide& side) {
   constexpr int kCols = TcWgrad<RP>::kCols;
-  chain_wait();
   const bool any = plan_tiles(plan) > 0;
-  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;  // of the C r values, as G lies
-  const int n = C * r, y = blockIdx.y;
+  const RowRuns run = side.run;
+  const int C = side.C, col_tiles = side.col_tiles;
+  float* G = side.G;
+  const float* partial = side.partial;
+  const int n = C * r, y = blockIdx.y;  // of the C r values, as G lies
+  const int first = blockIdx.x * kJoinValues + static_cast<int>(threadIdx.x) * 4, stop = min(n, first + kJoinValues);
+  if (static_cast<int>(blockIdx.x) * kJoinValues >= n) return;
   if (y >= run.runs) {
-    for (int a = y - run.runs; a < plan.L; a += kZeroRows)
-      if (i < n && (!any || plan.seg[a] == plan.seg[a + 1]))
-        *reinterpret_cast<float4*>(G + static_cast<size_t>(a) * n + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (y >= run.runs + zero_rows) return;
+    for (int a = y - run.runs; a < plan.L; a += zero_rows)
+      if (!any || plan.seg[a] == plan.seg[a + 1])
+        for (int i = first; i < stop; i += 1024)
+          *reinterpret_cast<float4*>(G + static_cast<size_t>(a) * n + i) = make_float4(0.f, 0.f, 0.f, 0.f);
     return;
   }
   if (!any) return;
@@ -791,17 +809,39 @@ __global__ void __launch_bounds__(256) adapter_wgrad_join(PlanView plan, int C, 
     a += __syncthreads_count(k < plan.L && plan.seg[k + 1] <= end - 1);
   }
   const int lo = plan.seg[a], hi = plan.seg[a + 1];
-  if (hi <= end || lo < y * run.rows || i >= n) return;
-  // four neighbours of G: columns c .. c + 3 of row j (OUT_T), or rows j .. j + 3 of column c
-  const int y1 = (hi - 1) / run.rows, j = OUT_T ? i / C : i % r, c = OUT_T ? i % C : i / r;
-  const size_t at = OUT_T ? static_cast<size_t>(j) * kCols + c % kCols : static_cast<size_t>(c % kCols) * RP + j;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = y; k <= y1; ++k) {
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(
-        partial + (static_cast<size_t>(2 * k + (k == y ? 1 : 0)) * col_tiles + c / kCols) * (RP * kCols) + at));
-    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  if (hi <= end || lo < y * run.rows) return;
+  const int y1 = (hi - 1) / run.rows;
+  constexpr int U = kJoinValues / 1024;
+  float4 s[U];
+  size_t at[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    // four neighbours of G: columns c .. c + 3 of row j (OUT_T), or rows j .. j + 3 of column c
+    const int i = min(first + u * 1024, n - 4);
+    const int j = OUT_T ? i / C : i % r, c = OUT_T ? i % C : i / r;
+    at[u] = static_cast<size_t>(c / kCols) * (RP * kCols) +
+            (OUT_T ? static_cast<size_t>(j) * kCols + c % kCols : static_cast<size_t>(c % kCols) * RP + j);
+    s[u] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  *reinterpret_cast<float4*>(G + static_cast<size_t>(a) * n + i) = s;
+  for (int k = y; k <= y1; ++k) {
+    const float* p = partial + static_cast<size_t>(2 * k + (k == y ? 1 : 0)) * col_tiles * (RP * kCols);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p + at[u]));
+      s[u].x += v.x; s[u].y += v.y; s[u].z += v.z; s[u].w += v.w;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (first + u * 1024 < n) *reinterpret_cast<float4*>(G + static_cast<size_t>(a) * n + first + u * 1024) = s[u];
+}
+
+template <int RP>
+__global__ void __launch_bounds__(256) adapter_wgrad_join(PlanView plan, int r, int zero_rows, WgradSide dA,
+                                                          WgradSide dB) {
+  chain_wait();
+  if (blockIdx.z == 0) wgrad_join<RP, false>(plan, r, zero_rows, dA);
+  else wgrad_join<RP, true>(plan, r, zero_rows, dB);
 }
 
 }  // namespace moe
