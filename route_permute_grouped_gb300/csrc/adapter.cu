@@ -14,7 +14,10 @@ namespace moe {
 
 constexpr int kTileRows = 64;
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanChunks = 8;
+// Chunks up to which the placing blocks count all rows themselves; beyond, a launch
+// of its own counts first (random rows of 40 adapters: 2000 rows 5.7 us both ways,
+// 8192 rows 10.6 us and 5.8)
+constexpr int kPlanChunks = 2;
 constexpr int kMaxAdapters = 1024;
 constexpr int kAdSMs = 152;
 
@@ -68,7 +71,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_hist_kernel(const int32_t* 
   __syncthreads();
   const int t = blockIdx.x * kPlanThreads + threadIdx.x;
   bool bad = false;
-  if (t < T) atomicAdd(&s_h[plan_key(idx[t], L, bad)], 1);
+  const int key = t < T ? plan_key(idx[t], L, bad) : -1;
+  const unsigned peers = __match_any_sync(0xffffffffu, key);  // one addition for a warp's equal keys
+  if (key >= 0 && (threadIdx.x & 31) == __ffs(peers) - 1) atomicAdd(&s_h[key], __popc(peers));
   bad = __syncthreads_or(bad);
   int32_t* row = hist + static_cast<size_t>(blockIdx.x) * (L + 2);
   for (int i = threadIdx.x; i <= L; i += kPlanThreads) row[i] = s_h[i];
@@ -769,7 +774,6 @@ int moe_adapter_plan(const moe_adapter_config* cfg, const int32_t* adapter_idx, 
   uint8_t* b = static_cast<uint8_t*>(plan);
   DevStatus* ds = reinterpret_cast<DevStatus*>(b);
   int32_t* hist = reinterpret_cast<int32_t*>(b + L.hist);
-  // up to kPlanChunks chunks the placing blocks count for themselves
   const bool counted_first = L.chunks > kPlanChunks;
   if (counted_first) {
     plan_hist_kernel<<<L.chunks, kPlanThreads, 0, s>>>(adapter_idx, c.T, c.L, hist);

@@ -277,7 +277,7 @@ def test_a_plan_of_another_batch_is_reported():
         assert ops.device_status(ws) == ops.MOE_ERR_DEVICE_INDEX and torch.equal(y, c["base"])
 
 
-@pytest.mark.parametrize("T,L", [(1, 1), (1024, 3), (8192, 1024), (8193, 7), (70000, 40)])
+@pytest.mark.parametrize("T,L", [(1, 1), (1024, 3), (2048, 1024), (2049, 7), (70000, 40)])
 def test_plan_orders_rows_by_adapter(T, L):
     # the plan's order seen through rank-8 products with one-hot rows: each row gets its own adapter's
     # constant, and the gradient of an adapter counts its rows
