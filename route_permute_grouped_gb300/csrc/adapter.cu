@@ -71,7 +71,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_hist_kernel(const int32_t* 
   __syncthreads();
   const int t = blockIdx.x * kPlanThreads + threadIdx.x;
   bool bad = false;
-  const int key = t < T ? plan_key(idx[t], L, bad) : -1;
+  chain_wait();
+  const int key = t < T ? plan_key(__ldcg(idx + t), L, bad) : -1;
   const unsigned peers = __match_any_sync(0xffffffffu, key);  // one addition for a warp's equal keys
   if (key >= 0 && (threadIdx.x & 31) == __ffs(peers) - 1) atomicAdd(&s_h[key], __popc(peers));
   bad = __syncthreads_or(bad);
@@ -147,8 +148,8 @@ __global__ void __launch_bounds__(kPlanThreads)
   __syncthreads();
   const int t = me * kPlanThreads + tid;
   bool bad = false;
-  const int key = t < T ? plan_key(idx[t], L, bad) : -1;
   chain_wait();
+  const int key = t < T ? plan_key(__ldcg(idx + t), L, bad) : -1;
   const unsigned peers = __match_any_sync(0xffffffffu, key);
   const int rank = __popc(peers & ((1u << lane) - 1u));
   if (key >= 0 && rank == 0) s_warp[warp][key] = static_cast<uint8_t>(__popc(peers));
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int tc = (c0 + u) * kPlanThreads + tid;
-        a[u] = tc < T ? idx[tc] : INT_MIN;
+        a[u] = tc < T ? __ldcg(idx + tc) : INT_MIN;
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -227,7 +228,6 @@ __global__ void __launch_bounds__(kPlanThreads)
 // ---------------------------------------------------------------------------
 constexpr int kAdThreads = 128;
 constexpr int kBlockK = 64;
-constexpr int kStages = 3;
 
 // Shared-memory rows are padded by 16 bytes: the eight rows of an 8x8 matrix
 // then lie in different banks.
@@ -238,6 +238,9 @@ struct ShrinkSmem {
   static constexpr int kX = kTileRows * kXRow * 2;
   static constexpr int kW = (WT ? RP : kBlockK) * kWRow * 2;
   static constexpr int kStage = kX + kW;
+  // three blocks of an SM with as many stages as fit: at small ranks a block of 64
+  // is gone in less than a load takes
+  static constexpr int kStages = RP <= 32 ? 5 : (RP == 64 ? 4 : 3);
   static constexpr int kTotal = kStages * kStage;
 };
 
@@ -300,17 +303,17 @@ __global__ void __launch_bounds__(kAdThreads)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
+  for (int s = 0; s < S::kStages - 1; ++s) {
     if (kb0 + s < kb1) load(kb0 + s, s);
     cp_async_commit();
   }
   int slot = 0;
   for (int kb = kb0; kb < kb1; ++kb) {
-    cp_async_wait<kStages - 2>();
+    cp_async_wait<S::kStages - 2>();
     __syncthreads();
     {
-      const int nxt = kb + kStages - 1;
-      if (nxt < kb1) load(nxt, (slot + kStages - 1) % kStages);
+      const int nxt = kb + S::kStages - 1;
+      if (nxt < kb1) load(nxt, (slot + S::kStages - 1) % S::kStages);
       cp_async_commit();
     }
     if (warp * 16 < tile.z) {
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(kAdThreads)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[n][i] += part[n][i];
     }
-    slot = (slot + 1) % kStages;
+    slot = (slot + 1) % S::kStages;
   }
   chain_release();
   cp_async_wait<0>();
@@ -371,7 +374,8 @@ struct ExpandSmem {
   static constexpr int kW = (WT ? kTileCols : RP) * kWRow * 2;
   static constexpr int kYRow = 64 * (F32 ? 4 : 2) + 16;  // bytes of a row of a warp's 32 x 64 block
   static constexpr int kY = 32 * kYRow;
-  static constexpr int kTotal = kParts * kU + 2 * kW + 2 * 4 * kY + 4 * kTileRows;
+  static constexpr int kBufs = RP <= 32 && !F32 ? 3 : 2;  // tiles of W and of the base on hand
+  static constexpr int kTotal = kParts * kU + kBufs * (kW + 4 * kY) + 4 * kTileRows;
 };
 
 // out[t][c] = base[t][c] + sum_j u[position][j] W_a[j][c], u = s_a sum over the
@@ -398,7 +402,7 @@ __global__ void __launch_bounds__(kAdThreads, RP <= 64 && !F32 ? 3 : 2)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int first = blockIdx.y * steps * kTileCols, last = min(C, first + steps * kTileCols);
   if (first >= last) return;
-  int* s_tok = reinterpret_cast<int*>(smem + PARTS * S::kU + 2 * S::kW + 8 * S::kY);
+  int* s_tok = reinterpret_cast<int*>(smem + PARTS * S::kU + S::kBufs * (S::kW + 4 * S::kY));
   if (tid < tile.z) s_tok[tid] = plan.order[tile.y + tid];
   __syncthreads();
   if (tile.x < 0) {
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(kAdThreads, RP <= 64 && !F32 ? 3 : 2)
   const uint32_t sb = smem_u32(smem);
   const int wm = (warp & 1) * 32, wn = (warp >> 1) * 64;
   const bool mine = wm < tile.z;  // this warp has rows
-  uint8_t* sy0 = smem + PARTS * S::kU + 2 * S::kW + warp * S::kY;
+  uint8_t* sy0 = smem + PARTS * S::kU + S::kBufs * S::kW + warp * S::kY;
   auto load = [&](int c0, int slot) {
     const uint32_t sw = sb + PARTS * S::kU + slot * S::kW;
     if constexpr (WT) {
@@ -447,9 +451,12 @@ __global__ void __launch_bounds__(kAdThreads, RP <= 64 && !F32 ? 3 : 2)
                      true);
       }
     }
-    cp_async_commit();
   };
-  load(first, 0);
+#pragma unroll
+  for (int b = 0; b < S::kBufs - 1; ++b) {
+    if (first + b * kTileCols < last) load(first + b * kTileCols, b);
+    cp_async_commit();
+  }
   // u of the tile's rows
   const float sc = scale[tile.x];
   for (int i = tid; i < kTileRows * (RP / 4); i += kAdThreads) {
@@ -457,9 +464,17 @@ __global__ void __launch_bounds__(kAdThreads, RP <= 64 && !F32 ? 3 : 2)
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row < tile.z) {
       const float* p = parts + static_cast<size_t>(tile.y + row) * RP + j;
-      for (int s = 0; s < splits; ++s) {
-        const float4 w = __ldcg(reinterpret_cast<const float4*>(p + static_cast<size_t>(s) * T * RP));
-        v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+      // six splits in flight: one load after the other took half of a small call
+      for (int s0 = 0; s0 < splits; s0 += 6) {
+        float4 w[6];
+#pragma unroll
+        for (int q = 0; q < 6; ++q)
+          w[q] = s0 + q < splits ? __ldcg(reinterpret_cast<const float4*>(p + static_cast<size_t>(s0 + q) * T * RP))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < 6; ++q) {
+          v.x += w[q].x; v.y += w[q].y; v.z += w[q].z; v.w += w[q].w;
+        }
       }
     }
     const float f[4] = {v.x * sc, v.y * sc, v.z * sc, v.w * sc};
@@ -488,10 +503,12 @@ __global__ void __launch_bounds__(kAdThreads, RP <= 64 && !F32 ? 3 : 2)
         for (int k = 0; k < RP / 16; ++k) u_frag(ua[h][m][k], h, m, 16 * k);
   }
   int slot = 0;
-  for (int c0 = first; c0 < last; c0 += kTileCols, slot ^= 1) {
-    cp_async_wait<0>();
+  for (int c0 = first; c0 < last; c0 += kTileCols, slot = slot + 1 == S::kBufs ? 0 : slot + 1) {
+    cp_async_wait<S::kBufs - 2>();
     __syncthreads();  // this step's tiles are here, the last step's have been read
-    if (c0 + kTileCols < last) load(c0 + kTileCols, slot ^ 1);
+    const int ahead = c0 + (S::kBufs - 1) * kTileCols;
+    if (ahead < last) load(ahead, slot == 0 ? S::kBufs - 1 : slot - 1);
+    cp_async_commit();
     if (!mine) continue;
     const uint32_t sw = sb + PARTS * S::kU + slot * S::kW;
     float acc[2][8][4];
@@ -776,8 +793,7 @@ int moe_adapter_plan(const moe_adapter_config* cfg, const int32_t* adapter_idx, 
   int32_t* hist = reinterpret_cast<int32_t*>(b + L.hist);
   const bool counted_first = L.chunks > kPlanChunks;
   if (counted_first) {
-    plan_hist_kernel<<<L.chunks, kPlanThreads, 0, s>>>(adapter_idx, c.T, c.L, hist);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_chained(plan_hist_kernel, L.chunks, kPlanThreads, 0, s, adapter_idx, c.T, c.L, hist);
     if (e != cudaSuccess) return status_from_cuda(e);
   }
   int4* hdr = reinterpret_cast<int4*>(b + L.hdr);
@@ -786,15 +802,8 @@ int moe_adapter_plan(const moe_adapter_config* cfg, const int32_t* adapter_idx, 
   int4* big = reinterpret_cast<int4*>(b + L.big);
   int32_t* order = reinterpret_cast<int32_t*>(b + L.order);
   const int32_t* counted = counted_first ? hist : nullptr;
-  cudaError_t e = cudaSuccess;
-  if (counted_first) {
-    e = launch_chained(plan_place_kernel, L.chunks, kPlanThreads, 0, s, adapter_idx, c.T, c.L, L.chunks, counted, hdr,
-                       seg, tiles, L.max_tiles, big, L.max_big, order, ds);
-  } else {
-    plan_place_kernel<<<L.chunks, kPlanThreads, 0, s>>>(adapter_idx, c.T, c.L, L.chunks, counted, hdr, seg, tiles,
-                                                        L.max_tiles, big, L.max_big, order, ds);
-    e = cudaGetLastError();
-  }
+  const cudaError_t e = launch_chained(plan_place_kernel, L.chunks, kPlanThreads, 0, s, adapter_idx, c.T, c.L, L.chunks,
+                                       counted, hdr, seg, tiles, L.max_tiles, big, L.max_big, order, ds);
   const int rc = status_from_cuda(e);
   record_stage(s, 45, counted_first ? 2 : 1);
   return rc;

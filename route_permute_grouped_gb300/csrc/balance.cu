@@ -75,14 +75,14 @@ __device__ __forceinline__ float side_sum(f2 v) {
 
 // `top`: the largest |logit| this lane has loaded so far
 template <int G, int NV, bool VEC>
-__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int gl, f2 (&v)[2 * NV], float& top) {
+__device__ __forceinline__ void load_row(const float* row, int E, int gl, f2 (&v)[2 * NV], float& top) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int e = 4 * (gl + G * j);
     float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     if constexpr (VEC) {
       if (e < E) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(row + e));
+        const float4 q = __ldcg(reinterpret_cast<const float4*>(row + e));
         x[0] = q.x; x[1] = q.y; x[2] = q.z; x[3] = q.w;
         top = fmaxf(fmaxf(top, fmaxf(fabsf(x[0]), fabsf(x[1]))), fmaxf(fabsf(x[2]), fabsf(x[3])));
       }
@@ -90,7 +90,7 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (e + i < E) {
-          x[i] = __ldg(row + e + i);
+          x[i] = row[e + i];
           top = fmaxf(top, fabsf(x[i]));
         }
     }
@@ -283,7 +283,7 @@ __device__ __forceinline__ void part_of_sequence(const BalParams& p, const BalCh
   const int32_t* idx = p.topk + static_cast<size_t>(ch.lo) * p.k;
   for (int i = tid; i < slots; i += kBalThreads) {
     if (p.mask != nullptr && p.mask[ch.lo + i / p.k] == 0) continue;
-    const int e = __ldg(idx + i);
+    const int e = __ldcg(idx + i);
     if (e < 0 || e >= p.E) set_status(p.st, MOE_ERR_DEVICE_INDEX, 50);
     else atomicAdd(&s_cnt[e], 1);
   }
@@ -376,6 +376,7 @@ __device__ __forceinline__ void part_of_sequence(const BalParams& p, const BalCh
 
 template <int G, int NV, bool VEC, bool SIG>
 __global__ void __launch_bounds__(kBalThreads, 4) balance_part_kernel(const BalParams p) {
+  chain_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
   const int lo = blockIdx.x * p.CH, hi = min(p.T, lo + p.CH);
   // the first sequence that ends behind the first row
@@ -405,8 +406,8 @@ __global__ void __launch_bounds__(32 * kBalJoinWarps) balance_join_kernel(const 
   __shared__ int s_last;
   const int s = blockIdx.x, cg = blockIdx.y, groups = gridDim.y, E = p.E;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = seq_begin(p.off, s, p.S, p.T), e = seq_begin(p.off, s + 1, p.S, p.T);
   chain_wait();
+  const int b = seq_begin(p.off, s, p.S, p.T), e = seq_begin(p.off, s + 1, p.S, p.T);
   if (tid == 0 && p.off != nullptr) {
     const int rb = p.off[s], re = p.off[s + 1];
     if (rb < 0 || re < rb || re > p.T) set_status(p.st, MOE_ERR_DEVICE_INDEX, 51);
@@ -531,9 +532,9 @@ constexpr int kBalBwdThreads = 256;
 constexpr int kBalBwdWarps = kBalBwdThreads / 32;
 template <int G, int NV, bool VEC, bool SIG>
 __global__ void __launch_bounds__(kBalBwdThreads, 4)
-    balance_bwd_kernel(const BalParams p, const float* __restrict__ dlosses, int rows_per_block,
-                       float* __restrict__ dlogits) {
+    balance_bwd_kernel(const BalParams p, const float* dlosses, int rows_per_block, float* dlogits) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  chain_wait();
   const int lo = static_cast<int>(min(static_cast<long long>(blockIdx.x) * rows_per_block, static_cast<long long>(p.T)));
   const int hi = static_cast<int>(min(static_cast<long long>(lo) + rows_per_block, static_cast<long long>(p.T)));
   // the last sequence that begins at or before the block's first row
@@ -625,10 +626,11 @@ __global__ void __launch_bounds__(kBalBwdThreads, 4)
 template <class F>
 static cudaError_t balance_dispatch(int E, bool sigmoid, F f) {
   const bool vec = E % 4 == 0;
+  cudaError_t e = cudaSuccess;
 #define MOE_BAL_SIG(G, NV, VEC)                                                                                  \
   do {                                                                                                           \
-    if (sigmoid) f(std::integral_constant<int, G>{}, std::integral_constant<int, NV>{}, VEC{}, std::true_type{}); \
-    else f(std::integral_constant<int, G>{}, std::integral_constant<int, NV>{}, VEC{}, std::false_type{});       \
+    if (sigmoid) e = f(std::integral_constant<int, G>{}, std::integral_constant<int, NV>{}, VEC{}, std::true_type{}); \
+    else e = f(std::integral_constant<int, G>{}, std::integral_constant<int, NV>{}, VEC{}, std::false_type{});       \
   } while (0)
 #define MOE_BAL(G, NV)                               \
   do {                                               \
@@ -643,7 +645,7 @@ static cudaError_t balance_dispatch(int E, bool sigmoid, F f) {
   else MOE_BAL(32, 2);
 #undef MOE_BAL
 #undef MOE_BAL_SIG
-  return cudaGetLastError();
+  return e;
 }
 
 static int check_balance(const moe_balance_config* c) {
@@ -758,8 +760,9 @@ int moe_balance_loss_fwd(const moe_balance_config* cfg, const float* logits, con
   p.stats = stats;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = balance_dispatch(c.E, p.sigmoid, [&](auto g, auto nv, auto vec, auto sig) {
-    balance_part_kernel<decltype(g)::value, decltype(nv)::value, decltype(vec)::value, decltype(sig)::value>
-        <<<L.blocks, kBalThreads, 0, s>>>(p);
+    return launch_chained(
+        balance_part_kernel<decltype(g)::value, decltype(nv)::value, decltype(vec)::value, decltype(sig)::value>,
+        L.blocks, kBalThreads, 0, s, p);
   });
   if (e != cudaSuccess) return status_from_cuda(e);
   // few, long sequences: a large block for each; many short ones: small blocks
@@ -788,8 +791,9 @@ int moe_balance_loss_bwd(const moe_balance_config* cfg, const float* logits, con
   const int rows = balance_block_rows(c.T);
   const int grid = (c.T + rows - 1) / rows;
   const cudaError_t e = balance_dispatch(c.E, p.sigmoid, [&](auto g, auto nv, auto vec, auto sig) {
-    balance_bwd_kernel<decltype(g)::value, decltype(nv)::value, decltype(vec)::value, decltype(sig)::value>
-        <<<grid, kBalBwdThreads, 0, s>>>(p, dlosses, rows, dlogits);
+    return launch_chained(
+        balance_bwd_kernel<decltype(g)::value, decltype(nv)::value, decltype(vec)::value, decltype(sig)::value>, grid,
+        kBalBwdThreads, 0, s, p, dlosses, rows, dlogits);
   });
   record_stage(s, 44, 1);
   return status_from_cuda(e);

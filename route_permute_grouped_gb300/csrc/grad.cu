@@ -163,13 +163,13 @@ struct Squares {
 };
 
 template <int DT>
-__device__ __forceinline__ void norm_chunk(const uint4* __restrict__ v, long long vecs, long long at, Squares& sq) {
+__device__ __forceinline__ void norm_chunk(const uint4* v, long long vecs, long long at, Squares& sq) {
   constexpr int PER = DT == MOE_FP32 ? 4 : 8;
   uint4 w[kVecsPerThread];
 #pragma unroll
   for (int j = 0; j < kVecsPerThread; ++j) {
     const long long i = at + j * kGradThreads + threadIdx.x;
-    w[j] = i < vecs ? __ldg(v + i) : make_uint4(0, 0, 0, 0);
+    w[j] = i < vecs ? __ldcg(v + i) : make_uint4(0, 0, 0, 0);
   }
   float f[kVecsPerThread * PER];
 #pragma unroll
@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kGradThreads)
     norm_kernel(const __grid_constant__ GradBlock<N> b, NormPartial* __restrict__ partials, int at_partial, int all,
                 int kind, int* __restrict__ ticket, float* __restrict__ norm) {
   Squares sq;
+  chain_wait();
   for (ChunkWalk<N> run(b, blockIdx.x); run.c < b.chunks; run.next(b, gridDim.x)) {
     const int c = run.c, t = run.t;
     const int dt = b.dtype[t];
@@ -316,7 +317,7 @@ __device__ __forceinline__ void fetch(const GradBlock<N>& b, int c, Chunk& k) {
 #pragma unroll
   for (int j = 0; j < kVecsPerThread; ++j) {
     const long long i = k.at + j * kGradThreads + threadIdx.x;
-    if (i < k.sp.vecs) k.w[j] = v[i];
+    if (i < k.sp.vecs) k.w[j] = __ldcg(v + i);
   }
 }
 template <int DT>
@@ -340,7 +341,7 @@ __device__ __forceinline__ void scale_chunk(const Chunk& k, uint4* __restrict__ 
 // then neither read further nor written. The chunks go from the last one down:
 // what the norm's pass read last is what L2 still holds. A block's first chunk is
 // on its way while the norm's last block still adds up: the norm's kernel only
-// reads it.
+// reads it, and has waited for all ahead of it.
 template <int N>
 __global__ void __launch_bounds__(kGradThreads) clip_kernel(const __grid_constant__ GradBlock<N> b,
                                                             const float* __restrict__ norm, float max_norm) {
@@ -383,6 +384,10 @@ template <int N>
 static auto clip_kernel_of(const GradBlock<N>*) {
   return clip_kernel<N>;
 }
+template <int N>
+static auto norm_kernel_of(const GradBlock<N>*) {
+  return norm_kernel<N>;
+}
 static int grad_grid(int chunks) { return std::max(1, std::min(chunks, std::min(4 * num_sms(), kMaxPartials))); }
 
 // launches `f` with the block in the smallest parameter size that holds it
@@ -422,9 +427,13 @@ static int run_norm(const GradList& l, int kind, float* norm, void* ws, cudaStre
   int at = 0;
   for (int i = 0; i < l.launches; ++i) {
     const int grid = grad_grid(l.block[i].chunks);
+    cudaError_t e2 = cudaSuccess;
     const cudaError_t e = with_block(l.block[i], [&](const auto& b) {
-      norm_kernel<<<grid, kGradThreads, 0, s>>>(b, partials, at, all, kind, ticket, norm);
+      using Block = std::remove_cv_t<std::remove_reference_t<decltype(b)>>;
+      e2 = launch_chained(norm_kernel_of(static_cast<const Block*>(nullptr)), grid, kGradThreads, 0, s, b, partials, at,
+                          all, kind, ticket, norm);
     });
+    if (e2 != cudaSuccess) return status_from_cuda(e2);
     if (e != cudaSuccess) return status_from_cuda(e);
     record_stage(s, 40, 1);
     at += grid;

@@ -301,3 +301,62 @@ def test_plan_orders_rows_by_adapter(T, L):
     g = ops.adapter_bwd(cfg, dy, x, A, B, torch.ones(L, device="cuda"), plan, u)
     count = np.bincount(idx[idx >= 0], minlength=L)
     assert np.array_equal(g["dB"][:, 0, 3].cpu().numpy(), count) and int(g["dB"].sum()) == count.sum()
+
+
+@pytest.mark.parametrize("T", [70, 2100])
+@pytest.mark.parametrize("before", ["kernel", "memset", "copy", "join"])
+def test_captured_behind_other_work(before, T):
+    # the calls' first kernels in a capture behind a torch kernel, a memset, a device copy, or the join of two
+    # streams; all of it must have finished before they read
+    d = _inputs(T, 128, 192, 3, 16, 6)
+    c = {k: v.cuda() for k, v in d.items()}
+    cfg = ops.make_adapter_config(T, 128, 192, 3, 16)
+    ix = torch.from_numpy(_idx(T, 3, 1).astype(np.int32)).cuda()
+    src_x, src_ix = c["x"].clone(), ix.clone()
+    big = torch.ones(1 << 26, device="cuda")       # long enough to be still running
+    plan, ws, y = ops.adapter_plan(cfg, ix), ops.adapter_workspace(cfg), torch.empty_like(c["base"])
+    want = ops.adapter_fwd(cfg, c["x"], c["A"], c["B"], c["scale"], plan, base=c["base"]).clone()
+    s, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def work():
+        big.mul_(1.0)
+        if before == "kernel":
+            torch.add(src_x, 0, out=c["x"])
+            torch.add(src_ix, 0, out=ix)
+        elif before == "memset":
+            torch.add(src_x, 0, out=c["x"])
+            ix.zero_()
+        elif before == "copy":
+            c["x"].copy_(src_x)
+            ix.copy_(src_ix)
+        else:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                big.mul_(1.0)
+                torch.add(src_x, 0, out=c["x"])
+            torch.add(src_ix, 0, out=ix)
+            torch.cuda.current_stream().wait_stream(side)
+        ops.adapter_plan(cfg, ix, plan=plan)
+        if before == "join":
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                big.mul_(1.0)
+            torch.cuda.current_stream().wait_stream(side)
+        ops.adapter_fwd(cfg, c["x"], c["A"], c["B"], c["scale"], plan, base=c["base"], y=y, ws=ws)
+
+    if before == "memset":
+        want = ops.adapter_fwd(cfg, src_x, c["A"], c["B"], c["scale"], ops.adapter_plan(cfg, torch.zeros_like(ix)), base=c["base"])
+    torch.cuda.synchronize()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        work()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        work()
+    for _ in range(3):
+        y.zero_(), c["x"].zero_(), ix.fill_(2)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
