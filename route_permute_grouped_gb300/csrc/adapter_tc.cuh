@@ -543,7 +543,8 @@ struct TcWgrad {
   static constexpr int kTotal = NST * kStage + sizeof(TcBars<NST>) + 1024;
 };
 
-// the rows of run y: positions [y rows, (y + 1) rows) of those with an adapter
+// the rows of run y: positions [y rows, (y + 1) rows) of those with an adapter;
+// rows = 0: those of adapter y
 struct RowRuns {
   int rows, runs;
 };
@@ -576,16 +577,29 @@ __global__ void __launch_bounds__(TcRoles<4, 7>::kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto* bars = reinterpret_cast<TcBars<NST>*>(smem + NST * S::kStage);
   chain_wait();
-  if (plan_tiles(plan) == 0) return;
-  const int live = plan.seg[plan.L];
-  const int P0 = blockIdx.y * run.rows, P1 = min(live, P0 + run.rows);
-  if (P0 >= P1) return;
+  const bool any = plan_tiles(plan) > 0;
   const int warp = warp_id(), lane = lane_id(), c0 = blockIdx.x * S::kCols;
-  // the first adapter with rows behind P0
-  int a0 = 0;
-  for (int i0 = 0; i0 < plan.L; i0 += R::kThreads) {
-    const int i = i0 + static_cast<int>(threadIdx.x);
-    a0 += __syncthreads_count(i < plan.L && plan.seg[i + 1] <= P0);
+  int P0, P1, a0 = 0;
+  if (run.rows == 0) {
+    a0 = blockIdx.y;
+    P0 = any ? plan.seg[a0] : 0;
+    P1 = any ? plan.seg[a0 + 1] : 0;
+    if (P0 >= P1) {  // no rows: zeros
+      float* g = G + static_cast<size_t>(a0) * C * r;
+      const int cols = min(S::kCols, C - c0);
+      for (int i = threadIdx.x; i < cols * r; i += R::kThreads)
+        g[OUT_T ? static_cast<size_t>(i / cols) * C + c0 + i % cols : static_cast<size_t>(c0) * r + i] = 0.0f;
+      return;
+    }
+  } else {
+    P0 = blockIdx.y * run.rows;
+    P1 = any ? min(plan.seg[plan.L], P0 + run.rows) : 0;
+    if (P0 >= P1) return;
+    // the first adapter with rows behind P0
+    for (int i0 = 0; i0 < plan.L; i0 += R::kThreads) {
+      const int i = i0 + static_cast<int>(threadIdx.x);
+      a0 += __syncthreads_count(i < plan.L && plan.seg[i + 1] <= P0);
+    }
   }
   const uint32_t base = smem_u32(smem);
   tc_init<R>(bars, 1, S::kTmem);
