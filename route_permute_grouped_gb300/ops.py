@@ -264,10 +264,10 @@ def _p(t):
     return c_void_p(t.data_ptr())
 
 
-def _stream():
+def _stream(_raw=torch._C._cuda_getCurrentRawStream, _device=torch._C._cuda_getDevice):
     """The current stream of the current device, as the library takes it (the
     raw handle: building a torch.cuda.Stream for it costs microseconds)."""
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _raw(_device())
 
 
 def _check(st, where):
@@ -787,16 +787,20 @@ def layer_bwd_nvfp4(cfg, dO, x, router_w, nvbw, saved, ws=None, grads=None, dlog
 # ---------------------------------------------------------------------------
 # Router losses with gradients
 # ---------------------------------------------------------------------------
-def _arg(where, name, t, dtype, shape, optional=False):
+def _arg(where, name, t, dtype, shape, optional=False, _device=torch._C._cuda_getDevice):
     """A tensor argument of the calls below: on the current CUDA device,
-    contiguous, of the given type (or one of them) and shape; its address."""
-    if isinstance(t, torch.Tensor):
-        if ((t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)) and t.shape == shape and t.is_contiguous()):
-            d = t.get_device()  # -1: not on a GPU
-            if d >= 0 and d == torch._C._cuda_getDevice():
-                return t.data_ptr()
-    elif t is None and optional:
+    contiguous, of the given type (or one of them) and shape; its address. What a
+    call spends here is most of its time on the host, so the usual case comes
+    first and asks as little as it can."""
+    if t is None and optional:
         return None
+    try:
+        if (t.dtype is dtype or (dtype.__class__ is tuple and t.dtype in dtype)) and t.shape == shape and t.is_contiguous():
+            d = t.get_device()  # -1: not on a GPU
+            if d >= 0 and d == _device():
+                return t.data_ptr()
+    except AttributeError:
+        pass
     raise _arg_error(where, name, t, dtype if type(dtype) is tuple else (dtype,), shape)
 
 
@@ -816,10 +820,9 @@ def _arg_error(where, name, t, dtypes, shape):
 def _ws_arg(where, ws, nbytes):
     if not isinstance(ws, torch.Tensor):
         raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: the workspace must be a uint8 tensor")
-    p = _arg(where, "the workspace", ws, torch.uint8, ws.shape)
     if ws.numel() < nbytes:
         raise MoeError(MOE_ERR_WORKSPACE_TOO_SMALL, where)
-    return p
+    return _arg(where, "the workspace", ws, torch.uint8, ws.shape)
 
 
 _size_cache = {}
@@ -879,7 +882,7 @@ def balance_loss_fwd(cfg, logits, topk_idx, seq_offsets=None, token_mask=None, w
     counts = torch.empty((cfg.n_seqs, cfg.E), dtype=torch.int32, device=dev)
     stats = torch.empty(n_stats, dtype=torch.float32, device=dev)
     ws = _scratch(n_ws, dev) if ws is None else ws
-    st = lib().moe_balance_loss_fwd(ctypes.byref(cfg), *args, _p(losses), _p(counts), _p(stats),
+    st = lib().moe_balance_loss_fwd(ctypes.byref(cfg), *args, losses.data_ptr(), counts.data_ptr(), stats.data_ptr(),
                                     _ws_arg(w, ws, n_ws), ws.numel(), _stream())
     _check(st, "moe_balance_loss_fwd")
     return losses, counts, stats
@@ -897,9 +900,11 @@ def balance_loss_bwd(cfg, logits, stats, dlosses=None, seq_offsets=None, token_m
             _arg(w, "seq_offsets", seq_offsets, torch.int32, (cfg.n_seqs + 1,), optional=True),
             _arg(w, "token_mask", token_mask, (torch.bool, torch.uint8), (cfg.T,), optional=True)]
     if dlogits is None:
-        dlogits = torch.empty((cfg.T, cfg.E), dtype=torch.float32, device=logits.device)
-    st = lib().moe_balance_loss_bwd(ctypes.byref(cfg), *args, _arg(w, "dlogits", dlogits, torch.float32,
-                                                                   (cfg.T, cfg.E)), _stream())
+        dlogits = torch.empty_like(logits)
+        dp = dlogits.data_ptr()
+    else:
+        dp = _arg(w, "dlogits", dlogits, torch.float32, (cfg.T, cfg.E))
+    st = lib().moe_balance_loss_bwd(ctypes.byref(cfg), *args, dp, _stream())
     _check(st, "moe_balance_loss_bwd")
     return dlogits
 
@@ -933,9 +938,12 @@ def adapter_plan(cfg, adapter_idx, plan=None):
     w = "adapter_plan"
     n = _size("moe_adapter_plan_bytes", cfg)
     idx = _arg(w, "adapter_idx", adapter_idx, torch.int32, (cfg.T,))
-    plan = torch.empty(n, dtype=torch.uint8, device=adapter_idx.device) if plan is None else plan
-    _check(lib().moe_adapter_plan(ctypes.byref(cfg), idx, _ws_arg(w, plan, n), plan.numel(), _stream()),
-           "moe_adapter_plan")
+    if plan is None:
+        plan = torch.empty(n, dtype=torch.uint8, device=adapter_idx.device)
+        pp = plan.data_ptr()
+    else:
+        pp = _ws_arg(w, plan, n)
+    _check(lib().moe_adapter_plan(ctypes.byref(cfg), idx, pp, plan.numel(), _stream()), "moe_adapter_plan")
     return plan
 
 
@@ -954,14 +962,17 @@ def adapter_fwd(cfg, x, A, B, scale, plan, base=None, y=None, u=None, ws=None):
     w = "adapter_fwd"
     xp = _arg(w, "x", x, torch.bfloat16, (cfg.T, cfg.K))
     weights = _adapter_args(w, cfg, A, B, scale, plan)
-    bp = _arg(w, "base", base, _out_dtype(cfg), (cfg.T, cfg.N), optional=True)
+    out = _out_dtype(cfg)
+    bp = _arg(w, "base", base, out, (cfg.T, cfg.N), optional=True)
     up = None if u is None else _ws_arg(w, u, _size("moe_adapter_saved_bytes", cfg))
     ws = adapter_workspace(cfg, False, x.device) if ws is None else ws
     wp = _ws_arg(w, ws, _size("moe_adapter_workspace_bytes", cfg, 0))
     if y is None:
-        y = torch.empty((cfg.T, cfg.N), dtype=_out_dtype(cfg), device=x.device)
-    st = lib().moe_adapter_fwd(ctypes.byref(cfg), xp, *weights, bp, _arg(w, "y", y, _out_dtype(cfg), (cfg.T, cfg.N)),
-                               up, wp, ws.numel(), _stream())
+        y = torch.empty_like(base) if base is not None else torch.empty((cfg.T, cfg.N), dtype=out, device=x.device)
+        yp = y.data_ptr()
+    else:
+        yp = _arg(w, "y", y, out, (cfg.T, cfg.N))
+    st = lib().moe_adapter_fwd(ctypes.byref(cfg), xp, *weights, bp, yp, up, wp, ws.numel(), _stream())
     _check(st, "moe_adapter_fwd")
     return y
 
