@@ -12,7 +12,8 @@ def router_probs(l, score):
         e = np.exp(l - l.max(1, keepdims=True))
         return e / e.sum(1, keepdims=True), np.ones_like(l)
     t = np.exp(-np.abs(l))
-    s = np.where(l >= 0, 1 / (1 + t), t / (1 + t))
+    s = np.minimum(l, 0) - np.log1p(t)  # log sigmoid: a row's sigmoids may all lie below the smallest number
+    s = np.exp(s - s.max(1, keepdims=True))
     return s / s.sum(1, keepdims=True), np.where(l >= 0, t / (1 + t), 1 / (1 + t))
 
 

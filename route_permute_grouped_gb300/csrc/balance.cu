@@ -125,13 +125,15 @@ __device__ __forceinline__ void group_sum2(float& a, float& b, int gl) {
 // the sum of the unnormalised scores times w.
 //
 // What bounds a row beside its bytes is its instructions (the first kernels: 36
-// an element, 113 us for 131021 x 256 sigmoid scores; these: 38 us) and the
+// an element, 113 us for 131021 x 256 sigmoid scores; these: 36 us) and the
 // special functions among them (16 a clock and SM). So m is 0 (NEAR) as long as no
 // logit of the warp's rows is beyond 40 in magnitude: no maximum is reduced, one
 // exponential x = exp(l) serves both scores, sigmoid(l) = x / (1 + x) and
 // 1 - sigmoid(l) = 1 / (1 + x) without cancellation, and the sum stays below
-// 256 e^40. Rows with larger logits take m = max l and exp(-|l|). exp is
-// exp2(x log2 e): the argument is off by half a step of itself, as l - m is.
+// 256 e^40. Rows with larger logits take m = max l and exp(-|l|); where m < 0 their
+// sigmoids exp(l) / (1 + exp(l)) come without the factor exp(m), which their sum
+// has too: below -88 it leaves fp32's range. exp is exp2(x log2 e): the argument
+// is off by half a step of itself, as l - m is.
 constexpr float kNear = 40.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -180,7 +182,8 @@ __device__ __forceinline__ void row_scores(int gl, f2 (&v)[kBalUnroll][2 * NV], 
           const float2 l = unpack2(l2);
           const float tx = __expf(-fabsf(l.x)), ty = __expf(-fabsf(l.y));
           const float rx = rcp_approx(1.0f + tx), ry = rcp_approx(1.0f + ty);
-          a = pack2(l.x >= 0.0f ? rx : tx * rx, l.y >= 0.0f ? ry : ty * ry);
+          const float2 q = unpack2(v[u][i]);  // (m < 0: no l is above 0)
+          a = pack2(l.x >= 0.0f ? rx : (m[u] < 0.0f ? q.x : tx) * rx, l.y >= 0.0f ? ry : (m[u] < 0.0f ? q.y : ty) * ry);
           b = pack2(l.x >= 0.0f ? tx * rx : rx, l.y >= 0.0f ? ty * ry : ry);
         }
         s[u][i] = BWD ? mul2(a, b) : a;
@@ -660,7 +663,7 @@ static int check_balance(const moe_balance_config* c) {
 }
 
 // Rows of a block: one wave of four blocks for each SM (blocks of half a wave more
-// than that took 70 us where one wave takes 39), whole passes of a block
+// than that took 70 us where one wave takes 36), whole passes of a block
 static int balance_block_rows(int T, int S) {
   const int want = (T + 4 * 152 - 1) / (4 * 152);
   // a block takes its sequences one after the other: short ones in smaller blocks

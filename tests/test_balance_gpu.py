@@ -133,6 +133,15 @@ def test_large_logits_do_not_overflow():
         assert np.isfinite(losses).all() and np.isfinite(d).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [6, 40, 200])
+def test_rows_of_very_small_or_large_scores(score, E):
+    # every sigmoid of a row below fp32's range, near its end, or 1
+    l, idx = _case(120, E, 3, 13)
+    l += np.array([-1000.0, -200.0, -95.0, -60.0, 0.0, 60.0, 500.0], np.float32)[np.arange(120) % 7][:, None]
+    _compare(l, idx, 3, score, [0, 50, 120])
+
+
 def test_default_gradients_and_no_z_loss():
     l, idx = _case(70, 8, 2, 8)
     cfg = ops.make_balance_config(70, 8, 2, balance_coeff=0.5)
