@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_hist_kernel(const int32_t* 
   const int t = blockIdx.x * kPlanThreads + threadIdx.x;
   bool bad = false;
   chain_wait();
+  chain_release();
   const int key = t < T ? plan_key(__ldcg(idx + t), L, bad) : -1;
   const unsigned peers = __match_any_sync(0xffffffffu, key);  // one addition for a warp's equal keys
   if (key >= 0 && (threadIdx.x & 31) == __ffs(peers) - 1) atomicAdd(&s_h[key], __popc(peers));
@@ -81,7 +82,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_hist_kernel(const int32_t* 
   int32_t* row = hist + static_cast<size_t>(blockIdx.x) * (L + 2);
   for (int i = threadIdx.x; i <= L; i += kPlanThreads) row[i] = s_h[i];
   if (threadIdx.x == 0) row[L + 1] = bad;
-  chain_release();
 }
 
 // exclusive scan of two values per key over s_a and s_b ([L + 1], in place) by
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   __syncthreads();
   const int t = me * kPlanThreads + tid;
   bool bad = false;
-  chain_wait();
+  if (hist == nullptr) chain_wait();  // the call's first kernel; else hist's launch is, which has waited
   const int key = t < T ? plan_key(__ldcg(idx + t), L, bad) : -1;
   const unsigned peers = __match_any_sync(0xffffffffu, key);
   const int rank = __popc(peers & ((1u << lane) - 1u));
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       }
     }
   } else {
+    chain_wait();
     for (int i = tid; i < keys; i += kPlanThreads) {
       int n = 0, before = 0;
 #pragma unroll 8
@@ -258,6 +259,7 @@ __global__ void __launch_bounds__(kAdThreads)
   extern __shared__ __align__(16) uint8_t smem[];
   using S = ShrinkSmem<RP, WT>;
   chain_wait();
+  chain_release();
   const int4 tile = __ldcg(plan.tiles + blockIdx.x);  // (in bounds for every block, of use to the first ones)
   if (static_cast<int>(blockIdx.x) >= plan_tiles(plan)) return;
   if (tile.x < 0) return;
@@ -349,7 +351,6 @@ __global__ void __launch_bounds__(kAdThreads)
     }
     slot = (slot + 1) % S::kStages;
   }
-  chain_release();
   cp_async_wait<0>();
   float* out = parts + (static_cast<size_t>(blockIdx.y) * T + tile.y) * RP;
 #pragma unroll
@@ -391,9 +392,10 @@ struct ExpandSmem {
 // own 32 x 64 piece of the output in whole 128-byte lines. The blocks of the
 // first columns keep u's three parts for the weight gradients (u_keep:
 // [3][T][RP]).
-// Base and out pass once, W_a comes from L2 once for every 64 rows; what bounds the
-// batches it serves is latency (64 rows of 48 adapters, N = 4096, rank 16: 7 MB in
-// 8.9 us; 1 row: 6.0 us).
+// W and base are asked for before the wait for the shrink, whose call's first kernel
+// has waited for them. Base and out pass once, W_a comes from L2 once for every 64
+// rows; what bounds the batches it serves is latency (64 rows of 48 adapters, N =
+// 4096, rank 16: 7 MB in 8.9 us; 1 row: 6.0 us).
 template <int RP, bool WT, bool F32>
 __global__ void __launch_bounds__(kAdThreads, RP <= 64 && !F32 ? 3 : 2)
     adapter_expand_kernel(const float* __restrict__ parts, int splits, const float* __restrict__ scale,
@@ -402,17 +404,20 @@ __global__ void __launch_bounds__(kAdThreads, RP <= 64 && !F32 ? 3 : 2)
   extern __shared__ __align__(16) uint8_t smem[];
   using S = ExpandSmem<RP, WT, F32>;
   constexpr int EB = F32 ? 4 : 2, PER = 16 / EB, PIECES = 64 / PER, PARTS = S::kParts;
-  chain_wait();
+  chain_release();
   const int4 tile = __ldcg(plan.tiles + blockIdx.x);  // (in bounds for every block, of use to the first ones)
-  if (static_cast<int>(blockIdx.x) >= plan_tiles(plan)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int first = blockIdx.y * steps * kTileCols, last = min(C, first + steps * kTileCols);
-  if (first >= last) return;
+  if (static_cast<int>(blockIdx.x) >= plan_tiles(plan) || first >= last) {
+    chain_wait();
+    return;
+  }
   int* s_tok = reinterpret_cast<int*>(smem + PARTS * S::kU + S::kBufs * (S::kW + 4 * S::kY));
   if (tid < tile.z) s_tok[tid] = plan.order[tile.y + tid];
   __syncthreads();
   if (tile.x < 0) {
     // rows without an adapter: the base as it is
+    chain_wait();
     if (base_in == out) return;
     const int vecs = (last - first) / PER;
     for (int row = warp; row < tile.z; row += kAdThreads / 32) {
@@ -465,6 +470,7 @@ __global__ void __launch_bounds__(kAdThreads, RP <= 64 && !F32 ? 3 : 2)
   }
   // u of the tile's rows
   const float sc = scale[tile.x];
+  chain_wait();
   for (int i = tid; i < kTileRows * (RP / 4); i += kAdThreads) {
     const int row = i / (RP / 4), j = (i % (RP / 4)) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -740,13 +746,13 @@ static cudaError_t launch_expand(const moe_adapter_config& c, int C, const float
 
 template <int RP, bool OUT_T>
 static cudaError_t launch_wgrad(const moe_adapter_config& c, const WgradSide& side, const void* X, const void* V,
-                                const PlanView& pv, cudaStream_t s) {
+                                const PlanView& pv, bool v_ready, cudaStream_t s) {
   constexpr int sm = TcWgrad<RP>::kTotal;
   const cudaError_t e = allow_smem<adapter_wgrad_tc<RP, OUT_T>>(sm);
   if (e != cudaSuccess) return e;
   return launch_chained(adapter_wgrad_tc<RP, OUT_T>, dim3(side.col_tiles, side.run.runs), TcWgrad<RP>::R::kThreads, sm, s,
                         static_cast<const __nv_bfloat16*>(X), static_cast<const __nv_bfloat16*>(V), pv, c.T, c.r, side,
-                        static_cast<uint64_t>(wait_limit_ns()));
+                        v_ready, static_cast<uint64_t>(wait_limit_ns()));
 }
 template <int RP>
 static cudaError_t launch_wgrad_join(const moe_adapter_config& c, const WgradSide& dA, const WgradSide& dB,
@@ -888,7 +894,7 @@ int moe_adapter_bwd(const moe_adapter_config* cfg, const moe_bf16* dy, const moe
   if (e != cudaSuccess) return status_from_cuda(e);
   record_stage(s, 46, 1);
   // dB reads dy again while much of it is still in L2
-  MOE_RANK(c.r, e = launch_wgrad<RP, true>(c, side_b, dy, u_saved, pv, s));
+  MOE_RANK(c.r, e = launch_wgrad<RP, true>(c, side_b, dy, u_saved, pv, true, s));
   if (e != cudaSuccess) return status_from_cuda(e);
   record_stage(s, 48, 1);
   if (c.out_fp32)
@@ -897,7 +903,7 @@ int moe_adapter_bwd(const moe_adapter_config* cfg, const moe_bf16* dy, const moe
     MOE_RANK(c.r, e = launch_expand<RP, true, false>(c, c.K, parts, splits, scale, A, pv, P, dx_base, dx, du, s));
   if (e != cudaSuccess) return status_from_cuda(e);
   record_stage(s, 47, 1);
-  MOE_RANK(c.r, e = launch_wgrad<RP, false>(c, side_a, x, du, pv, s));
+  MOE_RANK(c.r, e = launch_wgrad<RP, false>(c, side_a, x, du, pv, false, s));
   if (e != cudaSuccess) return status_from_cuda(e);
   record_stage(s, 48, 1);
   if (side_a.run.rows == 0) return status_from_cuda(e);

@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(TcRoles<4, 4>::kThreads, RP <= 64 ? 2 : 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto* bars = reinterpret_cast<TcBars<NST>*>(smem + NST * S::kStage);
   chain_wait();
+  chain_release();
   const int4 tile = __ldcg(plan.big + blockIdx.x);  // (in bounds for every block, of use to the first ones)
   if (static_cast<int>(blockIdx.x) >= plan_tiles(plan, true)) return;
   if (tile.x < 0) return;
@@ -266,7 +267,6 @@ __global__ void __launch_bounds__(TcRoles<4, 4>::kThreads, RP <= 64 ? 2 : 1)
       for (int j = 0; j < RP; j += 4) out[j / 4] = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
     }
   }
-  chain_release();
   tc_end<R>(bars, S::kTmem, lim);
 }
 
@@ -298,7 +298,10 @@ struct TcExpand {
 // against the same tile of W_a, [r][C] (WT = false) or [C][r] (WT = true). Bound by
 // base and out (16384 x 4096, rank 64: 268 MB in 54 us, 5.0 TB/s, against 47 to 52
 // for a tiled copy). The blocks of the first columns keep u's three parts for the
-// weight gradients (u_keep: [3][T][RP]).
+// weight gradients (u_keep: [3][T][RP]). What the caller passes (plan, W_a, base)
+// is on its way before the block waits for the kernel ahead, here and in the
+// weight gradients (mixed batch of 5003 rows, 40 adapters, rank 24, step 118 -> 109
+// us; one row, forward 9.0 -> 7.7).
 template <int RP, bool WT, bool F32>
 __global__ void __launch_bounds__(TcRoles<8, 3>::kThreads, TcExpand<RP, WT, F32>::kBlocks)
     adapter_expand_tc(const float* __restrict__ parts, int splits, const float* __restrict__ scale,
@@ -311,16 +314,18 @@ __global__ void __launch_bounds__(TcRoles<8, 3>::kThreads, TcExpand<RP, WT, F32>
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto* bars = reinterpret_cast<TcBars<NST>*>(smem + S::kU + NST * S::kStage);
   int* s_tok = reinterpret_cast<int*>(bars + 1);
-  chain_wait();
+  chain_release();
   const int4 tile = __ldcg(plan.big + blockIdx.x);  // (in bounds for every block, of use to the first ones)
-  if (static_cast<int>(blockIdx.x) >= plan_tiles(plan, true)) return;
   const int first = blockIdx.y * steps * NC, last = min(C, first + steps * NC);
-  if (first >= last) return;
   const int warp = warp_id(), lane = lane_id();
-  if (tile.x < 0 && base_in == out) return;
+  if (static_cast<int>(blockIdx.x) >= plan_tiles(plan, true) || first >= last || (tile.x < 0 && base_in == out)) {
+    chain_wait();
+    return;
+  }
   if (threadIdx.x < static_cast<unsigned>(tile.z)) s_tok[threadIdx.x] = plan.order[tile.y + threadIdx.x];
   if (tile.x < 0) {
     // rows without an adapter: the base as it is
+    chain_wait();
     __syncthreads();
     const int vecs = (last - first) / PER;
     for (int row = warp; row < tile.z; row += R::kThreads / 32) {
@@ -340,6 +345,7 @@ __global__ void __launch_bounds__(TcRoles<8, 3>::kThreads, TcExpand<RP, WT, F32>
   // flight. (A row a thread, four warps: 11 us of a block's 60.)
   const auto build_u = [&]() {
     const float sc = scale[tile.x];
+    chain_wait();
     constexpr int U8 = RP / 8, kItems = 128 * U8;
 #pragma unroll 1
     for (int i0 = threadIdx.x; i0 < kItems; i0 += 2 * R::kThreads) {
@@ -522,7 +528,6 @@ __global__ void __launch_bounds__(TcRoles<8, 3>::kThreads, TcExpand<RP, WT, F32>
       }
     }
   }
-  chain_release();
   tc_end<R>(bars, S::kTmem, lim);
 }
 
@@ -564,13 +569,14 @@ struct WgradSide {
 // partial (at most two a run: at its start and at its end) that
 // adapter_wgrad_join adds up. V's three bf16 parts lie side by side as the MMA's N,
 // so X is read from shared memory once for the three; their sums are added in the
-// epilogue, the small ones first. OUT_T: G_a is stored [r][C] (dB), else [C][r].
+// epilogue, the small ones first. v_ready: V is the caller's, not the kernel
+// ahead's. OUT_T: G_a is stored [r][C] (dB), else [C][r].
 // Bound by the rows of X, read once (16384 x 4096, rank 64: 134 MB in 34 us for dB,
 // whose dy is in L2 in part, 39 for dA; the tensor pipe at 37%).
 template <int RP, bool OUT_T>
 __global__ void __launch_bounds__(TcRoles<4, 7>::kThreads, 1)
     adapter_wgrad_tc(const __nv_bfloat16* __restrict__ X, const __nv_bfloat16* __restrict__ V, PlanView plan, int T,
-                     int r, WgradSide side, uint64_t lim) {
+                     int r, WgradSide side, bool v_ready, uint64_t lim) {
   using S = TcWgrad<RP>;
   using R = typename S::R;
   constexpr int NST = S::NST, CT = S::CT;
@@ -581,7 +587,7 @@ __global__ void __launch_bounds__(TcRoles<4, 7>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto* bars = reinterpret_cast<TcBars<NST>*>(smem + NST * S::kStage);
-  chain_wait();
+  chain_release();
   const bool any = plan_tiles(plan) > 0;
   const int warp = warp_id(), lane = lane_id(), c0 = blockIdx.x * S::kCols;
   int P0, P1, a0 = 0;
@@ -594,12 +600,16 @@ __global__ void __launch_bounds__(TcRoles<4, 7>::kThreads, 1)
       const int cols = min(S::kCols, C - c0);
       for (int i = threadIdx.x; i < cols * r; i += R::kThreads)
         g[OUT_T ? static_cast<size_t>(i / cols) * C + c0 + i % cols : static_cast<size_t>(c0) * r + i] = 0.0f;
+      chain_wait();
       return;
     }
   } else {
     P0 = blockIdx.y * run.rows;
     P1 = any ? min(plan.seg[plan.L], P0 + run.rows) : 0;
-    if (P0 >= P1) return;
+    if (P0 >= P1) {
+      chain_wait();
+      return;
+    }
     // the first adapter with rows behind P0
     for (int i0 = 0; i0 < plan.L; i0 += R::kThreads) {
       const int i = i0 + static_cast<int>(threadIdx.x);
@@ -609,6 +619,8 @@ __global__ void __launch_bounds__(TcRoles<4, 7>::kThreads, 1)
   const uint32_t base = smem_u32(smem);
   tc_init<R>(bars, 1, S::kTmem);
   const uint32_t tmem = bars->tmem;
+  // (the copies before their first of V; the others before a wait that has a limit)
+  if (!v_ready && warp <= R::kOwner) chain_wait();
 
   if (warp > R::kOwner) {
     const int p = threadIdx.x - R::kFirstProducer, w = warp - R::kOwner - 1;
@@ -642,6 +654,7 @@ __global__ void __launch_bounds__(TcRoles<4, 7>::kThreads, 1)
             cp_async16(sx + (c8 >> 3) * 8192 + swz(row, c8 & 7), in ? X + static_cast<size_t>(tok) * C + c : X, in);
           }
         }
+        if (ring.i == 0 && !v_ready) chain_wait();
         constexpr int kPieces = 64 * (RP / 8);
 #pragma unroll
         for (int k = 0; k < (kPieces + R::kProducers - 1) / R::kProducers; ++k) {
@@ -788,7 +801,7 @@ __global__ void __launch_bounds__(TcRoles<4, 7>::kThreads, 1)
       }
     }
   }
-  chain_release();
+  chain_wait();
   tc_end<R>(bars, S::kTmem, lim);
 }
 
@@ -830,6 +843,7 @@ __device__ __forceinline__ void wgrad_join(const PlanView& plan, int r, int zero
   }
   const int lo = plan.seg[a], hi = plan.seg[a + 1];
   if (hi <= end || lo < y * run.rows) return;
+  chain_wait();
   const int y1 = (hi - 1) / run.rows;
   constexpr int U = kJoinValues / 1024;
   float4 s[U];
@@ -859,9 +873,9 @@ __device__ __forceinline__ void wgrad_join(const PlanView& plan, int r, int zero
 template <int RP>
 __global__ void __launch_bounds__(256) adapter_wgrad_join(PlanView plan, int r, int zero_rows, WgradSide dA,
                                                           WgradSide dB) {
-  chain_wait();
   if (blockIdx.z == 0) wgrad_join<RP, false>(plan, r, zero_rows, dA);
   else wgrad_join<RP, true>(plan, r, zero_rows, dB);
+  chain_wait();
 }
 
 }  // namespace moe

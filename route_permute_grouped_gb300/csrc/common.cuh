@@ -58,7 +58,11 @@ __device__ __forceinline__ uint64_t globaltimer() {
 // kernel may start when every block of this one has called chain_release or
 // ended, and waits in chain_wait until this one has finished and its writes are
 // visible. What runs before chain_wait must not touch memory that an earlier
-// kernel writes or reads-and-expects-unchanged. What the kernel ahead wrote is read
+// kernel writes or reads-and-expects-unchanged. A kernel that releases only behind
+// its own wait (a call's first one) lets the call's later kernels read what the
+// caller passed before they wait: all ahead of the call has ended by then. Each of
+// those waits before its blocks end, on every path, so that the end of a call's
+// last kernel is the end of all. What the kernel ahead wrote is read
 // by ordinary or L2 loads (__ldcg): a read-only load (__ldg, or one the compiler
 // makes of a const __restrict__ pointer) may be moved to before the wait.
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
