@@ -542,8 +542,8 @@ __global__ void __launch_bounds__(kBalBwdThreads, 4)
   chain_wait();
   const int lo = static_cast<int>(min(static_cast<long long>(blockIdx.x) * rows_per_block, static_cast<long long>(p.T)));
   const int hi = static_cast<int>(min(static_cast<long long>(lo) + rows_per_block, static_cast<long long>(p.T)));
-  // the last sequence that begins at or before the block's first row
-  const int s0 = p.off == nullptr ? 0 : count_le(p.S, [&](int i) { return seq_begin(p.off, i, p.S, p.T); }, lo) - 1;
+  // the last sequence that begins at or before the block's last row
+  const int s0 = p.off == nullptr ? 0 : count_le(p.S, [&](int i) { return seq_begin(p.off, i, p.S, p.T); }, hi - 1) - 1;
   const float* tail = p.stats + static_cast<size_t>(p.S) * p.E;
   const float gb = (dlosses != nullptr ? dlosses[0] : 1.0f) * tail[0];
   const float gz = (dlosses != nullptr ? dlosses[1] : 1.0f) * tail[1];
@@ -554,19 +554,20 @@ __global__ void __launch_bounds__(kBalBwdThreads, 4)
   f2 w[2 * NV];
 #pragma unroll
   for (int i = 0; i < 2 * NV; ++i) w[i] = both(0.0f);
-  for (int t0 = lo + warp * RPW; t0 < hi; t0 += U * kBalBwdWarps * RPW) {
+  constexpr int kPass = U * kBalBwdWarps * RPW;
+  for (int t0 = lo + warp * RPW + (hi - lo - 1) / kPass * kPass; t0 >= lo; t0 -= kPass) {
     f2 v[U][2 * NV];
     float top = 0.0f;
     int seq[U];  // -1: no valid row
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = U - 1; u >= 0; --u) {
       const int t = t0 + u * kBalBwdWarps * RPW + grp;
       seq[u] = -1;
       if (t < hi) {
-        if (t >= end && s + 1 < p.S) {  // rows come in ascending order
-          while (s + 1 < p.S && seq_begin(p.off, s + 1, p.S, p.T) <= t) ++s;
-          begin = seq_begin(p.off, s, p.S, p.T);
-          end = seq_begin(p.off, s + 1, p.S, p.T);
+        if (t < begin && s >= 0) {  // rows come in descending order
+          while (s >= 0 && seq_begin(p.off, s, p.S, p.T) > t) --s;
+          begin = s >= 0 ? seq_begin(p.off, s, p.S, p.T) : 0;
+          end = s >= 0 ? seq_begin(p.off, s + 1, p.S, p.T) : 0;
         }
         if (s >= 0 && t >= begin && t < end && (p.mask == nullptr || p.mask[t] != 0)) seq[u] = s;
       }
