@@ -6,6 +6,7 @@
 #include <algorithm>
 
 #include "host_util.h"
+#include "mma.cuh"
 
 namespace moe {
 
@@ -73,16 +74,35 @@ __device__ __forceinline__ float side_sum(f2 v) {
   return x.x + x.y;
 }
 
+// Rows of whole 16-byte pieces (VEC) come through shared memory, two passes of a
+// warp ahead: each lane copies the pieces that it will hold, so no other thread's
+// copies are waited for, and its registers stay free for the rows at hand (loads to
+// registers: 131021 x 256 sigmoid both ways 90.5 us for 83, 65536 x 256 softmax 43
+// for 39).
+constexpr int kAhead = 2;
+template <int NV>
+using RowRing = float4[kAhead][kBalUnroll][NV][kBalThreads];
+template <int G, int NV, bool VEC>
+__device__ __forceinline__ void ask_row(RowRing<NV>& ring, int slot, int u, const float* row, int E, int gl) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int e = 4 * (gl + G * j);
+      if (e < E) cp_async16(smem_u32(&ring[slot][u][j][threadIdx.x]), row + e, true);
+    }
+  }
+}
 // `top`: the largest |logit| this lane has loaded so far
 template <int G, int NV, bool VEC>
-__device__ __forceinline__ void load_row(const float* row, int E, int gl, f2 (&v)[2 * NV], float& top) {
+__device__ __forceinline__ void load_row(const RowRing<NV>& ring, int slot, int u, const float* row, int E, int gl,
+                                         f2 (&v)[2 * NV], float& top) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int e = 4 * (gl + G * j);
     float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     if constexpr (VEC) {
       if (e < E) {
-        const float4 q = __ldcg(reinterpret_cast<const float4*>(row + e));
+        const float4 q = ring[slot][u][j][threadIdx.x];
         x[0] = q.x; x[1] = q.y; x[2] = q.z; x[3] = q.w;
         top = fmaxf(fmaxf(top, fmaxf(fabsf(x[0]), fabsf(x[1]))), fmaxf(fabsf(x[2]), fabsf(x[3])));
       }
@@ -125,7 +145,7 @@ __device__ __forceinline__ void group_sum2(float& a, float& b, int gl) {
 // the sum of the unnormalised scores times w.
 //
 // What bounds a row beside its bytes is its instructions (the first kernels: 36
-// an element, 113 us for 131021 x 256 sigmoid scores; these: 36 us) and the
+// an element, 113 us for 131021 x 256 sigmoid scores; these: 33 us) and the
 // special functions among them (16 a clock and SM). So m is 0 (NEAR) as long as no
 // logit of the warp's rows is beyond 40 in magnitude: no maximum is reduced, one
 // exponential x = exp(l) serves both scores, sigmoid(l) = x / (1 + x) and
@@ -267,8 +287,8 @@ struct BalParams {
 
 // Forward, first pass: each block's sums of p, counts, sum of lse^2 and number
 // of valid rows for every sequence in its rows. Bound by HBM and, beside it, its
-// instructions (131021 x 256 sigmoid: 134 MB in 36 us, 3.7 TB/s, issue slots at 50%;
-// 65536 x 256 softmax: 67 MB in 19). The sums over rows stay in registers, one set per lane
+// instructions (131021 x 256 sigmoid: 134 MB in 33 us, 4.1 TB/s; 65536 x 256
+// softmax: 67 MB in 16). The sums over rows stay in registers, one set per lane
 // group, and are joined over the groups and warps in a fixed order.
 struct BalChunk {
   int lo, hi;
@@ -279,7 +299,22 @@ __device__ __forceinline__ void part_of_sequence(const BalParams& p, const BalCh
   __shared__ float s_sum[kBalWarps][256];
   __shared__ float s_z[kBalWarps];
   __shared__ int s_n[kBalWarps];
+  __shared__ RowRing<NV> s_rows;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gl = lane & (G - 1), grp = lane / G;
+  constexpr int RPW = 32 / G, U = kBalUnroll, kPass = U * kBalWarps * RPW;
+  const auto row_of = [&](int t0, int u) { return t0 + u * kBalWarps * RPW + grp; };
+  const auto valid = [&](int t) { return t < ch.hi && (p.mask == nullptr || p.mask[t] != 0); };
+  const auto ask = [&](int t0, int slot) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = row_of(t0, u);
+      if (VEC && valid(t)) ask_row<G, NV, VEC>(s_rows, slot, u, p.logits + static_cast<size_t>(t) * p.E, p.E, gl);
+    }
+    if (VEC) cp_async_commit();
+  };
+  const int first = ch.lo + warp * RPW;
+  for (int i = 0; i < kAhead; ++i) ask(first + i * kPass, i);
   __syncthreads();  // the last sequence's sums have been read
   s_cnt[tid] = 0;
   __syncthreads();
@@ -292,29 +327,29 @@ __device__ __forceinline__ void part_of_sequence(const BalParams& p, const BalCh
     if (e < 0 || e >= p.E) set_status(p.st, MOE_ERR_DEVICE_INDEX, 50);
     else atomicAdd(&s_cnt[e], 1);
   }
-  const int gl = lane & (G - 1), grp = lane / G;
-  constexpr int RPW = 32 / G, U = kBalUnroll;
   f2 acc2[2 * NV];
 #pragma unroll
   for (int i = 0; i < 2 * NV; ++i) acc2[i] = both(0.0f);
   float z = 0.0f;
   int n = 0;
-  for (int t0 = ch.lo + warp * RPW; t0 < ch.hi; t0 += U * kBalWarps * RPW) {
+  for (int t0 = first, slot = 0; t0 < ch.hi; t0 += kPass, slot ^= 1) {
     f2 v[U][2 * NV];
     float top = 0.0f;
     bool ok[U];
+    if (VEC) cp_async_wait<kAhead - 1>();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int t = t0 + u * kBalWarps * RPW + grp;
-      ok[u] = t < ch.hi && (p.mask == nullptr || p.mask[t] != 0);
+      const int t = row_of(t0, u);
+      ok[u] = valid(t);
       if (ok[u]) {
-        load_row<G, NV, VEC>(p.logits + static_cast<size_t>(t) * p.E, p.E, gl, v[u], top);
+        load_row<G, NV, VEC>(s_rows, slot, u, p.logits + static_cast<size_t>(t) * p.E, p.E, gl, v[u], top);
       } else {
 #pragma unroll
         for (int i = 0; i < 2 * NV; ++i) v[u][i] = both(0.0f);
       }
     }
     const bool near = __all_sync(0xffffffffu, top <= kNear);
+    ask(t0 + kAhead * kPass, slot);  // (what the slot held has been read: `near` needed it)
     f2 s[U][2 * NV];
     float inv[U], lse[U], sinv[U], dot[U];
     const auto none = [](int) {};
@@ -530,35 +565,48 @@ __global__ void __launch_bounds__(32 * kBalJoinWarps) balance_join_kernel(const 
   }
 }
 
-// Backward: one pass over the logits. w is the sequence's weight row
+// Backward: one pass over the logits, each block's rows from the last one up: of
+// the rows that the forward's pass read, the later ones are still in L2. w is the sequence's weight row
 // alpha E c / (k n^2); the mean over the sequences and the losses' own
-// gradients scale it. Bound by HBM (131021 x 256 sigmoid: 268 MB in 50 us, 5.4 TB/s).
+// gradients scale it. Bound by HBM (131021 x 256 sigmoid: 268 MB in 46 us, 5.8 TB/s).
 constexpr int kBalBwdThreads = 256;
 constexpr int kBalBwdWarps = kBalBwdThreads / 32;
 template <int G, int NV, bool VEC, bool SIG>
 __global__ void __launch_bounds__(kBalBwdThreads, 4)
     balance_bwd_kernel(const BalParams p, const float* dlosses, int rows_per_block, float* dlogits) {
+  __shared__ RowRing<NV> s_rows;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   chain_wait();
   const int lo = static_cast<int>(min(static_cast<long long>(blockIdx.x) * rows_per_block, static_cast<long long>(p.T)));
   const int hi = static_cast<int>(min(static_cast<long long>(lo) + rows_per_block, static_cast<long long>(p.T)));
+  const int gl = lane & (G - 1), grp = lane / G;
+  constexpr int RPW = 32 / G, U = kBalUnroll, kPass = U * kBalBwdWarps * RPW;
+  const auto ask = [&](int t0, int slot) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * kBalBwdWarps * RPW + grp;
+      if (VEC && t0 >= lo && t < hi && (p.mask == nullptr || p.mask[t] != 0))
+        ask_row<G, NV, VEC>(s_rows, slot, u, p.logits + static_cast<size_t>(t) * p.E, p.E, gl);
+    }
+    if (VEC) cp_async_commit();
+  };
+  const int first = lo + warp * RPW + (hi - lo - 1) / kPass * kPass;
+  for (int i = 0; i < kAhead; ++i) ask(first - i * kPass, i);
   // the last sequence that begins at or before the block's last row
   const int s0 = p.off == nullptr ? 0 : count_le(p.S, [&](int i) { return seq_begin(p.off, i, p.S, p.T); }, hi - 1) - 1;
   const float* tail = p.stats + static_cast<size_t>(p.S) * p.E;
   const float gb = (dlosses != nullptr ? dlosses[0] : 1.0f) * tail[0];
   const float gz = (dlosses != nullptr ? dlosses[1] : 1.0f) * tail[1];
-  const int gl = lane & (G - 1), grp = lane / G;
-  constexpr int RPW = 32 / G, U = kBalUnroll;
   int s = s0, have = -1;  // the sequence of the row at hand, and the one whose weights w holds
   int begin = s >= 0 ? seq_begin(p.off, s, p.S, p.T) : 0, end = s >= 0 ? seq_begin(p.off, s + 1, p.S, p.T) : 0;
   f2 w[2 * NV];
 #pragma unroll
   for (int i = 0; i < 2 * NV; ++i) w[i] = both(0.0f);
-  constexpr int kPass = U * kBalBwdWarps * RPW;
-  for (int t0 = lo + warp * RPW + (hi - lo - 1) / kPass * kPass; t0 >= lo; t0 -= kPass) {
+  for (int t0 = first, slot = 0; t0 >= lo; t0 -= kPass, slot ^= 1) {
     f2 v[U][2 * NV];
     float top = 0.0f;
     int seq[U];  // -1: no valid row
+    if (VEC) cp_async_wait<kAhead - 1>();
 #pragma unroll
     for (int u = U - 1; u >= 0; --u) {
       const int t = t0 + u * kBalBwdWarps * RPW + grp;
@@ -572,13 +620,14 @@ __global__ void __launch_bounds__(kBalBwdThreads, 4)
         if (s >= 0 && t >= begin && t < end && (p.mask == nullptr || p.mask[t] != 0)) seq[u] = s;
       }
       if (seq[u] >= 0) {
-        load_row<G, NV, VEC>(p.logits + static_cast<size_t>(t) * p.E, p.E, gl, v[u], top);
+        load_row<G, NV, VEC>(s_rows, slot, u, p.logits + static_cast<size_t>(t) * p.E, p.E, gl, v[u], top);
       } else {
 #pragma unroll
         for (int i = 0; i < 2 * NV; ++i) v[u][i] = both(0.0f);
       }
     }
     const bool near = __all_sync(0xffffffffu, top <= kNear);
+    ask(t0 - kAhead * kPass, slot);
     const auto weights_of = [&](int u) {
       if (seq[u] < 0 || seq[u] == have) return;
       have = seq[u];
