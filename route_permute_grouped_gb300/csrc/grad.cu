@@ -204,7 +204,7 @@ struct ChunkWalk {
 // Each CTA's sum (fp64) and largest magnitude go to its partial; the CTA that
 // arrives last, over all launches of a list, adds them in a fixed order, writes
 // the norm and puts the ticket back to 0. Bound by HBM: 2.42 GB in 350 us, 6.9 TB/s;
-// 35 MB in 18 us, where the launch, the first loads and the join weigh as much.
+// 35 MB in 18 us from a cold L2, where the launch, the first loads and the join weigh as much.
 struct NormPartial {
   double sum;
   unsigned long long top;
@@ -343,19 +343,20 @@ __device__ __forceinline__ void scale_chunk(const Chunk& k, uint4* __restrict__ 
 // what the norm's pass read last is what L2 still holds. A block's first chunk is
 // on its way while the norm's last block still adds up: the norm's kernel only
 // reads it, and has waited for all ahead of it. Bound by HBM: 2.42 GB scaled in
-// 738 us, 6.5 TB/s; norm and scaling of 35 MB, the second out of L2, 23 us.
+// 690 us, 7.0 TB/s; norm and scaling of 35 MB, the second out of L2, 20 us.
 template <int N>
 __global__ void __launch_bounds__(kGradThreads) clip_kernel(const __grid_constant__ GradBlock<N> b,
-                                                            const float* __restrict__ norm, float max_norm) {
+                                                            const float* __restrict__ norm, float max_norm, int resident) {
   const int grid = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
   const bool any = first < b.chunks;
   int i = any ? (b.chunks - 1 - first) / grid : 0;
   Chunk k;
-  if (any) fetch(b, first + i * grid, k);
+  if (any && first < resident) fetch(b, first + i * grid, k);
   chain_wait();
   float coef = max_norm / (__ldcg(norm) + 1e-6f);
   if (coef > 1.0f) coef = 1.0f;
   if (!any || (coef == 1.0f && !b.apart)) return;
+  if (first >= resident) fetch(b, first + i * grid, k);
   while (true) {
     if (coef != 1.0f || k.it.in != k.it.out) {
       uint8_t* ob = static_cast<uint8_t*>(k.it.out) + static_cast<size_t>(k.sp.head) * k.eb;
@@ -390,7 +391,15 @@ template <int N>
 static auto norm_kernel_of(const GradBlock<N>*) {
   return norm_kernel<N>;
 }
-static int grad_grid(int chunks) { return std::max(1, std::min(chunks, std::min(4 * num_sms(), kMaxPartials))); }
+// Blocks of the norm: what is resident at a time (twice that, 123 MB: 32.1 us for
+// norm and clipping below the threshold, 27.4 so)
+static int norm_grid(int chunks) { return std::max(1, std::min({chunks, 2 * num_sms(), kMaxPartials})); }
+// Blocks of the clipping: the resident ones while those have up to 16 chunks, more
+// beyond: blocks that go through hundreds of chunks drift apart (norm and clipping in
+// us with two chunks a block, 16, and resident blocks alone: 140 MB 70, 66, 66; 560
+// MB 254, 259, 267; 2400 MB 1019, 1036, 1091; but with two chunks a block 37000
+// blocks start for nothing where nothing is scaled).
+static int clip_grid(int chunks) { return std::max(1, std::min(chunks, std::max(2 * num_sms(), chunks / 16))); }
 
 // launches `f` with the block in the smallest parameter size that holds it
 template <class F>
@@ -425,10 +434,10 @@ static int run_norm(const GradList& l, int kind, float* norm, void* ws, cudaStre
   int* ticket = &static_cast<DevStatus*>(ws)->chunk_counter;
   NormPartial* partials = reinterpret_cast<NormPartial*>(static_cast<uint8_t*>(ws) + sizeof(DevStatus));
   int all = 0;
-  for (int i = 0; i < l.launches; ++i) all += grad_grid(l.block[i].chunks);
+  for (int i = 0; i < l.launches; ++i) all += norm_grid(l.block[i].chunks);
   int at = 0;
   for (int i = 0; i < l.launches; ++i) {
-    const int grid = grad_grid(l.block[i].chunks);
+    const int grid = norm_grid(l.block[i].chunks);
     cudaError_t e2 = cudaSuccess;
     const cudaError_t e = with_block(l.block[i], [&](const auto& b) {
       using Block = std::remove_cv_t<std::remove_reference_t<decltype(b)>>;
@@ -543,8 +552,8 @@ int moe_clip_grad_norm(const void* list, int kind, float max_norm, float* norm, 
     cudaError_t e2 = cudaSuccess;
     const cudaError_t e = with_block(l->block[i], [&](const auto& b) {
       using Block = std::remove_cv_t<std::remove_reference_t<decltype(b)>>;
-      e2 = launch_chained(clip_kernel_of(static_cast<const Block*>(nullptr)), grad_grid(b.chunks), kGradThreads, 0, s,
-                          b, static_cast<const float*>(norm), max_norm);
+      e2 = launch_chained(clip_kernel_of(static_cast<const Block*>(nullptr)), clip_grid(b.chunks), kGradThreads, 0, s,
+                          b, static_cast<const float*>(norm), max_norm, 2 * num_sms());
     });
     if (e2 != cudaSuccess) return status_from_cuda(e2);
     if (e != cudaSuccess) return status_from_cuda(e);
