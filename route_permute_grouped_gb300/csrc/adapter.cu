@@ -619,11 +619,13 @@ static int shrink_splits(const moe_adapter_config& c, int C) {
 // rows of 64, rank 64: 37, 43; 4096 rows of one, rank 64: 32, 46.
 constexpr int kTcRows = 2048;
 static int big_tiles(const moe_adapter_config& c) { return c.T / 128 + std::min(c.T, c.L); }
-// two blocks for each SM, at most four splits (as above: each is read again by
-// every block of the expanding product)
+// two blocks for each SM, at most four splits, or eight up to rank 32 (as above: each
+// is read again by every block of the expanding product. Forward with four, eight
+// splits in us: 4133 rows, 7168 to 2048, rank 32 47.2, 45.4; 2048 rows, 4096 to 4096,
+// rank 16 16.9, 14.9, rank 64 24.8, 26.0; 4096 rows, rank 64 32.4, 36.9)
 static int shrink_splits_tc(const moe_adapter_config& c, int C) {
   const int nkb = (C + 63) / 64;
-  return std::max(1, std::min({2 * kAdSMs / big_tiles(c), nkb, 4}));
+  return std::max(1, std::min({2 * kAdSMs / big_tiles(c), nkb, padded_rank(c.r) <= 32 ? 8 : 4}));
 }
 // A block for each adapter and column tile instead of runs of rows: small batches
 // of many adapters have a run or two, whose one block goes through all their
