@@ -570,9 +570,13 @@ __global__ void __launch_bounds__(32 * kBalJoinWarps) balance_join_kernel(const 
 // alpha E c / (k n^2); the mean over the sequences and the losses' own
 // gradients scale it. Bound by HBM (131021 x 256 sigmoid: 268 MB in 46 us, 5.8 TB/s).
 constexpr int kBalBwdThreads = 256;
+// Resident blocks on an SM: sigmoid scores need more than 64 registers (131021 x 256
+// both ways, inputs not in L2: four blocks 91.3 us, three 88.8; 65536 x 256 softmax:
+// four 38.5, three 40.6)
+constexpr int bal_bwd_blocks(bool sigmoid) { return sigmoid ? 3 : 4; }
 constexpr int kBalBwdWarps = kBalBwdThreads / 32;
 template <int G, int NV, bool VEC, bool SIG>
-__global__ void __launch_bounds__(kBalBwdThreads, 4)
+__global__ void __launch_bounds__(kBalBwdThreads, bal_bwd_blocks(SIG))
     balance_bwd_kernel(const BalParams p, const float* dlosses, int rows_per_block, float* dlogits) {
   __shared__ RowRing<NV> s_rows;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -714,10 +718,10 @@ static int check_balance(const moe_balance_config* c) {
   return MOE_OK;
 }
 
-// Rows of a block: one wave of four blocks for each SM (blocks of half a wave more
-// than that took 70 us where one wave takes 36), whole passes of a block
-static int balance_block_rows(int T, int S) {
-  const int want = (T + 4 * 152 - 1) / (4 * 152);
+// Rows of a block: one wave of `resident` blocks for each SM (half a wave more than
+// that took 70 us where one wave took 36)
+static int balance_block_rows(int T, int S, int resident) {
+  const int want = (T + resident * 152 - 1) / (resident * 152);
   // a block takes its sequences one after the other: short ones in smaller blocks
   const int least = std::min(32, std::max(4, T / S));
   return std::max(least, want);
@@ -735,7 +739,7 @@ static BalWs balance_ws(const moe_balance_config& c) {
     o += (b + 255) & ~size_t(255);
     return at;
   };
-  w.CH = balance_block_rows(c.T, c.n_seqs);
+  w.CH = balance_block_rows(c.T, c.n_seqs, 4);
   w.blocks = (c.T + w.CH - 1) / w.CH;
   w.slots = w.blocks + c.n_seqs;
   const size_t n = w.slots, S = c.n_seqs;
@@ -846,7 +850,7 @@ int moe_balance_loss_bwd(const moe_balance_config* cfg, const float* logits, con
   BalParams p = balance_params(c, logits, seq_offsets, token_mask);
   p.stats = const_cast<float*>(stats);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int rows = balance_block_rows(c.T, 1);
+  const int rows = balance_block_rows(c.T, 1, bal_bwd_blocks(p.sigmoid != 0));
   const int grid = (c.T + rows - 1) / rows;
   const cudaError_t e = balance_dispatch(c.E, p.sigmoid, [&](auto g, auto nv, auto vec, auto sig) {
     return launch_chained(
