@@ -318,10 +318,8 @@ __global__ void __launch_bounds__(TcRoles<8, 3>::kThreads, TcExpand<RP, WT, F32>
   const int4 tile = __ldcg(plan.big + blockIdx.x);  // (in bounds for every block, of use to the first ones)
   const int first = blockIdx.y * steps * NC, last = min(C, first + steps * NC);
   const int warp = warp_id(), lane = lane_id();
-  if (static_cast<int>(blockIdx.x) >= plan_tiles(plan, true) || first >= last || (tile.x < 0 && base_in == out)) {
-    chain_wait();
-    return;
-  }
+  if (static_cast<int>(blockIdx.x) >= plan_tiles(plan, true) || first >= last || (tile.x < 0 && base_in == out))
+    return chain_leave();
   if (threadIdx.x < static_cast<unsigned>(tile.z)) s_tok[threadIdx.x] = plan.order[tile.y + threadIdx.x];
   if (tile.x < 0) {
     // rows without an adapter: the base as it is
@@ -606,10 +604,7 @@ __global__ void __launch_bounds__(TcRoles<4, 7>::kThreads, 1)
   } else {
     P0 = blockIdx.y * run.rows;
     P1 = any ? min(plan.seg[plan.L], P0 + run.rows) : 0;
-    if (P0 >= P1) {
-      chain_wait();
-      return;
-    }
+    if (P0 >= P1) return chain_leave();
     // the first adapter with rows behind P0
     for (int i0 = 0; i0 < plan.L; i0 += R::kThreads) {
       const int i = i0 + static_cast<int>(threadIdx.x);

@@ -60,12 +60,17 @@ __device__ __forceinline__ uint64_t globaltimer() {
 // visible. What runs before chain_wait must not touch memory that an earlier
 // kernel writes or reads-and-expects-unchanged. A kernel that releases only behind
 // its own wait (a call's first one) lets the call's later kernels read what the
-// caller passed before they wait: all ahead of the call has ended by then. Each of
-// those waits before its blocks end, on every path, so that the end of a call's
-// last kernel is the end of all. What the kernel ahead wrote is read
+// caller passed before they wait: all ahead of the call has ended by then. The
+// first block of each of those waits before it ends, on every path, as does every
+// block that works, so that the end of a call's last kernel is the end of all. What the kernel ahead wrote is read
 // by ordinary or L2 loads (__ldcg): a read-only load (__ldg, or one the compiler
 // makes of a const __restrict__ pointer) may be moved to before the wait.
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// for blocks that find nothing to do: the first block waits for the grid, the others
+// leave their place to blocks with work
+__device__ __forceinline__ void chain_leave() {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) chain_wait();
+}
 __device__ __forceinline__ void chain_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
