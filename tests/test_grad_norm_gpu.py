@@ -67,6 +67,27 @@ def test_below_the_threshold_every_bit_stays():
     assert all(torch.equal(a, b) for a, b in zip(out, keep))
 
 
+@pytest.mark.parametrize("apart", [False, True])
+def test_more_chunks_than_resident_blocks(apart):
+    # 5500 chunks and more: the clipping's later blocks start after the norm is known
+    g = torch.Generator("cuda").manual_seed(5)
+    ts = [torch.randn(n, generator=g, device="cuda").to(t) for n, t in
+          [(45_000_001, torch.float32), (3, torch.float32), (9_000_007, torch.bfloat16)]]
+    keep = [t.clone() for t in ts]
+    out = [torch.zeros_like(t) for t in ts] if apart else None
+    tl = ops.tensor_list(ts, out=out)
+    want = float(torch.stack([t.double().square().sum() for t in keep]).sum().sqrt())
+    norm = ops.clip_grad_norm(tl, 1e9)
+    assert abs(float(norm) - want) <= 18 * HALF * want
+    assert all(torch.equal(a, b) for a, b in zip(out if apart else ts, keep))
+    norm = ops.clip_grad_norm(tl, 2.5)
+    assert abs(float(norm) - want) <= 18 * HALF * want
+    for t, k in zip(out if apart else ts, keep):
+        w = k.double() * (2.5 / (want + 1e-6))
+        assert bool(((t.double() - w).abs() <= (24 * HALF + TYPES[t.dtype]) * w.abs() + 2.0 ** -134).all())
+    assert not apart or all(torch.equal(a, b) for a, b in zip(ts, keep))
+
+
 @pytest.mark.parametrize("shift", [1, 2, 3, 5])
 @pytest.mark.parametrize("dtype", list(TYPES))
 def test_views_at_odd_offsets(dtype, shift):
