@@ -360,3 +360,60 @@ def test_captured_behind_other_work(before, T):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("T", [1, 70, 1500, 2100, 5000])
+def test_inputs_written_right_before_and_overwritten_right_after(T, captured):
+    # the calls' later kernels ask for inputs before the kernel ahead has ended: whatever is enqueued ahead of a
+    # call must be seen by all of them, and nothing enqueued behind it by any
+    K, N, L, r = 256, 320, 5, 24
+    cfg = ops.make_adapter_config(T, K, N, L, r)
+    names = ("x", "A", "B", "scale", "base", "dy", "dx_base")
+    sets = []
+    for seed in (1, 2, 3):
+        c = {k: v.cuda() for k, v in _inputs(T, K, N, L, r, seed).items()}
+        c["idx"] = torch.from_numpy(_idx(T, L, seed).astype(np.int32)).cuda()
+        sets.append(c)
+    live = {k: torch.empty_like(v) for k, v in sets[0].items()}
+    ws, u, plan = ops.adapter_workspace(cfg, training=True), ops.alloc_adapter_saved(cfg), ops.adapter_plan(cfg, sets[0]["idx"])
+
+    def step(c, grads=None):
+        ops.adapter_plan(cfg, c["idx"], plan=plan)
+        y = ops.adapter_fwd(cfg, *(c[k] for k in names[:4]), plan, base=c["base"], u=u, ws=ws)
+        g = ops.adapter_bwd(cfg, c["dy"], *(c[k] for k in names[:4]), plan, u, dx_base=c["dx_base"], grads=grads, ws=ws)
+        return [y, g["dx"], g["dA"], g["dB"]]
+
+    want = []
+    for c in sets:
+        want.append([t.clone() for t in step(c)])
+        torch.cuda.synchronize()
+
+    def run():
+        got = []
+        for c in sets * 3:
+            for k, v in live.items():
+                torch.add(c[k], 0, out=v)
+            got.append(step(live))
+            for v in live.values():
+                v.fill_(1)
+        return got
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    if captured:
+        with torch.cuda.stream(s):
+            run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            got = run()
+        g.replay()
+    else:
+        with torch.cuda.stream(s):
+            got = run()
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        for a, b in zip(out, want[i % 3]):
+            assert torch.equal(a, b), i
+    assert ops.device_status(plan) == 0 and ops.device_status(ws) == 0
