@@ -264,10 +264,11 @@ def _p(t):
     return c_void_p(t.data_ptr())
 
 
-def _stream(_raw=torch._C._cuda_getCurrentRawStream, _device=torch._C._cuda_getDevice):
-    """The current stream of the current device, as the library takes it (the
-    raw handle: building a torch.cuda.Stream for it costs microseconds)."""
-    return _raw(_device())
+def _stream(dev=None, _raw=torch._C._cuda_getCurrentRawStream, _device=torch._C._cuda_getDevice):
+    """The current stream of the current device (dev, where the caller knows it),
+    as the library takes it (the raw handle: building a torch.cuda.Stream for it
+    costs microseconds)."""
+    return _raw(_device() if dev is None else dev)
 
 
 def _check(st, where):
@@ -787,17 +788,17 @@ def layer_bwd_nvfp4(cfg, dO, x, router_w, nvbw, saved, ws=None, grads=None, dlog
 # ---------------------------------------------------------------------------
 # Router losses with gradients
 # ---------------------------------------------------------------------------
-def _arg(where, name, t, dtype, shape, optional=False, _device=torch._C._cuda_getDevice):
-    """A tensor argument of the calls below: on the current CUDA device,
-    contiguous, of the given type (or one of them) and shape; its address. What a
-    call spends here is most of its time on the host, so the usual case comes
-    first and asks as little as it can."""
+def _arg(where, name, t, dtype, shape, dev=None, optional=False, _device=torch._C._cuda_getDevice):
+    """A tensor argument of the calls below: on the current CUDA device (dev, from
+    a call's second argument on), contiguous, of the given type (or one of them)
+    and shape; its address. What a call spends here is most of its time on the
+    host, so the usual case comes first and asks as little as it can."""
     if t is None and optional:
         return None
     try:
         if (t.dtype is dtype or (dtype.__class__ is tuple and t.dtype in dtype)) and t.shape == shape and t.is_contiguous():
             d = t.get_device()  # -1: not on a GPU
-            if d >= 0 and d == _device():
+            if d == dev or (dev is None and d >= 0 and d == _device()):
                 return t.data_ptr()
     except AttributeError:
         pass
@@ -817,12 +818,17 @@ def _arg_error(where, name, t, dtypes, shape):
     return MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} {why}")
 
 
-def _ws_arg(where, ws, nbytes):
+def _ws_arg(where, ws, nbytes, dev):
+    try:
+        if ws.dtype is torch.uint8 and ws.numel() >= nbytes and ws.is_contiguous() and ws.get_device() == dev:
+            return ws.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(ws, torch.Tensor):
         raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: the workspace must be a uint8 tensor")
     if ws.numel() < nbytes:
         raise MoeError(MOE_ERR_WORKSPACE_TOO_SMALL, where)
-    return _arg(where, "the workspace", ws, torch.uint8, ws.shape)
+    return _arg(where, "the workspace", ws, torch.uint8, ws.shape, dev)
 
 
 _size_cache = {}
@@ -873,17 +879,18 @@ def balance_loss_fwd(cfg, logits, topk_idx, seq_offsets=None, token_mask=None, w
     (None with one sequence: all rows), token_mask [T] bool or uint8."""
     w = "balance_loss_fwd"
     n_ws, n_stats = _balance_sizes(cfg)
-    args = [_arg(w, "logits", logits, torch.float32, (cfg.T, cfg.E)),
-            _arg(w, "topk_idx", topk_idx, torch.int32, (cfg.T, cfg.k)),
-            _arg(w, "seq_offsets", seq_offsets, torch.int32, (cfg.n_seqs + 1,), optional=True),
-            _arg(w, "token_mask", token_mask, (torch.bool, torch.uint8), (cfg.T,), optional=True)]
+    lp = _arg(w, "logits", logits, torch.float32, (cfg.T, cfg.E))
+    d = logits.get_device()
+    args = [lp, _arg(w, "topk_idx", topk_idx, torch.int32, (cfg.T, cfg.k), d),
+            _arg(w, "seq_offsets", seq_offsets, torch.int32, (cfg.n_seqs + 1,), d, optional=True),
+            _arg(w, "token_mask", token_mask, (torch.bool, torch.uint8), (cfg.T,), d, optional=True)]
     dev = logits.device
     losses = torch.empty(2, dtype=torch.float32, device=dev)
     counts = torch.empty((cfg.n_seqs, cfg.E), dtype=torch.int32, device=dev)
     stats = torch.empty(n_stats, dtype=torch.float32, device=dev)
     ws = _scratch(n_ws, dev) if ws is None else ws
     st = lib().moe_balance_loss_fwd(ctypes.byref(cfg), *args, losses.data_ptr(), counts.data_ptr(), stats.data_ptr(),
-                                    _ws_arg(w, ws, n_ws), ws.numel(), _stream())
+                                    _ws_arg(w, ws, n_ws, d), ws.numel(), _stream(d))
     _check(st, "moe_balance_loss_fwd")
     return losses, counts, stats
 
@@ -894,17 +901,18 @@ def balance_loss_bwd(cfg, logits, stats, dlosses=None, seq_offsets=None, token_m
     own router gradient."""
     w = "balance_loss_bwd"
     n_stats = _balance_sizes(cfg)[1]
-    args = [_arg(w, "logits", logits, torch.float32, (cfg.T, cfg.E)),
-            _arg(w, "stats", stats, torch.float32, (n_stats,)),
-            _arg(w, "dlosses", dlosses, torch.float32, (2,), optional=True),
-            _arg(w, "seq_offsets", seq_offsets, torch.int32, (cfg.n_seqs + 1,), optional=True),
-            _arg(w, "token_mask", token_mask, (torch.bool, torch.uint8), (cfg.T,), optional=True)]
+    lp = _arg(w, "logits", logits, torch.float32, (cfg.T, cfg.E))
+    d = logits.get_device()
+    args = [lp, _arg(w, "stats", stats, torch.float32, (n_stats,), d),
+            _arg(w, "dlosses", dlosses, torch.float32, (2,), d, optional=True),
+            _arg(w, "seq_offsets", seq_offsets, torch.int32, (cfg.n_seqs + 1,), d, optional=True),
+            _arg(w, "token_mask", token_mask, (torch.bool, torch.uint8), (cfg.T,), d, optional=True)]
     if dlogits is None:
         dlogits = torch.empty_like(logits)
         dp = dlogits.data_ptr()
     else:
-        dp = _arg(w, "dlogits", dlogits, torch.float32, (cfg.T, cfg.E))
-    st = lib().moe_balance_loss_bwd(ctypes.byref(cfg), *args, dp, _stream())
+        dp = _arg(w, "dlogits", dlogits, torch.float32, (cfg.T, cfg.E), d)
+    st = lib().moe_balance_loss_bwd(ctypes.byref(cfg), *args, dp, _stream(d))
     _check(st, "moe_balance_loss_bwd")
     return dlogits
 
@@ -938,20 +946,21 @@ def adapter_plan(cfg, adapter_idx, plan=None):
     w = "adapter_plan"
     n = _size("moe_adapter_plan_bytes", cfg)
     idx = _arg(w, "adapter_idx", adapter_idx, torch.int32, (cfg.T,))
+    d = adapter_idx.get_device()
     if plan is None:
         plan = torch.empty(n, dtype=torch.uint8, device=adapter_idx.device)
         pp = plan.data_ptr()
     else:
-        pp = _ws_arg(w, plan, n)
-    _check(lib().moe_adapter_plan(ctypes.byref(cfg), idx, pp, plan.numel(), _stream()), "moe_adapter_plan")
+        pp = _ws_arg(w, plan, n, d)
+    _check(lib().moe_adapter_plan(ctypes.byref(cfg), idx, pp, plan.numel(), _stream(d)), "moe_adapter_plan")
     return plan
 
 
-def _adapter_args(w, cfg, A, B, scale, plan):
-    return (_arg(w, "A", A, torch.bfloat16, (cfg.L, cfg.K, cfg.r)),
-            _arg(w, "B", B, torch.bfloat16, (cfg.L, cfg.r, cfg.N)),
-            _arg(w, "scale", scale, torch.float32, (cfg.L,)),
-            _ws_arg(w, plan, _size("moe_adapter_plan_bytes", cfg)))
+def _adapter_args(w, cfg, A, B, scale, plan, d):
+    return (_arg(w, "A", A, torch.bfloat16, (cfg.L, cfg.K, cfg.r), d),
+            _arg(w, "B", B, torch.bfloat16, (cfg.L, cfg.r, cfg.N), d),
+            _arg(w, "scale", scale, torch.float32, (cfg.L,), d),
+            _ws_arg(w, plan, _size("moe_adapter_plan_bytes", cfg), d))
 
 
 def adapter_fwd(cfg, x, A, B, scale, plan, base=None, y=None, u=None, ws=None):
@@ -961,18 +970,19 @@ def adapter_fwd(cfg, x, A, B, scale, plan, base=None, y=None, u=None, ws=None):
     u (alloc_adapter_saved): keep what adapter_bwd needs."""
     w = "adapter_fwd"
     xp = _arg(w, "x", x, torch.bfloat16, (cfg.T, cfg.K))
-    weights = _adapter_args(w, cfg, A, B, scale, plan)
+    d = x.get_device()
+    weights = _adapter_args(w, cfg, A, B, scale, plan, d)
     out = _out_dtype(cfg)
-    bp = _arg(w, "base", base, out, (cfg.T, cfg.N), optional=True)
-    up = None if u is None else _ws_arg(w, u, _size("moe_adapter_saved_bytes", cfg))
+    bp = _arg(w, "base", base, out, (cfg.T, cfg.N), d, optional=True)
+    up = None if u is None else _ws_arg(w, u, _size("moe_adapter_saved_bytes", cfg), d)
     ws = adapter_workspace(cfg, False, x.device) if ws is None else ws
-    wp = _ws_arg(w, ws, _size("moe_adapter_workspace_bytes", cfg, 0))
+    wp = _ws_arg(w, ws, _size("moe_adapter_workspace_bytes", cfg, 0), d)
     if y is None:
         y = torch.empty_like(base) if base is not None else torch.empty((cfg.T, cfg.N), dtype=out, device=x.device)
         yp = y.data_ptr()
     else:
-        yp = _arg(w, "y", y, out, (cfg.T, cfg.N))
-    st = lib().moe_adapter_fwd(ctypes.byref(cfg), xp, *weights, bp, yp, up, wp, ws.numel(), _stream())
+        yp = _arg(w, "y", y, out, (cfg.T, cfg.N), d)
+    st = lib().moe_adapter_fwd(ctypes.byref(cfg), xp, *weights, bp, yp, up, wp, ws.numel(), _stream(d))
     _check(st, "moe_adapter_fwd")
     return y
 
@@ -989,18 +999,19 @@ def adapter_bwd(cfg, dy, x, A, B, scale, plan, u, dx_base=None, grads=None, ws=N
     dy [T, N] bf16; the gradient of base is dy itself."""
     w = "adapter_bwd"
     dyp = _arg(w, "dy", dy, torch.bfloat16, (cfg.T, cfg.N))
-    xp = _arg(w, "x", x, torch.bfloat16, (cfg.T, cfg.K))
-    weights = _adapter_args(w, cfg, A, B, scale, plan)
-    up = _ws_arg(w, u, _size("moe_adapter_saved_bytes", cfg))
-    bp = _arg(w, "dx_base", dx_base, _out_dtype(cfg), (cfg.T, cfg.K), optional=True)
+    d = dy.get_device()
+    xp = _arg(w, "x", x, torch.bfloat16, (cfg.T, cfg.K), d)
+    weights = _adapter_args(w, cfg, A, B, scale, plan, d)
+    up = _ws_arg(w, u, _size("moe_adapter_saved_bytes", cfg), d)
+    bp = _arg(w, "dx_base", dx_base, _out_dtype(cfg), (cfg.T, cfg.K), d, optional=True)
     ws = adapter_workspace(cfg, True, x.device) if ws is None else ws
-    wp = _ws_arg(w, ws, _size("moe_adapter_workspace_bytes", cfg, 1))
+    wp = _ws_arg(w, ws, _size("moe_adapter_workspace_bytes", cfg, 1), d)
     g = alloc_adapter_grads(cfg, x.device) if grads is None else grads
     st = lib().moe_adapter_bwd(ctypes.byref(cfg), dyp, xp, *weights, up, bp,
-                               _arg(w, "dx", g["dx"], _out_dtype(cfg), (cfg.T, cfg.K)),
-                               _arg(w, "dA", g["dA"], torch.float32, (cfg.L, cfg.K, cfg.r)),
-                               _arg(w, "dB", g["dB"], torch.float32, (cfg.L, cfg.r, cfg.N)),
-                               wp, ws.numel(), _stream())
+                               _arg(w, "dx", g["dx"], _out_dtype(cfg), (cfg.T, cfg.K), d),
+                               _arg(w, "dA", g["dA"], torch.float32, (cfg.L, cfg.K, cfg.r), d),
+                               _arg(w, "dB", g["dB"], torch.float32, (cfg.L, cfg.r, cfg.N), d),
+                               wp, ws.numel(), _stream(d))
     _check(st, "moe_adapter_bwd")
     return g
 
@@ -1068,7 +1079,7 @@ def _norm_call(where, tensors, kind, ws, call):
         raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: the tensors must be on the current CUDA device")
     n = int(lib().moe_grad_norm_workspace_bytes())
     ws = _scratch(n, torch.device("cuda", tl.device)) if ws is None else ws
-    wp = _ws_arg(where, ws, n)
+    wp = _ws_arg(where, ws, n, tl.device)
     norm = torch.empty(1, dtype=torch.float32, device=ws.device)
     _check(call(tl.ptr, NORM_KIND[kind], _p(norm), wp, ws.numel()), where)
     return norm
