@@ -827,7 +827,9 @@ int moe_balance_loss_fwd(const moe_balance_config* cfg, const float* logits, con
         L.blocks, kBalThreads, 0, s, p);
   });
   if (e != cudaSuccess) return status_from_cuda(e);
-  // few, long sequences: a large block for each; many short ones: small blocks
+  // few, long sequences: a large block for each; many short ones: small blocks (both
+  // ways in us with large blocks, small: 65536 x 256 in one sequence 38.5, 43.4; 131021
+  // x 256 in 61 96, 82.6)
   const dim3 grid(c.n_seqs, (c.E + 31) / 32);
   e = L.slots / c.n_seqs > 40 ? launch_chained(balance_join_kernel<32>, grid, 1024, 0, s, p)
                               : launch_chained(balance_join_kernel<4>, grid, 128, 0, s, p);
