@@ -554,7 +554,9 @@ typedef struct {
 } moe_balance_config;
 
 /* Workspace bytes of moe_balance_loss_fwd and the number of floats in its
- * `stats` output (0 for an invalid config). */
+ * `stats` output (0 for an invalid config). A call leaves the
+ * workspace's first 256 bytes as it found them but for a status that it
+ * records, so one buffer serves it and the calls below in turn. */
 size_t moe_balance_workspace_bytes(const moe_balance_config* cfg);
 size_t moe_balance_stats_floats(const moe_balance_config* cfg);
 
@@ -684,7 +686,8 @@ size_t moe_tensor_list_bytes(int n);
 int moe_tensor_list_build(const moe_tensor* tensors, int n, void* list, size_t list_bytes);
 
 /* Workspace bytes of both calls. The first 256 bytes must be 0 before the
- * workspace's first use (the calls leave them 0). */
+ * workspace's first use; the calls leave them 0, and the calls of the router
+ * losses and the adapters change nothing there but the status. */
 size_t moe_grad_norm_workspace_bytes(void);
 
 /* norm [1] fp32. An empty list has norm 0. */

@@ -562,6 +562,7 @@ __global__ void __launch_bounds__(32 * kBalJoinWarps) balance_join_kernel(const 
     float* tail = p.stats + static_cast<size_t>(p.S) * E;
     tail[0] = share;
     tail[1] = 2.0f * per;
+    *p.ticket = 0;  // the workspace as it was found: other calls count from 0 in the same word
   }
 }
 
