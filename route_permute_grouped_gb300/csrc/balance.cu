@@ -92,14 +92,16 @@ __device__ __forceinline__ void ask_row(RowRing<NV>& ring, int slot, int u, cons
     }
   }
 }
-// `top`: the largest |logit| this lane has loaded so far
+// `top`: the largest |logit| this lane has loaded so far. Places behind the last
+// expert hold a finite value whose exponential is 0 (row_scores).
+constexpr float kNoExpert = -1e30f;
 template <int G, int NV, bool VEC>
 __device__ __forceinline__ void load_row(const RowRing<NV>& ring, int slot, int u, const float* row, int E, int gl,
                                          f2 (&v)[2 * NV], float& top) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int e = 4 * (gl + G * j);
-    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    float x[4] = {kNoExpert, kNoExpert, kNoExpert, kNoExpert};
     if constexpr (VEC) {
       if (e < E) {
         const float4 q = ring[slot][u][j][threadIdx.x];
@@ -126,16 +128,26 @@ __device__ __forceinline__ float group_max(float x) {
 }
 // The sums of a and of b over the lanes of a group: the halves of the group
 // exchange one of the two first, so each reduces one value (G = 32: 6 shuffles
-// for two sums instead of 10).
+// for two sums instead of 10). half_sum leaves the sum of b in the group's upper
+// half and that of a in the lower one, swap_halves gives both to every lane.
 template <int G>
-__device__ __forceinline__ void group_sum2(float& a, float& b, int gl) {
+__device__ __forceinline__ float half_sum(float a, float b, int gl) {
   const bool up = (gl & (G / 2)) != 0;
   float keep = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, G / 2);
 #pragma unroll
   for (int o = G / 4; o > 0; o >>= 1) keep += __shfl_xor_sync(0xffffffffu, keep, o);
+  return keep;
+}
+template <int G>
+__device__ __forceinline__ void swap_halves(float keep, float& a, float& b, int gl) {
+  const bool up = (gl & (G / 2)) != 0;
   const float other = __shfl_xor_sync(0xffffffffu, keep, G / 2);
   a = up ? other : keep;
   b = up ? keep : other;
+}
+template <int G>
+__device__ __forceinline__ void group_sum2(float& a, float& b, int gl) {
+  swap_halves<G>(half_sum<G>(a, b, gl), a, b, gl);
 }
 
 // The score functions of the kBalUnroll = 2 rows of a group. On return v holds
@@ -152,10 +164,15 @@ __device__ __forceinline__ void group_sum2(float& a, float& b, int gl) {
 // 1 - sigmoid(l) = 1 / (1 + x) without cancellation, and the sum stays below
 // 256 e^40. Rows with larger logits take m = max l and exp(-|l|); where m < 0 their
 // sigmoids exp(l) / (1 + exp(l)) come without the factor exp(m), which their sum
-// has too: below -88 it leaves fp32's range. exp is exp2(x log2 e): the argument
-// is off by half a step of itself, as l - m is.
+// has too: below -88 it leaves fp32's range.
+// exp(l) is 2^h (1 + c) with h = round(l log2 e) and c = l - h ln 2, what the
+// rounding of h has left (one fused product; c^2 is below 2^-38): without c every
+// row that lies around 35 would be off by half a step of 50, 7.5e-7 of its
+// probabilities in the mean. Behind a subtracted maximum c is not needed: h is off
+// by half a step of itself, as l - m is. The logarithm and the reciprocal of a
+// row's sum are taken once for each half of the group's lanes, a row for each.
 constexpr float kNear = 40.0f;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ float rcp_approx(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -167,10 +184,10 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return r;
 }
 template <int G, int NV, bool SIG, bool BWD, bool NEAR, class Weights>
-__device__ __forceinline__ void row_scores(int gl, f2 (&v)[kBalUnroll][2 * NV], f2 (&s)[kBalUnroll][2 * NV],
-                                           const f2 (&w)[2 * NV], Weights weights_of, float (&inv)[kBalUnroll],
-                                           float (&lse)[kBalUnroll], float (&sinv)[kBalUnroll],
-                                           float (&dot)[kBalUnroll]) {
+__device__ __forceinline__ void row_scores(int gl, int E, bool need_lse, f2 (&v)[kBalUnroll][2 * NV],
+                                           f2 (&s)[kBalUnroll][2 * NV], const f2 (&w)[2 * NV], Weights weights_of,
+                                           float (&inv)[kBalUnroll], float (&lse)[kBalUnroll],
+                                           float (&sinv)[kBalUnroll], float (&dot)[kBalUnroll]) {
   static_assert(kBalUnroll == 2, "the sums are reduced in pairs");
   float sum[2], ssum[2], m[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -179,8 +196,11 @@ __device__ __forceinline__ void row_scores(int gl, f2 (&v)[kBalUnroll][2 * NV], 
       m[u] = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 2 * NV; ++i) {
+        const int e = 4 * (gl + G * (i >> 1)) + 2 * (i & 1);
         const float2 l = unpack2(v[u][i]);
-        m[u] = fmaxf(m[u], fmaxf(l.x, l.y));
+        v[u][i] = pack2(e < E ? l.x : -INFINITY, e + 1 < E ? l.y : -INFINITY);
+        const float2 k = unpack2(v[u][i]);
+        m[u] = fmaxf(m[u], fmaxf(k.x, k.y));
       }
       m[u] = group_max<G>(m[u]);
     }
@@ -189,8 +209,10 @@ __device__ __forceinline__ void row_scores(int gl, f2 (&v)[kBalUnroll][2 * NV], 
 #pragma unroll
     for (int i = 0; i < 2 * NV; ++i) {
       const f2 l2 = v[u][i];
-      const float2 x = unpack2(mul2(NEAR ? l2 : add2(l2, both(-m[u])), both(kLog2e)));
+      const f2 h2 = mul2(NEAR ? l2 : add2(l2, both(-m[u])), both(kLog2e));
+      const float2 x = unpack2(h2);
       v[u][i] = pack2(ex2_approx(x.x), ex2_approx(x.y));
+      if constexpr (NEAR) v[u][i] = fma2(v[u][i], fma2(h2, both(-kLn2), l2), v[u][i]);
       sum2 = add2(sum2, v[u][i]);
       if constexpr (SIG) {
         f2 a, b;
@@ -200,7 +222,7 @@ __device__ __forceinline__ void row_scores(int gl, f2 (&v)[kBalUnroll][2 * NV], 
           a = mul2(v[u][i], b);
         } else {
           const float2 l = unpack2(l2);
-          const float tx = __expf(-fabsf(l.x)), ty = __expf(-fabsf(l.y));
+          const float tx = expf(-fabsf(l.x)), ty = expf(-fabsf(l.y));
           const float rx = rcp_approx(1.0f + tx), ry = rcp_approx(1.0f + ty);
           const float2 q = unpack2(v[u][i]);  // (m < 0: no l is above 0)
           a = pack2(l.x >= 0.0f ? rx : (m[u] < 0.0f ? q.x : tx) * rx, l.y >= 0.0f ? ry : (m[u] < 0.0f ? q.y : ty) * ry);
@@ -217,15 +239,16 @@ __device__ __forceinline__ void row_scores(int gl, f2 (&v)[kBalUnroll][2 * NV], 
     ssum[u] = SIG ? side_sum(ssum2) : 0.0f;
     dot[u] = BWD ? side_sum(dot2) : 0.0f;
   }
-  group_sum2<G>(sum[0], sum[1], gl);
-  if constexpr (SIG) group_sum2<G>(ssum[0], ssum[1], gl);
-  if constexpr (BWD) group_sum2<G>(dot[0], dot[1], gl);
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    lse[u] = m[u] + __logf(sum[u]);
-    inv[u] = __fdividef(1.0f, sum[u]);
-    if constexpr (SIG) sinv[u] = __fdividef(1.0f, ssum[u]);
+  const float half = half_sum<G>(sum[0], sum[1], gl);
+  swap_halves<G>(rcp_approx(half), inv[0], inv[1], gl);
+  lse[0] = lse[1] = 0.0f;
+  if (need_lse) {
+    swap_halves<G>(logf(half), lse[0], lse[1], gl);
+    lse[0] += m[0];
+    lse[1] += m[1];
   }
+  if constexpr (SIG) swap_halves<G>(rcp_approx(half_sum<G>(ssum[0], ssum[1], gl)), sinv[0], sinv[1], gl);
+  if constexpr (BWD) group_sum2<G>(dot[0], dot[1], gl);
 }
 
 // A sum in two floats: s + e is the exact sum so far but for the roundings of e.
@@ -353,8 +376,8 @@ __device__ __forceinline__ void part_of_sequence(const BalParams& p, const BalCh
     f2 s[U][2 * NV];
     float inv[U], lse[U], sinv[U], dot[U];
     const auto none = [](int) {};
-    if (near) row_scores<G, NV, SIG, false, true>(gl, v, s, acc2, none, inv, lse, sinv, dot);
-    else row_scores<G, NV, SIG, false, false>(gl, v, s, acc2, none, inv, lse, sinv, dot);
+    if (near) row_scores<G, NV, SIG, false, true>(gl, p.E, p.need_lse, v, s, acc2, none, inv, lse, sinv, dot);
+    else row_scores<G, NV, SIG, false, false>(gl, p.E, p.need_lse, v, s, acc2, none, inv, lse, sinv, dot);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (ok[u]) {
@@ -645,8 +668,8 @@ __global__ void __launch_bounds__(kBalBwdThreads, bal_bwd_blocks(SIG))
     };
     f2 q[U][2 * NV];
     float inv[U], lse[U], sinv[U], dot[U];
-    if (near) row_scores<G, NV, SIG, true, true>(gl, v, q, w, weights_of, inv, lse, sinv, dot);
-    else row_scores<G, NV, SIG, true, false>(gl, v, q, w, weights_of, inv, lse, sinv, dot);
+    if (near) row_scores<G, NV, SIG, true, true>(gl, p.E, p.need_lse, v, q, w, weights_of, inv, lse, sinv, dot);
+    else row_scores<G, NV, SIG, true, false>(gl, p.E, p.need_lse, v, q, w, weights_of, inv, lse, sinv, dot);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int t = t0 + u * kBalBwdWarps * RPW + grp;
