@@ -229,6 +229,8 @@ __device__ __forceinline__ void row_scores(int gl, int E, bool need_lse, f2 (&v)
           b = pack2(l.x >= 0.0f ? tx * rx : rx, l.y >= 0.0f ? ty * ry : ry);
         }
         s[u][i] = BWD ? mul2(a, b) : a;
+        // the softmax of a row with a logit of +inf is no number, but only the z-loss wants it
+        if (!NEAR && !need_lse) v[u][i] = both(0.0f);
         ssum2 = add2(ssum2, a);
         if constexpr (BWD) dot2 = fma2(a, w[i], dot2);
       } else if constexpr (BWD) {

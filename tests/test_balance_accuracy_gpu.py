@@ -87,3 +87,23 @@ def test_logarithm_of_sums_near_one(E):
     soft = np.exp(l64 - lse)
     err = np.abs(d - ref) / (2 / 400 * soft)           # the error of lse itself, and 26 half steps of the product
     assert float(np.max(err - 26 * HALF * np.abs(lse))) <= 18 * HALF
+
+
+@pytest.mark.parametrize("E", [6, 40, 256])
+def test_infinite_logits_of_valid_rows_under_sigmoid_scores(E):
+    # a sigmoid of +inf is 1 with slope 0: without the z-loss (whose log-sum-exp is infinite there) all is finite
+    l = _logits(90, E, 0.0)
+    l[::7, 2] = np.inf
+    l[3, :] = np.inf
+    l[::5, 4] = -np.inf
+    idx = np.random.default_rng(1).integers(0, E, (90, 3)).astype(np.int32)
+    cfg = ops.make_balance_config(90, E, 3, score="sigmoid", balance_coeff=1.0)
+    lg = torch.from_numpy(l).cuda()
+    losses, counts, stats = ops.balance_loss_fwd(cfg, lg, torch.from_numpy(idx).cuda())
+    d = ops.balance_loss_bwd(cfg, lg, stats).cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        ref_l, ref_c, ref_d, size = TO.balance(l.astype(np.float64), idx, 3, "sigmoid", 1.0)
+    assert np.array_equal(counts.cpu().numpy(), ref_c) and float(losses[1]) == 0.0
+    assert abs(float(losses[0]) - ref_l[0]) <= 32 * HALF * ref_l[0]
+    # terms of at most: three exponentials and three reciprocals (18), two sums (26), six products
+    assert np.all(np.abs(d - ref_d) <= 50 * HALF * size + 1e-38)
