@@ -543,10 +543,11 @@ int moe_layer_bwd_nvfp4(const moe_config* cfg, const moe_bf16* dO, const moe_bf1
  * adds nothing; with no valid token at all both losses are 0.
  * Shapes: T >= 1, E <= 256, 1 <= k <= min(E, 16), n_seqs <= 65536,
  * T*k < 2^30. Exponentials are good to 2 ulp wherever the row lies (where a
- * logit of its neighbours in the batch is beyond 40 in magnitude: to 2 ulp and
- * half a step for each unit that the logit lies below the row's largest one),
- * reciprocals to 1 ulp, logarithms to 1 ulp. Sums are fp32 within about a hundred rows and two floats
- * (48 bits) beyond, in a fixed order.
+ * logit of it or of a neighbour in the batch is beyond 40 in magnitude: to 2 ulp
+ * and half a step for each unit that the logit lies below the row's largest),
+ * reciprocals and logarithms to 1 ulp. Sums over rows are fp32 in runs of at
+ * most 64 rows and in the at most 12 additions that join the runs of a block,
+ * and two floats (48 bits) beyond, in a fixed order.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int T, E, k;

@@ -706,6 +706,10 @@ __global__ void __launch_bounds__(kBalBwdThreads, bal_bwd_blocks(SIG))
   }
 }
 
+// Lanes of a row (below) and rows that a lane group may add up in fp32
+constexpr int kBalRun = 64;
+static int balance_lanes(int E) { return E <= 16 ? 2 : (E <= 32 ? 4 : (E <= 64 ? 8 : (E <= 128 ? 16 : 32))); }
+
 // Lanes of a row by E: the smallest group whose lanes hold eight experts each, so
 // that a warp's shuffles serve several rows (72025 x 128: 31.8 us with four experts
 // a lane, 26.9 with eight); four each for up to 8 experts.
@@ -728,7 +732,7 @@ static cudaError_t balance_dispatch(int E, bool sigmoid, F f) {
   else if (E <= 32) MOE_BAL(4, 2);
   else if (E <= 64) MOE_BAL(8, 2);
   else if (E <= 128) MOE_BAL(16, 2);
-  else MOE_BAL(32, 2);
+  else MOE_BAL(32, 2);  // (balance_lanes gives the same)
 #undef MOE_BAL
 #undef MOE_BAL_SIG
   return e;
@@ -766,6 +770,14 @@ static BalWs balance_ws(const moe_balance_config& c) {
     return at;
   };
   w.CH = balance_block_rows(c.T, c.n_seqs, 4);
+  // The sums over a block's rows are fp32 in its lane groups: of a longer batch (from
+  // 311297 rows of more than 128 experts on) as many whole waves of blocks as keep a
+  // group's run at kBalRun rows.
+  const int most = kBalRun * kBalWarps * (32 / balance_lanes(c.E));
+  if (w.CH > most) {
+    const int blocks = 4 * 152 * ((w.CH + most - 1) / most);
+    w.CH = (c.T + blocks - 1) / blocks;
+  }
   w.blocks = (c.T + w.CH - 1) / w.CH;
   w.slots = w.blocks + c.n_seqs;
   const size_t n = w.slots, S = c.n_seqs;
