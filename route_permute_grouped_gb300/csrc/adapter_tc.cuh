@@ -64,6 +64,10 @@ struct TcBars {
   uint32_t tmem;
   int abort;
 };
+// The block's tensor memory is allocated before the kernel behind may start: that
+// kernel's blocks allocate too and may then wait for this one's end, so a block that
+// still had to allocate beside them could wait for ever (tcgen05.alloc has no limit).
+// As it is, whoever waits with tensor memory in hand waits for blocks that have theirs.
 template <class R, int NST>
 __device__ __forceinline__ void tc_init(TcBars<NST>* b, int empty_count, uint32_t tmem_cols) {
   if (threadIdx.x == 0) {
@@ -87,6 +91,7 @@ __device__ __forceinline__ void tc_init(TcBars<NST>* b, int empty_count, uint32_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  chain_release();
 }
 // Every thread ends here. After a wait that ran out the MMAs in flight are given
 // their (bounded) time before the tensor memory is freed.
@@ -166,7 +171,6 @@ __global__ void __launch_bounds__(TcRoles<4, 4>::kThreads, RP <= 64 ? 2 : 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto* bars = reinterpret_cast<TcBars<NST>*>(smem + NST * S::kStage);
   chain_wait();
-  chain_release();
   const int4 tile = __ldcg(plan.big + blockIdx.x);  // (in bounds for every block, of use to the first ones)
   if (static_cast<int>(blockIdx.x) >= plan_tiles(plan, true)) return;
   if (tile.x < 0) return;
@@ -314,7 +318,6 @@ __global__ void __launch_bounds__(TcRoles<8, 3>::kThreads, TcExpand<RP, WT, F32>
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto* bars = reinterpret_cast<TcBars<NST>*>(smem + S::kU + NST * S::kStage);
   int* s_tok = reinterpret_cast<int*>(bars + 1);
-  chain_release();
   const int4 tile = __ldcg(plan.big + blockIdx.x);  // (in bounds for every block, of use to the first ones)
   const int first = blockIdx.y * steps * NC, last = min(C, first + steps * NC);
   const int warp = warp_id(), lane = lane_id();
@@ -585,7 +588,6 @@ __global__ void __launch_bounds__(TcRoles<4, 7>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto* bars = reinterpret_cast<TcBars<NST>*>(smem + NST * S::kStage);
-  chain_release();
   const bool any = plan_tiles(plan) > 0;
   const int warp = warp_id(), lane = lane_id(), c0 = blockIdx.x * S::kCols;
   int P0, P1, a0 = 0;

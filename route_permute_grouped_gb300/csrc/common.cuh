@@ -66,12 +66,13 @@ __device__ __forceinline__ uint64_t globaltimer() {
 // by ordinary or L2 loads (__ldcg): a read-only load (__ldg, or one the compiler
 // makes of a const __restrict__ pointer) may be moved to before the wait.
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void chain_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // for blocks that find nothing to do: the first block waits for the grid, the others
 // leave their place to blocks with work
 __device__ __forceinline__ void chain_leave() {
+  chain_release();
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) chain_wait();
 }
-__device__ __forceinline__ void chain_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
 // bf16 helpers
