@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gemm_tc.cuh"
 
 namespace moe {
@@ -34,9 +36,17 @@ int num_sms();
 // A launch that may begin before the kernel ahead of it in the stream has ended
 // (programmatic dependent launch); the kernel calls chain_wait() before it
 // reads or writes anything that the one ahead, whatever it is, may touch. It hides
-// most of a launch's latency, about 1 us.
+// most of a launch's latency, about 1 us. The launch reads each argument as the
+// kernel's parameter of that place, so they must be of one type (a pointer may gain const).
+template <class P, class A>
+constexpr bool launch_fits() {
+  using Q = std::remove_cv_t<P>;
+  return std::is_same_v<Q, A> || (std::is_pointer_v<Q> && std::is_pointer_v<A> && std::is_convertible_v<A, Q>);
+}
 template <class... P, class... A>
 cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A&... args) {
+  static_assert(sizeof...(P) == sizeof...(A), "the kernel takes another number of arguments");
+  static_assert((launch_fits<P, A>() && ...), "an argument is not of its parameter's type");
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;

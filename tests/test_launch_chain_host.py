@@ -1,6 +1,11 @@
-"""What the overlapping launches rely on, read from the sources. CPU only."""
+"""What the overlapping launches rely on, read from the sources or asked of the
+compiler. CPU only."""
+import concurrent.futures as cf
 import os
 import re
+import subprocess
+
+from route_permute_grouped_gb300 import build as B
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "route_permute_grouped_gb300", "csrc")
@@ -39,3 +44,31 @@ def test_tensor_memory_is_allocated_before_the_next_kernel_may_start():
         before = body[:body.index("tc_init<R>(")]
         for leave in re.finditer(r"chain_leave\(\)", before):
             assert before[:leave.start()].rstrip().endswith("return"), m.group(1)
+
+
+LAUNCHES = """
+#include "host_util.h"
+namespace moe {
+__global__ void k(const float* p, size_t n, uint64_t lim) {}
+cudaError_t go(float* p, const int* q, int i, size_t n, uint64_t lim) { return launch_chained(k, 1, 32, 0, nullptr, %s); }
+}
+"""
+
+
+def test_launches_take_arguments_of_the_parameters_types_only(tmp_path):
+    # a launch hands the kernel the addresses of its arguments: one too few or of another width would be read past its end
+    forms = {"p, n, lim": True, "p, n": False, "p, i, lim": False, "p, n, i": False, "q, n, lim": False, "p, n, lim, i": False}
+
+    def compiles(item):
+        i, args = item
+        src = tmp_path / f"t{i}.cu"
+        src.write_text(LAUNCHES % args)
+        cmd = [B._nvcc(), *B.ARCH, "-std=c++17", "--expt-relaxed-constexpr", "-O0", "-I", CSRC, "-I", os.path.join(ROOT, "include"),
+               "-c", str(src), "-o", str(tmp_path / f"t{i}.o")]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        return args, r.returncode == 0, r.stderr
+
+    with cf.ThreadPoolExecutor(len(forms)) as ex:
+        for args, ok, err in ex.map(compiles, enumerate(forms)):
+            assert ok == forms[args], (args, err)
+            assert ok or "argument" in err, (args, err)
