@@ -643,7 +643,8 @@ static RowRuns wgrad_runs(const moe_adapter_config& c, int C, int* col_tiles, si
   RowRuns run;
   run.rows = ((c.T + want - 1) / want + 63) / 64 * 64;
   run.runs = (c.T + run.rows - 1) / run.rows;
-  *partial_floats = 2 * static_cast<size_t>(run.runs) * *col_tiles * cols * rp;
+  // (a single run holds every adapter whole: nothing is left to add up)
+  *partial_floats = run.runs == 1 ? 0 : 2 * static_cast<size_t>(run.runs) * *col_tiles * cols * rp;
   return run;
 }
 
