@@ -264,10 +264,16 @@ def _p(t):
     return c_void_p(t.data_ptr())
 
 
-def _stream(dev=None, _raw=torch._C._cuda_getCurrentRawStream, _device=torch._C._cuda_getDevice):
+# The current device and its current stream as a raw handle: building a torch.cuda.Stream
+# costs microseconds. A torch without these two (one built without CUDA, where the
+# configurations and the host's checks still work) has the public calls.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _stream(dev=None, _raw=_current_raw_stream, _device=_current_device):
     """The current stream of the current device (dev, where the caller knows it),
-    as the library takes it (the raw handle: building a torch.cuda.Stream for it
-    costs microseconds)."""
+    as the library takes it."""
     return _raw(_device() if dev is None else dev)
 
 
@@ -788,7 +794,7 @@ def layer_bwd_nvfp4(cfg, dO, x, router_w, nvbw, saved, ws=None, grads=None, dlog
 # ---------------------------------------------------------------------------
 # Router losses with gradients
 # ---------------------------------------------------------------------------
-def _arg(where, name, t, dtype, shape, dev=None, optional=False, _device=torch._C._cuda_getDevice):
+def _arg(where, name, t, dtype, shape, dev=None, optional=False, _device=_current_device):
     """A tensor argument of the calls below: on the current CUDA device (dev, from
     a call's second argument on), contiguous, of the given type (or one of them)
     and shape; its address. What a call spends here is most of its time on the
