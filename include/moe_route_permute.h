@@ -661,9 +661,10 @@ int moe_adapter_bwd(const moe_adapter_config* cfg, const moe_bf16* dy, const moe
  *          (MOE_NORM_MAX);
  *   coef = min(1, max_norm / (norm + 1e-6)),  out = round(g * coef).
  * Squares are summed over 16 or 32 elements in fp32 and from there in two
- * floats or fp64, in a fixed order; where fp32 squares would overflow or lose bits they are taken
- * in fp64. A NaN anywhere makes the norm NaN, and every clipped gradient; an
- * infinite norm scales by 0 (infinities become NaN).
+ * floats or fp64, in a fixed order; where fp32 squares would overflow or lose
+ * bits they are taken in fp64. A NaN anywhere makes the norm NaN, and every
+ * clipped gradient. An infinite max_norm scales nothing else. Below it an
+ * infinite norm, or one beyond fp32, scales by 0 (infinities become NaN).
  * ------------------------------------------------------------------------- */
 typedef enum { MOE_FP32 = 0, MOE_BF16 = 1, MOE_FP16 = 2 } moe_dtype;
 typedef enum { MOE_NORM_L2 = 0, MOE_NORM_MAX = 1 } moe_norm_kind;

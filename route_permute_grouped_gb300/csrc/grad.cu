@@ -338,7 +338,7 @@ __device__ __forceinline__ void scale_chunk(const Chunk& k, uint4* __restrict__ 
 }
 
 // g = round(g * coef), coef = min(1, max_norm / (norm + 1e-6)) (NaN for a NaN
-// norm). coef = 1 leaves every bit as it is, so tensors scaled in place are
+// norm, 1 for an infinite max_norm and any other norm). coef = 1 leaves every bit as it is, so tensors scaled in place are
 // then neither read further nor written. The chunks go from the last one down:
 // what the norm's pass read last is what L2 still holds. A block's first chunk is
 // on its way while the norm's last block still adds up: the norm's kernel only
@@ -353,8 +353,9 @@ __global__ void __launch_bounds__(kGradThreads) clip_kernel(const __grid_constan
   Chunk k;
   if (any && first < resident) fetch(b, first + i * grid, k);
   chain_wait();
-  float coef = max_norm / (__ldcg(norm) + 1e-6f);
-  if (coef > 1.0f) coef = 1.0f;
+  const float n = __ldcg(norm);
+  float coef = max_norm / (n + 1e-6f);
+  if (coef > 1.0f || (isinf(max_norm) && !isnan(n))) coef = 1.0f;
   if (!any || (coef == 1.0f && !b.apart)) return;
   if (first >= resident) fetch(b, first + i * grid, k);
   while (true) {

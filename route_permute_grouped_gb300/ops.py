@@ -1100,7 +1100,8 @@ def grad_norm(tensors, kind="l2", ws=None):
 
 def clip_grad_norm(tensors, max_norm, kind="l2", ws=None):
     """Scale the gradients by min(1, max_norm / (norm + 1e-6)), in place or into
-    the tensor_list's out; returns the norm before ([1] fp32)."""
+    the tensor_list's out (max_norm infinite: by 1); returns the norm before
+    ([1] fp32)."""
     return _norm_call("moe_clip_grad_norm", tensors, kind, ws,
                       lambda p, k, norm, w, nb: lib().moe_clip_grad_norm(p, k, float(max_norm), norm, w, nb,
                                                                          _stream()))
