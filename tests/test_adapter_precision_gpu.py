@@ -85,23 +85,25 @@ def test_long_inner_sums(K, T, r):
 
 
 @pytest.mark.parametrize("r", [16, 64, 128])
-@pytest.mark.parametrize("T,L", [(1000, 1), (8192, 1), (30000, 1), (30001, 3)])
-def test_long_sums_over_rows(T, L, r):
-    # u and du are 1 in every column: the weight gradients are column sums of x and of dy over an adapter's rows
-    K, N = 136, 200
+# (10000 columns and more leave a block a run of several thousand rows; narrow ones split them over all blocks)
+@pytest.mark.parametrize("T,L,K,N", [(1000, 1, 136, 200), (8192, 1, 136, 200), (30000, 1, 136, 200), (30001, 3, 136, 200),
+                                     (12000, 1, 10000, 64), (20001, 2, 64, 16008)])
+def test_long_sums_over_rows(T, L, K, N, r):
+    # u and du are equal in every row: the weight gradients are their products with column sums of x and of dy
     g = torch.Generator(device="cuda").manual_seed(T + r)
     pos = lambda *shape: (torch.rand(shape, generator=g, device="cuda") + 0.5).to(torch.bfloat16)
     cfg = ops.make_adapter_config(T, K, N, L, r, out_fp32=True)
     x, dy = pos(T, K), pos(T, N)
     x[:, 0], dy[:, 0] = 1, 1
-    A, B = torch.zeros((L, K, r), device="cuda"), torch.zeros((L, r, N), device="cuda")
-    A[:, 0], B[:, :, 0] = 1, 1
-    A, B = A.to(torch.bfloat16), B.to(torch.bfloat16)
+    A, B = torch.zeros((L, K, r), dtype=torch.bfloat16, device="cuda"), torch.zeros((L, r, N), dtype=torch.bfloat16, device="cuda")
+    A[:, 0], B[:, :, 0] = pos(L, r), pos(L, r)
+    scale = torch.rand(L, generator=g, device="cuda") + 0.5
     idx = torch.randint(0, L, (T,), generator=g, device="cuda").to(torch.int32)
-    plan, u, one = ops.adapter_plan(cfg, idx), ops.alloc_adapter_saved(cfg), torch.ones(L, device="cuda")
-    ops.adapter_fwd(cfg, x, A, B, one, plan, u=u)
-    grads = ops.adapter_bwd(cfg, dy, x, A, B, one, plan, u)
+    plan, u = ops.adapter_plan(cfg, idx), ops.alloc_adapter_saved(cfg)
+    ops.adapter_fwd(cfg, x, A, B, scale, plan, u=u)
+    grads = ops.adapter_bwd(cfg, dy, x, A, B, scale, plan, u)
     for a in range(L):
         q = idx == a
-        assert abs(_bias(grads["dA"][a], x[q].double().sum(0)[:, None].expand(K, r))) <= 1e-6
-        assert abs(_bias(grads["dB"][a], dy[q].double().sum(0)[None].expand(r, N))) <= 1e-6
+        c = scale[a].double()
+        assert abs(_bias(grads["dA"][a], x[q].sum(0, dtype=torch.float64)[:, None] * (c * B[a, :, 0].double())[None])) <= 1e-6
+        assert abs(_bias(grads["dB"][a], (c * A[a, 0].double())[:, None] * dy[q].sum(0, dtype=torch.float64)[None])) <= 1e-6
