@@ -572,8 +572,9 @@ int moe_balance_loss_fwd(const moe_balance_config* cfg, const float* logits, con
                          const int32_t* seq_offsets, const uint8_t* token_mask, float* losses,
                          int32_t* counts, float* stats, void* ws, size_t ws_bytes, void* stream);
 
-/* dlogits [T,E] fp32 (every row written). dlosses [2] fp32: the gradients of
- * the two losses (NULL: 1 and 1). */
+/* dlogits [T,E] fp32 (every row written; it may be logits itself, any other
+ * overlap with logits or stats is MOE_ERR_INVALID_ARG). dlosses [2] fp32: the
+ * gradients of the two losses (NULL: 1 and 1). */
 int moe_balance_loss_bwd(const moe_balance_config* cfg, const float* logits, const float* stats,
                          const float* dlosses, const int32_t* seq_offsets, const uint8_t* token_mask,
                          float* dlogits, void* stream);
@@ -641,7 +642,7 @@ int moe_adapter_plan(const moe_adapter_config* cfg, const int32_t* adapter_idx, 
 
 /* y from x, as above. base NULL: zeros; y may be base itself (rows without an
  * adapter are then not touched); a y that overlaps base otherwise is
- * MOE_ERR_INVALID_ARG. u_saved
+ * MOE_ERR_INVALID_ARG. y may lie over x (which the backward then lacks). u_saved
  * (moe_adapter_saved_bytes, may be NULL) receives what the backward needs. */
 int moe_adapter_fwd(const moe_adapter_config* cfg, const moe_bf16* x, const moe_bf16* A, const moe_bf16* B,
                     const float* scale, const void* plan, const void* base, void* y, void* u_saved, void* ws,

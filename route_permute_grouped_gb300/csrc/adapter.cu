@@ -766,11 +766,6 @@ static cudaError_t launch_wgrad_join(const moe_adapter_config& c, const WgradSid
                         0, s, pv, c.r, zero_rows, dA, dB);
 }
 
-// two arrays of `a_bytes` and `b_bytes` that share memory
-static bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a != nullptr && b != nullptr && x < y + b_bytes && y < x + a_bytes;
-}
 static bool any_misaligned(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0) return true;

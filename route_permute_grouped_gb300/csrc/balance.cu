@@ -887,6 +887,10 @@ int moe_balance_loss_bwd(const moe_balance_config* cfg, const float* logits, con
                         static_cast<const void*>(dlosses), static_cast<const void*>(seq_offsets),
                         static_cast<const void*>(token_mask), static_cast<const void*>(dlogits)})
     if (misaligned16(q)) return MOE_ERR_INVALID_ARG;
+  // in place a thread writes what it has read itself; shifted, what another block has still to read
+  const size_t lb = 4 * static_cast<size_t>(c.T) * c.E, sb = 4 * (static_cast<size_t>(c.n_seqs) * c.E + 2);
+  if ((dlogits != logits && overlap(logits, lb, dlogits, lb)) || overlap(stats, sb, dlogits, lb))
+    return MOE_ERR_INVALID_ARG;
   BalParams p = balance_params(c, logits, seq_offsets, token_mask);
   p.stats = const_cast<float*>(stats);
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -33,6 +33,12 @@ bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t ou
 
 int num_sms();
 
+// two arrays of `a_bytes` and `b_bytes` that share memory
+inline bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + b_bytes && y < x + a_bytes;
+}
+
 // A launch that may begin before the kernel ahead of it in the stream has ended
 // (programmatic dependent launch); the kernel calls chain_wait() before it
 // reads or writes anything that the one ahead, whatever it is, may touch. It hides
