@@ -865,11 +865,11 @@ int moe_balance_loss_fwd(const moe_balance_config* cfg, const float* logits, con
         L.blocks, kBalThreads, 0, s, p);
   });
   if (e != cudaSuccess) return status_from_cuda(e);
-  // few, long sequences: a large block for each; many short ones: small blocks (both
-  // ways in us with large blocks, small: 65536 x 256 in one sequence 38.5, 43.4; 131021
-  // x 256 in 61 96, 82.6)
+  // a large block for each of few, long sequences, small blocks for many short ones (forward in us
+  // with large blocks, small, by slots a sequence: 131072 x 256, 608 35.1, 39.9; 304 33.8, 35.3; 152
+  // 34.6, 33.5; 61 34.4, 32.3; 11 45.7, 33.5; 16384 x 128, 257 11.7, 12.2; 129 11.6, 10.4; 43 13.2, 11.0)
   const dim3 grid(c.n_seqs, (c.E + 31) / 32);
-  e = L.slots / c.n_seqs > 40 ? launch_chained(balance_join_kernel<32>, grid, 1024, 0, s, p)
+  e = L.slots / c.n_seqs > 200 ? launch_chained(balance_join_kernel<32>, grid, 1024, 0, s, p)
                               : launch_chained(balance_join_kernel<4>, grid, 128, 0, s, p);
   record_stage(s, 43, 2);
   return status_from_cuda(e);
