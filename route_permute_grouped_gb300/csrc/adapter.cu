@@ -626,10 +626,12 @@ static int shrink_splits_tc(const moe_adapter_config& c, int C) {
 }
 // A block for each adapter and column tile instead of runs of rows: small batches
 // of many adapters have a run or two, whose one block goes through all their
-// adapters (training step in us, by adapter and by runs: 90 rows of 35 adapters 32
-// and 102, 685 of 9 71 and 84, 2000 of 8 71 and 84; of one adapter, whose rows one
-// block then goes through, 2000 rows 135 and 106).
-static bool wgrad_by_adapter(const moe_adapter_config& c) { return c.T <= 1024 || (c.T < 2048 && c.L >= 4); }
+// adapters; a block of few adapters goes through all of an adapter's rows (backward
+// of 4096 to 4096 in us by adapter, by runs: rank 64, 90 rows of 12 adapters 35, 91; 400
+// rows of one 33, 31; 1000 of one 47, 38, of two 37, 41; 1500 of two 50, 50, of three 44,
+// 50; 2000 of three 56, 56, of four 52, 57; rank 16, 400 of one 18, 18; 1000 of one 30,
+// 22, of two 21, 22; 1500 of two 29, 26, of three 25, 27; 2000 of three 31, 30, of six 26, 30).
+static bool wgrad_by_adapter(const moe_adapter_config& c) { return c.T < 2048 && c.T <= 512 * c.L; }
 // Runs of rows of the weight gradients: together with the column tiles about one
 // block for each SM
 static RowRuns wgrad_runs(const moe_adapter_config& c, int C, int* col_tiles, size_t* partial_floats) {
