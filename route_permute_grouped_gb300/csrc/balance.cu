@@ -865,11 +865,14 @@ int moe_balance_loss_fwd(const moe_balance_config* cfg, const float* logits, con
         L.blocks, kBalThreads, 0, s, p);
   });
   if (e != cudaSuccess) return status_from_cuda(e);
-  // a large block for each of few, long sequences, small blocks for many short ones (forward in us
-  // with large blocks, small, by slots a sequence: 131072 x 256, 608 35.1, 39.9; 304 33.8, 35.3; 152
-  // 34.6, 33.5; 61 34.4, 32.3; 11 45.7, 33.5; 16384 x 128, 257 11.7, 12.2; 129 11.6, 10.4; 43 13.2, 11.0)
+  // a large block for each of few, long sequences, small blocks for many short ones. Both ways in us
+  // with large blocks, small, by slots a sequence: equal sequences of 16384 x 128, 513 17.9, 20.4; 257
+  // 17.1, 17.7; 171 17.4, 16.8; 103 17.4, 15.8; 65 16.5, 14.1; of 131072 x 256, 304 79.4, 81.4; 152
+  // 80.7, 79.8; 61 80.6, 78.2; cut at random, where the longest is two to three times the mean, 16384 x
+  // 128, 129 17.8, 18.3; 86 17.6, 17.7; 65 17.8, 17.3; 131072 x 256, 152 82.0, 83.0; 76 82.4, 82.4; 41
+  // 82.0, 81.3. The border lies between the two kinds' own, 200 and 70: neither loses much.
   const dim3 grid(c.n_seqs, (c.E + 31) / 32);
-  e = L.slots / c.n_seqs > 200 ? launch_chained(balance_join_kernel<32>, grid, 1024, 0, s, p)
+  e = L.slots / c.n_seqs > 100 ? launch_chained(balance_join_kernel<32>, grid, 1024, 0, s, p)
                               : launch_chained(balance_join_kernel<4>, grid, 128, 0, s, p);
   record_stage(s, 43, 2);
   return status_from_cuda(e);
