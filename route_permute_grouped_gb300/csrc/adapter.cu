@@ -157,23 +157,21 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (key >= 0 && rank == 0) s_warp[warp][key] = static_cast<uint8_t>(__popc(peers));
   if (hist == nullptr) {
     // few chunks: every block counts them all (s_first holds counts until the scan)
-    for (int c0 = 0; c0 < chunks; c0 += 4) {
-      int a[4];
+    int a[kPlanChunks];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int tc = (c0 + u) * kPlanThreads + tid;
-        a[u] = tc < T ? __ldcg(idx + tc) : INT_MIN;
-      }
+    for (int c = 0; c < kPlanChunks; ++c) {
+      const int tc = c * kPlanThreads + tid;
+      a[c] = tc < T ? __ldcg(idx + tc) : INT_MIN;
+    }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        bool b = false;
-        const int k = (c0 + u) * kPlanThreads + tid < T ? plan_key(a[u], L, b) : -1;
-        bad |= b;
-        const unsigned same = __match_any_sync(0xffffffffu, k);
-        if (k >= 0 && lane == __ffs(same) - 1) {
-          atomicAdd(&s_first[k], __popc(same));
-          if (c0 + u < me) atomicAdd(&s_before[k], __popc(same));
-        }
+    for (int c = 0; c < kPlanChunks; ++c) {
+      bool b = false;
+      const int k = c * kPlanThreads + tid < T ? plan_key(a[c], L, b) : -1;
+      bad |= b;
+      const unsigned same = __match_any_sync(0xffffffffu, k);
+      if (k >= 0 && lane == __ffs(same) - 1) {
+        atomicAdd(&s_first[k], __popc(same));
+        if (c < me) atomicAdd(&s_before[k], __popc(same));
       }
     }
   } else {
