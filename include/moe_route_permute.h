@@ -544,7 +544,7 @@ int moe_layer_bwd_nvfp4(const moe_config* cfg, const moe_bf16* dO, const moe_bf1
  * Shapes: T >= 1, E <= 256, 1 <= k <= min(E, 16), n_seqs <= 65536,
  * T*k < 2^30. Exponentials are good to 2 ulp wherever the row lies (where a
  * logit of it or of a neighbour in the batch is beyond 40 in magnitude: to 2 ulp
- * and half a step for each unit that the logit lies below the row's largest),
+ * and 1.2 for each unit that the logit lies below the row's largest),
  * reciprocals and logarithms to 1 ulp. Sums over rows are fp32 in runs of at
  * most 64 rows and in the at most 12 additions that join the runs of a block,
  * and two floats (48 bits) beyond, in a fixed order.
@@ -603,8 +603,9 @@ int moe_layer_bwd_nvfp4_dlogits(const moe_config* cfg, const moe_bf16* dO, const
 
 /* ---------------------------------------------------------------------------
  * Low-rank adapters of many requests beside a shared projection x [T,K] W
- * (the shared expert's projections, or any projection around the layer): row
- * t uses the adapter adapter_idx[t] of its request,
+ * around the layer, whose output the caller has (the layer's own calls fuse the
+ * experts' projections with SwiGLU and take no adapters): row t uses the adapter
+ * adapter_idx[t] of its request,
  *   y[t] = base[t] + scale[a] (x[t] A[a]) B[a],   a = adapter_idx[t],
  * A [L,K,r], B [L,r,N] bf16, scale [L] fp32, base and y [T,N] bf16 (fp32 if
  * out_fp32; base is the shared projection's output). Rows with a negative
@@ -615,7 +616,8 @@ int moe_layer_bwd_nvfp4_dlogits(const moe_config* cfg, const moe_bf16* dO, const
  * (fp32; zero for an adapter without rows). Products of bf16 inputs are exact
  * and accumulate in fp32; u = scale x A and du (fp32) enter their second
  * product in bf16 parts, two for bf16 results and three (24 bits) for fp32
- * ones. Every sum has a fixed order.
+ * ones. Every sum has a fixed order. A row's infinities and NaN reach its own
+ * results and its adapter's gradients only, where infinities may become NaN.
  * Shapes: K, N, r multiples of 8, r <= 128, L <= 1024, 1 <= T <= 2^21,
  * K, N <= 2^20. Adapters of smaller rank are padded with zeros to r.
  * ------------------------------------------------------------------------- */
@@ -687,7 +689,8 @@ typedef struct {
  * touches no GPU. Memory that is written (out, or data in place) must overlap
  * no other tensor of the list, and an out its own data only as the same
  * address: MOE_ERR_INVALID_ARG otherwise. The list stays valid as long as the
- * tensors stay where they are. */
+ * tensors stay where they are: gradients that are written into the same buffers
+ * every step need it built once. */
 size_t moe_tensor_list_bytes(int n);
 int moe_tensor_list_build(const moe_tensor* tensors, int n, void* list, size_t list_bytes);
 

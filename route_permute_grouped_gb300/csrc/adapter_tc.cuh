@@ -300,8 +300,8 @@ struct TcExpand {
 // out[t][c] = base[t][c] + sum_j u[position][j] W_a[j][c], u = s_a sum over the
 // splits of parts. u's bf16 parts lie side by side along the contraction, each
 // against the same tile of W_a, [r][C] (WT = false) or [C][r] (WT = true). Bound by
-// base and out (16384 x 4096, rank 64: 268 MB in 54 us, 5.0 TB/s, against 47 to 52
-// for a tiled copy). The blocks of the first columns keep u's three parts for the
+// base and out (16384 x 4096, rank 64: 268 MB in 54 us, 5.0 TB/s, behind the shrink
+// in a graph, 57 to 64 from a cold L2, against 47 to 52 for a tiled copy). The blocks of the first columns keep u's three parts for the
 // weight gradients (u_keep: [3][T][RP]). What the caller passes (plan, W_a, base)
 // is on its way before the block waits for the kernel ahead, here and in the
 // weight gradients (mixed batch of 5003 rows, 40 adapters, rank 24, step 118 -> 109

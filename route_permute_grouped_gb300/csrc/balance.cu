@@ -157,7 +157,7 @@ __device__ __forceinline__ void group_sum2(float& a, float& b, int gl) {
 // the sum of the unnormalised scores times w.
 //
 // What bounds a row beside its bytes is its instructions (the first kernels: 36
-// an element, 113 us for 131021 x 256 sigmoid scores; these: 33 us) and the
+// an element, 113 us for 131021 x 256 sigmoid scores; these: 36 us) and the
 // special functions among them (16 a clock and SM). So m is 0 (NEAR) as long as no
 // logit of the warp's rows is beyond 40 in magnitude: no maximum is reduced, one
 // exponential x = exp(l) serves both scores, sigmoid(l) = x / (1 + x) and
@@ -312,8 +312,8 @@ struct BalParams {
 
 // Forward, first pass: each block's sums of p, counts, sum of lse^2 and number
 // of valid rows for every sequence in its rows. Bound by HBM and, beside it, its
-// instructions (131021 x 256 sigmoid: 134 MB in 33 us, 4.1 TB/s; 65536 x 256
-// softmax: 67 MB in 16). The sums over rows stay in registers, one set per lane
+// instructions (131021 x 256 sigmoid: 134 MB in 36 us, 3.7 TB/s; 65536 x 256
+// softmax: 67 MB in 18). The sums over rows stay in registers, one set per lane
 // group, and are joined over the groups and warps in a fixed order.
 struct BalChunk {
   int lo, hi;
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(32 * kBalJoinWarps) balance_join_kernel(const 
 // Backward: one pass over the logits, each block's rows from the last one up: of
 // the rows that the forward's pass read, the later ones are still in L2. w is the sequence's weight row
 // alpha E c / (k n^2); the mean over the sequences and the losses' own
-// gradients scale it. Bound by HBM (131021 x 256 sigmoid: 268 MB in 46 us, 5.8 TB/s).
+// gradients scale it. Bound by HBM (131021 x 256 sigmoid: 268 MB in 48 us, 5.6 TB/s).
 constexpr int kBalBwdThreads = 256;
 // Resident blocks on an SM: sigmoid scores need more than 64 registers (131021 x 256
 // both ways, inputs not in L2: four blocks 91.3 us, three 88.8; 65536 x 256 softmax:

@@ -1065,7 +1065,10 @@ class TensorList:
 def tensor_list(tensors, out=None):
     """A list of gradients (contiguous fp32, bf16 or fp16 CUDA tensors, views at
     any offset) for grad_norm and clip_grad_norm, built once for buffers that
-    stay where they are. out: where the clipped values go (None: in place)."""
+    stay where they are: building takes the host 1 us a tensor in place and 1.5
+    with an out (384 tensors 0.40 and 0.59 ms, where norm and clipping take
+    0.02), and calls that are given the tensors themselves build it each time.
+    out: where the clipped values go (None: in place)."""
     tensors = list(tensors)
     out = None if out is None else list(out)
     if out is not None and len(out) != len(tensors):
