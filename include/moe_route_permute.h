@@ -707,6 +707,129 @@ int moe_grad_norm(const void* list, int kind, float* norm, void* ws, size_t ws_b
 int moe_clip_grad_norm(const void* list, int kind, float max_norm, float* norm, void* ws, size_t ws_bytes,
                        void* stream);
 
+/* ---------------------------------------------------------------------------
+ * MXFP4 (OCP Microscaling Formats v1.0): E2M1 elements (magnitudes 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6), blocks of 32 consecutive elements along a product's contraction
+ * share a power of two 2^s, s = floor(log2 max|v|) - 2 clamped to [-127, 127] (-127
+ * for a block of zeros; E8M0 byte s + 127); elements are v / 2^s rounded to nearest,
+ * ties to the even code, saturating. A block with an infinity or a NaN has the byte
+ * 255 and stands for NaN as a whole. Codes are packed two per byte, element 2j in
+ * the low nibble.
+ * ------------------------------------------------------------------------- */
+
+/* Row-major quantisation of x [M,K] bf16 (K a multiple of 32, blocks along K): q
+ * [M,K/2] codes, scales [M,K/32]; and the way back, which is exact. */
+int moe_mx4_quantize(const moe_bf16* x, long long M, int K, uint8_t* q, uint8_t* scales, void* stream);
+int moe_mx4_dequantize(const uint8_t* q, const uint8_t* scales, long long M, int K, moe_bf16* x, void* stream);
+
+/* The layer's quantised weights, device buffers owned by the caller (sizes from
+ * moe_mx4_weight_bytes; codes 32-byte aligned), written by
+ * moe_mx4_quantize_weights: W1 and W3 in blocks along H, W2 along F, in tiles of
+ * 128 columns x 128 elements of k (opaque: w13 tile (e, f / 128, h / 128) is 16 KB,
+ * W1's 128 columns of 64 bytes, then W3's; w2 tile (e, h / 128, f / 128) 8 KB; sf13,
+ * sf2 hold 512 bytes for 128 columns, byte 16 (c % 32) + 4 (c / 32) + b the scale of
+ * column c's block b). w13s .. sf2s: the shared expert's, NULL without one. Requires H, F
+ * and F_shared multiples of 128. */
+typedef struct {
+  uint8_t* w13;
+  uint8_t* sf13;
+  uint8_t* w2;
+  uint8_t* sf2;
+  uint8_t* w13s;
+  uint8_t* sf13s;
+  uint8_t* w2s;
+  uint8_t* sf2s;
+} moe_mx4_weights;
+
+/* Bytes of the buffers, which = 0..7 in field order (0 for an invalid config or
+ * shape, and for the shared expert's without one). */
+size_t moe_mx4_weight_bytes(const moe_config* cfg, int which);
+
+/* Quantise the bf16 weights of the layer (Ws1, Ws3, Ws2 when F_shared > 0, else
+ * ignored), and the way back into bf16 weights, which is exact. */
+int moe_mx4_quantize_weights(const moe_config* cfg, const moe_bf16* W1, const moe_bf16* W3, const moe_bf16* W2,
+                             const moe_bf16* Ws1, const moe_bf16* Ws3, const moe_bf16* Ws2, const moe_mx4_weights* w,
+                             void* stream);
+int moe_mx4_dequantize_weights(const moe_config* cfg, const moe_mx4_weights* w, moe_bf16* W1, moe_bf16* W3,
+                               moe_bf16* W2, moe_bf16* Ws1, moe_bf16* Ws3, moe_bf16* Ws2, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The whole layer for a few tokens (decoding): T <= MOE_FEW_MAX_T, otherwise the
+ * computation of moe_layer_fwd at inference, in one kernel that reads the weights of
+ * the selected experts once. Intermediates are fp32 throughout (inter_fp32 and
+ * aux_coeff have no effect): the tensor cores multiply bf16 weights with x and with
+ * a = gate SiLU(x W1) (x W3) in two bf16 parts (2^-17 of a; three, 2^-25, with
+ * out_fp32). topk_idx [T,k] and topk_gate [T,k] receive the routing. y may be x
+ * itself. Every sum has a fixed order. A row's infinities and NaN reach its own
+ * results only; infinities may become NaN.
+ * The kernel's blocks wait for one another (a cooperative launch over all SMs),
+ * with bounded waits: MOE_ERR_DEVICE_TIMEOUT in the workspace's status. The
+ * workspace's first 256 bytes must be 0 before its first use; a call leaves them 0
+ * but for the status. Two calls in flight need two workspaces.
+ * ------------------------------------------------------------------------- */
+#define MOE_FEW_MAX_T 64
+
+/* Workspace bytes of the two calls below (mxfp4 != 0: of the second); 0 for an
+ * invalid config or shape. */
+size_t moe_few_workspace_bytes(const moe_config* cfg, int mxfp4);
+
+int moe_layer_few_fwd(const moe_config* cfg, const moe_bf16* x, const moe_bf16* router_w, const float* expert_bias,
+                      const float* logit_bias, const moe_bf16* W1, const moe_bf16* W3, const moe_bf16* W2,
+                      const moe_bf16* Ws1, const moe_bf16* Ws3, const moe_bf16* Ws2, int32_t* topk_idx,
+                      float* topk_gate, void* y, void* ws, size_t ws_bytes, void* stream);
+
+/* The same with MXFP4 weights, the shared expert's included. The activations keep
+ * their precision: x and a enter the products in E4M3 parts with a power of two for
+ * 32 elements, x in two (exact unless an element lies 2^-15 below its block's
+ * largest, 2^-22 of that then), a in three (2^-12; five, 2^-20, with out_fp32). */
+int moe_layer_few_fwd_mxfp4(const moe_config* cfg, const moe_bf16* x, const moe_bf16* router_w,
+                            const float* expert_bias, const float* logit_bias, const moe_mx4_weights* w,
+                            int32_t* topk_idx, float* topk_gate, void* y, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Norms before and after a block, with its gate and the scaled residual:
+ *   u = post ? y rms(y) post_weight : y,  rms(v) = 1 / sqrt(mean(v^2) + eps),
+ *   h = residual_scale residual + gate u   (residual: if any; gate: 1, per channel or
+ *                                           per token),
+ *   n = h rms(h) pre_weight                (the next block's input; if pre),
+ * each row in fp32 from the inputs to the one rounding of every output (n from the
+ * unrounded h). y [T,H] is the block's output: bf16, fp32 with out_fp32, as the layer
+ * writes it; residual and h bf16, fp32 with residual_fp32; n bf16; weights and a
+ * gate per channel [H], a gate per token [T] fp32; stats [T,2] fp32 what the backward
+ * needs. A norm alone is the call without post, gate and residual.
+ * Backward of <dh, h> + <dn, n>:
+ *   dy bf16, dresidual as residual, dpost_weight, dpre_weight [H], dgate as gate, fp32.
+ * dh (may be NULL: zeros) as residual; dn bf16, fp32 with out_fp32, as the layer's
+ * dx. Sums over rows are fp32 for at most 64 rows and two floats beyond, in a fixed
+ * order. Shapes: H a multiple of 8, H <= 16384, T >= 1.
+ * ------------------------------------------------------------------------- */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 } moe_gate_kind;
+typedef struct {
+  int T, H;
+  float eps;
+  int residual;          /* 0 or 1 */
+  float residual_scale;
+  int gate;              /* moe_gate_kind */
+  int post, pre;         /* 0 or 1 */
+  int residual_fp32;
+  int out_fp32;
+} moe_norm_config;
+
+/* h may be NULL, residual itself, or (of one type) y; n may be y (both bf16); any
+ * other overlap of an output with an input or another output is
+ * MOE_ERR_INVALID_ARG. Arguments that the config does not ask for are ignored. */
+int moe_block_norm_fwd(const moe_norm_config* cfg, const void* y, const void* residual, const float* post_weight,
+                       const float* gate, const float* pre_weight, void* h, moe_bf16* n, float* stats, void* stream);
+
+/* Workspace bytes of the backward (0 for an invalid config). */
+size_t moe_norm_workspace_bytes(const moe_norm_config* cfg);
+
+/* dresidual may be dh, dy may be dn (both bf16). */
+int moe_block_norm_bwd(const moe_norm_config* cfg, const void* dh, const void* dn, const void* y,
+                       const void* residual, const float* post_weight, const float* gate, const float* pre_weight,
+                       const float* stats, moe_bf16* dy, void* dresidual, float* dpost_weight, float* dgate,
+                       float* dpre_weight, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, returns in *status_out the first device-side error
  * recorded in `ws` since the last read (MOE_OK if none) and clears it. For
  * tests and debugging; the hot path never calls it. */
@@ -745,7 +868,8 @@ void moe_debug_set_fault(int fault);
  * moe_write_ceiling; 32 NVFP4 down data gradient (da), 33 NVFP4 SwiGLU
  * backward, 34 NVFP4 gate/up data gradient; 40 gradient norm, 41 clipping, 43
  * balance loss, 44 its backward, 45 adapter plan, 46-48 an adapter product: to
- * rank r, from rank r, weight gradient).
+ * rank r, from rank r, weight gradient; 50 the layer for a few tokens, 51 MXFP4
+ * quantisation, 52 the way back, 53 block norms, 54 their backward, 55 its sums).
  * moe_profile_stop() stops recording. moe_profile_read() waits for the events
  * and returns their number; ms[i] is the time from event i-1 to event i
  * (0 for call starts). moe_debug_launch_count() returns the number of kernels

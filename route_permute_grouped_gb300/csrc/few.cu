@@ -1,0 +1,1136 @@
+// The whole MoE layer for a few tokens in one kernel (few.cuh: what bounds it, the
+// schedule and the operands).
+#include <string.h>
+
+#include <atomic>
+#include <initializer_list>
+
+#include "few.cuh"
+
+namespace moe {
+
+namespace {
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+// One block's forms of the block-scaled MMA and of the scales' copy (common.cuh has
+// the pairs'): A is E2M1, 16 elements in the first 8 of 16 bytes, B E4M3.
+__device__ __forceinline__ void umma_mx_w(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t d_hi, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %7, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %4, [%5], [%6], p;\n\t}" ::"r"(
+          d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(d_hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_cp_32x128b_x4(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// kind::mxf8f6f4 with E2M1 A (format 5), E4M3 B, both K-major
+__device__ __forceinline__ uint32_t idesc_mxf4f8(int N) { return idesc_mxf8_f32(128, N) | (5u << 7); }
+
+__device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void red_release(unsigned* p, unsigned v) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Wait (bounded) until *p has reached n. False when the wait ran out or the block gave up.
+__device__ __forceinline__ bool wait_count(const unsigned* p, unsigned n, FewCtl* c, const FewParams& q, int where) {
+  const uint64_t t0 = globaltimer();
+  for (unsigned it = 1;; ++it) {
+    if (ld_acquire(p) >= n) return true;
+    if (*static_cast<volatile int*>(&c->abort)) return false;
+    if ((it & 63u) == 0 && globaltimer() - t0 > q.lim) {
+      *static_cast<volatile int*>(&c->abort) = 1;
+      set_status(q.status, MOE_ERR_DEVICE_TIMEOUT, where);
+      return false;
+    }
+  }
+}
+// the epilogue warps' barrier, alone and with the conjunction of a condition: they
+// share barriers, so all of them go on or none does
+__device__ __forceinline__ void epi_sync() { named_bar_sync(1, kFewEpi); }
+__device__ __forceinline__ bool epi_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+// a whole warp's bounded wait: all lanes go on or none does
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, FewCtl* c, const FewParams& p, int where) {
+  const bool ok = mbar_wait_bounded(bar, parity, &c->abort, p.lim, p.status, where);
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+// All blocks' epilogue warps (thread `et` of a block's 256): what they wrote before is
+// visible to all after. False for every thread of a block whose wait ran out.
+__device__ __forceinline__ bool grid_sync(unsigned* counter, FewCtl* c, const FewParams& p, int et, int where) {
+  epi_sync();
+  if (et == 0) {
+    __threadfence();
+    red_release(counter, 1u);
+    wait_count(counter, gridDim.x, c, p, where);
+  }
+  epi_sync();
+  const bool ok = epi_all(*static_cast<volatile int*>(&c->abort) == 0);
+  __threadfence();
+  return ok;
+}
+
+// order-preserving unsigned image of a float that is no NaN (0 is below all of them)
+__device__ __forceinline__ uint32_t sort_key(float z) {
+  const uint32_t u = __float_as_uint(z + 0.0f);  // -0 and 0 are equal
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+// value of an E4M3 byte that is no NaN
+__device__ __forceinline__ float e4m3_float(uint32_t c) {
+  const uint32_t e = (c >> 3) & 15u, m = c & 7u;
+  const float v = e == 0 ? static_cast<float>(m) * 0.001953125f : __uint_as_float(((e + 120u) << 23) | (m << 20));
+  return (c & 0x80u) ? -v : v;
+}
+// the power of two of a block's E4M3 parts: 2^e maps the block's largest magnitude into
+// [128, 256); every further part has 2^-4 of the one before. Not below the smallest
+// scale for the last part. 1 << 20: the block holds an infinity or a NaN
+__device__ __forceinline__ int part_exponent(float amax, int parts) {
+  const int bits = static_cast<int>(__float_as_uint(amax) >> 23);
+  if (bits >= 255) return 1 << 20;
+  const int e = bits - 127 - 7;
+  const int least = -127 + 4 * (parts - 1);
+  return e > least ? e : least;
+}
+__device__ __forceinline__ uint32_t part_byte(int e, int part) {
+  return e >= (1 << 20) ? 255u : static_cast<uint32_t>(e - 4 * part + 127);
+}
+__device__ __forceinline__ float part_inverse(int e) {
+  return e >= (1 << 20) ? 1.0f : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
+
+// ---------------------------------------------------------------------------
+// router
+// ---------------------------------------------------------------------------
+// logits[t][e] for 8 tokens and one expert an item: the block's 8 warps share H, 8
+// products to a 16-byte load, fp32 fused multiply-adds
+__device__ void few_logits(const FewParams& p, FewCtl* c, int et) {
+  const int warp = et >> 5, lane = et & 31;
+  const int tg = (p.T + 7) >> 3, items = p.E * tg;
+  const int nv = p.H >> 3;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int e = item % p.E, t0 = item / p.E * 8;
+    const int nt = min(8, p.T - t0);
+    const uint4* w = reinterpret_cast<const uint4*>(p.wr + static_cast<size_t>(e) * p.H);
+    const uint4* x = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t0) * p.H);
+    float acc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+    for (int v = et; v < nv; v += kFewEpi) {
+      const uint4 wv = __ldg(w + v);
+      uint4 xv[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < nt) xv[j] = __ldg(x + static_cast<size_t>(j) * nv + v);
+      const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j < nt) {
+          const uint32_t xx[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            acc[j] = fmaf(bf16_lo(xx[q]), bf16_lo(ww[q]), acc[j]);
+            acc[j] = fmaf(bf16_hi(xx[q]), bf16_hi(ww[q]), acc[j]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j < nt) {
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], d);
+        if (lane == 0) c->scratch[warp][j] = acc[j];
+      }
+    }
+    epi_sync();
+    if (et < nt) {
+      float s = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s += c->scratch[q][et];
+      p.logits[static_cast<size_t>(t0 + et) * p.E + e] = s + (p.lb != nullptr ? __ldg(p.lb + e) : 0.0f);
+    }
+    epi_sync();
+  }
+}
+
+// x in E4M3 parts: a thread a block of 32
+__device__ void few_split_x(const FewParams& p, int et) {
+  const int nb = p.H >> 5;
+  for (int i = blockIdx.x * kFewEpi + et; i < p.T * nb; i += gridDim.x * kFewEpi) {
+    const int t = i / nb, b = i - t * nb;
+    const uint4* src = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * p.H + b * 32);
+    float v[32], amax = 0.0f;
+    bool bad = false;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4 w = __ldg(src + q);
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[8 * q + 2 * j] = bf16_lo(ww[j]);
+        v[8 * q + 2 * j + 1] = bf16_hi(ww[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      amax = fmaxf(amax, fabsf(v[j]));
+      bad |= v[j] != v[j];
+    }
+    const int e = part_exponent(bad ? INFINITY : amax, p.P1);
+    const float inv = part_inverse(e);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= inv;
+    for (int q = 0; q < p.P1; ++q) {
+      const size_t row = static_cast<size_t>(t) * p.P1 + q;
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w[j] = cvt_e4m3x2(v[4 * j], v[4 * j + 1]) | (cvt_e4m3x2(v[4 * j + 2], v[4 * j + 3]) << 16);
+#pragma unroll
+        for (int b4 = 0; b4 < 4; ++b4) v[4 * j + b4] = (v[4 * j + b4] - e4m3_float((w[j] >> (8 * b4)) & 255u)) * 16.0f;
+      }
+      uint4* dst = reinterpret_cast<uint4*>(p.xq + row * p.H + b * 32);
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      p.x_sf[row * nb + b] = static_cast<uint8_t>(part_byte(e, q));
+    }
+  }
+}
+
+// Selection and gates of token t by one warp, as the router's epilogue does it
+// (router_sel.cuh): z = logits, probabilities or sigmoids (+ expert bias), NaN as
+// -inf, an optional group limit, the k largest with ties to the lower index, gates
+// from the unbiased scores. Lane i < k leaves with slot i.
+__device__ void few_select(const FewParams& p, float* zs, int t, int lane, int& e_out, float& g_out) {
+  const float* L = p.logits + static_cast<size_t>(t) * p.E;
+  int e_sel = 0;
+  if (p.force) {
+    e_sel = static_cast<int>((static_cast<long long>(t) * p.k + lane) % p.E);
+  } else {
+    float z[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane + 32 * i;
+      z[i] = e < p.E ? __ldcg(L + e) : -INFINITY;
+    }
+    if (p.mode == RSEL_SOFTMAX) {
+      float m = -INFINITY, s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, z[i]);
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        z[i] = lane + 32 * i < p.E ? expf(z[i] - m) : 0.0f;
+        s += z[i];
+      }
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = z[i] / s;
+    } else if (p.mode == RSEL_SIGMOID) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = 1.0f / (1.0f + expf(-z[i]));
+    }
+    if (p.mode != RSEL_LOGIT && p.eb != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (lane + 32 * i < p.E) z[i] += __ldg(p.eb + lane + 32 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (z[i] != z[i]) z[i] = -INFINITY;
+    if (p.groups > 1 && p.topk_groups < p.groups) {
+      const int gsz = p.E / p.groups;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) zs[lane + 32 * i] = z[i];
+      __syncwarp();
+      uint32_t key = 0;
+      if (lane < p.groups) {
+        float b1 = -INFINITY, b2 = -INFINITY;
+        for (int j = 0; j < gsz; ++j) {
+          const float v = zs[lane * gsz + j];
+          if (v > b1) {
+            b2 = b1;
+            b1 = v;
+          } else if (v > b2) {
+            b2 = v;
+          }
+        }
+        key = sort_key(gsz >= 2 ? b1 + b2 : b1);
+      }
+      uint32_t kept = 0;
+      for (int s = 0; s < p.topk_groups; ++s) {
+        const uint32_t best = __reduce_max_sync(0xffffffffu, key);
+        const int g = __ffs(__ballot_sync(0xffffffffu, key == best)) - 1;
+        kept |= 1u << g;
+        if (lane == g) key = 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (lane + 32 * i < p.E && !((kept >> ((lane + 32 * i) / gsz)) & 1u)) z[i] = -INFINITY;
+      __syncwarp();
+    }
+    uint32_t key[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) key[i] = lane + 32 * i < p.E ? sort_key(z[i]) : 0u;
+    for (int s = 0; s < p.k; ++s) {
+      uint32_t mine = 0;
+      int at = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (key[i] > mine) {
+          mine = key[i];
+          at = lane + 32 * i;
+        }
+      }
+      const uint32_t best = __reduce_max_sync(0xffffffffu, mine);
+      const int e = static_cast<int>(__reduce_min_sync(0xffffffffu, mine == best ? static_cast<unsigned>(at) : 0xffffffu));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (e == lane + 32 * i) key[i] = 0u;
+      if (lane == s) e_sel = e;
+    }
+  }
+  const bool on = lane < p.k;
+  const float l = on ? __ldcg(L + e_sel) : -INFINITY;
+  float w;
+  if (p.mode == RSEL_SIGMOID) {
+    w = on ? 1.0f / (1.0f + expf(-l)) : 0.0f;
+  } else {
+    float m = l;
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    w = on ? expf(l - m) : 0.0f;
+  }
+  float sum = w;
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  e_out = e_sel;
+  g_out = p.gate_scale / sum * w;
+}
+
+// The block's plan from the slots' experts and gates: experts with rows in ascending
+// order, their rows in token order
+__device__ void few_plan(const FewParams& p, FewCtl* c, int et) {
+  const int R = p.T * p.k, warp = et >> 5, lane = et & 31;
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(c->eidx);
+  const uint32_t mine = static_cast<uint32_t>(et);
+  int m = 0;
+  if (et < p.E) {
+    for (int r = 0; r < R; r += 4) {
+      const uint32_t v = w[r >> 2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m += (r + j < R && ((v >> (8 * j)) & 255u) == mine) ? 1 : 0;
+    }
+  }
+  int off = m, at = m > 0 ? 1 : 0, mx = m;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, off, d), b = __shfl_up_sync(0xffffffffu, at, d);
+    if (lane >= d) {
+      off += a;
+      at += b;
+    }
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  if (lane == 31) {
+    c->warp_sum[warp] = off;
+    c->warp_act[warp] = at;
+    c->warp_max[warp] = mx;
+  }
+  epi_sync();
+  int o0 = 0, a0 = 0;
+  for (int q = 0; q < warp; ++q) {
+    o0 += c->warp_sum[q];
+    a0 += c->warp_act[q];
+  }
+  off += o0 - m;
+  at += a0 - (m > 0 ? 1 : 0);
+  if (m > 0) {
+    c->act[at] = static_cast<uint8_t>(et);
+    c->off[at] = off;
+    int n = 0;
+    for (int r = 0; r < R && n < m; r += 4) {
+      const uint32_t v = w[r >> 2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (r + j < R && ((v >> (8 * j)) & 255u) == mine) {
+          c->tok[off + n] = static_cast<uint8_t>((r + j) / p.k);
+          c->gate[off + n] = c->sgate[r + j];
+          ++n;
+        }
+      }
+    }
+  }
+  if (et == 0) {
+    int na = 0, most = p.Fs ? p.T : 0;
+    for (int q = 0; q < 8; ++q) {
+      na += c->warp_act[q];
+      most = max(most, c->warp_max[q]);
+    }
+    c->nact = na;
+    c->mmax = most;
+    c->off[na] = R;
+  }
+  epi_sync();
+}
+
+// Router, selection and plan by the epilogue warps; false when a wait ran out
+template <bool MX>
+__device__ bool few_route(const FewParams& p, FewCtl* c, int et) {
+  const int warp = et >> 5, lane = et & 31;
+  for (int i = blockIdx.x * kFewEpi + et; i < p.cnt_words; i += gridDim.x * kFewEpi) p.cnt[i] = 0u;
+  if constexpr (MX) few_split_x(p, et);
+  few_logits(p, c, et);
+  if (!grid_sync(p.sync, c, p, et, 81)) return false;
+  // a few tokens: every block selects for all of them, which saves the second wait
+  const bool all = p.T <= kFewRedundant;
+  for (int t = all ? warp : static_cast<int>(blockIdx.x + gridDim.x * warp); t < p.T; t += all ? 8 : 8 * gridDim.x) {
+    int e;
+    float g;
+    few_select(p, c->scratch[warp], t, lane, e, g);
+    if (lane < p.k) {
+      if (all) {
+        c->eidx[t * p.k + lane] = static_cast<uint8_t>(e);
+        c->sgate[t * p.k + lane] = g;
+      }
+      if (!all || blockIdx.x == 0) {
+        p.idx[t * p.k + lane] = e;
+        p.gate[t * p.k + lane] = g;
+      }
+    }
+  }
+  if (!all) {
+    if (!grid_sync(p.sync + 1, c, p, et, 82)) return false;
+    for (int r = et; r < p.T * p.k; r += kFewEpi) {
+      c->eidx[r] = static_cast<uint8_t>(__ldcg(p.idx + r));
+      c->sgate[r] = __ldcg(p.gate + r);
+    }
+  }
+  epi_sync();
+  few_plan(p, c, et);
+  return true;
+}
+
+// ---------------------------------------------------------------------------
+// ends of a tile
+// ---------------------------------------------------------------------------
+// Where a block's share of a cut tile lies: it has at most one that begins inside a
+// tile (its first) and one that ends inside (its last)
+__device__ __forceinline__ size_t piece_slot(const FewSplit& s, int block, int u0) {
+  return 2 * static_cast<size_t>(block) + (s.start(block) > u0 ? 0 : 1);
+}
+
+// Sum over the pieces of element `o` of a cut tile, in the blocks' order
+struct FewPieces {
+  const float* part;
+  size_t stride;  // floats of a slot
+  FewSplit s;
+  int u0, c0, c1;
+  __device__ __forceinline__ float sum(size_t o) const {
+    float v = 0.0f;
+    for (int b = c0; b <= c1; ++b)
+      if (s.start(b + 1) > s.start(b)) v += __ldcg(part + piece_slot(s, b, u0) * stride + o);
+    return v;
+  }
+};
+
+// The block's share of a cut tile to the workspace; true in every thread of the block
+// that is the last to arrive
+__device__ __forceinline__ bool few_leave(const float* acc, int n, float* part, size_t stride, const FewSplit& s,
+                                          int u0, int pieces, unsigned* cnt, FewCtl* c, int et) {
+  float4* dst = reinterpret_cast<float4*>(part + piece_slot(s, blockIdx.x, u0) * stride);
+  const float4* src = reinterpret_cast<const float4*>(acc);
+  for (int i = et; i < n / 4; i += kFewEpi) __stcg(dst + i, src[i]);
+  __threadfence();
+  epi_sync();
+  if (et == 0) c->flag = atomicAdd(cnt, 1u) == static_cast<unsigned>(pieces - 1) ? 1 : 0;
+  epi_sync();
+  if (c->flag == 0) return false;
+  __threadfence();
+  return true;
+}
+
+// SwiGLU of m rows x 128 columns from h1, h3 (fp32 sums), gated, split into the parts of
+// the down product's operand. Row j's values: whole tiles from `acc` [m][256], cut ones
+// from their pieces.
+template <bool MX>
+__device__ void few_activate(const FewParams& p, const FewCtl* c, const float* acc, const FewPieces* pc, int m, int i,
+                             int tile, int et) {
+  const int f = 128 * tile + (et & 127), lane = et & 31;
+  const int Fx = i < 0 ? p.Fs : p.F;
+  const int row0 = i < 0 ? 0 : c->off[i];
+  uint8_t* dst = i < 0 ? p.as : p.a;
+  uint8_t* dsf = i < 0 ? p.as_sf : p.a_sf;
+  for (int j = et >> 7; j < m; j += 2) {
+    float h1, h3;
+    if (pc == nullptr) {
+      h1 = acc[j * 256 + (et & 127)];
+      h3 = acc[j * 256 + 128 + (et & 127)];
+    } else {
+      h1 = pc->sum(static_cast<size_t>(j) * 256 + (et & 127));
+      h3 = pc->sum(static_cast<size_t>(j) * 256 + 128 + (et & 127));
+    }
+    float a = h1 / (1.0f + expf(-h1)) * h3;
+    if (i >= 0) a *= c->gate[row0 + j];
+    const size_t row = static_cast<size_t>(row0 + j) * p.P2;
+    if constexpr (MX) {
+      float amax = fabsf(a);
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+      const bool bad = __any_sync(0xffffffffu, a != a);
+      const int e = part_exponent(bad ? INFINITY : amax, p.P2);
+      float v = a * part_inverse(e);
+      for (int q = 0; q < p.P2; ++q) {
+        const uint32_t code = cvt_e4m3x2(v, 0.0f) & 255u;
+        dst[(row + q) * Fx + f] = static_cast<uint8_t>(code);
+        if (lane == 0) dsf[(row + q) * (Fx >> 5) + (f >> 5)] = static_cast<uint8_t>(part_byte(e, q));
+        v = (v - e4m3_float(code)) * 16.0f;
+      }
+    } else if (f < Fx) {
+      __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(dst);
+      __nv_bfloat16 v[3];
+      split_bf16(a, v[0], v[1], v[2]);
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        if (q < p.P2) d[(row + q) * Fx + f] = v[q];
+    }
+  }
+}
+
+__device__ __forceinline__ void few_store_y(const FewParams& p, int t, int h, float v) {
+  if (h >= p.H) return;
+  const size_t o = static_cast<size_t>(t) * p.H + h;
+  if (p.out_fp32) static_cast<float*>(p.y)[o] = v;
+  else static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
+}
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
+template <bool MX>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    few_kernel(const __grid_constant__ FewParams p, const __grid_constant__ FewMaps maps) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // layout assumption broken: report, touch nothing
+    if (threadIdx.x == 0) set_status(p.status, MOE_ERR_CUDA, 99);
+    return;
+  }
+  FewCtl* c = reinterpret_cast<FewCtl*>(smem + kFewCtlOff);
+  const int warp = warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kFewStages; ++s) {
+      mbar_init(c->full + s, 1 + kFewCopiers);
+      mbar_init(c->empty + s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(c->tfull + b, 1);
+      mbar_init(c->tempty + b, kFewEpi / 32);
+    }
+    mbar_init(&c->plan, 1);
+    mbar_init(&c->drain, 1);
+    c->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&c->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c->tmem;
+  const int first_phase = p.Fs ? 0 : 1;
+  volatile int* abort_flag = &c->abort;
+  const int G = gridDim.x;
+  constexpr int kSubBytes = 128;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ weights
+    if (lane == 0) {
+      int n = 0;  // stages so far
+      bool ok = true;
+      FewGeo g = few_geo(p.P1, p.P2, p.T, p.T, MX);
+      for (int ph = first_phase; ph < 3 && ok; ++ph) {
+        if (ph == 1) {
+          if (!mbar_wait_bounded(&c->plan, 0, abort_flag, p.lim, p.status, 83)) break;
+          g = few_geo(p.P1, p.P2, p.T, c->mmax, MX);
+        }
+        FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
+        FewChunk ch;
+        while (ok && w.next(ch)) {
+          const int e = ch.i < 0 ? 0 : c->act[ch.i];
+          const bool sh = ch.i < 0;
+          const int Fx = sh ? p.Fs : p.F;
+          for (int kb = ch.kb; kb < ch.kb + ch.nkb; ++kb, ++n) {
+            const int s = n % g.nst;
+            if (!mbar_wait_bounded(c->empty + s, ((n / g.nst) & 1) ^ 1, abort_flag, p.lim, p.status, 84)) {
+              ok = false;
+              break;
+            }
+            uint8_t* sA = smem + s * g.stage;
+            uint64_t* bar = c->full + s;
+            const uint64_t pol = l2_policy_evict_first();
+            if (ph < 2) {
+              if constexpr (MX) {
+                mbar_arrive_expect_tx(bar, kFewATile + 1024);  // 4-bit loads announce the bytes they read
+                const size_t blk = (static_cast<size_t>(e) * (sh ? p.ns1s : p.ns1) + ch.tile) * p.nsb1 + kb;
+                const CUtensorMap* m = &maps.m[sh ? 3 : 0];
+                tma_load_2d_hint(sA, m, bar, 0, static_cast<int>(blk * 256), pol);
+                tma_load_2d_hint(sA + kFewATile, m, bar, 0, static_cast<int>(blk * 256 + 128), pol);
+                bulk_load(sA + kFewABytes + g.b_bytes, (sh ? p.sf13s : p.sf13) + blk * 1024, 1024, bar);
+              } else {
+                mbar_arrive_expect_tx(bar, kFewABytes);
+                const CUtensorMap* m1 = &maps.m[sh ? 3 : 0];
+                const CUtensorMap* m3 = &maps.m[sh ? 4 : 1];
+                const int f = ch.tile * 128, row = e * p.H + kb * 64;
+                tma_load_2d_hint(sA, m1, bar, f, row, pol);
+                tma_load_2d_hint(sA + 8192, m1, bar, f + 64, row, pol);
+                tma_load_2d_hint(sA + 16384, m3, bar, f, row, pol);
+                tma_load_2d_hint(sA + 24576, m3, bar, f + 64, row, pol);
+              }
+            } else {
+              const int nsb = sh ? p.nsb2s : p.nsb2;
+              const int sb0 = kb * g.sub2, ns = min(g.sub2, nsb - sb0);
+              const CUtensorMap* m = &maps.m[sh ? 5 : 2];
+              if constexpr (MX) {
+                mbar_arrive_expect_tx(bar, ns * (kFewATile / 2 + 512));
+                const size_t blk = (static_cast<size_t>(e) * p.ns2 + ch.tile) * nsb + sb0;
+                for (int q = 0; q < ns; ++q)
+                  tma_load_2d_hint(sA + q * kFewATile, m, bar, 0, static_cast<int>((blk + q) * 128), pol);
+                bulk_load(sA + kFewABytes + g.b_bytes, (sh ? p.sf2s : p.sf2) + blk * 512, ns * 512, bar);
+              } else {
+                mbar_arrive_expect_tx(bar, ns * kFewATile);
+                for (int q = 0; q < ns; ++q) {
+                  const int row = e * Fx + (sb0 + q) * 64;
+                  tma_load_2d_hint(sA + q * kFewATile, m, bar, ch.tile * 128, row, pol);
+                  tma_load_2d_hint(sA + q * kFewATile + 8192, m, bar, ch.tile * 128 + 64, row, pol);
+                }
+              }
+            }
+          }
+        }
+      }
+      if (*abort_flag) {  // copies in flight have time to land before the block ends
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 200000ull) __nanosleep(1000);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA
+    int n = 0, na = 0;  // stages, accumulators so far
+    bool ok = true;
+    FewGeo g = few_geo(p.P1, p.P2, p.T, p.T, MX);
+    const uint32_t d_hi = sdesc_hi_sw128(1024);
+    const uint64_t sf_hi = static_cast<uint64_t>((128u >> 4) | (1u << 14)) << 32;
+    constexpr uint32_t kAStep = MX ? (32u >> 4) : (2048u >> 4);
+    int used[2] = {0, 0};  // times that each accumulator has been filled
+    for (int ph = first_phase; ph < 3 && ok; ++ph) {
+      if (ph == 1) {
+        if (!warp_wait(&c->plan, 0, c, p, 85)) break;
+        g = few_geo(p.P1, p.P2, p.T, c->mmax, MX);
+      }
+      FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
+      FewChunk ch;
+      const int parts = ph < 2 ? p.P1 : p.P2;
+      const int nbuf = ph < 2 ? g.nbuf1 : g.nbuf2;
+      const int acc_cols = ph < 2 ? 2 * g.n1 : g.n2;
+      na = 0;
+      // the phases lay their accumulators out differently: all earlier ones have been read
+      for (int b = 0; b < 2 && ok; ++b)
+        if (used[b] > 0) ok = warp_wait(c->tempty + b, (used[b] & 1) ^ 1, c, p, 86);
+      while (ok && w.next(ch)) {
+        const int m = ch.i < 0 ? p.T : c->off[ch.i + 1] - c->off[ch.i];
+        const int N = few_cols(parts, m);
+        const int buf = na % nbuf;
+        ++na;
+        // every earlier use of this accumulator has been read
+        if (!warp_wait(c->tempty + buf, (used[buf] & 1) ^ 1, c, p, 86)) {
+          ok = false;
+          break;
+        }
+        ++used[buf];
+        tc_fence_after();
+        const uint32_t d0 = tmem + buf * acc_cols;
+        for (int kb = ch.kb; kb < ch.kb + ch.nkb; ++kb, ++n) {
+          const int s = n % g.nst;
+          if (!warp_wait(c->full + s, (n / g.nst) & 1, c, p, 87)) {
+            ok = false;
+            break;
+          }
+          // the tokens' copies are generic-proxy writes: ordered before the MMAs' reads
+          fence_proxy_async_smem();
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t sA = smem_u32(smem) + s * g.stage;
+            const uint32_t a0 = sdesc_lo(sA, MX ? 16u : 8192u), b0 = sdesc_lo(sA + kFewABytes, 16u);
+            int ns = 2;
+            if (ph == 2) ns = min(g.sub2, (ch.i < 0 ? p.nsb2s : p.nsb2) - kb * g.sub2);
+            const int nblk = ph < 2 ? g.nblk1 : g.nblk2;
+            const uint32_t region = tmem + 448 + (n & 1) * 32;
+            if constexpr (MX) {
+              // scales to tensor memory: A's four columns a tile, then B's four for 128 rows
+              const uint32_t sf = sdesc_lo(sA + kFewABytes + g.b_bytes, 128u);
+              const int nb = ph < 2 ? nblk : ns * nblk;
+              for (int q = 0; q < ns; ++q) tmem_cp_32x128b_x4(region + 4 * q, sf_hi | (sf + q * (512u >> 4)));
+              for (int q = 0; q < nb; ++q)
+                tmem_cp_32x128b_x4(region + 8 + 4 * q, sf_hi | (sf + ((1024u + 512u * q) >> 4)));
+            }
+            const uint32_t go = kb > ch.kb ? 1u : 0u;
+            for (int q = 0; q < ns; ++q) {
+              // phases 0, 1: W1's then W3's tile against the same tokens, two accumulators;
+              // phase 2: two sub-blocks of W2, each against its own, one accumulator
+              const uint32_t a_lo = a0 + q * (kFewATile >> 4);
+              const uint32_t b_lo = ph < 2 ? b0 : b0 + q * ((g.n2 * kSubBytes) >> 4);
+              const uint32_t d = ph < 2 ? d0 + q * g.n1 : d0;
+              const uint32_t go_q = ph < 2 ? go : (go | (q > 0 ? 1u : 0u));
+              for (int n0 = 0; n0 < N; n0 += 256) {
+                const int nn = min(256, N - n0);
+                const uint32_t idesc = MX ? idesc_mxf4f8(nn) : idesc_bf16_f32(128, nn, true, false);
+                const uint32_t bn = b_lo + ((n0 * kSubBytes) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  const uint32_t acc = go_q | (kk > 0 ? 1u : 0u);
+                  if constexpr (MX)
+                    umma_mx_w(d + n0, a_lo + kk * kAStep, bn + kk * (32u >> 4), d_hi,
+                              idesc | (static_cast<uint32_t>(kk) << 29) | (static_cast<uint32_t>(kk) << 4),
+                              region + 4 * q, region + 8 + (ph < 2 ? 0 : 4 * nblk * q) + n0 / 32, acc);
+                  else
+                    umma_bf16_w(d + n0, a_lo + kk * kAStep, bn + kk * (32u >> 4), d_hi, idesc, acc);
+                }
+              }
+            }
+            umma_commit(c->empty + s);
+          }
+          __syncwarp();
+        }
+        if (lane == 0) umma_commit(c->tfull + buf);
+        __syncwarp();
+      }
+    }
+    if (*abort_flag) {  // the MMAs in flight end before the tensor memory is freed
+      int zero = 0;
+      if (lane == 0) umma_commit(&c->drain);
+      __syncwarp();
+      mbar_wait_bounded(&c->drain, 0, &zero, p.lim, nullptr, 0);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ tokens
+    const int ct = threadIdx.x - 64;
+    int n = 0;
+    bool ok = true;
+    FewGeo g = few_geo(p.P1, p.P2, p.T, p.T, MX);
+    const int xld = p.H * (MX ? 1 : 2);
+    for (int ph = first_phase; ph < 3 && ok; ++ph) {
+      if (ph == 0 && MX) {
+        // the parts of x come from all blocks
+        if (lane == 0) ok = wait_count(p.sync, gridDim.x, c, p, 88);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+      }
+      if (ph == 1) {
+        if (!warp_wait(&c->plan, 0, c, p, 89)) break;
+        g = few_geo(p.P1, p.P2, p.T, c->mmax, MX);
+      }
+      if (ph == 2) {
+        // all activations are there
+        if (lane == 0) ok = wait_count(p.sync + 2, p.ns1s + c->nact * p.ns1, c, p, 90);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+      }
+      FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
+      FewChunk ch;
+      const int parts = ph < 2 ? p.P1 : p.P2;
+      while (ok && w.next(ch)) {
+        const bool sh = ch.i < 0;
+        const int r0 = sh ? 0 : c->off[ch.i];
+        const int m = sh ? p.T : c->off[ch.i + 1] - r0;
+        const int mp = (m + 7) & ~7;
+        const int Fx = sh ? p.Fs : p.F;
+        for (int kb = ch.kb; kb < ch.kb + ch.nkb; ++kb, ++n) {
+          const int s = n % g.nst;
+          if (!warp_wait(c->empty + s, ((n / g.nst) & 1) ^ 1, c, p, 91)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sB = smem_u32(smem) + s * g.stage + kFewABytes;
+          const uint32_t sSF = sB + g.b_bytes + 1024;
+          int ns = 1, sb0 = kb;
+          if (ph == 2) {
+            sb0 = kb * g.sub2;
+            ns = min(g.sub2, (sh ? p.nsb2s : p.nsb2) - sb0);
+          }
+          for (int q = 0; q < ns; ++q) {
+            const int sb = sb0 + q;
+            const uint32_t sBq = sB + q * g.n2 * kSubBytes;
+            for (int it = ct; it < parts * m * 8; it += kFewCopiers) {
+              const int r = it >> 3, ck = it & 7;
+              const int part = r / m, j = r - part * m;
+              const uint8_t* src;
+              if (ph < 2) {
+                const int t = sh ? j : c->tok[r0 + j];
+                src = MX ? p.xq + (static_cast<size_t>(t) * parts + part) * xld
+                         : reinterpret_cast<const uint8_t*>(p.x) + static_cast<size_t>(t) * xld;
+              } else {
+                src = (sh ? p.as : p.a) + (static_cast<size_t>(r0 + j) * parts + part) * (Fx * (MX ? 1 : 2));
+              }
+              const int nrow = part * mp + j;
+              cp_async16(sBq + nrow * 128 + ((ck ^ (nrow & 7)) << 4), src + sb * kSubBytes + ck * 16, true);
+            }
+            if constexpr (MX) {
+              for (int r = ct; r < parts * m; r += kFewCopiers) {
+                const int part = r / m, j = r - part * m;
+                const uint8_t* src;
+                if (ph < 2) {
+                  const int t = sh ? j : c->tok[r0 + j];
+                  src = p.x_sf + (static_cast<size_t>(t) * parts + part) * (p.H >> 5);
+                } else {
+                  src = (sh ? p.as_sf : p.a_sf) + (static_cast<size_t>(r0 + j) * parts + part) * (Fx >> 5);
+                }
+                const int nrow = part * mp + j;
+                cp_async4(sSF + 512 * ((ph < 2 ? 0 : q * g.nblk2) + (nrow >> 7)) + 16 * (nrow & 31) +
+                              4 * ((nrow >> 5) & 3),
+                          src + sb * 4);
+              }
+            }
+          }
+          cp_async_arrive(c->full + s);
+        }
+      }
+    }
+    cp_async_wait_all();
+  } else {
+    // ------------------------------------------------------------ router, epilogue
+    const int et = threadIdx.x - 128, q4 = warp & 3, half = (warp - 4) >> 2;
+    const int row = 32 * q4 + lane;  // the thread's column of the weight tile (TMEM lane)
+    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q4) << 16);
+    bool ok = few_route<MX>(p, c, et);
+    if (ok && et == 0) mbar_arrive(&c->plan);
+    int used[2] = {0, 0};
+    const FewGeo g = few_geo(p.P1, p.P2, p.T, ok ? c->mmax : p.T, MX);
+    float* acc = reinterpret_cast<float*>(smem + g.acc_off);
+    unsigned* cnt = p.cnt;
+    for (int ph = first_phase; ph < 3 && ok; ++ph) {
+      FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
+      FewChunk ch;
+      const int nbuf = ph < 2 ? g.nbuf1 : g.nbuf2;
+      const int acc_cols = ph < 2 ? 2 * g.n1 : g.n2;
+      const int parts = ph < 2 ? p.P1 : p.P2;
+      int na = 0;
+      while (ok && w.next(ch)) {
+        const int r0 = ch.i < 0 ? 0 : c->off[ch.i];
+        const int m = ch.i < 0 ? p.T : c->off[ch.i + 1] - r0;
+        const int mp = (m + 7) & ~7;
+        const int buf = na % nbuf;
+        ++na;
+        if (ph == 2 && ch.first) {
+          for (int i = et; i < p.T * 32; i += kFewEpi) reinterpret_cast<float4*>(acc)[i] = make_float4(0, 0, 0, 0);
+          epi_sync();
+        }
+        ok = epi_all(mbar_wait_bounded(c->tfull + buf, used[buf] & 1, abort_flag, p.lim, p.status, 92));
+        if (!ok) break;
+        ++used[buf];
+        tc_fence_after();
+        const uint32_t d0 = tl + buf * acc_cols + (ph < 2 ? half * g.n1 : 0);
+        for (int j0 = ph < 2 ? 0 : 8 * half; j0 < mp; j0 += ph < 2 ? 8 : 16) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+          for (int q = 0; q < parts; ++q) {
+            uint32_t r[8];
+            tmem_ld8(d0 + q * mp + j0, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(r[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (j0 + j < m) {
+              if (ph < 2) {
+                float* a = acc + (j0 + j) * 256 + half * 128 + row;
+                *a = ch.first ? v[j] : *a + v[j];
+              } else {
+                acc[(ch.i < 0 ? j0 + j : c->tok[r0 + j0 + j]) * 128 + row] += v[j];
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c->tempty + buf);
+        epi_sync();
+        if (!ch.last) continue;
+        const int ti = w.tile_index(), u0 = ti * w.per;
+        const FewSplit& s = w.s;
+        const int pieces = s.pieces(u0, u0 + w.per);
+        if (ph < 2) {
+          float* part = ph == 0 ? p.part0 : p.part1;
+          const size_t stride = static_cast<size_t>(p.T) * 256;
+          bool mine = true;
+          FewPieces pc{part, stride, s, u0, s.owner(u0), s.owner(u0 + w.per - 1)};
+          if (pieces > 1)
+            mine = few_leave(acc, m * 256, part, stride, s, u0, pieces, cnt + ti, c, et);
+          if (mine) {
+            few_activate<MX>(p, c, acc, pieces > 1 ? &pc : nullptr, m, ch.i, ch.tile, et);
+            __threadfence();
+          }
+          epi_sync();
+          if (mine && et == 0) red_release(p.sync + 2, 1u);
+        } else {
+          const size_t stride = static_cast<size_t>(p.T) * 128;
+          if (pieces == 1) {
+            for (int i = et; i < p.T * 128; i += kFewEpi) few_store_y(p, i >> 7, 128 * ch.tile + (i & 127), acc[i]);
+          } else if (few_leave(acc, p.T * 128, p.part2, stride, s, u0, pieces, cnt + ti, c, et)) {
+            const FewPieces pc{p.part2, stride, s, u0, s.owner(u0), s.owner(u0 + w.per - 1)};
+            for (int i = et; i < p.T * 128; i += kFewEpi)
+              few_store_y(p, i >> 7, 128 * ch.tile + (i & 127), pc.sum(i));
+          }
+          epi_sync();
+        }
+      }
+      cnt += ph == 0 ? p.ns1s : p.E * p.ns1;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0) {
+    // the last block to end leaves the counters at 0, as it found them
+    __threadfence();
+    if (atomicAdd(p.sync + 3, 1u) == gridDim.x - 1) {
+      for (int i = 0; i < 4; ++i) p.sync[i] = 0u;
+    }
+  }
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+static size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
+// Where things lie in the workspace
+struct FewLayout {
+  size_t logits, cnt, part0, part1, part2, a, as, a_sf, as_sf, xq, x_sf, total;
+  int cnt_words;
+};
+static int few_parts1(bool mx) { return mx ? 2 : 1; }
+static int few_parts2(const moe_config& c, bool mx) { return mx ? (c.out_fp32 ? 5 : 3) : (c.out_fp32 ? 3 : 2); }
+static FewLayout few_layout(const moe_config& c, bool mx, int G) {
+  FewLayout L{};
+  const size_t T = c.T, R = T * c.k, F = c.F, Fs = c.F_shared, H = c.H, P2 = few_parts2(c, mx);
+  const size_t eb = mx ? 1 : 2;
+  size_t o = sizeof(DevStatus);
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += up256(bytes);
+    return at;
+  };
+  L.cnt_words = (c.F_shared + 127) / 128 + c.E * ((c.F + 127) / 128) + (c.H + 127) / 128;
+  L.logits = take(4 * T * c.E);
+  L.cnt = take(4 * static_cast<size_t>(L.cnt_words));
+  // a block's two partials of a phase
+  L.part0 = take(Fs ? 2 * static_cast<size_t>(G) * T * 256 * 4 : 0);
+  L.part1 = take(2 * static_cast<size_t>(G) * T * 256 * 4);
+  L.part2 = take(2 * static_cast<size_t>(G) * T * 128 * 4);
+  L.a = take(R * P2 * F * eb);
+  L.as = take(T * P2 * Fs * eb);
+  if (mx) {
+    L.a_sf = take(R * P2 * F / 32);
+    L.as_sf = take(T * P2 * Fs / 32);
+    L.xq = take(T * 2 * H);
+    L.x_sf = take(T * 2 * H / 32);
+  }
+  L.total = o;
+  return L;
+}
+
+size_t few_workspace_bytes(const moe_config& c, bool mx) { return few_layout(c, mx, num_sms()).total; }
+
+template <bool MX>
+static cudaError_t few_start(const FewParams& p, const FewMaps& maps, cudaStream_t st) {
+  static std::atomic<unsigned long long> set{0};  // devices whose kernel has its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(set.load() & bit)) {
+    e = cudaFuncSetAttribute(few_kernel<MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit);
+  }
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeCooperative;  // the blocks wait for one another
+  attr.val.cooperative = 1;
+  cfg.gridDim = dim3(num_sms());
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = kFewSmem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few_kernel<MX>, p, maps);
+}
+
+int run_few(const moe_config& c, const FewArgs& q, bool mx, void* ws, cudaStream_t st) {
+  const int G = num_sms();
+  const FewLayout L = few_layout(c, mx, G);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  FewParams p{};
+  p.T = c.T; p.H = c.H; p.E = c.E; p.k = c.k; p.F = c.F; p.Fs = c.F_shared;
+  const bool grouped = !c.force_balanced && c.n_groups > 1 && c.topk_groups < c.n_groups;
+  const bool softmax = c.score == MOE_SCORE_SOFTMAX;
+  p.mode = !softmax ? RSEL_SIGMOID : ((q.expert_bias == nullptr && !grouped) ? RSEL_LOGIT : RSEL_SOFTMAX);
+  p.groups = grouped ? c.n_groups : 1;
+  p.topk_groups = c.topk_groups;
+  p.force = c.force_balanced;
+  p.gate_scale = c.gate_scale;
+  p.P1 = few_parts1(mx);
+  p.P2 = few_parts2(c, mx);
+  const int ks = mx ? 128 : 64;
+  // the tensor cores' sums round towards zero: fp32 results take them in runs of 128
+  // products (512 under block scales, which lose less), joined in fp32
+  p.flush = c.out_fp32 ? (mx ? 512 : 128) / ks : 1 << 30;
+  p.out_fp32 = c.out_fp32;
+  p.ns1 = (c.F + 127) / 128;
+  p.ns1s = (c.F_shared + 127) / 128;
+  p.ns2 = (c.H + 127) / 128;
+  p.nsb1 = c.H / ks;
+  p.nsb2 = c.F / ks;
+  p.nsb2s = c.F_shared / ks;
+  p.x = q.x; p.wr = q.router_w; p.eb = q.expert_bias; p.lb = q.logit_bias;
+  p.idx = q.topk_idx; p.gate = q.topk_gate; p.y = q.y;
+  p.status = reinterpret_cast<DevStatus*>(base);
+  p.sync = reinterpret_cast<unsigned*>(base + 64);
+  p.logits = reinterpret_cast<float*>(base + L.logits);
+  p.cnt = reinterpret_cast<unsigned*>(base + L.cnt);
+  p.cnt_words = L.cnt_words;
+  p.part0 = reinterpret_cast<float*>(base + L.part0);
+  p.part1 = reinterpret_cast<float*>(base + L.part1);
+  p.part2 = reinterpret_cast<float*>(base + L.part2);
+  p.a = base + L.a; p.as = base + L.as; p.a_sf = base + L.a_sf; p.as_sf = base + L.as_sf;
+  p.xq = base + L.xq; p.x_sf = base + L.x_sf;
+  p.lim = wait_limit_ns();
+  FewMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  bool ok = true;
+  if (mx) {
+    const moe_mx4_weights& w = *q.mx4;
+    p.sf13 = w.sf13; p.sf2 = w.sf2; p.sf13s = w.sf13s; p.sf2s = w.sf2s;
+    ok = make_map_fp4(&maps.m[0], w.w13, static_cast<uint64_t>(c.E) * p.ns1 * p.nsb1 * 256) &&
+         make_map_fp4(&maps.m[2], w.w2, static_cast<uint64_t>(c.E) * p.ns2 * p.nsb2 * 128);
+    if (c.F_shared)
+      ok = ok && make_map_fp4(&maps.m[3], w.w13s, static_cast<uint64_t>(p.ns1s) * p.nsb1 * 256) &&
+           make_map_fp4(&maps.m[5], w.w2s, static_cast<uint64_t>(p.ns2) * p.nsb2s * 128);
+  } else {
+    const uint64_t E = c.E, H = c.H, F = c.F, Fs = c.F_shared;
+    ok = make_map_bf16(&maps.m[0], q.W1, F, E * H, 2 * F, 64, 64) && make_map_bf16(&maps.m[1], q.W3, F, E * H, 2 * F, 64, 64) &&
+         make_map_bf16(&maps.m[2], q.W2, H, E * F, 2 * H, 64, 64);
+    if (Fs)
+      ok = ok && make_map_bf16(&maps.m[3], q.Ws1, Fs, H, 2 * Fs, 64, 64) &&
+           make_map_bf16(&maps.m[4], q.Ws3, Fs, H, 2 * Fs, 64, 64) && make_map_bf16(&maps.m[5], q.Ws2, H, Fs, 2 * H, 64, 64);
+  }
+  if (!ok) return MOE_ERR_CUDA;
+  return status_from_cuda(mx ? few_start<true>(p, maps, st) : few_start<false>(p, maps, st));
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+static int check_few(const moe_config* cfg, bool mx) {
+  const int s = validate_config(cfg);
+  if (s != MOE_OK) return s;
+  const int unit = mx ? 128 : 64;
+  if (cfg->T > MOE_FEW_MAX_T || cfg->H % unit || cfg->F % unit || cfg->F_shared % unit) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // tile and unit counts stay within 32 bits
+  if (cfg->H > (1 << 17) || cfg->F > (1 << 17) || cfg->F_shared > (1 << 17)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+static bool few_aligned(std::initializer_list<const void*> ps, uintptr_t to) {
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) & (to - 1)) return false;
+  return true;
+}
+static int few_call(const moe_config* cfg, const FewArgs& q, bool mx, void* ws, size_t ws_bytes, void* stream) {
+  if (!q.x || !q.router_w || !q.topk_idx || !q.topk_gate || !q.y || !ws) return MOE_ERR_INVALID_ARG;
+  if (!few_aligned({q.x, q.router_w, q.expert_bias, q.logit_bias, q.topk_idx, q.topk_gate, q.y, ws}, 16))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < few_workspace_bytes(*cfg, mx)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int r = run_few(*cfg, q, mx, ws, s);
+  if (r == MOE_OK) record_stage(s, 50, 1);
+  return r;
+}
+
+extern "C" {
+
+size_t moe_few_workspace_bytes(const moe_config* cfg, int mxfp4) {
+  return check_few(cfg, mxfp4 != 0) != MOE_OK ? 0 : few_workspace_bytes(*cfg, mxfp4 != 0);
+}
+
+int moe_layer_few_fwd(const moe_config* cfg, const moe_bf16* x, const moe_bf16* router_w, const float* expert_bias,
+                      const float* logit_bias, const moe_bf16* W1, const moe_bf16* W3, const moe_bf16* W2,
+                      const moe_bf16* Ws1, const moe_bf16* Ws3, const moe_bf16* Ws2, int32_t* topk_idx,
+                      float* topk_gate, void* y, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx("moe_layer_few_fwd");
+  const int s = check_few(cfg, false);
+  if (s != MOE_OK) return s;
+  if (!W1 || !W3 || !W2 || (cfg->F_shared && (!Ws1 || !Ws3 || !Ws2))) return MOE_ERR_INVALID_ARG;
+  if (!few_aligned({W1, W3, W2, Ws1, Ws3, Ws2}, 16)) return MOE_ERR_INVALID_ARG;
+  auto b = [](const moe_bf16* v) { return reinterpret_cast<const __nv_bfloat16*>(v); };
+  const FewArgs q{b(x), b(router_w), expert_bias, logit_bias, b(W1), b(W3), b(W2), b(Ws1), b(Ws3), b(Ws2), nullptr,
+                  topk_idx, topk_gate, y};
+  return few_call(cfg, q, false, ws, ws_bytes, stream);
+}
+
+int moe_layer_few_fwd_mxfp4(const moe_config* cfg, const moe_bf16* x, const moe_bf16* router_w,
+                            const float* expert_bias, const float* logit_bias, const moe_mx4_weights* w,
+                            int32_t* topk_idx, float* topk_gate, void* y, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx("moe_layer_few_fwd_mxfp4");
+  const int s = check_few(cfg, true);
+  if (s != MOE_OK) return s;
+  if (!w || !w->w13 || !w->sf13 || !w->w2 || !w->sf2) return MOE_ERR_INVALID_ARG;
+  if (cfg->F_shared && (!w->w13s || !w->sf13s || !w->w2s || !w->sf2s)) return MOE_ERR_INVALID_ARG;
+  if (!few_aligned({w->w13, w->w2, w->w13s, w->w2s}, 32) || !few_aligned({w->sf13, w->sf2, w->sf13s, w->sf2s}, 16))
+    return MOE_ERR_INVALID_ARG;
+  auto b = [](const moe_bf16* v) { return reinterpret_cast<const __nv_bfloat16*>(v); };
+  const FewArgs q{b(x), b(router_w), expert_bias, logit_bias, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, w,
+                  topk_idx, topk_gate, y};
+  return few_call(cfg, q, true, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

@@ -31,6 +31,11 @@ struct NvtxRange {
 bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                    uint32_t box_inner, uint32_t box_outer);
 
+// 2-D map over `rows` rows of 128 four-bit elements (64 bytes), boxes of 128 rows; a
+// row takes 128 bytes of shared memory, 16 elements in the first 8 of every 16
+// bytes, 128-byte swizzle. A box announces the 8192 bytes it reads.
+bool make_map_fp4(CUtensorMap* m, const void* base, uint64_t rows);
+
 int num_sms();
 
 // two arrays of `a_bytes` and `b_bytes` that share memory
@@ -72,6 +77,8 @@ void record_stage(cudaStream_t s, int tag, int launches);
 // MOE_OK for cudaSuccess, else MOE_ERR_CUDA with the CUDA message on stderr.
 int status_from_cuda(cudaError_t e);
 unsigned long long wait_limit_ns();
+// the checks of a layer's config that every entry point makes
+int validate_config(const moe_config* c);
 int debug_fault();
 
 // 3-D fp32 tensor map over [outer2, outer1, inner] (row-major), box
@@ -83,6 +90,19 @@ bool make_map_f32_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t 
 cudaError_t launch_gemm(int kind, const GemmParams& p, const CUtensorMap& ma, const CUtensorMap& mb0,
                         const CUtensorMap& mb1, int grid, cudaStream_t st, const CUtensorMap* out0 = nullptr,
                         const CUtensorMap* out1 = nullptr);
+
+// few.cu: the whole layer for a few tokens; mx: MXFP4 weights
+struct FewArgs {
+  const __nv_bfloat16 *x, *router_w;
+  const float *expert_bias, *logit_bias;
+  const __nv_bfloat16 *W1, *W3, *W2, *Ws1, *Ws3, *Ws2;
+  const moe_mx4_weights* mx4;
+  int32_t* topk_idx;
+  float* topk_gate;
+  void* y;
+};
+size_t few_workspace_bytes(const moe_config& c, bool mx);
+int run_few(const moe_config& c, const FewArgs& q, bool mx, void* ws, cudaStream_t st);
 
 // permute.cu
 // With x_q != nullptr the permute writes MXFP8 rows (x_q [R, H] codes and the

@@ -1,0 +1,311 @@
+// MXFP4 (OCP Microscaling Formats v1.0, MXFP4): blocks of 32 consecutive elements
+// along the contraction share a power of two 2^s, s = floor(log2 max|v|) - 2 clamped to
+// [-127, 127] (-127 for a block of zeros), kept as the E8M0 byte s + 127; an element is
+// v / 2^s rounded to E2M1 (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6; to nearest, ties to the
+// even code, saturating at 6). A block with an infinity or a NaN has the byte 255: all of
+// it stands for NaN.
+//
+// All kernels here move bytes: per element 2 of bf16 one way and 17/32 of codes and
+// scales the other. Rows: four lanes a block, so that every access of a warp is
+// contiguous. Weights: a block of threads turns a tile of 128 k x 128 columns, its
+// loads 128 bytes of a weight row a warp, and stages the codes in shared memory, which
+// then leave as the 8 KB run that few.cuh's copies read.
+#include <cuda_fp4.h>
+
+#include <initializer_list>
+
+#include "host_util.h"
+
+namespace moe {
+
+// scale byte of a block of maximum amax; 255: it holds an infinity or a NaN (bad)
+__device__ __forceinline__ uint32_t mx4_scale_byte(float amax, bool bad) {
+  const uint32_t e = __float_as_uint(amax) >> 23;
+  if (bad || e == 255u) return 255u;
+  return e > 2u ? e - 2u : 0u;
+}
+// v / 2^s as a factor: s + 127 = sb <= 252, so that 2^-s is a normal fp32 number
+__device__ __forceinline__ float mx4_inverse(uint32_t sb) {
+  return sb == 255u ? 0.0f : __uint_as_float((254u - sb) << 23);
+}
+// 2^s (a subnormal fp32 number for sb = 0), NaN for 255
+__device__ __forceinline__ float mx4_scale(uint32_t sb) {
+  return sb == 255u ? __uint_as_float(0x7fc00000u) : sb == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(sb << 23);
+}
+__device__ __forceinline__ uint32_t mx4_pair(float lo, float hi) {
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest));
+}
+// value of a code: s eem
+__device__ __forceinline__ float mx4_value(uint32_t c) {
+  const uint32_t e = (c >> 1) & 3u, m = c & 1u;
+  const float v = e == 0 ? 0.5f * static_cast<float>(m) : __uint_as_float(((e + 126u) << 23) | (m << 22));
+  return (c & 8u) ? -v : v;
+}
+
+// x [M, K] -> q [M, K/2], s [M, K/32]; a thread 8 elements, four to a block
+__global__ void __launch_bounds__(256) mx4_quantize_kernel(const __nv_bfloat16* x, long long n8, uint8_t* q,
+                                                           uint8_t* s) {
+  chain_wait();
+  const long long step = static_cast<long long>(gridDim.x) * 256;
+  // (whole groups of four lanes run or skip: n8 is a multiple of 4)
+  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += step) {
+    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(x) + i);
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    float v[8], amax = 0.0f;
+    int bad = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_lo(ww[j]);
+      v[2 * j + 1] = bf16_hi(ww[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      amax = fmaxf(amax, fabsf(v[j]));
+      bad |= v[j] != v[j] ? 1 : 0;
+    }
+    const unsigned group = 0xFu << (threadIdx.x & 28);
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+      amax = fmaxf(amax, __shfl_xor_sync(group, amax, d));
+      bad |= __shfl_xor_sync(group, bad, d);
+    }
+    const uint32_t sb = mx4_scale_byte(amax, bad != 0);
+    const float inv = mx4_inverse(sb);
+    uint32_t c = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float lo = sb == 255u ? 0.0f : v[2 * j] * inv, hi = sb == 255u ? 0.0f : v[2 * j + 1] * inv;
+      c |= mx4_pair(lo, hi) << (8 * j);
+    }
+    reinterpret_cast<uint32_t*>(q)[i] = c;
+    if ((threadIdx.x & 3) == 0) s[i >> 2] = static_cast<uint8_t>(sb);
+  }
+}
+
+__device__ __forceinline__ uint4 mx4_expand(uint32_t c, float scale) {
+  uint32_t r[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    r[j] = pack_bf16x2(mx4_value(c >> (8 * j)) * scale, mx4_value(c >> (8 * j + 4)) * scale);
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// the way back, exact (every value is a bf16 number); a thread 8 elements
+__global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t* q, const uint8_t* s, long long n8,
+                                                             __nv_bfloat16* x) {
+  chain_wait();
+  const long long step = static_cast<long long>(gridDim.x) * 256;
+  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += step) {
+    const uint32_t c = __ldcg(reinterpret_cast<const uint32_t*>(q) + i);
+    reinterpret_cast<uint4*>(x)[i] = mx4_expand(c, mx4_scale(__ldcg(s + (i >> 2))));
+  }
+}
+
+// A weight [E][K][N] bf16 and where its tiles go: tile (e, column block nb, k block kb)
+// is code block (e nblocks + nb) nkb + kb of `tiles` 8 KB tiles (W1 and W3 interleave:
+// tiles = 2), `which` of them; its 512 scale bytes likewise.
+struct Mx4Weight {
+  const __nv_bfloat16* w;
+  __nv_bfloat16* out;  // the way back
+  uint8_t *q, *sf;
+  int K, N, tiles, which;
+  long long first;     // its first tile among all of the launch
+};
+struct Mx4Weights {
+  Mx4Weight w[6];
+  int n;
+  long long total;
+};
+
+// code tile: column r's 128 elements along k are bytes 64 r ..; scale byte
+// 16 (r % 32) + 4 (r / 32) + b that of its block b
+template <bool BACK>
+__global__ void __launch_bounds__(256) mx4_weights_kernel(const __grid_constant__ Mx4Weights a) {
+  __shared__ __align__(16) uint8_t codes[128 * 64];
+  __shared__ __align__(16) uint8_t scales[512];
+  chain_wait();
+  const int warp = warp_id(), lane = lane_id();
+  const int b = warp & 3, col = (warp >> 2) * 64 + 2 * lane;  // the thread's block along k and its two columns
+  for (long long t = blockIdx.x; t < a.total; t += gridDim.x) {
+    int i = 0;
+    while (i + 1 < a.n && t >= a.w[i + 1].first) ++i;
+    const Mx4Weight& w = a.w[i];
+    const int nkb = w.K >> 7, nnb = w.N >> 7;
+    const long long r = t - w.first;
+    // columns innermost: neighbouring blocks read neighbouring parts of the weight's rows
+    const int nb = static_cast<int>(r % nnb);
+    const long long r2 = r / nnb;
+    const int kb = static_cast<int>(r2 % nkb);
+    const long long e = r2 / nkb;
+    const long long blk = ((e * nnb + nb) * nkb + kb) * w.tiles + w.which;
+    const size_t at = (static_cast<size_t>(e) * w.K + 128 * kb + 32 * b) * w.N + 128 * nb + col;
+    if constexpr (!BACK) {
+      uint32_t v[32];
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(w.w + at);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __ldcs(src + static_cast<size_t>(j) * (w.N >> 1));
+      float m0 = 0.0f, m1 = 0.0f;
+      bool bad0 = false, bad1 = false;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float x0 = bf16_lo(v[j]), x1 = bf16_hi(v[j]);
+        m0 = fmaxf(m0, fabsf(x0));
+        m1 = fmaxf(m1, fabsf(x1));
+        bad0 |= x0 != x0;
+        bad1 |= x1 != x1;
+      }
+      const uint32_t s0 = mx4_scale_byte(m0, bad0), s1 = mx4_scale_byte(m1, bad1);
+      const float i0 = mx4_inverse(s0), i1 = mx4_inverse(s1);
+      uint32_t c0[4] = {0, 0, 0, 0}, c1[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        c0[j >> 2] |= mx4_pair(bf16_lo(v[2 * j]) * i0, bf16_lo(v[2 * j + 1]) * i0) << (8 * (j & 3));
+        c1[j >> 2] |= mx4_pair(bf16_hi(v[2 * j]) * i1, bf16_hi(v[2 * j + 1]) * i1) << (8 * (j & 3));
+      }
+      if (s0 == 255u) c0[0] = c0[1] = c0[2] = c0[3] = 0u;
+      if (s1 == 255u) c1[0] = c1[1] = c1[2] = c1[3] = 0u;
+      __syncthreads();  // the tile before has left
+      *reinterpret_cast<uint4*>(codes + col * 64 + b * 16) = make_uint4(c0[0], c0[1], c0[2], c0[3]);
+      *reinterpret_cast<uint4*>(codes + (col + 1) * 64 + b * 16) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+      scales[16 * (col & 31) + 4 * (col >> 5) + b] = static_cast<uint8_t>(s0);
+      scales[16 * ((col + 1) & 31) + 4 * (col >> 5) + b] = static_cast<uint8_t>(s1);
+      __syncthreads();
+      uint4* q = reinterpret_cast<uint4*>(w.q + blk * 8192);
+      for (int k = threadIdx.x; k < 512; k += 256) q[k] = reinterpret_cast<const uint4*>(codes)[k];
+      if (threadIdx.x < 32) reinterpret_cast<uint4*>(w.sf + blk * 512)[threadIdx.x] = reinterpret_cast<const uint4*>(scales)[threadIdx.x];
+    } else {
+      __syncthreads();
+      const uint4* q = reinterpret_cast<const uint4*>(w.q + blk * 8192);
+      for (int k = threadIdx.x; k < 512; k += 256) reinterpret_cast<uint4*>(codes)[k] = __ldcg(q + k);
+      if (threadIdx.x < 32) reinterpret_cast<uint4*>(scales)[threadIdx.x] = __ldcg(reinterpret_cast<const uint4*>(w.sf + blk * 512) + threadIdx.x);
+      __syncthreads();
+      const uint4 a0 = *reinterpret_cast<const uint4*>(codes + col * 64 + b * 16);
+      const uint4 a1 = *reinterpret_cast<const uint4*>(codes + (col + 1) * 64 + b * 16);
+      const uint32_t c0[4] = {a0.x, a0.y, a0.z, a0.w}, c1[4] = {a1.x, a1.y, a1.z, a1.w};
+      const float f0 = mx4_scale(scales[16 * (col & 31) + 4 * (col >> 5) + b]);
+      const float f1 = mx4_scale(scales[16 * ((col + 1) & 31) + 4 * (col >> 5) + b]);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(w.out + at);
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        dst[static_cast<size_t>(j) * (w.N >> 1)] =
+            pack_bf16x2(mx4_value(c0[j >> 3] >> (4 * (j & 7))) * f0, mx4_value(c1[j >> 3] >> (4 * (j & 7))) * f1);
+    }
+  }
+}
+
+static int check_mx4(const moe_config* cfg) {
+  const int s = validate_config(cfg);
+  if (s != MOE_OK) return s;
+  if (cfg->H % 128 || cfg->F % 128 || cfg->F_shared % 128) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+static bool mx4_aligned(std::initializer_list<const void*> ps, uintptr_t to) {
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) & (to - 1)) return false;
+  return true;
+}
+
+static int mx4_weights(const moe_config* cfg, const void* const (&bf)[6], const moe_mx4_weights* w, bool back,
+                       void* stream) {
+  const int st = check_mx4(cfg);
+  if (st != MOE_OK) return st;
+  const moe_config& c = *cfg;
+  const int n = c.F_shared ? 6 : 3;
+  if (!w || !w->w13 || !w->sf13 || !w->w2 || !w->sf2) return MOE_ERR_INVALID_ARG;
+  if (c.F_shared && (!w->w13s || !w->sf13s || !w->w2s || !w->sf2s)) return MOE_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i)
+    if (!bf[i] || !mx4_aligned({bf[i]}, 16)) return MOE_ERR_INVALID_ARG;
+  if (!mx4_aligned({w->w13, w->w2, w->w13s, w->w2s}, 32) || !mx4_aligned({w->sf13, w->sf2, w->sf13s, w->sf2s}, 16))
+    return MOE_ERR_INVALID_ARG;
+  Mx4Weights a{};
+  a.n = n;
+  for (int i = 0; i < n; ++i) {
+    Mx4Weight& m = a.w[i];
+    const bool sh = i >= 3, down = i % 3 == 2;
+    const int F = sh ? c.F_shared : c.F;
+    m.w = static_cast<const __nv_bfloat16*>(bf[i]);
+    m.out = static_cast<__nv_bfloat16*>(const_cast<void*>(bf[i]));
+    m.q = down ? (sh ? w->w2s : w->w2) : (sh ? w->w13s : w->w13);
+    m.sf = down ? (sh ? w->sf2s : w->sf2) : (sh ? w->sf13s : w->sf13);
+    m.K = down ? F : c.H;
+    m.N = down ? c.H : F;
+    m.tiles = down ? 1 : 2;
+    m.which = down ? 0 : i % 3;
+    m.first = a.total;
+    a.total += static_cast<long long>(sh ? 1 : c.E) * (m.K / 128) * (m.N / 128);
+  }
+  const long long most = 8ll * num_sms();
+  const int grid = static_cast<int>(a.total < most ? a.total : most);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = back ? launch_chained(mx4_weights_kernel<true>, dim3(grid), dim3(256), 0, s, a)
+                             : launch_chained(mx4_weights_kernel<false>, dim3(grid), dim3(256), 0, s, a);
+  const int r = status_from_cuda(e);
+  if (r == MOE_OK) record_stage(s, back ? 52 : 51, 1);
+  return r;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_mx4_weight_bytes(const moe_config* cfg, int which) {
+  if (check_mx4(cfg) != MOE_OK) return 0;
+  const size_t F = which < 4 ? cfg->F : cfg->F_shared, n = static_cast<size_t>(which < 4 ? cfg->E : 1) * cfg->H * F;
+  switch (which & 3) {
+    case 0: return which < 8 && which >= 0 ? n : 0;            // w13, w13s
+    case 1: return which < 8 && which >= 0 ? n / 16 : 0;       // sf13, sf13s
+    case 2: return which < 8 && which >= 0 ? n / 2 : 0;        // w2, w2s
+    default: return which < 8 && which >= 0 ? n / 32 : 0;      // sf2, sf2s
+  }
+}
+
+int moe_mx4_quantize_weights(const moe_config* cfg, const moe_bf16* W1, const moe_bf16* W3, const moe_bf16* W2,
+                             const moe_bf16* Ws1, const moe_bf16* Ws3, const moe_bf16* Ws2, const moe_mx4_weights* w,
+                             void* stream) {
+  NvtxRange nvtx("moe_mx4_quantize_weights");
+  const void* bf[6] = {W1, W3, W2, Ws1, Ws3, Ws2};
+  return mx4_weights(cfg, bf, w, false, stream);
+}
+
+int moe_mx4_dequantize_weights(const moe_config* cfg, const moe_mx4_weights* w, moe_bf16* W1, moe_bf16* W3,
+                               moe_bf16* W2, moe_bf16* Ws1, moe_bf16* Ws3, moe_bf16* Ws2, void* stream) {
+  NvtxRange nvtx("moe_mx4_dequantize_weights");
+  const void* bf[6] = {W1, W3, W2, Ws1, Ws3, Ws2};
+  return mx4_weights(cfg, bf, w, true, stream);
+}
+
+static int mx4_rows_check(const void* x, long long M, int K, const uint8_t* q, const uint8_t* s) {
+  if (!x || !q || !s || M < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+  if (!mx4_aligned({x, q, s}, 16)) return MOE_ERR_INVALID_ARG;
+  if (K % 32 || M > (1ll << 60) / K) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+int moe_mx4_quantize(const moe_bf16* x, long long M, int K, uint8_t* q, uint8_t* scales, void* stream) {
+  NvtxRange nvtx("moe_mx4_quantize");
+  int r = mx4_rows_check(x, M, K, q, scales);
+  if (r != MOE_OK) return r;
+  const long long n8 = M * K / 8, blocks = (n8 + 255) / 256, most = 16ll * num_sms();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  r = status_from_cuda(launch_chained(mx4_quantize_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+                                      dim3(256), 0, s, reinterpret_cast<const __nv_bfloat16*>(x), n8, q, scales));
+  if (r == MOE_OK) record_stage(s, 51, 1);
+  return r;
+}
+
+int moe_mx4_dequantize(const uint8_t* q, const uint8_t* scales, long long M, int K, moe_bf16* x, void* stream) {
+  NvtxRange nvtx("moe_mx4_dequantize");
+  int r = mx4_rows_check(x, M, K, q, scales);
+  if (r != MOE_OK) return r;
+  const long long n8 = M * K / 8, blocks = (n8 + 255) / 256, most = 16ll * num_sms();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  r = status_from_cuda(launch_chained(mx4_dequantize_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+                                      dim3(256), 0, s, q, scales, n8, reinterpret_cast<__nv_bfloat16*>(x)));
+  if (r == MOE_OK) record_stage(s, 52, 1);
+  return r;
+}
+
+}  // extern "C"

@@ -187,6 +187,24 @@ def lib():
                   "moe_balance_loss_fwd", "moe_balance_loss_bwd", "moe_adapter_plan", "moe_adapter_fwd",
                   "moe_adapter_bwd", "moe_tensor_list_build", "moe_grad_norm", "moe_clip_grad_norm"):
             getattr(L, n).restype = c_int
+        L.moe_mx4_weight_bytes.restype = c_size_t
+        L.moe_mx4_weight_bytes.argtypes = [POINTER(MoeConfig), c_int]
+        L.moe_mx4_quantize.argtypes = [vp, c_longlong, c_int, vp, vp, vp]
+        L.moe_mx4_dequantize.argtypes = [vp, vp, c_longlong, c_int, vp, vp]
+        L.moe_mx4_quantize_weights.argtypes = [POINTER(MoeConfig)] + [vp] * 6 + [POINTER(MoeMx4Weights), vp]
+        L.moe_mx4_dequantize_weights.argtypes = [POINTER(MoeConfig), POINTER(MoeMx4Weights)] + [vp] * 7
+        L.moe_few_workspace_bytes.restype = c_size_t
+        L.moe_few_workspace_bytes.argtypes = [POINTER(MoeConfig), c_int]
+        L.moe_layer_few_fwd.argtypes = [POINTER(MoeConfig)] + [vp] * 14 + [c_size_t, vp]
+        L.moe_layer_few_fwd_mxfp4.argtypes = [POINTER(MoeConfig)] + [vp] * 4 + [POINTER(MoeMx4Weights)] + [vp] * 4 + [
+            c_size_t, vp]
+        L.moe_norm_workspace_bytes.restype = c_size_t
+        L.moe_norm_workspace_bytes.argtypes = [POINTER(MoeNormConfig)]
+        L.moe_block_norm_fwd.argtypes = [POINTER(MoeNormConfig)] + [vp] * 9
+        L.moe_block_norm_bwd.argtypes = [POINTER(MoeNormConfig)] + [vp] * 14 + [c_size_t, vp]
+        for n in ("moe_mx4_quantize", "moe_mx4_dequantize", "moe_mx4_quantize_weights", "moe_mx4_dequantize_weights",
+                  "moe_layer_few_fwd", "moe_layer_few_fwd_mxfp4", "moe_block_norm_fwd", "moe_block_norm_bwd"):
+            getattr(L, n).restype = c_int
         _lib = L
     return _lib
 
@@ -199,7 +217,8 @@ STAGE_NAMES = {20: "nv_quantize", 21: "nv_gemm", 22: "mx_quantize_tokens", 24: "
                17: "permute_bwd", 18: "router_wgrad", 19: "aux_loss", 30: "read_ceiling",
                31: "write_ceiling", 40: "grad_norm", 41: "grad_clip", 43: "balance_loss",
                44: "balance_loss_bwd", 45: "adapter_plan", 46: "adapter_shrink", 47: "adapter_expand",
-               48: "adapter_wgrad", 32: "nv_dgrad_down", 33: "nv_swiglu_bwd", 34: "nv_dgrad_gate_up"}
+               48: "adapter_wgrad", 50: "layer_few", 51: "mx4_quantize", 52: "mx4_dequantize",
+               53: "block_norm", 54: "block_norm_bwd", 55: "block_norm_sums", 32: "nv_dgrad_down", 33: "nv_swiglu_bwd", 34: "nv_dgrad_gate_up"}
 
 
 def profile_start(capacity: int) -> None:
@@ -1108,3 +1127,251 @@ def clip_grad_norm(tensors, max_norm, kind="l2", ws=None):
     return _norm_call("moe_clip_grad_norm", tensors, kind, ws,
                       lambda p, k, norm, w, nb: lib().moe_clip_grad_norm(p, k, float(max_norm), norm, w, nb,
                                                                          _stream()))
+
+
+# ---------------------------------------------------------------------------
+# MXFP4: rows and the layer's weights
+# ---------------------------------------------------------------------------
+class MoeMx4Weights(ctypes.Structure):
+    """Mirror of moe_mx4_weights (eight device pointers)."""
+    _fields_ = [(n, c_void_p) for n in ("w13", "sf13", "w2", "sf2", "w13s", "sf13s", "w2s", "sf2s")]
+
+
+def _mx4_rows(where, x, K):
+    if K < 1 or K % 32:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, f"{where}: rows must hold blocks of 32")
+    if x < 1:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: there must be rows")
+
+
+def mx4_quantize(x):
+    """MXFP4 of the rows of x [M, K] bf16 (K a multiple of 32): (codes [M, K/2]
+    uint8, element 2j in the low nibble, scales [M, K/32] uint8, E8M0)."""
+    w = "mx4_quantize"
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{w}: x must be a matrix")
+    M, K = x.shape
+    _mx4_rows(w, M, K)
+    xp = _arg(w, "x", x, torch.bfloat16, (M, K))
+    codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
+    _check(lib().moe_mx4_quantize(xp, M, K, codes.data_ptr(), scales.data_ptr(), _stream(x.get_device())),
+           "moe_mx4_quantize")
+    return codes, scales
+
+
+def mx4_dequantize(codes, scales):
+    """The values [M, K] bf16 that mx4_quantize's codes and scales stand for, exactly."""
+    w = "mx4_dequantize"
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{w}: codes must be a matrix")
+    M, K = codes.shape[0], 2 * codes.shape[1]
+    _mx4_rows(w, M, K)
+    cp = _arg(w, "codes", codes, torch.uint8, (M, K // 2))
+    d = codes.get_device()
+    sp = _arg(w, "scales", scales, torch.uint8, (M, K // 32), d)
+    x = torch.empty((M, K), dtype=torch.bfloat16, device=codes.device)
+    _check(lib().moe_mx4_dequantize(cp, sp, M, K, x.data_ptr(), _stream(d)), "moe_mx4_dequantize")
+    return x
+
+
+def _layer_weights(w, cfg, W1, W3, W2, Ws, d=None):
+    """The addresses of the layer's six bf16 weights, the shared expert's None without one."""
+    bf, Fs = torch.bfloat16, cfg.F_shared
+    p = [_arg(w, "W1", W1, bf, (cfg.E, cfg.H, cfg.F), d)]
+    d = W1.get_device()
+    p += [_arg(w, "W3", W3, bf, (cfg.E, cfg.H, cfg.F), d), _arg(w, "W2", W2, bf, (cfg.E, cfg.F, cfg.H), d)]
+    if not Fs:
+        return p + [None] * 3
+    if Ws is None or len(Ws) != 3:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{w}: Ws must be the shared expert's three weights")
+    return p + [_arg(w, "Ws1", Ws[0], bf, (cfg.H, Fs), d), _arg(w, "Ws3", Ws[1], bf, (cfg.H, Fs), d),
+                _arg(w, "Ws2", Ws[2], bf, (Fs, cfg.H), d)]
+
+
+def _mx4_sizes(cfg):
+    fields = [n for n, _ in MoeMx4Weights._fields_]
+    used = fields if cfg.F_shared else fields[:4]
+    return [(n, _size("moe_mx4_weight_bytes", cfg, i)) for i, n in enumerate(used)]
+
+
+def _mx4_struct(w, cfg, q, d):
+    got = {}
+    for n, size in _mx4_sizes(cfg):
+        if q.get(n) is None:
+            raise MoeError(MOE_ERR_INVALID_ARG, f"{w}: the weights lack {n}")
+        got[n] = _arg(w, n, q[n], torch.uint8, (size,), d)
+    return MoeMx4Weights(*[got.get(n) for n, _ in MoeMx4Weights._fields_])
+
+
+def mx4_quantize_weights(cfg, W1, W3, W2, Ws=None):
+    """MXFP4 weights of the layer, the shared expert's included (cfg.F_shared, Ws), for
+    layer_few_fwd_mxfp4: a dict of uint8 tensors."""
+    w = "mx4_quantize_weights"
+    p = _layer_weights(w, cfg, W1, W3, W2, Ws)
+    q = {n: torch.empty(size, dtype=torch.uint8, device=W1.device) for n, size in _mx4_sizes(cfg)}
+    d = W1.get_device()
+    _check(lib().moe_mx4_quantize_weights(ctypes.byref(cfg), *p, ctypes.byref(_mx4_struct(w, cfg, q, d)), _stream(d)),
+           "moe_mx4_quantize_weights")
+    return q
+
+
+def mx4_dequantize_weights(cfg, q):
+    """(W1, W3, W2, Ws) bf16 that mx4_quantize_weights' dict stands for, exactly (Ws:
+    the shared expert's three, None without one)."""
+    w = "mx4_dequantize_weights"
+    dev = q["w13"].device
+    st = _mx4_struct(w, cfg, q, _current_device())
+    new = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    E, H, F, Fs = cfg.E, cfg.H, cfg.F, cfg.F_shared
+    W = [new(E, H, F), new(E, H, F), new(E, F, H)]
+    Ws = [new(H, Fs), new(H, Fs), new(Fs, H)] if Fs else None
+    p = [t.data_ptr() for t in W] + ([t.data_ptr() for t in Ws] if Fs else [None] * 3)
+    _check(lib().moe_mx4_dequantize_weights(ctypes.byref(cfg), ctypes.byref(st), *p, _stream(dev.index)),
+           "moe_mx4_dequantize_weights")
+    return W[0], W[1], W[2], None if Ws is None else tuple(Ws)
+
+
+# ---------------------------------------------------------------------------
+# The whole layer for a few tokens
+# ---------------------------------------------------------------------------
+FEW_MAX_T = 64
+
+
+def few_workspace(cfg, mxfp4=False, device="cuda"):
+    """Workspace of layer_few_fwd (mxfp4: of layer_few_fwd_mxfp4). Two calls in flight
+    need two."""
+    return _scratch(_size("moe_few_workspace_bytes", cfg, int(mxfp4)), device)
+
+
+def _few_args(w, cfg, x, router_w, expert_bias, logit_bias, ws, y, mxfp4):
+    n = _size("moe_few_workspace_bytes", cfg, int(mxfp4))
+    xp = _arg(w, "x", x, torch.bfloat16, (cfg.T, cfg.H))
+    d, dev = x.get_device(), x.device
+    head = (xp, _arg(w, "router_w", router_w, torch.bfloat16, (cfg.E, cfg.H), d),
+            _arg(w, "expert_bias", expert_bias, torch.float32, (cfg.E,), d, optional=True),
+            _arg(w, "logit_bias", logit_bias, torch.float32, (cfg.E,), d, optional=True))
+    idx = torch.empty((cfg.T, cfg.k), dtype=torch.int32, device=dev)
+    gate = torch.empty((cfg.T, cfg.k), dtype=torch.float32, device=dev)
+    out = _out_dtype(cfg)
+    if y is None:
+        y = torch.empty((cfg.T, cfg.H), dtype=out, device=dev)
+        yp = y.data_ptr()
+    else:
+        yp = _arg(w, "y", y, out, (cfg.T, cfg.H), d)
+    ws = _scratch(n, dev) if ws is None else ws
+    tail = (idx.data_ptr(), gate.data_ptr(), yp, _ws_arg(w, ws, n, d), ws.numel(), _stream(d))
+    return head, tail, (y, idx, gate), d
+
+
+def layer_few_fwd(cfg, x, router_w, W1, W3, W2, expert_bias=None, logit_bias=None, Ws=None, ws=None, y=None):
+    """layer_fwd at inference for at most FEW_MAX_T tokens, in one kernel: (y [T, H],
+    topk_idx [T, k], topk_gate [T, k]). ws from few_workspace; y may be x."""
+    w = "layer_few_fwd"
+    head, tail, out, d = _few_args(w, cfg, x, router_w, expert_bias, logit_bias, ws, y, False)
+    _check(lib().moe_layer_few_fwd(ctypes.byref(cfg), *head, *_layer_weights(w, cfg, W1, W3, W2, Ws, d), *tail),
+           "moe_layer_few_fwd")
+    return out
+
+
+def layer_few_fwd_mxfp4(cfg, x, router_w, q, expert_bias=None, logit_bias=None, ws=None, y=None):
+    """layer_few_fwd with MXFP4 weights (q from mx4_quantize_weights); the activations
+    keep their precision. ws from few_workspace(cfg, mxfp4=True)."""
+    w = "layer_few_fwd_mxfp4"
+    head, tail, out, d = _few_args(w, cfg, x, router_w, expert_bias, logit_bias, ws, y, True)
+    _check(lib().moe_layer_few_fwd_mxfp4(ctypes.byref(cfg), *head, ctypes.byref(_mx4_struct(w, cfg, q, d)), *tail),
+           "moe_layer_few_fwd_mxfp4")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Norms before and after a block, its gate and the scaled residual
+# ---------------------------------------------------------------------------
+class MoeNormConfig(ctypes.Structure):
+    _fields_ = [("T", c_int), ("H", c_int), ("eps", c_float), ("residual", c_int), ("residual_scale", c_float),
+                ("gate", c_int), ("post", c_int), ("pre", c_int), ("residual_fp32", c_int), ("out_fp32", c_int)]
+
+
+GATE = {"none": 0, "channel": 1, "token": 2}
+
+
+def make_norm_config(T, H, eps=1e-6, residual=True, residual_scale=1.0, gate="none", post=False, pre=True,
+                     residual_fp32=False, out_fp32=False) -> MoeNormConfig:
+    """h = residual_scale residual + gate u, u = the norm of y (post) or y; n = the norm
+    of h (pre). out_fp32: y and n's gradient fp32, as the layer's y and dx."""
+    return MoeNormConfig(T, H, eps, int(residual), residual_scale, GATE[gate] if isinstance(gate, str) else gate,
+                         int(post), int(pre), int(residual_fp32), int(out_fp32))
+
+
+def norm_workspace(cfg, device="cuda"):
+    return _scratch(_size("moe_norm_workspace_bytes", cfg), device)
+
+
+def _norm_args(w, cfg, y, residual, post_weight, gate, pre_weight, d=None):
+    T, H, f32 = cfg.T, cfg.H, torch.float32
+    p = [_arg(w, "y", y, _out_dtype(cfg), (T, H), d)]
+    d = y.get_device()
+    stream = f32 if cfg.residual_fp32 else torch.bfloat16
+    vec = lambda name, t, on, shape: _arg(w, name, t, f32, shape, d) if on else None
+    return p + [_arg(w, "residual", residual, stream, (T, H), d) if cfg.residual else None,
+                vec("post_weight", post_weight, cfg.post, (H,)),
+                vec("gate", gate, cfg.gate, (T,) if cfg.gate == 2 else (H,)),
+                vec("pre_weight", pre_weight, cfg.pre, (H,))], d, stream
+
+
+def block_norm_fwd(cfg, y, residual=None, post_weight=None, gate=None, pre_weight=None, h=None, n=None):
+    """(h [T, H], n [T, H] bf16 or None, stats [T, 2] for the backward) of the block's
+    output y (cfg from make_norm_config). residual and h bf16 (fp32 with
+    cfg.residual_fp32), weights [H] and gate [H] or [T] fp32. h may be residual."""
+    w = "block_norm_fwd"
+    _size("moe_norm_workspace_bytes", cfg)
+    p, d, stream = _norm_args(w, cfg, y, residual, post_weight, gate, pre_weight)
+    T, H, dev = cfg.T, cfg.H, y.device
+    h = torch.empty((T, H), dtype=stream, device=dev) if h is None else h
+    if cfg.pre and n is None:
+        n = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    stats = torch.empty((T, 2), dtype=torch.float32, device=dev)
+    st = lib().moe_block_norm_fwd(ctypes.byref(cfg), *p, _arg(w, "h", h, stream, (T, H), d),
+                                  _arg(w, "n", n, torch.bfloat16, (T, H), d) if cfg.pre else None, stats.data_ptr(),
+                                  _stream(d))
+    _check(st, "moe_block_norm_fwd")
+    return h, n if cfg.pre else None, stats
+
+
+def alloc_norm_grads(cfg, device="cuda"):
+    T, H, f32 = cfg.T, cfg.H, torch.float32
+    new = lambda dt, *shape: torch.empty(shape, dtype=dt, device=device)
+    g = {"dy": new(torch.bfloat16, T, H)}
+    if cfg.residual:
+        g["dresidual"] = new(f32 if cfg.residual_fp32 else torch.bfloat16, T, H)
+    if cfg.post:
+        g["dpost"] = new(f32, H)
+    if cfg.gate:
+        g["dgate"] = new(f32, T if cfg.gate == 2 else H)
+    if cfg.pre:
+        g["dpre"] = new(f32, H)
+    return g
+
+
+def block_norm_bwd(cfg, dn, y, stats, dh=None, residual=None, post_weight=None, gate=None, pre_weight=None, ws=None,
+                   grads=None):
+    """Gradients of block_norm_fwd from those of n (dn [T, H], bf16, fp32 with
+    cfg.out_fp32; None without pre) and of h (dh as residual; None: zeros): dict with
+    dy [T, H] bf16 and, where cfg has them, dresidual, dpost, dgate, dpre."""
+    w = "block_norm_bwd"
+    nb = _size("moe_norm_workspace_bytes", cfg)
+    p, d, stream = _norm_args(w, cfg, y, residual, post_weight, gate, pre_weight)
+    T, H, f32 = cfg.T, cfg.H, torch.float32
+    dhp = _arg(w, "dh", dh, stream, (T, H), d, optional=True)
+    dnp = _arg(w, "dn", dn, _out_dtype(cfg), (T, H), d) if cfg.pre else None
+    sp = _arg(w, "stats", stats, f32, (T, 2), d)
+    ws = _scratch(nb, y.device) if ws is None else ws
+    wp = _ws_arg(w, ws, nb, d)
+    g = alloc_norm_grads(cfg, y.device) if grads is None else grads
+    out = lambda name, on, dt, shape: _arg(w, name, g.get(name), dt, shape, d) if on else None
+    st = lib().moe_block_norm_bwd(ctypes.byref(cfg), dhp, dnp, *p, sp, out("dy", True, torch.bfloat16, (T, H)),
+                                  out("dresidual", cfg.residual, stream, (T, H)), out("dpost", cfg.post, f32, (H,)),
+                                  out("dgate", cfg.gate, f32, (T,) if cfg.gate == 2 else (H,)),
+                                  out("dpre", cfg.pre, f32, (H,)), wp, ws.numel(), _stream(d))
+    _check(st, "moe_block_norm_bwd")
+    return g
