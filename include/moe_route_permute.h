@@ -723,25 +723,19 @@ int moe_mx4_quantize(const moe_bf16* x, long long M, int K, uint8_t* q, uint8_t*
 int moe_mx4_dequantize(const uint8_t* q, const uint8_t* scales, long long M, int K, moe_bf16* x, void* stream);
 
 /* The layer's quantised weights, device buffers owned by the caller (sizes from
- * moe_mx4_weight_bytes; codes 32-byte aligned), written by
- * moe_mx4_quantize_weights: W1 and W3 in blocks along H, W2 along F, in tiles of
- * 128 columns x 128 elements of k (opaque: w13 tile (e, f / 128, h / 128) is 16 KB,
- * W1's 128 columns of 64 bytes, then W3's; w2 tile (e, h / 128, f / 128) 8 KB; sf13,
- * sf2 hold 512 bytes for 128 columns, byte 16 (c % 32) + 4 (c / 32) + b the scale of
- * column c's block b). w13s .. sf2s: the shared expert's, NULL without one. Requires H, F
- * and F_shared multiples of 128. */
+ * moe_mx4_weight_bytes), written by moe_mx4_quantize_weights: W1 and W3 in blocks
+ * along H, W2 along F. Opaque: tiles of 128 columns x 256 elements of k (zeros beyond
+ * the last), 16 KB of codes and 1 KB of scales each; w13 tile pair (e, f / 128,
+ * h / 256) is W1's, then W3's, w2 tile (e, h / 128, f / 256) W2's. w13s, w2s: the
+ * shared expert's, NULL without one. Requires H, F and F_shared multiples of 128. */
 typedef struct {
   uint8_t* w13;
-  uint8_t* sf13;
   uint8_t* w2;
-  uint8_t* sf2;
   uint8_t* w13s;
-  uint8_t* sf13s;
   uint8_t* w2s;
-  uint8_t* sf2s;
 } moe_mx4_weights;
 
-/* Bytes of the buffers, which = 0..7 in field order (0 for an invalid config or
+/* Bytes of the buffers, which = 0..3 in field order (0 for an invalid config or
  * shape, and for the shared expert's without one). */
 size_t moe_mx4_weight_bytes(const moe_config* cfg, int which);
 
@@ -779,9 +773,9 @@ int moe_layer_few_fwd(const moe_config* cfg, const moe_bf16* x, const moe_bf16* 
                       float* topk_gate, void* y, void* ws, size_t ws_bytes, void* stream);
 
 /* The same with MXFP4 weights, the shared expert's included. The activations keep
- * their precision: x and a enter the products in E4M3 parts with a power of two for
- * 32 elements, x in two (exact unless an element lies 2^-15 below its block's
- * largest, 2^-22 of that then), a in three (2^-12; five, 2^-20, with out_fp32). */
+ * their precision: x and a enter the products as sums of five MXFP4 parts (eight with
+ * out_fp32), each 3 bits below the one before: an element is off by at most 2^-13
+ * (2^-22) of the largest of its 32. */
 int moe_layer_few_fwd_mxfp4(const moe_config* cfg, const moe_bf16* x, const moe_bf16* router_w,
                             const float* expert_bias, const float* logit_bias, const moe_mx4_weights* w,
                             int32_t* topk_idx, float* topk_gate, void* y, void* ws, size_t ws_bytes, void* stream);

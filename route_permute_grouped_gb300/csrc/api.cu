@@ -135,19 +135,6 @@ static bool make_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64
   return r == CUDA_SUCCESS;
 }
 
-bool make_map_fp4(CUtensorMap* m, const void* base, uint64_t rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {128, rows};
-  cuuint64_t strides[1] = {64};
-  cuuint32_t box[2] = {128, 128};
-  cuuint32_t es[2] = {1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void*>(base), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 bool make_map_f32_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t mid, uint64_t outer) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;

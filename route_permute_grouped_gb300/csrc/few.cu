@@ -1,11 +1,14 @@
 // The whole MoE layer for a few tokens in one kernel (few.cuh: what bounds it, the
 // schedule and the operands).
+#include <cuda_fp4.h>
 #include <string.h>
 
 #include <atomic>
 #include <initializer_list>
+#include <type_traits>
 
 #include "few.cuh"
+#include "router_sel.cuh"
 
 namespace moe {
 
@@ -17,7 +20,8 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "r"(taddr));
 }
 // One block's forms of the block-scaled MMA and of the scales' copy (common.cuh has
-// the pairs'): A is E2M1, 16 elements in the first 8 of 16 bytes, B E4M3.
+// the pairs'): E2M1 operands two to a byte, K = 64, two E8M0 scales a row, the bytes 0, 1
+// or 2, 3 of a cell by the descriptor's scale ids.
 __device__ __forceinline__ void umma_mx_w(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t d_hi, uint32_t idesc,
                                           uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
@@ -25,7 +29,7 @@ __device__ __forceinline__ void umma_mx_w(uint32_t d_tmem, uint32_t a_lo, uint32
       "setp.ne.b32 p, %7, 0;\n\t"
       "mov.b64 da, {%1, %3};\n\t"
       "mov.b64 db, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, %4, [%5], [%6], p;\n\t}" ::"r"(
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %4, [%5], [%6], p;\n\t}" ::"r"(
           d_tmem),
       "r"(a_lo), "r"(b_lo), "r"(d_hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
@@ -33,8 +37,26 @@ __device__ __forceinline__ void umma_mx_w(uint32_t d_tmem, uint32_t a_lo, uint32
 __device__ __forceinline__ void tmem_cp_32x128b_x4(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
-// kind::mxf8f6f4 with E2M1 A (format 5), E4M3 B, both K-major
-__device__ __forceinline__ uint32_t idesc_mxf4f8(int N) { return idesc_mxf8_f32(128, N) | (5u << 7); }
+// kind::mxf4: E2M1 A and B (format 1), E8M0 scales (bit 23)
+__device__ __forceinline__ uint32_t idesc_mxf4(int N) { return idesc_nvf4_f32(128, N) | (1u << 23); }
+
+// weights on their way into L2 before their stage is free
+__device__ __forceinline__ void l2_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void bulk_load_hint(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar)), "l"(pol)
+      : "memory");
+}
 
 __device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
   unsigned v;
@@ -44,8 +66,9 @@ __device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
 __device__ __forceinline__ void red_release(unsigned* p, unsigned v) {
   asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok) {
+  const int n = ok ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
 // Wait (bounded) until *p has reached n. False when the wait ran out or the block gave up.
@@ -102,85 +125,104 @@ __device__ __forceinline__ uint32_t sort_key(float z) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// value of an E4M3 byte that is no NaN
-__device__ __forceinline__ float e4m3_float(uint32_t c) {
-  const uint32_t e = (c >> 3) & 15u, m = c & 7u;
-  const float v = e == 0 ? static_cast<float>(m) * 0.001953125f : __uint_as_float(((e + 120u) << 23) | (m << 20));
-  return (c & 0x80u) ? -v : v;
-}
-// the power of two of a block's E4M3 parts: 2^e maps the block's largest magnitude into
-// [128, 256); every further part has 2^-4 of the one before. Not below the smallest
-// scale for the last part. 1 << 20: the block holds an infinity or a NaN
+// The power of two of a block's first E2M1 part: its unit 2^e has the largest magnitude
+// at 6 or below. The second part's unit is 2^-2 of the first's, every further one's 2^-3
+// of the one before: a part leaves at most 1 (the step above 4 halved), then at most 1/2
+// of its unit, which is 4 of the next. Not below the smallest scale for the last part.
+// kFewBad: the block holds an infinity or a NaN.
+constexpr int kFewBad = 1 << 20;
+__device__ __forceinline__ int part_shift(int part) { return part == 0 ? 0 : 3 * part - 1; }
 __device__ __forceinline__ int part_exponent(float amax, int parts) {
-  const int bits = static_cast<int>(__float_as_uint(amax) >> 23);
-  if (bits >= 255) return 1 << 20;
-  const int e = bits - 127 - 7;
-  const int least = -127 + 4 * (parts - 1);
+  const uint32_t u = __float_as_uint(amax);
+  if (u >= 0x7f800000u) return kFewBad;
+  const int e = static_cast<int>(u >> 23) - 127 - ((u & 0x7fffffu) > 0x400000u ? 1 : 2);
+  const int least = -127 + part_shift(parts - 1);
   return e > least ? e : least;
 }
 __device__ __forceinline__ uint32_t part_byte(int e, int part) {
-  return e >= (1 << 20) ? 255u : static_cast<uint32_t>(e - 4 * part + 127);
+  return e >= kFewBad ? 255u : static_cast<uint32_t>(e - part_shift(part) + 127);
 }
+// 2^-e
 __device__ __forceinline__ float part_inverse(int e) {
-  return e >= (1 << 20) ? 1.0f : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  return e >= kFewBad ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
+// what the part leaves, in the next one's unit
+__device__ __forceinline__ float part_rest(float v, float q, int part) { return (v - q) * (part == 0 ? 4.0f : 8.0f); }
+__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest));
+}
+// value of a code (low four bits): s eem
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+  const uint32_t e = (c >> 1) & 3u, m = c & 1u;
+  const float v = e == 0 ? 0.5f * static_cast<float>(m) : __uint_as_float(((e + 126u) << 23) | (m << 22));
+  return (c & 8u) ? -v : v;
 }
 
 // ---------------------------------------------------------------------------
 // router
 // ---------------------------------------------------------------------------
-// logits[t][e] for 8 tokens and one expert an item: the block's 8 warps share H, 8
-// products to a 16-byte load, fp32 fused multiply-adds
-__device__ void few_logits(const FewParams& p, FewCtl* c, int et) {
+// logits[t][e], an item of NE experts x 8 tokens a block: its 8 warps share H, 8 products
+// to a 16-byte load, fp32 fused multiply-adds; the 32 lanes' sums meet in a halving
+// butterfly, the warps' in shared memory
+template <int NE>
+__device__ __noinline__ void few_logits_of(const FewParams& p, FewCtl* c, int et) {
   const int warp = et >> 5, lane = et & 31;
-  const int tg = (p.T + 7) >> 3, items = p.E * tg;
+  const int eg = (p.E + NE - 1) / NE, items = eg * ((p.T + 7) >> 3);
   const int nv = p.H >> 3;
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int e = item % p.E, t0 = item / p.E * 8;
-    const int nt = min(8, p.T - t0);
-    const uint4* w = reinterpret_cast<const uint4*>(p.wr + static_cast<size_t>(e) * p.H);
+    const int e0 = item % eg * NE, t0 = item / eg * 8;
+    const int ne = min(NE, p.E - e0), nt = min(8, p.T - t0);
+    const uint4* w = reinterpret_cast<const uint4*>(p.wr + static_cast<size_t>(e0) * p.H);
     const uint4* x = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t0) * p.H);
-    float acc[8];
+    float acc[32];  // [expert][token]
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+    for (int j = 0; j < 32; ++j) acc[j] = 0.0f;
     for (int v = et; v < nv; v += kFewEpi) {
-      const uint4 wv = __ldg(w + v);
-      uint4 xv[8];
+      uint4 wv[NE], xv[8];
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        if (i < ne) wv[i] = __ldg(w + static_cast<size_t>(i) * nv + v);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (j < nt) xv[j] = __ldg(x + static_cast<size_t>(j) * nv + v);
-      const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (j < nt) {
           const uint32_t xx[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            acc[j] = fmaf(bf16_lo(xx[q]), bf16_lo(ww[q]), acc[j]);
-            acc[j] = fmaf(bf16_hi(xx[q]), bf16_hi(ww[q]), acc[j]);
+          for (int i = 0; i < NE; ++i) {
+            const uint32_t ww[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              acc[8 * i + j] = fmaf(bf16_lo(xx[q]), bf16_lo(ww[q]), acc[8 * i + j]);
+              acc[8 * i + j] = fmaf(bf16_hi(xx[q]), bf16_hi(ww[q]), acc[8 * i + j]);
+            }
           }
         }
       }
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j < nt) {
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], d);
-        if (lane == 0) c->scratch[warp][j] = acc[j];
-      }
-    }
+    c->scratch[warp][lane] = lane_column_sums(acc, lane);
     epi_sync();
-    if (et < nt) {
+    if (et < 32 && (et >> 3) < ne && (et & 7) < nt) {
       float s = 0.0f;
 #pragma unroll
       for (int q = 0; q < 8; ++q) s += c->scratch[q][et];
-      p.logits[static_cast<size_t>(t0 + et) * p.E + e] = s + (p.lb != nullptr ? __ldg(p.lb + e) : 0.0f);
+      const int e = e0 + (et >> 3), t = t0 + (et & 7);
+      p.logits[static_cast<size_t>(t) * p.E + e] = s + (p.lb != nullptr ? __ldg(p.lb + e) : 0.0f);
     }
     epi_sync();
   }
 }
+// the more experts an item has the fewer times x is read and unpacked, as long as
+// there are items for the blocks
+__device__ void few_logits(const FewParams& p, FewCtl* c, int et) {
+  const int pairs = p.E * ((p.T + 7) >> 3), G = gridDim.x;
+  if (pairs >= 4 * G) few_logits_of<4>(p, c, et);
+  else if (pairs >= 2 * G) few_logits_of<2>(p, c, et);
+  else few_logits_of<1>(p, c, et);
+}
 
-// x in E4M3 parts: a thread a block of 32
+// x in E2M1 parts: a thread a block of 32
 __device__ void few_split_x(const FewParams& p, int et) {
   const int nb = p.H >> 5;
   for (int i = blockIdx.x * kFewEpi + et; i < p.T * nb; i += gridDim.x * kFewEpi) {
@@ -206,19 +248,18 @@ __device__ void few_split_x(const FewParams& p, int et) {
     const int e = part_exponent(bad ? INFINITY : amax, p.P1);
     const float inv = part_inverse(e);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] *= inv;
+    for (int j = 0; j < 32; ++j) v[j] = e >= kFewBad ? 0.0f : v[j] * inv;
     for (int q = 0; q < p.P1; ++q) {
       const size_t row = static_cast<size_t>(t) * p.P1 + q;
-      uint32_t w[8];
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        w[j] = cvt_e4m3x2(v[4 * j], v[4 * j + 1]) | (cvt_e4m3x2(v[4 * j + 2], v[4 * j + 3]) << 16);
-#pragma unroll
-        for (int b4 = 0; b4 < 4; ++b4) v[4 * j + b4] = (v[4 * j + b4] - e4m3_float((w[j] >> (8 * b4)) & 255u)) * 16.0f;
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t c = e2m1_pair(v[2 * j], v[2 * j + 1]);
+        w[j >> 2] |= c << (8 * (j & 3));
+        v[2 * j] = part_rest(v[2 * j], e2m1_value(c), q);
+        v[2 * j + 1] = part_rest(v[2 * j + 1], e2m1_value(c >> 4), q);
       }
-      uint4* dst = reinterpret_cast<uint4*>(p.xq + row * p.H + b * 32);
-      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      *reinterpret_cast<uint4*>(p.xq + row * (p.H >> 1) + b * 16) = make_uint4(w[0], w[1], w[2], w[3]);
       p.x_sf[row * nb + b] = static_cast<uint8_t>(part_byte(e, q));
     }
   }
@@ -337,21 +378,22 @@ __device__ void few_select(const FewParams& p, float* zs, int t, int lane, int& 
   g_out = p.gate_scale / sum * w;
 }
 
-// The block's plan from the slots' experts and gates: experts with rows in ascending
-// order, their rows in token order
+// The block's plan from the slots' experts and gates: entries of the experts in ascending
+// order, their rows in token order (a row's place is the number of its expert's tokens
+// before it, from a bit a token)
 __device__ void few_plan(const FewParams& p, FewCtl* c, int et) {
   const int R = p.T * p.k, warp = et >> 5, lane = et & 31;
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(c->eidx);
-  const uint32_t mine = static_cast<uint32_t>(et);
-  int m = 0;
-  if (et < p.E) {
-    for (int r = 0; r < R; r += 4) {
-      const uint32_t v = w[r >> 2];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) m += (r + j < R && ((v >> (8 * j)) & 255u) == mine) ? 1 : 0;
-    }
+  c->has[et][0] = c->has[et][1] = 0u;
+  epi_sync();
+  for (int r = et; r < R; r += kFewEpi) {
+    const int t = r / p.k;
+    atomicOr(&c->has[c->eidx[r]][t >> 5], 1u << (t & 31));
   }
-  int off = m, at = m > 0 ? 1 : 0, mx = m;
+  epi_sync();
+  const int m = __popc(c->has[et][0]) + __popc(c->has[et][1]);
+  // an expert's rows in as few entries as hold them, of one size
+  const int ng = (m + p.mcap - 1) / p.mcap, per = ng > 0 ? (m + ng - 1) / ng : 0;
+  int off = m, at = ng, mx = per;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int a = __shfl_up_sync(0xffffffffu, off, d), b = __shfl_up_sync(0xffffffffu, at, d);
@@ -360,46 +402,42 @@ __device__ void few_plan(const FewParams& p, FewCtl* c, int et) {
       at += b;
     }
   }
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  mx = __reduce_max_sync(0xffffffffu, mx);
   if (lane == 31) {
     c->warp_sum[warp] = off;
     c->warp_act[warp] = at;
     c->warp_max[warp] = mx;
   }
   epi_sync();
-  int o0 = 0, a0 = 0;
-  for (int q = 0; q < warp; ++q) {
-    o0 += c->warp_sum[q];
-    a0 += c->warp_act[q];
-  }
-  off += o0 - m;
-  at += a0 - (m > 0 ? 1 : 0);
-  if (m > 0) {
-    c->act[at] = static_cast<uint8_t>(et);
-    c->off[at] = off;
-    int n = 0;
-    for (int r = 0; r < R && n < m; r += 4) {
-      const uint32_t v = w[r >> 2];
+  int na = 0, most = p.Fs ? min(p.T, p.mcap) : 0;
+  off -= m;
+  at -= ng;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (r + j < R && ((v >> (8 * j)) & 255u) == mine) {
-          c->tok[off + n] = static_cast<uint8_t>((r + j) / p.k);
-          c->gate[off + n] = c->sgate[r + j];
-          ++n;
-        }
-      }
+  for (int q = 0; q < 8; ++q) {
+    if (q < warp) {
+      off += c->warp_sum[q];
+      at += c->warp_act[q];
     }
+    na += c->warp_act[q];
+    most = max(most, c->warp_max[q]);
   }
+  for (int g = 0; g < ng; ++g) {
+    c->act[at + g] = static_cast<uint8_t>(et);
+    c->off[at + g] = off + g * per;
+  }
+  c->eoff[et] = off;
   if (et == 0) {
-    int na = 0, most = p.Fs ? p.T : 0;
-    for (int q = 0; q < 8; ++q) {
-      na += c->warp_act[q];
-      most = max(most, c->warp_max[q]);
-    }
     c->nact = na;
     c->mmax = most;
     c->off[na] = R;
+  }
+  epi_sync();
+  for (int r = et; r < R; r += kFewEpi) {
+    const int t = r / p.k, e = c->eidx[r];
+    const uint32_t below = (1u << (t & 31)) - 1u;
+    const int row = c->eoff[e] + (t < 32 ? __popc(c->has[e][0] & below) : __popc(c->has[e][0]) + __popc(c->has[e][1] & below));
+    c->tok[row] = static_cast<uint8_t>(t);
+    c->gate[row] = c->sgate[r];
   }
   epi_sync();
 }
@@ -444,77 +482,79 @@ __device__ bool few_route(const FewParams& p, FewCtl* c, int et) {
 // ---------------------------------------------------------------------------
 // ends of a tile
 // ---------------------------------------------------------------------------
-// Where a block's share of a cut tile lies: it has at most one that begins inside a
-// tile (its first) and one that ends inside (its last)
-__device__ __forceinline__ size_t piece_slot(const FewSplit& s, int block, int u0) {
-  return 2 * static_cast<size_t>(block) + (s.start(block) > u0 ? 0 : 1);
-}
-
-// Sum over the pieces of element `o` of a cut tile, in the blocks' order
-struct FewPieces {
-  const float* part;
-  size_t stride;  // floats of a slot
-  FewSplit s;
-  int u0, c0, c1;
-  __device__ __forceinline__ float sum(size_t o) const {
-    float v = 0.0f;
-    for (int b = c0; b <= c1; ++b)
-      if (s.start(b + 1) > s.start(b)) v += __ldcg(part + piece_slot(s, b, u0) * stride + o);
-    return v;
-  }
-};
-
 // The block's share of a cut tile to the workspace; true in every thread of the block
 // that is the last to arrive
-__device__ __forceinline__ bool few_leave(const float* acc, int n, float* part, size_t stride, const FewSplit& s,
-                                          int u0, int pieces, unsigned* cnt, FewCtl* c, int et) {
-  float4* dst = reinterpret_cast<float4*>(part + piece_slot(s, blockIdx.x, u0) * stride);
+__device__ __forceinline__ bool few_leave(const float* acc, int n, float* part, size_t stride, const FewPieces& pc,
+                                          unsigned* cnt, FewCtl* c, int et) {
+  float4* dst = reinterpret_cast<float4*>(part + pc.slot(blockIdx.x) * stride);
   const float4* src = reinterpret_cast<const float4*>(acc);
   for (int i = et; i < n / 4; i += kFewEpi) __stcg(dst + i, src[i]);
   __threadfence();
   epi_sync();
-  if (et == 0) c->flag = atomicAdd(cnt, 1u) == static_cast<unsigned>(pieces - 1) ? 1 : 0;
+  if (et == 0) c->flag = atomicAdd(cnt, 1u) == static_cast<unsigned>(pc.count() - 1) ? 1 : 0;
   epi_sync();
   if (c->flag == 0) return false;
   __threadfence();
   return true;
 }
+// The sum of a cut tile's n floats, in the blocks' order, into `acc`; four float4 of a
+// piece on their way at a time
+__device__ __forceinline__ void few_join(float* acc, int n, const float* part, size_t stride, const FewPieces& pc,
+                                         int et) {
+  const int n4 = n / 4;
+  for (int base = et; base < n4; base += 4 * kFewEpi) {
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+    for (int b = pc.c0; b <= pc.c1; ++b) {
+      const float4* src = reinterpret_cast<const float4*>(part + pc.slot(b) * stride);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (base + k * kFewEpi < n4) {
+          const float4 w = __ldcg(src + base + k * kFewEpi);
+          v[k].x += w.x;
+          v[k].y += w.y;
+          v[k].z += w.z;
+          v[k].w += w.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (base + k * kFewEpi < n4) reinterpret_cast<float4*>(acc)[base + k * kFewEpi] = v[k];
+  }
+  epi_sync();
+}
 
-// SwiGLU of m rows x 128 columns from h1, h3 (fp32 sums), gated, split into the parts of
-// the down product's operand. Row j's values: whole tiles from `acc` [m][256], cut ones
-// from their pieces.
+// SwiGLU of an entry's rows x 128 columns from h1, h3 (fp32 sums acc [rows][2][128]), gated, split
+// into the parts of the down product's operand
 template <bool MX>
-__device__ void few_activate(const FewParams& p, const FewCtl* c, const float* acc, const FewPieces* pc, int m, int i,
-                             int tile, int et) {
+__device__ void few_activate(const FewParams& p, const FewCtl* c, const float* acc, const FewRows& rw, int i, int tile,
+                             int et) {
   const int f = 128 * tile + (et & 127), lane = et & 31;
   const int Fx = i < 0 ? p.Fs : p.F;
-  const int row0 = i < 0 ? 0 : c->off[i];
   uint8_t* dst = i < 0 ? p.as : p.a;
   uint8_t* dsf = i < 0 ? p.as_sf : p.a_sf;
-  for (int j = et >> 7; j < m; j += 2) {
-    float h1, h3;
-    if (pc == nullptr) {
-      h1 = acc[j * 256 + (et & 127)];
-      h3 = acc[j * 256 + 128 + (et & 127)];
-    } else {
-      h1 = pc->sum(static_cast<size_t>(j) * 256 + (et & 127));
-      h3 = pc->sum(static_cast<size_t>(j) * 256 + 128 + (et & 127));
-    }
+  for (int j = et >> 7; j < rw.m; j += 2) {
+    const float h1 = acc[j * 256 + (et & 127)], h3 = acc[j * 256 + 128 + (et & 127)];
     float a = h1 / (1.0f + expf(-h1)) * h3;
-    if (i >= 0) a *= c->gate[row0 + j];
-    const size_t row = static_cast<size_t>(row0 + j) * p.P2;
+    if (i >= 0) a *= c->gate[rw.r0 + j];
+    const size_t row = static_cast<size_t>(rw.r0 + j) * p.P2;
     if constexpr (MX) {
+      // a warp holds a block of 32 along F
       float amax = fabsf(a);
 #pragma unroll
       for (int d = 16; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
       const bool bad = __any_sync(0xffffffffu, a != a);
       const int e = part_exponent(bad ? INFINITY : amax, p.P2);
-      float v = a * part_inverse(e);
+      float v = e >= kFewBad ? 0.0f : a * part_inverse(e);
       for (int q = 0; q < p.P2; ++q) {
-        const uint32_t code = cvt_e4m3x2(v, 0.0f) & 255u;
-        dst[(row + q) * Fx + f] = static_cast<uint8_t>(code);
+        const uint32_t code = e2m1_pair(v, 0.0f) & 15u;
+        const uint32_t next = __shfl_down_sync(0xffffffffu, code, 1);
+        if ((lane & 1) == 0) dst[(row + q) * (Fx >> 1) + (f >> 1)] = static_cast<uint8_t>(code | (next << 4));
         if (lane == 0) dsf[(row + q) * (Fx >> 5) + (f >> 5)] = static_cast<uint8_t>(part_byte(e, q));
-        v = (v - e4m3_float(code)) * 16.0f;
+        v = part_rest(v, e2m1_value(code), q);
       }
     } else if (f < Fx) {
       __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(dst);
@@ -577,66 +617,80 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ weights
     if (lane == 0) {
+      if constexpr (!MX)
+        for (int i = 0; i < (p.Fs ? 6 : 3); ++i) tma_prefetch_desc(&maps.m[i]);
+      const uint64_t pol = l2_policy_evict_first();
+      // one stage's weights: into shared memory (LOAD), or into L2
+      auto weights = [&](auto load, const FewGeo& g, int ph, const FewChunk& ch, int kb, uint8_t* sA, uint64_t* bar) {
+        constexpr bool LOAD = decltype(load)::value;
+        const bool sh = ch.i < 0;
+        const int e = sh ? 0 : c->act[ch.i];
+        const int nsb = ph < 2 ? p.nsb1 : sh ? p.nsb2s : p.nsb2;
+        const int sb0 = ph < 2 ? kb : kb * g.sub2, ns = ph < 2 ? 2 : min(g.sub2, nsb - sb0);
+        if constexpr (MX) {
+          // a stage's tiles are one run of bytes
+          const uint8_t* w = ph < 2 ? (sh ? p.w13s : p.w13) : (sh ? p.w2s : p.w2);
+          const size_t t = (static_cast<size_t>(e) * (ph == 2 ? p.ns2 : sh ? p.ns1s : p.ns1) + ch.tile) * nsb + sb0;
+          const uint8_t* src = w + t * (ph < 2 ? 2 : 1) * few_tile(true);
+          const uint32_t bytes = ns * few_tile(true);
+          if constexpr (LOAD) {
+            mbar_arrive_expect_tx(bar, bytes);
+            bulk_load_hint(sA, src, bytes, bar, pol);
+          } else {
+            l2_prefetch(src, bytes);
+          }
+        } else {
+          auto box = [&](uint8_t* dst, const CUtensorMap* m, int c0, int c1) {
+            if constexpr (LOAD) tma_load_2d_hint(dst, m, bar, c0, c1, pol);
+            else l2_prefetch_2d(m, c0, c1);
+          };
+          if constexpr (LOAD) mbar_arrive_expect_tx(bar, ns * kFewATile);
+          for (int q = 0; q < ns; ++q) {
+            // phases 0, 1: W1's and W3's tile of one k sub-block; 2: W2's of two
+            const CUtensorMap* m = &maps.m[(sh ? 3 : 0) + (ph < 2 ? q : 2)];
+            const int row = ph < 2 ? e * p.H + kb * 64 : e * (sh ? p.Fs : p.F) + (sb0 + q) * 64;
+            box(sA + q * kFewATile, m, ch.tile * 128, row);
+            box(sA + q * kFewATile + 8192, m, ch.tile * 128 + 64, row);
+          }
+        }
+      };
       int n = 0;  // stages so far
       bool ok = true;
-      FewGeo g = few_geo(p.P1, p.P2, p.T, p.T, MX);
+      FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), p.runs, MX);
       for (int ph = first_phase; ph < 3 && ok; ++ph) {
         if (ph == 1) {
           if (!mbar_wait_bounded(&c->plan, 0, abort_flag, p.lim, p.status, 83)) break;
-          g = few_geo(p.P1, p.P2, p.T, c->mmax, MX);
+          g = few_geo(p.P1, p.P2, p.T, c->mmax, p.runs, MX);
         }
+        bool ahead = ph == 2;
         FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
         FewChunk ch;
         while (ok && w.next(ch)) {
-          const int e = ch.i < 0 ? 0 : c->act[ch.i];
-          const bool sh = ch.i < 0;
-          const int Fx = sh ? p.Fs : p.F;
           for (int kb = ch.kb; kb < ch.kb + ch.nkb; ++kb, ++n) {
             const int s = n % g.nst;
-            if (!mbar_wait_bounded(c->empty + s, ((n / g.nst) & 1) ^ 1, abort_flag, p.lim, p.status, 84)) {
-              ok = false;
-              break;
-            }
-            uint8_t* sA = smem + s * g.stage;
-            uint64_t* bar = c->full + s;
-            const uint64_t pol = l2_policy_evict_first();
-            if (ph < 2) {
-              if constexpr (MX) {
-                mbar_arrive_expect_tx(bar, kFewATile + 1024);  // 4-bit loads announce the bytes they read
-                const size_t blk = (static_cast<size_t>(e) * (sh ? p.ns1s : p.ns1) + ch.tile) * p.nsb1 + kb;
-                const CUtensorMap* m = &maps.m[sh ? 3 : 0];
-                tma_load_2d_hint(sA, m, bar, 0, static_cast<int>(blk * 256), pol);
-                tma_load_2d_hint(sA + kFewATile, m, bar, 0, static_cast<int>(blk * 256 + 128), pol);
-                bulk_load(sA + kFewABytes + g.b_bytes, (sh ? p.sf13s : p.sf13) + blk * 1024, 1024, bar);
-              } else {
-                mbar_arrive_expect_tx(bar, kFewABytes);
-                const CUtensorMap* m1 = &maps.m[sh ? 3 : 0];
-                const CUtensorMap* m3 = &maps.m[sh ? 4 : 1];
-                const int f = ch.tile * 128, row = e * p.H + kb * 64;
-                tma_load_2d_hint(sA, m1, bar, f, row, pol);
-                tma_load_2d_hint(sA + 8192, m1, bar, f + 64, row, pol);
-                tma_load_2d_hint(sA + 16384, m3, bar, f, row, pol);
-                tma_load_2d_hint(sA + 24576, m3, bar, f + 64, row, pol);
-              }
-            } else {
-              const int nsb = sh ? p.nsb2s : p.nsb2;
-              const int sb0 = kb * g.sub2, ns = min(g.sub2, nsb - sb0);
-              const CUtensorMap* m = &maps.m[sh ? 5 : 2];
-              if constexpr (MX) {
-                mbar_arrive_expect_tx(bar, ns * (kFewATile / 2 + 512));
-                const size_t blk = (static_cast<size_t>(e) * p.ns2 + ch.tile) * nsb + sb0;
-                for (int q = 0; q < ns; ++q)
-                  tma_load_2d_hint(sA + q * kFewATile, m, bar, 0, static_cast<int>((blk + q) * 128), pol);
-                bulk_load(sA + kFewABytes + g.b_bytes, (sh ? p.sf2s : p.sf2) + blk * 512, ns * 512, bar);
-              } else {
-                mbar_arrive_expect_tx(bar, ns * kFewATile);
-                for (int q = 0; q < ns; ++q) {
-                  const int row = e * Fx + (sb0 + q) * 64;
-                  tma_load_2d_hint(sA + q * kFewATile, m, bar, ch.tile * 128, row, pol);
-                  tma_load_2d_hint(sA + q * kFewATile + 8192, m, bar, ch.tile * 128 + 64, row, pol);
+            const uint32_t parity = ((n / g.nst) & 1) ^ 1;
+            if (!mbar_try_wait(c->empty + s, parity)) {
+              if (ahead) {
+                // the ring is full and the blocks are about to wait for the last activations:
+                // the memory goes on with what comes next
+                FewWalk aw = w;
+                FewChunk ac = ch;
+                ac.nkb -= kb - ac.kb;
+                ac.kb = kb;
+                for (int i = 0; i < kFewAhead; ++i) {
+                  if (ac.nkb == 0 && !aw.next(ac)) break;
+                  weights(std::false_type{}, g, ph, ac, ac.kb, nullptr, nullptr);
+                  ++ac.kb;
+                  --ac.nkb;
                 }
+                ahead = false;
+              }
+              if (!mbar_wait_bounded(c->empty + s, parity, abort_flag, p.lim, p.status, 84)) {
+                ok = false;
+                break;
               }
             }
+            weights(std::true_type{}, g, ph, ch, kb, smem + s * g.stage, c->full + s);
           }
         }
       }
@@ -649,7 +703,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // ------------------------------------------------------------ MMA
     int n = 0, na = 0;  // stages, accumulators so far
     bool ok = true;
-    FewGeo g = few_geo(p.P1, p.P2, p.T, p.T, MX);
+    FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), p.runs, MX);
     const uint32_t d_hi = sdesc_hi_sw128(1024);
     const uint64_t sf_hi = static_cast<uint64_t>((128u >> 4) | (1u << 14)) << 32;
     constexpr uint32_t kAStep = MX ? (32u >> 4) : (2048u >> 4);
@@ -657,20 +711,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     for (int ph = first_phase; ph < 3 && ok; ++ph) {
       if (ph == 1) {
         if (!warp_wait(&c->plan, 0, c, p, 85)) break;
-        g = few_geo(p.P1, p.P2, p.T, c->mmax, MX);
+        g = few_geo(p.P1, p.P2, p.T, c->mmax, p.runs, MX);
       }
       FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
       FewChunk ch;
       const int parts = ph < 2 ? p.P1 : p.P2;
       const int nbuf = ph < 2 ? g.nbuf1 : g.nbuf2;
-      const int acc_cols = ph < 2 ? 2 * g.n1 : g.n2;
+      const int run_cols = ph < 2 ? 2 * g.n1 : g.n2;  // an accumulator's columns
+      const int acc_cols = run_cols * (ph < 2 ? g.acc1 : g.acc2);
       na = 0;
       // the phases lay their accumulators out differently: all earlier ones have been read
       for (int b = 0; b < 2 && ok; ++b)
         if (used[b] > 0) ok = warp_wait(c->tempty + b, (used[b] & 1) ^ 1, c, p, 86);
       while (ok && w.next(ch)) {
-        const int m = ch.i < 0 ? p.T : c->off[ch.i + 1] - c->off[ch.i];
-        const int N = few_cols(parts, m);
+        const int N = few_cols(parts, FewRows(p, c, ch.i).m);
         const int buf = na % nbuf;
         ++na;
         // every earlier use of this accumulator has been read
@@ -692,38 +746,45 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           tc_fence_after();
           if (lane == 0) {
             const uint32_t sA = smem_u32(smem) + s * g.stage;
-            const uint32_t a0 = sdesc_lo(sA, MX ? 16u : 8192u), b0 = sdesc_lo(sA + kFewABytes, 16u);
+            const uint32_t a0 = sdesc_lo(sA, MX ? 16u : 8192u), b0 = sdesc_lo(sA + 2 * few_tile(MX), 16u);
             int ns = 2;
             if (ph == 2) ns = min(g.sub2, (ch.i < 0 ? p.nsb2s : p.nsb2) - kb * g.sub2);
             const int nblk = ph < 2 ? g.nblk1 : g.nblk2;
-            const uint32_t region = tmem + 448 + (n & 1) * 32;
+            const uint32_t region = tmem + kFewSfCol + (n & 1) * kFewSfRegion;
             if constexpr (MX) {
-              // scales to tensor memory: A's four columns a tile, then B's four for 128 rows
-              const uint32_t sf = sdesc_lo(sA + kFewABytes + g.b_bytes, 128u);
-              const int nb = ph < 2 ? nblk : ns * nblk;
-              for (int q = 0; q < ns; ++q) tmem_cp_32x128b_x4(region + 4 * q, sf_hi | (sf + q * (512u >> 4)));
+              // scales to tensor memory, four columns for 128 rows and 128 elements: A's two a
+              // tile, behind its codes, then B's two for 128 rows
+              const uint32_t sfa = sdesc_lo(sA + kFewATile, 128u), sfb = sdesc_lo(sA + 2 * few_tile(true) + g.b_bytes, 128u);
+              const int nb = 2 * (ph < 2 ? nblk : ns * nblk);
+              for (int q = 0; q < 2 * ns; ++q)
+                tmem_cp_32x128b_x4(region + 4 * q,
+                                   sf_hi | (sfa + (((q >> 1) * few_tile(true) + (q & 1) * kFewSf) >> 4)));
               for (int q = 0; q < nb; ++q)
-                tmem_cp_32x128b_x4(region + 8 + 4 * q, sf_hi | (sf + ((1024u + 512u * q) >> 4)));
+                tmem_cp_32x128b_x4(region + 16 + 4 * q, sf_hi | (sfb + ((kFewSf * q) >> 4)));
             }
-            const uint32_t go = kb > ch.kb ? 1u : 0u;
+            const int run = (kb - ch.kb) / w.run;
+            const uint32_t go = kb - ch.kb > run * w.run ? 1u : 0u;
+            const uint32_t dr = d0 + run * run_cols;
             for (int q = 0; q < ns; ++q) {
               // phases 0, 1: W1's then W3's tile against the same tokens, two accumulators;
               // phase 2: two sub-blocks of W2, each against its own, one accumulator
-              const uint32_t a_lo = a0 + q * (kFewATile >> 4);
+              const uint32_t a_lo = a0 + q * (few_tile(MX) >> 4);
               const uint32_t b_lo = ph < 2 ? b0 : b0 + q * ((g.n2 * kSubBytes) >> 4);
-              const uint32_t d = ph < 2 ? d0 + q * g.n1 : d0;
+              const uint32_t d = ph < 2 ? dr + q * g.n1 : dr;
               const uint32_t go_q = ph < 2 ? go : (go | (q > 0 ? 1u : 0u));
+              // B's scale columns: [sub-block][half of it][128 rows]
+              const uint32_t sb = region + 16 + (ph < 2 ? 0 : 8 * nblk * q);
               for (int n0 = 0; n0 < N; n0 += 256) {
                 const int nn = min(256, N - n0);
-                const uint32_t idesc = MX ? idesc_mxf4f8(nn) : idesc_bf16_f32(128, nn, true, false);
+                const uint32_t idesc = MX ? idesc_mxf4(nn) : idesc_bf16_f32(128, nn, true, false);
                 const uint32_t bn = b_lo + ((n0 * kSubBytes) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                   const uint32_t acc = go_q | (kk > 0 ? 1u : 0u);
                   if constexpr (MX)
                     umma_mx_w(d + n0, a_lo + kk * kAStep, bn + kk * (32u >> 4), d_hi,
-                              idesc | (static_cast<uint32_t>(kk) << 29) | (static_cast<uint32_t>(kk) << 4),
-                              region + 4 * q, region + 8 + (ph < 2 ? 0 : 4 * nblk * q) + n0 / 32, acc);
+                              idesc | (static_cast<uint32_t>(2 * (kk & 1)) << 29) | (static_cast<uint32_t>(2 * (kk & 1)) << 4),
+                              region + 8 * q + 4 * (kk >> 1), sb + 4 * nblk * (kk >> 1) + n0 / 32, acc);
                   else
                     umma_bf16_w(d + n0, a_lo + kk * kAStep, bn + kk * (32u >> 4), d_hi, idesc, acc);
                 }
@@ -748,8 +809,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int ct = threadIdx.x - 64;
     int n = 0;
     bool ok = true;
-    FewGeo g = few_geo(p.P1, p.P2, p.T, p.T, MX);
-    const int xld = p.H * (MX ? 1 : 2);
+    FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), p.runs, MX);
     for (int ph = first_phase; ph < 3 && ok; ++ph) {
       if (ph == 0 && MX) {
         // the parts of x come from all blocks
@@ -759,11 +819,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
       if (ph == 1) {
         if (!warp_wait(&c->plan, 0, c, p, 89)) break;
-        g = few_geo(p.P1, p.P2, p.T, c->mmax, MX);
+        g = few_geo(p.P1, p.P2, p.T, c->mmax, p.runs, MX);
       }
       if (ph == 2) {
         // all activations are there
-        if (lane == 0) ok = wait_count(p.sync + 2, p.ns1s + c->nact * p.ns1, c, p, 90);
+        if (lane == 0) ok = wait_count(p.sync + 2, p.nsh * p.ns1s + c->nact * p.ns1, c, p, 90);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok) break;
       }
@@ -772,54 +832,45 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const int parts = ph < 2 ? p.P1 : p.P2;
       while (ok && w.next(ch)) {
         const bool sh = ch.i < 0;
-        const int r0 = sh ? 0 : c->off[ch.i];
-        const int m = sh ? p.T : c->off[ch.i + 1] - r0;
-        const int mp = (m + 7) & ~7;
-        const int Fx = sh ? p.Fs : p.F;
+        const FewRows rw(p, c, ch.i);
+        const int m = rw.m, rows = parts * m;
+        // bytes of a row of the operand and of its scales
+        const int len = MX ? (ph < 2 ? p.H : sh ? p.Fs : p.F) >> 1 : 2 * (ph < 2 ? p.H : sh ? p.Fs : p.F);
+        const uint8_t* base = ph < 2 ? (MX ? p.xq : reinterpret_cast<const uint8_t*>(p.x)) : sh ? p.as : p.a;
+        const uint8_t* sf = ph < 2 ? p.x_sf : sh ? p.as_sf : p.a_sf;
+        // column n of the operand is row j's part n / m: where that row begins
+        auto row_of = [&](int n) {
+          const int part = n / m, j = n - part * m;
+          const int r = ph < 2 && !sh ? c->tok[rw.r0 + j] : rw.r0 + j;
+          return static_cast<size_t>(r) * parts + part;
+        };
         for (int kb = ch.kb; kb < ch.kb + ch.nkb; ++kb, ++n) {
           const int s = n % g.nst;
           if (!warp_wait(c->empty + s, ((n / g.nst) & 1) ^ 1, c, p, 91)) {
             ok = false;
             break;
           }
-          const uint32_t sB = smem_u32(smem) + s * g.stage + kFewABytes;
-          const uint32_t sSF = sB + g.b_bytes + 1024;
+          const uint32_t sB = smem_u32(smem) + s * g.stage + 2 * few_tile(MX);
           int ns = 1, sb0 = kb;
           if (ph == 2) {
             sb0 = kb * g.sub2;
             ns = min(g.sub2, (sh ? p.nsb2s : p.nsb2) - sb0);
           }
           for (int q = 0; q < ns; ++q) {
-            const int sb = sb0 + q;
+            const int at = (sb0 + q) * kSubBytes;
             const uint32_t sBq = sB + q * g.n2 * kSubBytes;
-            for (int it = ct; it < parts * m * 8; it += kFewCopiers) {
+            for (int it = ct; it < rows * 8; it += kFewCopiers) {
               const int r = it >> 3, ck = it & 7;
-              const int part = r / m, j = r - part * m;
-              const uint8_t* src;
-              if (ph < 2) {
-                const int t = sh ? j : c->tok[r0 + j];
-                src = MX ? p.xq + (static_cast<size_t>(t) * parts + part) * xld
-                         : reinterpret_cast<const uint8_t*>(p.x) + static_cast<size_t>(t) * xld;
-              } else {
-                src = (sh ? p.as : p.a) + (static_cast<size_t>(r0 + j) * parts + part) * (Fx * (MX ? 1 : 2));
-              }
-              const int nrow = part * mp + j;
-              cp_async16(sBq + nrow * 128 + ((ck ^ (nrow & 7)) << 4), src + sb * kSubBytes + ck * 16, true);
+              const bool in = at + ck * 16 < len;  // beyond a row's end: zeros
+              cp_async16(sBq + r * 128 + ((ck ^ (r & 7)) << 4), base + row_of(r) * len + (in ? at + ck * 16 : 0), in);
             }
             if constexpr (MX) {
-              for (int r = ct; r < parts * m; r += kFewCopiers) {
-                const int part = r / m, j = r - part * m;
-                const uint8_t* src;
-                if (ph < 2) {
-                  const int t = sh ? j : c->tok[r0 + j];
-                  src = p.x_sf + (static_cast<size_t>(t) * parts + part) * (p.H >> 5);
-                } else {
-                  src = (sh ? p.as_sf : p.a_sf) + (static_cast<size_t>(r0 + j) * parts + part) * (Fx >> 5);
-                }
-                const int nrow = part * mp + j;
-                cp_async4(sSF + 512 * ((ph < 2 ? 0 : q * g.nblk2) + (nrow >> 7)) + 16 * (nrow & 31) +
-                              4 * ((nrow >> 5) & 3),
-                          src + sb * 4);
+              const int slen = len >> 4, nblk = ph < 2 ? g.nblk1 : g.nblk2;
+              const uint32_t sS = sB + g.b_bytes + 2 * kFewSf * nblk * q;
+              for (int it = ct; it < rows * 2; it += kFewCopiers) {
+                const int r = it >> 1, half = it & 1, b = (sb0 + q) * 8 + half * 4;
+                cp_async4(sS + kFewSf * (nblk * half + (r >> 7)) + 16 * (r & 31) + 4 * ((r >> 5) & 3),
+                          sf + row_of(r) * slen + (b < slen ? b : 0), b < slen);
               }
             }
           }
@@ -836,20 +887,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     bool ok = few_route<MX>(p, c, et);
     if (ok && et == 0) mbar_arrive(&c->plan);
     int used[2] = {0, 0};
-    const FewGeo g = few_geo(p.P1, p.P2, p.T, ok ? c->mmax : p.T, MX);
+    const FewGeo g = few_geo(p.P1, p.P2, p.T, ok ? c->mmax : 1, p.runs, MX);
     float* acc = reinterpret_cast<float*>(smem + g.acc_off);
     unsigned* cnt = p.cnt;
     for (int ph = first_phase; ph < 3 && ok; ++ph) {
       FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
       FewChunk ch;
       const int nbuf = ph < 2 ? g.nbuf1 : g.nbuf2;
-      const int acc_cols = ph < 2 ? 2 * g.n1 : g.n2;
+      const int run_cols = ph < 2 ? 2 * g.n1 : g.n2;
+      const int acc_cols = run_cols * (ph < 2 ? g.acc1 : g.acc2);
       const int parts = ph < 2 ? p.P1 : p.P2;
       int na = 0;
       while (ok && w.next(ch)) {
-        const int r0 = ch.i < 0 ? 0 : c->off[ch.i];
-        const int m = ch.i < 0 ? p.T : c->off[ch.i + 1] - r0;
-        const int mp = (m + 7) & ~7;
+        const FewRows rw(p, c, ch.i);
+        const int m = rw.m;
         const int buf = na % nbuf;
         ++na;
         if (ph == 2 && ch.first) {
@@ -861,16 +912,26 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         ++used[buf];
         tc_fence_after();
         const uint32_t d0 = tl + buf * acc_cols + (ph < 2 ? half * g.n1 : 0);
-        for (int j0 = ph < 2 ? 0 : 8 * half; j0 < mp; j0 += ph < 2 ? 8 : 16) {
+        const int nrun = (ch.nkb + w.run - 1) / w.run;
+        for (int j0 = ph < 2 ? 0 : 8 * half; j0 < m; j0 += ph < 2 ? 8 : 16) {
           float v[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-          for (int q = 0; q < parts; ++q) {
-            uint32_t r[8];
-            tmem_ld8(d0 + q * mp + j0, r);
+          // every run's and part's columns, four reads on their way at a time
+          const int n = nrun * parts;
+          for (int q0 = 0; q0 < n; q0 += 4) {
+            uint32_t r[4][8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int q = q0 + k;
+              if (q < n) tmem_ld8(d0 + q / parts * run_cols + q % parts * m + j0, r[k]);
+            }
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(r[j]);
+            for (int k = 0; k < 4; ++k)
+              if (q0 + k < n)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(r[k][j]);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -879,7 +940,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 float* a = acc + (j0 + j) * 256 + half * 128 + row;
                 *a = ch.first ? v[j] : *a + v[j];
               } else {
-                acc[(ch.i < 0 ? j0 + j : c->tok[r0 + j0 + j]) * 128 + row] += v[j];
+                acc[(ch.i < 0 ? rw.r0 + j0 + j : c->tok[rw.r0 + j0 + j]) * 128 + row] += v[j];
               }
             }
           }
@@ -890,34 +951,34 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         epi_sync();
         if (!ch.last) continue;
         const int ti = w.tile_index(), u0 = ti * w.per;
-        const FewSplit& s = w.s;
-        const int pieces = s.pieces(u0, u0 + w.per);
+        const FewPieces pc(w.s, u0, u0 + w.per);
         if (ph < 2) {
           float* part = ph == 0 ? p.part0 : p.part1;
           const size_t stride = static_cast<size_t>(p.T) * 256;
           bool mine = true;
-          FewPieces pc{part, stride, s, u0, s.owner(u0), s.owner(u0 + w.per - 1)};
-          if (pieces > 1)
-            mine = few_leave(acc, m * 256, part, stride, s, u0, pieces, cnt + ti, c, et);
+          if (pc.count() > 1) {
+            mine = few_leave(acc, m * 256, part, stride, pc, cnt + ti, c, et);
+            if (mine) few_join(acc, m * 256, part, stride, pc, et);
+          }
           if (mine) {
-            few_activate<MX>(p, c, acc, pieces > 1 ? &pc : nullptr, m, ch.i, ch.tile, et);
+            few_activate<MX>(p, c, acc, rw, ch.i, ch.tile, et);
             __threadfence();
           }
           epi_sync();
           if (mine && et == 0) red_release(p.sync + 2, 1u);
         } else {
           const size_t stride = static_cast<size_t>(p.T) * 128;
-          if (pieces == 1) {
-            for (int i = et; i < p.T * 128; i += kFewEpi) few_store_y(p, i >> 7, 128 * ch.tile + (i & 127), acc[i]);
-          } else if (few_leave(acc, p.T * 128, p.part2, stride, s, u0, pieces, cnt + ti, c, et)) {
-            const FewPieces pc{p.part2, stride, s, u0, s.owner(u0), s.owner(u0 + w.per - 1)};
-            for (int i = et; i < p.T * 128; i += kFewEpi)
-              few_store_y(p, i >> 7, 128 * ch.tile + (i & 127), pc.sum(i));
+          bool mine = true;
+          if (pc.count() > 1) {
+            mine = few_leave(acc, p.T * 128, p.part2, stride, pc, cnt + ti, c, et);
+            if (mine) few_join(acc, p.T * 128, p.part2, stride, pc, et);
           }
+          if (mine)
+            for (int i = et; i < p.T * 128; i += kFewEpi) few_store_y(p, i >> 7, 128 * ch.tile + (i & 127), acc[i]);
           epi_sync();
         }
       }
-      cnt += ph == 0 ? p.ns1s : p.E * p.ns1;
+      cnt += ph == 0 ? p.nsh * p.ns1s : kFewMaxEnt * p.ns1;
     }
   }
   tc_fence_before();
@@ -947,32 +1008,33 @@ struct FewLayout {
   size_t logits, cnt, part0, part1, part2, a, as, a_sf, as_sf, xq, x_sf, total;
   int cnt_words;
 };
-static int few_parts1(bool mx) { return mx ? 2 : 1; }
-static int few_parts2(const moe_config& c, bool mx) { return mx ? (c.out_fp32 ? 5 : 3) : (c.out_fp32 ? 3 : 2); }
+static int few_parts1(const moe_config& c, bool mx) { return mx ? (c.out_fp32 ? 8 : 5) : 1; }
+static int few_parts2(const moe_config& c, bool mx) { return mx ? (c.out_fp32 ? 8 : 5) : (c.out_fp32 ? 3 : 2); }
 static FewLayout few_layout(const moe_config& c, bool mx, int G) {
   FewLayout L{};
   const size_t T = c.T, R = T * c.k, F = c.F, Fs = c.F_shared, H = c.H, P2 = few_parts2(c, mx);
-  const size_t eb = mx ? 1 : 2;
+  const size_t P1 = few_parts1(c, mx);
   size_t o = sizeof(DevStatus);
   auto take = [&](size_t bytes) {
     const size_t at = o;
     o += up256(bytes);
     return at;
   };
-  L.cnt_words = (c.F_shared + 127) / 128 + c.E * ((c.F + 127) / 128) + (c.H + 127) / 128;
+  // (the shared expert has at most as many entries as tokens)
+  L.cnt_words = c.T * ((c.F_shared + 127) / 128) + kFewMaxEnt * ((c.F + 127) / 128) + (c.H + 127) / 128;
   L.logits = take(4 * T * c.E);
   L.cnt = take(4 * static_cast<size_t>(L.cnt_words));
   // a block's two partials of a phase
   L.part0 = take(Fs ? 2 * static_cast<size_t>(G) * T * 256 * 4 : 0);
   L.part1 = take(2 * static_cast<size_t>(G) * T * 256 * 4);
   L.part2 = take(2 * static_cast<size_t>(G) * T * 128 * 4);
-  L.a = take(R * P2 * F * eb);
-  L.as = take(T * P2 * Fs * eb);
+  L.a = take(mx ? R * P2 * F / 2 : R * P2 * F * 2);
+  L.as = take(mx ? T * P2 * Fs / 2 : T * P2 * Fs * 2);
   if (mx) {
     L.a_sf = take(R * P2 * F / 32);
     L.as_sf = take(T * P2 * Fs / 32);
-    L.xq = take(T * 2 * H);
-    L.x_sf = take(T * 2 * H / 32);
+    L.xq = take(T * P1 * H / 2);
+    L.x_sf = take(T * P1 * H / 32);
   }
   L.total = o;
   return L;
@@ -1018,19 +1080,24 @@ int run_few(const moe_config& c, const FewArgs& q, bool mx, void* ws, cudaStream
   p.topk_groups = c.topk_groups;
   p.force = c.force_balanced;
   p.gate_scale = c.gate_scale;
-  p.P1 = few_parts1(mx);
+  p.P1 = few_parts1(c, mx);
   p.P2 = few_parts2(c, mx);
-  const int ks = mx ? 128 : 64;
+  p.mcap = few_mcap(p.P1, mx);
+  p.nsh = c.F_shared ? (c.T + p.mcap - 1) / p.mcap : 0;
+  p.msh = p.nsh ? (c.T + p.nsh - 1) / p.nsh : 0;
+  const int ks = mx ? 256 : 64;
   // the tensor cores' sums round towards zero: fp32 results take them in runs of 128
-  // products (512 under block scales, which lose less), joined in fp32
-  p.flush = c.out_fp32 ? (mx ? 512 : 128) / ks : 1 << 30;
+  // products (512 under block scales, which lose less), joined in fp32: 4e-7 of the
+  // result, 1.4e-6 with runs of 512
+  p.run = c.out_fp32 ? (mx ? 512 : 128) / ks : 1 << 20;
+  p.runs = c.out_fp32 && !mx ? 4 : 1;
   p.out_fp32 = c.out_fp32;
   p.ns1 = (c.F + 127) / 128;
   p.ns1s = (c.F_shared + 127) / 128;
   p.ns2 = (c.H + 127) / 128;
-  p.nsb1 = c.H / ks;
-  p.nsb2 = c.F / ks;
-  p.nsb2s = c.F_shared / ks;
+  p.nsb1 = (c.H + ks - 1) / ks;
+  p.nsb2 = (c.F + ks - 1) / ks;
+  p.nsb2s = (c.F_shared + ks - 1) / ks;
   p.x = q.x; p.wr = q.router_w; p.eb = q.expert_bias; p.lb = q.logit_bias;
   p.idx = q.topk_idx; p.gate = q.topk_gate; p.y = q.y;
   p.status = reinterpret_cast<DevStatus*>(base);
@@ -1049,12 +1116,7 @@ int run_few(const moe_config& c, const FewArgs& q, bool mx, void* ws, cudaStream
   bool ok = true;
   if (mx) {
     const moe_mx4_weights& w = *q.mx4;
-    p.sf13 = w.sf13; p.sf2 = w.sf2; p.sf13s = w.sf13s; p.sf2s = w.sf2s;
-    ok = make_map_fp4(&maps.m[0], w.w13, static_cast<uint64_t>(c.E) * p.ns1 * p.nsb1 * 256) &&
-         make_map_fp4(&maps.m[2], w.w2, static_cast<uint64_t>(c.E) * p.ns2 * p.nsb2 * 128);
-    if (c.F_shared)
-      ok = ok && make_map_fp4(&maps.m[3], w.w13s, static_cast<uint64_t>(p.ns1s) * p.nsb1 * 256) &&
-           make_map_fp4(&maps.m[5], w.w2s, static_cast<uint64_t>(p.ns2) * p.nsb2s * 128);
+    p.w13 = w.w13; p.w2 = w.w2; p.w13s = w.w13s; p.w2s = w.w2s;
   } else {
     const uint64_t E = c.E, H = c.H, F = c.F, Fs = c.F_shared;
     ok = make_map_bf16(&maps.m[0], q.W1, F, E * H, 2 * F, 64, 64) && make_map_bf16(&maps.m[1], q.W3, F, E * H, 2 * F, 64, 64) &&
@@ -1123,10 +1185,8 @@ int moe_layer_few_fwd_mxfp4(const moe_config* cfg, const moe_bf16* x, const moe_
   NvtxRange nvtx("moe_layer_few_fwd_mxfp4");
   const int s = check_few(cfg, true);
   if (s != MOE_OK) return s;
-  if (!w || !w->w13 || !w->sf13 || !w->w2 || !w->sf2) return MOE_ERR_INVALID_ARG;
-  if (cfg->F_shared && (!w->w13s || !w->sf13s || !w->w2s || !w->sf2s)) return MOE_ERR_INVALID_ARG;
-  if (!few_aligned({w->w13, w->w2, w->w13s, w->w2s}, 32) || !few_aligned({w->sf13, w->sf2, w->sf13s, w->sf2s}, 16))
-    return MOE_ERR_INVALID_ARG;
+  if (!w || !w->w13 || !w->w2 || (cfg->F_shared && (!w->w13s || !w->w2s))) return MOE_ERR_INVALID_ARG;
+  if (!few_aligned({w->w13, w->w2, w->w13s, w->w2s}, 16)) return MOE_ERR_INVALID_ARG;
   auto b = [](const moe_bf16* v) { return reinterpret_cast<const __nv_bfloat16*>(v); };
   const FewArgs q{b(x), b(router_w), expert_bias, logit_bias, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, w,
                   topk_idx, topk_gate, y};

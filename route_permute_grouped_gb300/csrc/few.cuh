@@ -21,17 +21,18 @@
 // Phases: 0 the shared expert's gate and up products (needs no routing: its
 // weights stream while the router works), 1 the routed experts', 2 all down
 // products. A stage of phases 0 and 1 holds one k sub-block (128 bytes: 64 bf16,
-// 128 MXFP4 elements) of 128 columns of W1 and of W3, a stage of phase 2 up to two
+// 256 MXFP4 elements) of 128 columns of W1 and of W3, a stage of phase 2 up to two
 // sub-blocks of 128 columns of W2.
 //
-// Operands: bf16 weights multiply bf16 parts of the tokens (x itself; the
-// activation a in two parts, three for fp32 results: 2^-17 and 2^-25 of a).
-// MXFP4 weights (E2M1 with a power of two for 32 elements along k) multiply E4M3
-// parts of the tokens, each with its own power of two for 32 elements: x in two
-// parts, which hold a bf16 exactly unless it lies 2^-15 below its block's maximum
-// (2^-22 of that maximum then); a in three (2^-12), five for fp32 results (2^-20).
-// The parts are further columns of the N operand, of which the tensor cores have
-// plenty to spare.
+// Operands: bf16 weights multiply bf16 parts of the tokens (x itself; the activation
+// a in two parts, three for fp32 results: 2^-17 and 2^-25 of a). MXFP4 weights stay
+// packed, two to a byte, in shared memory: the block-scaled MMA takes them with E2M1
+// tokens, a power of two for 32 elements on either side. So x and a enter as sums of E2M1
+// parts, every part with its own powers of two: a part leaves at most half the largest
+// step of the one before, 3 bits a part, 2^-12 of a block's unit after five (2^-21 after
+// eight, for fp32 results). The parts are further columns of the N operand, of which the
+// tensor cores have plenty to spare. (Unpacked 4-bit weights with E4M3 tokens need fewer
+// parts, but the copies that unpack move 8 bytes a cycle: 2.5 TB/s over all SMs.)
 #pragma once
 #include "host_util.h"
 #include "mma.cuh"
@@ -44,9 +45,11 @@ constexpr int kFewEpi = 256;
 constexpr int kFewCopiers = 64;
 constexpr int kFewStages = 8;      // at most
 constexpr int kFewMaxR = kFewMaxT * 16;
+constexpr int kFewMaxEnt = 320;    // runs of rows of one expert
 constexpr int kFewATile = 16384;   // 128 columns x 128 bytes
-constexpr int kFewABytes = 2 * kFewATile;
+constexpr int kFewSf = 512;        // scales of 128 columns (rows) x 128 MXFP4 elements
 constexpr int kFewSmem = 232448;   // 227 KB
+constexpr int kFewAhead = 8;       // stages of phase 2 asked for into L2 while the blocks wait
 constexpr int kFewRedundant = 16;  // tokens up to which every block selects for itself
 
 // A block's own plan of the batch (shared memory)
@@ -54,11 +57,13 @@ struct FewCtl {
   uint64_t full[kFewStages], empty[kFewStages], tfull[2], tempty[2], plan, drain;
   uint32_t tmem;
   int abort;
-  int nact, mmax;            // experts with rows, most rows of one (shared expert: T)
+  int nact, mmax;            // entries: runs of rows of one expert; most rows of one
   int flag;
   int warp_sum[8], warp_act[8], warp_max[8];
-  int off[257];              // first row of active expert i
-  uint8_t act[256];          // expert of active expert i
+  uint32_t has[256][2];      // expert -> its tokens
+  int eoff[256];             // expert -> its first row
+  int off[kFewMaxEnt + 1];   // first row of entry i
+  uint8_t act[kFewMaxEnt];   // its expert
   uint8_t tok[kFewMaxR];     // row -> token
   float gate[kFewMaxR];      // row -> gate
   uint8_t eidx[kFewMaxR];    // slot (token-major) -> expert
@@ -73,7 +78,10 @@ struct FewParams {
   int mode, groups, topk_groups, force;  // router (RouterSelMode)
   float gate_scale;
   int P1, P2;                // parts of x and of a
-  int flush;                 // most products accumulated in tensor memory, in k sub-blocks
+  int mcap;                  // rows of an entry, at most
+  int nsh, msh;              // entries of the shared expert, rows of one
+  int run;                   // k sub-blocks summed by one accumulator in tensor memory
+  int runs;                  // accumulators of a chunk, at most
   int out_fp32;
   int ns1, ns1s, ns2;        // tiles of 128 columns: F, Fs, H
   int nsb1, nsb2, nsb2s;     // k sub-blocks: H, F, Fs
@@ -90,12 +98,12 @@ struct FewParams {
   uint8_t *a, *as;           // parts of the activations: rows x parts x (F or Fs)
   uint8_t *a_sf, *as_sf;     // MXFP4: their scale bytes
   uint8_t *xq, *x_sf;        // MXFP4: parts of x and their scale bytes
-  const uint8_t *sf13, *sf2, *sf13s, *sf2s;
+  const uint8_t *w13, *w2, *w13s, *w2s;  // MXFP4 tiles, codes and scales
   DevStatus* status;
   unsigned long long lim;
 };
 struct FewMaps {
-  CUtensorMap m[6];          // W1, W3, W2, Ws1, Ws3, Ws2; MXFP4: w13, -, w2, ws13, -, ws2
+  CUtensorMap m[6];          // W1, W3, W2, Ws1, Ws3, Ws2 (bf16)
 };
 
 // What a stage holds and how many there are, from the largest number of rows
@@ -104,10 +112,20 @@ struct FewGeo {
   int sub2;                  // sub-blocks of a phase 2 stage
   int b_bytes, nblk1, nblk2, stage, nst;
   int acc_off;               // fp32 sums in shared memory
-  int nbuf1, nbuf2;          // accumulators in tensor memory
+  int acc1, acc2;            // accumulators of a chunk in tensor memory
+  int nbuf1, nbuf2;          // chunks there at a time
 };
-__host__ __device__ __forceinline__ int few_cols(int parts, int m) { return (parts * ((m + 7) & ~7) + 15) & ~15; }
-__host__ __device__ __forceinline__ FewGeo few_geo(int P1, int P2, int T, int mmax, bool mx) {
+__host__ __device__ constexpr int few_tile(bool mx) { return kFewATile + (mx ? 2 * kFewSf : 0); }
+// columns of the N operand: part q of row j is column q m + j
+__host__ __device__ __forceinline__ int few_cols(int parts, int m) { return (parts * m + 15) & ~15; }
+// accumulator columns of tensor memory: the rest holds scales, or is left to reads of
+// eight columns that begin below
+__host__ __device__ constexpr int few_acc_cols(bool mx) { return mx ? 416 : 496; }
+constexpr int kFewSfCol = 416, kFewSfRegion = 48;  // two regions, in turn: 16 columns of A's, 32 of B's
+__host__ __device__ __forceinline__ int few_mcap(int P1, bool mx) {
+  return mx ? few_acc_cols(true) / 2 / 16 * 16 / P1 : kFewMaxT;
+}
+__host__ __device__ __forceinline__ FewGeo few_geo(int P1, int P2, int T, int mmax, int runs, bool mx) {
   FewGeo g;
   g.n1 = few_cols(P1, mmax);
   g.n2 = few_cols(P2, mmax);
@@ -116,40 +134,57 @@ __host__ __device__ __forceinline__ FewGeo few_geo(int P1, int P2, int T, int mm
   g.b_bytes = 128 * (g.n1 > g.sub2 * g.n2 ? g.n1 : g.sub2 * g.n2);
   g.nblk1 = (g.n1 + 127) >> 7;
   g.nblk2 = (g.n2 + 127) >> 7;
-  const int sfb = 512 * (g.nblk1 > g.sub2 * g.nblk2 ? g.nblk1 : g.sub2 * g.nblk2);
-  g.stage = kFewABytes + g.b_bytes + (mx ? (1024 + sfb + 1023) / 1024 * 1024 : 0);
+  const int nblk = g.nblk1 > g.sub2 * g.nblk2 ? g.nblk1 : g.sub2 * g.nblk2;
+  g.stage = 2 * few_tile(mx) + g.b_bytes + (mx ? 2 * kFewSf * nblk : 0);
   const int acc = mmax * 1024 > T * 512 ? mmax * 1024 : T * 512;
   g.acc_off = kFewCtlOff - (acc + 1023) / 1024 * 1024;
   g.nst = g.acc_off / g.stage;
   if (g.nst > kFewStages) g.nst = kFewStages;
-  const int cols = mx ? 448 : 512;  // the rest holds scales
-  g.nbuf1 = 4 * g.n1 <= cols ? 2 : 1;
-  g.nbuf2 = 2 * g.n2 <= cols ? 2 : 1;
+  const int cols = few_acc_cols(mx);
+  g.acc1 = g.acc2 = runs;
+  while (g.acc1 > 1 && 4 * g.n1 * g.acc1 > cols) g.acc1 >>= 1;
+  while (g.acc2 > 1 && 2 * g.n2 * g.acc2 > cols) g.acc2 >>= 1;
+  g.nbuf1 = 4 * g.n1 * g.acc1 <= cols ? 2 : 1;
+  g.nbuf2 = 2 * g.n2 * g.acc2 <= cols ? 2 : 1;
   return g;
 }
 
-// Equal contiguous runs of U units over G blocks
+// Equal contiguous runs of U units over the first G blocks of the grid, each of at least
+// kFewRun units while there are enough: a tile cut into shorter ones costs more to
+// join than the blocks gain.
+constexpr int kFewRun = 4;
 struct FewSplit {
   int U, G;
+  __host__ __device__ __forceinline__ void set(int units, int blocks) {
+    U = units;
+    const int most = (units + kFewRun - 1) / kFewRun;
+    G = blocks < most ? blocks : most;
+  }
   __host__ __device__ __forceinline__ int start(int c) const {
-    return static_cast<int>(static_cast<long long>(U) * c / G);
+    return c >= G ? U : static_cast<int>(static_cast<long long>(U) * c / G);
   }
   // the block that has unit u
   __host__ __device__ __forceinline__ int owner(int u) const {
     return static_cast<int>(((static_cast<long long>(u) + 1) * G - 1) / U);
   }
-  // blocks that share units [u0, u1): all blocks owner(u0) .. owner(u1 - 1) with a unit
-  __host__ __device__ __forceinline__ int pieces(int u0, int u1) const {
-    const int a = owner(u0), b = owner(u1 - 1);
-    int n = 0;
-    for (int c = a; c <= b; ++c) n += start(c + 1) > start(c) ? 1 : 0;
-    return n;
+};
+// Blocks c0 .. c1 share the tile of units [u0, u1). A block has at most one share that
+// begins inside a tile (its first) and one that ends inside (its last): its two slots
+// in the workspace.
+struct FewPieces {
+  int c0, c1;
+  __host__ __device__ __forceinline__ FewPieces(const FewSplit& s, int u0, int u1) : c0(s.owner(u0)), c1(s.owner(u1 - 1)) {}
+  __host__ __device__ __forceinline__ int count() const { return c1 - c0 + 1; }
+  __host__ __device__ __forceinline__ size_t slot(int block) const {
+    return 2 * static_cast<size_t>(block) + (block == c0 ? 1 : 0);
   }
 };
 
-// A run of k blocks of one tile and one expert, accumulated at once
+// Consecutive stages of one tile and one expert that the epilogue takes at once. Where
+// tensor-memory sums are kept short (FewParams::run), each `run` stages have an
+// accumulator of their own.
 struct FewChunk {
-  int i;       // active expert; -1: the shared one
+  int i;       // entry; -1 - g: the shared expert's entry g
   int tile;    // 128-column tile: of F (phases 0 and 1), of H (phase 2)
   int kb, nkb; // first stage of the expert's k, stages
   bool first, last;  // of this block's segment of the tile
@@ -159,25 +194,27 @@ struct FewChunk {
 struct FewWalk {
   FewSplit s;
   int phase, u, u0, u1;
-  int kbs, kbr, per;   // stages of the shared expert's and a routed expert's k, of a tile
-  int ns, flush;
+  int kbs, kbr, shared, per;  // stages of the shared expert's and a routed expert's k, of all shared entries, of a tile
+  int ns, flush, run;
   __host__ __device__ __forceinline__ FewWalk(int ph, const FewParams& p, const FewGeo& g, int nact, int c, int G) {
     phase = ph;
     if (ph < 2) {
       ns = ph == 0 ? p.ns1s : p.ns1;
       per = p.nsb1;
-      s.U = (ph == 0 ? 1 : nact) * ns * per;
-      kbs = kbr = per;
-      flush = p.flush;
+      s.set((ph == 0 ? p.nsh : nact) * ns * per, G);
+      kbs = kbr = shared = per;
+      run = p.run;
+      flush = run >= 1 << 20 ? run : run * g.acc1;
     } else {
       ns = p.ns2;
       kbr = (p.nsb2 + g.sub2 - 1) / g.sub2;
-      kbs = p.Fs ? (p.nsb2s + g.sub2 - 1) / g.sub2 : 0;
-      per = kbs + nact * kbr;
-      s.U = ns * per;
-      flush = p.flush / g.sub2;
+      kbs = (p.nsb2s + g.sub2 - 1) / g.sub2;
+      shared = p.nsh * kbs;
+      per = shared + nact * kbr;
+      s.set(ns * per, G);
+      run = p.run < g.sub2 ? 1 : p.run / g.sub2;
+      flush = run >= 1 << 20 ? run : run * g.acc2;
     }
-    s.G = G;
     u = u0 = s.start(c);
     u1 = s.start(c + 1);
   }
@@ -186,19 +223,21 @@ struct FewWalk {
     const int t = u / per, r = u - t * per;
     int lim;
     if (phase < 2) {
-      c.i = phase == 0 ? -1 : t / ns;
-      c.tile = phase == 0 ? t : t - c.i * ns;
+      const int e = t / ns;
+      c.i = phase == 0 ? -1 - e : e;
+      c.tile = t - e * ns;
       c.kb = r;
       lim = per - r;
     } else {
       c.tile = t;
-      if (r < kbs) {
-        c.i = -1;
-        c.kb = r;
-        lim = kbs - r;
+      if (r < shared) {
+        const int e = r / kbs;
+        c.i = -1 - e;
+        c.kb = r - e * kbs;
+        lim = kbs - c.kb;
       } else {
-        c.i = (r - kbs) / kbr;
-        c.kb = r - kbs - c.i * kbr;
+        c.i = (r - shared) / kbr;
+        c.kb = r - shared - c.i * kbr;
         lim = kbr - c.kb;
       }
     }
@@ -212,6 +251,20 @@ struct FewWalk {
   }
   // the tile that the chunk just walked belongs to: index in the phase, first unit
   __host__ __device__ __forceinline__ int tile_index() const { return (u - 1) / per; }
+};
+
+// An entry's rows: the first (of the routed rows; the shared expert's: token) and how many
+struct FewRows {
+  int r0, m;
+  __device__ __forceinline__ FewRows(const FewParams& p, const FewCtl* c, int i) {
+    if (i < 0) {
+      r0 = (-1 - i) * p.msh;
+      m = p.T - r0 < p.msh ? p.T - r0 : p.msh;
+    } else {
+      r0 = c->off[i];
+      m = c->off[i + 1] - r0;
+    }
+  }
 };
 
 }  // namespace moe

@@ -31,11 +31,6 @@ struct NvtxRange {
 bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                    uint32_t box_inner, uint32_t box_outer);
 
-// 2-D map over `rows` rows of 128 four-bit elements (64 bytes), boxes of 128 rows; a
-// row takes 128 bytes of shared memory, 16 elements in the first 8 of every 16
-// bytes, 128-byte swizzle. A box announces the 8192 bytes it reads.
-bool make_map_fp4(CUtensorMap* m, const void* base, uint64_t rows);
-
 int num_sms();
 
 // two arrays of `a_bytes` and `b_bytes` that share memory

@@ -8,8 +8,8 @@
 // All kernels here move bytes: per element 2 of bf16 one way and 17/32 of codes and
 // scales the other. Rows: four lanes a block, so that every access of a warp is
 // contiguous. Weights: a block of threads turns a tile of 128 k x 128 columns, its
-// loads 128 bytes of a weight row a warp, and stages the codes in shared memory, which
-// then leave as the 8 KB run that few.cuh's copies read.
+// loads 128 bytes of a weight row a warp, and stages the codes in shared memory, from
+// where they leave in the layout that few.cuh's copies read.
 #include <cuda_fp4.h>
 
 #include <initializer_list>
@@ -17,6 +17,8 @@
 #include "host_util.h"
 
 namespace moe {
+
+constexpr int kMx4Tile = 16384 + 1024;  // codes and scales of 128 columns x 256 elements
 
 // scale byte of a block of maximum amax; 255: it holds an infinity or a NaN (bad)
 __device__ __forceinline__ uint32_t mx4_scale_byte(float amax, bool bad) {
@@ -101,15 +103,18 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t* q, c
   }
 }
 
-// A weight [E][K][N] bf16 and where its tiles go: tile (e, column block nb, k block kb)
-// is code block (e nblocks + nb) nkb + kb of `tiles` 8 KB tiles (W1 and W3 interleave:
-// tiles = 2), `which` of them; its 512 scale bytes likewise.
+// A weight [E][K][N] bf16 and where its tiles go. A tile holds 128 columns x 256 elements
+// of k as the few-token kernel's shared memory has them: a column's 128 bytes of codes
+// with their 16-byte chunks swizzled (chunk c of column r at c ^ (r % 8)), 16 KB, then two
+// times 512 scale bytes, byte 16 (r % 32) + 4 (r / 32) + b of half h that of column r's
+// block 4 h + b. Tile (e, column block nb, k block kb) is number ((e nnb + nb) nkb + kb)
+// `tiles` + `which` (W1 and W3 alternate: tiles = 2); k beyond K is zeros.
 struct Mx4Weight {
   const __nv_bfloat16* w;
   __nv_bfloat16* out;  // the way back
-  uint8_t *q, *sf;
+  uint8_t* q;
   int K, N, tiles, which;
-  long long first;     // its first tile among all of the launch
+  long long first;     // its first half tile among all of the launch
 };
 struct Mx4Weights {
   Mx4Weight w[6];
@@ -117,8 +122,7 @@ struct Mx4Weights {
   long long total;
 };
 
-// code tile: column r's 128 elements along k are bytes 64 r ..; scale byte
-// 16 (r % 32) + 4 (r / 32) + b that of its block b
+// half a tile at a time: 128 elements of k
 template <bool BACK>
 __global__ void __launch_bounds__(256) mx4_weights_kernel(const __grid_constant__ Mx4Weights a) {
   __shared__ __align__(16) uint8_t codes[128 * 64];
@@ -130,20 +134,24 @@ __global__ void __launch_bounds__(256) mx4_weights_kernel(const __grid_constant_
     int i = 0;
     while (i + 1 < a.n && t >= a.w[i + 1].first) ++i;
     const Mx4Weight& w = a.w[i];
-    const int nkb = w.K >> 7, nnb = w.N >> 7;
+    const int nkb = (w.K + 255) >> 8, nnb = w.N >> 7;
     const long long r = t - w.first;
     // columns innermost: neighbouring blocks read neighbouring parts of the weight's rows
     const int nb = static_cast<int>(r % nnb);
     const long long r2 = r / nnb;
-    const int kb = static_cast<int>(r2 % nkb);
-    const long long e = r2 / nkb;
-    const long long blk = ((e * nnb + nb) * nkb + kb) * w.tiles + w.which;
-    const size_t at = (static_cast<size_t>(e) * w.K + 128 * kb + 32 * b) * w.N + 128 * nb + col;
+    const int k2 = static_cast<int>(r2 % (2 * nkb)), half = k2 & 1;
+    const long long e = r2 / (2 * nkb);
+    uint8_t* tile = w.q + (((e * nnb + nb) * nkb + (k2 >> 1)) * w.tiles + w.which) * kMx4Tile;
+    const bool in = 128 * k2 < w.K;  // (beyond: the last tile's second half)
+    const size_t at = (static_cast<size_t>(e) * w.K + 128 * k2 + 32 * b) * w.N + 128 * nb + col;
+    // 16-byte chunk i of the half: column i / 4, block i % 4
+    auto chunk = [&](int i) { return reinterpret_cast<uint4*>(tile + (i >> 2) * 128 + (((4 * half + (i & 3)) ^ ((i >> 2) & 7)) << 4)); };
+    uint4* sf = reinterpret_cast<uint4*>(tile + 16384 + 512 * half);
     if constexpr (!BACK) {
       uint32_t v[32];
       const uint32_t* src = reinterpret_cast<const uint32_t*>(w.w + at);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = __ldcs(src + static_cast<size_t>(j) * (w.N >> 1));
+      for (int j = 0; j < 32; ++j) v[j] = in ? __ldcs(src + static_cast<size_t>(j) * (w.N >> 1)) : 0u;
       float m0 = 0.0f, m1 = 0.0f;
       bool bad0 = false, bad1 = false;
 #pragma unroll
@@ -164,21 +172,20 @@ __global__ void __launch_bounds__(256) mx4_weights_kernel(const __grid_constant_
       }
       if (s0 == 255u) c0[0] = c0[1] = c0[2] = c0[3] = 0u;
       if (s1 == 255u) c1[0] = c1[1] = c1[2] = c1[3] = 0u;
-      __syncthreads();  // the tile before has left
+      __syncthreads();  // the half before has left
       *reinterpret_cast<uint4*>(codes + col * 64 + b * 16) = make_uint4(c0[0], c0[1], c0[2], c0[3]);
       *reinterpret_cast<uint4*>(codes + (col + 1) * 64 + b * 16) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
       scales[16 * (col & 31) + 4 * (col >> 5) + b] = static_cast<uint8_t>(s0);
       scales[16 * ((col + 1) & 31) + 4 * (col >> 5) + b] = static_cast<uint8_t>(s1);
       __syncthreads();
-      uint4* q = reinterpret_cast<uint4*>(w.q + blk * 8192);
-      for (int k = threadIdx.x; k < 512; k += 256) q[k] = reinterpret_cast<const uint4*>(codes)[k];
-      if (threadIdx.x < 32) reinterpret_cast<uint4*>(w.sf + blk * 512)[threadIdx.x] = reinterpret_cast<const uint4*>(scales)[threadIdx.x];
+      for (int i = threadIdx.x; i < 512; i += 256) *chunk(i) = reinterpret_cast<const uint4*>(codes)[i];
+      if (threadIdx.x < 32) sf[threadIdx.x] = reinterpret_cast<const uint4*>(scales)[threadIdx.x];
     } else {
       __syncthreads();
-      const uint4* q = reinterpret_cast<const uint4*>(w.q + blk * 8192);
-      for (int k = threadIdx.x; k < 512; k += 256) reinterpret_cast<uint4*>(codes)[k] = __ldcg(q + k);
-      if (threadIdx.x < 32) reinterpret_cast<uint4*>(scales)[threadIdx.x] = __ldcg(reinterpret_cast<const uint4*>(w.sf + blk * 512) + threadIdx.x);
+      for (int i = threadIdx.x; i < 512; i += 256) reinterpret_cast<uint4*>(codes)[i] = __ldcg(chunk(i));
+      if (threadIdx.x < 32) reinterpret_cast<uint4*>(scales)[threadIdx.x] = __ldcg(sf + threadIdx.x);
       __syncthreads();
+      if (!in) continue;
       const uint4 a0 = *reinterpret_cast<const uint4*>(codes + col * 64 + b * 16);
       const uint4 a1 = *reinterpret_cast<const uint4*>(codes + (col + 1) * 64 + b * 16);
       const uint32_t c0[4] = {a0.x, a0.y, a0.z, a0.w}, c1[4] = {a1.x, a1.y, a1.z, a1.w};
@@ -212,12 +219,10 @@ static int mx4_weights(const moe_config* cfg, const void* const (&bf)[6], const 
   if (st != MOE_OK) return st;
   const moe_config& c = *cfg;
   const int n = c.F_shared ? 6 : 3;
-  if (!w || !w->w13 || !w->sf13 || !w->w2 || !w->sf2) return MOE_ERR_INVALID_ARG;
-  if (c.F_shared && (!w->w13s || !w->sf13s || !w->w2s || !w->sf2s)) return MOE_ERR_INVALID_ARG;
+  if (!w || !w->w13 || !w->w2 || (c.F_shared && (!w->w13s || !w->w2s))) return MOE_ERR_INVALID_ARG;
   for (int i = 0; i < n; ++i)
     if (!bf[i] || !mx4_aligned({bf[i]}, 16)) return MOE_ERR_INVALID_ARG;
-  if (!mx4_aligned({w->w13, w->w2, w->w13s, w->w2s}, 32) || !mx4_aligned({w->sf13, w->sf2, w->sf13s, w->sf2s}, 16))
-    return MOE_ERR_INVALID_ARG;
+  if (!mx4_aligned({w->w13, w->w2, w->w13s, w->w2s}, 16)) return MOE_ERR_INVALID_ARG;
   Mx4Weights a{};
   a.n = n;
   for (int i = 0; i < n; ++i) {
@@ -227,13 +232,12 @@ static int mx4_weights(const moe_config* cfg, const void* const (&bf)[6], const 
     m.w = static_cast<const __nv_bfloat16*>(bf[i]);
     m.out = static_cast<__nv_bfloat16*>(const_cast<void*>(bf[i]));
     m.q = down ? (sh ? w->w2s : w->w2) : (sh ? w->w13s : w->w13);
-    m.sf = down ? (sh ? w->sf2s : w->sf2) : (sh ? w->sf13s : w->sf13);
     m.K = down ? F : c.H;
     m.N = down ? c.H : F;
     m.tiles = down ? 1 : 2;
     m.which = down ? 0 : i % 3;
     m.first = a.total;
-    a.total += static_cast<long long>(sh ? 1 : c.E) * (m.K / 128) * (m.N / 128);
+    a.total += static_cast<long long>(sh ? 1 : c.E) * ((m.K + 255) / 256 * 2) * (m.N / 128);
   }
   const long long most = 8ll * num_sms();
   const int grid = static_cast<int>(a.total < most ? a.total : most);
@@ -252,14 +256,11 @@ using namespace moe;
 extern "C" {
 
 size_t moe_mx4_weight_bytes(const moe_config* cfg, int which) {
-  if (check_mx4(cfg) != MOE_OK) return 0;
-  const size_t F = which < 4 ? cfg->F : cfg->F_shared, n = static_cast<size_t>(which < 4 ? cfg->E : 1) * cfg->H * F;
-  switch (which & 3) {
-    case 0: return which < 8 && which >= 0 ? n : 0;            // w13, w13s
-    case 1: return which < 8 && which >= 0 ? n / 16 : 0;       // sf13, sf13s
-    case 2: return which < 8 && which >= 0 ? n / 2 : 0;        // w2, w2s
-    default: return which < 8 && which >= 0 ? n / 32 : 0;      // sf2, sf2s
-  }
+  if (check_mx4(cfg) != MOE_OK || which < 0 || which > 3) return 0;
+  const bool shared = which >= 2, down = which & 1;
+  const size_t F = shared ? cfg->F_shared : cfg->F, H = cfg->H, E = shared ? 1 : cfg->E;
+  const size_t tiles = down ? (H / 128) * ((F + 255) / 256) : 2 * (F / 128) * ((H + 255) / 256);
+  return F == 0 ? 0 : E * tiles * kMx4Tile;
 }
 
 int moe_mx4_quantize_weights(const moe_config* cfg, const moe_bf16* W1, const moe_bf16* W3, const moe_bf16* W2,

@@ -1133,8 +1133,8 @@ def clip_grad_norm(tensors, max_norm, kind="l2", ws=None):
 # MXFP4: rows and the layer's weights
 # ---------------------------------------------------------------------------
 class MoeMx4Weights(ctypes.Structure):
-    """Mirror of moe_mx4_weights (eight device pointers)."""
-    _fields_ = [(n, c_void_p) for n in ("w13", "sf13", "w2", "sf2", "w13s", "sf13s", "w2s", "sf2s")]
+    """Mirror of moe_mx4_weights (four device pointers)."""
+    _fields_ = [(n, c_void_p) for n in ("w13", "w2", "w13s", "w2s")]
 
 
 def _mx4_rows(where, x, K):
@@ -1191,7 +1191,7 @@ def _layer_weights(w, cfg, W1, W3, W2, Ws, d=None):
 
 def _mx4_sizes(cfg):
     fields = [n for n, _ in MoeMx4Weights._fields_]
-    used = fields if cfg.F_shared else fields[:4]
+    used = fields if cfg.F_shared else fields[:2]
     return [(n, _size("moe_mx4_weight_bytes", cfg, i)) for i, n in enumerate(used)]
 
 
