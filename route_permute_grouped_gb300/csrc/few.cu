@@ -14,6 +14,18 @@ namespace moe {
 
 namespace {
 
+// One thread of a converged warp. The compiler knows that it is one: an MMA then takes
+// 79 cycles at 16 columns (the 4 KB of weights it reads from shared memory); behind a
+// comparison of the lane it is issued by a loop over the lanes, 153 cycles each.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -616,7 +628,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ weights
-    if (lane == 0) {
+    if (elect_one()) {
       if constexpr (!MX)
         for (int i = 0; i < (p.Fs ? 6 : 3); ++i) tma_prefetch_desc(&maps.m[i]);
       const uint64_t pol = l2_policy_evict_first();
@@ -656,11 +668,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       };
       int n = 0;  // stages so far
       bool ok = true;
-      FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), p.runs, MX);
+      FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), MX);
       for (int ph = first_phase; ph < 3 && ok; ++ph) {
         if (ph == 1) {
           if (!mbar_wait_bounded(&c->plan, 0, abort_flag, p.lim, p.status, 83)) break;
-          g = few_geo(p.P1, p.P2, p.T, c->mmax, p.runs, MX);
+          g = few_geo(p.P1, p.P2, p.T, c->mmax, MX);
         }
         bool ahead = ph == 2;
         FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
@@ -703,22 +715,30 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // ------------------------------------------------------------ MMA
     int n = 0, na = 0;  // stages, accumulators so far
     bool ok = true;
-    FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), p.runs, MX);
+    FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), MX);
     const uint32_t d_hi = sdesc_hi_sw128(1024);
     const uint64_t sf_hi = static_cast<uint64_t>((128u >> 4) | (1u << 14)) << 32;
     constexpr uint32_t kAStep = MX ? (32u >> 4) : (2048u >> 4);
     int used[2] = {0, 0};  // times that each accumulator has been filled
+    auto step = [&](uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, int q, int kk, uint32_t sfb,
+                    uint32_t region, bool go) {
+      const uint32_t id = 2 * (kk & 1);
+      if constexpr (MX)
+        umma_mx_w(d, a_lo, b_lo, d_hi, idesc | (id << 29) | (id << 4), region + 8 * q + 4 * (kk >> 1), sfb, go ? 1u : 0u);
+      else
+        umma_bf16_w(d, a_lo, b_lo, d_hi, idesc, go ? 1u : 0u);
+    };
     for (int ph = first_phase; ph < 3 && ok; ++ph) {
       if (ph == 1) {
         if (!warp_wait(&c->plan, 0, c, p, 85)) break;
-        g = few_geo(p.P1, p.P2, p.T, c->mmax, p.runs, MX);
+        g = few_geo(p.P1, p.P2, p.T, c->mmax, MX);
       }
       FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
       FewChunk ch;
       const int parts = ph < 2 ? p.P1 : p.P2;
       const int nbuf = ph < 2 ? g.nbuf1 : g.nbuf2;
-      const int run_cols = ph < 2 ? 2 * g.n1 : g.n2;  // an accumulator's columns
-      const int acc_cols = run_cols * (ph < 2 ? g.acc1 : g.acc2);
+      const int il = ph < 2 ? g.il1 : g.il2, il_cols = ph < 2 ? 2 * g.n1 : g.n2;
+      const int acc_cols = il * il_cols;
       na = 0;
       // the phases lay their accumulators out differently: all earlier ones have been read
       for (int b = 0; b < 2 && ok; ++b)
@@ -744,7 +764,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           // the tokens' copies are generic-proxy writes: ordered before the MMAs' reads
           fence_proxy_async_smem();
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             const uint32_t sA = smem_u32(smem) + s * g.stage;
             const uint32_t a0 = sdesc_lo(sA, MX ? 16u : 8192u), b0 = sdesc_lo(sA + 2 * few_tile(MX), 16u);
             int ns = 2;
@@ -762,45 +782,42 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               for (int q = 0; q < nb; ++q)
                 tmem_cp_32x128b_x4(region + 16 + 4 * q, sf_hi | (sfb + ((kFewSf * q) >> 4)));
             }
-            const int run = (kb - ch.kb) / w.run;
-            const uint32_t go = kb - ch.kb > run * w.run ? 1u : 0u;
-            const uint32_t dr = d0 + run * run_cols;
-            for (int q = 0; q < ns; ++q) {
-              // phases 0, 1: W1's then W3's tile against the same tokens, two accumulators;
-              // phase 2: two sub-blocks of W2, each against its own, one accumulator
-              const uint32_t a_lo = a0 + q * (few_tile(MX) >> 4);
-              const uint32_t b_lo = ph < 2 ? b0 : b0 + q * ((g.n2 * kSubBytes) >> 4);
-              const uint32_t d = ph < 2 ? dr + q * g.n1 : dr;
-              const uint32_t go_q = ph < 2 ? go : (go | (q > 0 ? 1u : 0u));
-              // B's scale columns: [sub-block][half of it][128 rows]
-              const uint32_t sb = region + 16 + (ph < 2 ? 0 : 8 * nblk * q);
-              for (int n0 = 0; n0 < N; n0 += 256) {
-                const int nn = min(256, N - n0);
-                const uint32_t idesc = MX ? idesc_mxf4(nn) : idesc_bf16_f32(128, nn, true, false);
-                const uint32_t bn = b_lo + ((n0 * kSubBytes) >> 4);
+            const bool begun = kb > ch.kb;
+            for (int n0 = 0; n0 < N; n0 += 256) {
+              const int nn = min(256, N - n0);
+              const uint32_t idesc = MX ? idesc_mxf4(nn) : idesc_bf16_f32(128, nn, true, false);
+              const uint32_t bn = b0 + ((n0 * kSubBytes) >> 4);
+              // phases 0, 1: W1's and W3's tile against the same tokens, accumulators of their
+              // own; phase 2: two sub-blocks of W2, each against its own. Step kk along k of
+              // either goes to accumulator kk % il
+              if (ph < 2) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                  const uint32_t acc = go_q | (kk > 0 ? 1u : 0u);
-                  if constexpr (MX)
-                    umma_mx_w(d + n0, a_lo + kk * kAStep, bn + kk * (32u >> 4), d_hi,
-                              idesc | (static_cast<uint32_t>(2 * (kk & 1)) << 29) | (static_cast<uint32_t>(2 * (kk & 1)) << 4),
-                              region + 8 * q + 4 * (kk >> 1), sb + 4 * nblk * (kk >> 1) + n0 / 32, acc);
-                  else
-                    umma_bf16_w(d + n0, a_lo + kk * kAStep, bn + kk * (32u >> 4), d_hi, idesc, acc);
-                }
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                  for (int q = 0; q < 2; ++q)
+                    step(d0 + (kk & (il - 1)) * il_cols + q * g.n1 + n0, a0 + q * (few_tile(MX) >> 4) + kk * kAStep,
+                         bn + kk * (32u >> 4), idesc, q, kk, region + 16 + 4 * nblk * (kk >> 1) + n0 / 32, region,
+                         begun || kk >= il);
+              } else {
+                for (int q = 0; q < ns; ++q)
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    step(d0 + (kk & (il - 1)) * il_cols + n0, a0 + q * (few_tile(MX) >> 4) + kk * kAStep,
+                         bn + q * ((g.n2 * kSubBytes) >> 4) + kk * (32u >> 4), idesc, q, kk,
+                         region + 16 + 4 * nblk * (2 * q + (kk >> 1)) + n0 / 32, region, begun || q > 0 || kk >= il);
               }
             }
             umma_commit(c->empty + s);
           }
           __syncwarp();
         }
-        if (lane == 0) umma_commit(c->tfull + buf);
+        if (elect_one()) umma_commit(c->tfull + buf);
         __syncwarp();
       }
     }
     if (*abort_flag) {  // the MMAs in flight end before the tensor memory is freed
       int zero = 0;
-      if (lane == 0) umma_commit(&c->drain);
+      if (elect_one()) umma_commit(&c->drain);
       __syncwarp();
       mbar_wait_bounded(&c->drain, 0, &zero, p.lim, nullptr, 0);
     }
@@ -809,7 +826,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int ct = threadIdx.x - 64;
     int n = 0;
     bool ok = true;
-    FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), p.runs, MX);
+    FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), MX);
     for (int ph = first_phase; ph < 3 && ok; ++ph) {
       if (ph == 0 && MX) {
         // the parts of x come from all blocks
@@ -819,7 +836,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
       if (ph == 1) {
         if (!warp_wait(&c->plan, 0, c, p, 89)) break;
-        g = few_geo(p.P1, p.P2, p.T, c->mmax, p.runs, MX);
+        g = few_geo(p.P1, p.P2, p.T, c->mmax, MX);
       }
       if (ph == 2) {
         // all activations are there
@@ -887,15 +904,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     bool ok = few_route<MX>(p, c, et);
     if (ok && et == 0) mbar_arrive(&c->plan);
     int used[2] = {0, 0};
-    const FewGeo g = few_geo(p.P1, p.P2, p.T, ok ? c->mmax : 1, p.runs, MX);
+    const FewGeo g = few_geo(p.P1, p.P2, p.T, ok ? c->mmax : 1, MX);
     float* acc = reinterpret_cast<float*>(smem + g.acc_off);
     unsigned* cnt = p.cnt;
     for (int ph = first_phase; ph < 3 && ok; ++ph) {
       FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
       FewChunk ch;
       const int nbuf = ph < 2 ? g.nbuf1 : g.nbuf2;
-      const int run_cols = ph < 2 ? 2 * g.n1 : g.n2;
-      const int acc_cols = run_cols * (ph < 2 ? g.acc1 : g.acc2);
+      const int il = ph < 2 ? g.il1 : g.il2, il_cols = ph < 2 ? 2 * g.n1 : g.n2;
+      const int acc_cols = il * il_cols;
       const int parts = ph < 2 ? p.P1 : p.P2;
       int na = 0;
       while (ok && w.next(ch)) {
@@ -912,24 +929,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         ++used[buf];
         tc_fence_after();
         const uint32_t d0 = tl + buf * acc_cols + (ph < 2 ? half * g.n1 : 0);
-        const int nrun = (ch.nkb + w.run - 1) / w.run;
         for (int j0 = ph < 2 ? 0 : 8 * half; j0 < m; j0 += ph < 2 ? 8 : 16) {
           float v[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-          // every run's and part's columns, four reads on their way at a time
-          const int n = nrun * parts;
-          for (int q0 = 0; q0 < n; q0 += 4) {
+          // every part's columns in every accumulator, four reads on their way at a time
+          for (int q = 0; q < parts; ++q) {
             uint32_t r[4][8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int q = q0 + k;
-              if (q < n) tmem_ld8(d0 + q / parts * run_cols + q % parts * m + j0, r[k]);
-            }
+            for (int k = 0; k < 4; ++k)
+              if (k < il) tmem_ld8(d0 + k * il_cols + q * m + j0, r[k]);
             tmem_ld_wait();
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (q0 + k < n)
+              if (k < il)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(r[k][j]);
           }
@@ -1086,11 +1099,11 @@ int run_few(const moe_config& c, const FewArgs& q, bool mx, void* ws, cudaStream
   p.nsh = c.F_shared ? (c.T + p.mcap - 1) / p.mcap : 0;
   p.msh = p.nsh ? (c.T + p.nsh - 1) / p.nsh : 0;
   const int ks = mx ? 256 : 64;
-  // the tensor cores' sums round towards zero: fp32 results take them in runs of 128
+  // the tensor cores' sums round towards zero: fp32 results take them in chains of 128
   // products (512 under block scales, which lose less), joined in fp32: 4e-7 of the
-  // result, 1.4e-6 with runs of 512
-  p.run = c.out_fp32 ? (mx ? 512 : 128) / ks : 1 << 20;
-  p.runs = c.out_fp32 && !mx ? 4 : 1;
+  // result, 1.4e-6 with chains of 512
+  p.chain = c.out_fp32 ? (mx ? 512 : 128) : 1 << 24;
+  p.ks = ks;
   p.out_fp32 = c.out_fp32;
   p.ns1 = (c.F + 127) / 128;
   p.ns1s = (c.F_shared + 127) / 128;

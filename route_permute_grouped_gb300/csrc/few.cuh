@@ -49,7 +49,7 @@ constexpr int kFewMaxEnt = 320;    // runs of rows of one expert
 constexpr int kFewATile = 16384;   // 128 columns x 128 bytes
 constexpr int kFewSf = 512;        // scales of 128 columns (rows) x 128 MXFP4 elements
 constexpr int kFewSmem = 232448;   // 227 KB
-constexpr int kFewAhead = 8;       // stages of phase 2 asked for into L2 while the blocks wait
+constexpr int kFewAhead = 0;       // stages of phase 2 asked for into L2 while the blocks wait
 constexpr int kFewRedundant = 16;  // tokens up to which every block selects for itself
 
 // A block's own plan of the batch (shared memory)
@@ -80,10 +80,10 @@ struct FewParams {
   int P1, P2;                // parts of x and of a
   int mcap;                  // rows of an entry, at most
   int nsh, msh;              // entries of the shared expert, rows of one
-  int run;                   // k sub-blocks summed by one accumulator in tensor memory
-  int runs;                  // accumulators of a chunk, at most
+  int chain;                 // products summed by one accumulator in tensor memory, at most
   int out_fp32;
   int ns1, ns1s, ns2;        // tiles of 128 columns: F, Fs, H
+  int ks;                    // elements of a k sub-block
   int nsb1, nsb2, nsb2s;     // k sub-blocks: H, F, Fs
   const __nv_bfloat16 *x, *wr;
   const float *eb, *lb;
@@ -112,8 +112,8 @@ struct FewGeo {
   int sub2;                  // sub-blocks of a phase 2 stage
   int b_bytes, nblk1, nblk2, stage, nst;
   int acc_off;               // fp32 sums in shared memory
-  int acc1, acc2;            // accumulators of a chunk in tensor memory
-  int nbuf1, nbuf2;          // chunks there at a time
+  int il1, il2;              // accumulators that the steps along k take in turn
+  int nbuf1, nbuf2;          // chunks in tensor memory at a time
 };
 __host__ __device__ constexpr int few_tile(bool mx) { return kFewATile + (mx ? 2 * kFewSf : 0); }
 // columns of the N operand: part q of row j is column q m + j
@@ -125,7 +125,7 @@ constexpr int kFewSfCol = 416, kFewSfRegion = 48;  // two regions, in turn: 16 c
 __host__ __device__ __forceinline__ int few_mcap(int P1, bool mx) {
   return mx ? few_acc_cols(true) / 2 / 16 * 16 / P1 : kFewMaxT;
 }
-__host__ __device__ __forceinline__ FewGeo few_geo(int P1, int P2, int T, int mmax, int runs, bool mx) {
+__host__ __device__ __forceinline__ FewGeo few_geo(int P1, int P2, int T, int mmax, bool mx) {
   FewGeo g;
   g.n1 = few_cols(P1, mmax);
   g.n2 = few_cols(P2, mmax);
@@ -141,11 +141,11 @@ __host__ __device__ __forceinline__ FewGeo few_geo(int P1, int P2, int T, int mm
   g.nst = g.acc_off / g.stage;
   if (g.nst > kFewStages) g.nst = kFewStages;
   const int cols = few_acc_cols(mx);
-  g.acc1 = g.acc2 = runs;
-  while (g.acc1 > 1 && 4 * g.n1 * g.acc1 > cols) g.acc1 >>= 1;
-  while (g.acc2 > 1 && 2 * g.n2 * g.acc2 > cols) g.acc2 >>= 1;
-  g.nbuf1 = 4 * g.n1 * g.acc1 <= cols ? 2 : 1;
-  g.nbuf2 = 2 * g.n2 * g.acc2 <= cols ? 2 : 1;
+  // the steps along k take several accumulators in turn: each adds a part of the products
+  g.il1 = 8 * g.n1 * 2 <= cols ? 4 : 4 * g.n1 * 2 <= cols ? 2 : 1;
+  g.il2 = 4 * g.n2 * 2 <= cols ? 4 : 2 * g.n2 * 2 <= cols ? 2 : 1;
+  g.nbuf1 = 4 * g.n1 * g.il1 <= cols ? 2 : 1;
+  g.nbuf2 = 2 * g.n2 * g.il2 <= cols ? 2 : 1;
   return g;
 }
 
@@ -180,9 +180,8 @@ struct FewPieces {
   }
 };
 
-// Consecutive stages of one tile and one expert that the epilogue takes at once. Where
-// tensor-memory sums are kept short (FewParams::run), each `run` stages have an
-// accumulator of their own.
+// Consecutive stages of one tile and one expert, summed in tensor memory, that the
+// epilogue takes at once
 struct FewChunk {
   int i;       // entry; -1 - g: the shared expert's entry g
   int tile;    // 128-column tile: of F (phases 0 and 1), of H (phase 2)
@@ -195,7 +194,7 @@ struct FewWalk {
   FewSplit s;
   int phase, u, u0, u1;
   int kbs, kbr, shared, per;  // stages of the shared expert's and a routed expert's k, of all shared entries, of a tile
-  int ns, flush, run;
+  int ns, flush;
   __host__ __device__ __forceinline__ FewWalk(int ph, const FewParams& p, const FewGeo& g, int nact, int c, int G) {
     phase = ph;
     if (ph < 2) {
@@ -203,8 +202,7 @@ struct FewWalk {
       per = p.nsb1;
       s.set((ph == 0 ? p.nsh : nact) * ns * per, G);
       kbs = kbr = shared = per;
-      run = p.run;
-      flush = run >= 1 << 20 ? run : run * g.acc1;
+      flush = p.chain * g.il1 / p.ks;
     } else {
       ns = p.ns2;
       kbr = (p.nsb2 + g.sub2 - 1) / g.sub2;
@@ -212,9 +210,9 @@ struct FewWalk {
       shared = p.nsh * kbs;
       per = shared + nact * kbr;
       s.set(ns * per, G);
-      run = p.run < g.sub2 ? 1 : p.run / g.sub2;
-      flush = run >= 1 << 20 ? run : run * g.acc2;
+      flush = p.chain * g.il2 / (p.ks * g.sub2);
     }
+    if (flush < 1) flush = 1;
     u = u0 = s.start(c);
     u1 = s.start(c + 1);
   }
