@@ -5,7 +5,6 @@
 
 #include <atomic>
 #include <initializer_list>
-#include <type_traits>
 
 #include "few.cuh"
 #include "router_sel.cuh"
@@ -51,16 +50,6 @@ __device__ __forceinline__ void tmem_cp_32x128b_x4(uint32_t taddr, uint64_t desc
 }
 // kind::mxf4: E2M1 A and B (format 1), E8M0 scales (bit 23)
 __device__ __forceinline__ uint32_t idesc_mxf4(int N) { return idesc_nvf4_f32(128, N) | (1u << 23); }
-
-// weights on their way into L2 before their stage is free
-__device__ __forceinline__ void l2_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
-               "r"(c0), "r"(c1)
-               : "memory");
-}
-__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
 
 __device__ __forceinline__ void bulk_load_hint(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t pol) {
   asm volatile(
@@ -173,6 +162,15 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
 // ---------------------------------------------------------------------------
 // router
 // ---------------------------------------------------------------------------
+// a load whose line stays in L2 while the experts' weights stream through
+__device__ __forceinline__ uint4 ld_keep(const uint4* p, uint64_t policy) {
+  uint4 v;
+  asm volatile("ld.global.nc.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p), "l"(policy));
+  return v;
+}
+
 // logits[t][e], an item of NE experts x 8 tokens a block: its 8 warps share H, 8 products
 // to a 16-byte load, fp32 fused multiply-adds; the 32 lanes' sums meet in a halving
 // butterfly, the warps' in shared memory
@@ -181,6 +179,7 @@ __device__ __noinline__ void few_logits_of(const FewParams& p, FewCtl* c, int et
   const int warp = et >> 5, lane = et & 31;
   const int eg = (p.E + NE - 1) / NE, items = eg * ((p.T + 7) >> 3);
   const int nv = p.H >> 3;
+  const uint64_t keep = l2_policy_evict_last();
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const int e0 = item % eg * NE, t0 = item / eg * 8;
     const int ne = min(NE, p.E - e0), nt = min(8, p.T - t0);
@@ -189,11 +188,12 @@ __device__ __noinline__ void few_logits_of(const FewParams& p, FewCtl* c, int et
     float acc[32];  // [expert][token]
 #pragma unroll
     for (int j = 0; j < 32; ++j) acc[j] = 0.0f;
+#pragma unroll(NE == 1 ? 2 : 1)
     for (int v = et; v < nv; v += kFewEpi) {
       uint4 wv[NE], xv[8];
 #pragma unroll
       for (int i = 0; i < NE; ++i)
-        if (i < ne) wv[i] = __ldg(w + static_cast<size_t>(i) * nv + v);
+        if (i < ne) wv[i] = ld_keep(w + static_cast<size_t>(i) * nv + v, keep);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (j < nt) xv[j] = __ldg(x + static_cast<size_t>(j) * nv + v);
@@ -283,16 +283,16 @@ __device__ void few_split_x(const FewParams& p, int et) {
 // from the unbiased scores. Lane i < k leaves with slot i.
 __device__ void few_select(const FewParams& p, float* zs, int t, int lane, int& e_out, float& g_out) {
   const float* L = p.logits + static_cast<size_t>(t) * p.E;
+  float l[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) l[i] = lane + 32 * i < p.E ? __ldcg(L + lane + 32 * i) : -INFINITY;
   int e_sel = 0;
   if (p.force) {
     e_sel = static_cast<int>((static_cast<long long>(t) * p.k + lane) % p.E);
   } else {
     float z[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = lane + 32 * i;
-      z[i] = e < p.E ? __ldcg(L + e) : -INFINITY;
-    }
+    for (int i = 0; i < 8; ++i) z[i] = l[i];
     if (p.mode == RSEL_SOFTMAX) {
       float m = -INFINITY, s = 0.0f;
 #pragma unroll
@@ -373,15 +373,20 @@ __device__ void few_select(const FewParams& p, float* zs, int t, int lane, int& 
     }
   }
   const bool on = lane < p.k;
-  const float l = on ? __ldcg(L + e_sel) : -INFINITY;
+  float ls = -INFINITY;  // the selected expert's logit, from the lane that has it
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = __shfl_sync(0xffffffffu, l[i], e_sel & 31);
+    if (on && (e_sel >> 5) == i) ls = v;
+  }
   float w;
   if (p.mode == RSEL_SIGMOID) {
-    w = on ? 1.0f / (1.0f + expf(-l)) : 0.0f;
+    w = on ? 1.0f / (1.0f + expf(-ls)) : 0.0f;
   } else {
-    float m = l;
+    float m = ls;
 #pragma unroll
     for (int d = 8; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    w = on ? expf(l - m) : 0.0f;
+    w = on ? expf(ls - m) : 0.0f;
   }
   float sum = w;
 #pragma unroll
@@ -440,8 +445,8 @@ __device__ void few_plan(const FewParams& p, FewCtl* c, int et) {
   c->eoff[et] = off;
   if (et == 0) {
     c->nact = na;
-    c->mmax = most;
     c->off[na] = R;
+    c->geo = few_geo(p.P1, p.P2, p.T, most, p.mx);
   }
   epi_sync();
   for (int r = et; r < R; r += kFewEpi) {
@@ -494,49 +499,77 @@ __device__ bool few_route(const FewParams& p, FewCtl* c, int et) {
 // ---------------------------------------------------------------------------
 // ends of a tile
 // ---------------------------------------------------------------------------
-// The block's share of a cut tile to the workspace; true in every thread of the block
-// that is the last to arrive
-__device__ __forceinline__ bool few_leave(const float* acc, int n, float* part, size_t stride, const FewPieces& pc,
-                                          unsigned* cnt, FewCtl* c, int et) {
-  float4* dst = reinterpret_cast<float4*>(part + pc.slot(blockIdx.x) * stride);
+// The block's share of a cut tile that begins elsewhere, to the workspace
+__device__ __forceinline__ void few_leave(const float* acc, int n, float* part, size_t stride, unsigned* cnt, int et) {
+  float4* dst = reinterpret_cast<float4*>(part + blockIdx.x * stride);
   const float4* src = reinterpret_cast<const float4*>(acc);
   for (int i = et; i < n / 4; i += kFewEpi) __stcg(dst + i, src[i]);
-  __threadfence();
   epi_sync();
-  if (et == 0) c->flag = atomicAdd(cnt, 1u) == static_cast<unsigned>(pc.count() - 1) ? 1 : 0;
-  epi_sync();
-  if (c->flag == 0) return false;
-  __threadfence();
-  return true;
+  if (et == 0) red_release(cnt, 1u);
 }
-// The sum of a cut tile's n floats, in the blocks' order, into `acc`; four float4 of a
-// piece on their way at a time
-__device__ __forceinline__ void few_join(float* acc, int n, const float* part, size_t stride, const FewPieces& pc,
-                                         int et) {
+// The rest of a cut tile that begins here: once the other blocks' sums are there, added to
+// `acc` in the blocks' order. False when the wait ran out.
+__device__ __forceinline__ bool few_join(float* acc, int n, const float* part, size_t stride, const FewPieces& pc,
+                                         const unsigned* cnt, FewCtl* c, const FewParams& p, int et) {
+  bool ok = true;
+  if (et == 0) ok = wait_count(cnt, pc.c1 - pc.c0, c, p, 93);
+  if (!epi_all(ok)) return false;
+  float4* a = reinterpret_cast<float4*>(acc);
+  auto piece = [&](int b) { return reinterpret_cast<const float4*>(part + b * stride); };
+  auto add = [](float4& v, const float4& w) {
+    v.x += w.x;
+    v.y += w.y;
+    v.z += w.z;
+    v.w += w.w;
+  };
   const int n4 = n / 4;
-  for (int base = et; base < n4; base += 4 * kFewEpi) {
-    float4 v[4];
+  if (n4 <= kFewEpi) {
+    // few floats: eight pieces on their way at a time
+    if (et < n4) {
+      float4 v = a[et];
+      for (int b = pc.c0 + 1; b <= pc.c1; b += 8) {
+        float4 w[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
-    for (int b = pc.c0; b <= pc.c1; ++b) {
-      const float4* src = reinterpret_cast<const float4*>(part + pc.slot(b) * stride);
+        for (int k = 0; k < 8; ++k)
+          if (b + k <= pc.c1) w[k] = __ldcg(piece(b + k) + et);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (base + k * kFewEpi < n4) {
-          const float4 w = __ldcg(src + base + k * kFewEpi);
-          v[k].x += w.x;
-          v[k].y += w.y;
-          v[k].z += w.z;
-          v[k].w += w.w;
+        for (int k = 0; k < 8; ++k)
+          if (b + k <= pc.c1) add(v, w[k]);
+      }
+      a[et] = v;
+    }
+  } else {
+    // a thread's four float4 of two pieces
+    for (int base = et; base < n4; base += 4 * kFewEpi) {
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (base + k * kFewEpi < n4) v[k] = a[base + k * kFewEpi];
+      for (int b = pc.c0 + 1; b <= pc.c1; b += 2) {
+        const float4 *s0 = piece(b), *s1 = piece(min(b + 1, pc.c1));
+        float4 w0[4], w1[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (base + k * kFewEpi < n4) {
+            w0[k] = __ldcg(s0 + base + k * kFewEpi);
+            w1[k] = __ldcg(s1 + base + k * kFewEpi);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (base + k * kFewEpi < n4) {
+            add(v[k], w0[k]);
+            if (b < pc.c1) add(v[k], w1[k]);
+          }
         }
       }
-    }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (base + k * kFewEpi < n4) reinterpret_cast<float4*>(acc)[base + k * kFewEpi] = v[k];
+      for (int k = 0; k < 4; ++k)
+        if (base + k * kFewEpi < n4) a[base + k * kFewEpi] = v[k];
+    }
   }
   epi_sync();
+  return true;
 }
 
 // SwiGLU of an entry's rows x 128 columns from h1, h3 (fp32 sums acc [rows][2][128]), gated, split
@@ -632,77 +665,45 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if constexpr (!MX)
         for (int i = 0; i < (p.Fs ? 6 : 3); ++i) tma_prefetch_desc(&maps.m[i]);
       const uint64_t pol = l2_policy_evict_first();
-      // one stage's weights: into shared memory (LOAD), or into L2
-      auto weights = [&](auto load, const FewGeo& g, int ph, const FewChunk& ch, int kb, uint8_t* sA, uint64_t* bar) {
-        constexpr bool LOAD = decltype(load)::value;
-        const bool sh = ch.i < 0;
-        const int e = sh ? 0 : c->act[ch.i];
-        const int nsb = ph < 2 ? p.nsb1 : sh ? p.nsb2s : p.nsb2;
-        const int sb0 = ph < 2 ? kb : kb * g.sub2, ns = ph < 2 ? 2 : min(g.sub2, nsb - sb0);
-        if constexpr (MX) {
-          // a stage's tiles are one run of bytes
-          const uint8_t* w = ph < 2 ? (sh ? p.w13s : p.w13) : (sh ? p.w2s : p.w2);
-          const size_t t = (static_cast<size_t>(e) * (ph == 2 ? p.ns2 : sh ? p.ns1s : p.ns1) + ch.tile) * nsb + sb0;
-          const uint8_t* src = w + t * (ph < 2 ? 2 : 1) * few_tile(true);
-          const uint32_t bytes = ns * few_tile(true);
-          if constexpr (LOAD) {
-            mbar_arrive_expect_tx(bar, bytes);
-            bulk_load_hint(sA, src, bytes, bar, pol);
-          } else {
-            l2_prefetch(src, bytes);
-          }
-        } else {
-          auto box = [&](uint8_t* dst, const CUtensorMap* m, int c0, int c1) {
-            if constexpr (LOAD) tma_load_2d_hint(dst, m, bar, c0, c1, pol);
-            else l2_prefetch_2d(m, c0, c1);
-          };
-          if constexpr (LOAD) mbar_arrive_expect_tx(bar, ns * kFewATile);
-          for (int q = 0; q < ns; ++q) {
-            // phases 0, 1: W1's and W3's tile of one k sub-block; 2: W2's of two
-            const CUtensorMap* m = &maps.m[(sh ? 3 : 0) + (ph < 2 ? q : 2)];
-            const int row = ph < 2 ? e * p.H + kb * 64 : e * (sh ? p.Fs : p.F) + (sb0 + q) * 64;
-            box(sA + q * kFewATile, m, ch.tile * 128, row);
-            box(sA + q * kFewATile + 8192, m, ch.tile * 128 + 64, row);
-          }
-        }
-      };
       int n = 0;  // stages so far
       bool ok = true;
       FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), MX);
       for (int ph = first_phase; ph < 3 && ok; ++ph) {
         if (ph == 1) {
           if (!mbar_wait_bounded(&c->plan, 0, abort_flag, p.lim, p.status, 83)) break;
-          g = few_geo(p.P1, p.P2, p.T, c->mmax, MX);
+          g = c->geo;
         }
-        bool ahead = ph == 2;
         FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
         FewChunk ch;
         while (ok && w.next(ch)) {
+          const bool sh = ch.i < 0;
+          const int e = sh ? 0 : c->act[ch.i];
+          const int nsb = !w.down ? p.nsb1 : sh ? p.nsb2s : p.nsb2;
           for (int kb = ch.kb; kb < ch.kb + ch.nkb; ++kb, ++n) {
             const int s = n % g.nst;
-            const uint32_t parity = ((n / g.nst) & 1) ^ 1;
-            if (!mbar_try_wait(c->empty + s, parity)) {
-              if (ahead) {
-                // the ring is full and the blocks are about to wait for the last activations:
-                // the memory goes on with what comes next
-                FewWalk aw = w;
-                FewChunk ac = ch;
-                ac.nkb -= kb - ac.kb;
-                ac.kb = kb;
-                for (int i = 0; i < kFewAhead; ++i) {
-                  if (ac.nkb == 0 && !aw.next(ac)) break;
-                  weights(std::false_type{}, g, ph, ac, ac.kb, nullptr, nullptr);
-                  ++ac.kb;
-                  --ac.nkb;
-                }
-                ahead = false;
-              }
-              if (!mbar_wait_bounded(c->empty + s, parity, abort_flag, p.lim, p.status, 84)) {
-                ok = false;
-                break;
+            if (!mbar_wait_bounded(c->empty + s, ((n / g.nst) & 1) ^ 1, abort_flag, p.lim, p.status, 84)) {
+              ok = false;
+              break;
+            }
+            uint8_t* sA = smem + s * g.stage;
+            uint64_t* bar = c->full + s;
+            const int sb0 = !w.down ? kb : kb * g.sub2, ns = !w.down ? 2 : min(g.sub2, nsb - sb0);
+            if constexpr (MX) {
+              // a stage's tiles are one run of bytes
+              const uint8_t* src = !w.down ? (sh ? p.w13s : p.w13) : (sh ? p.w2s : p.w2);
+              const size_t t = (static_cast<size_t>(e) * (w.down ? p.ns2 : sh ? p.ns1s : p.ns1) + ch.tile) * nsb + sb0;
+              mbar_arrive_expect_tx(bar, ns * few_tile(true));
+              bulk_load_hint(sA, src + t * (w.down ? 1 : 2) * few_tile(true), ns * few_tile(true), bar, pol);
+            } else {
+              mbar_arrive_expect_tx(bar, ns * kFewATile);
+              for (int q = 0; q < ns; ++q) {
+                // W1's and W3's tile of one k sub-block, or W2's of two
+                const CUtensorMap* m = &maps.m[(sh ? 3 : 0) + (w.down ? 2 : q)];
+                const int row = w.down ? e * (sh ? p.Fs : p.F) + (sb0 + q) * 64 : e * p.H + kb * 64;
+                tma_load_2d_hint(sA + q * kFewATile, m, bar, ch.tile * 128, row, pol);
+                tma_load_2d_hint(sA + q * kFewATile + 8192, m, bar, ch.tile * 128 + 64, row, pol);
               }
             }
-            weights(std::true_type{}, g, ph, ch, kb, smem + s * g.stage, c->full + s);
           }
         }
       }
@@ -731,17 +732,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     for (int ph = first_phase; ph < 3 && ok; ++ph) {
       if (ph == 1) {
         if (!warp_wait(&c->plan, 0, c, p, 85)) break;
-        g = few_geo(p.P1, p.P2, p.T, c->mmax, MX);
+        g = c->geo;
       }
       FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
       FewChunk ch;
-      const int parts = ph < 2 ? p.P1 : p.P2;
-      const int nbuf = ph < 2 ? g.nbuf1 : g.nbuf2;
-      const int il = ph < 2 ? g.il1 : g.il2, il_cols = ph < 2 ? 2 * g.n1 : g.n2;
+      const int parts = w.down ? p.P2 : p.P1;
+      const int nbuf = w.down ? g.nbuf2 : g.nbuf1;
+      const int il = w.down ? g.il2 : g.il1, il_cols = w.down ? g.n2 : 2 * g.n1;
       const int acc_cols = il * il_cols;
       na = 0;
-      // the phases lay their accumulators out differently: all earlier ones have been read
-      for (int b = 0; b < 2 && ok; ++b)
+      // W2's accumulators are laid out differently: all of the others have been read
+      for (int b = 0; b < 2 && ok && ph == 2; ++b)
         if (used[b] > 0) ok = warp_wait(c->tempty + b, (used[b] & 1) ^ 1, c, p, 86);
       while (ok && w.next(ch)) {
         const int N = few_cols(parts, FewRows(p, c, ch.i).m);
@@ -768,14 +769,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             const uint32_t sA = smem_u32(smem) + s * g.stage;
             const uint32_t a0 = sdesc_lo(sA, MX ? 16u : 8192u), b0 = sdesc_lo(sA + 2 * few_tile(MX), 16u);
             int ns = 2;
-            if (ph == 2) ns = min(g.sub2, (ch.i < 0 ? p.nsb2s : p.nsb2) - kb * g.sub2);
-            const int nblk = ph < 2 ? g.nblk1 : g.nblk2;
+            if (w.down) ns = min(g.sub2, (ch.i < 0 ? p.nsb2s : p.nsb2) - kb * g.sub2);
+            const int nblk = w.down ? g.nblk2 : g.nblk1;
             const uint32_t region = tmem + kFewSfCol + (n & 1) * kFewSfRegion;
             if constexpr (MX) {
               // scales to tensor memory, four columns for 128 rows and 128 elements: A's two a
               // tile, behind its codes, then B's two for 128 rows
               const uint32_t sfa = sdesc_lo(sA + kFewATile, 128u), sfb = sdesc_lo(sA + 2 * few_tile(true) + g.b_bytes, 128u);
-              const int nb = 2 * (ph < 2 ? nblk : ns * nblk);
+              const int nb = 2 * (w.down ? ns * nblk : nblk);
               for (int q = 0; q < 2 * ns; ++q)
                 tmem_cp_32x128b_x4(region + 4 * q,
                                    sf_hi | (sfa + (((q >> 1) * few_tile(true) + (q & 1) * kFewSf) >> 4)));
@@ -790,7 +791,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               // phases 0, 1: W1's and W3's tile against the same tokens, accumulators of their
               // own; phase 2: two sub-blocks of W2, each against its own. Step kk along k of
               // either goes to accumulator kk % il
-              if (ph < 2) {
+              if (!w.down) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -828,68 +829,72 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     bool ok = true;
     FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), MX);
     for (int ph = first_phase; ph < 3 && ok; ++ph) {
-      if (ph == 0 && MX) {
-        // the parts of x come from all blocks
-        if (lane == 0) ok = wait_count(p.sync, gridDim.x, c, p, 88);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
-      }
+      const unsigned* counter = nullptr;
+      unsigned want = 0;
       if (ph == 1) {
         if (!warp_wait(&c->plan, 0, c, p, 89)) break;
-        g = few_geo(p.P1, p.P2, p.T, c->mmax, MX);
+        g = c->geo;
       }
-      if (ph == 2) {
-        // all activations are there
-        if (lane == 0) ok = wait_count(p.sync + 2, p.nsh * p.ns1s + c->nact * p.ns1, c, p, 90);
+      FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
+      if (ph == 0 && MX) {  // the parts of x come from all blocks
+        counter = p.sync;
+        want = gridDim.x;
+      } else if (ph == 2) {  // all activations
+        counter = p.sync + 2;
+        want = p.nsh * p.ns1s + c->nact * p.ns1;
+      }
+      if (counter != nullptr && w.u < w.u1) {
+        if (lane == 0) ok = wait_count(counter, want, c, p, 90);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok) break;
       }
-      FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
       FewChunk ch;
-      const int parts = ph < 2 ? p.P1 : p.P2;
+      const int parts = w.down ? p.P2 : p.P1;
       while (ok && w.next(ch)) {
         const bool sh = ch.i < 0;
         const FewRows rw(p, c, ch.i);
         const int m = rw.m, rows = parts * m;
         // bytes of a row of the operand and of its scales
-        const int len = MX ? (ph < 2 ? p.H : sh ? p.Fs : p.F) >> 1 : 2 * (ph < 2 ? p.H : sh ? p.Fs : p.F);
-        const uint8_t* base = ph < 2 ? (MX ? p.xq : reinterpret_cast<const uint8_t*>(p.x)) : sh ? p.as : p.a;
-        const uint8_t* sf = ph < 2 ? p.x_sf : sh ? p.as_sf : p.a_sf;
-        // column n of the operand is row j's part n / m: where that row begins
-        auto row_of = [&](int n) {
-          const int part = n / m, j = n - part * m;
-          const int r = ph < 2 && !sh ? c->tok[rw.r0 + j] : rw.r0 + j;
-          return static_cast<size_t>(r) * parts + part;
-        };
+        const int width = !w.down ? p.H : sh ? p.Fs : p.F, len = MX ? width >> 1 : 2 * width;
+        const uint8_t* base = !w.down ? (MX ? p.xq : reinterpret_cast<const uint8_t*>(p.x)) : sh ? p.as : p.a;
+        const uint8_t* sf = !w.down ? p.x_sf : sh ? p.as_sf : p.a_sf;
+        // column n of the operand is row j's part n / m: the source's row, once a chunk
+        // (each of the two warps has a table: no barrier that one of them might not reach)
+        uint16_t* table = c->rows[warp - 2];
+        __syncwarp();
+        for (int r = lane; r < rows; r += 32) {
+          const int part = r / m, j = r - part * m;
+          table[r] = static_cast<uint16_t>((!w.down && !sh ? c->tok[rw.r0 + j] : rw.r0 + j) * parts + part);
+        }
+        __syncwarp();
+        const int nsb = sh ? p.nsb2s : p.nsb2;
         for (int kb = ch.kb; kb < ch.kb + ch.nkb; ++kb, ++n) {
           const int s = n % g.nst;
           if (!warp_wait(c->empty + s, ((n / g.nst) & 1) ^ 1, c, p, 91)) {
             ok = false;
             break;
           }
-          const uint32_t sB = smem_u32(smem) + s * g.stage + 2 * few_tile(MX);
-          int ns = 1, sb0 = kb;
-          if (ph == 2) {
-            sb0 = kb * g.sub2;
-            ns = min(g.sub2, (sh ? p.nsb2s : p.nsb2) - sb0);
-          }
+          uint32_t sB = smem_u32(smem) + s * g.stage + 2 * few_tile(MX);
+          uint32_t sS = sB + g.b_bytes;
+          const int sb0 = w.down ? kb * g.sub2 : kb, ns = w.down ? min(g.sub2, nsb - sb0) : 1;
           for (int q = 0; q < ns; ++q) {
-            const int at = (sb0 + q) * kSubBytes;
-            const uint32_t sBq = sB + q * g.n2 * kSubBytes;
-            for (int it = ct; it < rows * 8; it += kFewCopiers) {
-              const int r = it >> 3, ck = it & 7;
-              const bool in = at + ck * 16 < len;  // beyond a row's end: zeros
-              cp_async16(sBq + r * 128 + ((ck ^ (r & 7)) << 4), base + row_of(r) * len + (in ? at + ck * 16 : 0), in);
-            }
+            // thread: 16-byte chunk ct % 8 of rows ct / 8, + 8, ..; zeros beyond a row's end
+            const int at = (sb0 + q) * kSubBytes + (ct & 7) * 16;
+            const bool in = at < len;
+            const uint8_t* src = base + (in ? at : 0);
+            const uint32_t dst = sB + (ct >> 3) * 128 + (((ct & 7) ^ ((ct >> 3) & 7)) << 4);
+            for (int r = ct >> 3, i = 0; r < rows; r += 8, ++i)
+              cp_async16(dst + i * 1024, src + static_cast<size_t>(table[r]) * len, in);
             if constexpr (MX) {
-              const int slen = len >> 4, nblk = ph < 2 ? g.nblk1 : g.nblk2;
-              const uint32_t sS = sB + g.b_bytes + 2 * kFewSf * nblk * q;
-              for (int it = ct; it < rows * 2; it += kFewCopiers) {
-                const int r = it >> 1, half = it & 1, b = (sb0 + q) * 8 + half * 4;
+              const int slen = len >> 4, nblk = w.down ? g.nblk2 : g.nblk1;
+              const int half = ct & 1, b = (sb0 + q) * 8 + half * 4;
+              const uint8_t* ssrc = sf + (b < slen ? b : 0);
+              for (int r = ct >> 1; r < rows; r += kFewCopiers / 2)
                 cp_async4(sS + kFewSf * (nblk * half + (r >> 7)) + 16 * (r & 31) + 4 * ((r >> 5) & 3),
-                          sf + row_of(r) * slen + (b < slen ? b : 0), b < slen);
-              }
+                          ssrc + static_cast<size_t>(table[r]) * slen, b < slen);
+              sS += 2 * kFewSf * nblk;
             }
+            sB += g.n2 * kSubBytes;
           }
           cp_async_arrive(c->full + s);
         }
@@ -904,23 +909,23 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     bool ok = few_route<MX>(p, c, et);
     if (ok && et == 0) mbar_arrive(&c->plan);
     int used[2] = {0, 0};
-    const FewGeo g = few_geo(p.P1, p.P2, p.T, ok ? c->mmax : 1, MX);
+    const FewGeo g = c->geo;
     float* acc = reinterpret_cast<float*>(smem + g.acc_off);
     unsigned* cnt = p.cnt;
     for (int ph = first_phase; ph < 3 && ok; ++ph) {
       FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
       FewChunk ch;
-      const int nbuf = ph < 2 ? g.nbuf1 : g.nbuf2;
-      const int il = ph < 2 ? g.il1 : g.il2, il_cols = ph < 2 ? 2 * g.n1 : g.n2;
+      const int nbuf = w.down ? g.nbuf2 : g.nbuf1;
+      const int il = w.down ? g.il2 : g.il1, il_cols = w.down ? g.n2 : 2 * g.n1;
       const int acc_cols = il * il_cols;
-      const int parts = ph < 2 ? p.P1 : p.P2;
+      const int parts = w.down ? p.P2 : p.P1;
       int na = 0;
       while (ok && w.next(ch)) {
         const FewRows rw(p, c, ch.i);
         const int m = rw.m;
         const int buf = na % nbuf;
         ++na;
-        if (ph == 2 && ch.first) {
+        if (w.down && ch.first) {
           for (int i = et; i < p.T * 32; i += kFewEpi) reinterpret_cast<float4*>(acc)[i] = make_float4(0, 0, 0, 0);
           epi_sync();
         }
@@ -928,8 +933,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         if (!ok) break;
         ++used[buf];
         tc_fence_after();
-        const uint32_t d0 = tl + buf * acc_cols + (ph < 2 ? half * g.n1 : 0);
-        for (int j0 = ph < 2 ? 0 : 8 * half; j0 < m; j0 += ph < 2 ? 8 : 16) {
+        const uint32_t d0 = tl + buf * acc_cols + (w.down ? 0 : half * g.n1);
+        for (int j0 = w.down ? 8 * half : 0; j0 < m; j0 += w.down ? 16 : 8) {
           float v[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] = 0.0f;
@@ -949,7 +954,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             if (j0 + j < m) {
-              if (ph < 2) {
+              if (!w.down) {
                 float* a = acc + (j0 + j) * 256 + half * 128 + row;
                 *a = ch.first ? v[j] : *a + v[j];
               } else {
@@ -963,35 +968,24 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         if (lane == 0) mbar_arrive(c->tempty + buf);
         epi_sync();
         if (!ch.last) continue;
-        const int ti = w.tile_index(), u0 = ti * w.per;
-        const FewPieces pc(w.s, u0, u0 + w.per);
-        if (ph < 2) {
-          float* part = ph == 0 ? p.part0 : p.part1;
-          const size_t stride = static_cast<size_t>(p.T) * 256;
-          bool mine = true;
-          if (pc.count() > 1) {
-            mine = few_leave(acc, m * 256, part, stride, pc, cnt + ti, c, et);
-            if (mine) few_join(acc, m * 256, part, stride, pc, et);
-          }
-          if (mine) {
-            few_activate<MX>(p, c, acc, rw, ch.i, ch.tile, et);
-            __threadfence();
-          }
-          epi_sync();
-          if (mine && et == 0) red_release(p.sync + 2, 1u);
+        const int ti = w.tile_index(), n = w.down ? p.T * 128 : m * 256;
+        const FewPieces pc = w.pieces(ti);
+        const size_t stride = static_cast<size_t>(p.T) * (w.down ? 128 : 256);
+        if (static_cast<int>(blockIdx.x) != pc.c0) {
+          few_leave(acc, n, p.part[ph], stride, cnt + ti, et);
         } else {
-          const size_t stride = static_cast<size_t>(p.T) * 128;
-          bool mine = true;
-          if (pc.count() > 1) {
-            mine = few_leave(acc, p.T * 128, p.part2, stride, pc, cnt + ti, c, et);
-            if (mine) few_join(acc, p.T * 128, p.part2, stride, pc, et);
+          if (pc.c1 > pc.c0) ok = few_join(acc, n, p.part[ph], stride, pc, cnt + ti, c, p, et);
+          if (!ok) break;
+          if (!w.down) {
+            few_activate<MX>(p, c, acc, rw, ch.i, ch.tile, et);
+          } else {
+            for (int i = et; i < n; i += kFewEpi) few_store_y(p, i >> 7, 128 * ch.tile + (i & 127), acc[i]);
           }
-          if (mine)
-            for (int i = et; i < p.T * 128; i += kFewEpi) few_store_y(p, i >> 7, 128 * ch.tile + (i & 127), acc[i]);
-          epi_sync();
         }
+        epi_sync();
+        if (!w.down && static_cast<int>(blockIdx.x) == pc.c0 && et == 0) red_release(p.sync + 2, 1u);
       }
-      cnt += ph == 0 ? p.nsh * p.ns1s : kFewMaxEnt * p.ns1;
+      cnt += ph == 0 ? p.nsh * p.ns1s : c->nact * p.ns1;
     }
   }
   tc_fence_before();
@@ -1018,7 +1012,7 @@ static size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Where things lie in the workspace
 struct FewLayout {
-  size_t logits, cnt, part0, part1, part2, a, as, a_sf, as_sf, xq, x_sf, total;
+  size_t logits, cnt, part[3], a, as, a_sf, as_sf, xq, x_sf, total;
   int cnt_words;
 };
 static int few_parts1(const moe_config& c, bool mx) { return mx ? (c.out_fp32 ? 8 : 5) : 1; }
@@ -1037,10 +1031,9 @@ static FewLayout few_layout(const moe_config& c, bool mx, int G) {
   L.cnt_words = c.T * ((c.F_shared + 127) / 128) + kFewMaxEnt * ((c.F + 127) / 128) + (c.H + 127) / 128;
   L.logits = take(4 * T * c.E);
   L.cnt = take(4 * static_cast<size_t>(L.cnt_words));
-  // a block's two partials of a phase
-  L.part0 = take(Fs ? 2 * static_cast<size_t>(G) * T * 256 * 4 : 0);
-  L.part1 = take(2 * static_cast<size_t>(G) * T * 256 * 4);
-  L.part2 = take(2 * static_cast<size_t>(G) * T * 128 * 4);
+  // a block's partial sums of a phase
+  for (int ph = 0; ph < 3; ++ph)
+    L.part[ph] = take(ph == 0 && !Fs ? 0 : static_cast<size_t>(G) * T * (ph < 2 ? 256 : 128) * 4);
   L.a = take(mx ? R * P2 * F / 2 : R * P2 * F * 2);
   L.as = take(mx ? T * P2 * Fs / 2 : T * P2 * Fs * 2);
   if (mx) {
@@ -1095,6 +1088,7 @@ int run_few(const moe_config& c, const FewArgs& q, bool mx, void* ws, cudaStream
   p.gate_scale = c.gate_scale;
   p.P1 = few_parts1(c, mx);
   p.P2 = few_parts2(c, mx);
+  p.mx = mx ? 1 : 0;
   p.mcap = few_mcap(p.P1, mx);
   p.nsh = c.F_shared ? (c.T + p.mcap - 1) / p.mcap : 0;
   p.msh = p.nsh ? (c.T + p.nsh - 1) / p.nsh : 0;
@@ -1118,9 +1112,7 @@ int run_few(const moe_config& c, const FewArgs& q, bool mx, void* ws, cudaStream
   p.logits = reinterpret_cast<float*>(base + L.logits);
   p.cnt = reinterpret_cast<unsigned*>(base + L.cnt);
   p.cnt_words = L.cnt_words;
-  p.part0 = reinterpret_cast<float*>(base + L.part0);
-  p.part1 = reinterpret_cast<float*>(base + L.part1);
-  p.part2 = reinterpret_cast<float*>(base + L.part2);
+  for (int ph = 0; ph < 3; ++ph) p.part[ph] = reinterpret_cast<float*>(base + L.part[ph]);
   p.a = base + L.a; p.as = base + L.as; p.a_sf = base + L.a_sf; p.as_sf = base + L.as_sf;
   p.xq = base + L.xq; p.x_sf = base + L.x_sf;
   p.lim = wait_limit_ns();

@@ -10,19 +10,21 @@
 // never stops:
 //  - the units of a phase (one weight tile of 32 KB each in shared memory) are
 //    dealt to the blocks in equal contiguous runs, whatever the experts' number;
-//    a tile cut by a run's border is joined from fp32 partials by whichever of
-//    its blocks comes last, always in the blocks' order;
+//    a tile cut by a run's border is joined from fp32 partials by the block that has its
+//    beginning, in the blocks' order. The others have theirs at the start of their
+//    runs, so that the partials are mostly there when they are wanted: the end of a
+//    phase is then four trips to L2 (a partial, the activations there and back, a
+//    count), 9 us of 71 less for one token than with the last block to arrive joining;
 //  - one thread copies weights (TMA) as far ahead as the ring of stages allows,
 //    over the borders of tiles and phases: while the blocks wait for one another
 //    between the phases, the next phase's weights are already on their way;
 //  - the tokens' operand follows by 16-byte copies of two other warps as soon as
 //    it exists.
 //
-// Phases: 0 the shared expert's gate and up products (needs no routing: its
-// weights stream while the router works), 1 the routed experts', 2 all down
-// products. A stage of phases 0 and 1 holds one k sub-block (128 bytes: 64 bf16,
-// 256 MXFP4 elements) of 128 columns of W1 and of W3, a stage of phase 2 up to two
-// sub-blocks of 128 columns of W2.
+// Phases: 0 the shared expert's gate and up products (needs no routing: its weights
+// stream while the router works), 1 the routed experts', 2 all down products. A stage of
+// phases 0 and 1 holds one k sub-block (128 bytes: 64 bf16, 256 MXFP4 elements) of 128
+// columns of W1 and of W3, a stage of phase 2 up to two sub-blocks of 128 columns of W2.
 //
 // Operands: bf16 weights multiply bf16 parts of the tokens (x itself; the activation
 // a in two parts, three for fp32 results: 2^-17 and 2^-25 of a). MXFP4 weights stay
@@ -49,15 +51,23 @@ constexpr int kFewMaxEnt = 320;    // runs of rows of one expert
 constexpr int kFewATile = 16384;   // 128 columns x 128 bytes
 constexpr int kFewSf = 512;        // scales of 128 columns (rows) x 128 MXFP4 elements
 constexpr int kFewSmem = 232448;   // 227 KB
-constexpr int kFewAhead = 0;       // stages of phase 2 asked for into L2 while the blocks wait
 constexpr int kFewRedundant = 16;  // tokens up to which every block selects for itself
 
+// What a stage holds and how many there are, from the largest number of rows
+struct FewGeo {
+  int n1, n2;                // columns of an expert's N operand, at most
+  int sub2;                  // sub-blocks of a stage of W2
+  int b_bytes, nblk1, nblk2, stage, nst;
+  int acc_off;               // fp32 sums in shared memory
+  int il1, il2;              // accumulators that the steps along k take in turn
+  int nbuf1, nbuf2;          // chunks in tensor memory at a time
+};
 // A block's own plan of the batch (shared memory)
 struct FewCtl {
   uint64_t full[kFewStages], empty[kFewStages], tfull[2], tempty[2], plan, drain;
   uint32_t tmem;
   int abort;
-  int nact, mmax;            // entries: runs of rows of one expert; most rows of one
+  int nact;                  // entries: runs of rows of one expert
   int flag;
   int warp_sum[8], warp_act[8], warp_max[8];
   uint32_t has[256][2];      // expert -> its tokens
@@ -68,7 +78,9 @@ struct FewCtl {
   float gate[kFewMaxR];      // row -> gate
   uint8_t eidx[kFewMaxR];    // slot (token-major) -> expert
   float sgate[kFewMaxR];     // slot -> gate
+  uint16_t rows[2][448];     // a copying warp's chunk: column of the N operand -> row of its source
   float scratch[8][256];     // a warp's selection values; the router's partial sums
+  FewGeo geo;
 };
 constexpr int kFewCtl = (sizeof(FewCtl) + 1023) / 1024 * 1024;
 constexpr int kFewCtlOff = kFewSmem - kFewCtl;
@@ -78,6 +90,7 @@ struct FewParams {
   int mode, groups, topk_groups, force;  // router (RouterSelMode)
   float gate_scale;
   int P1, P2;                // parts of x and of a
+  int mx;                    // MXFP4 weights
   int mcap;                  // rows of an entry, at most
   int nsh, msh;              // entries of the shared expert, rows of one
   int chain;                 // products summed by one accumulator in tensor memory, at most
@@ -91,10 +104,10 @@ struct FewParams {
   float* gate;
   void* y;
   float* logits;             // [T, E]
-  unsigned* sync;            // barrier 1, barrier 2, finished tiles, ended blocks
-  unsigned* cnt;             // arrivals of a cut tile: phase 0, 1, 2
+  unsigned* sync;            // barrier 1, barrier 2, finished tiles of phases 0 and 1, ended blocks
+  unsigned* cnt;             // partials of a cut tile that are there: phase 0, 1, 2
   int cnt_words;
-  float *part0, *part1, *part2;
+  float* part[3];            // a phase's partial sums, a slot a block
   uint8_t *a, *as;           // parts of the activations: rows x parts x (F or Fs)
   uint8_t *a_sf, *as_sf;     // MXFP4: their scale bytes
   uint8_t *xq, *x_sf;        // MXFP4: parts of x and their scale bytes
@@ -106,15 +119,6 @@ struct FewMaps {
   CUtensorMap m[6];          // W1, W3, W2, Ws1, Ws3, Ws2 (bf16)
 };
 
-// What a stage holds and how many there are, from the largest number of rows
-struct FewGeo {
-  int n1, n2;                // columns of an expert's N operand, at most
-  int sub2;                  // sub-blocks of a phase 2 stage
-  int b_bytes, nblk1, nblk2, stage, nst;
-  int acc_off;               // fp32 sums in shared memory
-  int il1, il2;              // accumulators that the steps along k take in turn
-  int nbuf1, nbuf2;          // chunks in tensor memory at a time
-};
 __host__ __device__ constexpr int few_tile(bool mx) { return kFewATile + (mx ? 2 * kFewSf : 0); }
 // columns of the N operand: part q of row j is column q m + j
 __host__ __device__ __forceinline__ int few_cols(int parts, int m) { return (parts * m + 15) & ~15; }
@@ -154,37 +158,33 @@ __host__ __device__ __forceinline__ FewGeo few_geo(int P1, int P2, int T, int mm
 // join than the blocks gain.
 constexpr int kFewRun = 4;
 struct FewSplit {
-  int U, G;
+  int U, G, q, r;  // units, blocks; the first r blocks have q + 1 units, the others q
   __host__ __device__ __forceinline__ void set(int units, int blocks) {
     U = units;
     const int most = (units + kFewRun - 1) / kFewRun;
     G = blocks < most ? blocks : most;
+    q = G > 0 ? U / G : 0;
+    r = U - q * G;
   }
-  __host__ __device__ __forceinline__ int start(int c) const {
-    return c >= G ? U : static_cast<int>(static_cast<long long>(U) * c / G);
-  }
+  __host__ __device__ __forceinline__ int start(int c) const { return c >= G ? U : c * q + (c < r ? c : r); }
   // the block that has unit u
   __host__ __device__ __forceinline__ int owner(int u) const {
-    return static_cast<int>(((static_cast<long long>(u) + 1) * G - 1) / U);
+    const int big = r * (q + 1);
+    return u < big ? u / (q + 1) : r + (u - big) / q;
   }
 };
-// Blocks c0 .. c1 share the tile of units [u0, u1). A block has at most one share that
-// begins inside a tile (its first) and one that ends inside (its last): its two slots
-// in the workspace.
+// Blocks c0 .. c1 share a tile. c0 has its beginning and joins it; the others leave their
+// sums in their slot of the workspace (a block has at most one share that begins inside a
+// tile: its first).
 struct FewPieces {
   int c0, c1;
-  __host__ __device__ __forceinline__ FewPieces(const FewSplit& s, int u0, int u1) : c0(s.owner(u0)), c1(s.owner(u1 - 1)) {}
-  __host__ __device__ __forceinline__ int count() const { return c1 - c0 + 1; }
-  __host__ __device__ __forceinline__ size_t slot(int block) const {
-    return 2 * static_cast<size_t>(block) + (block == c0 ? 1 : 0);
-  }
 };
 
 // Consecutive stages of one tile and one expert, summed in tensor memory, that the
 // epilogue takes at once
 struct FewChunk {
   int i;       // entry; -1 - g: the shared expert's entry g
-  int tile;    // 128-column tile: of F (phases 0 and 1), of H (phase 2)
+  int tile;    // 128-column tile: of F (phases 0 to 2), of H
   int kb, nkb; // first stage of the expert's k, stages
   bool first, last;  // of this block's segment of the tile
 };
@@ -193,11 +193,13 @@ struct FewChunk {
 struct FewWalk {
   FewSplit s;
   int phase, u, u0, u1;
+  bool down;
   int kbs, kbr, shared, per;  // stages of the shared expert's and a routed expert's k, of all shared entries, of a tile
   int ns, flush;
   __host__ __device__ __forceinline__ FewWalk(int ph, const FewParams& p, const FewGeo& g, int nact, int c, int G) {
     phase = ph;
-    if (ph < 2) {
+    down = ph == 2;
+    if (!down) {
       ns = ph == 0 ? p.ns1s : p.ns1;
       per = p.nsb1;
       s.set((ph == 0 ? p.nsh : nact) * ns * per, G);
@@ -216,11 +218,15 @@ struct FewWalk {
     u = u0 = s.start(c);
     u1 = s.start(c + 1);
   }
+  // the blocks that share tile t of the phase
+  __host__ __device__ __forceinline__ FewPieces pieces(int t) const {
+    return FewPieces{s.owner(t * per), s.owner((t + 1) * per - 1)};
+  }
   __host__ __device__ __forceinline__ bool next(FewChunk& c) {
     if (u >= u1) return false;
     const int t = u / per, r = u - t * per;
     int lim;
-    if (phase < 2) {
+    if (!down) {
       const int e = t / ns;
       c.i = phase == 0 ? -1 - e : e;
       c.tile = t - e * ns;
