@@ -10,9 +10,15 @@
 //   dr = a dH,  dy = ry (g dH wp - y ry^2 / H S2),  S2 = sum g dH wp y,
 // and since dH is linear in S1, S2 = SA + S1 SB with sums of A and B alone: one
 // reduction over the block for a row. The gradients of the weights and of a channel
-// gate are sums over rows: a thread adds its columns' in fp32 over at most 64 rows,
-// then in two floats in the workspace; a second kernel joins the blocks' in order.
+// gate are sums over rows, dpre's of dn h rh and one more for both others,
+//   D = sum g_t dH y ry  (g_t: a token's gate),  dpost = g D,  dgate = wp D:
+// a thread adds its columns' in fp32 over at most 64 rows, then in two floats in the
+// workspace; a second kernel joins the blocks' in order.
+#include <atomic>
+#include <type_traits>
+
 #include "host_util.h"
+#include "mma.cuh"
 
 namespace moe {
 
@@ -28,6 +34,7 @@ struct NormParams {
   void *h, *dr;
   __nv_bfloat16 *n, *dy;
   float *stats, *dgate, *part;
+  int lo;                    // a block has more than kNormFlush rows: sums in two floats
   const float* cstats;
 };
 
@@ -195,195 +202,301 @@ __device__ __forceinline__ void two_add(float& hi, float& lo, float v) {
   hi = s;
 }
 
-template <bool RF, bool OF, int NC>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ NormParams p) {
+// A thread's 16-byte copies of its columns of the rows ahead, `S` rows deep in shared
+// memory; it waits for its own copies alone. Rows of four tensors lie behind one another,
+// fp32 ones in two planes of 16 bytes a thread.
+template <bool RF, bool OF, int NC, int S>
+struct NormRing {
+  static constexpr int kY = OF ? 2 : 1, kR = RF ? 2 : 1;  // planes
+  uint8_t* base;
+  int n8;
+  __device__ __forceinline__ uint8_t* at(int stage, int plane, int i) const {
+    return base + ((static_cast<size_t>(stage) * (2 * kY + 2 * kR) + plane) * n8 + i) * 16;
+  }
+  template <int P>
+  __device__ __forceinline__ void put(int stage, int plane, int i, const void* src, size_t i8) const {
+    const uint4* q = static_cast<const uint4*>(src) + P * i8;
+#pragma unroll
+    for (int k = 0; k < P; ++k) cp_async16(smem_u32(at(stage, plane + k, i)), q + k, true);
+  }
+  // y, the residual, dn, dh of a row (those that there are)
+  __device__ __forceinline__ void load(const NormParams& p, int stage, int row) const {
+    if (row < p.T) {
+      const size_t r8 = static_cast<size_t>(row) * n8;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int i = threadIdx.x + c * blockDim.x;
+        if (i < n8) {
+          put<kY>(stage, 0, i, p.y, r8 + i);
+          if (p.pre) put<kY>(stage, kY, i, p.dn, r8 + i);
+          if (p.res) put<kR>(stage, 2 * kY, i, p.r, r8 + i);
+          if (p.dh != nullptr) put<kR>(stage, 2 * kY + kR, i, p.dh, r8 + i);
+        }
+      }
+    }
+    cp_async_commit();
+  }
+  template <bool F32>
+  __device__ __forceinline__ void get(int stage, int plane, int i, float (&v)[8]) const {
+    Vec8<F32> x;
+    x.a = *reinterpret_cast<const uint4*>(at(stage, plane, i));
+    if constexpr (F32) x.b = *reinterpret_cast<const uint4*>(at(stage, plane + 1, i));
+    x.get(v);
+  }
+};
+
+// FULL: with a post norm or a gate, whose gradients are another sum a column. A thread
+// holds a column's sums, its weights, A and h: 64 registers for 8 columns, two blocks of
+// 512 threads an SM (or one of 1024). S: rows on their way in shared memory; 0: straight from
+// global memory (rows too long for it).
+template <bool RF, bool OF, bool FULL, int NC, int S>
+__global__ void __launch_bounds__(1024, 1) norm_bwd_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2 * 96];
+  using Ring = NormRing<RF, OF, NC, S>;
   chain_wait();
   chain_release();
   int turn = 0;
   const int n8 = p.H >> 3;
   const float inv = 1.0f / static_cast<float>(p.H);
-  const bool channel = p.gate == MOE_GATE_CHANNEL, token = p.gate == MOE_GATE_TOKEN;
-  const bool second = p.post || token;  // a sum for dy or for the token's gate
-  float an[NC][8], ap[NC][8], ag[NC][8];  // of dpre, dpost, dgate
+  const bool token = FULL && p.gate == MOE_GATE_TOKEN, post = FULL && p.post;
+  const bool sum_d = FULL && (p.post || p.gate == MOE_GATE_CHANNEL);
+  float an[NC][8], ad[FULL ? NC : 1][8];  // the sums of dpre and D
+  float wn[NC][8], gw[FULL ? NC : 1][8];  // pre weight, gate x post weight
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) an[c][j] = ap[c][j] = ag[c][j] = 0.0f;
-  // a block's sums: [3][H], then what two floats keep beyond
-  float* hi = p.part + static_cast<size_t>(blockIdx.x) * 6 * p.H;
+    for (int j = 0; j < 8; ++j) {
+      an[c][j] = wn[c][j] = 0.0f;
+      if constexpr (FULL) {
+        ad[c][j] = 0.0f;
+        gw[c][j] = 1.0f;
+      }
+    }
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int i = threadIdx.x + c * blockDim.x;
+    if (i < n8) {
+      if (p.pre) weights8(p.wn, i, wn[c]);
+      if constexpr (FULL) {
+        if (p.post) weights8(p.wp, i, gw[c]);
+        if (p.gate == MOE_GATE_CHANNEL) {
+          float g[8];
+          weights8(p.g, i, g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) gw[c][j] *= g[j];
+        }
+      }
+    }
+  }
+  // a block's sums: [2][H], then what two floats keep beyond
+  float* hi = p.part + static_cast<size_t>(blockIdx.x) * 4 * p.H;
   auto flush = [&](bool first) {
+    const size_t beyond = 2 * static_cast<size_t>(p.H);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int i = threadIdx.x + c * blockDim.x;
-      if (i >= n8) continue;
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        if (!(k == 0 ? p.pre : k == 1 ? p.post : channel)) continue;
-        float* d = hi + static_cast<size_t>(k) * p.H + 8 * i;
+      for (int k = 0; k < (FULL ? 2 : 1); ++k) {
+        float(&v)[8] = k == 0 ? an[c] : ad[FULL ? c : 0];
+        if (i < n8 && (k == 0 ? p.pre != 0 : sum_d)) {
+          float4* d = reinterpret_cast<float4*>(hi + static_cast<size_t>(k) * p.H) + 2 * i;
+          float4* e = reinterpret_cast<float4*>(hi + static_cast<size_t>(k) * p.H + beyond) + 2 * i;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float v = k == 0 ? an[c][j] : k == 1 ? ap[c][j] : ag[c][j], lo = 0.0f;
-          if (!first) {
-            float s = d[j];
-            lo = d[3 * static_cast<size_t>(p.H) + j];
-            two_add(s, lo, v);
-            v = s;
+          for (int q = 0; q < 2; ++q) {
+            float4 s = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            float4 lo = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (!first) {
+              const float4 w = s;
+              s = d[q];
+              lo = e[q];
+              two_add(s.x, lo.x, w.x);
+              two_add(s.y, lo.y, w.y);
+              two_add(s.z, lo.z, w.z);
+              two_add(s.w, lo.w, w.w);
+            }
+            d[q] = s;
+            if (p.lo) e[q] = lo;
           }
-          d[j] = v;
-          d[3 * static_cast<size_t>(p.H) + j] = lo;
         }
-      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) an[c][j] = ap[c][j] = ag[c][j] = 0.0f;
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+      }
     }
   };
-  int rows = 0;
+  const Ring ring{smem, n8};
+  if constexpr (S > 0)
+    for (int k = 0; k + 1 < S; ++k) ring.load(p, k, blockIdx.x + k * gridDim.x);
+  // a row's scalars, asked for a row ahead
+  float ry1 = 1.0f, rh1 = 0.0f, gt1 = 1.0f;
+  auto scalars = [&](int row) {
+    if (row < p.T) {
+      if (post) ry1 = p.cstats[2 * static_cast<size_t>(row)];
+      if (p.pre) rh1 = p.cstats[2 * static_cast<size_t>(row) + 1];
+      if (token) gt1 = p.g[row];
+    }
+  };
+  scalars(blockIdx.x);
+  int rows = 0, stage = 0;
   bool first = true;
   for (int row = blockIdx.x; row < p.T; row += gridDim.x) {
     const size_t r8 = static_cast<size_t>(row) * n8;
-    Vec8<OF> yv[NC], nv[NC];
-    Vec8<RF> rv[NC], hv[NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int i = threadIdx.x + c * blockDim.x;
-      if (i < n8) {
-        yv[c].load(p.y, r8 + i);
-        if (p.res) rv[c].load(p.r, r8 + i);
-        if (p.pre) nv[c].load(p.dn, r8 + i);
-        if (p.dh != nullptr) hv[c].load(p.dh, r8 + i);
-      }
+    if constexpr (S > 0) {
+      // (a thread reads and writes its own places only)
+      ring.load(p, stage == 0 ? S - 1 : stage - 1, row + (S - 1) * gridDim.x);
+      cp_async_wait<S - 1>();
     }
-    const float ry = p.post ? p.cstats[2 * static_cast<size_t>(row)] : 1.0f;
-    const float rh = p.pre ? p.cstats[2 * static_cast<size_t>(row) + 1] : 0.0f;
-    const float gt = token ? p.g[row] : 1.0f;
-    const float bf = -rh * rh * rh * inv;
-    float s[3] = {0.0f, 0.0f, 0.0f};
-    float A[NC][8], h[NC][8], u[NC][8];
+    const float ry = ry1, rh = rh1, gt = gt1, bf = -rh * rh * rh * inv;
+    scalars(row + gridDim.x);
+    auto get_own = [&](int i, auto f32, const void* src, int plane, float(&v)[8]) {
+      constexpr bool F32 = decltype(f32)::value;
+      if constexpr (S > 0) {
+        ring.template get<F32>(stage, plane, i, v);
+      } else {
+        Vec8<F32> x;
+        x.load(src, r8 + i);
+        x.get(v);
+      }
+    };
+    constexpr std::bool_constant<RF> rf{};
+    constexpr std::bool_constant<OF> of{};
+    float s0 = 0.0f, sa = 0.0f, sb = 0.0f;
+    float A[NC][8], h[NC][8];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int i = threadIdx.x + c * blockDim.x;
       if (i < n8) {
-        float w[8], g[8], t[8];
-        yv[c].get(u[c]);
-        if (p.post) {
-          weights8(p.wp, i, w);
+        float t[8], x[8];  // x: what the sums for dy (or a token's gate) take A and B with
+        get_own(i, of, p.y, 0, x);
+        if constexpr (FULL) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) u[c][j] = u[c][j] * ry * w[j];
+          for (int j = 0; j < 8; ++j) x[j] = x[j] * ry * gw[c][j];
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = gt;
-        if (channel) weights8(p.g, i, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[c][j] = g[j] * u[c][j];
+        for (int j = 0; j < 8; ++j) h[c][j] = token ? gt * x[j] : x[j];
         if (p.res) {
-          rv[c].get(t);
+          get_own(i, rf, p.r, 2 * Ring::kY, t);
 #pragma unroll
           for (int j = 0; j < 8; ++j) h[c][j] = fmaf(p.a, t[j], h[c][j]);
         }
-        if (p.dh != nullptr) hv[c].get(A[c]);
-        else {
+        if (p.dh != nullptr) {
+          get_own(i, rf, p.dh, 2 * Ring::kY + Ring::kR, A[c]);
+        } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) A[c][j] = 0.0f;
         }
         if (p.pre) {
-          nv[c].get(t);
-          weights8(p.wn, i, w);
+          get_own(i, of, p.dn, Ring::kY, t);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             an[c][j] = fmaf(t[j], h[c][j] * rh, an[c][j]);
-            const float d = t[j] * w[j];
-            s[0] = fmaf(d, h[c][j], s[0]);
+            const float d = t[j] * wn[c][j];
+            s0 = fmaf(d, h[c][j], s0);
             A[c][j] = fmaf(rh, d, A[c][j]);
           }
         }
-        if (second) {
-          // g u = g y ry wp: the sums are of ry S2; a token's gate wants them without g
+        if constexpr (FULL) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float x = (token ? 1.0f : g[j]) * u[c][j];
-            s[1] = fmaf(A[c][j], x, s[1]);
-            s[2] = fmaf(bf * h[c][j], x, s[2]);
+            sa = fmaf(A[c][j], x[j], sa);
+            sb = fmaf(bf * h[c][j], x[j], sb);
           }
         }
       }
     }
     float s1 = 0.0f, s2 = 0.0f;
-    if (p.pre || second) {
+    if constexpr (FULL) {
+      float s[3] = {s0, sa, sb};
       block_sum(s, red, turn);
       s1 = s[0] * bf;
       s2 = fmaf(s[0], s[2], s[1]);
+    } else {
+      float s[1] = {s0};
+      block_sum(s, red, turn);
+      s1 = s[0] * bf;
     }
     if (token && threadIdx.x == 0) p.dgate[row] = s2;
-    // dy = ry (g dH wp) - y ry^2 / H (ry S2)
-    const float yf = p.post ? (token ? gt : 1.0f) * s2 * ry * ry * inv : 0.0f;
+    // dy = ry (g dH wp) - (y ry) ry / H (ry S2); a token's sums are without its g
+    const float yf = post ? (token ? gt : 1.0f) * s2 * ry * inv : 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int i = threadIdx.x + c * blockDim.x;
       if (i < n8) {
-        float w[8], g[8], t[8], d[8];
+        float (&d)[8] = A[c];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = fmaf(s1, h[c][j], A[c][j]);
+        for (int j = 0; j < 8; ++j) d[j] = fmaf(s1, h[c][j], d[j]);
         if (p.res) {
+          float t[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) t[j] = p.a * d[j];
           store8<RF>(p.dr, r8 + i, t);
         }
-        if (channel) {
-          weights8(p.g, i, g);
+        if constexpr (FULL) {
+          float t[8];
+          get_own(i, of, p.y, 0, t);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            ag[c][j] = fmaf(d[j], u[c][j], ag[c][j]);
-            d[j] *= g[j];
-          }
-        } else if (token) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] *= gt;
-        }
-        if (p.post) {
-          weights8(p.wp, i, w);
-          yv[c].get(t);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            ap[c][j] = fmaf(d[j], t[j] * ry, ap[c][j]);
-            d[j] = fmaf(d[j] * w[j], ry, -t[j] * yf);
+            t[j] *= ry;
+            d[j] *= gt;
+            ad[c][j] = fmaf(d[j], t[j], ad[c][j]);
+            d[j] = ry * (d[j] * gw[c][j]) - t[j] * yf;
           }
         }
         store8<false>(p.dy, r8 + i, d);
       }
     }
-    if (++rows == kNormFlush) {
+    if (p.part != nullptr && ++rows == kNormFlush) {
       flush(first);
       first = false;
       rows = 0;
     }
+    if (++stage == S) stage = 0;
   }
   if (p.part != nullptr && (rows > 0 || first)) flush(first);
+  if constexpr (S > 0) cp_async_wait_all();
 }
 
-// out[k][j] = sum over the blocks of hi + lo; a thread a column and a sixteenth of the blocks
-__global__ void __launch_bounds__(512) norm_join_kernel(const float* part, int blocks, int H, float* dpre, float* dpost,
-                                                        float* dgate) {
-  __shared__ double s[16][33];
+// dpre (blockIdx.y 0), or dpost and dgate from D (1): sums over the blocks of hi + lo, in two
+// floats; a thread a column and a sixteenth of the blocks, four of them on their way at a
+// time
+__global__ void __launch_bounds__(512) norm_join_kernel(const float* part, int blocks, int H, int lo, const float* wp,
+                                                        const float* g, float* dpre, float* dpost, float* dgate) {
+  __shared__ float s[2][16][33];
   chain_wait();
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), k = blockIdx.y, q = threadIdx.x >> 5;
-  float* out = k == 0 ? dpre : k == 1 ? dpost : dgate;
-  if (out == nullptr) return;
-  double v = 0.0;
+  const int lane = threadIdx.x & 31, col = blockIdx.x * 32 + lane, k = blockIdx.y, q = threadIdx.x >> 5;
+  if (k == 0 ? dpre == nullptr : dpost == nullptr && dgate == nullptr) return;
+  float hi = 0.0f, rest = 0.0f;
   if (col < H) {
     const float* src = part + static_cast<size_t>(k) * H + col;
-    for (int b = q; b < blocks; b += 16) {
-      const float* r = src + static_cast<size_t>(b) * 6 * H;
-      v += static_cast<double>(__ldcg(r)) + static_cast<double>(__ldcg(r + 3 * static_cast<size_t>(H)));
+    const size_t step = 4 * static_cast<size_t>(H);
+    for (int b = q; b < blocks; b += 64) {
+      float v[4], w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* r = src + (b + 16 * i) * step;
+        v[i] = b + 16 * i < blocks ? __ldcg(r) : 0.0f;
+        w[i] = lo && b + 16 * i < blocks ? __ldcg(r + 2 * static_cast<size_t>(H)) : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        two_add(hi, rest, v[i]);
+        rest += w[i];
+      }
     }
   }
-  s[q][threadIdx.x & 31] = v;
+  s[0][q][lane] = hi;
+  s[1][q][lane] = rest;
   __syncthreads();
   if (q == 0 && col < H) {
-    double t = 0.0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t += s[i][threadIdx.x];
-    out[col] = static_cast<float>(t);
+    for (int i = 1; i < 16; ++i) {
+      two_add(hi, rest, s[0][i][lane]);
+      rest += s[1][i][lane];
+    }
+    const float d = hi + rest;
+    if (k == 0) dpre[col] = d;
+    if (k == 1 && dpost != nullptr) dpost[col] = g != nullptr ? g[col] * d : d;
+    if (k == 1 && dgate != nullptr) dgate[col] = wp != nullptr ? wp[col] * d : d;
   }
 }
 
@@ -397,27 +510,62 @@ static int check_norm(const moe_norm_config* c) {
   if (c->H % 8 || c->H > kNormMaxH) return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
 }
-static int norm_blocks(const moe_norm_config& c) { return c.T < 2 * num_sms() ? c.T : 2 * num_sms(); }
+// runs of 8 columns a thread in the backward
+static int norm_runs(int H) { return H <= 8192 ? 1 : 2; }
+static dim3 norm_threads(int H, int nc) { return dim3(((H / 8 + nc - 1) / nc + 31) / 32 * 32); }
+// blocks of the backward: those that an SM holds at once, at 64 registers a thread
+static int norm_blocks(const moe_norm_config& c) {
+  const int per = 1024 / static_cast<int>(norm_threads(c.H, norm_runs(c.H)).x);
+  const int most = (per < 16 ? per : 16) * num_sms();
+  return c.T < most ? c.T : most;
+}
 static bool norm_sums(const moe_norm_config& c) { return c.pre || c.post || c.gate == MOE_GATE_CHANNEL; }
 
-// runs of 8 columns a thread: 512 threads at most
-static int norm_runs(int H) { return H <= 1024 ? 1 : H <= 8192 ? 2 : 4; }
-static dim3 norm_threads(int H) {
-  const int nc = norm_runs(H), n = (H / 8 + nc - 1) / nc;
-  return dim3((n + 31) / 32 * 32);
-}
+constexpr size_t kNormSmem = 230400;
 
-template <bool BWD>
-static cudaError_t launch_norm(const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
-  const int nc = norm_runs(c.H);
-  auto go = [&](auto kern) { return launch_chained(kern, dim3(grid), norm_threads(c.H), 0, s, p); };
-#define MOE_NORM(RF, OF)                                                                       \
-  (nc == 1   ? go(BWD ? norm_bwd_kernel<RF, OF, 1> : norm_fwd_kernel<RF, OF, 1>)               \
-   : nc == 2 ? go(BWD ? norm_bwd_kernel<RF, OF, 2> : norm_fwd_kernel<RF, OF, 2>)               \
-             : go(BWD ? norm_bwd_kernel<RF, OF, 4> : norm_fwd_kernel<RF, OF, 4>))
-  if (c.residual_fp32) return c.out_fp32 ? MOE_NORM(true, true) : MOE_NORM(true, false);
-  return c.out_fp32 ? MOE_NORM(false, true) : MOE_NORM(false, false);
-#undef MOE_NORM
+template <bool RF, bool OF, int NC>
+static cudaError_t launch_fwd(const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
+  return launch_chained(norm_fwd_kernel<RF, OF, NC>, dim3(grid), norm_threads(c.H, NC), 0, s, p);
+}
+template <bool RF, bool OF, bool FULL, int NC, int S>
+static cudaError_t launch_bwd(const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
+  const size_t bytes = static_cast<size_t>(S) * c.H * (2 * (OF ? 4 : 2) + 2 * (RF ? 4 : 2));
+  if constexpr (S > 0) {
+    static std::atomic<unsigned long long> set{0};  // devices whose kernel has its shared memory
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!(set.load() & (1ull << (dev & 63)))) {
+      e = cudaFuncSetAttribute(norm_bwd_kernel<RF, OF, FULL, NC, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
+      if (e != cudaSuccess) return e;
+      set.fetch_or(1ull << (dev & 63));
+    }
+  }
+  return launch_chained(norm_bwd_kernel<RF, OF, FULL, NC, S>, dim3(grid), norm_threads(c.H, NC), bytes, s, p);
+}
+// rows on their way: two where an SM's blocks have the shared memory for it, one beside
+// the row at work else, none for the longest rows
+template <bool RF, bool OF, bool FULL>
+static cudaError_t launch_bwd(const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
+  const size_t row = static_cast<size_t>(c.H) * (2 * (OF ? 4 : 2) + 2 * (RF ? 4 : 2));
+  const int per = 1024 / static_cast<int>(norm_threads(c.H, 1).x);
+  if (c.H > 8192) return launch_bwd<RF, OF, FULL, 2, 0>(c, p, grid, s);
+  if (3 * row * (per < 16 ? per : 16) <= kNormSmem) return launch_bwd<RF, OF, FULL, 1, 3>(c, p, grid, s);
+  if (2 * row <= kNormSmem) return launch_bwd<RF, OF, FULL, 1, 2>(c, p, grid, s);
+  return launch_bwd<RF, OF, FULL, 1, 0>(c, p, grid, s);
+}
+template <bool RF, bool OF>
+static cudaError_t launch_norm(bool bwd, const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
+  const int n8 = c.H / 8;
+  if (!bwd) {
+    if (n8 <= 128) return launch_fwd<RF, OF, 1>(c, p, grid, s);
+    return n8 <= 1024 ? launch_fwd<RF, OF, 2>(c, p, grid, s) : launch_fwd<RF, OF, 4>(c, p, grid, s);
+  }
+  return c.post || c.gate ? launch_bwd<RF, OF, true>(c, p, grid, s) : launch_bwd<RF, OF, false>(c, p, grid, s);
+}
+static cudaError_t launch_norm(bool bwd, const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
+  if (c.residual_fp32) return c.out_fp32 ? launch_norm<true, true>(bwd, c, p, grid, s) : launch_norm<true, false>(bwd, c, p, grid, s);
+  return c.out_fp32 ? launch_norm<false, true>(bwd, c, p, grid, s) : launch_norm<false, false>(bwd, c, p, grid, s);
 }
 
 struct NormArray {
@@ -468,14 +616,14 @@ int moe_block_norm_fwd(const moe_norm_config* cfg, const void* y, const void* re
   p.h = h; p.n = reinterpret_cast<__nv_bfloat16*>(n); p.stats = stats;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int most = 16 * num_sms();
-  r = status_from_cuda(launch_norm<false>(c, p, c.T < most ? c.T : most, s));
+  r = status_from_cuda(launch_norm(false, c, p, c.T < most ? c.T : most, s));
   if (r == MOE_OK) record_stage(s, 53, 1);
   return r;
 }
 
 size_t moe_norm_workspace_bytes(const moe_norm_config* cfg) {
   if (check_norm(cfg) != MOE_OK) return 0;
-  return sizeof(DevStatus) + 24ull * cfg->H * norm_blocks(*cfg);
+  return sizeof(DevStatus) + 16ull * cfg->H * norm_blocks(*cfg);
 }
 
 int moe_block_norm_bwd(const moe_norm_config* cfg, const void* dh, const void* dn, const void* y,
@@ -519,17 +667,20 @@ int moe_block_norm_bwd(const moe_norm_config* cfg, const void* dh, const void* d
   p.res = c.residual; p.gate = c.gate; p.post = c.post; p.pre = c.pre;
   p.y = y; p.r = residual; p.dh = dh; p.dn = dn; p.wp = post_weight; p.g = gate; p.wn = pre_weight;
   p.dr = dresidual; p.dy = reinterpret_cast<__nv_bfloat16*>(dy); p.cstats = stats; p.dgate = dgate;
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sizeof(DevStatus));
+  p.part = norm_sums(c) ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sizeof(DevStatus)) : nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int blocks = norm_blocks(c);
-  r = status_from_cuda(launch_norm<true>(c, p, blocks, s));
+  p.lo = c.T > kNormFlush * blocks ? 1 : 0;
+  r = status_from_cuda(launch_norm(true, c, p, blocks, s));
   if (r != MOE_OK) return r;
   record_stage(s, 54, 1);
   if (!norm_sums(c)) return MOE_OK;
   const float* part = p.part;
-  float* dg = c.gate == MOE_GATE_CHANNEL ? dgate : nullptr;
-  r = status_from_cuda(launch_chained(norm_join_kernel, dim3((c.H + 31) / 32, 3), dim3(512), 0, s, part, blocks, c.H,
-                                      dpre_weight, dpost_weight, dg));
+  const bool channel = c.gate == MOE_GATE_CHANNEL;
+  float* dg = channel ? dgate : nullptr;
+  const float* cg = channel ? gate : nullptr;
+  r = status_from_cuda(launch_chained(norm_join_kernel, dim3((c.H + 31) / 32, 2), dim3(512), 0, s, part, blocks, c.H,
+                                      p.lo, post_weight, cg, dpre_weight, dpost_weight, dg));
   if (r == MOE_OK) record_stage(s, 55, 1);
   return r;
 }
