@@ -247,10 +247,11 @@ struct NormRing {
 
 // FULL: with a post norm or a gate, whose gradients are another sum a column. A thread
 // holds a column's sums, its weights, A and h: 64 registers for 8 columns, two blocks of
-// 512 threads an SM (or one of 1024). S: rows on their way in shared memory; 0: straight from
+// 512 threads an SM or one of MAXT (72 registers up to 896 threads: the 64 of 1024 spill,
+// into an L1 that shared memory has left small). S: rows on their way in shared memory; 0: straight from
 // global memory (rows too long for it).
-template <bool RF, bool OF, bool FULL, int NC, int S>
-__global__ void __launch_bounds__(1024, 1) norm_bwd_kernel(const __grid_constant__ NormParams p) {
+template <bool RF, bool OF, bool FULL, int NC, int S, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1) norm_bwd_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2 * 96];
   using Ring = NormRing<RF, OF, NC, S>;
@@ -514,9 +515,12 @@ static int check_norm(const moe_norm_config* c) {
 static int norm_runs(int H) { return H <= 8192 ? 1 : 2; }
 static dim3 norm_threads(int H, int nc) { return dim3(((H / 8 + nc - 1) / nc + 31) / 32 * 32); }
 // blocks of the backward: those that an SM holds at once, at 64 registers a thread
+static int norm_per_sm(int H) {
+  const int per = 1024 / static_cast<int>(norm_threads(H, norm_runs(H)).x);
+  return per < 16 ? per : 16;
+}
 static int norm_blocks(const moe_norm_config& c) {
-  const int per = 1024 / static_cast<int>(norm_threads(c.H, norm_runs(c.H)).x);
-  const int most = (per < 16 ? per : 16) * num_sms();
+  const int most = norm_per_sm(c.H) * num_sms();
   return c.T < most ? c.T : most;
 }
 static bool norm_sums(const moe_norm_config& c) { return c.pre || c.post || c.gate == MOE_GATE_CHANNEL; }
@@ -527,32 +531,35 @@ template <bool RF, bool OF, int NC>
 static cudaError_t launch_fwd(const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
   return launch_chained(norm_fwd_kernel<RF, OF, NC>, dim3(grid), norm_threads(c.H, NC), 0, s, p);
 }
-template <bool RF, bool OF, bool FULL, int NC, int S>
+template <bool RF, bool OF, bool FULL, int NC, int S, int MAXT>
 static cudaError_t launch_bwd(const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
   const size_t bytes = static_cast<size_t>(S) * c.H * (2 * (OF ? 4 : 2) + 2 * (RF ? 4 : 2));
+  const auto kernel = norm_bwd_kernel<RF, OF, FULL, NC, S, MAXT>;
   if constexpr (S > 0) {
     static std::atomic<unsigned long long> set{0};  // devices whose kernel has its shared memory
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (!(set.load() & (1ull << (dev & 63)))) {
-      e = cudaFuncSetAttribute(norm_bwd_kernel<RF, OF, FULL, NC, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
       if (e != cudaSuccess) return e;
       set.fetch_or(1ull << (dev & 63));
     }
   }
-  return launch_chained(norm_bwd_kernel<RF, OF, FULL, NC, S>, dim3(grid), norm_threads(c.H, NC), bytes, s, p);
+  return launch_chained(kernel, dim3(grid), norm_threads(c.H, NC), bytes, s, p);
 }
 // rows on their way: two where an SM's blocks have the shared memory for it, one beside
 // the row at work else, none for the longest rows
 template <bool RF, bool OF, bool FULL>
 static cudaError_t launch_bwd(const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
   const size_t row = static_cast<size_t>(c.H) * (2 * (OF ? 4 : 2) + 2 * (RF ? 4 : 2));
-  const int per = 1024 / static_cast<int>(norm_threads(c.H, 1).x);
-  if (c.H > 8192) return launch_bwd<RF, OF, FULL, 2, 0>(c, p, grid, s);
-  if (3 * row * (per < 16 ? per : 16) <= kNormSmem) return launch_bwd<RF, OF, FULL, 1, 3>(c, p, grid, s);
-  if (2 * row <= kNormSmem) return launch_bwd<RF, OF, FULL, 1, 2>(c, p, grid, s);
-  return launch_bwd<RF, OF, FULL, 1, 0>(c, p, grid, s);
+  if (c.H > 8192) return launch_bwd<RF, OF, FULL, 2, 0, 1024>(c, p, grid, s);
+  if (c.H > 7168)
+    return 2 * row <= kNormSmem ? launch_bwd<RF, OF, FULL, 1, 2, 1024>(c, p, grid, s)
+                                : launch_bwd<RF, OF, FULL, 1, 0, 1024>(c, p, grid, s);
+  if (c.H > 4096) return launch_bwd<RF, OF, FULL, 1, 2, 896>(c, p, grid, s);  // (at most 224 KB)
+  return 3 * row * norm_per_sm(c.H) <= kNormSmem ? launch_bwd<RF, OF, FULL, 1, 3, 512>(c, p, grid, s)
+                                                 : launch_bwd<RF, OF, FULL, 1, 2, 512>(c, p, grid, s);
 }
 template <bool RF, bool OF>
 static cudaError_t launch_norm(bool bwd, const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
