@@ -754,7 +754,8 @@ int moe_mx4_dequantize_weights(const moe_config* cfg, const moe_mx4_weights* w, 
  * aux_coeff have no effect): the tensor cores multiply bf16 weights with x and with
  * a = gate SiLU(x W1) (x W3) in two bf16 parts (2^-17 of a; three, 2^-25, with
  * out_fp32). topk_idx [T,k] and topk_gate [T,k] receive the routing. y may be x
- * itself. Every sum has a fixed order. A row's infinities and NaN reach its own
+ * itself (both bf16); any other overlap of an output is MOE_ERR_INVALID_ARG. Every
+ * sum has a fixed order. A row's infinities and NaN reach its own
  * results only; infinities may become NaN.
  * The kernel's blocks wait for one another (a cooperative launch over all SMs),
  * with bounded waits: MOE_ERR_DEVICE_TIMEOUT in the workspace's status. The
@@ -840,8 +841,9 @@ size_t moe_abi_struct_bytes(int which);
 /* Test hooks (not for production use). moe_debug_set_wait_limit_ns sets the
  * limit of every bounded device wait (default 2e9 ns = 2 s; 0 restores the
  * default). moe_debug_set_fault(1) makes the permute scan's first token chunk
- * skip publishing its counts, so that the other chunks' waits run out and the
- * device status reports MOE_ERR_DEVICE_TIMEOUT; moe_debug_set_fault(0) turns
+ * skip publishing its counts, and the few-token kernel's first block its arrivals at
+ * the blocks' barriers, so that the others' waits run out and the device status
+ * reports MOE_ERR_DEVICE_TIMEOUT; moe_debug_set_fault(0) turns
  * it off. Both are process-wide. */
 void moe_debug_set_wait_limit_ns(long long ns);
 void moe_debug_set_fault(int fault);

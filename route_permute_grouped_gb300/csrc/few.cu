@@ -111,7 +111,7 @@ __device__ __forceinline__ bool grid_sync(unsigned* counter, FewCtl* c, const Fe
   epi_sync();
   if (et == 0) {
     __threadfence();
-    red_release(counter, 1u);
+    if (!(p.fault && blockIdx.x == 0)) red_release(counter, 1u);
     wait_count(counter, gridDim.x, c, p, where);
   }
   epi_sync();
@@ -1116,6 +1116,7 @@ int run_few(const moe_config& c, const FewArgs& q, bool mx, void* ws, cudaStream
   p.a = base + L.a; p.as = base + L.as; p.a_sf = base + L.a_sf; p.as_sf = base + L.as_sf;
   p.xq = base + L.xq; p.x_sf = base + L.x_sf;
   p.lim = wait_limit_ns();
+  p.fault = debug_fault();
   FewMaps maps;
   memset(&maps, 0, sizeof(maps));
   bool ok = true;
@@ -1152,13 +1153,38 @@ static bool few_aligned(std::initializer_list<const void*> ps, uintptr_t to) {
     if (reinterpret_cast<uintptr_t>(p) & (to - 1)) return false;
   return true;
 }
+// bytes of what a call reads and writes: outputs may overlap nothing else, but y may be x
+struct FewArray {
+  const void* p;
+  size_t bytes;
+};
 static int few_call(const moe_config* cfg, const FewArgs& q, bool mx, void* ws, size_t ws_bytes, void* stream) {
+  const moe_config& c = *cfg;
   if (!q.x || !q.router_w || !q.topk_idx || !q.topk_gate || !q.y || !ws) return MOE_ERR_INVALID_ARG;
   if (!few_aligned({q.x, q.router_w, q.expert_bias, q.logit_bias, q.topk_idx, q.topk_gate, q.y, ws}, 16))
     return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < few_workspace_bytes(*cfg, mx)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = few_workspace_bytes(c, mx);
+  const size_t TH = static_cast<size_t>(c.T) * c.H, Tk = 4 * static_cast<size_t>(c.T) * c.k, HF = static_cast<size_t>(c.H) * c.F;
+  const size_t HFs = static_cast<size_t>(c.H) * c.F_shared;
+  const FewArray out[4] = {{q.y, TH * (c.out_fp32 ? 4 : 2)}, {q.topk_idx, Tk}, {q.topk_gate, Tk}, {ws, need}};
+  FewArray in[10] = {{q.x, 2 * TH}, {q.router_w, 2 * static_cast<size_t>(c.E) * c.H}, {q.expert_bias, 4ull * c.E},
+                     {q.logit_bias, 4ull * c.E}, {q.W1, 2 * c.E * HF}, {q.W3, 2 * c.E * HF}, {q.W2, 2 * c.E * HF},
+                     {c.F_shared ? q.Ws1 : nullptr, 2 * HFs}, {c.F_shared ? q.Ws3 : nullptr, 2 * HFs},
+                     {c.F_shared ? q.Ws2 : nullptr, 2 * HFs}};
+  if (mx) {
+    const uint8_t* w[4] = {q.mx4->w13, q.mx4->w2, c.F_shared ? q.mx4->w13s : nullptr, c.F_shared ? q.mx4->w2s : nullptr};
+    for (int i = 0; i < 4; ++i) in[4 + i] = FewArray{w[i], moe_mx4_weight_bytes(cfg, i)};
+  }
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return MOE_ERR_INVALID_ARG;
+    for (int j = 0; j < 10; ++j)
+      if (overlap(out[i].p, out[i].bytes, in[j].p, in[j].bytes) && !(i == 0 && j == 0 && q.y == q.x && !c.out_fp32))
+        return MOE_ERR_INVALID_ARG;
+  }
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int r = run_few(*cfg, q, mx, ws, s);
+  const int r = run_few(c, q, mx, ws, s);
   if (r == MOE_OK) record_stage(s, 50, 1);
   return r;
 }

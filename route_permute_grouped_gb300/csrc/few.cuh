@@ -114,6 +114,7 @@ struct FewParams {
   const uint8_t *w13, *w2, *w13s, *w2s;  // MXFP4 tiles, codes and scales
   DevStatus* status;
   unsigned long long lim;
+  int fault;                 // test hook: block 0 does not arrive at the blocks' barriers
 };
 struct FewMaps {
   CUtensorMap m[6];          // W1, W3, W2, Ws1, Ws3, Ws2 (bf16)

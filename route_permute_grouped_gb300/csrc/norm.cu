@@ -190,8 +190,10 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const __grid_constant__ N
         }
       }
       if (threadIdx.x == 0) p.stats[2 * static_cast<size_t>(row) + 1] = rh;
+    } else if (threadIdx.x == 0) {
+      p.stats[2 * static_cast<size_t>(row) + 1] = 0.0f;
     }
-    if (threadIdx.x == 0 && p.post) p.stats[2 * static_cast<size_t>(row)] = ry;
+    if (threadIdx.x == 0) p.stats[2 * static_cast<size_t>(row)] = ry;
   }
 }
 
