@@ -1137,41 +1137,43 @@ class MoeMx4Weights(ctypes.Structure):
     _fields_ = [(n, c_void_p) for n in ("w13", "w2", "w13s", "w2s")]
 
 
-def _mx4_rows(where, x, K):
+def _mx4_rows(where, name, t, per):
+    """(M, K) of a matrix with `per` elements a value, refused where its rows hold no blocks of 32."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} must be a matrix")
+    M, K = t.shape
+    K *= per
     if K < 1 or K % 32:
         raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, f"{where}: rows must hold blocks of 32")
-    if x < 1:
+    if M < 1:
         raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: there must be rows")
+    return M, K
 
 
 def mx4_quantize(x):
     """MXFP4 of the rows of x [M, K] bf16 (K a multiple of 32): (codes [M, K/2]
     uint8, element 2j in the low nibble, scales [M, K/32] uint8, E8M0)."""
-    w = "mx4_quantize"
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{w}: x must be a matrix")
-    M, K = x.shape
-    _mx4_rows(w, M, K)
-    xp = _arg(w, "x", x, torch.bfloat16, (M, K))
-    codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
-    _check(lib().moe_mx4_quantize(xp, M, K, codes.data_ptr(), scales.data_ptr(), _stream(x.get_device())),
-           "moe_mx4_quantize")
+    M, K = _mx4_rows("mx4_quantize", "x", x, 1)
+    xp = _arg("mx4_quantize", "x", x, torch.bfloat16, (M, K))
+    dev, u8 = x.device, torch.uint8
+    codes, scales = torch.empty((M, K // 2), dtype=u8, device=dev), torch.empty((M, K // 32), dtype=u8, device=dev)
+    st = lib().moe_mx4_quantize(xp, M, K, codes.data_ptr(), scales.data_ptr(), _stream(dev.index))
+    if st:
+        _check(st, "moe_mx4_quantize")
     return codes, scales
 
 
 def mx4_dequantize(codes, scales):
     """The values [M, K] bf16 that mx4_quantize's codes and scales stand for, exactly."""
     w = "mx4_dequantize"
-    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{w}: codes must be a matrix")
-    M, K = codes.shape[0], 2 * codes.shape[1]
-    _mx4_rows(w, M, K)
+    M, K = _mx4_rows(w, "codes", codes, 2)
     cp = _arg(w, "codes", codes, torch.uint8, (M, K // 2))
-    d = codes.get_device()
-    sp = _arg(w, "scales", scales, torch.uint8, (M, K // 32), d)
-    x = torch.empty((M, K), dtype=torch.bfloat16, device=codes.device)
-    _check(lib().moe_mx4_dequantize(cp, sp, M, K, x.data_ptr(), _stream(d)), "moe_mx4_dequantize")
+    dev = codes.device
+    sp = _arg(w, "scales", scales, torch.uint8, (M, K // 32), dev.index)
+    x = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    st = lib().moe_mx4_dequantize(cp, sp, M, K, x.data_ptr(), _stream(dev.index))
+    if st:
+        _check(st, "moe_mx4_dequantize")
     return x
 
 
@@ -1307,16 +1309,41 @@ def norm_workspace(cfg, device="cuda"):
     return _scratch(_size("moe_norm_workspace_bytes", cfg), device)
 
 
-def _norm_args(w, cfg, y, residual, post_weight, gate, pre_weight, d=None):
-    T, H, f32 = cfg.T, cfg.H, torch.float32
-    p = [_arg(w, "y", y, _out_dtype(cfg), (T, H), d)]
+class _NormPlan:
+    """What a norm config says, read from the struct once: shapes, types, flags."""
+
+    def __init__(self, cfg):
+        self.nbytes = _size("moe_norm_workspace_bytes", cfg)
+        self.T, self.H = cfg.T, cfg.H
+        self.full, self.vec, self.stats = (cfg.T, cfg.H), (cfg.H,), (cfg.T, 2)
+        self.stream = torch.float32 if cfg.residual_fp32 else torch.bfloat16
+        self.io = _out_dtype(cfg)
+        self.residual, self.post, self.pre = bool(cfg.residual), bool(cfg.post), bool(cfg.pre)
+        self.gate = (None, (cfg.H,), (cfg.T,))[cfg.gate]
+
+
+_norm_plans = {}
+
+
+def _norm_plan(cfg):
+    key = bytes(cfg)
+    plan = _norm_plans.get(key)
+    if plan is None:
+        plan = _NormPlan(cfg)
+        if len(_norm_plans) >= 4096:
+            _norm_plans.clear()
+        _norm_plans[key] = plan
+    return plan
+
+
+def _norm_args(w, q, y, residual, post_weight, gate, pre_weight):
+    f32 = torch.float32
+    yp = _arg(w, "y", y, q.io, q.full)
     d = y.get_device()
-    stream = f32 if cfg.residual_fp32 else torch.bfloat16
-    vec = lambda name, t, on, shape: _arg(w, name, t, f32, shape, d) if on else None
-    return p + [_arg(w, "residual", residual, stream, (T, H), d) if cfg.residual else None,
-                vec("post_weight", post_weight, cfg.post, (H,)),
-                vec("gate", gate, cfg.gate, (T,) if cfg.gate == 2 else (H,)),
-                vec("pre_weight", pre_weight, cfg.pre, (H,))], d, stream
+    return d, (yp, _arg(w, "residual", residual, q.stream, q.full, d) if q.residual else None,
+               _arg(w, "post_weight", post_weight, f32, q.vec, d) if q.post else None,
+               _arg(w, "gate", gate, f32, q.gate, d) if q.gate else None,
+               _arg(w, "pre_weight", pre_weight, f32, q.vec, d) if q.pre else None)
 
 
 def block_norm_fwd(cfg, y, residual=None, post_weight=None, gate=None, pre_weight=None, h=None, n=None):
@@ -1324,32 +1351,39 @@ def block_norm_fwd(cfg, y, residual=None, post_weight=None, gate=None, pre_weigh
     output y (cfg from make_norm_config). residual and h bf16 (fp32 with
     cfg.residual_fp32), weights [H] and gate [H] or [T] fp32. h may be residual."""
     w = "block_norm_fwd"
-    _size("moe_norm_workspace_bytes", cfg)
-    p, d, stream = _norm_args(w, cfg, y, residual, post_weight, gate, pre_weight)
-    T, H, dev = cfg.T, cfg.H, y.device
-    h = torch.empty((T, H), dtype=stream, device=dev) if h is None else h
-    if cfg.pre and n is None:
-        n = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    stats = torch.empty((T, 2), dtype=torch.float32, device=dev)
-    st = lib().moe_block_norm_fwd(ctypes.byref(cfg), *p, _arg(w, "h", h, stream, (T, H), d),
-                                  _arg(w, "n", n, torch.bfloat16, (T, H), d) if cfg.pre else None, stats.data_ptr(),
-                                  _stream(d))
-    _check(st, "moe_block_norm_fwd")
-    return h, n if cfg.pre else None, stats
+    q = _norm_plan(cfg)
+    d, p = _norm_args(w, q, y, residual, post_weight, gate, pre_weight)
+    dev = y.device
+    if h is None:
+        h = torch.empty(q.full, dtype=q.stream, device=dev)
+        hp = h.data_ptr()
+    else:
+        hp = _arg(w, "h", h, q.stream, q.full, d)
+    if not q.pre:
+        n = np_ = None
+    elif n is None:
+        n = torch.empty(q.full, dtype=torch.bfloat16, device=dev)
+        np_ = n.data_ptr()
+    else:
+        np_ = _arg(w, "n", n, torch.bfloat16, q.full, d)
+    stats = torch.empty(q.stats, dtype=torch.float32, device=dev)
+    st = lib().moe_block_norm_fwd(ctypes.byref(cfg), *p, hp, np_, stats.data_ptr(), _stream(d))
+    if st:
+        _check(st, "moe_block_norm_fwd")
+    return h, n, stats
 
 
 def alloc_norm_grads(cfg, device="cuda"):
-    T, H, f32 = cfg.T, cfg.H, torch.float32
-    new = lambda dt, *shape: torch.empty(shape, dtype=dt, device=device)
-    g = {"dy": new(torch.bfloat16, T, H)}
-    if cfg.residual:
-        g["dresidual"] = new(f32 if cfg.residual_fp32 else torch.bfloat16, T, H)
-    if cfg.post:
-        g["dpost"] = new(f32, H)
-    if cfg.gate:
-        g["dgate"] = new(f32, T if cfg.gate == 2 else H)
-    if cfg.pre:
-        g["dpre"] = new(f32, H)
+    q, f32 = _norm_plan(cfg), torch.float32
+    g = {"dy": torch.empty(q.full, dtype=torch.bfloat16, device=device)}
+    if q.residual:
+        g["dresidual"] = torch.empty(q.full, dtype=q.stream, device=device)
+    if q.post:
+        g["dpost"] = torch.empty(q.vec, dtype=f32, device=device)
+    if q.gate:
+        g["dgate"] = torch.empty(q.gate, dtype=f32, device=device)
+    if q.pre:
+        g["dpre"] = torch.empty(q.vec, dtype=f32, device=device)
     return g
 
 
@@ -1359,19 +1393,23 @@ def block_norm_bwd(cfg, dn, y, stats, dh=None, residual=None, post_weight=None, 
     cfg.out_fp32; None without pre) and of h (dh as residual; None: zeros): dict with
     dy [T, H] bf16 and, where cfg has them, dresidual, dpost, dgate, dpre."""
     w = "block_norm_bwd"
-    nb = _size("moe_norm_workspace_bytes", cfg)
-    p, d, stream = _norm_args(w, cfg, y, residual, post_weight, gate, pre_weight)
-    T, H, f32 = cfg.T, cfg.H, torch.float32
-    dhp = _arg(w, "dh", dh, stream, (T, H), d, optional=True)
-    dnp = _arg(w, "dn", dn, _out_dtype(cfg), (T, H), d) if cfg.pre else None
-    sp = _arg(w, "stats", stats, f32, (T, 2), d)
-    ws = _scratch(nb, y.device) if ws is None else ws
-    wp = _ws_arg(w, ws, nb, d)
-    g = alloc_norm_grads(cfg, y.device) if grads is None else grads
-    out = lambda name, on, dt, shape: _arg(w, name, g.get(name), dt, shape, d) if on else None
-    st = lib().moe_block_norm_bwd(ctypes.byref(cfg), dhp, dnp, *p, sp, out("dy", True, torch.bfloat16, (T, H)),
-                                  out("dresidual", cfg.residual, stream, (T, H)), out("dpost", cfg.post, f32, (H,)),
-                                  out("dgate", cfg.gate, f32, (T,) if cfg.gate == 2 else (H,)),
-                                  out("dpre", cfg.pre, f32, (H,)), wp, ws.numel(), _stream(d))
+    q = _norm_plan(cfg)
+    f32 = torch.float32
+    d, p = _norm_args(w, q, y, residual, post_weight, gate, pre_weight)
+    dhp = _arg(w, "dh", dh, q.stream, q.full, d, optional=True)
+    dnp = _arg(w, "dn", dn, q.io, q.full, d) if q.pre else None
+    sp = _arg(w, "stats", stats, f32, q.stats, d)
+    ws = _scratch(q.nbytes, y.device) if ws is None else ws
+    wp = _ws_arg(w, ws, q.nbytes, d)
+    if grads is None:
+        g = alloc_norm_grads(cfg, y.device)
+        out = lambda name, on, dt, shape: g[name].data_ptr() if on else None
+    else:
+        g = grads
+        out = lambda name, on, dt, shape: _arg(w, name, g.get(name), dt, shape, d) if on else None
+    st = lib().moe_block_norm_bwd(ctypes.byref(cfg), dhp, dnp, *p, sp, out("dy", True, torch.bfloat16, q.full),
+                                  out("dresidual", q.residual, q.stream, q.full), out("dpost", q.post, f32, q.vec),
+                                  out("dgate", q.gate, f32, q.gate), out("dpre", q.pre, f32, q.vec), wp, ws.numel(),
+                                  _stream(d))
     _check(st, "moe_block_norm_bwd")
     return g
