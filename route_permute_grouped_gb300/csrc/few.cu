@@ -499,23 +499,27 @@ __device__ bool few_route(const FewParams& p, FewCtl* c, int et) {
 // ---------------------------------------------------------------------------
 // ends of a tile
 // ---------------------------------------------------------------------------
-// The block's share of a cut tile that begins elsewhere, to the workspace
-__device__ __forceinline__ void few_leave(const float* acc, int n, float* part, size_t stride, unsigned* cnt, int et) {
-  float4* dst = reinterpret_cast<float4*>(part + blockIdx.x * stride);
+// The block's share of a tile that is joined elsewhere, to a slot of the workspace
+__device__ __forceinline__ void few_leave(const float* acc, int n, float* slot, unsigned* cnt, int et) {
+  float4* dst = reinterpret_cast<float4*>(slot);
   const float4* src = reinterpret_cast<const float4*>(acc);
   for (int i = et; i < n / 4; i += kFewEpi) __stcg(dst + i, src[i]);
   epi_sync();
   if (et == 0) red_release(cnt, 1u);
 }
-// The rest of a cut tile that begins here: once the other blocks' sums are there, added to
-// `acc` in the blocks' order. False when the wait ran out.
-__device__ __forceinline__ bool few_join(float* acc, int n, const float* part, size_t stride, const FewPieces& pc,
-                                         const unsigned* cnt, FewCtl* c, const FewParams& p, int et) {
+// The rest of a tile, `na` shares from slot `a0` of part_a on and then `nb` from b0 of part_b:
+// once all are there, added to `acc` in this order. False when the wait ran out.
+__device__ __forceinline__ bool few_join(float* acc, int n, size_t stride, const float* part_a, int a0, int na,
+                                         const float* part_b, int b0, int nb, const unsigned* cnt, FewCtl* c,
+                                         const FewParams& p, int et) {
   bool ok = true;
-  if (et == 0) ok = wait_count(cnt, pc.c1 - pc.c0, c, p, 93);
+  if (et == 0) ok = wait_count(cnt, na + nb, c, p, 93);
   if (!epi_all(ok)) return false;
   float4* a = reinterpret_cast<float4*>(acc);
-  auto piece = [&](int b) { return reinterpret_cast<const float4*>(part + b * stride); };
+  const int all = na + nb;
+  auto piece = [&](int i) {
+    return reinterpret_cast<const float4*>(i < na ? part_a + (a0 + i) * stride : part_b + (b0 + i - na) * stride);
+  };
   auto add = [](float4& v, const float4& w) {
     v.x += w.x;
     v.y += w.y;
@@ -527,14 +531,14 @@ __device__ __forceinline__ bool few_join(float* acc, int n, const float* part, s
     // few floats: eight pieces on their way at a time
     if (et < n4) {
       float4 v = a[et];
-      for (int b = pc.c0 + 1; b <= pc.c1; b += 8) {
+      for (int i = 0; i < all; i += 8) {
         float4 w[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (b + k <= pc.c1) w[k] = __ldcg(piece(b + k) + et);
+          if (i + k < all) w[k] = __ldcg(piece(i + k) + et);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (b + k <= pc.c1) add(v, w[k]);
+          if (i + k < all) add(v, w[k]);
       }
       a[et] = v;
     }
@@ -545,8 +549,8 @@ __device__ __forceinline__ bool few_join(float* acc, int n, const float* part, s
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (base + k * kFewEpi < n4) v[k] = a[base + k * kFewEpi];
-      for (int b = pc.c0 + 1; b <= pc.c1; b += 2) {
-        const float4 *s0 = piece(b), *s1 = piece(min(b + 1, pc.c1));
+      for (int i = 0; i < all; i += 2) {
+        const float4 *s0 = piece(i), *s1 = piece(min(i + 1, all - 1));
         float4 w0[4], w1[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -559,7 +563,7 @@ __device__ __forceinline__ bool few_join(float* acc, int n, const float* part, s
         for (int k = 0; k < 4; ++k) {
           if (base + k * kFewEpi < n4) {
             add(v[k], w0[k]);
-            if (b < pc.c1) add(v[k], w1[k]);
+            if (i + 1 < all) add(v[k], w1[k]);
           }
         }
       }
@@ -668,7 +672,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       int n = 0;  // stages so far
       bool ok = true;
       FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), MX);
-      for (int ph = first_phase; ph < 3 && ok; ++ph) {
+      for (int ph = first_phase; ph < 5 && ok; ++ph) {
         if (ph == 1) {
           if (!mbar_wait_bounded(&c->plan, 0, abort_flag, p.lim, p.status, 83)) break;
           g = c->geo;
@@ -729,7 +733,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       else
         umma_bf16_w(d, a_lo, b_lo, d_hi, idesc, go ? 1u : 0u);
     };
-    for (int ph = first_phase; ph < 3 && ok; ++ph) {
+    for (int ph = first_phase; ph < 5 && ok; ++ph) {
       if (ph == 1) {
         if (!warp_wait(&c->plan, 0, c, p, 85)) break;
         g = c->geo;
@@ -742,7 +746,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const int acc_cols = il * il_cols;
       na = 0;
       // W2's accumulators are laid out differently: all of the others have been read
-      for (int b = 0; b < 2 && ok && ph == 2; ++b)
+      for (int b = 0; b < 2 && ok && ph == 3; ++b)
         if (used[b] > 0) ok = warp_wait(c->tempty + b, (used[b] & 1) ^ 1, c, p, 86);
       while (ok && w.next(ch)) {
         const int N = few_cols(parts, FewRows(p, c, ch.i).m);
@@ -788,8 +792,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               const int nn = min(256, N - n0);
               const uint32_t idesc = MX ? idesc_mxf4(nn) : idesc_bf16_f32(128, nn, true, false);
               const uint32_t bn = b0 + ((n0 * kSubBytes) >> 4);
-              // phases 0, 1: W1's and W3's tile against the same tokens, accumulators of their
-              // own; phase 2: two sub-blocks of W2, each against its own. Step kk along k of
+              // phases 0 to 2: W1's and W3's tile against the same tokens, accumulators of their
+              // own; 3, 4: two sub-blocks of W2, each against its own. Step kk along k of
               // either goes to accumulator kk % il
               if (!w.down) {
 #pragma unroll
@@ -828,7 +832,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     int n = 0;
     bool ok = true;
     FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), MX);
-    for (int ph = first_phase; ph < 3 && ok; ++ph) {
+    for (int ph = first_phase; ph < 5 && ok; ++ph) {
       const unsigned* counter = nullptr;
       unsigned want = 0;
       if (ph == 1) {
@@ -839,9 +843,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (ph == 0 && MX) {  // the parts of x come from all blocks
         counter = p.sync;
         want = gridDim.x;
-      } else if (ph == 2) {  // all activations
+      } else if (ph == 3) {  // the activations of phases 0 and 1
         counter = p.sync + 2;
-        want = p.nsh * p.ns1s + c->nact * p.ns1;
+        want = p.nsh * p.ns1s + few_half(c->nact) * p.ns1;
+      } else if (ph == 4) {
+        counter = p.sync + 3;
+        want = (c->nact - few_half(c->nact)) * p.ns1;
       }
       if (counter != nullptr && w.u < w.u1) {
         if (lane == 0) ok = wait_count(counter, want, c, p, 90);
@@ -912,7 +919,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const FewGeo g = c->geo;
     float* acc = reinterpret_cast<float*>(smem + g.acc_off);
     unsigned* cnt = p.cnt;
-    for (int ph = first_phase; ph < 3 && ok; ++ph) {
+    const bool halved = ok && few_half(c->nact) < c->nact;
+    for (int ph = first_phase; ph < 5 && ok; ++ph) {
       FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
       FewChunk ch;
       const int nbuf = w.down ? g.nbuf2 : g.nbuf1;
@@ -968,13 +976,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         if (lane == 0) mbar_arrive(c->tempty + buf);
         epi_sync();
         if (!ch.last) continue;
-        const int ti = w.tile_index(), n = w.down ? p.T * 128 : m * 256;
+        const int ti = w.tile_index(), n = w.down ? p.T * 128 : m * 256, me = blockIdx.x;
         const FewPieces pc = w.pieces(ti);
         const size_t stride = static_cast<size_t>(p.T) * (w.down ? 128 : 256);
-        if (static_cast<int>(blockIdx.x) != pc.c0) {
-          few_leave(acc, n, p.part[ph], stride, cnt + ti, et);
+        const bool early = ph == 3 && halved;  // joined in the next phase
+        if (early || me != pc.c0) {
+          few_leave(acc, n, p.part[ph] + (early ? me + ti : me) * stride, cnt + ti, et);
         } else {
-          if (pc.c1 > pc.c0) ok = few_join(acc, n, p.part[ph], stride, pc, cnt + ti, c, p, et);
+          FewPieces pa{0, -1};
+          if (ph == 4) pa = FewWalk(3, p, g, c->nact, 0, G).pieces(ti);
+          const int na = pa.c1 - pa.c0 + 1, nb = pc.c1 - pc.c0;
+          if (na + nb > 0) ok = few_join(acc, n, stride, p.part[3], pa.c0 + ti, na, p.part[ph], me + 1, nb, cnt + ti, c, p, et);
           if (!ok) break;
           if (!w.down) {
             few_activate<MX>(p, c, acc, rw, ch.i, ch.tile, et);
@@ -983,9 +995,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           }
         }
         epi_sync();
-        if (!w.down && static_cast<int>(blockIdx.x) == pc.c0 && et == 0) red_release(p.sync + 2, 1u);
+        if (!w.down && me == pc.c0 && et == 0) red_release(p.sync + (ph == 2 ? 3 : 2), 1u);
       }
-      cnt += ph == 0 ? p.nsh * p.ns1s : c->nact * p.ns1;
+      // the counters of the next phase's tiles; both phases of W2 share theirs
+      const int half = few_half(c->nact);
+      cnt += ph == 0 ? p.nsh * p.ns1s : ph == 1 ? half * p.ns1 : ph == 2 ? (c->nact - half) * p.ns1 : 0;
     }
   }
   tc_fence_before();
@@ -997,8 +1011,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (threadIdx.x == 0) {
     // the last block to end leaves the counters at 0, as it found them
     __threadfence();
-    if (atomicAdd(p.sync + 3, 1u) == gridDim.x - 1) {
-      for (int i = 0; i < 4; ++i) p.sync[i] = 0u;
+    if (atomicAdd(p.sync + 4, 1u) == gridDim.x - 1) {
+      for (int i = 0; i < 5; ++i) p.sync[i] = 0u;
     }
   }
 }
@@ -1012,7 +1026,7 @@ static size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Where things lie in the workspace
 struct FewLayout {
-  size_t logits, cnt, part[3], a, as, a_sf, as_sf, xq, x_sf, total;
+  size_t logits, cnt, part[5], a, as, a_sf, as_sf, xq, x_sf, total;
   int cnt_words;
 };
 static int few_parts1(const moe_config& c, bool mx) { return mx ? (c.out_fp32 ? 8 : 5) : 1; }
@@ -1031,9 +1045,13 @@ static FewLayout few_layout(const moe_config& c, bool mx, int G) {
   L.cnt_words = c.T * ((c.F_shared + 127) / 128) + kFewMaxEnt * ((c.F + 127) / 128) + (c.H + 127) / 128;
   L.logits = take(4 * T * c.E);
   L.cnt = take(4 * static_cast<size_t>(L.cnt_words));
-  // a block's partial sums of a phase
-  for (int ph = 0; ph < 3; ++ph)
-    L.part[ph] = take(ph == 0 && !Fs ? 0 : static_cast<size_t>(G) * T * (ph < 2 ? 256 : 128) * 4);
+  // a phase's partial sums: a slot a block, in phase 3 another for each of its tiles
+  const bool halves = c.T * c.k >= kFewHalve;
+  for (int ph = 0; ph < 5; ++ph) {
+    const bool used = ph == 0 ? Fs > 0 : (ph & 1) || halves;
+    const size_t slots = static_cast<size_t>(G) + (ph == 3 ? (c.H + 127) / 128 : 0);
+    L.part[ph] = take(used ? slots * T * (ph < 3 ? 256 : 128) * 4 : 0);
+  }
   L.a = take(mx ? R * P2 * F / 2 : R * P2 * F * 2);
   L.as = take(mx ? T * P2 * Fs / 2 : T * P2 * Fs * 2);
   if (mx) {
@@ -1112,7 +1130,7 @@ int run_few(const moe_config& c, const FewArgs& q, bool mx, void* ws, cudaStream
   p.logits = reinterpret_cast<float*>(base + L.logits);
   p.cnt = reinterpret_cast<unsigned*>(base + L.cnt);
   p.cnt_words = L.cnt_words;
-  for (int ph = 0; ph < 3; ++ph) p.part[ph] = reinterpret_cast<float*>(base + L.part[ph]);
+  for (int ph = 0; ph < 5; ++ph) p.part[ph] = reinterpret_cast<float*>(base + L.part[ph]);
   p.a = base + L.a; p.as = base + L.as; p.a_sf = base + L.a_sf; p.as_sf = base + L.as_sf;
   p.xq = base + L.xq; p.x_sf = base + L.x_sf;
   p.lim = wait_limit_ns();

@@ -22,9 +22,14 @@
 //    it exists.
 //
 // Phases: 0 the shared expert's gate and up products (needs no routing: its weights
-// stream while the router works), 1 the routed experts', 2 all down products. A stage of
-// phases 0 and 1 holds one k sub-block (128 bytes: 64 bf16, 256 MXFP4 elements) of 128
-// columns of W1 and of W3, a stage of phase 2 up to two sub-blocks of 128 columns of W2.
+// stream while the router works); 1 and 2 those of the first and second half of the
+// routed entries; 3 the down products of the shared expert and the first half, 4 those of
+// the second. So a half's activations are joined and finished while the other half's
+// weights stream (61 tokens, 128 experts: 700 to 685 us). Few entries (one token: eight)
+// are not halved: phases 2 and 4 are empty then, since a half would end before the other's
+// activations are there. A stage of phases 0 to 2 holds one k sub-block (128 bytes: 64
+// bf16, 256 MXFP4 elements) of 128 columns of W1 and of W3, a stage of phases 3 and 4 up to
+// two sub-blocks of 128 columns of W2.
 //
 // Operands: bf16 weights multiply bf16 parts of the tokens (x itself; the activation
 // a in two parts, three for fp32 results: 2^-17 and 2^-25 of a). MXFP4 weights stay
@@ -104,10 +109,10 @@ struct FewParams {
   float* gate;
   void* y;
   float* logits;             // [T, E]
-  unsigned* sync;            // barrier 1, barrier 2, finished tiles of phases 0 and 1, ended blocks
-  unsigned* cnt;             // partials of a cut tile that are there: phase 0, 1, 2
+  unsigned* sync;            // barrier 1, barrier 2, finished tiles of phases 0 and 1 and of 2, ended blocks
+  unsigned* cnt;             // partials of a cut tile that are there: phases 0, 1, 2, both of W2
   int cnt_words;
-  float* part[3];            // a phase's partial sums, a slot a block
+  float* part[5];            // a phase's partial sums
   uint8_t *a, *as;           // parts of the activations: rows x parts x (F or Fs)
   uint8_t *a_sf, *as_sf;     // MXFP4: their scale bytes
   uint8_t *xq, *x_sf;        // MXFP4: parts of x and their scale bytes
@@ -154,6 +159,10 @@ __host__ __device__ __forceinline__ FewGeo few_geo(int P1, int P2, int T, int mm
   return g;
 }
 
+// routed entries of phases 1 and 3
+constexpr int kFewHalve = 16;
+__host__ __device__ __forceinline__ int few_half(int nact) { return nact < kFewHalve ? nact : (nact + 1) >> 1; }
+
 // Equal contiguous runs of U units over the first G blocks of the grid, each of at least
 // kFewRun units while there are enough: a tile cut into shorter ones costs more to
 // join than the blocks gain.
@@ -174,9 +183,10 @@ struct FewSplit {
     return u < big ? u / (q + 1) : r + (u - big) / q;
   }
 };
-// Blocks c0 .. c1 share a tile. c0 has its beginning and joins it; the others leave their
-// sums in their slot of the workspace (a block has at most one share that begins inside a
-// tile: its first).
+// Blocks c0 .. c1 share a tile of a phase. c0 has its beginning and joins it; the others
+// leave their sums in their slot of the workspace (a block has at most one share that
+// begins inside a tile: its first). W2's tiles are joined in their last phase: the shares
+// of the phase before lie in slots of their own, block + tile.
 struct FewPieces {
   int c0, c1;
 };
@@ -195,23 +205,26 @@ struct FewWalk {
   FewSplit s;
   int phase, u, u0, u1;
   bool down;
+  int i0;                     // first routed entry of the phase
   int kbs, kbr, shared, per;  // stages of the shared expert's and a routed expert's k, of all shared entries, of a tile
   int ns, flush;
   __host__ __device__ __forceinline__ FewWalk(int ph, const FewParams& p, const FewGeo& g, int nact, int c, int G) {
     phase = ph;
-    down = ph == 2;
+    down = ph >= 3;
+    const int half = few_half(nact), n = ph == 0 ? 0 : (ph & 1) ? half : nact - half;
+    i0 = ph == 0 || (ph & 1) ? 0 : half;
     if (!down) {
       ns = ph == 0 ? p.ns1s : p.ns1;
       per = p.nsb1;
-      s.set((ph == 0 ? p.nsh : nact) * ns * per, G);
+      s.set((ph == 0 ? p.nsh : n) * ns * per, G);
       kbs = kbr = shared = per;
       flush = p.chain * g.il1 / p.ks;
     } else {
       ns = p.ns2;
       kbr = (p.nsb2 + g.sub2 - 1) / g.sub2;
       kbs = (p.nsb2s + g.sub2 - 1) / g.sub2;
-      shared = p.nsh * kbs;
-      per = shared + nact * kbr;
+      shared = ph == 3 ? p.nsh * kbs : 0;
+      per = shared + n * kbr;
       s.set(ns * per, G);
       flush = p.chain * g.il2 / (p.ks * g.sub2);
     }
@@ -219,7 +232,7 @@ struct FewWalk {
     u = u0 = s.start(c);
     u1 = s.start(c + 1);
   }
-  // the blocks that share tile t of the phase
+  // the blocks that share tile t of the phase (which has work)
   __host__ __device__ __forceinline__ FewPieces pieces(int t) const {
     return FewPieces{s.owner(t * per), s.owner((t + 1) * per - 1)};
   }
@@ -229,7 +242,7 @@ struct FewWalk {
     int lim;
     if (!down) {
       const int e = t / ns;
-      c.i = phase == 0 ? -1 - e : e;
+      c.i = phase == 0 ? -1 - e : i0 + e;
       c.tile = t - e * ns;
       c.kb = r;
       lim = per - r;
@@ -241,8 +254,9 @@ struct FewWalk {
         c.kb = r - e * kbs;
         lim = kbs - c.kb;
       } else {
-        c.i = (r - shared) / kbr;
-        c.kb = r - shared - c.i * kbr;
+        const int e = (r - shared) / kbr;
+        c.i = i0 + e;
+        c.kb = r - shared - e * kbr;
         lim = kbr - c.kb;
       }
     }
