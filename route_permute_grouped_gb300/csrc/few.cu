@@ -162,15 +162,6 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
 // ---------------------------------------------------------------------------
 // router
 // ---------------------------------------------------------------------------
-// a load whose line stays in L2 while the experts' weights stream through
-__device__ __forceinline__ uint4 ld_keep(const uint4* p, uint64_t policy) {
-  uint4 v;
-  asm volatile("ld.global.nc.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p), "l"(policy));
-  return v;
-}
-
 // logits[t][e], an item of NE experts x 8 tokens a block: its 8 warps share H, 8 products
 // to a 16-byte load, fp32 fused multiply-adds; the 32 lanes' sums meet in a halving
 // butterfly, the warps' in shared memory
@@ -179,7 +170,6 @@ __device__ __noinline__ void few_logits_of(const FewParams& p, FewCtl* c, int et
   const int warp = et >> 5, lane = et & 31;
   const int eg = (p.E + NE - 1) / NE, items = eg * ((p.T + 7) >> 3);
   const int nv = p.H >> 3;
-  const uint64_t keep = l2_policy_evict_last();
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const int e0 = item % eg * NE, t0 = item / eg * 8;
     const int ne = min(NE, p.E - e0), nt = min(8, p.T - t0);
@@ -193,7 +183,7 @@ __device__ __noinline__ void few_logits_of(const FewParams& p, FewCtl* c, int et
       uint4 wv[NE], xv[8];
 #pragma unroll
       for (int i = 0; i < NE; ++i)
-        if (i < ne) wv[i] = ld_keep(w + static_cast<size_t>(i) * nv + v, keep);
+        if (i < ne) wv[i] = __ldg(w + static_cast<size_t>(i) * nv + v);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (j < nt) xv[j] = __ldg(x + static_cast<size_t>(j) * nv + v);
@@ -446,9 +436,9 @@ __device__ void few_plan(const FewParams& p, FewCtl* c, int et) {
   if (et == 0) {
     c->nact = na;
     c->off[na] = R;
-    c->geo = few_geo(p.P1, p.P2, p.T, most, p.mx);
   }
   epi_sync();
+  if (et == kFewEpi - 1) c->geo = few_geo(p.P1, p.P2, p.T, most, p.mx);
   for (int r = et; r < R; r += kFewEpi) {
     const int t = r / p.k, e = c->eidx[r];
     const uint32_t below = (1u << (t & 31)) - 1u;

@@ -50,7 +50,7 @@ constexpr int kFewMaxT = 64;
 constexpr int kFewThreads = 384;   // warp 0 weights, 1 MMA, 2-3 tokens, 4-11 router and epilogue
 constexpr int kFewEpi = 256;
 constexpr int kFewCopiers = 64;
-constexpr int kFewStages = 8;      // at most
+constexpr int kFewStages = 4;      // at most (five: 8 tokens 289 -> 291 us, with a shared expert 553 -> 564)
 constexpr int kFewMaxR = kFewMaxT * 16;
 constexpr int kFewMaxEnt = 320;    // runs of rows of one expert
 constexpr int kFewATile = 16384;   // 128 columns x 128 bytes
@@ -171,7 +171,7 @@ struct FewSplit {
   int U, G, q, r;  // units, blocks; the first r blocks have q + 1 units, the others q
   __host__ __device__ __forceinline__ void set(int units, int blocks) {
     U = units;
-    const int most = (units + kFewRun - 1) / kFewRun;
+    const int most = (U + kFewRun - 1) / kFewRun;
     G = blocks < most ? blocks : most;
     q = G > 0 ? U / G : 0;
     r = U - q * G;
