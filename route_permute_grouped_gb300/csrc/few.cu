@@ -224,45 +224,52 @@ __device__ void few_logits(const FewParams& p, FewCtl* c, int et) {
   else few_logits_of<1>(p, c, et);
 }
 
-// x in E2M1 parts: a thread a block of 32
+// x in E2M1 parts: four lanes a block of 32 along H, a warp 256 elements. Dealt from the last
+// block down: with few tokens those have no logits to compute
 __device__ void few_split_x(const FewParams& p, int et) {
-  const int nb = p.H >> 5;
-  for (int i = blockIdx.x * kFewEpi + et; i < p.T * nb; i += gridDim.x * kFewEpi) {
-    const int t = i / nb, b = i - t * nb;
-    const uint4* src = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * p.H + b * 32);
-    float v[32], amax = 0.0f;
-    bool bad = false;
+  const int nb = p.H >> 5, lane = et & 31, total = p.T * nb;
+  for (int u = gridDim.x - 1 - blockIdx.x + gridDim.x * (et >> 5); 8 * u < total; u += 8 * gridDim.x) {
+    const int i = min(8 * u + (lane >> 2), total - 1);  // the last warp's spare lanes: its last block once more
+    const bool on = 8 * u + (lane >> 2) < total;
+    const int t = i / nb, b = i - t * nb, part = lane & 3;
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * p.H + b * 32) + part);
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    float v[8], amax = 0.0f;
+    int bad = 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4 w = __ldg(src + q);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[8 * q + 2 * j] = bf16_lo(ww[j]);
-        v[8 * q + 2 * j + 1] = bf16_hi(ww[j]);
-      }
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_lo(ww[j]);
+      v[2 * j + 1] = bf16_hi(ww[j]);
     }
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
+    for (int j = 0; j < 8; ++j) {
       amax = fmaxf(amax, fabsf(v[j]));
       bad |= v[j] != v[j];
+    }
+#pragma unroll
+    for (int d = 1; d <= 2; d <<= 1) {
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+      bad |= __shfl_xor_sync(0xffffffffu, bad, d);
     }
     const int e = part_exponent(bad ? INFINITY : amax, p.P1);
     const float inv = part_inverse(e);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = e >= kFewBad ? 0.0f : v[j] * inv;
+    for (int j = 0; j < 8; ++j) v[j] = e >= kFewBad ? 0.0f : v[j] * inv;
+#pragma unroll 1
     for (int q = 0; q < p.P1; ++q) {
       const size_t row = static_cast<size_t>(t) * p.P1 + q;
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      uint32_t codes = 0u;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const uint32_t c = e2m1_pair(v[2 * j], v[2 * j + 1]);
-        w[j >> 2] |= c << (8 * (j & 3));
+        codes |= c << (8 * j);
         v[2 * j] = part_rest(v[2 * j], e2m1_value(c), q);
         v[2 * j + 1] = part_rest(v[2 * j + 1], e2m1_value(c >> 4), q);
       }
-      *reinterpret_cast<uint4*>(p.xq + row * (p.H >> 1) + b * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-      p.x_sf[row * nb + b] = static_cast<uint8_t>(part_byte(e, q));
+      if (on) {
+        *reinterpret_cast<uint32_t*>(p.xq + row * (p.H >> 1) + b * 16 + part * 4) = codes;
+        if (part == 0) p.x_sf[row * nb + b] = static_cast<uint8_t>(part_byte(e, q));
+      }
     }
   }
 }

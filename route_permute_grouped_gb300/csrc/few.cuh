@@ -50,7 +50,7 @@ constexpr int kFewMaxT = 64;
 constexpr int kFewThreads = 384;   // warp 0 weights, 1 MMA, 2-3 tokens, 4-11 router and epilogue
 constexpr int kFewEpi = 256;
 constexpr int kFewCopiers = 64;
-constexpr int kFewStages = 4;      // at most (five: 8 tokens 289 -> 291 us, with a shared expert 553 -> 564)
+constexpr int kFewStages = 4;      // at most (8 tokens: three 301, four 295.7, five 295.6 us; one token 69.1, 68.1, 68.2)
 constexpr int kFewMaxR = kFewMaxT * 16;
 constexpr int kFewMaxEnt = 320;    // runs of rows of one expert
 constexpr int kFewATile = 16384;   // 128 columns x 128 bytes
