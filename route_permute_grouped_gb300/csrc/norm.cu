@@ -38,14 +38,31 @@ struct NormParams {
   const float* cstats;
 };
 
-// 8 elements of a row, from bf16 or fp32
-template <bool F32>
+// A thread's 8 columns of a row (run i of n8): with bf16 streams alone 8i .. 8i + 7, one
+// 16-byte access; where a stream is fp32 (SP) four in each half of the row, quads i and n8 + i,
+// so that a warp's 16-byte accesses of either half are one run of bytes (8i .. 8i + 7 in fp32
+// would be two accesses that touch every sector by half: 5003 x 7168 with an fp32 stream,
+// forward 88 us and backward 179 against 78 and 121).
+template <bool SP>
+__device__ __forceinline__ int quad(int i, int n8, int k) {
+  return SP ? i + k * n8 : 2 * i + k;
+}
+template <bool F32, bool SP>
 struct Vec8 {
+  static_assert(SP || !F32, "fp32 streams are split");
   uint4 a, b;
-  __device__ __forceinline__ void load(const void* base, size_t i8) {
-    const uint4* p = static_cast<const uint4*>(base) + (F32 ? 2 : 1) * i8;
-    a = __ldcs(p);
-    if constexpr (F32) b = __ldcs(p + 1);
+  __device__ __forceinline__ void load(const void* base, size_t row, int i, int n8) {
+    if constexpr (F32) {
+      const uint4* p = static_cast<const uint4*>(base) + 2 * row * n8;
+      a = __ldcs(p + quad<SP>(i, n8, 0));
+      b = __ldcs(p + quad<SP>(i, n8, 1));
+    } else if constexpr (SP) {
+      const uint2* p = static_cast<const uint2*>(base) + 2 * row * n8;
+      const uint2 u = __ldcs(p + quad<SP>(i, n8, 0)), v = __ldcs(p + quad<SP>(i, n8, 1));
+      a = make_uint4(u.x, u.y, v.x, v.y);
+    } else {
+      a = __ldcs(static_cast<const uint4*>(base) + row * n8 + i);
+    }
   }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -65,20 +82,31 @@ struct Vec8 {
     }
   }
 };
-template <bool F32>
-__device__ __forceinline__ void store8(void* base, size_t i8, const float (&v)[8]) {
-  uint4* p = static_cast<uint4*>(base) + (F32 ? 2 : 1) * i8;
+template <bool F32, bool SP>
+__device__ __forceinline__ void store8(void* base, size_t row, int i, int n8, const float (&v)[8]) {
   if constexpr (F32) {
-    p[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-    p[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+    uint4* p = static_cast<uint4*>(base) + 2 * row * n8;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      p[quad<SP>(i, n8, k)] = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]),
+                                         __float_as_uint(v[4 * k + 2]), __float_as_uint(v[4 * k + 3]));
+  } else if constexpr (SP) {
+    uint2* p = static_cast<uint2*>(base) + 2 * row * n8;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      p[quad<SP>(i, n8, k)] = make_uint2(pack_bf16x2(v[4 * k], v[4 * k + 1]), pack_bf16x2(v[4 * k + 2], v[4 * k + 3]));
   } else {
-    p[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    static_cast<uint4*>(base)[row * n8 + i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                         pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   }
 }
-__device__ __forceinline__ void weights8(const float* w, int i8, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(w)[2 * i8], b = reinterpret_cast<const float4*>(w)[2 * i8 + 1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+template <bool SP>
+__device__ __forceinline__ void weights8(const float* w, int i, int n8, float (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float4 a = reinterpret_cast<const float4*>(w)[quad<SP>(i, n8, k)];
+    v[4 * k] = a.x; v[4 * k + 1] = a.y; v[4 * k + 2] = a.z; v[4 * k + 3] = a.w;
+  }
 }
 
 // Sums of N values over the block, in every thread; `s` alternates between two halves, so
@@ -111,18 +139,18 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const __grid_constant__ N
   __shared__ float red[2 * 96];
   chain_wait();
   int turn = 0;
+  constexpr bool SP = RF || OF;
   const int n8 = p.H >> 3;
   const float inv = 1.0f / static_cast<float>(p.H);
   for (int row = blockIdx.x; row < p.T; row += gridDim.x) {
-    const size_t r8 = static_cast<size_t>(row) * n8;
-    Vec8<OF> yv[NC];
-    Vec8<RF> rv[NC];
+    Vec8<OF, SP> yv[NC];
+    Vec8<RF, SP> rv[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int i = threadIdx.x + c * blockDim.x;
       if (i < n8) {
-        yv[c].load(p.y, r8 + i);
-        if (p.res) rv[c].load(p.r, r8 + i);
+        yv[c].load(p.y, row, i, n8);
+        if (p.res) rv[c].load(p.r, row, i, n8);
       }
     }
     float ry = 1.0f, h[NC][8];
@@ -151,13 +179,13 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const __grid_constant__ N
       if (i < n8) {
         if (p.post) {
           float w[8];
-          weights8(p.wp, i, w);
+          weights8<SP>(p.wp, i, n8, w);
 #pragma unroll
           for (int j = 0; j < 8; ++j) h[c][j] = h[c][j] * ry * w[j];
         }
         if (p.gate == MOE_GATE_CHANNEL) {
           float w[8];
-          weights8(p.g, i, w);
+          weights8<SP>(p.g, i, n8, w);
 #pragma unroll
           for (int j = 0; j < 8; ++j) h[c][j] *= w[j];
         } else if (p.gate == MOE_GATE_TOKEN) {
@@ -170,7 +198,7 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const __grid_constant__ N
 #pragma unroll
           for (int j = 0; j < 8; ++j) h[c][j] = fmaf(p.a, r[j], h[c][j]);
         }
-        if (p.h != nullptr) store8<RF>(p.h, r8 + i, h[c]);
+        if (p.h != nullptr) store8<RF, SP>(p.h, row, i, n8, h[c]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[0] = fmaf(h[c][j], h[c][j], s[0]);
       }
@@ -183,10 +211,10 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const __grid_constant__ N
         const int i = threadIdx.x + c * blockDim.x;
         if (i < n8) {
           float w[8];
-          weights8(p.wn, i, w);
+          weights8<SP>(p.wn, i, n8, w);
 #pragma unroll
           for (int j = 0; j < 8; ++j) h[c][j] = h[c][j] * rh * w[j];
-          store8<false>(p.n, r8 + i, h[c]);
+          store8<false, SP>(p.n, row, i, n8, h[c]);
         }
       }
       if (threadIdx.x == 0) p.stats[2 * static_cast<size_t>(row) + 1] = rh;
@@ -207,32 +235,44 @@ __device__ __forceinline__ void two_add(float& hi, float& lo, float v) {
 // A thread's 16-byte copies of its columns of the rows ahead, `S` rows deep in shared
 // memory; it waits for its own copies alone. Rows of four tensors lie behind one another,
 // fp32 ones in two planes of 16 bytes a thread.
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <bool RF, bool OF, int NC, int S>
 struct NormRing {
   static constexpr int kY = OF ? 2 : 1, kR = RF ? 2 : 1;  // planes
+  static constexpr bool SP = RF || OF;
   uint8_t* base;
   int n8;
   __device__ __forceinline__ uint8_t* at(int stage, int plane, int i) const {
     return base + ((static_cast<size_t>(stage) * (2 * kY + 2 * kR) + plane) * n8 + i) * 16;
   }
   template <int P>
-  __device__ __forceinline__ void put(int stage, int plane, int i, const void* src, size_t i8) const {
-    const uint4* q = static_cast<const uint4*>(src) + P * i8;
-#pragma unroll
-    for (int k = 0; k < P; ++k) cp_async16(smem_u32(at(stage, plane + k, i)), q + k, true);
+  __device__ __forceinline__ void put(int stage, int plane, int i, const void* src, size_t row) const {
+    const uint8_t* q = static_cast<const uint8_t*>(src) + row * n8 * (16 * P);
+    const uint32_t dst = smem_u32(at(stage, plane, i));
+    if constexpr (P == 2) {
+      cp_async16(dst, q + 16 * quad<SP>(i, n8, 0), true);
+      cp_async16(dst + 16 * n8, q + 16 * quad<SP>(i, n8, 1), true);
+    } else if constexpr (SP) {
+      cp_async8(dst, q + 8 * quad<SP>(i, n8, 0));
+      cp_async8(dst + 8, q + 8 * quad<SP>(i, n8, 1));
+    } else {
+      cp_async16(dst, q + 16 * i, true);
+    }
   }
   // y, the residual, dn, dh of a row (those that there are)
   __device__ __forceinline__ void load(const NormParams& p, int stage, int row) const {
     if (row < p.T) {
-      const size_t r8 = static_cast<size_t>(row) * n8;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int i = threadIdx.x + c * blockDim.x;
         if (i < n8) {
-          put<kY>(stage, 0, i, p.y, r8 + i);
-          if (p.pre) put<kY>(stage, kY, i, p.dn, r8 + i);
-          if (p.res) put<kR>(stage, 2 * kY, i, p.r, r8 + i);
-          if (p.dh != nullptr) put<kR>(stage, 2 * kY + kR, i, p.dh, r8 + i);
+          put<kY>(stage, 0, i, p.y, row);
+          if (p.pre) put<kY>(stage, kY, i, p.dn, row);
+          if (p.res) put<kR>(stage, 2 * kY, i, p.r, row);
+          if (p.dh != nullptr) put<kR>(stage, 2 * kY + kR, i, p.dh, row);
         }
       }
     }
@@ -240,7 +280,7 @@ struct NormRing {
   }
   template <bool F32>
   __device__ __forceinline__ void get(int stage, int plane, int i, float (&v)[8]) const {
-    Vec8<F32> x;
+    Vec8<F32, SP> x;
     x.a = *reinterpret_cast<const uint4*>(at(stage, plane, i));
     if constexpr (F32) x.b = *reinterpret_cast<const uint4*>(at(stage, plane + 1, i));
     x.get(v);
@@ -257,6 +297,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1) norm_bwd_kernel(con
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2 * 96];
   using Ring = NormRing<RF, OF, NC, S>;
+  constexpr bool SP = RF || OF;
   chain_wait();
   chain_release();
   int turn = 0;
@@ -280,12 +321,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1) norm_bwd_kernel(con
   for (int c = 0; c < NC; ++c) {
     const int i = threadIdx.x + c * blockDim.x;
     if (i < n8) {
-      if (p.pre) weights8(p.wn, i, wn[c]);
+      if (p.pre) weights8<SP>(p.wn, i, n8, wn[c]);
       if constexpr (FULL) {
-        if (p.post) weights8(p.wp, i, gw[c]);
+        if (p.post) weights8<SP>(p.wp, i, n8, gw[c]);
         if (p.gate == MOE_GATE_CHANNEL) {
           float g[8];
-          weights8(p.g, i, g);
+          weights8<SP>(p.g, i, n8, g);
 #pragma unroll
           for (int j = 0; j < 8; ++j) gw[c][j] *= g[j];
         }
@@ -303,23 +344,23 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1) norm_bwd_kernel(con
       for (int k = 0; k < (FULL ? 2 : 1); ++k) {
         float(&v)[8] = k == 0 ? an[c] : ad[FULL ? c : 0];
         if (i < n8 && (k == 0 ? p.pre != 0 : sum_d)) {
-          float4* d = reinterpret_cast<float4*>(hi + static_cast<size_t>(k) * p.H) + 2 * i;
-          float4* e = reinterpret_cast<float4*>(hi + static_cast<size_t>(k) * p.H + beyond) + 2 * i;
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
+            float4* d = reinterpret_cast<float4*>(hi + static_cast<size_t>(k) * p.H) + quad<SP>(i, n8, q);
+            float4* e = reinterpret_cast<float4*>(hi + static_cast<size_t>(k) * p.H + beyond) + quad<SP>(i, n8, q);
             float4 s = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
             float4 lo = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (!first) {
               const float4 w = s;
-              s = d[q];
-              lo = e[q];
+              s = *d;
+              lo = *e;
               two_add(s.x, lo.x, w.x);
               two_add(s.y, lo.y, w.y);
               two_add(s.z, lo.z, w.z);
               two_add(s.w, lo.w, w.w);
             }
-            d[q] = s;
-            if (p.lo) e[q] = lo;
+            *d = s;
+            if (p.lo) *e = lo;
           }
         }
 #pragma unroll
@@ -343,7 +384,6 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1) norm_bwd_kernel(con
   int rows = 0, stage = 0;
   bool first = true;
   for (int row = blockIdx.x; row < p.T; row += gridDim.x) {
-    const size_t r8 = static_cast<size_t>(row) * n8;
     if constexpr (S > 0) {
       // (a thread reads and writes its own places only)
       ring.load(p, stage == 0 ? S - 1 : stage - 1, row + (S - 1) * gridDim.x);
@@ -356,8 +396,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1) norm_bwd_kernel(con
       if constexpr (S > 0) {
         ring.template get<F32>(stage, plane, i, v);
       } else {
-        Vec8<F32> x;
-        x.load(src, r8 + i);
+        Vec8<F32, SP> x;
+        x.load(src, row, i, n8);
         x.get(v);
       }
     };
@@ -432,7 +472,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1) norm_bwd_kernel(con
           float t[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) t[j] = p.a * d[j];
-          store8<RF>(p.dr, r8 + i, t);
+          store8<RF, SP>(p.dr, row, i, n8, t);
         }
         if constexpr (FULL) {
           float t[8];
@@ -445,7 +485,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1) norm_bwd_kernel(con
             d[j] = ry * (d[j] * gw[c][j]) - t[j] * yf;
           }
         }
-        store8<false>(p.dy, r8 + i, d);
+        store8<false, SP>(p.dy, row, i, n8, d);
       }
     }
     if (p.part != nullptr && ++rows == kNormFlush) {
