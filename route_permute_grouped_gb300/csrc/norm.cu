@@ -109,6 +109,25 @@ __device__ __forceinline__ void weights8(const float* w, int i, int n8, float (&
   }
 }
 
+// Sum of one value over the warp, of three: a lane of the k-th run of eight leaves with the k-th's
+// (six exchanges for fifteen: the exchanges' pipe takes one a cycle and SM)
+__device__ __forceinline__ float warp_sum(const float (&v)[1], int) {
+  float s = v[0];
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  return s;
+}
+__device__ __forceinline__ float warp_sum(const float (&v)[3], int lane) {
+  const bool up = lane & 16, odd = lane & 8;
+  float a = up ? v[2] : v[0], b = up ? 0.0f : v[1];
+  a += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+  b += __shfl_xor_sync(0xffffffffu, up ? v[1] : 0.0f, 16);
+  float s = odd ? b : a;
+  s += __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+#pragma unroll
+  for (int d = 4; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  return s;
+}
 // Sums of N values over the block, in every thread; `s` alternates between two halves, so
 // that one barrier a sum is enough
 template <int N>
@@ -116,21 +135,14 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float* s, int& turn) {
   const int warp = warp_id(), lane = lane_id(), nw = blockDim.x >> 5;
   float* b = s + (turn & 1) * 96;
   ++turn;
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) b[i * 32 + warp] = v[i];
-  }
+  const float mine = warp_sum(v, lane);
+  if ((lane & 7) == 0 && (lane >> 3) < N) b[(lane >> 3) * 32 + warp] = mine;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = lane < nw ? b[i * 32 + lane] : 0.0f;
+  const float all = warp_sum(v, lane);
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+  for (int i = 0; i < N; ++i) v[i] = N == 1 ? all : __shfl_sync(0xffffffffu, all, 8 * i);
 }
 
 // RF: residual stream fp32, OF: y (and dn) fp32; NC runs of 8 columns a thread
