@@ -718,7 +718,8 @@ int moe_clip_grad_norm(const void* list, int kind, float max_norm, float* norm, 
  * ------------------------------------------------------------------------- */
 
 /* Row-major quantisation of x [M,K] bf16 (K a multiple of 32, blocks along K): q
- * [M,K/2] codes, scales [M,K/32]; and the way back, which is exact. */
+ * [M,K/2] codes, scales [M,K/32]; and the way back, which is exact. Here and below
+ * bf16, codes and scales may not overlap (MOE_ERR_INVALID_ARG). */
 int moe_mx4_quantize(const moe_bf16* x, long long M, int K, uint8_t* q, uint8_t* scales, void* stream);
 int moe_mx4_dequantize(const uint8_t* q, const uint8_t* scales, long long M, int K, moe_bf16* x, void* stream);
 
@@ -796,7 +797,7 @@ int moe_layer_few_fwd_mxfp4(const moe_config* cfg, const moe_bf16* x, const moe_
  *   dy bf16, dresidual as residual, dpost_weight, dpre_weight [H], dgate as gate, fp32.
  * dh (may be NULL: zeros) as residual; dn bf16, fp32 with out_fp32, as the layer's
  * dx. Sums over rows are fp32 for at most 64 rows and two floats beyond, in a fixed
- * order. Shapes: H a multiple of 8, H <= 16384, T >= 1.
+ * order. Shapes: H a multiple of 8, H <= 16384, 1 <= T <= 2^30.
  * ------------------------------------------------------------------------- */
 typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 } moe_gate_kind;
 typedef struct {

@@ -234,6 +234,16 @@ static int mx4_weights(const moe_config* cfg, const void* const (&bf)[6], const 
   for (int i = 0; i < n; ++i)
     if (!bf[i] || !mx4_aligned({bf[i]}, 16)) return MOE_ERR_INVALID_ARG;
   if (!mx4_aligned({w->w13, w->w2, w->w13s, w->w2s}, 16)) return MOE_ERR_INVALID_ARG;
+  const uint8_t* q[4] = {w->w13, w->w2, w->w13s, w->w2s};
+  const int nq = c.F_shared ? 4 : 2;
+  for (int i = 0; i < nq; ++i) {
+    const size_t bytes = moe_mx4_weight_bytes(cfg, i);
+    for (int j = 0; j < n; ++j)
+      if (overlap(q[i], bytes, bf[j], 2ull * (j >= 3 ? c.F_shared : static_cast<size_t>(c.E) * c.F) * c.H))
+        return MOE_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(q[i], bytes, q[j], moe_mx4_weight_bytes(cfg, j))) return MOE_ERR_INVALID_ARG;
+  }
   Mx4Weights a{};
   a.n = n;
   for (int i = 0; i < n; ++i) {
@@ -293,6 +303,8 @@ static int mx4_rows_check(const void* x, long long M, int K, const uint8_t* q, c
   if (!x || !q || !s || M < 1 || K < 1) return MOE_ERR_INVALID_ARG;
   if (!mx4_aligned({x, q, s}, 16)) return MOE_ERR_INVALID_ARG;
   if (K % 32 || M > (1ll << 60) / K) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const size_t n = static_cast<size_t>(M) * K;
+  if (overlap(x, 2 * n, q, n / 2) || overlap(x, 2 * n, s, n / 32) || overlap(q, n / 2, s, n / 32)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 

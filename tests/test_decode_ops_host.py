@@ -181,3 +181,18 @@ def test_norm_refuses_overlapping_outputs(lib):
     p = _apart(14)
     p[8] = P(p[1].value + nbytes)  # behind it
     assert lib.moe_block_norm_bwd(ctypes.byref(cfg), *p, 16, None) == SMALL
+
+
+def test_mx4_refuses_overlaps(lib):
+    x, q, s = 1 << 24, 2 << 24, 3 << 24
+    call = lambda x, q, s: {lib.moe_mx4_quantize(P(x), 4, 64, P(q), P(s), None), lib.moe_mx4_dequantize(P(q), P(s), 4, 64, P(x), None)}
+    for a in ((x, x + 496, s), (x, x - 112, s), (x, q, x + 16), (x, q, q + 112), (x, x, s)):
+        assert call(*a) == {BAD}, a
+    cfg = ops.make_config(1, 128, 2, 1, 128, F_shared=128)
+    for i in range(4):
+        for over in list(range(1, 7)) + [10 + j for j in range(4) if j != i]:
+            w = [(10 + j) << 24 for j in range(4)]
+            w[i] = (over << 24) + 16
+            p = _apart(6)
+            assert lib.moe_mx4_quantize_weights(ctypes.byref(cfg), *p, _weights(*w), None) == BAD, (i, over)
+            assert lib.moe_mx4_dequantize_weights(ctypes.byref(cfg), _weights(*w), *p, None) == BAD, (i, over)
