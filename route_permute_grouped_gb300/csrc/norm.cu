@@ -562,7 +562,8 @@ static int check_norm(const moe_norm_config* c) {
   for (int v : {c->residual, c->post, c->pre, c->residual_fp32, c->out_fp32})
     if (v != 0 && v != 1) return MOE_ERR_INVALID_ARG;
   if (c->residual_scale != c->residual_scale) return MOE_ERR_INVALID_ARG;
-  if (c->H % 8 || c->H > kNormMaxH) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // (a row index and a stride of blocks beyond it stay within 32 bits)
+  if (c->H % 8 || c->H > kNormMaxH || c->T > (1 << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
 }
 // runs of 8 columns a thread in the backward

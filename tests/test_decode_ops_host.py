@@ -196,3 +196,13 @@ def test_mx4_refuses_overlaps(lib):
             p = _apart(6)
             assert lib.moe_mx4_quantize_weights(ctypes.byref(cfg), *p, _weights(*w), None) == BAD, (i, over)
             assert lib.moe_mx4_dequantize_weights(ctypes.byref(cfg), _weights(*w), *p, None) == BAD, (i, over)
+
+
+def test_norm_rows_beyond_32_bit_indices_are_refused(lib):
+    # a thread's next row, row + blocks, would pass 2^31
+    for T in ((1 << 30) + 1, (1 << 31) - 1):
+        cfg = ops.make_norm_config(T, 8)
+        assert lib.moe_norm_workspace_bytes(ctypes.byref(cfg)) == 0
+        far = [P((i + 1) << 44) for i in range(14)]
+        assert lib.moe_block_norm_fwd(ctypes.byref(cfg), *far[:8], None) == SHAPE
+        assert lib.moe_block_norm_bwd(ctypes.byref(cfg), *far, 1 << 40, None) == SHAPE
