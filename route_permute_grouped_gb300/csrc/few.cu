@@ -844,10 +844,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         want = gridDim.x;
       } else if (ph == 3) {  // the activations of phases 0 and 1
         counter = p.sync + 2;
-        want = p.nsh * p.ns1s + few_half(c->nact) * p.ns1;
+        want = p.nsh * p.ns1s + few_half(c->nact, MX) * p.ns1;
       } else if (ph == 4) {
         counter = p.sync + 3;
-        want = (c->nact - few_half(c->nact)) * p.ns1;
+        want = (c->nact - few_half(c->nact, MX)) * p.ns1;
       }
       if (counter != nullptr && w.u < w.u1) {
         if (lane == 0) ok = wait_count(counter, want, c, p, 90);
@@ -918,7 +918,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const FewGeo g = c->geo;
     float* acc = reinterpret_cast<float*>(smem + g.acc_off);
     unsigned* cnt = p.cnt;
-    const bool halved = ok && few_half(c->nact) < c->nact;
+    const bool halved = ok && few_half(c->nact, MX) < c->nact;
     for (int ph = first_phase; ph < 5 && ok; ++ph) {
       FewWalk w(ph, p, g, ph == 0 ? 0 : c->nact, blockIdx.x, G);
       FewChunk ch;
@@ -997,7 +997,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         if (!w.down && me == pc.c0 && et == 0) red_release(p.sync + (ph == 2 ? 3 : 2), 1u);
       }
       // the counters of the next phase's tiles; both phases of W2 share theirs
-      const int half = few_half(c->nact);
+      const int half = few_half(c->nact, MX);
       cnt += ph == 0 ? p.nsh * p.ns1s : ph == 1 ? half * p.ns1 : ph == 2 ? (c->nact - half) * p.ns1 : 0;
     }
   }

@@ -25,9 +25,8 @@
 // stream while the router works); 1 and 2 those of the first and second half of the
 // routed entries; 3 the down products of the shared expert and the first half, 4 those of
 // the second. So a half's activations are joined and finished while the other half's
-// weights stream (61 tokens, 128 experts: 700 to 685 us). Few entries (one token: eight)
-// are not halved: phases 2 and 4 are empty then, since a half would end before the other's
-// activations are there. A stage of phases 0 to 2 holds one k sub-block (128 bytes: 64
+// weights stream. Few entries (one token: eight) are not halved (few_half): phases 2 and 4 are
+// empty then, since a half would end before the other's activations are there. A stage of phases 0 to 2 holds one k sub-block (128 bytes: 64
 // bf16, 256 MXFP4 elements) of 128 columns of W1 and of W3, a stage of phases 3 and 4 up to
 // two sub-blocks of 128 columns of W2.
 //
@@ -56,7 +55,9 @@ constexpr int kFewMaxEnt = 320;    // runs of rows of one expert
 constexpr int kFewATile = 16384;   // 128 columns x 128 bytes
 constexpr int kFewSf = 512;        // scales of 128 columns (rows) x 128 MXFP4 elements
 constexpr int kFewSmem = 232448;   // 227 KB
-constexpr int kFewRedundant = 16;  // tokens up to which every block selects for itself
+// tokens up to which every block selects for itself, without a second wait of all blocks for one
+// another (128 experts, one token 68.2 us for 70.4, 8 295.6 for 296.1; 12 tokens 388.3 for 387.9, 24 556 for 553)
+constexpr int kFewRedundant = 8;
 
 // What a stage holds and how many there are, from the largest number of rows
 struct FewGeo {
@@ -159,20 +160,22 @@ __host__ __device__ __forceinline__ FewGeo few_geo(int P1, int P2, int T, int mm
   return g;
 }
 
-// routed entries of phases 1 and 3
-constexpr int kFewHalve = 16;
-__host__ __device__ __forceinline__ int few_half(int nact) { return nact < kFewHalve ? nact : (nact + 1) >> 1; }
+// Routed entries of phases 1 and 3: half of them where there are enough that a half outlasts the
+// join of the other (128 experts of 4096 x 1536, bf16: 8 tokens 295 us for 301, 33 613 for 621, 61 699 for
+// 702; one token 68 either way, with MXFP4 weights 48 for 42), under MXFP4 while the halves' further
+// partial sums weigh less than that (4 tokens, some 28 entries, 71 us for 73; 8, some 51, 113 for 111, 24 196 for 191)
+constexpr int kFewHalve = 16, kFewHalveMx = 48;
+__host__ __device__ __forceinline__ int few_half(int nact, bool mx) {
+  return nact < kFewHalve || (mx && nact >= kFewHalveMx) ? nact : (nact + 1) >> 1;
+}
 
-// Equal contiguous runs of U units over the first G blocks of the grid, each of at least
-// kFewRun units while there are enough: a tile cut into shorter ones costs more to
-// join than the blocks gain.
-constexpr int kFewRun = 4;
+// Equal contiguous runs of U units over the first G blocks of the grid (runs of at least four
+// units instead: one MXFP4 token of 512 x 256 30.3 us for 23.6, one of 4096 x 1536 41.7 for 41.3)
 struct FewSplit {
   int U, G, q, r;  // units, blocks; the first r blocks have q + 1 units, the others q
   __host__ __device__ __forceinline__ void set(int units, int blocks) {
     U = units;
-    const int most = (U + kFewRun - 1) / kFewRun;
-    G = blocks < most ? blocks : most;
+    G = blocks < U ? blocks : U;
     q = G > 0 ? U / G : 0;
     r = U - q * G;
   }
@@ -211,7 +214,7 @@ struct FewWalk {
   __host__ __device__ __forceinline__ FewWalk(int ph, const FewParams& p, const FewGeo& g, int nact, int c, int G) {
     phase = ph;
     down = ph >= 3;
-    const int half = few_half(nact), n = ph == 0 ? 0 : (ph & 1) ? half : nact - half;
+    const int half = few_half(nact, p.mx), n = ph == 0 ? 0 : (ph & 1) ? half : nact - half;
     i0 = ph == 0 || (ph & 1) ? 0 : half;
     if (!down) {
       ns = ph == 0 ? p.ns1s : p.ns1;

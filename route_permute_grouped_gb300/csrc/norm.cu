@@ -603,8 +603,10 @@ static cudaError_t launch_bwd(const moe_norm_config& c, const NormParams& p, int
   }
   return launch_chained(kernel, dim3(grid), norm_threads(c.H, NC), bytes, s, p);
 }
-// rows on their way: two where an SM's blocks have the shared memory for it, one beside
-// the row at work else, none for the longest rows
+// One row on its way beside the row at work (two, where they fit: 16384 x 4096 138 us for 137), none where two
+// rows pass the shared memory. Up to 7168 columns 896 threads of 72 registers (1024 of 64: 5003 x 7168
+// with an fp32 stream 147 us for 117, 4096 x 7168 106 for 85); up to 4096 blocks of at most 512 threads,
+// several an SM.
 template <bool RF, bool OF, bool FULL>
 static cudaError_t launch_bwd(const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
   const size_t row = static_cast<size_t>(c.H) * (2 * (OF ? 4 : 2) + 2 * (RF ? 4 : 2));
@@ -613,8 +615,7 @@ static cudaError_t launch_bwd(const moe_norm_config& c, const NormParams& p, int
     return 2 * row <= kNormSmem ? launch_bwd<RF, OF, FULL, 1, 2, 1024>(c, p, grid, s)
                                 : launch_bwd<RF, OF, FULL, 1, 0, 1024>(c, p, grid, s);
   if (c.H > 4096) return launch_bwd<RF, OF, FULL, 1, 2, 896>(c, p, grid, s);  // (at most 224 KB)
-  return 3 * row * norm_per_sm(c.H) <= kNormSmem ? launch_bwd<RF, OF, FULL, 1, 3, 512>(c, p, grid, s)
-                                                 : launch_bwd<RF, OF, FULL, 1, 2, 512>(c, p, grid, s);
+  return launch_bwd<RF, OF, FULL, 1, 2, 512>(c, p, grid, s);
 }
 template <bool RF, bool OF>
 static cudaError_t launch_norm(bool bwd, const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
