@@ -216,7 +216,8 @@ __device__ __noinline__ void few_logits_of(const FewParams& p, FewCtl* c, int et
   }
 }
 // the more experts an item has the fewer times x is read and unpacked, as long as
-// there are items for the blocks
+// there are items for the blocks (128 experts: 24 tokens two 552 us, one 562, four 559; 64 tokens four
+// 716, one 724; 8 tokens one 295.4, four 297.1)
 __device__ void few_logits(const FewParams& p, FewCtl* c, int et) {
   const int pairs = p.E * ((p.T + 7) >> 3), G = gridDim.x;
   if (pairs >= 4 * G) few_logits_of<4>(p, c, et);
@@ -690,7 +691,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
             uint8_t* sA = smem + s * g.stage;
             uint64_t* bar = c->full + s;
-            const int sb0 = !w.down ? kb : kb * g.sub2, ns = !w.down ? 2 : min(g.sub2, nsb - sb0);
+            const int sb0 = !w.down ? kb : kb * kFewSub2, ns = !w.down ? 2 : min(kFewSub2, nsb - sb0);
             if constexpr (MX) {
               // a stage's tiles are one run of bytes
               const uint8_t* src = !w.down ? (sh ? p.w13s : p.w13) : (sh ? p.w2s : p.w2);
@@ -772,7 +773,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             const uint32_t sA = smem_u32(smem) + s * g.stage;
             const uint32_t a0 = sdesc_lo(sA, MX ? 16u : 8192u), b0 = sdesc_lo(sA + 2 * few_tile(MX), 16u);
             int ns = 2;
-            if (w.down) ns = min(g.sub2, (ch.i < 0 ? p.nsb2s : p.nsb2) - kb * g.sub2);
+            if (w.down) ns = min(kFewSub2, (ch.i < 0 ? p.nsb2s : p.nsb2) - kb * kFewSub2);
             const int nblk = w.down ? g.nblk2 : g.nblk1;
             const uint32_t region = tmem + kFewSfCol + (n & 1) * kFewSfRegion;
             if constexpr (MX) {
@@ -882,7 +883,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           }
           uint32_t sB = smem_u32(smem) + s * g.stage + 2 * few_tile(MX);
           uint32_t sS = sB + g.b_bytes;
-          const int sb0 = w.down ? kb * g.sub2 : kb, ns = w.down ? min(g.sub2, nsb - sb0) : 1;
+          const int sb0 = w.down ? kb * kFewSub2 : kb, ns = w.down ? min(kFewSub2, nsb - sb0) : 1;
           for (int q = 0; q < ns; ++q) {
             // thread: 16-byte chunk ct % 8 of rows ct / 8, + 8, ..; zeros beyond a row's end
             const int at = (sb0 + q) * kSubBytes + (ct & 7) * 16;

@@ -26,9 +26,15 @@
 // routed entries; 3 the down products of the shared expert and the first half, 4 those of
 // the second. So a half's activations are joined and finished while the other half's
 // weights stream. Few entries (one token: eight) are not halved (few_half): phases 2 and 4 are
-// empty then, since a half would end before the other's activations are there. A stage of phases 0 to 2 holds one k sub-block (128 bytes: 64
-// bf16, 256 MXFP4 elements) of 128 columns of W1 and of W3, a stage of phases 3 and 4 up to
-// two sub-blocks of 128 columns of W2.
+// empty then, since a half would end before the other's activations are there. A stage of
+// phases 0 to 2 holds one k sub-block (128 bytes: 64 bf16, 256 MXFP4 elements) of 128
+// columns of W1 and of W3, a stage of phases 3 and 4 up to two sub-blocks of 128 columns of W2.
+//
+// Measured, 128 experts of 4096 x 1536, eight a token: one token 68 us (302 MB: 4.4 TB/s; the
+// router and the plan take 10, the ends of the two phases 6 and 3, during which little is
+// read), 8 tokens 295, 61 tokens 699 (4.74 GB: 6.8 TB/s, as fast as memory is read);
+// with MXFP4 weights one token 41 (80 MB: 2.0 TB/s), 33 tokens 208 (1.1 GB: 5.4 TB/s, a unit's
+// sixteen small MMAs and their scales take 0.4 of its 0.7 us).
 //
 // Operands: bf16 weights multiply bf16 parts of the tokens (x itself; the activation
 // a in two parts, three for fp32 results: 2^-17 and 2^-25 of a). MXFP4 weights stay
@@ -52,6 +58,8 @@ constexpr int kFewCopiers = 64;
 constexpr int kFewStages = 4;      // at most (8 tokens: three 301, four 295.7, five 295.6 us; one token 69.1, 68.1, 68.2)
 constexpr int kFewMaxR = kFewMaxT * 16;
 constexpr int kFewMaxEnt = 320;    // runs of rows of one expert
+constexpr int kFewSub2 = 2;        // k sub-blocks of a stage of W2, as many tiles as one of W1 and W3 (one: 8 tokens 319 us
+                                   // for 295, 33 with MXFP4 weights 227 for 209)
 constexpr int kFewATile = 16384;   // 128 columns x 128 bytes
 constexpr int kFewSf = 512;        // scales of 128 columns (rows) x 128 MXFP4 elements
 constexpr int kFewSmem = 232448;   // 227 KB
@@ -62,7 +70,6 @@ constexpr int kFewRedundant = 8;
 // What a stage holds and how many there are, from the largest number of rows
 struct FewGeo {
   int n1, n2;                // columns of an expert's N operand, at most
-  int sub2;                  // sub-blocks of a stage of W2
   int b_bytes, nblk1, nblk2, stage, nst;
   int acc_off;               // fp32 sums in shared memory
   int il1, il2;              // accumulators that the steps along k take in turn
@@ -140,16 +147,14 @@ __host__ __device__ __forceinline__ FewGeo few_geo(int P1, int P2, int T, int mm
   FewGeo g;
   g.n1 = few_cols(P1, mmax);
   g.n2 = few_cols(P2, mmax);
-  // two sub-blocks of W2 a stage unless the tokens' side outgrows the weights'
-  g.sub2 = 2 * g.n2 * 128 <= kFewATile ? 2 : 1;
-  g.b_bytes = 128 * (g.n1 > g.sub2 * g.n2 ? g.n1 : g.sub2 * g.n2);
   g.nblk1 = (g.n1 + 127) >> 7;
   g.nblk2 = (g.n2 + 127) >> 7;
-  const int nblk = g.nblk1 > g.sub2 * g.nblk2 ? g.nblk1 : g.sub2 * g.nblk2;
-  g.stage = 2 * few_tile(mx) + g.b_bytes + (mx ? 2 * kFewSf * nblk : 0);
   const int acc = mmax * 1024 > T * 512 ? mmax * 1024 : T * 512;
   g.acc_off = kFewCtlOff - (acc + 1023) / 1024 * 1024;
-  g.nst = g.acc_off / g.stage;
+  g.b_bytes = 128 * (g.n1 > kFewSub2 * g.n2 ? g.n1 : kFewSub2 * g.n2);
+  const int nblk = g.nblk1 > kFewSub2 * g.nblk2 ? g.nblk1 : kFewSub2 * g.nblk2;
+  g.stage = 2 * few_tile(mx) + g.b_bytes + (mx ? 2 * kFewSf * nblk : 0);
+  g.nst = g.acc_off / g.stage;  // (one at least: 64 rows of an expert, three parts)
   if (g.nst > kFewStages) g.nst = kFewStages;
   const int cols = few_acc_cols(mx);
   // the steps along k take several accumulators in turn: each adds a part of the products
@@ -224,12 +229,12 @@ struct FewWalk {
       flush = p.chain * g.il1 / p.ks;
     } else {
       ns = p.ns2;
-      kbr = (p.nsb2 + g.sub2 - 1) / g.sub2;
-      kbs = (p.nsb2s + g.sub2 - 1) / g.sub2;
+      kbr = (p.nsb2 + kFewSub2 - 1) / kFewSub2;
+      kbs = (p.nsb2s + kFewSub2 - 1) / kFewSub2;
       shared = ph == 3 ? p.nsh * kbs : 0;
       per = shared + n * kbr;
       s.set(ns * per, G);
-      flush = p.chain * g.il2 / (p.ks * g.sub2);
+      flush = p.chain * g.il2 / (p.ks * kFewSub2);
     }
     if (flush < 1) flush = 1;
     u = u0 = s.start(c);

@@ -14,6 +14,10 @@
 //   D = sum g_t dH y ry  (g_t: a token's gate),  dpost = g D,  dgate = wp D:
 // a thread adds its columns' in fp32 over at most 64 rows, then in two floats in the
 // workspace; a second kernel joins the blocks' in order.
+// Measured: 16384 x 4096 in bf16 (residual and norm) forward 86 us, 6.25 TB/s, backward 137, 5.9 TB/s,
+// 8 of it the join; 5003 x 7168 with both norms, a channel gate and an fp32 stream 77 us, 5.6 TB/s, and
+// 117, 5.5 TB/s: what is lost there are the rows' one (forward two) sums over a block that has an SM
+// nearly to itself.
 #include <atomic>
 #include <type_traits>
 
@@ -22,7 +26,7 @@
 
 namespace moe {
 
-constexpr int kNormFlush = 64;   // rows added in fp32 alone
+constexpr int kNormFlush = 64;   // rows added in fp32 alone (16: backward of 16384 x 4096 150 us for 137)
 constexpr int kNormMaxH = 16384;
 
 struct NormParams {
@@ -621,6 +625,8 @@ template <bool RF, bool OF>
 static cudaError_t launch_norm(bool bwd, const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
   const int n8 = c.H / 8;
   if (!bwd) {
+    // runs of 8 columns a thread, in blocks of at most 512 threads (16384 x 4096: one run 93 us, two 86, four
+    // 90; 5003 x 7168 two 77, four 84)
     if (n8 <= 128) return launch_fwd<RF, OF, 1>(c, p, grid, s);
     return n8 <= 1024 ? launch_fwd<RF, OF, 2>(c, p, grid, s) : launch_fwd<RF, OF, 4>(c, p, grid, s);
   }
