@@ -157,7 +157,10 @@ __host__ __device__ __forceinline__ FewGeo few_geo(int P1, int P2, int T, int mm
   g.nst = g.acc_off / g.stage;  // (one at least: 64 rows of an expert, three parts)
   if (g.nst > kFewStages) g.nst = kFewStages;
   const int cols = few_acc_cols(mx);
-  // the steps along k take several accumulators in turn: each adds a part of the products
+  // the steps along k take several accumulators in turn: each adds a part of the products, so that
+  // fp32 results' chains end once a stage or two (one accumulator: 16 tokens of 8 experts of
+  // 4096 x 14336 571 us for 437; bf16 results within 1% either way); two sets of them, where they fit, while
+  // the epilogue reads one (one set: 8 tokens 297.7 us for 294.1, 33 with MXFP4 weights 212 for 208)
   g.il1 = 8 * g.n1 * 2 <= cols ? 4 : 4 * g.n1 * 2 <= cols ? 2 : 1;
   g.il2 = 4 * g.n2 * 2 <= cols ? 4 : 2 * g.n2 * 2 <= cols ? 2 : 1;
   g.nbuf1 = 4 * g.n1 * g.il1 <= cols ? 2 : 1;
