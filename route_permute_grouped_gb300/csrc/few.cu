@@ -284,6 +284,11 @@ __device__ void few_select(const FewParams& p, float* zs, int t, int lane, int& 
   float l[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) l[i] = lane + 32 * i < p.E ? __ldcg(L + lane + 32 * i) : -INFINITY;
+  if (p.mode == RSEL_LOGIT && !p.force) {  // where logits are what is selected by, a NaN's gate is 0 too
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (l[i] != l[i]) l[i] = -INFINITY;
+  }
   int e_sel = 0;
   if (p.force) {
     e_sel = static_cast<int>((static_cast<long long>(t) * p.k + lane) % p.E);
@@ -304,8 +309,9 @@ __device__ void few_select(const FewParams& p, float* zs, int t, int lane, int& 
       }
 #pragma unroll
       for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+      // (a row with a NaN or no finite maximum: probabilities 0 but for the NaN, the bias selects)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = z[i] / s;
+      for (int i = 0; i < 8; ++i) z[i] = s > 0.0f ? z[i] / s : z[i] * 0.0f;
     } else if (p.mode == RSEL_SIGMOID) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[i] = 1.0f / (1.0f + expf(-z[i]));

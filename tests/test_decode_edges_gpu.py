@@ -163,3 +163,23 @@ def test_norms_of_fp32_streams_at_odd_widths(H):
         if name == "dy":
             bound += (2.0 ** -8 * f(grads[name]).abs() * v.abs()).sum()
         assert abs((f(grads[name]) * v).sum() - want) <= bound, name
+
+
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(torch.float32).min, float("nan"), float("inf")])
+@pytest.mark.parametrize("left", [0, 1, 2, 5])
+@pytest.mark.parametrize("opts", [dict(), dict(score="sigmoid"), dict(score="sigmoid", n_groups=4, topk_groups=2), dict(bias=True),
+                                  dict(force_balanced=True)])
+def test_masked_experts_are_routed_as_in_the_layer(low, left, opts):
+    # a logit bias that leaves `left` experts of 16 (none, fewer than k, k, more): the same experts and gates as
+    # layer_fwd takes, whatever they are. Logits of either are off by at most 256 2^-24 sum |x w|, which is below 30
+    # here: 4.6e-4, twice that in a gate's quotient of exponentials, for both 1.8e-3 < 2^-9
+    L = Layer(5, 256, 16, 2, 128, **opts)
+    L.lb = torch.full((16,), low, device="cuda")
+    keep = torch.tensor([3, 4, 9, 12, 15][:left], dtype=torch.long, device="cuda")
+    L.lb[keep] = 0.0
+    y, idx, gate = L.run()
+    saved = ops.alloc_saved(L.cfg)
+    want = ops.layer_fwd(L.cfg, L.x, L.router_w, *L.W, expert_bias=L.eb, logit_bias=L.lb, saved=saved)
+    assert torch.equal(idx, saved["topk_idx"].view_as(idx))
+    assert torch.allclose(gate, saved["topk_gate"].view_as(gate), rtol=2.0 ** -9, atol=0, equal_nan=True)
+    assert torch.equal(y.isnan(), want.isnan())
