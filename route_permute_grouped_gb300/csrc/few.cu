@@ -1035,12 +1035,10 @@ struct FewLayout {
   size_t logits, cnt, part[5], a, as, a_sf, as_sf, xq, x_sf, total;
   int cnt_words;
 };
-static int few_parts1(const moe_config& c, bool mx) { return mx ? (c.out_fp32 ? 8 : 5) : 1; }
-static int few_parts2(const moe_config& c, bool mx) { return mx ? (c.out_fp32 ? 8 : 5) : (c.out_fp32 ? 3 : 2); }
 static FewLayout few_layout(const moe_config& c, bool mx, int G) {
   FewLayout L{};
-  const size_t T = c.T, R = T * c.k, F = c.F, Fs = c.F_shared, H = c.H, P2 = few_parts2(c, mx);
-  const size_t P1 = few_parts1(c, mx);
+  const size_t T = c.T, R = T * c.k, F = c.F, Fs = c.F_shared, H = c.H, P2 = few_parts2(mx, c.out_fp32);
+  const size_t P1 = few_parts1(mx, c.out_fp32);
   size_t o = sizeof(DevStatus);
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -1110,8 +1108,8 @@ int run_few(const moe_config& c, const FewArgs& q, bool mx, void* ws, cudaStream
   p.topk_groups = c.topk_groups;
   p.force = c.force_balanced;
   p.gate_scale = c.gate_scale;
-  p.P1 = few_parts1(c, mx);
-  p.P2 = few_parts2(c, mx);
+  p.P1 = few_parts1(mx, c.out_fp32);
+  p.P2 = few_parts2(mx, c.out_fp32);
   p.mx = mx ? 1 : 0;
   p.mcap = few_mcap(p.P1, mx);
   p.nsh = c.F_shared ? (c.T + p.mcap - 1) / p.mcap : 0;

@@ -134,6 +134,9 @@ struct FewMaps {
 };
 
 __host__ __device__ constexpr int few_tile(bool mx) { return kFewATile + (mx ? 2 * kFewSf : 0); }
+// parts of x and of a
+__host__ __device__ constexpr int few_parts1(bool mx, bool fp32) { return mx ? (fp32 ? 8 : 5) : 1; }
+__host__ __device__ constexpr int few_parts2(bool mx, bool fp32) { return mx ? (fp32 ? 8 : 5) : fp32 ? 3 : 2; }
 // columns of the N operand: part q of row j is column q m + j
 __host__ __device__ __forceinline__ int few_cols(int parts, int m) { return (parts * m + 15) & ~15; }
 // accumulator columns of tensor memory: the rest holds scales, or is left to reads of
@@ -157,12 +160,15 @@ __host__ __device__ __forceinline__ FewGeo few_geo(int P1, int P2, int T, int mm
   g.nst = g.acc_off / g.stage;  // (one at least: 64 rows of an expert, three parts)
   if (g.nst > kFewStages) g.nst = kFewStages;
   const int cols = few_acc_cols(mx);
-  // the steps along k take several accumulators in turn: each adds a part of the products, so that
-  // fp32 results' chains end once a stage or two (one accumulator: 16 tokens of 8 experts of
-  // 4096 x 14336 571 us for 437; bf16 results within 1% either way); two sets of them, where they fit, while
-  // the epilogue reads one (one set: 8 tokens 297.7 us for 294.1, 33 with MXFP4 weights 212 for 208)
-  g.il1 = 8 * g.n1 * 2 <= cols ? 4 : 4 * g.n1 * 2 <= cols ? 2 : 1;
-  g.il2 = 4 * g.n2 * 2 <= cols ? 4 : 2 * g.n2 * 2 <= cols ? 2 : 1;
+  // the steps along k of fp32 results take several accumulators in turn: each adds a part of the
+  // products, so that their chains end once a stage or two (one accumulator: 16 tokens of 8
+  // experts of 4096 x 14336 571 us for 437). bf16 results are as near with one, which is read
+  // sooner (one MXFP4 token 40.7 us with four, 40.2; 33 tokens 208, 207)
+  const bool fp32 = P2 != few_parts2(mx, false);
+  g.il1 = !fp32 ? 1 : 8 * g.n1 * 2 <= cols ? 4 : 4 * g.n1 * 2 <= cols ? 2 : 1;
+  g.il2 = !fp32 ? 1 : 4 * g.n2 * 2 <= cols ? 4 : 2 * g.n2 * 2 <= cols ? 2 : 1;
+  // two sets of them, where they fit, while the epilogue reads one (one set: 8 tokens 297.7 us for
+  // 294.1, 33 with MXFP4 weights 212 for 208)
   g.nbuf1 = 4 * g.n1 * g.il1 <= cols ? 2 : 1;
   g.nbuf2 = 2 * g.n2 * g.il2 <= cols ? 2 : 1;
   return g;
