@@ -33,8 +33,8 @@
 // Measured, 128 experts of 4096 x 1536, eight a token: one token 68 us (302 MB: 4.4 TB/s; the
 // router and the plan take 10, the ends of the two phases 6 and 3, during which little is
 // read), 8 tokens 295, 61 tokens 699 (4.74 GB: 6.8 TB/s, as fast as memory is read);
-// with MXFP4 weights one token 41 (80 MB: 2.0 TB/s), 33 tokens 208 (1.1 GB: 5.4 TB/s, a unit's
-// sixteen small MMAs and their scales take 0.4 of its 0.7 us).
+// with MXFP4 weights one token 40 (80 MB: 2.0 TB/s), 33 tokens 207 (1.1 GB: 5.4 TB/s, a unit's
+// eight small MMAs and their scales take 0.4 of its 0.7 us).
 //
 // Operands: bf16 weights multiply bf16 parts of the tokens (x itself; the activation
 // a in two parts, three for fp32 results: 2^-17 and 2^-25 of a). MXFP4 weights stay
