@@ -797,7 +797,8 @@ int moe_layer_few_fwd_mxfp4(const moe_config* cfg, const moe_bf16* x, const moe_
  *   dy bf16, dresidual as residual, dpost_weight, dpre_weight [H], dgate as gate, fp32.
  * dh (may be NULL: zeros) as residual; dn bf16, fp32 with out_fp32, as the layer's
  * dx. Sums over rows are fp32 for at most 64 rows and two floats beyond, in a fixed
- * order. Shapes: H a multiple of 8, H <= 16384, 1 <= T <= 2^30.
+ * order. A row is right in both directions while the sum of its squares (y's with post, h's
+ * with pre) stays in fp32: an rms from about 2^-63 (eps 0) to 2^64 / sqrt(H). Shapes: H a multiple of 8, H <= 16384, 1 <= T <= 2^30.
  * ------------------------------------------------------------------------- */
 typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 } moe_gate_kind;
 typedef struct {

@@ -6,10 +6,12 @@
 // out; backward y, r, dh, dn in, dy, dr out): a block of threads holds a row in
 // registers from its loads to its stores, and h is computed again in the backward
 // rather than kept. With dnw = dn wn the backward is
-//   dH = A + S1 B,  A = dh + rh dnw,  B = -h rh^3 / H,  S1 = sum dnw h,
-//   dr = a dH,  dy = ry (g dH wp - y ry^2 / H S2),  S2 = sum g dH wp y,
-// and since dH is linear in S1, S2 = SA + S1 SB with sums of A and B alone: one
-// reduction over the block for a row. The gradients of the weights and of a channel
+//   dH = A + S1 hh,  A = dh + rh dnw,  hh = h rh,  S1 = -rh / H sum dnw hh,
+//   dr = a dH,  dy = ry (g dH wp - yy / H S2),  yy = y ry,  S2 = sum g dH wp yy,
+// and since dH is linear in S1, S2 = SA + S1 SB with sums of A and hh alone: one
+// reduction over the block for a row. No power of rh or ry above the first is formed: a
+// row is right wherever the forward's sum of squares is (rh^3 leaves fp32 at rows of 1e13
+// and of 1e-13). The gradients of the weights and of a channel
 // gate are sums over rows, dpre's of dn h rh and one more for both others,
 //   D = sum g_t dH y ry  (g_t: a token's gate),  dpost = g D,  dgate = wp D:
 // a thread adds its columns' in fp32 over at most 64 rows, then in two floats in the
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1) norm_bwd_kernel(con
       ring.load(p, stage == 0 ? S - 1 : stage - 1, row + (S - 1) * gridDim.x);
       cp_async_wait<S - 1>();
     }
-    const float ry = ry1, rh = rh1, gt = gt1, bf = -rh * rh * rh * inv;
+    const float ry = ry1, rh = rh1, gt = gt1;
     scalars(row + gridDim.x);
     auto get_own = [&](int i, auto f32, const void* src, int plane, float(&v)[8]) {
       constexpr bool F32 = decltype(f32)::value;
@@ -420,12 +422,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1) norm_bwd_kernel(con
     constexpr std::bool_constant<RF> rf{};
     constexpr std::bool_constant<OF> of{};
     float s0 = 0.0f, sa = 0.0f, sb = 0.0f;
-    float A[NC][8], h[NC][8];
+    float A[NC][8], h[NC][8];  // h: with pre, h rh from the sums on
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int i = threadIdx.x + c * blockDim.x;
       if (i < n8) {
-        float t[8], x[8];  // x: what the sums for dy (or a token's gate) take A and B with
+        float t[8], x[8];  // x: what the sums for dy (or a token's gate) take A and hh with
         get_own(i, of, p.y, 0, x);
         if constexpr (FULL) {
 #pragma unroll
@@ -448,7 +450,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1) norm_bwd_kernel(con
           get_own(i, of, p.dn, Ring::kY, t);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            an[c][j] = fmaf(t[j], h[c][j] * rh, an[c][j]);
+            h[c][j] *= rh;
+            an[c][j] = fmaf(t[j], h[c][j], an[c][j]);
             const float d = t[j] * wn[c][j];
             s0 = fmaf(d, h[c][j], s0);
             A[c][j] = fmaf(rh, d, A[c][j]);
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1) norm_bwd_kernel(con
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             sa = fmaf(A[c][j], x[j], sa);
-            sb = fmaf(bf * h[c][j], x[j], sb);
+            sb = fmaf(h[c][j], x[j], sb);
           }
         }
       }
@@ -467,12 +470,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 2 : 1) norm_bwd_kernel(con
     if constexpr (FULL) {
       float s[3] = {s0, sa, sb};
       block_sum(s, red, turn);
-      s1 = s[0] * bf;
-      s2 = fmaf(s[0], s[2], s[1]);
+      s1 = s[0] * -rh * inv;
+      s2 = p.pre ? fmaf(s1, s[2], s[1]) : s[1];  // (without pre h is as large as it is)
     } else {
       float s[1] = {s0};
       block_sum(s, red, turn);
-      s1 = s[0] * bf;
+      s1 = s[0] * -rh * inv;
     }
     if (token && threadIdx.x == 0) p.dgate[row] = s2;
     // dy = ry (g dH wp) - (y ry) ry / H (ry S2); a token's sums are without its g
