@@ -741,7 +741,8 @@ typedef struct {
 size_t moe_mx4_weight_bytes(const moe_config* cfg, int which);
 
 /* Quantise the bf16 weights of the layer (Ws1, Ws3, Ws2 when F_shared > 0, else
- * ignored), and the way back into bf16 weights, which is exact. */
+ * ignored), and the way back into bf16 weights, which is exact (none of them may
+ * overlap another there: MOE_ERR_INVALID_ARG). */
 int moe_mx4_quantize_weights(const moe_config* cfg, const moe_bf16* W1, const moe_bf16* W3, const moe_bf16* W2,
                              const moe_bf16* Ws1, const moe_bf16* Ws3, const moe_bf16* Ws2, const moe_mx4_weights* w,
                              void* stream);

@@ -237,14 +237,17 @@ static int mx4_weights(const moe_config* cfg, const void* const (&bf)[6], const 
   if (!mx4_aligned({w->w13, w->w2, w->w13s, w->w2s}, 16)) return MOE_ERR_INVALID_ARG;
   const uint8_t* q[4] = {w->w13, w->w2, w->w13s, w->w2s};
   const int nq = c.F_shared ? 4 : 2;
+  auto bf_bytes = [&](int j) { return 2ull * (j >= 3 ? c.F_shared : static_cast<size_t>(c.E) * c.F) * c.H; };
   for (int i = 0; i < nq; ++i) {
     const size_t bytes = moe_mx4_weight_bytes(cfg, i);
     for (int j = 0; j < n; ++j)
-      if (overlap(q[i], bytes, bf[j], 2ull * (j >= 3 ? c.F_shared : static_cast<size_t>(c.E) * c.F) * c.H))
-        return MOE_ERR_INVALID_ARG;
+      if (overlap(q[i], bytes, bf[j], bf_bytes(j))) return MOE_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)
       if (overlap(q[i], bytes, q[j], moe_mx4_weight_bytes(cfg, j))) return MOE_ERR_INVALID_ARG;
   }
+  for (int i = 0; back && i < n; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(bf[i], bf_bytes(i), bf[j], bf_bytes(j))) return MOE_ERR_INVALID_ARG;
   Mx4Weights a{};
   a.n = n;
   for (int i = 0; i < n; ++i) {
