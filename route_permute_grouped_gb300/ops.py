@@ -1197,8 +1197,10 @@ def _mx4_sizes(cfg):
     return [(n, _size("moe_mx4_weight_bytes", cfg, i)) for i, n in enumerate(used)]
 
 
-def _mx4_struct(w, cfg, q, d):
+def _mx4_struct(w, cfg, q, d=None):
     got = {}
+    if not isinstance(q, dict):
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{w}: the weights must be mx4_quantize_weights' dict")
     for n, size in _mx4_sizes(cfg):
         if q.get(n) is None:
             raise MoeError(MOE_ERR_INVALID_ARG, f"{w}: the weights lack {n}")
@@ -1222,8 +1224,8 @@ def mx4_dequantize_weights(cfg, q):
     """(W1, W3, W2, Ws) bf16 that mx4_quantize_weights' dict stands for, exactly (Ws:
     the shared expert's three, None without one)."""
     w = "mx4_dequantize_weights"
+    st = _mx4_struct(w, cfg, q)
     dev = q["w13"].device
-    st = _mx4_struct(w, cfg, q, _current_device())
     new = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device=dev)
     E, H, F, Fs = cfg.E, cfg.H, cfg.F, cfg.F_shared
     W = [new(E, H, F), new(E, H, F), new(E, F, H)]
