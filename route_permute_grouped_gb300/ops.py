@@ -1143,8 +1143,8 @@ def _mx4_rows(where, name, t, per):
         raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {name} must be a matrix")
     M, K = t.shape
     K *= per
-    if K < 1 or K % 32:
-        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, f"{where}: rows must hold blocks of 32")
+    if K < 1 or K % 32 or K >= 1 << 31:  # (the library takes K as an int)
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, f"{where}: rows must hold blocks of 32, fewer than 2^31 elements")
     if M < 1:
         raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: there must be rows")
     return M, K

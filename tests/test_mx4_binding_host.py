@@ -14,3 +14,14 @@ def test_weights_that_are_not_there(q):
     with pytest.raises(ops.MoeError) as e:
         ops.mx4_dequantize_weights(cfg, q)
     assert e.value.status == ops.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("K", [1 << 31, (1 << 32) + 32])
+def test_rows_longer_than_the_library_takes(K):
+    # K is an int there: 2^32 + 32 would arrive as 32. (A row of one element's memory; nothing is read)
+    long = lambda n, t: torch.zeros(1, dtype=t).expand(1, n)
+    for call in (lambda: ops.mx4_quantize(long(K, torch.bfloat16)),
+                 lambda: ops.mx4_dequantize(long(K // 2, U8), long(K // 32, U8))):
+        with pytest.raises(ops.MoeError) as e:
+            call()
+        assert e.value.status == ops.MOE_ERR_UNSUPPORTED_SHAPE
