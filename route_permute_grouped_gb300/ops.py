@@ -859,10 +859,18 @@ def _ws_arg(where, ws, nbytes, dev):
 _size_cache = {}
 
 
+def _device_key():
+    """The current device, by which sizes are kept: some go by its number of SMs (-1 where there is none)."""
+    try:
+        return _current_device()
+    except (RuntimeError, AssertionError):  # no driver; a torch built without CUDA
+        return -1
+
+
 def _size(name, cfg, *more):
     """A size the library gives for a config, asked once for each config's
-    values; raises for a config it refuses."""
-    key = (name, bytes(cfg), more)
+    values and device; raises for a config it refuses."""
+    key = (name, bytes(cfg), more, _device_key())
     n = _size_cache.get(key)
     if n is None:
         n = int(getattr(lib(), name)(ctypes.byref(cfg), *more))
@@ -1328,7 +1336,7 @@ _norm_plans = {}
 
 
 def _norm_plan(cfg):
-    key = bytes(cfg)
+    key = bytes(cfg), _device_key()
     plan = _norm_plans.get(key)
     if plan is None:
         plan = _NormPlan(cfg)
