@@ -629,6 +629,36 @@ __device__ __forceinline__ void few_store_y(const FewParams& p, int t, int h, fl
   else static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
 }
 
+// What a block that gave up has under way ends before it does: copies to shared memory, which
+// report to `full`, and MMAs. All threads, behind their roles; n: stages that the thread's warp
+// has begun. The threads that fill stages may have left at different ones, and a barrier of
+// `full` turns only when all of them have arrived: each arrives for those that another one
+// began. (The last stage begun found the one before it in its place taken, so that
+// all had arrived there: only the last g.nst barriers are open.)
+template <bool MX>
+__device__ __noinline__ void few_drain(const FewParams& p, FewCtl* c, int n) {
+  const int warp = warp_id();
+  int given_up = 0;  // the block's own flag is set
+  if (warp != 1 && warp < 4) atomicMax(&c->stages, n);
+  __syncthreads();
+  const int last = c->stages;
+  if (last > 0) {
+    // (with a shared expert the stages are the same before and after the plan, without one there are none before)
+    const FewGeo g = p.Fs ? few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), MX) : c->geo;
+    const bool weights = warp == 0 && elect_one();
+    if (weights || warp == 2 || warp == 3)
+      for (int i = n; i < last; ++i) mbar_arrive(c->full + i % g.nst);
+    if (weights)
+      for (int i = max(0, last - g.nst); i < last; ++i)
+        mbar_wait_bounded(c->full + i % g.nst, (i / g.nst) & 1, &given_up, p.lim, nullptr, 0);
+  }
+  if (warp == 1) {
+    if (elect_one()) umma_commit(&c->drain);
+    __syncwarp();
+    mbar_wait_bounded(&c->drain, 0, &given_up, p.lim, nullptr, 0);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
@@ -654,6 +684,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     mbar_init(&c->plan, 1);
     mbar_init(&c->drain, 1);
     c->abort = 0;
+    c->stages = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -668,6 +699,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   volatile int* abort_flag = &c->abort;
   const int G = gridDim.x;
   constexpr int kSubBytes = 128;
+  int n = 0;  // stages so far, of the warps that fill or take them
 
   if (warp == 0) {
     // ------------------------------------------------------------ weights
@@ -675,7 +707,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if constexpr (!MX)
         for (int i = 0; i < (p.Fs ? 6 : 3); ++i) tma_prefetch_desc(&maps.m[i]);
       const uint64_t pol = l2_policy_evict_first();
-      int n = 0;  // stages so far
       bool ok = true;
       FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), MX);
       for (int ph = first_phase; ph < 5 && ok; ++ph) {
@@ -717,14 +748,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           }
         }
       }
-      if (*abort_flag) {  // copies in flight have time to land before the block ends
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 200000ull) __nanosleep(1000);
-      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
-    int n = 0, na = 0;  // stages, accumulators so far
+    int na = 0;  // accumulators so far
     bool ok = true;
     FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), MX);
     const uint32_t d_hi = sdesc_hi_sw128(1024);
@@ -826,16 +853,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         __syncwarp();
       }
     }
-    if (*abort_flag) {  // the MMAs in flight end before the tensor memory is freed
-      int zero = 0;
-      if (elect_one()) umma_commit(&c->drain);
-      __syncwarp();
-      mbar_wait_bounded(&c->drain, 0, &zero, p.lim, nullptr, 0);
-    }
   } else if (warp < 4) {
     // ------------------------------------------------------------ tokens
     const int ct = threadIdx.x - 64;
-    int n = 0;
     bool ok = true;
     FewGeo g = few_geo(p.P1, p.P2, p.T, min(p.T, p.mcap), MX);
     for (int ph = first_phase; ph < 5 && ok; ++ph) {
@@ -1010,6 +1030,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag) few_drain<MX>(p, c, n);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

@@ -81,7 +81,7 @@ struct FewCtl {
   uint32_t tmem;
   int abort;
   int nact;                  // entries: runs of rows of one expert
-  int flag;
+  int stages;                // that a block has begun which gave up
   int warp_sum[8], warp_act[8], warp_max[8];
   uint32_t has[256][2];      // expert -> its tokens
   int eoff[256];             // expert -> its first row
