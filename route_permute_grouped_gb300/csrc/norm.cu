@@ -576,18 +576,29 @@ static int check_norm(const moe_norm_config* c) {
 // runs of 8 columns a thread in the backward
 static int norm_runs(int H) { return H <= 8192 ? 1 : 2; }
 static dim3 norm_threads(int H, int nc) { return dim3(((H / 8 + nc - 1) / nc + 31) / 32 * 32); }
-// blocks of the backward: those that an SM holds at once, at 64 registers a thread
-static int norm_per_sm(int H) {
-  const int per = 1024 / static_cast<int>(norm_threads(H, norm_runs(H)).x);
+constexpr size_t kNormSmem = 230400;      // of a block, at most
+constexpr size_t kNormSmemSM = 233472;    // of an SM
+constexpr size_t kNormSmemOther = 1792;   // a block's sums and what the system keeps
+
+// bytes of a row of y, dn, the residual and dh
+static size_t norm_row_bytes(const moe_norm_config& c) {
+  return static_cast<size_t>(c.H) * 2 * ((c.out_fp32 ? 4 : 2) + (c.residual_fp32 ? 4 : 2));
+}
+// rows on their way in shared memory in the backward: none where rows are too long for two
+static int norm_ring(const moe_norm_config& c) { return c.H <= 8192 && 2 * norm_row_bytes(c) <= kNormSmem ? 2 : 0; }
+// blocks of the backward: those that an SM holds at once, at 64 registers a thread and with their rows (counted
+// by threads alone: 32768 x 1024 fp32 in and out, gate and both norms, 8 blocks for 6, 162 us for 133; 16384 x 2048 164 for 134)
+static int norm_per_sm(const moe_norm_config& c) {
+  int per = 1024 / static_cast<int>(norm_threads(c.H, norm_runs(c.H)).x);
+  const int hold = static_cast<int>(kNormSmemSM / (norm_ring(c) * norm_row_bytes(c) + kNormSmemOther));
+  if (per > hold) per = hold;
   return per < 16 ? per : 16;
 }
 static int norm_blocks(const moe_norm_config& c) {
-  const int most = norm_per_sm(c.H) * num_sms();
+  const int most = norm_per_sm(c) * num_sms();
   return c.T < most ? c.T : most;
 }
 static bool norm_sums(const moe_norm_config& c) { return c.pre || c.post || c.gate == MOE_GATE_CHANNEL; }
-
-constexpr size_t kNormSmem = 230400;
 
 template <bool RF, bool OF, int NC>
 static cudaError_t launch_fwd(const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
@@ -595,7 +606,7 @@ static cudaError_t launch_fwd(const moe_norm_config& c, const NormParams& p, int
 }
 template <bool RF, bool OF, bool FULL, int NC, int S, int MAXT>
 static cudaError_t launch_bwd(const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
-  const size_t bytes = static_cast<size_t>(S) * c.H * (2 * (OF ? 4 : 2) + 2 * (RF ? 4 : 2));
+  const size_t bytes = S * norm_row_bytes(c);
   const auto kernel = norm_bwd_kernel<RF, OF, FULL, NC, S, MAXT>;
   if constexpr (S > 0) {
     static std::atomic<unsigned long long> set{0};  // devices whose kernel has its shared memory
@@ -616,10 +627,9 @@ static cudaError_t launch_bwd(const moe_norm_config& c, const NormParams& p, int
 // several an SM.
 template <bool RF, bool OF, bool FULL>
 static cudaError_t launch_bwd(const moe_norm_config& c, const NormParams& p, int grid, cudaStream_t s) {
-  const size_t row = static_cast<size_t>(c.H) * (2 * (OF ? 4 : 2) + 2 * (RF ? 4 : 2));
   if (c.H > 8192) return launch_bwd<RF, OF, FULL, 2, 0, 1024>(c, p, grid, s);
   if (c.H > 7168)
-    return 2 * row <= kNormSmem ? launch_bwd<RF, OF, FULL, 1, 2, 1024>(c, p, grid, s)
+    return norm_ring(c) ? launch_bwd<RF, OF, FULL, 1, 2, 1024>(c, p, grid, s)
                                 : launch_bwd<RF, OF, FULL, 1, 0, 1024>(c, p, grid, s);
   if (c.H > 4096) return launch_bwd<RF, OF, FULL, 1, 2, 896>(c, p, grid, s);  // (at most 224 KB)
   return launch_bwd<RF, OF, FULL, 1, 2, 512>(c, p, grid, s);
