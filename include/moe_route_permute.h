@@ -775,10 +775,11 @@ int moe_layer_few_fwd(const moe_config* cfg, const moe_bf16* x, const moe_bf16* 
                       const moe_bf16* Ws1, const moe_bf16* Ws3, const moe_bf16* Ws2, int32_t* topk_idx,
                       float* topk_gate, void* y, void* ws, size_t ws_bytes, void* stream);
 
-/* The same with MXFP4 weights, the shared expert's included. The activations keep
- * their precision: x and a enter the products as sums of five MXFP4 parts (eight with
- * out_fp32), each 3 bits below the one before: an element is off by at most 2^-13
- * (2^-22) of the largest of its 32. */
+/* The same with MXFP4 weights, the shared expert's included. x and a enter the
+ * products as sums of five MXFP4 parts (eight with out_fp32), each 3 bits below the one
+ * before: an element is off by at most 2^-13 (2^-22) of the largest of its 32 or by
+ * 2^-128, whichever is more. With five parts elements below a sixteenth of the largest
+ * so have fewer bits than bf16 keeps. */
 int moe_layer_few_fwd_mxfp4(const moe_config* cfg, const moe_bf16* x, const moe_bf16* router_w,
                             const float* expert_bias, const float* logit_bias, const moe_mx4_weights* w,
                             int32_t* topk_idx, float* topk_gate, void* y, void* ws, size_t ws_bytes, void* stream);

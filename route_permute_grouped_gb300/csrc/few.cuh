@@ -7,7 +7,7 @@
 // token of a 128-expert layer 302 MB of bf16, 80 MB of MXFP4. So the weights are
 // the M operand of the tensor cores (128 output columns a tile), the few tokens
 // the N operand, and everything is arranged so that the stream of weight tiles
-// never stops:
+// goes on from the first to the last, as far as the ring of stages holds them:
 //  - the units of a phase (one weight tile of 32 KB each in shared memory) are
 //    dealt to the blocks in equal contiguous runs, whatever the experts' number;
 //    a tile cut by a run's border is joined from fp32 partials by the block that has its
@@ -20,6 +20,14 @@
 //    between the phases, the next phase's weights are already on their way;
 //  - the tokens' operand follows by 16-byte copies of two other warps as soon as
 //    it exists.
+// A stage holds both, and is as large as the entry with most rows wants, in every phase
+// (few_geo); with a shared expert that is min(T, mcap) rows whatever the routing, more than its
+// entries have where there are several. Four stages become two from 41 rows on (fp32 results 33;
+// MXFP4 weights 20, with fp32 results 13) and one from 54 rows with fp32 results, under MXFP4
+// from 36 (25): then no weights are on their way during a stage's MMAs. 32 experts of 4096 x 1536 with a
+// shared expert of that size, and without: 64 tokens 245 and 220 us, fp32 results 459 and 271; MXFP4
+// weights, 40 tokens 167 and 119, 64 tokens 195 and 158, fp32 results 313 and 273 (the shared
+// expert's weights themselves are 6 us, 1.5 in MXFP4).
 //
 // Phases: 0 the shared expert's gate and up products (needs no routing: its weights
 // stream while the router works); 1 and 2 those of the first and second half of the
@@ -42,7 +50,8 @@
 // tokens, a power of two for 32 elements on either side. So x and a enter as sums of E2M1
 // parts, every part with its own powers of two: a part leaves at most half the largest
 // step of the one before, 3 bits a part, 2^-12 of a block's unit after five (2^-21 after
-// eight, for fp32 results). The parts are further columns of the N operand, of which the
+// eight, for fp32 results), 2^-13 of its largest element: elements below a sixteenth of that
+// keep fewer bits than bf16 has (after eight, below 2^-13 of it). The parts are further columns of the N operand, of which the
 // tensor cores have plenty to spare. (Unpacked 4-bit weights with E4M3 tokens need fewer
 // parts, but the copies that unpack move 8 bytes a cycle: 2.5 TB/s over all SMs.)
 #pragma once

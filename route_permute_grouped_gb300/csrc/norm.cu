@@ -16,10 +16,14 @@
 //   D = sum g_t dH y ry  (g_t: a token's gate),  dpost = g D,  dgate = wp D:
 // a thread adds its columns' in fp32 over at most 64 rows, then in two floats in the
 // workspace; a second kernel joins the blocks' in order.
-// Measured: 16384 x 4096 in bf16 (residual and norm) forward 86 us, 6.25 TB/s, backward 137, 5.9 TB/s,
-// 8 of it the join; 5003 x 7168 with both norms, a channel gate and an fp32 stream 77 us, 5.6 TB/s, and
-// 117, 5.5 TB/s: what is lost there are the rows' one (forward two) sums over a block that has an SM
-// nearly to itself.
+// Measured: 16384 x 4096 in bf16 (residual and norm) forward 86 us, 6.2 TB/s, backward 140, 5.8 TB/s,
+// 8 of it the join; 5003 x 7168 with both norms, a channel gate and an fp32 stream 78 us, 5.5 TB/s, and
+// 119, 5.4 TB/s: what is lost there are the rows' one (forward two) sums over a block that has an SM
+// nearly to itself. y and dn fp32 too: 8192 x 4096 without post norm and gate 80 us, 5.9 TB/s, and 112, 6.6 TB/s,
+// with them 90 and 169, 4.4 TB/s; 16384 x 2048 with them 84 and 134, 5.5 TB/s. Longer rows: 4096 x 8192 in bf16 49 us,
+// 5.5 TB/s, and 68, 5.9 TB/s, with both norms, gate and fp32 stream 71 and 128, 4.7 TB/s (registers held to 64 of
+// 1024 threads); 2048 x 16384 59 us, 4.5 TB/s, and 124, 3.3 TB/s, with all of it 101 and 192, 3.1 TB/s (two runs a
+// thread in those registers, up to 1.4 KB a thread spilled, and no row ahead in shared memory).
 #include <atomic>
 #include <type_traits>
 

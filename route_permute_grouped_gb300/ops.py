@@ -1287,8 +1287,9 @@ def layer_few_fwd(cfg, x, router_w, W1, W3, W2, expert_bias=None, logit_bias=Non
 
 
 def layer_few_fwd_mxfp4(cfg, x, router_w, q, expert_bias=None, logit_bias=None, ws=None, y=None):
-    """layer_few_fwd with MXFP4 weights (q from mx4_quantize_weights); the activations
-    keep their precision. ws from few_workspace(cfg, mxfp4=True)."""
+    """layer_few_fwd with MXFP4 weights (q from mx4_quantize_weights). An element of x, or
+    of the activation, counts with an error of at most 2^-13 of the largest of its 32 (with
+    cfg.out_fp32 2^-22). ws from few_workspace(cfg, mxfp4=True)."""
     w = "layer_few_fwd_mxfp4"
     head, tail, out, d = _few_args(w, cfg, x, router_w, expert_bias, logit_bias, ws, y, True)
     _check(lib().moe_layer_few_fwd_mxfp4(ctypes.byref(cfg), *head, ctypes.byref(_mx4_struct(w, cfg, q, d)), *tail),
